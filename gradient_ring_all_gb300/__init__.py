@@ -1,5 +1,6 @@
 """Python binding of the GB300 ring all-reduce library (C ABI in
-``include/ring_allreduce.h``).
+``include/ring_allreduce.h``; the training-step operators of
+``include/ra_operators.h`` are bound in ``operators.py`` and offered here).
 
 The functions carry the C names and only marshal arguments: every step of
 the all-reduce runs in the library's CUDA kernels.  PyTorch supplies device
@@ -27,6 +28,8 @@ __all__ = [
     "RA_STAGED_STATIC_MAX_P", "RA_HOST_AUTO", "RA_HOST_DIRECT", "RA_HOST_STAGED", "ra_reduce_scatter_avg",
     "ra_all_gather", "ra_allreduce_avg_bf16_wire", "ra_allreduce_avg_single_reducer", "Reducer", "ra_check_device_errors", "ra_selftest_wait_timeout", "ra_selftest_bounds_check", "ra_chunk_range", "ra_status_str",
     "ra_last_cuda_error", "RA_OK", "RA_ERR_TIMEOUT", "RA_ERR_BOUNDS", "CHECKED",
+    "Checkpoint8", "ra_checkpoint8_pack", "ra_checkpoint8_unpack", "ra_embedding_lookup", "ra_embedding_grad",
+    "ra_linear", "ra_linear_dgrad", "ra_linear_wgrad",
 ]
 
 RA_F32 = 0
@@ -402,3 +405,21 @@ def ra_status_str(status: int) -> str:
 
 def ra_last_cuda_error() -> int:
     return load().ra_last_cuda_error()
+
+
+
+# ---------------------------------------------------------------------------
+# the training-step operators (operators.py), imported on first use: the ring's
+# calls and the build need no torch
+
+_OPERATORS = ("Checkpoint8", "ra_checkpoint8_pack", "ra_checkpoint8_unpack", "ra_embedding_lookup", "ra_embedding_grad",
+              "ra_linear", "ra_linear_dgrad", "ra_linear_wgrad")
+
+
+def __getattr__(name):
+    if name in _OPERATORS:
+        from . import operators
+        for nm in _OPERATORS:
+            globals()[nm] = getattr(operators, nm)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

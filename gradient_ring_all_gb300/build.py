@@ -2,7 +2,7 @@
 
     python -m gradient_ring_all_gb300.build [--force] [--verbose-ptxas] [--checked]
 
-Compiles each csrc/*.cu into _build/*.o in parallel with nvcc and links
+Compiles each csrc/*.cu and csrc/operators/*.cu into _build/*.o in parallel with nvcc and links
 lib/libgradient_ring_all.so against the shared CUDA runtime.  A stamp of the
 sources and flags skips the work when nothing changed.  --checked builds the
 bounds-checked library instead (RA_CHECKED=1: every kernel verifies each
@@ -44,8 +44,12 @@ def _cuda_lib_dir(nvcc: str) -> str:
 
 
 def _sources():
-    cu = sorted(f for f in os.listdir(CSRC) if f.endswith(".cu"))
-    deps = sorted(f for f in os.listdir(CSRC) if f.endswith((".cuh", ".h")))
+    """The library's .cu files and the headers they include, as paths below csrc/."""
+    names = []
+    for sub in ("", "operators"):
+        names += [os.path.join(sub, f) for f in os.listdir(os.path.join(CSRC, sub))]
+    cu = sorted(f for f in names if f.endswith(".cu"))
+    deps = sorted(f for f in names if f.endswith((".cuh", ".h")))
     return cu, deps
 
 
@@ -55,8 +59,9 @@ def _stamp(extra) -> str:
     for f in cu + deps:
         with open(os.path.join(CSRC, f), "rb") as fh:
             h.update(f.encode() + b"\0" + fh.read())
-    with open(os.path.join(ROOT, "include", "ring_allreduce.h"), "rb") as fh:
-        h.update(fh.read())
+    for f in ("ring_allreduce.h", "ra_operators.h"):
+        with open(os.path.join(ROOT, "include", f), "rb") as fh:
+            h.update(fh.read())
     h.update(" ".join(ARCH + NVCC_FLAGS + list(extra)).encode())
     return h.hexdigest()
 
@@ -81,7 +86,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, checked: bool | None
     cu, _ = _sources()
 
     def compile_one(f):
-        obj = os.path.join(bdir, f[:-3] + ".o")
+        obj = os.path.join(bdir, os.path.basename(f)[:-3] + ".o")
         cmd = [nvcc, *ARCH, *NVCC_FLAGS, *extra, "-c", os.path.join(CSRC, f), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:

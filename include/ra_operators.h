@@ -1,0 +1,154 @@
+/*
+ * ra_operators.h -- C ABI of the training-step operators of the GB300 ring
+ * all-reduce library (libgradient_ring_all.so): the calls that produce the
+ * gradients which the ring averages.
+ *
+ *   ra_embedding_lookup    rows of an embedding table, scaled
+ *   ra_embedding_grad      the table's gradient, summed by sorted token
+ *   ra_linear              act(x w + bias) + residual on the tensor cores
+ *   ra_linear_dgrad        (dy w^T) * act'(z) + residual
+ *   ra_linear_wgrad        act(z)^T dy and the column sums of dy
+ *   ra_checkpoint8_pack    an activation kept in 8 bits
+ *   ra_checkpoint8_unpack  and restored
+ *
+ * The layers are those of the Transformer whose gradients the library's
+ * workloads average ("How GPipe works", section 1: embedding V x d, weights
+ * d x h and h x d with biases).  A checkpoint is what section 6 of the same
+ * page (re-materialisation) trades for recomputation: the activation that the
+ * backward pass needs, here at 33/32 byte a value.
+ *
+ * Conventions, besides those of ring_allreduce.h (asynchronous on `stream`,
+ * arguments checked before anything is queued, the caller owns all device
+ * memory, no state kept between calls):
+ *   - a matrix is row-major: element (r, c) of `a` at a[r * ld + c], ld >= its
+ *     columns; ld is not looked at where there is one row.  Rows and columns
+ *     stay below 2^31, byte offsets may be larger.
+ *   - an output shares no byte with an input, unless the call says so
+ *     (RA_ERR_OVERLAP).  Column slices of one array with one ld may interleave.
+ *   - a size of zero is allowed: nothing to write is RA_OK without a launch, an
+ *     empty sum is zero.
+ *   - results do not change from call to call: every sum is added in an order
+ *     that the sizes and the token ids alone decide.
+ *   - NaN and infinities go through by the formulas.
+ */
+#ifndef RA_OPERATORS_H
+#define RA_OPERATORS_H
+
+#include "ring_allreduce.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Activations, computed in binary32:
+ *   relu  max(z, 0)
+ *   gelu  z * (1 + erf(z / sqrt 2)) / 2
+ *   silu  z / (1 + exp(-z)) */
+typedef enum { RA_ACT_NONE = 0, RA_ACT_RELU = 1, RA_ACT_GELU = 2, RA_ACT_SILU = 3 } ra_act;
+
+/*
+ * An activation of rows x cols in 8 bits.  RA_CHECKPOINT8_GROUP neighbours of
+ * a row (the last group of a row may be short) share one step, a power of two;
+ * each value is the nearest whole number of steps (ties to even), -127 .. 127:
+ *   q  rows * groups * 32 bytes, group g of row r at q + (r * groups + g) * 32,
+ *      the short group's rest zero; 16-byte aligned
+ *   e  rows * groups bytes; the step is 2^(e - 127)
+ * with groups = ceil(cols / 32).  e is 6 below the (biased) exponent of the
+ * group's largest magnitude, one more where that would round to 128 steps, and
+ * between 1 and 248 (a group whose largest magnitude is 255 * 2^120 or more is
+ * taken times 127/128, so that no restored value is infinite): the error is at most half a step, 1/127.5 of that magnitude.  A
+ * power-of-two step makes every restored value exact in bf16 (and in
+ * binary32), so the tensor cores read a checkpoint without a second rounding.
+ * A group with an infinity or a NaN is marked (e = 255, q = 0) and reads back as
+ * NaN throughout, so that such a value is not lost.
+ */
+#define RA_CHECKPOINT8_GROUP 32
+
+ra_status ra_checkpoint8_pack(const void *x, int64_t ld, int dtype, int64_t rows, int64_t cols, int8_t *q, uint8_t *e,
+                              void *stream);
+
+/* out = act(the values that q and e stand for) in `dtype`. */
+ra_status ra_checkpoint8_unpack(const int8_t *q, const uint8_t *e, int64_t rows, int64_t cols, int act, void *out,
+                                int64_t ld, int dtype, void *stream);
+
+/*
+ * ra_embedding_lookup -- out[t, :] = scale * table[ids[t], :], t in [0, tokens);
+ * the binary32 product is rounded to `dtype`.  An id outside [0, vocab) is padding:
+ * its row is zero.
+ *   table   vocab x d, out  tokens x d, both of `dtype`
+ *   ids     tokens integers of id_bytes (4 or 8), contiguous
+ */
+ra_status ra_embedding_lookup(const void *table, int64_t ld_table, int dtype, int64_t vocab, int64_t d, const void *ids,
+                              int id_bytes, int64_t tokens, float scale, void *out, int64_t ld_out, void *stream);
+
+/*
+ * ra_embedding_grad -- the gradient of that lookup:
+ *   out[v, :] = scale * sum over t with ids[t] = v of grad[t, :]
+ * for every v in [0, vocab), zero where no token has id v.  The sum is
+ * binary32; it and, with `accumulate`, out's former value are rounded to
+ * out_dtype once.  accumulate != 0 adds to out (micro-batches, tied weights)
+ * and leaves rows without a token alone.  Ids outside [0, vocab) count for
+ * nothing, whatever their rows of grad hold.
+ *   ws, ws_bytes  device workspace of at least
+ *                 ra_embedding_grad_workspace_bytes(tokens, vocab, d), 16-byte
+ *                 aligned
+ */
+size_t ra_embedding_grad_workspace_bytes(int64_t tokens, int64_t vocab, int64_t d);
+ra_status ra_embedding_grad(const void *grad, int64_t ld_grad, int grad_dtype, const void *ids, int id_bytes, int64_t tokens,
+                            float scale, int accumulate, void *out, int64_t ld_out, int out_dtype, int64_t vocab, int64_t d,
+                            void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * ra_linear -- y = act(x w + bias) + residual.
+ *   x, w      m x k and k x n, bf16; products are summed in binary32
+ *   bias      n values of bias_dtype (RA_F32 or RA_BF16), or NULL
+ *   residual  m x n of res_dtype, or NULL; may be y itself (same address, ld
+ *             and type)
+ *   save_q, save_e  NULL, or the 8-bit checkpoint (m x n) that receives
+ *             z = x w + bias, for ra_linear_dgrad and ra_linear_wgrad
+ *   y         m x n of y_dtype, rounded once
+ *   ws        device workspace of ra_linear_workspace_bytes(m, k, n), 16-byte
+ *             aligned; may be NULL where x and w start on 16-byte boundaries
+ *             and their rows are multiples of 16 bytes apart (TMA reads them
+ *             in place; others are first laid out in the workspace)
+ */
+size_t ra_linear_workspace_bytes(int64_t m, int64_t k, int64_t n);
+ra_status ra_linear(const void *x, int64_t ld_x, const void *w, int64_t ld_w, int64_t m, int64_t k, int64_t n,
+                    const void *bias, int bias_dtype, int act, const void *residual, int64_t ld_res, int res_dtype,
+                    int8_t *save_q, uint8_t *save_e, void *y, int64_t ld_y, int y_dtype, void *ws, size_t ws_bytes,
+                    void *stream);
+
+/*
+ * ra_linear_dgrad -- dx = (dy w^T) * act'(z) + residual: the gradient with
+ * respect to the layer's input, carried on through the activation that made
+ * that input from z.
+ *   dy, w     m x n and k x n, bf16
+ *   z_q, z_e  the 8-bit checkpoint of z (m x k); NULL with RA_ACT_NONE
+ *   residual  m x k of res_dtype, or NULL; may be dx itself
+ *   dx        m x k of dx_dtype, rounded once
+ *   ws        as for ra_linear, for dy and w
+ */
+ra_status ra_linear_dgrad(const void *dy, int64_t ld_dy, const void *w, int64_t ld_w, int64_t m, int64_t k, int64_t n,
+                          const int8_t *z_q, const uint8_t *z_e, int act, const void *residual, int64_t ld_res, int res_dtype,
+                          void *dx, int64_t ld_dx, int dx_dtype, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * ra_linear_wgrad -- dw = a^T dy and db = the column sums of dy.
+ *   x         m x k, bf16: a = x; or NULL and
+ *   z_q, z_e  the 8-bit checkpoint of z (m x k): a = act(z), recomputed here
+ *             (act is RA_ACT_NONE with x).  With RA_ACT_NONE a is exact; else
+ *             act(z) is rounded to bf16 for the tensor cores
+ *   dy        m x n, bf16
+ *   dw        k x n of dw_dtype; accumulate != 0 adds to it (micro-batches)
+ *   db        n binary32 values, or NULL; accumulate holds for it too
+ *   ws        as for ra_linear, for x and dy; needed for a checkpoint
+ */
+ra_status ra_linear_wgrad(const void *x, int64_t ld_x, const int8_t *z_q, const uint8_t *z_e, int act, const void *dy,
+                          int64_t ld_dy, int64_t m, int64_t k, int64_t n, int accumulate, void *dw, int64_t ld_dw,
+                          int dw_dtype, float *db, void *ws, size_t ws_bytes, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* RA_OPERATORS_H */
