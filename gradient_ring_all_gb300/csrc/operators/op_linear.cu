@@ -1,5 +1,20 @@
-// op_linear.cu -- the linear layer and its gradients: ra_linear,
-// ra_linear_dgrad and ra_linear_wgrad.
+// op_linear.cu -- the linear layer and its gradients on the tensor cores:
+// ra_linear, ra_linear_dgrad and ra_linear_wgrad.
+//
+// All three are out = epilogue(A B) with A rows x k and B k x cols, bf16 in,
+// binary32 sums:
+//   forward  A = x   (a row's k values are neighbours)       "K-major"
+//            B = w   (the columns of one k are neighbours)   "MN-major"
+//   dgrad    A = dy, B = w^T: both K-major
+//   wgrad    A = x^T, B = dy: both MN-major
+// The tensor cores take either order from shared memory, so nothing is
+// transposed: TMA lays 128-byte swizzled tiles of 64 k by 128 rows and by BN
+// columns, one thread issues tcgen05.mma on them, the sums stay in TMEM, and
+// the epilogue warps read them from there.
+#include <cuda.h>
+
+#include <atomic>
+
 #include "op_common.cuh"
 
 namespace ra {
@@ -8,36 +23,87 @@ namespace {
 
 enum Mode { kForward = 0, kDgrad = 1, kWgrad = 2 };
 
-// the epilogue's operands; an output row is out[r * ldo ..]
+// ---------------------------------------------------------------------------
+// epilogue
+
+// what becomes of the sums; an output row is out[r * ldo ..]
 struct Epilogue {
     void *out;
     const void *bias, *res;
-    int8_t *q;   // forward: written; dgrad: read
+    int8_t *q;   // forward: the checkpoint of z, written; dgrad: read
     uint8_t *e;
     int64_t ldo, ldr, groups;
     int out_f32, bias_f32, res_f32, act;
+    int vec;     // bias and the rows of out and res start on 16-byte boundaries
 };
 
-__device__ __forceinline__ float load_any(const void *p, int64_t i, int f32) {
-    return f32 ? static_cast<const float *>(p)[i] : bf16_bits_to_f32(static_cast<const uint16_t *>(p)[i]);
+// v += the 32 values at p[0..32) (those below count, where not all are there)
+__device__ __forceinline__ void add32(const void *base, int64_t at, int f32, bool full, int count, float (&v)[32]) {
+    if (f32) {
+        const float *p = static_cast<const float *>(base) + at;
+        if (full) {
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                const float4 x = reinterpret_cast<const float4 *>(p)[g];
+                v[4 * g] += x.x;
+                v[4 * g + 1] += x.y;
+                v[4 * g + 2] += x.z;
+                v[4 * g + 3] += x.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (j < count) v[j] += p[j];
+        }
+    } else {
+        const uint16_t *p = static_cast<const uint16_t *>(base) + at;
+        if (full) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const uint4 x = reinterpret_cast<const uint4 *>(p)[g];
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[8 * g + 2 * k] += __uint_as_float(w[k] << 16);
+                    v[8 * g + 2 * k + 1] += __uint_as_float(w[k] & 0xffff0000u);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (j < count) v[j] += bf16_bits_to_f32(p[j]);
+        }
+    }
 }
 
 // 32 neighbouring columns of one output row, from column n0 (a multiple of
-// 32) on; `count` of them exist.
+// 32, so one checkpoint group) on; `count` of them exist.  The sums of columns
+// that do not exist are not looked at: they are zero, or NaN where A's row
+// holds an infinity.
 template <int MODE>
 __device__ __forceinline__ void finish32(const Epilogue &ep, int64_t row, int64_t n0, int count, float (&v)[32]) {
+    const bool full = count == 32 && ep.vec;
     if constexpr (MODE == kForward) {
-        if (ep.bias)
-            for (int j = 0; j < count; ++j) v[j] += load_any(ep.bias, n0 + j, ep.bias_f32);
+        if (ep.bias) add32(ep.bias, n0, ep.bias_f32, full, count, v);
         if (ep.q) {
             uint32_t top = 0;
-            for (int j = 0; j < 32; ++j) top = max(top, j < count ? magnitude_bits(v[j]) : 0u);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                if (j >= count) v[j] = 0.0f;
+                top = max(top, magnitude_bits(v[j]));
+            }
             const Step step = step_of(top);
             const int64_t u = row * ep.groups + n0 / kGroup;
-            for (int j = 0; j < 32; ++j) ep.q[u * kGroup + j] = j < count ? (int8_t)quantise(v[j], step) : 0;
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = quantise4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3], step);
+            uint4 *q = reinterpret_cast<uint4 *>(ep.q + u * kGroup);
+            q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            q[1] = make_uint4(w[4], w[5], w[6], w[7]);
             ep.e[u] = (uint8_t)step.e;
         }
         with_act(ep.act, [&](auto a) {
+#pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = act_value<decltype(a)::value>(v[j]);
         });
     }
@@ -45,76 +111,302 @@ __device__ __forceinline__ void finish32(const Epilogue &ep, int64_t row, int64_
         if (ep.q) {
             const int64_t u = row * ep.groups + n0 / kGroup;
             const float step = step_value(ep.e[u]);
+            const uint4 *q = reinterpret_cast<const uint4 *>(ep.q + u * kGroup);
+            const uint4 q0 = q[0], q1 = q[1];
+            const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
             with_act(ep.act, [&](auto a) {
-                for (int j = 0; j < 32; ++j) v[j] *= act_slope<decltype(a)::value>((float)ep.q[u * kGroup + j] * step);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] *= act_slope<decltype(a)::value>(dequantise(w[j / 4], j % 4, step));
             });
         }
     }
-    for (int j = 0; j < count; ++j) {
-        if (ep.res) v[j] += load_any(ep.res, row * ep.ldr + n0 + j, ep.res_f32);
-        if (ep.out_f32)
-            static_cast<float *>(ep.out)[row * ep.ldo + n0 + j] = v[j];
-        else
-            static_cast<uint16_t *>(ep.out)[row * ep.ldo + n0 + j] = (uint16_t)f32_to_bf16_bits(v[j]);
+    if (ep.res) add32(ep.res, row * ep.ldr + n0, ep.res_f32, full, count, v);
+    if (ep.out_f32) {
+        float *p = static_cast<float *>(ep.out) + row * ep.ldo + n0;
+        if (full) {
+#pragma unroll
+            for (int g = 0; g < 8; ++g) reinterpret_cast<float4 *>(p)[g] = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (j < count) p[j] = v[j];
+        }
+    } else {
+        uint16_t *p = static_cast<uint16_t *>(ep.out) + row * ep.ldo + n0;
+        if (full) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float *x = v + 8 * g;
+                reinterpret_cast<uint4 *>(p)[g] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (j < count) p[j] = (uint16_t)f32_to_bf16_bits(v[j]);
+        }
     }
 }
 
-// out[rows, cols] = sum over kk of A(row, kk) * B(kk, col); A(i, j) is at
-// a[i * a_row + j * a_k] and so on, and A may be an 8-bit checkpoint read
-// across its rows (act(z), rounded to bf16 as the tensor cores take it)
-struct Product {
-    const uint16_t *a, *b;
-    const int8_t *aq;
-    const uint8_t *ae;
-    int64_t a_row, a_k, b_k, b_col, a_groups;
-    int64_t rows, cols, k;
-    int a_act;
-    Epilogue ep;
+// ---------------------------------------------------------------------------
+// tcgen05, TMA and mbarrier instructions
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// wait for a phase, with the library's limit; the clock is read only where the
+// phase is not over yet
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+    uint32_t over;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(over) : "r"(bar), "r"(parity) : "memory");
+    return over || mbar_wait_bounded(bar, parity, kWaitLimitNs);
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+}
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Shared-memory operand descriptor of a 128-byte swizzled tile: start
+// address, the two strides between 8-row (1024-byte) swizzle atoms, in 16-byte
+// units.  K-major: atoms of 8 rows x 64 k, `sbo` from one 8 rows to the next,
+// lbo unused.  MN-major: atoms of 64 rows x 8 k, `lbo` from one 64 rows to the
+// next, `sbo` from one 8 k to the next.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// ---------------------------------------------------------------------------
+// the product
+
+constexpr int kBM = 128, kBK = 64;
+constexpr int kEpilogueWarps = 8;
+constexpr int kProductThreads = (kEpilogueWarps + 2) * 32;
+constexpr int kGroupM = 16;  // row tiles that share the columns' tiles in L2
+
+template <int BN>
+struct Shape {
+    static constexpr int kABytes = kBM * kBK * 2, kBBytes = BN * kBK * 2;
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+    static constexpr int kTmemCols = 2 * BN;  // two tiles' sums: one is finished while the next is made
+    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024 + 256;
 };
 
-template <int MODE>
-__global__ void __launch_bounds__(128) product_kernel(const Product p) {
-    __shared__ float ta[32][65], tb[32][65], acc_s[64][65];
-    pdl_enter();
-    const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
-    const int tr = threadIdx.x / 16 * 8, tc = threadIdx.x % 16 * 4;
-    float acc[8][4] = {};
-    for (int64_t k0 = 0; k0 < p.k; k0 += 32) {
-        for (int u = threadIdx.x; u < 32 * 64; u += 128) {
-            const int i = u % 64, kk = u / 64;
-            float av = 0.0f, bv = 0.0f;
-            if (k0 + kk < p.k && r0 + i < p.rows) {
-                if (p.aq) {
-                    const int64_t t = k0 + kk, c = r0 + i, g = t * p.a_groups + c / kGroup;
-                    float z = (float)p.aq[g * kGroup + c % kGroup] * step_value(p.ae[g]);
-                    with_act(p.a_act, [&](auto a) { z = act_value<decltype(a)::value>(z); });
-                    av = round_bf16(z);
-                } else {
-                    av = bf16_bits_to_f32(p.a[(r0 + i) * p.a_row + (k0 + kk) * p.a_k]);
-                }
-            }
-            if (k0 + kk < p.k && c0 + i < p.cols) bv = bf16_bits_to_f32(p.b[(k0 + kk) * p.b_k + (c0 + i) * p.b_col]);
-            ta[kk][i] = av;
-            tb[kk][i] = bv;
-        }
-        __syncthreads();
-        for (int kk = 0; kk < 32; ++kk)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(ta[kk][tr + i], tb[kk][tc + j], acc[i][j]);
-        __syncthreads();
-    }
-    for (int i = 0; i < 8; ++i)
-        for (int j = 0; j < 4; ++j) acc_s[tr + i][tc + j] = acc[i][j];
-    __syncthreads();
-    const int64_t row = r0 + threadIdx.x % 64, n0 = c0 + threadIdx.x / 64 * 32;
-    if (row >= p.rows || n0 >= p.cols) return;
-    float v[32];
-    for (int j = 0; j < 32; ++j) v[j] = acc_s[threadIdx.x % 64][threadIdx.x / 64 * 32 + j];
-    finish32<MODE>(p.ep, row, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
+struct alignas(64) Product {
+    CUtensorMap a, b;
+    Epilogue ep;
+    unsigned int *err;
+    int64_t rows, cols;
+    int tiles_m, tiles_n, steps;  // steps of kBK along k
+};
+
+// tile number -> its row and column: bands of kGroupM row tiles, down the band first
+__device__ __forceinline__ void tile_at(const Product &p, int tile, int *tm, int *tn) {
+    const int band = kGroupM * p.tiles_n;
+    const int first = tile / band * kGroupM;
+    const int height = p.tiles_m - first < kGroupM ? p.tiles_m - first : kGroupM;
+    const int in = tile - tile / band * band;
+    *tm = first + in % height;
+    *tn = in / height;
 }
 
+template <int MODE, int BN>
+__global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __grid_constant__ Product p) {
+    using S = Shape<BN>;
+    constexpr bool kAmn = MODE == kWgrad, kBmn = MODE != kDgrad;
+    extern __shared__ unsigned char raw[];
+    unsigned char *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    const uint32_t tiles = smem_addr(smem);
+    const uint32_t bars = tiles + S::kStages * S::kStageBytes;
+    const uint32_t full = bars, empty = full + 8 * S::kStages, done = empty + 8 * S::kStages, freed = done + 16, drained = freed + 16;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kStages * S::kStageBytes + 16 * S::kStages + 40);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+
+    if (warp == kEpilogueWarps) {
+        if (lane == 0) {
+            for (int s = 0; s < S::kStages; ++s) {
+                mbar_init(full + 8 * s, 1);
+                mbar_init(empty + 8 * s, 1);
+            }
+            for (int s = 0; s < 2; ++s) {
+                mbar_init(done + 8 * s, 1);
+                mbar_init(freed + 8 * s, kEpilogueWarps);
+            }
+            mbar_init(drained, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+    } else if (warp == kEpilogueWarps + 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)), "n"(S::kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const uint32_t tmem = *tmem_slot;
+    pdl_enter();
+
+    const int tile_count = p.tiles_m * p.tiles_n;
+    bool ok = true;
+    if (warp == kEpilogueWarps) {
+        if (lane == 0) {  // TMA
+            int s = 0;
+            uint32_t phase = 0;
+            int64_t issued = 0;
+            for (int tile = blockIdx.x; tile < tile_count && ok; tile += gridDim.x) {
+                int tm, tn;
+                tile_at(p, tile, &tm, &tn);
+                for (int k = 0; k < p.steps; ++k) {
+                    if (!(ok = wait(empty + 8 * s, phase ^ 1))) break;
+                    const uint32_t bar = full + 8 * s, a = tiles + s * S::kStageBytes, b = a + S::kABytes;
+                    mbar_expect(bar, S::kStageBytes);
+                    if constexpr (kAmn) {
+#pragma unroll
+                        for (int j = 0; j < kBM / 64; ++j) tma_load(a + j * 8192, &p.a, tm * kBM + j * 64, k * kBK, bar);
+                    } else {
+                        tma_load(a, &p.a, k * kBK, tm * kBM, bar);
+                    }
+                    if constexpr (kBmn) {
+#pragma unroll
+                        for (int j = 0; j < BN / 64; ++j) tma_load(b + j * 8192, &p.b, tn * BN + j * 64, k * kBK, bar);
+                    } else {
+                        tma_load(b, &p.b, k * kBK, tn * BN, bar);
+                    }
+                    ++issued;
+                    if (++s == S::kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            // shared memory must outlive the copies: the last ones' barriers
+            for (int64_t i = issued > S::kStages ? issued - S::kStages : 0; i < issued; ++i)
+                ok &= wait(full + 8 * (uint32_t)(i % S::kStages), (uint32_t)(i / S::kStages) & 1);
+        }
+    } else if (warp == kEpilogueWarps + 1) {
+        if (lane == 0) {  // tcgen05.mma
+            constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (kAmn ? 1u << 15 : 0) | (kBmn ? 1u << 16 : 0) | (BN / 8) << 17 | (kBM / 16) << 24;
+            int s = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            for (int tile = blockIdx.x; tile < tile_count && ok; tile += gridDim.x) {
+                if (!(ok = wait(freed + 8 * acc, acc_phase ^ 1))) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                for (int k = 0; k < p.steps; ++k) {
+                    if (!(ok = wait(full + 8 * s, phase))) break;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    const uint32_t a = tiles + s * S::kStageBytes, b = a + S::kABytes;
+#pragma unroll
+                    for (int j = 0; j < kBK / 16; ++j) {
+                        const uint64_t da = kAmn ? operand(a + j * 2048, 8192, 1024) : operand(a + j * 32, 16, 1024);
+                        const uint64_t db = kBmn ? operand(b + j * 2048, 8192, 1024) : operand(b + j * 32, 16, 1024);
+                        mma_bf16(tmem + acc * BN, da, db, idesc, k > 0 || j > 0);
+                    }
+                    mma_commit(empty + 8 * s);
+                    if (++s == S::kStages) {
+                        s = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+                mma_commit(done + 8 * acc);
+                if (++acc == 2) {
+                    acc = 0;
+                    acc_phase ^= 1;
+                }
+            }
+            // TMEM must outlive the products, also where a wait gave up
+            mma_commit(drained);
+            ok &= wait(drained, 0);
+        }
+    } else {
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        const int half = warp / 4;  // of the tile's columns
+        for (int tile = blockIdx.x; tile < tile_count; tile += gridDim.x) {
+            int tm, tn;
+            tile_at(p, tile, &tm, &tn);
+            ok = wait(done + 8 * acc, acc_phase);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const int64_t row = (int64_t)tm * kBM + warp % 4 * 32 + lane;
+            const int64_t c0 = (int64_t)tn * BN + half * (BN / 2);
+#pragma unroll 1
+            for (int c = 0; c < BN / 2; c += 32) {
+                if (c0 + c >= p.cols) break;
+                float v[32];
+                tmem_load32(tmem + acc * BN + half * (BN / 2) + c + ((uint32_t)(warp % 4 * 32) << 16), v);
+                if (p.steps == 0) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                }
+                const int count = (int)(p.cols - c0 - c < 32 ? p.cols - c0 - c : 32);
+                if (row < p.rows) finish32<MODE>(p.ep, row, c0 + c, count, v);
+                __syncwarp();
+            }
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            if (lane == 0) mbar_arrive(freed + 8 * acc);
+            if (++acc == 2) {
+                acc = 0;
+                acc_phase ^= 1;
+            }
+        }
+    }
+    if (!ok) atomicOr(p.err, 1u);
+    __syncwarp();
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (warp == kEpilogueWarps + 1) {
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kTmemCols));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// operands that TMA cannot read where they lie
+
+// rows x cols of bf16 at any stride, copied to rows `ldo` apart (a multiple of 8)
+constexpr int kStageThreads = 256;
+__global__ void __launch_bounds__(kStageThreads) lay_out_kernel(const uint16_t *x, int64_t ld, int64_t rows, int64_t cols, uint16_t *out, int64_t ldo) {
+    pdl_enter();
+    const int64_t units = ceil_div<int64_t>(cols, 8);  // of 8 columns
+    const int64_t total = rows * units;
+    for (int64_t u = (int64_t)blockIdx.x * kStageThreads + threadIdx.x; u < total; u += (int64_t)gridDim.x * kStageThreads) {
+        const int64_t r = u / units, c = (u - r * units) * 8;
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t lo = c + 2 * k < cols ? x[r * ld + c + 2 * k] : 0, hi = c + 2 * k + 1 < cols ? x[r * ld + c + 2 * k + 1] : 0;
+            w[k] = lo | hi << 16;
+        }
+        *reinterpret_cast<uint4 *>(out + r * ldo + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// column sums of a bf16 matrix
 __global__ void __launch_bounds__(128) column_sum_kernel(const uint16_t *dy, int64_t ld, int64_t m, int64_t n, int accumulate, float *db) {
     pdl_enter();
     const int64_t c = (int64_t)blockIdx.x * 128 + threadIdx.x;
@@ -124,19 +416,129 @@ __global__ void __launch_bounds__(128) column_sum_kernel(const uint16_t *dy, int
     db[c] = accumulate ? db[c] + s : s;
 }
 
+// ---------------------------------------------------------------------------
+// host
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static const EncodeTiled f = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return f;
+}
+
+// 64 columns by box_rows rows of a row-major bf16 matrix, 128-byte swizzled; what lies outside reads as zero
+cudaError_t tensor_map(CUtensorMap *map, const Mat &a, int box_rows) {
+    const EncodeTiled f = encode_tiled();
+    if (f == nullptr) return cudaErrorNotSupported;
+    const int64_t pitch = a.rows > 1 ? a.pitch() : ceil_div<int64_t>(a.row_bytes(), 16) * 16;
+    const cuuint64_t dims[2] = {(cuuint64_t)a.cols, (cuuint64_t)a.rows}, strides[1] = {(cuuint64_t)pitch};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, ones[2] = {1, 1};
+    const CUresult r = f(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(a.data), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+bool tma_readable(const Mat &a) { return a.aligned(16) && (a.rows <= 1 || a.pitch() < ((int64_t)1 << 40)); }
+
+int64_t laid_out_bytes(int64_t rows, int64_t cols) { return ceil_div<int64_t>(rows * ceil_div<int64_t>(cols, 8) * 16, 256) * 256; }
+
+// The caller's workspace, handed out front to back.
+struct Workspace {
+    char *at, *end;
+    bool ok;
+    Workspace(void *ws, size_t bytes)
+        : at(static_cast<char *>(ws)), end(at + bytes), ok(ws == nullptr || reinterpret_cast<uintptr_t>(ws) % 16 == 0) {
+        if (ws == nullptr) end = at;
+    }
+    void *take(int64_t bytes) {
+        if (!ok || bytes > end - at) return nullptr;
+        char *p = at;
+        at += bytes;
+        return p;
+    }
+};
+
+// a place in the workspace for an operand that TMA cannot read in place
+bool place(const Mat &a, Workspace *ws, Mat *out) {
+    *out = a;
+    if (a.empty() || tma_readable(a)) return true;
+    out->ld = ceil_div<int64_t>(a.cols, 8) * 8;
+    out->data = ws->take(laid_out_bytes(a.rows, a.cols));
+    return out->data != nullptr;
+}
+
+cudaError_t lay_out(const Mat &a, const Mat &placed, cudaStream_t s) {
+    if (a.data == placed.data) return cudaSuccess;
+    const int64_t blocks = ceil_div<int64_t>(a.rows * ceil_div<int64_t>(a.cols, 8), kStageThreads);
+    return launch_pdl(lay_out_kernel, blocks < 152 * 16 ? blocks : 152 * 16, kStageThreads, 0, s, static_cast<const uint16_t *>(a.data), a.ld, a.rows, a.cols,
+                      static_cast<uint16_t *>(const_cast<void *>(placed.data)), placed.ld);
+}
+
+cudaError_t sm_count(int *out) {
+    static std::atomic<int> known{0};
+    int n = known.load(std::memory_order_relaxed);
+    if (n == 0) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        known.store(n, std::memory_order_relaxed);
+    }
+    *out = n;
+    return cudaSuccess;
+}
+
+template <int MODE, int BN>
+cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaStream_t s) {
+    using S = Shape<BN>;
+    p.tiles_m = (int)ceil_div<int64_t>(p.rows, kBM);
+    p.tiles_n = (int)ceil_div<int64_t>(p.cols, BN);
+    cudaError_t e = cudaSuccess;
+    if (p.steps > 0) {
+        e = tensor_map(&p.a, a, MODE == kWgrad ? kBK : kBM);
+        if (e == cudaSuccess) e = tensor_map(&p.b, b, MODE == kDgrad ? BN : kBK);
+        if (e != cudaSuccess) return e;
+    }
+    static std::atomic<uint64_t> opted_in{0};  // a bit per device
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(opted_in.load(std::memory_order_acquire) >> dev & 1)) {
+        e = cudaFuncSetAttribute(product_kernel<MODE, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) opted_in.fetch_or((uint64_t)1 << dev, std::memory_order_acq_rel);
+    }
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    return launch_pdl(product_kernel<MODE, BN>, tiles < sms ? tiles : sms, kProductThreads, S::kSmem, s, p);
+}
+
+// out (rows x cols) = epilogue(A B); a and b as they lie in memory
 template <int MODE>
-cudaError_t launch_product(const Product &p, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ceil_div<int64_t>(p.cols, 64), (unsigned)ceil_div<int64_t>(p.rows, 64));
-    cfg.blockDim = dim3(128);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = RA_PDL;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, product_kernel<MODE>, p);
-    return e == cudaSuccess ? cudaGetLastError() : e;
+cudaError_t launch_product(const Mat &a, const Mat &b, int64_t rows, int64_t cols, int64_t k, Epilogue ep, const Mat &out, const Mat &bias, const Mat &res,
+                           cudaStream_t s) {
+    Product p = {};
+    p.ep = ep;
+    p.ep.vec = out.aligned(16) && (bias.empty() || bias.aligned(16)) && (res.empty() || res.aligned(16));
+    p.rows = rows;
+    p.cols = cols;
+    p.steps = (int)ceil_div<int64_t>(k, kBK);
+    int sms = 0;
+    cudaError_t e = device_error_word(&p.err);
+    if (e == cudaSuccess) e = sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    const int64_t tm = ceil_div<int64_t>(rows, kBM);
+    if (tm * ceil_div<int64_t>(cols, 64) >= kMaxExtent) return cudaErrorInvalidValue;
+    if (tm * ceil_div<int64_t>(cols, 128) <= sms / 2) return launch_tiles<MODE, 64>(p, a, b, sms, s);
+    if (tm * ceil_div<int64_t>(cols, 256) <= sms / 2) return launch_tiles<MODE, 128>(p, a, b, sms, s);
+    return launch_tiles<MODE, 256>(p, a, b, sms, s);
 }
 
 // the checkpoint's two arrays as matrices
@@ -162,20 +564,21 @@ extern "C" {
 
 size_t ra_linear_workspace_bytes(int64_t m, int64_t k, int64_t n) {
     if (m < 0 || k < 0 || n < 0 || m >= kMaxExtent || k >= kMaxExtent || n >= kMaxExtent) return 0;
-    return 0;
+    // at most two of the three matrices are laid out in one call
+    const int64_t mk = laid_out_bytes(m, k), kn = laid_out_bytes(k, n), mn = laid_out_bytes(m, n);
+    const int64_t least = mk < kn ? (mk < mn ? mk : mn) : (kn < mn ? kn : mn);
+    return (size_t)(mk + kn + mn - least);
 }
 
 ra_status ra_linear(const void *x, int64_t ld_x, const void *w, int64_t ld_w, int64_t m, int64_t k, int64_t n,
                     const void *bias, int bias_dtype, int act, const void *residual, int64_t ld_res, int res_dtype,
                     int8_t *save_q, uint8_t *save_e, void *y, int64_t ld_y, int y_dtype, void *ws, size_t ws_bytes,
                     void *stream) {
-    (void)ws;
-    (void)ws_bytes;
     const int ysz = esize(y_dtype);
     if (ysz == 0 || !act_ok(act)) return RA_ERR_INVALID_ARG;
     if ((bias && esize(bias_dtype) == 0) || (residual && esize(res_dtype) == 0)) return RA_ERR_INVALID_ARG;
     const Mat mx{x, m, k, ld_x, 2}, mw{w, k, n, ld_w, 2}, my{y, m, n, ld_y, ysz};
-    const Mat mb{bias, 1, bias ? n : 0, n, bias ? esize(bias_dtype) : 1};
+    const Mat mb{bias, bias ? 1 : 0, n, n, bias ? esize(bias_dtype) : 1};
     const Mat mr{residual, residual ? m : 0, n, residual ? ld_res : n, residual ? esize(res_dtype) : 1};
     if (!mat_ok(mx) || !mat_ok(mw) || !mat_ok(my) || !mat_ok(mb) || !mat_ok(mr)) return RA_ERR_INVALID_ARG;
     const Kept kept = kept_mats(save_q, save_e, m, n);
@@ -189,25 +592,27 @@ ra_status ra_linear(const void *x, int64_t ld_x, const void *w, int64_t ld_w, in
             if (mats_overlap(kept.q, *o) || mats_overlap(kept.e, *o)) return RA_ERR_OVERLAP;
         if (mats_overlap(kept.q, kept.e)) return RA_ERR_OVERLAP;
     }
-    Product p = {};
-    p.a = static_cast<const uint16_t *>(x);
-    p.b = static_cast<const uint16_t *>(w);
-    p.a_row = ld_x;
-    p.a_k = 1;
-    p.b_k = ld_w;
-    p.b_col = 1;
-    p.rows = m;
-    p.cols = n;
-    p.k = k;
-    p.ep = Epilogue{y, bias, residual, save_q, save_e, ld_y, ld_res, ceil_div<int64_t>(n, kGroup), y_dtype == RA_F32, bias_dtype == RA_F32, res_dtype == RA_F32, act};
-    return cuda_status(launch_product<kForward>(p, static_cast<cudaStream_t>(stream)));
+    Workspace space(ws, ws_bytes);
+    Mat a, b;
+    if (!place(mx, &space, &a) || !place(mw, &space, &b)) return RA_ERR_INVALID_ARG;
+    if (a.data != x || b.data != w) {
+        const Mat wm{ws, 1, (int64_t)ws_bytes, (int64_t)ws_bytes, 1};
+        const Mat *all[] = {&mx, &mw, &my, &mb, &mr, &kept.q, &kept.e};
+        for (int i = 0; i < (save_q ? 7 : 5); ++i)
+            if (mats_overlap(wm, *all[i])) return RA_ERR_OVERLAP;
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = lay_out(mx, a, s);
+    if (e == cudaSuccess) e = lay_out(mw, b, s);
+    if (e != cudaSuccess) return cuda_status(e);
+    const Epilogue ep{y, bias, residual, save_q, save_e, ld_y, ld_res, ceil_div<int64_t>(n, kGroup), y_dtype == RA_F32, bias_dtype == RA_F32,
+                      res_dtype == RA_F32, act, 0};
+    return cuda_status(launch_product<kForward>(a, b, m, n, k, ep, my, mb, mr, s));
 }
 
 ra_status ra_linear_dgrad(const void *dy, int64_t ld_dy, const void *w, int64_t ld_w, int64_t m, int64_t k, int64_t n,
                           const int8_t *z_q, const uint8_t *z_e, int act, const void *residual, int64_t ld_res, int res_dtype,
                           void *dx, int64_t ld_dx, int dx_dtype, void *ws, size_t ws_bytes, void *stream) {
-    (void)ws;
-    (void)ws_bytes;
     const int xsz = esize(dx_dtype);
     if (xsz == 0 || !act_ok(act) || (residual && esize(res_dtype) == 0)) return RA_ERR_INVALID_ARG;
     const Mat md{dy, m, n, ld_dy, 2}, mw{w, k, n, ld_w, 2}, mx{dx, m, k, ld_dx, xsz};
@@ -219,32 +624,33 @@ ra_status ra_linear_dgrad(const void *dy, int64_t ld_dy, const void *w, int64_t 
     if (mats_overlap(mx, md) || mats_overlap(mx, mw)) return RA_ERR_OVERLAP;
     if (mats_overlap(mx, mr) && !same_mat(mx, mr)) return RA_ERR_OVERLAP;
     if (act != RA_ACT_NONE && (mats_overlap(mx, kept.q) || mats_overlap(mx, kept.e))) return RA_ERR_OVERLAP;
-    Product p = {};
-    p.a = static_cast<const uint16_t *>(dy);
-    p.b = static_cast<const uint16_t *>(w);
-    p.a_row = ld_dy;
-    p.a_k = 1;
-    p.b_k = 1;
-    p.b_col = ld_w;
-    p.rows = m;
-    p.cols = k;
-    p.k = n;
-    p.ep = Epilogue{dx, nullptr, residual, act ? const_cast<int8_t *>(z_q) : nullptr, const_cast<uint8_t *>(z_e), ld_dx, ld_res,
-                    ceil_div<int64_t>(k, kGroup), dx_dtype == RA_F32, 0, res_dtype == RA_F32, act};
-    return cuda_status(launch_product<kDgrad>(p, static_cast<cudaStream_t>(stream)));
+    Workspace space(ws, ws_bytes);
+    Mat a, b;
+    if (!place(md, &space, &a) || !place(mw, &space, &b)) return RA_ERR_INVALID_ARG;
+    if (a.data != dy || b.data != w) {
+        const Mat wm{ws, 1, (int64_t)ws_bytes, (int64_t)ws_bytes, 1};
+        const Mat *all[] = {&md, &mw, &mx, &mr, &kept.q, &kept.e};
+        for (int i = 0; i < (act != RA_ACT_NONE ? 6 : 4); ++i)
+            if (mats_overlap(wm, *all[i])) return RA_ERR_OVERLAP;
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = lay_out(md, a, s);
+    if (e == cudaSuccess) e = lay_out(mw, b, s);
+    if (e != cudaSuccess) return cuda_status(e);
+    const Epilogue ep{dx, nullptr, residual, act ? const_cast<int8_t *>(z_q) : nullptr, const_cast<uint8_t *>(z_e), ld_dx, ld_res,
+                      ceil_div<int64_t>(k, kGroup), dx_dtype == RA_F32, 0, res_dtype == RA_F32, act, 0};
+    return cuda_status(launch_product<kDgrad>(a, b, m, k, n, ep, mx, Mat{nullptr, 0, 0, 0, 1}, mr, s));
 }
 
 ra_status ra_linear_wgrad(const void *x, int64_t ld_x, const int8_t *z_q, const uint8_t *z_e, int act, const void *dy,
                           int64_t ld_dy, int64_t m, int64_t k, int64_t n, int accumulate, void *dw, int64_t ld_dw,
                           int dw_dtype, float *db, void *ws, size_t ws_bytes, void *stream) {
-    (void)ws;
-    (void)ws_bytes;
     const int wsz = esize(dw_dtype);
     const bool from_kept = x == nullptr && (z_q != nullptr || z_e != nullptr);
     if (wsz == 0 || !act_ok(act) || (!from_kept && act != RA_ACT_NONE)) return RA_ERR_INVALID_ARG;
     if (x != nullptr && (z_q != nullptr || z_e != nullptr)) return RA_ERR_INVALID_ARG;
     const Mat mx{x, from_kept ? 0 : m, k, from_kept ? k : ld_x, 2}, md{dy, m, n, ld_dy, 2}, mw{dw, k, n, ld_dw, wsz};
-    const Mat mb{db, 1, db ? n : 0, n, 4};
+    const Mat mb{db, db ? 1 : 0, n, n, 4};
     if (!mat_ok(mx) || !mat_ok(md) || !mat_ok(mw) || !mat_ok(mb)) return RA_ERR_INVALID_ARG;
     if (m < 0 || m >= kMaxExtent) return RA_ERR_INVALID_ARG;
     const Kept kept = kept_mats(z_q, z_e, m, k);
@@ -254,30 +660,36 @@ ra_status ra_linear_wgrad(const void *x, int64_t ld_x, const int8_t *z_q, const 
         if (mats_overlap(mw, *in[i]) || mats_overlap(mb, *in[i])) return RA_ERR_OVERLAP;
     if (mats_overlap(mw, mb)) return RA_ERR_OVERLAP;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    Workspace space(ws, ws_bytes);
     if (!mw.empty()) {
-        Product p = {};
-        p.a = static_cast<const uint16_t *>(x);
-        p.aq = from_kept ? z_q : nullptr;
-        p.ae = z_e;
-        p.a_groups = ceil_div<int64_t>(k, kGroup);
-        p.a_act = act;
-        p.b = static_cast<const uint16_t *>(dy);
-        p.a_row = 1;
-        p.a_k = ld_x;
-        p.b_k = ld_dy;
-        p.b_col = 1;
-        p.rows = k;
-        p.cols = n;
-        p.k = m;
-        p.ep = Epilogue{dw, nullptr, accumulate ? dw : nullptr, nullptr, nullptr, ld_dw, ld_dw, 0, dw_dtype == RA_F32, 0, dw_dtype == RA_F32, 0};
-        const cudaError_t e = launch_product<kWgrad>(p, s);
+        Mat a, b;
+        if (from_kept) {
+            // the checkpoint's values (after the activation) as bf16 rows
+            a = Mat{nullptr, m, k, ceil_div<int64_t>(k, 8) * 8, 2};
+            if (!a.empty() && (a.data = space.take(laid_out_bytes(m, k))) == nullptr) return RA_ERR_INVALID_ARG;
+        } else if (!place(mx, &space, &a)) {
+            return RA_ERR_INVALID_ARG;
+        }
+        if (!place(md, &space, &b)) return RA_ERR_INVALID_ARG;
+        if (a.data != x || b.data != dy) {
+            const Mat wm{ws, 1, (int64_t)ws_bytes, (int64_t)ws_bytes, 1};
+            const Mat *all[] = {&mx, &md, &mw, &mb, &kept.q, &kept.e};
+            for (int i = 0; i < (from_kept ? 6 : 4); ++i)
+                if (mats_overlap(wm, *all[i])) return RA_ERR_OVERLAP;
+        }
+        if (from_kept && !a.empty()) {
+            const ra_status st = ra_checkpoint8_unpack(z_q, z_e, m, k, act, const_cast<void *>(a.data), a.ld, RA_BF16, stream);
+            if (st != RA_OK) return st;
+        }
+        cudaError_t e = from_kept ? cudaSuccess : lay_out(mx, a, s);
+        if (e == cudaSuccess) e = lay_out(md, b, s);
+        if (e != cudaSuccess) return cuda_status(e);
+        const Epilogue ep{dw, nullptr, accumulate ? dw : nullptr, nullptr, nullptr, ld_dw, ld_dw, 0, dw_dtype == RA_F32, 0, dw_dtype == RA_F32, 0, 0};
+        e = launch_product<kWgrad>(a, b, k, n, m, ep, mw, Mat{nullptr, 0, 0, 0, 1}, accumulate ? mw : Mat{nullptr, 0, 0, 0, 1}, s);
         if (e != cudaSuccess) return cuda_status(e);
     }
-    if (!mb.empty()) {
-        cudaLaunchConfig_t cfg = {};
-        (void)cfg;
+    if (!mb.empty())
         return cuda_status(launch_pdl(column_sum_kernel, ceil_div<int64_t>(n, 128), 128, 0, s, static_cast<const uint16_t *>(dy), ld_dy, m, n, accumulate, db));
-    }
     return RA_OK;
 }
 
