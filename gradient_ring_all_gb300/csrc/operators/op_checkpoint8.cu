@@ -18,18 +18,123 @@ struct PackParams {
     int act;
 };
 
-// One warp a group, a lane an element: any stride and alignment.
+// Unit number -> row and unit within it.  32-bit division where the numbers
+// fit (an ordinary size): a 64-bit one costs as much as the rest of a unit's
+// work.
+__device__ __forceinline__ void row_of(int64_t u, int64_t per_row, int64_t total, int64_t *r, int64_t *k) {
+    if (total <= 0x7fffffff) {
+        const uint32_t q = (uint32_t)u / (uint32_t)per_row;
+        *r = q;
+        *k = (uint32_t)u - q * (uint32_t)per_row;
+    } else {
+        *r = u / per_row;
+        *k = u - *r * per_row;
+    }
+}
+
+// Rows on 16-byte boundaries: a thread takes half a group, 16 values, with
+// 16-byte loads and stores; two neighbouring lanes settle the group's step.
+// Bound by memory: x once in (2 or 4 bytes a value), 33/32 byte out.
+template <class T>
+__global__ void __launch_bounds__(kThreadsCkpt) pack_kernel(const PackParams p) {
+    pdl_enter();
+    const int64_t halves = 2 * p.groups, total = p.rows * halves;
+    const int64_t stride = (int64_t)gridDim.x * kThreadsCkpt;
+    // both lanes of a pair run or neither: `total` is even
+    for (int64_t u = (int64_t)blockIdx.x * kThreadsCkpt + threadIdx.x; u < total; u += stride) {
+        int64_t r, k;
+        row_of(u, halves, total, &r, &k);
+        const T *src = static_cast<const T *>(p.x) + r * p.ld + k * 16;
+        const int64_t left = p.cols - k * 16;
+        float x[16];
+        if (left >= 16) {
+            load_w<T, 16>(src, x);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = j < left ? to_f32<T>(src[j]) : 0.0f;
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) top = max(top, magnitude_bits(x[j]));
+        const uint32_t pair = 3u << (threadIdx.x & 30);
+        const Step step = step_of(max(top, __shfl_xor_sync(pair, top, 1)));
+        uint32_t w[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) w[g] = quantise4(x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3], step);
+        reinterpret_cast<uint4 *>(p.q)[u] = make_uint4(w[0], w[1], w[2], w[3]);
+        if ((u & 1) == 0) p.e[u / 2] = (uint8_t)step.e;
+    }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kThreadsCkpt) unpack_kernel(const PackParams p) {
+    pdl_enter();
+    const int64_t halves = 2 * p.groups, total = p.rows * halves;
+    const int64_t stride = (int64_t)gridDim.x * kThreadsCkpt;
+    for (int64_t u = (int64_t)blockIdx.x * kThreadsCkpt + threadIdx.x; u < total; u += stride) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p.q) + u);
+        const float step = step_value(__ldg(p.e + u / 2));
+        int64_t r, k;
+        row_of(u, halves, total, &r, &k);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = dequantise(w[j / 4], j % 4, step);
+        with_act(p.act, [&](auto a) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = act_value<decltype(a)::value>(v[j]);
+        });
+        T *dst = static_cast<T *>(p.out) + r * p.ld + k * 16;
+        const int64_t left = p.cols - k * 16;
+        if (left >= 16) {
+            store_w<T, 16>(dst, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (j < left) dst[j] = from_f32<T>(v[j]);
+        }
+    }
+}
+
+// Byte j of the result is byte (lane mod 4) of lane j's word, of the four
+// lanes that differ in their low two bits: a 4 x 4 transposition.
+__device__ __forceinline__ uint32_t transpose4(uint32_t w, int lane) {
+    uint32_t o = __shfl_xor_sync(0xffffffffu, w, 1);
+    w = lane & 1 ? __byte_perm(o, w, 0x7351) : __byte_perm(w, o, 0x6240);
+    o = __shfl_xor_sync(0xffffffffu, w, 2);
+    return lane & 2 ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
+}
+
+// Any stride and alignment: a warp takes four groups, a lane one value of
+// each, so the loads are coalesced whatever the row's start; the transposition
+// makes words of the bytes.
 template <class T>
 __global__ void __launch_bounds__(kThreadsCkpt) pack_scalar_kernel(const PackParams p) {
     pdl_enter();
     const int lane = threadIdx.x & 31;
-    const int64_t total = p.rows * p.groups, step = (int64_t)gridDim.x * (kThreadsCkpt / 32);
-    for (int64_t u = (int64_t)blockIdx.x * (kThreadsCkpt / 32) + threadIdx.x / 32; u < total; u += step) {
-        const int64_t r = u / p.groups, c = (u - r * p.groups) * kGroup + lane;
-        const float x = c < p.cols ? to_f32<T>(static_cast<const T *>(p.x)[r * p.ld + c]) : 0.0f;
-        const Step step8 = step_of(__reduce_max_sync(0xffffffffu, magnitude_bits(x)));
-        p.q[u * kGroup + lane] = (int8_t)quantise(x, step8);
-        if (lane == 0) p.e[u] = (uint8_t)step8.e;
+    const int64_t quads = ceil_div<int64_t>(p.groups, 4), total = p.rows * quads;
+    const int64_t stride = (int64_t)gridDim.x * (kThreadsCkpt / 32);
+    for (int64_t u = (int64_t)blockIdx.x * (kThreadsCkpt / 32) + threadIdx.x / 32; u < total; u += stride) {
+        int64_t r, k;
+        row_of(u, quads, total, &r, &k);
+        const T *src = static_cast<const T *>(p.x) + r * p.ld;
+        float x[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int64_t c = (k * 4 + g) * kGroup + lane;
+            x[g] = c < p.cols ? to_f32<T>(__ldg(src + c)) : 0.0f;
+        }
+        uint32_t w = 0, e = 0;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const Step step = step_of(__reduce_max_sync(0xffffffffu, magnitude_bits(x[g])));
+            w |= quantise(x[g], step) << (8 * g);
+            if (lane == g) e = step.e;
+        }
+        w = transpose4(w, lane);  // four neighbouring values of group lane % 4
+        const int64_t first = r * p.groups + k * 4;
+        if (k * 4 + (lane & 3) < p.groups) reinterpret_cast<uint32_t *>(p.q + (first + (lane & 3)) * kGroup)[lane / 4] = w;
+        if (lane < 4 && k * 4 + lane < p.groups) p.e[first + lane] = (uint8_t)e;
     }
 }
 
@@ -37,21 +142,34 @@ template <class T>
 __global__ void __launch_bounds__(kThreadsCkpt) unpack_scalar_kernel(const PackParams p) {
     pdl_enter();
     const int lane = threadIdx.x & 31;
-    const int64_t total = p.rows * p.groups, step = (int64_t)gridDim.x * (kThreadsCkpt / 32);
-    for (int64_t u = (int64_t)blockIdx.x * (kThreadsCkpt / 32) + threadIdx.x / 32; u < total; u += step) {
-        const int64_t r = u / p.groups, c = (u - r * p.groups) * kGroup + lane;
-        float v = (float)p.q[u * kGroup + lane] * step_value(p.e[u]);
-        with_act(p.act, [&](auto a) { v = act_value<decltype(a)::value>(v); });
-        if (c < p.cols) static_cast<T *>(p.out)[r * p.ld + c] = from_f32<T>(v);
+    const int64_t quads = ceil_div<int64_t>(p.groups, 4), total = p.rows * quads;
+    const int64_t stride = (int64_t)gridDim.x * (kThreadsCkpt / 32);
+    for (int64_t u = (int64_t)blockIdx.x * (kThreadsCkpt / 32) + threadIdx.x / 32; u < total; u += stride) {
+        int64_t r, k;
+        row_of(u, quads, total, &r, &k);
+        const int64_t first = r * p.groups + k * 4;
+        const bool in = k * 4 + (lane & 3) < p.groups;
+        const uint32_t e = in ? p.e[first + (lane & 3)] : 1;
+        uint32_t w = in ? reinterpret_cast<const uint32_t *>(p.q + (first + (lane & 3)) * kGroup)[lane / 4] : 0;
+        w = transpose4(w, lane);  // the lane's value of each of the four groups
+        T *dst = static_cast<T *>(p.out) + r * p.ld;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            float v = dequantise(w, g, step_value(__shfl_sync(0xffffffffu, e, g)));
+            with_act(p.act, [&](auto a) { v = act_value<decltype(a)::value>(v); });
+            const int64_t c = (k * 4 + g) * kGroup + lane;
+            if (c < p.cols) dst[c] = from_f32<T>(v);
+        }
     }
 }
 
-ra_status launch_ckpt(bool pack, int dtype, const PackParams &p, cudaStream_t s) {
-    const int64_t blocks = ceil_div<int64_t>(p.rows * p.groups, kThreadsCkpt / 32);
+template <class T>
+ra_status launch_ckpt(bool pack, bool wide, const PackParams &p, cudaStream_t s) {
+    const int64_t blocks = wide ? ceil_div<int64_t>(p.rows * p.groups * 2, kThreadsCkpt)
+                                : ceil_div<int64_t>(p.rows * ceil_div<int64_t>(p.groups, 4), kThreadsCkpt / 32);
     const int64_t grid = blocks < kMaxGrid ? blocks : kMaxGrid;
-    if (dtype == RA_F32)
-        return cuda_status(launch_pdl(pack ? pack_scalar_kernel<float> : unpack_scalar_kernel<float>, grid, kThreadsCkpt, 0, s, p));
-    return cuda_status(launch_pdl(pack ? pack_scalar_kernel<uint16_t> : unpack_scalar_kernel<uint16_t>, grid, kThreadsCkpt, 0, s, p));
+    return cuda_status(wide ? launch_pdl(pack ? pack_kernel<T> : unpack_kernel<T>, grid, kThreadsCkpt, 0, s, p)
+                            : launch_pdl(pack ? pack_scalar_kernel<T> : unpack_scalar_kernel<T>, grid, kThreadsCkpt, 0, s, p));
 }
 
 ra_status run_ckpt(bool pack, const void *x, int64_t ld, int dtype, int64_t rows, int64_t cols, int8_t *q, uint8_t *e,
@@ -66,7 +184,8 @@ ra_status run_ckpt(bool pack, const void *x, int64_t ld, int dtype, int64_t rows
     const Mat mq{q, rows, groups * kGroup, groups * kGroup, 1}, me{e, rows, groups, groups, 1};
     if (mats_overlap(a, mq) || mats_overlap(a, me) || mats_overlap(mq, me)) return RA_ERR_OVERLAP;
     const PackParams p{x, const_cast<void *>(x), ld, q, e, rows, cols, groups, act};
-    return launch_ckpt(pack, dtype, p, static_cast<cudaStream_t>(stream));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dtype == RA_F32 ? launch_ckpt<float>(pack, a.aligned(16), p, s) : launch_ckpt<uint16_t>(pack, a.aligned(16), p, s);
 }
 
 }  // namespace

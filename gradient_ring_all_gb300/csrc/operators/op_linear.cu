@@ -13,6 +13,8 @@
 // the epilogue warps read them from there.
 #include <cuda.h>
 
+#include <cooperative_groups.h>
+
 #include <atomic>
 
 #include "op_common.cuh"
@@ -200,12 +202,31 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lbo, uint32_
     return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
+// the next of the two sums in TMEM
+__device__ __forceinline__ void flip(int &acc, uint32_t &phase) {
+    acc ^= 1;
+    if (acc == 0) phase ^= 1;
+}
+// a warp has read its part of a sum
+__device__ __forceinline__ void release(uint32_t bar, int lane) {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    if (lane == 0) mbar_arrive(bar);
+    __syncwarp();
+}
+
 // ---------------------------------------------------------------------------
 // the product
 
 constexpr int kBM = 128, kBK = 64;
 constexpr int kEpilogueWarps = 8;
 constexpr int kProductThreads = (kEpilogueWarps + 2) * 32;
+// The tensor core adds to its binary32 sums by truncation: a sum over k comes
+// out about 1e-9 k short (measured: 2.3e-7 at k = 256, 4.4e-6 at 4096, 3.8e-5
+// at 32768, all toward zero).  That is far below a bf16 result's rounding, but
+// not below a binary32 one's: there the tensor core sums kChunk steps (256 of
+// k) at a time, and the epilogue warps add the chunks in registers with rounding
+// to nearest, while the next chunk is made.
+constexpr int kChunk = 4;
 constexpr int kGroupM = 16;  // row tiles that share the columns' tiles in L2
 
 template <int BN>
@@ -235,7 +256,7 @@ __device__ __forceinline__ void tile_at(const Product &p, int tile, int *tm, int
     *tn = in / height;
 }
 
-template <int MODE, int BN>
+template <int MODE, int BN, bool F32>
 __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __grid_constant__ Product p) {
     using S = Shape<BN>;
     constexpr bool kAmn = MODE == kWgrad, kBmn = MODE != kDgrad;
@@ -313,9 +334,16 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
             int s = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             for (int tile = blockIdx.x; tile < tile_count && ok; tile += gridDim.x) {
-                if (!(ok = wait(freed + 8 * acc, acc_phase ^ 1))) break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                for (int k = 0; k < p.steps; ++k) {
+                for (int k = 0; k < p.steps || k == 0; ++k) {
+                    if (F32 ? k % kChunk == 0 : k == 0) {  // a new sum
+                        if (!(ok = wait(freed + 8 * acc, acc_phase ^ 1))) break;
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    }
+                    if (p.steps == 0) {
+                        mma_commit(done + 8 * acc);
+                        flip(acc, acc_phase);
+                        break;
+                    }
                     if (!(ok = wait(full + 8 * s, phase))) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     const uint32_t a = tiles + s * S::kStageBytes, b = a + S::kABytes;
@@ -323,19 +351,17 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
                     for (int j = 0; j < kBK / 16; ++j) {
                         const uint64_t da = kAmn ? operand(a + j * 2048, 8192, 1024) : operand(a + j * 32, 16, 1024);
                         const uint64_t db = kBmn ? operand(b + j * 2048, 8192, 1024) : operand(b + j * 32, 16, 1024);
-                        mma_bf16(tmem + acc * BN, da, db, idesc, k > 0 || j > 0);
+                        mma_bf16(tmem + acc * BN, da, db, idesc, (F32 ? k % kChunk : k) > 0 || j > 0);
                     }
                     mma_commit(empty + 8 * s);
                     if (++s == S::kStages) {
                         s = 0;
                         phase ^= 1;
                     }
-                }
-                if (!ok) break;
-                mma_commit(done + 8 * acc);
-                if (++acc == 2) {
-                    acc = 0;
-                    acc_phase ^= 1;
+                    if (k + 1 == p.steps || (F32 && k % kChunk == kChunk - 1)) {
+                        mma_commit(done + 8 * acc);
+                        flip(acc, acc_phase);
+                    }
                 }
             }
             // TMEM must outlive the products, also where a wait gave up
@@ -343,35 +369,70 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
             ok &= wait(drained, 0);
         }
     } else {
+        constexpr int kHalf = BN / 2;  // each four warps finish half of the columns
         int acc = 0;
         uint32_t acc_phase = 0;
-        const int half = warp / 4;  // of the tile's columns
-        for (int tile = blockIdx.x; tile < tile_count; tile += gridDim.x) {
+        const uint32_t mine = tmem + (warp / 4) * kHalf + ((uint32_t)(warp % 4 * 32) << 16);
+        for (int tile = blockIdx.x; tile < tile_count && ok; tile += gridDim.x) {
             int tm, tn;
             tile_at(p, tile, &tm, &tn);
-            ok = wait(done + 8 * acc, acc_phase);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const int64_t row = (int64_t)tm * kBM + warp % 4 * 32 + lane;
-            const int64_t c0 = (int64_t)tn * BN + half * (BN / 2);
-#pragma unroll 1
-            for (int c = 0; c < BN / 2; c += 32) {
-                if (c0 + c >= p.cols) break;
-                float v[32];
-                tmem_load32(tmem + acc * BN + half * (BN / 2) + c + ((uint32_t)(warp % 4 * 32) << 16), v);
-                if (p.steps == 0) {
+            const int64_t c0 = (int64_t)tn * BN + warp / 4 * kHalf;
+            if constexpr (F32) {
+                float sum[kHalf / 32][32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                for (int g = 0; g < kHalf / 32; ++g)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum[g][j] = 0.0f;
+                for (int k = 0; k < p.steps || k == 0; k += kChunk) {
+                    ok = __all_sync(0xffffffffu, wait(done + 8 * acc, acc_phase));
+                    if (!ok) break;
+                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                    if (p.steps > 0) {
+#pragma unroll
+                        for (int g = 0; g < kHalf / 32; ++g) {
+                            float v[32];
+                            tmem_load32(mine + acc * BN + g * 32, v);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) sum[g][j] += v[j];
+                        }
+                    }
+                    release(freed + 8 * acc, lane);
+                    flip(acc, acc_phase);
                 }
-                const int count = (int)(p.cols - c0 - c < 32 ? p.cols - c0 - c : 32);
-                if (row < p.rows) finish32<MODE>(p.ep, row, c0 + c, count, v);
+                if (!ok) break;
+#pragma unroll 1
+                for (int g = 0; g < kHalf / 32; ++g) {
+                    float v[32];
+#pragma unroll
+                    for (int h = 0; h < kHalf / 32; ++h)
+                        if (g == h) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = sum[h][j];
+                        }
+                    const int64_t n0 = c0 + g * 32;
+                    if (row < p.rows && n0 < p.cols) finish32<MODE>(p.ep, row, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
+                }
                 __syncwarp();
-            }
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            if (lane == 0) mbar_arrive(freed + 8 * acc);
-            if (++acc == 2) {
-                acc = 0;
-                acc_phase ^= 1;
+            } else {
+                ok = __all_sync(0xffffffffu, wait(done + 8 * acc, acc_phase));
+                if (!ok) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll 1
+                for (int g = 0; g < kHalf / 32; ++g) {
+                    const int64_t n0 = c0 + g * 32;
+                    if (n0 >= p.cols) break;
+                    float v[32];
+                    tmem_load32(mine + acc * BN + g * 32, v);
+                    if (p.steps == 0) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                    }
+                    if (row < p.rows) finish32<MODE>(p.ep, row, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
+                    __syncwarp();
+                }
+                release(freed + 8 * acc, lane);
+                flip(acc, acc_phase);
             }
         }
     }
@@ -406,14 +467,57 @@ __global__ void __launch_bounds__(kStageThreads) lay_out_kernel(const uint16_t *
     }
 }
 
-// column sums of a bf16 matrix
-__global__ void __launch_bounds__(128) column_sum_kernel(const uint16_t *dy, int64_t ld, int64_t m, int64_t n, int accumulate, float *db) {
+// Column sums of a bf16 matrix (the bias gradient).  A block takes a strip of
+// LANES * W columns, W at a time per thread, and its share of the rows; the
+// blocks of a cluster share a strip, and the first of them adds the others'
+// sums, in order, out of their shared memory.  Bound by reading dy once.
+constexpr int kColumnThreads = 256;
+template <int W, int LANES>
+__global__ void __launch_bounds__(kColumnThreads) column_sum_kernel(const uint16_t *dy, int64_t ld, int64_t m, int64_t n, int accumulate, float *db) {
+    constexpr int kRowsAtOnce = kColumnThreads / LANES, kCols = LANES * W, kFlight = 4;
+    __shared__ float part[kRowsAtOnce][kCols + 1];
+    __shared__ float sum[kCols];
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
     pdl_enter();
-    const int64_t c = (int64_t)blockIdx.x * 128 + threadIdx.x;
-    if (c >= n) return;
-    float s = 0.0f;
-    for (int64_t r = 0; r < m; ++r) s += bf16_bits_to_f32(dy[r * ld + c]);
-    db[c] = accumulate ? db[c] + s : s;
+    const int share = blockIdx.y, shares = gridDim.y;
+    const int64_t r0 = m * share / shares, r1 = m * (share + 1) / shares;
+    const int64_t c = (int64_t)blockIdx.x * kCols + threadIdx.x % LANES * W;
+    float acc[W] = {};
+    if (c < n) {
+        for (int64_t r = r0 + threadIdx.x / LANES; r < r1; r += kRowsAtOnce * kFlight) {
+            float x[kFlight][W];
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f) {
+                if (r + f * kRowsAtOnce < r1) {
+                    load_w<uint16_t, W>(dy + (r + f * kRowsAtOnce) * ld + c, x[f]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) x[f][j] = 0.0f;
+                }
+            }
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f)
+#pragma unroll
+                for (int j = 0; j < W; ++j) acc[j] += x[f][j];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < W; ++j) part[threadIdx.x / LANES][threadIdx.x % LANES * W + j] = acc[j];
+    __syncthreads();
+    if (threadIdx.x < kCols) {
+        float s = part[0][threadIdx.x];
+        for (int g = 1; g < kRowsAtOnce; ++g) s += part[g][threadIdx.x];
+        sum[threadIdx.x] = s;
+    }
+    cluster.sync();
+    if (share == 0 && threadIdx.x < kCols) {
+        float s = sum[threadIdx.x];
+        for (int q = 1; q < shares; ++q) s += cluster.map_shared_rank(sum, q)[threadIdx.x];
+        const int64_t at = (int64_t)blockIdx.x * kCols + threadIdx.x;
+        if (at < n) db[at] = accumulate ? db[at] + s : s;
+    }
+    cluster.sync();  // the sums stay until they are read
 }
 
 // ---------------------------------------------------------------------------
@@ -496,7 +600,29 @@ cudaError_t sm_count(int *out) {
     return cudaSuccess;
 }
 
-template <int MODE, int BN>
+cudaError_t launch_column_sum(const Mat &dy, int accumulate, float *db, cudaStream_t s) {
+    const bool wide = dy.aligned(16) && dy.cols % 8 == 0;
+    int shares = 1;  // blocks along the rows: at least 256 rows each, at most a portable cluster
+    while (shares < 8 && dy.rows / shares >= 512) shares *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ceil_div<int64_t>(dy.cols, wide ? 64 : 32), (unsigned)shares);
+    cfg.blockDim = dim3(kColumnThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = RA_PDL;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = (unsigned)shares;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, wide ? column_sum_kernel<8, 8> : column_sum_kernel<1, 32>, static_cast<const uint16_t *>(dy.data), dy.ld,
+                                             dy.rows, dy.cols, accumulate, db);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+template <int MODE, int BN, bool F32>
 cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaStream_t s) {
     using S = Shape<BN>;
     p.tiles_m = (int)ceil_div<int64_t>(p.rows, kBM);
@@ -512,12 +638,21 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !(opted_in.load(std::memory_order_acquire) >> dev & 1)) {
-        e = cudaFuncSetAttribute(product_kernel<MODE, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+        e = cudaFuncSetAttribute(product_kernel<MODE, BN, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
         if (e != cudaSuccess) return e;
         if (dev < 64) opted_in.fetch_or((uint64_t)1 << dev, std::memory_order_acq_rel);
     }
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-    return launch_pdl(product_kernel<MODE, BN>, tiles < sms ? tiles : sms, kProductThreads, S::kSmem, s, p);
+    return launch_pdl(product_kernel<MODE, BN, F32>, tiles < sms ? tiles : sms, kProductThreads, S::kSmem, s, p);
+}
+
+// The tile's width: the widest that leaves half of the SMs or more a tile.
+template <int MODE, bool F32>
+cudaError_t launch_width(Product &p, const Mat &a, const Mat &b, int sms, cudaStream_t s) {
+    const int64_t tm = ceil_div<int64_t>(p.rows, kBM);
+    if (tm * ceil_div<int64_t>(p.cols, 128) <= sms / 2) return launch_tiles<MODE, 64, F32>(p, a, b, sms, s);
+    if (tm * ceil_div<int64_t>(p.cols, 256) <= sms / 2) return launch_tiles<MODE, 128, F32>(p, a, b, sms, s);
+    return launch_tiles<MODE, 256, F32>(p, a, b, sms, s);
 }
 
 // out (rows x cols) = epilogue(A B); a and b as they lie in memory
@@ -536,9 +671,7 @@ cudaError_t launch_product(const Mat &a, const Mat &b, int64_t rows, int64_t col
     if (e != cudaSuccess) return e;
     const int64_t tm = ceil_div<int64_t>(rows, kBM);
     if (tm * ceil_div<int64_t>(cols, 64) >= kMaxExtent) return cudaErrorInvalidValue;
-    if (tm * ceil_div<int64_t>(cols, 128) <= sms / 2) return launch_tiles<MODE, 64>(p, a, b, sms, s);
-    if (tm * ceil_div<int64_t>(cols, 256) <= sms / 2) return launch_tiles<MODE, 128>(p, a, b, sms, s);
-    return launch_tiles<MODE, 256>(p, a, b, sms, s);
+    return ep.out_f32 ? launch_width<MODE, true>(p, a, b, sms, s) : launch_width<MODE, false>(p, a, b, sms, s);
 }
 
 // the checkpoint's two arrays as matrices
@@ -689,7 +822,7 @@ ra_status ra_linear_wgrad(const void *x, int64_t ld_x, const int8_t *z_q, const 
         if (e != cudaSuccess) return cuda_status(e);
     }
     if (!mb.empty())
-        return cuda_status(launch_pdl(column_sum_kernel, ceil_div<int64_t>(n, 128), 128, 0, s, static_cast<const uint16_t *>(dy), ld_dy, m, n, accumulate, db));
+        return cuda_status(launch_column_sum(md, accumulate, db, s));
     return RA_OK;
 }
 
