@@ -161,24 +161,88 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// wait for a phase, with the library's limit; the clock is read only where the
-// phase is not over yet
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+// Wait for a phase, for the library's limit at most; the clock is read only
+// where the phase is not over yet.
+__device__ __forceinline__ bool phase_over(uint32_t bar, uint32_t parity) {
     uint32_t over;
-    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
                  : "=r"(over) : "r"(bar), "r"(parity) : "memory");
-    return over || mbar_wait_bounded(bar, parity, kWaitLimitNs);
+    return over;
 }
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+    if (phase_over(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    while (!phase_over(bar, parity))
+        if (global_ns() - t0 > kWaitLimitNs) return false;
+    return true;
+}
+// One lane of a converged warp.  The TMA and MMA warps stay whole and choose a
+// lane for the instructions alone, so their operands stay in uniform registers:
+// a loop of one lane on its own issued a 256 x 256 x 64 step in about 700
+// cycles instead of the tensor core's 512.
+__device__ __forceinline__ bool elected() {
+    uint32_t one;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+    return one;
+}
+// the same shared-memory place in the pair's first block
+__device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// PAIR: two blocks of a cluster on neighbouring SMs work as one tensor core
+// (cta_group::2).  The loads of both count on the first one's barrier, and a
+// commit reaches the same barrier in both.
+template <bool PAIR>
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-                 ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+    if constexpr (PAIR)
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];"
+                     ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                     ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
 }
+template <bool PAIR>
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    if constexpr (PAIR)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar), "h"((uint16_t)3)
+                     : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
+template <bool PAIR>
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
-    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+    if constexpr (PAIR)
+        asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }"
+                     ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+    else
+        asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
+                     ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+}
+template <bool PAIR, int COLS>
+__device__ __forceinline__ void tmem_alloc(uint32_t slot) {
+    if constexpr (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "n"(COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "n"(COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+}
+template <bool PAIR, int COLS>
+__device__ __forceinline__ void tmem_free(uint32_t tmem) {
+    if constexpr (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(COLS));
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(COLS));
 }
 __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
     uint32_t *r = reinterpret_cast<uint32_t *>(v);
@@ -207,10 +271,16 @@ __device__ __forceinline__ void flip(int &acc, uint32_t &phase) {
     acc ^= 1;
     if (acc == 0) phase ^= 1;
 }
-// a warp has read its part of a sum
+// a warp has read its part of a sum (the barrier is the first block's)
+template <bool PAIR>
 __device__ __forceinline__ void release(uint32_t bar, int lane) {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    if (lane == 0) mbar_arrive(bar);
+    if (lane == 0) {
+        if constexpr (PAIR)
+            mbar_arrive_remote(bar);
+        else
+            mbar_arrive(bar);
+    }
     __syncwarp();
 }
 
@@ -229,16 +299,19 @@ constexpr int kProductThreads = (kEpilogueWarps + 2) * 32;
 constexpr int kChunk = 4;
 constexpr int kGroupM = 16;  // row tiles that share the columns' tiles in L2
 
-template <int BN>
+// A tile is BN columns wide and 128 rows high per block; in a pair each block
+// holds its own rows of A and half of B's columns, which the two share.
+template <int BN, bool PAIR>
 struct Shape {
-    static constexpr int kABytes = kBM * kBK * 2, kBBytes = BN * kBK * 2;
+    static constexpr int kBlocks = PAIR ? 2 : 1, kRows = kBM * kBlocks, kBCols = BN / kBlocks;
+    static constexpr int kABytes = kBM * kBK * 2, kBBytes = kBCols * kBK * 2;
     static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 6 : 8;
+    static constexpr int kStages = kStageBytes > 24576 ? 6 : 8;
     static constexpr int kTmemCols = 2 * BN;  // two tiles' sums: one is finished while the next is made
     static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024 + 256;
 };
 
-struct alignas(64) Product {
+struct Product {
     CUtensorMap a, b;
     Epilogue ep;
     unsigned int *err;
@@ -256,17 +329,20 @@ __device__ __forceinline__ void tile_at(const Product &p, int tile, int *tm, int
     *tn = in / height;
 }
 
-template <int MODE, int BN, bool F32>
+template <int MODE, int BN, bool PAIR, bool F32>
 __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __grid_constant__ Product p) {
-    using S = Shape<BN>;
+    using S = Shape<BN, PAIR>;
     constexpr bool kAmn = MODE == kWgrad, kBmn = MODE != kDgrad;
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     const uint32_t tiles = smem_addr(smem);
     const uint32_t bars = tiles + S::kStages * S::kStageBytes;
+    // full: a stage's copies have landed; empty: its products are done; done: a
+    // tile's sums are; freed: they have been read; drained: all products are
     const uint32_t full = bars, empty = full + 8 * S::kStages, done = empty + 8 * S::kStages, freed = done + 16, drained = freed + 16;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kStages * S::kStageBytes + 16 * S::kStages + 40);
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int rank = PAIR ? blockIdx.x & 1 : 0;
 
     if (warp == kEpilogueWarps) {
         if (lane == 0) {
@@ -276,107 +352,124 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
             }
             for (int s = 0; s < 2; ++s) {
                 mbar_init(done + 8 * s, 1);
-                mbar_init(freed + 8 * s, kEpilogueWarps);
+                mbar_init(freed + 8 * s, kEpilogueWarps * S::kBlocks);
             }
             mbar_init(drained, 1);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
+        __syncwarp();
     } else if (warp == kEpilogueWarps + 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)), "n"(S::kTmemCols) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tmem_alloc<PAIR, S::kTmemCols>(smem_addr(tmem_slot));
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    __syncthreads();
+    if constexpr (PAIR)
+        cluster_sync();
+    else
+        __syncthreads();
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     const uint32_t tmem = *tmem_slot;
     pdl_enter();
 
     const int tile_count = p.tiles_m * p.tiles_n;
     bool ok = true;
-    if (warp == kEpilogueWarps) {
-        if (lane == 0) {  // TMA
-            int s = 0;
-            uint32_t phase = 0;
-            int64_t issued = 0;
-            for (int tile = blockIdx.x; tile < tile_count && ok; tile += gridDim.x) {
-                int tm, tn;
-                tile_at(p, tile, &tm, &tn);
-                for (int k = 0; k < p.steps; ++k) {
-                    if (!(ok = wait(empty + 8 * s, phase ^ 1))) break;
-                    const uint32_t bar = full + 8 * s, a = tiles + s * S::kStageBytes, b = a + S::kABytes;
-                    mbar_expect(bar, S::kStageBytes);
+    if (warp == kEpilogueWarps) {  // TMA
+        int s = 0;
+        uint32_t phase = 0;
+        int64_t issued = 0;
+        for (int tile = blockIdx.x / S::kBlocks; tile < tile_count && ok; tile += gridDim.x / S::kBlocks) {
+            int tm, tn;
+            tile_at(p, tile, &tm, &tn);
+            const int row = tm * S::kRows + rank * kBM, col = tn * BN + rank * S::kBCols;
+            for (int k = 0; k < p.steps; ++k) {
+                ok = __all_sync(0xffffffffu, wait(empty + 8 * s, phase ^ 1));
+                if (!ok) break;
+                const uint32_t a = tiles + s * S::kStageBytes, b = a + S::kABytes;
+                const uint32_t bar = PAIR ? in_leader(full + 8 * s) : full + 8 * s;
+                if (elected()) {
+                    if (rank == 0) mbar_expect(full + 8 * s, S::kStageBytes * S::kBlocks);
                     if constexpr (kAmn) {
 #pragma unroll
-                        for (int j = 0; j < kBM / 64; ++j) tma_load(a + j * 8192, &p.a, tm * kBM + j * 64, k * kBK, bar);
+                        for (int j = 0; j < kBM / 64; ++j) tma_load<PAIR>(a + j * 8192, &p.a, row + j * 64, k * kBK, bar);
                     } else {
-                        tma_load(a, &p.a, k * kBK, tm * kBM, bar);
+                        tma_load<PAIR>(a, &p.a, k * kBK, row, bar);
                     }
                     if constexpr (kBmn) {
 #pragma unroll
-                        for (int j = 0; j < BN / 64; ++j) tma_load(b + j * 8192, &p.b, tn * BN + j * 64, k * kBK, bar);
+                        for (int j = 0; j < S::kBCols / 64; ++j) tma_load<PAIR>(b + j * 8192, &p.b, col + j * 64, k * kBK, bar);
                     } else {
-                        tma_load(b, &p.b, k * kBK, tn * BN, bar);
-                    }
-                    ++issued;
-                    if (++s == S::kStages) {
-                        s = 0;
-                        phase ^= 1;
+                        tma_load<PAIR>(b, &p.b, k * kBK, col, bar);
                     }
                 }
+                __syncwarp();
+                ++issued;
+                if (++s == S::kStages) {
+                    s = 0;
+                    phase ^= 1;
+                }
             }
-            // shared memory must outlive the copies: the last ones' barriers
-            for (int64_t i = issued > S::kStages ? issued - S::kStages : 0; i < issued; ++i)
-                ok &= wait(full + 8 * (uint32_t)(i % S::kStages), (uint32_t)(i / S::kStages) & 1);
         }
-    } else if (warp == kEpilogueWarps + 1) {
-        if (lane == 0) {  // tcgen05.mma
-            constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (kAmn ? 1u << 15 : 0) | (kBmn ? 1u << 16 : 0) | (BN / 8) << 17 | (kBM / 16) << 24;
+        // shared memory must outlive the copies and the products that read it
+        for (int64_t i = issued > S::kStages ? issued - S::kStages : 0; i < issued && ok; ++i)
+            ok = __all_sync(0xffffffffu, wait(empty + 8 * (uint32_t)(i % S::kStages), (uint32_t)(i / S::kStages) & 1));
+    } else if (warp == kEpilogueWarps + 1) {  // tcgen05.mma
+        if (rank == 0) {
+            constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (kAmn ? 1u << 15 : 0) | (kBmn ? 1u << 16 : 0) | (BN / 8) << 17 | (S::kRows / 16) << 24;
+            // 16 of k further on in a stage, and a stage further on, in the descriptors' 16-byte units
+            constexpr uint32_t a_next = (kAmn ? 2048 : 32) >> 4, b_next = (kBmn ? 2048 : 32) >> 4, stage_next = S::kStageBytes >> 4;
+            const uint64_t a0 = operand(tiles, kAmn ? 8192 : 16, 1024), b0 = operand(tiles + S::kABytes, kBmn ? 8192 : 16, 1024);
             int s = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
-            for (int tile = blockIdx.x; tile < tile_count && ok; tile += gridDim.x) {
+            for (int tile = blockIdx.x / S::kBlocks; tile < tile_count && ok; tile += gridDim.x / S::kBlocks) {
                 for (int k = 0; k < p.steps || k == 0; ++k) {
                     if (F32 ? k % kChunk == 0 : k == 0) {  // a new sum
-                        if (!(ok = wait(freed + 8 * acc, acc_phase ^ 1))) break;
+                        ok = __all_sync(0xffffffffu, wait(freed + 8 * acc, acc_phase ^ 1));
+                        if (!ok) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     }
-                    if (p.steps == 0) {
-                        mma_commit(done + 8 * acc);
-                        flip(acc, acc_phase);
-                        break;
-                    }
-                    if (!(ok = wait(full + 8 * s, phase))) break;
-                    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    const uint32_t a = tiles + s * S::kStageBytes, b = a + S::kABytes;
+                    const bool last = k + 1 >= p.steps || (F32 && k % kChunk == kChunk - 1);
+                    if (p.steps > 0) {
+                        ok = __all_sync(0xffffffffu, wait(full + 8 * s, phase));
+                        if (!ok) break;
+                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                        if (elected()) {
 #pragma unroll
-                    for (int j = 0; j < kBK / 16; ++j) {
-                        const uint64_t da = kAmn ? operand(a + j * 2048, 8192, 1024) : operand(a + j * 32, 16, 1024);
-                        const uint64_t db = kBmn ? operand(b + j * 2048, 8192, 1024) : operand(b + j * 32, 16, 1024);
-                        mma_bf16(tmem + acc * BN, da, db, idesc, (F32 ? k % kChunk : k) > 0 || j > 0);
+                            for (int j = 0; j < kBK / 16; ++j)
+                                mma_bf16<PAIR>(tmem + acc * BN, a0 + s * stage_next + j * a_next, b0 + s * stage_next + j * b_next, idesc,
+                                               (F32 ? k % kChunk : k) > 0 || j > 0);
+                            mma_commit<PAIR>(empty + 8 * s);
+                            if (last) mma_commit<PAIR>(done + 8 * acc);
+                        }
+                        if (++s == S::kStages) {
+                            s = 0;
+                            phase ^= 1;
+                        }
+                    } else if (elected()) {
+                        mma_commit<PAIR>(done + 8 * acc);
                     }
-                    mma_commit(empty + 8 * s);
-                    if (++s == S::kStages) {
-                        s = 0;
-                        phase ^= 1;
-                    }
-                    if (k + 1 == p.steps || (F32 && k % kChunk == kChunk - 1)) {
-                        mma_commit(done + 8 * acc);
-                        flip(acc, acc_phase);
-                    }
+                    __syncwarp();
+                    if (last) flip(acc, acc_phase);
                 }
             }
             // TMEM must outlive the products, also where a wait gave up
-            mma_commit(drained);
+            if (elected()) {
+                if constexpr (PAIR)
+                    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(drained) : "memory");
+                else
+                    mma_commit<false>(drained);
+            }
+            __syncwarp();
             ok &= wait(drained, 0);
         }
     } else {
+        const uint32_t freed_bar = PAIR ? in_leader(freed) : freed;
         constexpr int kHalf = BN / 2;  // each four warps finish half of the columns
         int acc = 0;
         uint32_t acc_phase = 0;
         const uint32_t mine = tmem + (warp / 4) * kHalf + ((uint32_t)(warp % 4 * 32) << 16);
-        for (int tile = blockIdx.x; tile < tile_count && ok; tile += gridDim.x) {
+        for (int tile = blockIdx.x / S::kBlocks; tile < tile_count && ok; tile += gridDim.x / S::kBlocks) {
             int tm, tn;
             tile_at(p, tile, &tm, &tn);
-            const int64_t row = (int64_t)tm * kBM + warp % 4 * 32 + lane;
+            const int64_t row = (int64_t)tm * S::kRows + rank * kBM + warp % 4 * 32 + lane;
             const int64_t c0 = (int64_t)tn * BN + warp / 4 * kHalf;
             if constexpr (F32) {
                 float sum[kHalf / 32][32];
@@ -397,7 +490,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
                             for (int j = 0; j < 32; ++j) sum[g][j] += v[j];
                         }
                     }
-                    release(freed + 8 * acc, lane);
+                    release<PAIR>(freed_bar + 8 * acc, lane);
                     flip(acc, acc_phase);
                 }
                 if (!ok) break;
@@ -431,7 +524,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
                     if (row < p.rows) finish32<MODE>(p.ep, row, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
                     __syncwarp();
                 }
-                release(freed + 8 * acc, lane);
+                release<PAIR>(freed_bar + 8 * acc, lane);
                 flip(acc, acc_phase);
             }
         }
@@ -439,10 +532,13 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
     if (!ok) atomicOr(p.err, 1u);
     __syncwarp();
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    __syncthreads();
+    if constexpr (PAIR)
+        cluster_sync();  // neither block's memory goes while the other may still reach it
+    else
+        __syncthreads();
     if (warp == kEpilogueWarps + 1) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kTmemCols));
+        tmem_free<PAIR, S::kTmemCols>(tmem);
     }
 }
 
@@ -622,15 +718,15 @@ cudaError_t launch_column_sum(const Mat &dy, int accumulate, float *db, cudaStre
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-template <int MODE, int BN, bool F32>
+template <int MODE, int BN, bool PAIR, bool F32>
 cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaStream_t s) {
-    using S = Shape<BN>;
-    p.tiles_m = (int)ceil_div<int64_t>(p.rows, kBM);
+    using S = Shape<BN, PAIR>;
+    p.tiles_m = (int)ceil_div<int64_t>(p.rows, S::kRows);
     p.tiles_n = (int)ceil_div<int64_t>(p.cols, BN);
     cudaError_t e = cudaSuccess;
     if (p.steps > 0) {
         e = tensor_map(&p.a, a, MODE == kWgrad ? kBK : kBM);
-        if (e == cudaSuccess) e = tensor_map(&p.b, b, MODE == kDgrad ? BN : kBK);
+        if (e == cudaSuccess) e = tensor_map(&p.b, b, MODE == kDgrad ? S::kBCols : kBK);
         if (e != cudaSuccess) return e;
     }
     static std::atomic<uint64_t> opted_in{0};  // a bit per device
@@ -638,21 +734,37 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !(opted_in.load(std::memory_order_acquire) >> dev & 1)) {
-        e = cudaFuncSetAttribute(product_kernel<MODE, BN, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+        e = cudaFuncSetAttribute(product_kernel<MODE, BN, PAIR, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
         if (e != cudaSuccess) return e;
         if (dev < 64) opted_in.fetch_or((uint64_t)1 << dev, std::memory_order_acq_rel);
     }
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-    return launch_pdl(product_kernel<MODE, BN, F32>, tiles < sms ? tiles : sms, kProductThreads, S::kSmem, s, p);
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, most = sms / S::kBlocks;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * S::kBlocks));
+    cfg.blockDim = dim3(kProductThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = RA_PDL;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = S::kBlocks;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, product_kernel<MODE, BN, PAIR, F32>, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-// The tile's width: the widest that leaves half of the SMs or more a tile.
+// The tile: the widest that leaves half of the SMs or more one; the widest is
+// a pair's.
 template <int MODE, bool F32>
 cudaError_t launch_width(Product &p, const Mat &a, const Mat &b, int sms, cudaStream_t s) {
     const int64_t tm = ceil_div<int64_t>(p.rows, kBM);
-    if (tm * ceil_div<int64_t>(p.cols, 128) <= sms / 2) return launch_tiles<MODE, 64, F32>(p, a, b, sms, s);
-    if (tm * ceil_div<int64_t>(p.cols, 256) <= sms / 2) return launch_tiles<MODE, 128, F32>(p, a, b, sms, s);
-    return launch_tiles<MODE, 256, F32>(p, a, b, sms, s);
+    if (tm * ceil_div<int64_t>(p.cols, 128) <= sms / 2) return launch_tiles<MODE, 64, false, F32>(p, a, b, sms, s);
+    if (tm * ceil_div<int64_t>(p.cols, 256) <= sms / 2) return launch_tiles<MODE, 128, false, F32>(p, a, b, sms, s);
+    return launch_tiles<MODE, 256, true, F32>(p, a, b, sms, s);
 }
 
 // out (rows x cols) = epilogue(A B); a and b as they lie in memory
