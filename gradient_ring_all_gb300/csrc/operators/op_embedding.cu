@@ -100,24 +100,60 @@ cudaError_t launch_lookup(const LookupParams &p, int width, cudaStream_t s) {
 //    a piece's edge the piece keeps a partial sum, and a second kernel joins
 //    these in order.  Which values are added in which order is fixed by the
 //    ids alone, so results do not change from call to call.
-// 3. Rows that no token names are set to zero (unless the gradient is added
-//    to what is there), by blocks that find their rows' tokens by a search in
-//    the sorted ids.
+// 3. The table's gradient is set to zero first (unless it is added to), by
+//    further blocks of the sorting launches: these few small blocks wait on
+//    latency, while the zeros need only the memory's write rate, so the sort
+//    costs next to nothing beside them.  Rows that tokens name are written
+//    twice; telling them apart first would put the zeros behind the sort.
 
 constexpr int kDigitBits = 8, kDigits = 1 << kDigitBits;
-constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
-constexpr int kSortRounds = 8;                             // tokens a thread holds
-constexpr int kSortTile = kSortThreads * kSortRounds;      // 4096
+constexpr int kSortThreads = 256, kSortWarps = kSortThreads / 32;
+constexpr int kSortRounds = 4;                         // tokens a thread holds
+constexpr int kSortTile = kSortThreads * kSortRounds;  // 1024
 constexpr int kPiece = 32;
-constexpr int kZeroRows = 16;  // table rows a zeroing block looks after
+
+// A share of the table gradient's rows that a launch sets to zero.
+struct ZeroShare {
+    void *out;
+    int64_t ld, d, row0, rows;  // ld and d in elements
+    int esz, wide;              // wide: rows are whole numbers of 16-byte words on 16-byte boundaries
+};
+constexpr int kZeroBlockBytes = 1 << 15, kMaxZeroBlocks = 152 * 8;
+
+// the work of block `at` of `blocks`
+template <int THREADS>
+__device__ __forceinline__ void zero_share(const ZeroShare &z, int64_t at, int64_t blocks) {
+    if (z.wide) {
+        const int64_t words = z.d * z.esz / 16, pitch = z.ld * z.esz / 16;
+        uint4 *base = static_cast<uint4 *>(z.out) + z.row0 * pitch;
+        if (words == pitch) {  // no gaps: one range
+            const int64_t n = z.rows * words;
+            for (int64_t i = at * THREADS + threadIdx.x; i < n; i += blocks * THREADS) base[i] = make_uint4(0, 0, 0, 0);
+        } else {
+            for (int64_t r = at; r < z.rows; r += blocks)
+                for (int64_t i = threadIdx.x; i < words; i += THREADS) base[r * pitch + i] = make_uint4(0, 0, 0, 0);
+        }
+    } else {
+        for (int64_t r = at; r < z.rows; r += blocks) {
+            const int64_t row = (z.row0 + r) * z.ld;
+            for (int64_t i = threadIdx.x; i < z.d; i += THREADS) {
+                if (z.esz == 4)
+                    static_cast<float *>(z.out)[row + i] = 0.0f;
+                else
+                    static_cast<uint16_t *>(z.out)[row + i] = 0;
+            }
+        }
+    }
+}
 
 struct SortParams {
+    ZeroShare zero;
     const void *ids;  // first pass
     const uint32_t *key_in, *pos_in;
     uint32_t *key_out, *pos_out;
     uint32_t *hist;  // [kDigits][tiles]
     int64_t tokens, vocab;
-    int tiles, shift;
+    int tiles, shift;  // blocks from `tiles` on set zeros
 };
 
 template <class I, bool FIRST>
@@ -134,6 +170,10 @@ template <class I, bool FIRST>
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortParams p) {
     __shared__ uint32_t count[kDigits];
     pdl_enter();
+    if (blockIdx.x >= p.tiles) {
+        zero_share<kSortThreads>(p.zero, blockIdx.x - p.tiles, gridDim.x - p.tiles);
+        return;
+    }
     for (int k = threadIdx.x; k < kDigits; k += kSortThreads) count[k] = 0;
     __syncthreads();
     const int64_t base = (int64_t)blockIdx.x * kSortTile;
@@ -148,9 +188,15 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortPara
 
 // exclusive prefix sums over `n` counts, in place, by one block
 constexpr int kScanThreads = 1024;
-__global__ void __launch_bounds__(kScanThreads) sort_scan_kernel(uint32_t *h, int64_t n) {
+__global__ void __launch_bounds__(kScanThreads) sort_scan_kernel(const SortParams p) {
     __shared__ uint32_t warp_sum[32];
     pdl_enter();
+    if (blockIdx.x >= 1) {
+        zero_share<kScanThreads>(p.zero, blockIdx.x - 1, gridDim.x - 1);
+        return;
+    }
+    uint32_t *h = p.hist;
+    const int64_t n = (int64_t)kDigits * p.tiles;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     uint32_t carry = 0;
     for (int64_t base = 0; base < n; base += kScanThreads) {
@@ -189,6 +235,10 @@ template <class I, bool FIRST>
 __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const SortParams p) {
     __shared__ uint32_t count[kSortWarps][kDigits];
     pdl_enter();
+    if (blockIdx.x >= p.tiles) {
+        zero_share<kSortThreads>(p.zero, blockIdx.x - p.tiles, gridDim.x - p.tiles);
+        return;
+    }
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
     for (int k = threadIdx.x; k < kSortWarps * kDigits; k += kSortThreads) (&count[0][0])[k] = 0;
     __syncthreads();
@@ -236,7 +286,6 @@ struct GradParams {
     float *part;  // [2 * pieces][d rounded up to 8]: a piece's first and last run
     int64_t ldg, ldo, ldp, tokens, vocab, d;
     int64_t pieces;
-    int zero_blocks;
     float scale;
     int accumulate;
 };
@@ -264,10 +313,7 @@ template <class TO, int W>
 __device__ __forceinline__ void finish_row(const GradParams &p, uint32_t v, int64_t c, float (&sum)[W]) {
     TO *o = static_cast<TO *>(p.out) + (int64_t)v * p.ldo + c;
     float old[W];
-    if (p.accumulate) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) old[j] = to_f32<TO>(o[j]);
-    }
+    if (p.accumulate) load_w<TO, W>(o, old);
 #pragma unroll
     for (int j = 0; j < W; ++j) {
         sum[j] = __fmul_rn(sum[j], p.scale);
@@ -279,33 +325,8 @@ __device__ __forceinline__ void finish_row(const GradParams &p, uint32_t v, int6
 template <class TI, class TO, int W>
 __global__ void __launch_bounds__(kGradThreads) grad_pieces_kernel(const GradParams p) {
     __shared__ uint32_t key[kPiece + 2], pos[kPiece];
-    __shared__ uint32_t touched[kZeroRows];
     pdl_enter();
     const int64_t c = ((int64_t)blockIdx.y * kGradThreads + threadIdx.x) * W;
-    if ((int64_t)blockIdx.x >= p.pieces) {  // rows that no token names
-        const int64_t v0 = ((int64_t)blockIdx.x - p.pieces) * kZeroRows;
-        const int64_t v1 = v0 + kZeroRows < p.vocab ? v0 + kZeroRows : p.vocab;
-        if (threadIdx.x < kZeroRows) touched[threadIdx.x] = 0;
-        __syncthreads();
-        if (threadIdx.x < 32) {
-            int64_t i = lower_bound_warp(p.key, p.tokens, (uint32_t)v0);
-            // skip from run to run: at most kZeroRows of them
-            while (i < p.tokens) {
-                const uint32_t v = p.key[i];
-                if ((int64_t)v >= v1) break;
-                if (threadIdx.x == 0) touched[v - v0] = 1;
-                i += lower_bound_warp(p.key + i, p.tokens - i, v + 1);
-            }
-        }
-        __syncthreads();
-        if (c >= p.d) return;
-        float zero[W];
-#pragma unroll
-        for (int j = 0; j < W; ++j) zero[j] = 0.0f;
-        for (int64_t v = v0; v < v1; ++v)
-            if (!touched[v - v0]) store_w<TO, W>(static_cast<TO *>(p.out) + v * p.ldo + c, zero);
-        return;
-    }
     const int64_t i0 = (int64_t)blockIdx.x * kPiece;
     const int count = (int)(p.tokens - i0 < kPiece ? p.tokens - i0 : kPiece);
     constexpr uint32_t kNone = 0xffffffffu;
@@ -319,12 +340,12 @@ __global__ void __launch_bounds__(kGradThreads) grad_pieces_kernel(const GradPar
     const TI *grad = static_cast<const TI *>(p.grad) + c;
     float sum[W];
     int begin = 0;  // of the open run
-    constexpr int kFlight = 4;
+    constexpr int kFlight = W * sizeof(TI) >= 16 ? 8 : 16;
     for (int k0 = 0; k0 < count; k0 += kFlight) {
-        float x[kFlight][W];
+        Raw<TI, W> x[kFlight];
 #pragma unroll
         for (int f = 0; f < kFlight; ++f)
-            if (k0 + f < count && key[k0 + f + 1] < p.vocab) load_w<TI, W>(grad + (int64_t)pos[k0 + f] * p.ldg, x[f]);
+            if (k0 + f < count && key[k0 + f + 1] < p.vocab) x[f].load(grad + (int64_t)pos[k0 + f] * p.ldg);
 #pragma unroll
         for (int f = 0; f < kFlight; ++f) {
             const int k = k0 + f;
@@ -353,29 +374,50 @@ __global__ void __launch_bounds__(kGradThreads) grad_pieces_kernel(const GradPar
 }
 
 // A block for each piece in which a run begins that later pieces go on with:
-// the piece's own partial sum and, in order, those of the pieces after it.
+// the piece's own partial sum and those of the pieces after it.  The block's
+// warps take consecutive shares of these pieces, which are then added in order.
+constexpr int kJoinWarps = 8;
 template <class TO, int W>
-__global__ void __launch_bounds__(kGradThreads) grad_join_kernel(const GradParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32) grad_join_kernel(const GradParams p) {
+    __shared__ float part[kJoinWarps][32 * W];
     pdl_enter();
     const int64_t i1 = ((int64_t)blockIdx.x + 1) * kPiece;  // the first token of the next piece
-    if (i1 >= p.tokens) return;
     const uint32_t v = p.key[i1];
     if (v >= p.vocab || p.key[i1 - 1] != v) return;
     if (i1 > kPiece && p.key[i1 - kPiece] == v && p.key[i1 - kPiece - 1] == v) return;  // begins earlier
-    const int64_t c = ((int64_t)blockIdx.y * kGradThreads + threadIdx.x) * W;
-    if (c >= p.d) return;
-    // pieces that begin with this run: blockIdx.x + 1 .. last
-    int64_t last = blockIdx.x + 1;
+    // the run's end, and so the pieces 0 .. count-1 that begin with it after this one
+    const int64_t end = i1 + lower_bound_warp(p.key + i1, p.tokens - i1, v + 1);
+    const int64_t count = ceil_div<int64_t>(end - i1, kPiece);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int64_t c = ((int64_t)blockIdx.y * 32 + lane) * W;
+    const int64_t k0 = count * warp / kJoinWarps, k1 = count * (warp + 1) / kJoinWarps;
     float sum[W];
-    load_w<float, W>(p.part + (2 * (int64_t)blockIdx.x + 1) * p.ldp + c, sum);
-    for (;; ++last) {
-        float x[W];
-        load_w<float, W>(p.part + 2 * last * p.ldp + c, x);
 #pragma unroll
-        for (int j = 0; j < W; ++j) sum[j] = __fadd_rn(sum[j], x[j]);
-        const int64_t next = (last + 1) * kPiece;
-        if (next >= p.tokens || p.key[next] != v || p.key[next - 1] != v) break;
+    for (int j = 0; j < W; ++j) sum[j] = 0.0f;
+    if (c < p.d) {
+        if (warp == 0) load_w<float, W>(p.part + (2 * (int64_t)blockIdx.x + 1) * p.ldp + c, sum);
+        const float *from = p.part + 2 * ((int64_t)blockIdx.x + 1) * p.ldp + c;
+        constexpr int kFlight = W > 4 ? 4 : 8;
+        for (int64_t k = k0; k < k1; k += kFlight) {
+            Raw<float, W> x[kFlight];
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f)
+                if (k + f < k1) x[f].load(from + 2 * (k + f) * p.ldp);
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f) {
+                if (k + f >= k1) break;
+#pragma unroll
+                for (int j = 0; j < W; ++j) sum[j] = __fadd_rn(sum[j], x[f][j]);
+            }
+        }
     }
+#pragma unroll
+    for (int j = 0; j < W; ++j) part[warp][j * 32 + lane] = sum[j];
+    __syncthreads();
+    if (warp != 0 || c >= p.d) return;
+    for (int w = 1; w < kJoinWarps; ++w)
+#pragma unroll
+        for (int j = 0; j < W; ++j) sum[j] = __fadd_rn(sum[j], part[w][j * 32 + lane]);
     finish_row<TO, W>(p, v, c, sum);
 }
 
@@ -406,24 +448,50 @@ GradPlan plan_grad(int64_t tokens, int64_t vocab, int64_t d) {
     return g;
 }
 
+int64_t zero_blocks(const ZeroShare &z) {
+    const int64_t blocks = ceil_div<int64_t>(z.rows * z.d * z.esz, kZeroBlockBytes);
+    return blocks < kMaxZeroBlocks ? blocks : kMaxZeroBlocks;
+}
+
+__global__ void __launch_bounds__(kSortThreads) zero_kernel(const ZeroShare z) {
+    pdl_enter();
+    zero_share<kSortThreads>(z, blockIdx.x, gridDim.x);
+}
+
+// The sorting launches (3 a pass); each also sets its share of `out` to zero,
+// where `zero.rows` asks for it.
 template <class I>
-cudaError_t launch_sort(const GradPlan &g, char *ws, const void *ids, int64_t tokens, int64_t vocab, cudaStream_t s) {
+cudaError_t launch_sort(const GradPlan &g, char *ws, const void *ids, int64_t tokens, int64_t vocab, const ZeroShare &zero, cudaStream_t s) {
+    const int launches = 3 * g.passes;
+    int launch = 0;
+    SortParams p = {};
+    auto share = [&]() -> int64_t {  // sets p.zero; the blocks it takes
+        p.zero = zero;
+        p.zero.row0 = zero.rows * launch / launches;
+        p.zero.rows = zero.rows * (launch + 1) / launches - p.zero.row0;
+        ++launch;
+        return zero_blocks(p.zero);
+    };
     for (int pass = 0; pass < g.passes; ++pass) {
         const int from = (pass + 1) & 1, to = pass & 1;
-        SortParams p{ids,
-                     reinterpret_cast<uint32_t *>(ws + g.key[from]),
-                     reinterpret_cast<uint32_t *>(ws + g.pos[from]),
-                     reinterpret_cast<uint32_t *>(ws + g.key[to]),
-                     reinterpret_cast<uint32_t *>(ws + g.pos[to]),
-                     reinterpret_cast<uint32_t *>(ws + g.hist),
-                     tokens, vocab, g.tiles, pass * kDigitBits};
-        cudaError_t e = pass == 0 ? launch_pdl(sort_count_kernel<I, true>, g.tiles, kSortThreads, 0, s, p)
-                                  : launch_pdl(sort_count_kernel<I, false>, g.tiles, kSortThreads, 0, s, p);
+        p.ids = ids;
+        p.key_in = reinterpret_cast<uint32_t *>(ws + g.key[from]);
+        p.pos_in = reinterpret_cast<uint32_t *>(ws + g.pos[from]);
+        p.key_out = reinterpret_cast<uint32_t *>(ws + g.key[to]);
+        p.pos_out = reinterpret_cast<uint32_t *>(ws + g.pos[to]);
+        p.hist = reinterpret_cast<uint32_t *>(ws + g.hist);
+        p.tokens = tokens;
+        p.vocab = vocab;
+        p.tiles = g.tiles;
+        p.shift = pass * kDigitBits;
+        int64_t extra = share();
+        cudaError_t e = launch_pdl(pass == 0 ? sort_count_kernel<I, true> : sort_count_kernel<I, false>, g.tiles + extra, kSortThreads, 0, s, p);
         if (e != cudaSuccess) return e;
-        e = launch_pdl(sort_scan_kernel, 1, kScanThreads, 0, s, p.hist, (int64_t)kDigits * g.tiles);
+        extra = share();
+        e = launch_pdl(sort_scan_kernel, 1 + extra, kScanThreads, 0, s, p);
         if (e != cudaSuccess) return e;
-        e = pass == 0 ? launch_pdl(sort_scatter_kernel<I, true>, g.tiles, kSortThreads, 0, s, p)
-                      : launch_pdl(sort_scatter_kernel<I, false>, g.tiles, kSortThreads, 0, s, p);
+        extra = share();
+        e = launch_pdl(pass == 0 ? sort_scatter_kernel<I, true> : sort_scatter_kernel<I, false>, g.tiles + extra, kSortThreads, 0, s, p);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -446,10 +514,9 @@ cudaError_t launch_2d(K kern, int64_t gx, int64_t gy, int threads, cudaStream_t 
 
 template <class TI, class TO, int W>
 cudaError_t launch_sums(const GradParams &p, cudaStream_t s) {
-    const int64_t gy = ceil_div<int64_t>(p.d, kGradThreads * W);
-    cudaError_t e = launch_2d(grad_pieces_kernel<TI, TO, W>, p.pieces + p.zero_blocks, gy, kGradThreads, s, p);
+    cudaError_t e = launch_2d(grad_pieces_kernel<TI, TO, W>, p.pieces, ceil_div<int64_t>(p.d, kGradThreads * W), kGradThreads, s, p);
     if (e != cudaSuccess || p.pieces < 2) return e;
-    return launch_2d(grad_join_kernel<TO, W>, p.pieces - 1, gy, kGradThreads, s, p);
+    return launch_2d(grad_join_kernel<TO, W>, p.pieces - 1, ceil_div<int64_t>(p.d, 32 * W), kJoinWarps * 32, s, p);
 }
 
 template <class TI, class TO>
@@ -508,21 +575,20 @@ ra_status ra_embedding_grad(const void *grad, int64_t ld_grad, int grad_dtype, c
     }
     if (mats_overlap(g, o) || mats_overlap(i, o)) return RA_ERR_OVERLAP;
     if (tokens == 0 && accumulate) return RA_OK;
-    const int64_t zero_blocks = accumulate ? 0 : ceil_div<int64_t>(vocab, kZeroRows);
-    if (plan.pieces + zero_blocks > kMaxGrid || ceil_div<int64_t>(d, kGradThreads) > 65535) return RA_ERR_UNSUPPORTED;
+    if (plan.pieces > kMaxGrid || ceil_div<int64_t>(d, 32) > 65535) return RA_ERR_UNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char *base = static_cast<char *>(ws);
-    if (tokens > 0) {
-        const cudaError_t e = id_bytes == 4 ? launch_sort<int32_t>(plan, base, ids, tokens, vocab, s)
-                                            : launch_sort<int64_t>(plan, base, ids, tokens, vocab, s);
-        if (e != cudaSuccess) return cuda_status(e);
-    }
+    const ZeroShare zero{out, ld_out, d, 0, accumulate ? 0 : vocab, osz, o.aligned(16) && o.row_bytes() % 16 == 0};
+    if (tokens == 0) return cuda_status(launch_pdl(zero_kernel, zero_blocks(zero), kSortThreads, 0, s, zero));
+    cudaError_t e = id_bytes == 4 ? launch_sort<int32_t>(plan, base, ids, tokens, vocab, zero, s)
+                                  : launch_sort<int64_t>(plan, base, ids, tokens, vocab, zero, s);
+    if (e != cudaSuccess) return cuda_status(e);
     const int sorted = (plan.passes + 1) & 1;
     const GradParams p{grad, out,
-                       tokens ? reinterpret_cast<const uint32_t *>(base + plan.key[sorted]) : nullptr,
-                       tokens ? reinterpret_cast<const uint32_t *>(base + plan.pos[sorted]) : nullptr,
-                       tokens ? reinterpret_cast<float *>(base + plan.part) : nullptr,
-                       ld_grad, ld_out, plan.ldp, tokens, vocab, d, plan.pieces, (int)zero_blocks, scale, accumulate};
+                       reinterpret_cast<const uint32_t *>(base + plan.key[sorted]),
+                       reinterpret_cast<const uint32_t *>(base + plan.pos[sorted]),
+                       reinterpret_cast<float *>(base + plan.part),
+                       ld_grad, ld_out, plan.ldp, tokens, vocab, d, plan.pieces, scale, accumulate};
     const int width = common_width(g, o, d, 16 / gsz);
     if (gsz == 4) return cuda_status(osz == 4 ? launch_grad<float, float>(p, width, s) : launch_grad<float, uint16_t>(p, width, s));
     return cuda_status(osz == 4 ? launch_grad<uint16_t, float>(p, width, s) : launch_grad<uint16_t, uint16_t>(p, width, s));

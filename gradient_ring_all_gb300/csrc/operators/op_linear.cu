@@ -139,7 +139,7 @@ __device__ __forceinline__ void finish32(const Epilogue &ep, int64_t row, int64_
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const float *x = v + 8 * g;
-                reinterpret_cast<uint4 *>(p)[g] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+                reinterpret_cast<uint4 *>(p)[g] = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
             }
         } else {
 #pragma unroll
@@ -297,7 +297,7 @@ constexpr int kProductThreads = (kEpilogueWarps + 2) * 32;
 // k) at a time, and the epilogue warps add the chunks in registers with rounding
 // to nearest, while the next chunk is made.
 constexpr int kChunk = 4;
-constexpr int kGroupM = 16;  // row tiles that share the columns' tiles in L2
+constexpr int kGroupM = 8;  // row tiles that share the columns' tiles in L2
 
 // A tile is BN columns wide and 128 rows high per block; in a pair each block
 // holds its own rows of A and half of B's columns, which the two share.
@@ -306,7 +306,7 @@ struct Shape {
     static constexpr int kBlocks = PAIR ? 2 : 1, kRows = kBM * kBlocks, kBCols = BN / kBlocks;
     static constexpr int kABytes = kBM * kBK * 2, kBBytes = kBCols * kBK * 2;
     static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = kStageBytes > 24576 ? 6 : 8;
+    static constexpr int kStages = kStageBytes > 24576 ? 7 : 8;
     static constexpr int kTmemCols = 2 * BN;  // two tiles' sums: one is finished while the next is made
     static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024 + 256;
 };
@@ -567,10 +567,10 @@ __global__ void __launch_bounds__(kStageThreads) lay_out_kernel(const uint16_t *
 // LANES * W columns, W at a time per thread, and its share of the rows; the
 // blocks of a cluster share a strip, and the first of them adds the others'
 // sums, in order, out of their shared memory.  Bound by reading dy once.
-constexpr int kColumnThreads = 256;
+constexpr int kColumnThreads = 512;
 template <int W, int LANES>
 __global__ void __launch_bounds__(kColumnThreads) column_sum_kernel(const uint16_t *dy, int64_t ld, int64_t m, int64_t n, int accumulate, float *db) {
-    constexpr int kRowsAtOnce = kColumnThreads / LANES, kCols = LANES * W, kFlight = 4;
+    constexpr int kRowsAtOnce = kColumnThreads / LANES, kCols = LANES * W, kFlight = 8;
     __shared__ float part[kRowsAtOnce][kCols + 1];
     __shared__ float sum[kCols];
     namespace cg = cooperative_groups;
@@ -582,15 +582,13 @@ __global__ void __launch_bounds__(kColumnThreads) column_sum_kernel(const uint16
     float acc[W] = {};
     if (c < n) {
         for (int64_t r = r0 + threadIdx.x / LANES; r < r1; r += kRowsAtOnce * kFlight) {
-            float x[kFlight][W];
+            Raw<uint16_t, W> x[kFlight];
 #pragma unroll
             for (int f = 0; f < kFlight; ++f) {
-                if (r + f * kRowsAtOnce < r1) {
-                    load_w<uint16_t, W>(dy + (r + f * kRowsAtOnce) * ld + c, x[f]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < W; ++j) x[f][j] = 0.0f;
-                }
+                if (r + f * kRowsAtOnce < r1)
+                    x[f].load(dy + (r + f * kRowsAtOnce) * ld + c);
+                else
+                    x[f].zero();
             }
 #pragma unroll
             for (int f = 0; f < kFlight; ++f)
@@ -601,11 +599,11 @@ __global__ void __launch_bounds__(kColumnThreads) column_sum_kernel(const uint16
 #pragma unroll
     for (int j = 0; j < W; ++j) part[threadIdx.x / LANES][threadIdx.x % LANES * W + j] = acc[j];
     __syncthreads();
-    if (threadIdx.x < kCols) {
-        float s = part[0][threadIdx.x];
-        for (int g = 1; g < kRowsAtOnce; ++g) s += part[g][threadIdx.x];
-        sum[threadIdx.x] = s;
+    for (int half = kRowsAtOnce / 2; half > 0; half /= 2) {  // a fixed tree
+        for (int u = threadIdx.x; u < half * kCols; u += kColumnThreads) part[u / kCols][u % kCols] += part[u / kCols + half][u % kCols];
+        __syncthreads();
     }
+    if (threadIdx.x < kCols) sum[threadIdx.x] = part[0][threadIdx.x];
     cluster.sync();
     if (share == 0 && threadIdx.x < kCols) {
         float s = sum[threadIdx.x];
