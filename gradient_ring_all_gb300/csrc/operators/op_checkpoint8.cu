@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreadsCkpt) pack_kernel(const PackParams p) 
         }
         uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) top = max(top, magnitude_bits(x[j]));
+        for (int j = 0; j < 16; j += 2) top = top_of(top, x[j], x[j + 1]);
         const uint32_t pair = 3u << (threadIdx.x & 30);
         const Step step = step_of(max(top, __shfl_xor_sync(pair, top, 1)));
         uint32_t w[4];

@@ -81,6 +81,16 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+// 32 bytes, a whole sector, in one access; p on a 32-byte boundary
+__device__ __forceinline__ void load_sector(const void *p, uint32_t (&w)[8]) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p) : "memory");
+}
+__device__ __forceinline__ void store_sector(void *p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
+
 template <class T>
 __device__ __forceinline__ float to_f32(T v);
 template <>
@@ -259,6 +269,13 @@ constexpr int kGroup = RA_CHECKPOINT8_GROUP;
 constexpr uint32_t kStepNan = 255;
 
 __device__ __forceinline__ uint32_t magnitude_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// the largest magnitude of three values, as bits; a NaN counts as the largest
+__device__ __forceinline__ uint32_t top_of(uint32_t top, float a, float b) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(__uint_as_float(top)), "f"(a), "f"(b));
+    return __float_as_uint(r) & 0x7fffffffu;
+}
 
 // A group's byte and the factor that turns its values into steps: 2^(127 - e),
 // with which the product is exact.  A marked group's factor is 0.  At the very

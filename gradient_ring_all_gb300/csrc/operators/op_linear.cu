@@ -36,7 +36,7 @@ struct Epilogue {
     uint8_t *e;
     int64_t ldo, ldr, groups;
     int out_f32, bias_f32, res_f32, act;
-    int vec;     // bias and the rows of out and res start on 16-byte boundaries
+    int vec;     // bias, the rows of out and res, and q start on 32-byte boundaries
 };
 
 // v += the 32 values at p[0..32) (those below count, where not all are there)
@@ -45,12 +45,11 @@ __device__ __forceinline__ void add32(const void *base, int64_t at, int f32, boo
         const float *p = static_cast<const float *>(base) + at;
         if (full) {
 #pragma unroll
-            for (int g = 0; g < 8; ++g) {
-                const float4 x = reinterpret_cast<const float4 *>(p)[g];
-                v[4 * g] += x.x;
-                v[4 * g + 1] += x.y;
-                v[4 * g + 2] += x.z;
-                v[4 * g + 3] += x.w;
+            for (int g = 0; g < 4; ++g) {
+                uint32_t w[8];
+                load_sector(p + 8 * g, w);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[8 * g + k] += __uint_as_float(w[k]);
             }
         } else {
 #pragma unroll
@@ -61,13 +60,13 @@ __device__ __forceinline__ void add32(const void *base, int64_t at, int f32, boo
         const uint16_t *p = static_cast<const uint16_t *>(base) + at;
         if (full) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const uint4 x = reinterpret_cast<const uint4 *>(p)[g];
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            for (int g = 0; g < 2; ++g) {
+                uint32_t w[8];
+                load_sector(p + 16 * g, w);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    v[8 * g + 2 * k] += __uint_as_float(w[k] << 16);
-                    v[8 * g + 2 * k + 1] += __uint_as_float(w[k] & 0xffff0000u);
+                for (int k = 0; k < 8; ++k) {
+                    v[16 * g + 2 * k] += __uint_as_float(w[k] << 16);
+                    v[16 * g + 2 * k + 1] += __uint_as_float(w[k] & 0xffff0000u);
                 }
             }
         } else {
@@ -90,18 +89,22 @@ __device__ __forceinline__ void finish32(const Epilogue &ep, int64_t row, int64_
         if (ep.q) {
             uint32_t top = 0;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
+            for (int j = 0; j < 32; ++j)
                 if (j >= count) v[j] = 0.0f;
-                top = max(top, magnitude_bits(v[j]));
-            }
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) top = top_of(top, v[j], v[j + 1]);
             const Step step = step_of(top);
             const int64_t u = row * ep.groups + n0 / kGroup;
             uint32_t w[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) w[k] = quantise4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3], step);
-            uint4 *q = reinterpret_cast<uint4 *>(ep.q + u * kGroup);
-            q[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            if (ep.vec) {
+                store_sector(ep.q + u * kGroup, w);
+            } else {
+                uint4 *q = reinterpret_cast<uint4 *>(ep.q + u * kGroup);
+                q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
             ep.e[u] = (uint8_t)step.e;
         }
         with_act(ep.act, [&](auto a) {
@@ -113,9 +116,13 @@ __device__ __forceinline__ void finish32(const Epilogue &ep, int64_t row, int64_
         if (ep.q) {
             const int64_t u = row * ep.groups + n0 / kGroup;
             const float step = step_value(ep.e[u]);
-            const uint4 *q = reinterpret_cast<const uint4 *>(ep.q + u * kGroup);
-            const uint4 q0 = q[0], q1 = q[1];
-            const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+            uint32_t w[8];
+            if (ep.vec) {
+                load_sector(ep.q + u * kGroup, w);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) w[k] = reinterpret_cast<const uint32_t *>(ep.q + u * kGroup)[k];
+            }
             with_act(ep.act, [&](auto a) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] *= act_slope<decltype(a)::value>(dequantise(w[j / 4], j % 4, step));
@@ -127,7 +134,12 @@ __device__ __forceinline__ void finish32(const Epilogue &ep, int64_t row, int64_
         float *p = static_cast<float *>(ep.out) + row * ep.ldo + n0;
         if (full) {
 #pragma unroll
-            for (int g = 0; g < 8; ++g) reinterpret_cast<float4 *>(p)[g] = make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+            for (int g = 0; g < 4; ++g) {
+                uint32_t w[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[8 * g + k]);
+                store_sector(p + 8 * g, w);
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -137,9 +149,11 @@ __device__ __forceinline__ void finish32(const Epilogue &ep, int64_t row, int64_
         uint16_t *p = static_cast<uint16_t *>(ep.out) + row * ep.ldo + n0;
         if (full) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float *x = v + 8 * g;
-                reinterpret_cast<uint4 *>(p)[g] = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+            for (int g = 0; g < 2; ++g) {
+                uint32_t w[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) w[k] = pack2(v[16 * g + 2 * k], v[16 * g + 2 * k + 1]);
+                store_sector(p + 16 * g, w);
             }
         } else {
 #pragma unroll
@@ -257,6 +271,16 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
 // Shared-memory operand descriptor of a 128-byte swizzled tile: start
 // address, the two strides between 8-row (1024-byte) swizzle atoms, in 16-byte
 // units.  K-major: atoms of 8 rows x 64 k, `sbo` from one 8 rows to the next,
@@ -288,15 +312,13 @@ __device__ __forceinline__ void release(uint32_t bar, int lane) {
 // the product
 
 constexpr int kBM = 128, kBK = 64;
-constexpr int kEpilogueWarps = 8;
-constexpr int kProductThreads = (kEpilogueWarps + 2) * 32;
 // The tensor core adds to its binary32 sums by truncation: a sum over k comes
 // out about 1e-9 k short (measured: 2.3e-7 at k = 256, 4.4e-6 at 4096, 3.8e-5
 // at 32768, all toward zero).  That is far below a bf16 result's rounding, but
-// not below a binary32 one's: there the tensor core sums kChunk steps (256 of
+// not below a binary32 one's: there the tensor core sums kChunk steps (512 of
 // k) at a time, and the epilogue warps add the chunks in registers with rounding
 // to nearest, while the next chunk is made.
-constexpr int kChunk = 4;
+constexpr int kChunk = 8;
 constexpr int kGroupM = 8;  // row tiles that share the columns' tiles in L2
 
 // A tile is BN columns wide and 128 rows high per block; in a pair each block
@@ -307,6 +329,8 @@ struct Shape {
     static constexpr int kABytes = kBM * kBK * 2, kBBytes = kBCols * kBK * 2;
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kStages = kStageBytes > 24576 ? 7 : 8;
+    // epilogue warps: four take the tile's 128 rows, and every further four share its columns
+    static constexpr int kWarps = BN >= 128 ? 16 : 8, kCols = BN / (kWarps / 4), kThreads = (kWarps + 2) * 32;
     static constexpr int kTmemCols = 2 * BN;  // two tiles' sums: one is finished while the next is made
     static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024 + 256;
 };
@@ -330,7 +354,7 @@ __device__ __forceinline__ void tile_at(const Product &p, int tile, int *tm, int
 }
 
 template <int MODE, int BN, bool PAIR, bool F32>
-__global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __grid_constant__ Product p) {
+__global__ void __launch_bounds__(Shape<BN, PAIR>::kThreads, 1) product_kernel(const __grid_constant__ Product p) {
     using S = Shape<BN, PAIR>;
     constexpr bool kAmn = MODE == kWgrad, kBmn = MODE != kDgrad;
     extern __shared__ unsigned char raw[];
@@ -344,7 +368,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int rank = PAIR ? blockIdx.x & 1 : 0;
 
-    if (warp == kEpilogueWarps) {
+    if (warp == S::kWarps) {
         if (lane == 0) {
             for (int s = 0; s < S::kStages; ++s) {
                 mbar_init(full + 8 * s, 1);
@@ -352,13 +376,13 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
             }
             for (int s = 0; s < 2; ++s) {
                 mbar_init(done + 8 * s, 1);
-                mbar_init(freed + 8 * s, kEpilogueWarps * S::kBlocks);
+                mbar_init(freed + 8 * s, S::kWarps * S::kBlocks);
             }
             mbar_init(drained, 1);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         __syncwarp();
-    } else if (warp == kEpilogueWarps + 1) {
+    } else if (warp == S::kWarps + 1) {
         tmem_alloc<PAIR, S::kTmemCols>(smem_addr(tmem_slot));
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -372,7 +396,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
 
     const int tile_count = p.tiles_m * p.tiles_n;
     bool ok = true;
-    if (warp == kEpilogueWarps) {  // TMA
+    if (warp == S::kWarps) {  // TMA
         int s = 0;
         uint32_t phase = 0;
         int64_t issued = 0;
@@ -411,7 +435,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
         // shared memory must outlive the copies and the products that read it
         for (int64_t i = issued > S::kStages ? issued - S::kStages : 0; i < issued && ok; ++i)
             ok = __all_sync(0xffffffffu, wait(empty + 8 * (uint32_t)(i % S::kStages), (uint32_t)(i / S::kStages) & 1));
-    } else if (warp == kEpilogueWarps + 1) {  // tcgen05.mma
+    } else if (warp == S::kWarps + 1) {  // tcgen05.mma
         if (rank == 0) {
             constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (kAmn ? 1u << 15 : 0) | (kBmn ? 1u << 16 : 0) | (BN / 8) << 17 | (S::kRows / 16) << 24;
             // 16 of k further on in a stage, and a stage further on, in the descriptors' 16-byte units
@@ -462,19 +486,18 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
         }
     } else {
         const uint32_t freed_bar = PAIR ? in_leader(freed) : freed;
-        constexpr int kHalf = BN / 2;  // each four warps finish half of the columns
         int acc = 0;
         uint32_t acc_phase = 0;
-        const uint32_t mine = tmem + (warp / 4) * kHalf + ((uint32_t)(warp % 4 * 32) << 16);
+        const uint32_t mine = tmem + (warp / 4) * S::kCols + ((uint32_t)(warp % 4 * 32) << 16);
         for (int tile = blockIdx.x / S::kBlocks; tile < tile_count && ok; tile += gridDim.x / S::kBlocks) {
             int tm, tn;
             tile_at(p, tile, &tm, &tn);
             const int64_t row = (int64_t)tm * S::kRows + rank * kBM + warp % 4 * 32 + lane;
-            const int64_t c0 = (int64_t)tn * BN + warp / 4 * kHalf;
+            const int64_t c0 = (int64_t)tn * BN + warp / 4 * S::kCols;
             if constexpr (F32) {
-                float sum[kHalf / 32][32];
+                float sum[S::kCols / 32][32];
 #pragma unroll
-                for (int g = 0; g < kHalf / 32; ++g)
+                for (int g = 0; g < S::kCols / 32; ++g)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) sum[g][j] = 0.0f;
                 for (int k = 0; k < p.steps || k == 0; k += kChunk) {
@@ -483,28 +506,21 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     if (p.steps > 0) {
 #pragma unroll
-                        for (int g = 0; g < kHalf / 32; ++g) {
-                            float v[32];
-                            tmem_load32(mine + acc * BN + g * 32, v);
+                        for (int g = 0; g < S::kCols / 16; ++g) {
+                            float v[16];
+                            tmem_load16(mine + acc * BN + g * 16, v);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) sum[g][j] += v[j];
+                            for (int j = 0; j < 16; ++j) sum[g / 2][g % 2 * 16 + j] += v[j];
                         }
                     }
                     release<PAIR>(freed_bar + 8 * acc, lane);
                     flip(acc, acc_phase);
                 }
                 if (!ok) break;
-#pragma unroll 1
-                for (int g = 0; g < kHalf / 32; ++g) {
-                    float v[32];
 #pragma unroll
-                    for (int h = 0; h < kHalf / 32; ++h)
-                        if (g == h) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j] = sum[h][j];
-                        }
+                for (int g = 0; g < S::kCols / 32; ++g) {
                     const int64_t n0 = c0 + g * 32;
-                    if (row < p.rows && n0 < p.cols) finish32<MODE>(p.ep, row, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
+                    if (row < p.rows && n0 < p.cols) finish32<MODE>(p.ep, row, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), sum[g]);
                 }
                 __syncwarp();
             } else {
@@ -512,7 +528,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll 1
-                for (int g = 0; g < kHalf / 32; ++g) {
+                for (int g = 0; g < S::kCols / 32; ++g) {
                     const int64_t n0 = c0 + g * 32;
                     if (n0 >= p.cols) break;
                     float v[32];
@@ -536,7 +552,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) product_kernel(const __gri
         cluster_sync();  // neither block's memory goes while the other may still reach it
     else
         __syncthreads();
-    if (warp == kEpilogueWarps + 1) {
+    if (warp == S::kWarps + 1) {
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         tmem_free<PAIR, S::kTmemCols>(tmem);
     }
@@ -739,7 +755,7 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, most = sms / S::kBlocks;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * S::kBlocks));
-    cfg.blockDim = dim3(kProductThreads);
+    cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -771,7 +787,7 @@ cudaError_t launch_product(const Mat &a, const Mat &b, int64_t rows, int64_t col
                            cudaStream_t s) {
     Product p = {};
     p.ep = ep;
-    p.ep.vec = out.aligned(16) && (bias.empty() || bias.aligned(16)) && (res.empty() || res.aligned(16));
+    p.ep.vec = out.aligned(32) && (bias.empty() || bias.aligned(32)) && (res.empty() || res.aligned(32)) && reinterpret_cast<uintptr_t>(ep.q) % 32 == 0;
     p.rows = rows;
     p.cols = cols;
     p.steps = (int)ceil_div<int64_t>(k, kBK);
