@@ -81,8 +81,11 @@ __device__ __forceinline__ void add32(const void *base, int64_t at, int f32, boo
 // 32, so one checkpoint group) on; `count` of them exist.  The sums of columns
 // that do not exist are not looked at: they are zero, or NaN where A's row
 // holds an infinity.
+// Returns the group's step byte (forward, with a checkpoint), which the caller
+// stores with its neighbours'.
 template <int MODE>
-__device__ __forceinline__ void finish32(const Epilogue &ep, int64_t row, int64_t n0, int count, float (&v)[32]) {
+__device__ __forceinline__ uint32_t finish32(const Epilogue &ep, int64_t row, int64_t n0, int count, float (&v)[32]) {
+    uint32_t step_byte = 0;
     const bool full = count == 32 && ep.vec;
     if constexpr (MODE == kForward) {
         if (ep.bias) add32(ep.bias, n0, ep.bias_f32, full, count, v);
@@ -105,7 +108,7 @@ __device__ __forceinline__ void finish32(const Epilogue &ep, int64_t row, int64_
                 q[0] = make_uint4(w[0], w[1], w[2], w[3]);
                 q[1] = make_uint4(w[4], w[5], w[6], w[7]);
             }
-            ep.e[u] = (uint8_t)step.e;
+            step_byte = step.e;
         }
         with_act(ep.act, [&](auto a) {
 #pragma unroll
@@ -160,6 +163,23 @@ __device__ __forceinline__ void finish32(const Epilogue &ep, int64_t row, int64_
             for (int j = 0; j < 32; ++j)
                 if (j < count) p[j] = (uint16_t)f32_to_bf16_bits(v[j]);
         }
+    }
+    return step_byte;
+}
+
+// the step bytes of COLS / 32 neighbouring groups of a row, in one store where
+// all are there and the place allows it
+template <int COLS>
+__device__ __forceinline__ void store_steps(const Epilogue &ep, int64_t row, int64_t n0, uint32_t bytes) {
+    constexpr int kCount = COLS / 32;
+    const int64_t g = n0 / kGroup;
+    uint8_t *p = ep.e + row * ep.groups + g;
+    if (kCount == 2 && g + 1 < ep.groups && reinterpret_cast<uintptr_t>(p) % 2 == 0) {
+        *reinterpret_cast<uint16_t *>(p) = (uint16_t)bytes;
+    } else {
+#pragma unroll
+        for (int k = 0; k < kCount; ++k)
+            if (g + k < ep.groups) p[k] = (uint8_t)(bytes >> (8 * k));
     }
 }
 
@@ -517,16 +537,19 @@ __global__ void __launch_bounds__(Shape<BN, PAIR>::kThreads, 1) product_kernel(c
                     flip(acc, acc_phase);
                 }
                 if (!ok) break;
+                uint32_t steps = 0;
 #pragma unroll
                 for (int g = 0; g < S::kCols / 32; ++g) {
                     const int64_t n0 = c0 + g * 32;
-                    if (row < p.rows && n0 < p.cols) finish32<MODE>(p.ep, row, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), sum[g]);
+                    if (row < p.rows && n0 < p.cols) steps |= finish32<MODE>(p.ep, row, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), sum[g]) << (8 * g);
                 }
+                if (MODE == kForward && p.ep.q && row < p.rows && c0 < p.cols) store_steps<S::kCols>(p.ep, row, c0, steps);
                 __syncwarp();
             } else {
                 ok = __all_sync(0xffffffffu, wait(done + 8 * acc, acc_phase));
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                uint32_t steps = 0;
 #pragma unroll 1
                 for (int g = 0; g < S::kCols / 32; ++g) {
                     const int64_t n0 = c0 + g * 32;
@@ -537,9 +560,10 @@ __global__ void __launch_bounds__(Shape<BN, PAIR>::kThreads, 1) product_kernel(c
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0.0f;
                     }
-                    if (row < p.rows) finish32<MODE>(p.ep, row, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
+                    if (row < p.rows) steps |= finish32<MODE>(p.ep, row, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v) << (8 * g);
                     __syncwarp();
                 }
+                if (MODE == kForward && p.ep.q && row < p.rows && c0 < p.cols) store_steps<S::kCols>(p.ep, row, c0, steps);
                 release<PAIR>(freed_bar + 8 * acc, lane);
                 flip(acc, acc_phase);
             }
@@ -586,7 +610,7 @@ __global__ void __launch_bounds__(kStageThreads) lay_out_kernel(const uint16_t *
 constexpr int kColumnThreads = 512;
 template <int W, int LANES>
 __global__ void __launch_bounds__(kColumnThreads) column_sum_kernel(const uint16_t *dy, int64_t ld, int64_t m, int64_t n, int accumulate, float *db) {
-    constexpr int kRowsAtOnce = kColumnThreads / LANES, kCols = LANES * W, kFlight = 8;
+    constexpr int kRowsAtOnce = kColumnThreads / LANES, kCols = LANES * W, kFlight = 16;
     __shared__ float part[kRowsAtOnce][kCols + 1];
     __shared__ float sum[kCols];
     namespace cg = cooperative_groups;
@@ -712,10 +736,13 @@ cudaError_t sm_count(int *out) {
 
 cudaError_t launch_column_sum(const Mat &dy, int accumulate, float *db, cudaStream_t s) {
     const bool wide = dy.aligned(16) && dy.cols % 8 == 0;
-    int shares = 1;  // blocks along the rows: at least 256 rows each, at most a portable cluster
+    auto kernel = wide ? column_sum_kernel<8, 16> : column_sum_kernel<1, 32>;
+    // blocks along the rows: at least 256 rows each, at most a portable cluster
+    // (16 a cluster were slower: 17 against 13 us at 8192 x 2048, 47 against 31 at 8192 x 8192)
+    int shares = 1;
     while (shares < 8 && dy.rows / shares >= 512) shares *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ceil_div<int64_t>(dy.cols, wide ? 64 : 32), (unsigned)shares);
+    cfg.gridDim = dim3((unsigned)ceil_div<int64_t>(dy.cols, wide ? 128 : 32), (unsigned)shares);
     cfg.blockDim = dim3(kColumnThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -727,7 +754,7 @@ cudaError_t launch_column_sum(const Mat &dy, int accumulate, float *db, cudaStre
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, wide ? column_sum_kernel<8, 8> : column_sum_kernel<1, 32>, static_cast<const uint16_t *>(dy.data), dy.ld,
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<const uint16_t *>(dy.data), dy.ld,
                                              dy.rows, dy.cols, accumulate, db);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
