@@ -5,6 +5,8 @@
 
 #include <math.h>
 
+#include <atomic>
+
 #include "../../../include/ra_operators.h"
 #include "../ra_internal.h"
 #include "../ra_kernels.cuh"
@@ -65,6 +67,18 @@ inline ra_status cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return RA_OK;
     record_cuda_error(e);
     return RA_ERR_CUDA;
+}
+
+// dynamic shared memory past 48 KB, asked for once per kernel and device
+template <auto KERNEL>
+inline cudaError_t opt_in_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1))) return e;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or((uint64_t)1 << dev, std::memory_order_acq_rel);
+    return e;
 }
 
 template <class I>

@@ -15,8 +15,6 @@
 
 #include <cooperative_groups.h>
 
-#include <atomic>
-
 #include "op_common.cuh"
 
 namespace ra {
@@ -770,15 +768,8 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
         if (e == cudaSuccess) e = tensor_map(&p.b, b, MODE == kDgrad ? S::kBCols : kBK);
         if (e != cudaSuccess) return e;
     }
-    static std::atomic<uint64_t> opted_in{0};  // a bit per device
-    int dev = 0;
-    e = cudaGetDevice(&dev);
+    e = opt_in_smem<product_kernel<MODE, BN, PAIR, F32>>((int)S::kSmem);
     if (e != cudaSuccess) return e;
-    if (dev >= 64 || !(opted_in.load(std::memory_order_acquire) >> dev & 1)) {
-        e = cudaFuncSetAttribute(product_kernel<MODE, BN, PAIR, F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
-        if (e != cudaSuccess) return e;
-        if (dev < 64) opted_in.fetch_or((uint64_t)1 << dev, std::memory_order_acq_rel);
-    }
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, most = sms / S::kBlocks;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * S::kBlocks));
