@@ -8,30 +8,6 @@ namespace {
 
 constexpr int kThreadsCkpt = 256;
 
-struct PackParams {
-    const void *x;  // pack: the activation; unpack: unused
-    void *out;      // unpack: the restored activation
-    int64_t ld;     // elements between the rows of x or out
-    int8_t *q;
-    uint8_t *e;
-    int64_t rows, cols, groups;  // groups a row
-    int act;
-};
-
-// Unit number -> row and unit within it.  32-bit division where the numbers
-// fit (an ordinary size): a 64-bit one costs as much as the rest of a unit's
-// work.
-__device__ __forceinline__ void row_of(int64_t u, int64_t per_row, int64_t total, int64_t *r, int64_t *k) {
-    if (total <= 0x7fffffff) {
-        const uint32_t q = (uint32_t)u / (uint32_t)per_row;
-        *r = q;
-        *k = (uint32_t)u - q * (uint32_t)per_row;
-    } else {
-        *r = u / per_row;
-        *k = u - *r * per_row;
-    }
-}
-
 // Rows on 16-byte boundaries: a thread takes half a group, 16 values, with
 // 16-byte loads and stores; two neighbouring lanes settle the group's step.
 // Bound by memory: x once in (2 or 4 bytes a value), 33/32 byte out.
@@ -69,31 +45,7 @@ __global__ void __launch_bounds__(kThreadsCkpt) pack_kernel(const PackParams p) 
 template <class T>
 __global__ void __launch_bounds__(kThreadsCkpt) unpack_kernel(const PackParams p) {
     pdl_enter();
-    const int64_t halves = 2 * p.groups, total = p.rows * halves;
-    const int64_t stride = (int64_t)gridDim.x * kThreadsCkpt;
-    for (int64_t u = (int64_t)blockIdx.x * kThreadsCkpt + threadIdx.x; u < total; u += stride) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p.q) + u);
-        const float step = step_value(__ldg(p.e + u / 2));
-        int64_t r, k;
-        row_of(u, halves, total, &r, &k);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-        float v[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = dequantise(w[j / 4], j % 4, step);
-        with_act(p.act, [&](auto a) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = act_value<decltype(a)::value>(v[j]);
-        });
-        T *dst = static_cast<T *>(p.out) + r * p.ld + k * 16;
-        const int64_t left = p.cols - k * 16;
-        if (left >= 16) {
-            store_w<T, 16>(dst, v);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-                if (j < left) dst[j] = from_f32<T>(v[j]);
-        }
-    }
+    unpack_halves<T>(p, (int64_t)blockIdx.x * kThreadsCkpt + threadIdx.x, (int64_t)gridDim.x * kThreadsCkpt);
 }
 
 // Byte j of the result is byte (lane mod 4) of lane j's word, of the four

@@ -324,5 +324,59 @@ __device__ __forceinline__ float dequantise(uint32_t word, int k, float step) {
     return (float)(int)(int8_t)(word >> (8 * k)) * step;
 }
 
+struct PackParams {
+    const void *x;  // pack: the activation
+    void *out;      // unpack: the restored activation, its rows on 16-byte boundaries
+    int64_t ld;     // elements between the rows of x or out
+    int8_t *q;
+    uint8_t *e;
+    int64_t rows, cols, groups;  // groups a row
+    int act;
+};
+
+// Unit number -> row and unit within it.  32-bit division where the numbers
+// fit (an ordinary size): a 64-bit one costs as much as the rest of a unit's
+// work.
+__device__ __forceinline__ void row_of(int64_t u, int64_t per_row, int64_t total, int64_t *r, int64_t *k) {
+    if (total <= 0x7fffffff) {
+        const uint32_t q = (uint32_t)u / (uint32_t)per_row;
+        *r = q;
+        *k = (uint32_t)u - q * (uint32_t)per_row;
+    } else {
+        *r = u / per_row;
+        *k = u - *r * per_row;
+    }
+}
+
+// Threads `first`, `first` + `stride`, .. restore half groups (16 values) to
+// rows on 16-byte boundaries.
+template <class T>
+__device__ __forceinline__ void unpack_halves(const PackParams &p, int64_t first, int64_t stride) {
+    const int64_t halves = 2 * p.groups, total = p.rows * halves;
+    for (int64_t u = first; u < total; u += stride) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p.q) + u);
+        const float step = step_value(__ldg(p.e + u / 2));
+        int64_t r, k;
+        row_of(u, halves, total, &r, &k);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = dequantise(w[j / 4], j % 4, step);
+        with_act(p.act, [&](auto a) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = act_value<decltype(a)::value>(v[j]);
+        });
+        T *dst = static_cast<T *>(p.out) + r * p.ld + k * 16;
+        const int64_t left = p.cols - k * 16;
+        if (left >= 16) {
+            store_w<T, 16>(dst, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (j < left) dst[j] = from_f32<T>(v[j]);
+        }
+    }
+}
+
 }  // namespace op
 }  // namespace ra

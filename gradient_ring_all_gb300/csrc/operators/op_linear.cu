@@ -23,6 +23,10 @@ namespace {
 
 enum Mode { kForward = 0, kDgrad = 1, kWgrad = 2 };
 
+// How blocks share tiles: one tile a block, one for a pair of blocks that work
+// as one tensor core, or one for a cluster that splits k.
+enum Kind { kSingle = 0, kPair = 1, kSplit = 2 };
+
 // ---------------------------------------------------------------------------
 // epilogue
 
@@ -217,12 +221,14 @@ __device__ __forceinline__ bool elected() {
     asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
     return one;
 }
-// the same shared-memory place in the pair's first block
-__device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
+// the same shared-memory place in another block of the cluster, and in a
+// pair's first
+__device__ __forceinline__ uint32_t in_block(uint32_t addr, int rank) {
     uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
+__device__ __forceinline__ uint32_t in_leader(uint32_t addr) { return in_block(addr, 0); }
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -341,12 +347,15 @@ constexpr int kGroupM = 8;  // row tiles that share the columns' tiles in L2
 
 // A tile is BN columns wide and 128 rows high per block; in a pair each block
 // holds its own rows of A and half of B's columns, which the two share.
-template <int BN, bool PAIR>
+template <int BN, int KIND>
 struct Shape {
-    static constexpr int kBlocks = PAIR ? 2 : 1, kRows = kBM * kBlocks, kBCols = BN / kBlocks;
+    static constexpr bool kIsPair = KIND == kPair, kIsSplit = KIND == kSplit;
+    static constexpr int kBlocks = kIsPair ? 2 : 1, kRows = kBM * kBlocks, kBCols = BN / kBlocks;
     static constexpr int kABytes = kBM * kBK * 2, kBBytes = kBCols * kBK * 2;
     static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = kStageBytes > 24576 ? 7 : 8;
+    // all of an SM's shared memory, or half of it where two blocks share an SM
+    static constexpr int kStages = kIsSplit ? 4 : kStageBytes > 24576 ? 7 : 8;
+    static constexpr int kBlocksPerSm = kIsSplit ? 2 : 1;
     // epilogue warps: four take the tile's 128 rows, and every further four share its columns
     static constexpr int kWarps = BN >= 128 ? 16 : 8, kCols = BN / (kWarps / 4), kThreads = (kWarps + 2) * 32;
     static constexpr int kTmemCols = 2 * BN;  // two tiles' sums: one is finished while the next is made
@@ -361,6 +370,7 @@ struct Product {
     unsigned int *err;
     int64_t rows, cols;
     int tiles_m, tiles_n, steps;  // steps of kBK along k
+    int splits;                   // blocks that share a tile's steps
     // wgrad: the column sums of B (dy) are wanted too
     float *db;
     const uint16_t *dy;
@@ -376,6 +386,14 @@ __device__ __forceinline__ void tile_at(const Product &p, int tile, int *tm, int
     const int in = tile - tile / band * band;
     *tm = first + in % height;
     *tn = in / height;
+}
+
+// 32 sums of a row of a split tile, column by column, over the stages (whose
+// products are done by then): the lanes of a warp are neighbours
+__device__ __forceinline__ void keep_sums(unsigned char *smem, int col, int row, const float (&v)[32]) {
+    float *to = reinterpret_cast<float *>(smem) + col * kBM + row;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) to[j * kBM] = v[j];
 }
 
 // The bias gradient, by the epilogue warps of the blocks with the first row
@@ -431,9 +449,10 @@ __device__ __forceinline__ void column_sums(const Product &p, int64_t c0, float 
     asm volatile("bar.sync 1, %0;" ::"n"(S::kWarps * 32) : "memory");
 }
 
-template <int MODE, int BN, bool PAIR, bool F32>
-__global__ void __launch_bounds__(Shape<BN, PAIR>::kThreads, 1) product_kernel(const __grid_constant__ Product p) {
-    using S = Shape<BN, PAIR>;
+template <int MODE, int BN, int KIND, bool F32>
+__global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kBlocksPerSm) product_kernel(const __grid_constant__ Product p) {
+    using S = Shape<BN, KIND>;
+    constexpr bool PAIR = S::kIsPair;
     constexpr bool kAmn = MODE == kWgrad, kBmn = MODE != kDgrad;
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
@@ -445,6 +464,12 @@ __global__ void __launch_bounds__(Shape<BN, PAIR>::kThreads, 1) product_kernel(c
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kStages * S::kStageBytes + 16 * S::kStages + 40);
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int rank = PAIR ? blockIdx.x & 1 : 0;
+    // the first tile and the distance to the next; the steps along k
+    const int share = S::kIsSplit ? p.splits : S::kBlocks;
+    const int tile0 = blockIdx.x / share, tile_step = gridDim.x / share;
+    const int part = S::kIsSplit ? blockIdx.x % p.splits : 0;
+    const int k_begin = S::kIsSplit ? p.steps * part / p.splits : 0, k_end = S::kIsSplit ? p.steps * (part + 1) / p.splits : p.steps;
+    const int steps = k_end - k_begin;
 
     if (warp == S::kWarps) {
         if (lane == 0) {
@@ -478,11 +503,11 @@ __global__ void __launch_bounds__(Shape<BN, PAIR>::kThreads, 1) product_kernel(c
         int s = 0;
         uint32_t phase = 0;
         int64_t issued = 0;
-        for (int tile = blockIdx.x / S::kBlocks; tile < tile_count && ok; tile += gridDim.x / S::kBlocks) {
+        for (int tile = tile0; tile < tile_count && ok; tile += tile_step) {
             int tm, tn;
             tile_at(p, tile, &tm, &tn);
             const int row = tm * S::kRows + rank * kBM, col = tn * BN + rank * S::kBCols;
-            for (int k = 0; k < p.steps; ++k) {
+            for (int k = k_begin; k < k_end; ++k) {
                 ok = __all_sync(0xffffffffu, wait(empty + 8 * s, phase ^ 1));
                 if (!ok) break;
                 const uint32_t a = tiles + s * S::kStageBytes, b = a + S::kABytes;
@@ -521,15 +546,15 @@ __global__ void __launch_bounds__(Shape<BN, PAIR>::kThreads, 1) product_kernel(c
             const uint64_t a0 = operand(tiles, kAmn ? 8192 : 16, 1024), b0 = operand(tiles + S::kABytes, kBmn ? 8192 : 16, 1024);
             int s = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
-            for (int tile = blockIdx.x / S::kBlocks; tile < tile_count && ok; tile += gridDim.x / S::kBlocks) {
-                for (int k = 0; k < p.steps || k == 0; ++k) {
+            for (int tile = tile0; tile < tile_count && ok; tile += tile_step) {
+                for (int k = 0; k < steps || k == 0; ++k) {
                     if (F32 ? k % kChunk == 0 : k == 0) {  // a new sum
                         ok = __all_sync(0xffffffffu, wait(freed + 8 * acc, acc_phase ^ 1));
                         if (!ok) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     }
-                    const bool last = k + 1 >= p.steps || (F32 && k % kChunk == kChunk - 1);
-                    if (p.steps > 0) {
+                    const bool last = k + 1 >= steps || (F32 && k % kChunk == kChunk - 1);
+                    if (steps > 0) {
                         ok = __all_sync(0xffffffffu, wait(full + 8 * s, phase));
                         if (!ok) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -567,12 +592,12 @@ __global__ void __launch_bounds__(Shape<BN, PAIR>::kThreads, 1) product_kernel(c
         int acc = 0;
         uint32_t acc_phase = 0;
         const uint32_t mine = tmem + (warp / 4) * S::kCols + ((uint32_t)(warp % 4 * 32) << 16);
-        for (int tile = blockIdx.x / S::kBlocks; tile < tile_count && ok; tile += gridDim.x / S::kBlocks) {
+        for (int tile = tile0; tile < tile_count && ok; tile += tile_step) {
             int tm, tn;
             tile_at(p, tile, &tm, &tn);
             const int64_t row = (int64_t)tm * S::kRows + rank * kBM + warp % 4 * 32 + lane;
             const int64_t c0 = (int64_t)tn * BN + warp / 4 * S::kCols;
-            if (MODE == kWgrad && p.db && tm == 0)
+            if (MODE == kWgrad && p.db && tm == 0 && part == 0)
                 column_sums<S>(p, (int64_t)tn * BN + rank * S::kBCols, reinterpret_cast<float *>(smem + S::kStages * S::kStageBytes + 256), warp, lane);
             if constexpr (F32) {
                 float sum[S::kCols / 32][32];
@@ -580,11 +605,11 @@ __global__ void __launch_bounds__(Shape<BN, PAIR>::kThreads, 1) product_kernel(c
                 for (int g = 0; g < S::kCols / 32; ++g)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) sum[g][j] = 0.0f;
-                for (int k = 0; k < p.steps || k == 0; k += kChunk) {
+                for (int k = 0; k < steps || k == 0; k += kChunk) {
                     ok = __all_sync(0xffffffffu, wait(done + 8 * acc, acc_phase));
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                    if (p.steps > 0) {
+                    if (steps > 0) {
 #pragma unroll
                         for (int g = 0; g < S::kCols / 16; ++g) {
                             float v[16];
@@ -597,33 +622,42 @@ __global__ void __launch_bounds__(Shape<BN, PAIR>::kThreads, 1) product_kernel(c
                     flip(acc, acc_phase);
                 }
                 if (!ok) break;
-                uint32_t steps = 0;
+                if constexpr (S::kIsSplit) {
+#pragma unroll
+                    for (int g = 0; g < S::kCols / 32; ++g) keep_sums(smem, warp / 4 * S::kCols + g * 32, warp % 4 * 32 + lane, sum[g]);
+                    continue;
+                }
+                uint32_t step_bytes = 0;
 #pragma unroll
                 for (int g = 0; g < S::kCols / 32; ++g) {
                     const int64_t n0 = c0 + g * 32;
-                    if (row < p.rows && n0 < p.cols) steps |= finish32<MODE>(p.ep, row, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), sum[g]) << (8 * g);
+                    if (row < p.rows && n0 < p.cols) step_bytes |= finish32<MODE>(p.ep, row, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), sum[g]) << (8 * g);
                 }
-                if (MODE == kForward && p.ep.q && row < p.rows && c0 < p.cols) store_steps<S::kCols>(p.ep, row, c0, steps);
+                if (MODE == kForward && !S::kIsSplit && p.ep.q && row < p.rows && c0 < p.cols) store_steps<S::kCols>(p.ep, row, c0, step_bytes);
                 __syncwarp();
             } else {
                 ok = __all_sync(0xffffffffu, wait(done + 8 * acc, acc_phase));
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                uint32_t steps = 0;
+                uint32_t step_bytes = 0;
 #pragma unroll 1
                 for (int g = 0; g < S::kCols / 32; ++g) {
                     const int64_t n0 = c0 + g * 32;
                     if (n0 >= p.cols) break;
                     float v[32];
                     tmem_load32(mine + acc * BN + g * 32, v);
-                    if (p.steps == 0) {
+                    if (steps == 0) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0.0f;
                     }
-                    if (row < p.rows) steps |= finish32<MODE>(p.ep, row, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v) << (8 * g);
+                    if constexpr (S::kIsSplit) {
+                        keep_sums(smem, warp / 4 * S::kCols + g * 32, warp % 4 * 32 + lane, v);
+                        continue;
+                    }
+                    if (row < p.rows) step_bytes |= finish32<MODE>(p.ep, row, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v) << (8 * g);
                     __syncwarp();
                 }
-                if (MODE == kForward && p.ep.q && row < p.rows && c0 < p.cols) store_steps<S::kCols>(p.ep, row, c0, steps);
+                if (MODE == kForward && !S::kIsSplit && p.ep.q && row < p.rows && c0 < p.cols) store_steps<S::kCols>(p.ep, row, c0, step_bytes);
                 release<PAIR>(freed_bar + 8 * acc, lane);
                 flip(acc, acc_phase);
             }
@@ -631,8 +665,33 @@ __global__ void __launch_bounds__(Shape<BN, PAIR>::kThreads, 1) product_kernel(c
     }
     if (!ok) atomicOr(p.err, 1u);
     __syncwarp();
+    if constexpr (S::kIsSplit) {
+        // every block's sums lie in its shared memory: each block adds and
+        // finishes its share of the rows, the splits in their order
+        cluster_sync();
+        const int height = kBM / p.splits, at = threadIdx.x % height, g = threadIdx.x / height;
+        int tm, tn;
+        tile_at(p, tile0, &tm, &tn);
+        const int in_tile = part * height + at;
+        const int64_t row = (int64_t)tm * kBM + in_tile, n0 = (int64_t)tn * BN + g * 32;
+        if (ok && g < BN / 32 && row < p.rows && n0 < p.cols) {
+            float v[32];
+            for (int q = 0; q < p.splits; ++q) {
+                const uint32_t from = in_block(tiles + (g * 32 * kBM + in_tile) * 4, q);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    float x;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(from + j * kBM * 4) : "memory");
+                    v[j] = q ? v[j] + x : x;
+                }
+            }
+            const uint32_t step_byte = finish32<MODE>(p.ep, row, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
+            if (MODE == kForward && p.ep.q) store_steps<32>(p.ep, row, n0, step_byte);
+        }
+        __syncwarp();
+    }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-    if constexpr (PAIR)
+    if constexpr (KIND != kSingle)
         cluster_sync();  // neither block's memory goes while the other may still reach it
     else
         __syncthreads();
@@ -645,22 +704,67 @@ __global__ void __launch_bounds__(Shape<BN, PAIR>::kThreads, 1) product_kernel(c
 // ---------------------------------------------------------------------------
 // operands that TMA cannot read where they lie
 
-// rows x cols of bf16 at any stride, copied to rows `ldo` apart (a multiple of 8)
-constexpr int kStageThreads = 256;
-__global__ void __launch_bounds__(kStageThreads) lay_out_kernel(const uint16_t *x, int64_t ld, int64_t rows, int64_t cols, uint16_t *out, int64_t ldo) {
-    pdl_enter();
-    const int64_t units = ceil_div<int64_t>(cols, 8);  // of 8 columns
-    const int64_t total = rows * units;
-    for (int64_t u = (int64_t)blockIdx.x * kStageThreads + threadIdx.x; u < total; u += (int64_t)gridDim.x * kStageThreads) {
-        const int64_t r = u / units, c = (u - r * units) * 8;
-        uint32_t w[4];
+// An operand to bring into the workspace, as bf16 rows on 16-byte boundaries:
+// a bf16 matrix of any stride, or an 8-bit checkpoint (through its activation).
+struct Layout {
+    const uint16_t *x;  // null: the checkpoint
+    int64_t ld, rows, cols;
+    uint16_t *out;
+    int64_t ldo;
+    PackParams kept;
+    int64_t blocks;  // that work on it
+};
+struct Layouts {
+    Layout a, b;
+};
+
+constexpr int kLayoutThreads = 256;
+
+// Eight columns a thread.  A row may start at any 2-byte address: the two
+// aligned 16-byte words around the eight values are loaded and shifted, except
+// at the matrix's own ends, beyond which nothing is read.
+__device__ __forceinline__ void lay_out(const Layout &l, int64_t block) {
+    const int64_t units = ceil_div<int64_t>(l.cols, 8), total = l.rows * units;
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(l.x), hi = reinterpret_cast<uintptr_t>(l.x + (l.rows - 1) * l.ld + l.cols);
+    for (int64_t u = block * kLayoutThreads + threadIdx.x; u < total; u += l.blocks * kLayoutThreads) {
+        int64_t r, c;
+        row_of(u, units, total, &r, &c);
+        c *= 8;
+        const uint16_t *src = l.x + r * l.ld + c;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(src), word = at & ~(uintptr_t)15;
+        uint32_t w[8];
+        if (c + 8 <= l.cols && word >= lo && word + 32 <= hi) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(word)), y = __ldg(reinterpret_cast<const uint4 *>(word) + 1);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+            if (at & 8)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t lo = c + 2 * k < cols ? x[r * ld + c + 2 * k] : 0, hi = c + 2 * k + 1 < cols ? x[r * ld + c + 2 * k + 1] : 0;
-            w[k] = lo | hi << 16;
+                for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+            if (at & 4)
+#pragma unroll
+                for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+            if (at & 2)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t even = c + 2 * k < l.cols ? src[2 * k] : 0, odd = c + 2 * k + 1 < l.cols ? src[2 * k + 1] : 0;
+                w[k] = even | odd << 16;
+            }
         }
-        *reinterpret_cast<uint4 *>(out + r * ldo + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(l.out + r * l.ldo + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
+}
+
+__global__ void __launch_bounds__(kLayoutThreads) layout_kernel(const Layouts p) {
+    pdl_enter();
+    const bool first = blockIdx.x < p.a.blocks;
+    const Layout &l = first ? p.a : p.b;
+    const int64_t block = first ? blockIdx.x : blockIdx.x - p.a.blocks;
+    if (l.x)
+        lay_out(l, block);
+    else
+        unpack_halves<uint16_t>(l.kept, block * kLayoutThreads + threadIdx.x, l.blocks * kLayoutThreads);
 }
 
 // Column sums of a bf16 matrix (the bias gradient) in a launch of their own,
@@ -774,11 +878,26 @@ bool place(const Mat &a, Workspace *ws, Mat *out) {
     return out->data != nullptr;
 }
 
-cudaError_t lay_out(const Mat &a, const Mat &placed, cudaStream_t s) {
-    if (a.data == placed.data) return cudaSuccess;
-    const int64_t blocks = ceil_div<int64_t>(a.rows * ceil_div<int64_t>(a.cols, 8), kStageThreads);
-    return launch_pdl(lay_out_kernel, blocks < 152 * 16 ? blocks : 152 * 16, kStageThreads, 0, s, static_cast<const uint16_t *>(a.data), a.ld, a.rows, a.cols,
-                      static_cast<uint16_t *>(const_cast<void *>(placed.data)), placed.ld);
+Layout layout_of(const Mat &a, const Mat &placed) {
+    Layout l = {};
+    if (a.data == placed.data) return l;
+    l = Layout{static_cast<const uint16_t *>(a.data), a.ld, a.rows, a.cols, static_cast<uint16_t *>(const_cast<void *>(placed.data)), placed.ld, {}, 0};
+    const int64_t blocks = ceil_div<int64_t>(a.rows * ceil_div<int64_t>(a.cols, 8), kLayoutThreads);
+    l.blocks = blocks < kMaxGrid / 2 ? blocks : kMaxGrid / 2;
+    return l;
+}
+
+Layout layout_of(const PackParams &kept) {
+    Layout l = {};
+    l.kept = kept;
+    const int64_t blocks = ceil_div<int64_t>(kept.rows * kept.groups * 2, kLayoutThreads);
+    l.blocks = blocks < kMaxGrid / 2 ? blocks : kMaxGrid / 2;
+    return l;
+}
+
+cudaError_t launch_layouts(const Layouts &p, cudaStream_t s) {
+    if (p.a.blocks + p.b.blocks == 0) return cudaSuccess;
+    return launch_pdl(layout_kernel, p.a.blocks + p.b.blocks, kLayoutThreads, 0, s, p);
 }
 
 cudaError_t sm_count(int *out) {
@@ -820,22 +939,24 @@ cudaError_t launch_column_sum(const Mat &dy, int accumulate, float *db, cudaStre
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-template <int MODE, int BN, bool PAIR, bool F32>
-cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaStream_t s) {
-    using S = Shape<BN, PAIR>;
+template <int MODE, int BN, int KIND, bool F32>
+cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaStream_t s, int splits = 1) {
+    using S = Shape<BN, KIND>;
     p.tiles_m = p.rows > 0 ? (int)ceil_div<int64_t>(p.rows, S::kRows) : 1;  // no rows: column sums alone
     p.tiles_n = (int)ceil_div<int64_t>(p.cols, BN);
+    p.splits = splits;
     cudaError_t e = cudaSuccess;
     if (p.steps > 0) {
         e = tensor_map(&p.a, a, MODE == kWgrad ? kBK : kBM);
         if (e == cudaSuccess) e = tensor_map(&p.b, b, MODE == kDgrad ? S::kBCols : kBK);
         if (e != cudaSuccess) return e;
     }
-    e = opt_in_smem<product_kernel<MODE, BN, PAIR, F32>>((int)S::kSmem);
+    e = opt_in_smem<product_kernel<MODE, BN, KIND, F32>>((int)S::kSmem);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, most = sms / S::kBlocks;
+    const int cluster = S::kIsSplit ? splits : S::kBlocks;
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, most = S::kIsSplit ? tiles : sms / S::kBlocks;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * S::kBlocks));
+    cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * cluster));
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = S::kSmem;
     cfg.stream = s;
@@ -843,23 +964,28 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = RA_PDL;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = S::kBlocks;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, product_kernel<MODE, BN, PAIR, F32>, p);
+    cfg.numAttrs = KIND == kSingle ? 1 : 2;
+    e = cudaLaunchKernelEx(&cfg, product_kernel<MODE, BN, KIND, F32>, p);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 // The tile: the widest that leaves half of the SMs or more one; the widest is
-// a pair's.
+// a pair's.  Where even the narrowest tiles leave SMs idle and k is long
+// enough, clusters of 2 to 8 blocks split it, two blocks an SM, so long as each
+// keeps 4 steps.
 template <int MODE, bool F32>
 cudaError_t launch_width(Product &p, const Mat &a, const Mat &b, int sms, cudaStream_t s) {
-    const int64_t tm = ceil_div<int64_t>(p.rows, kBM);
-    if (tm * ceil_div<int64_t>(p.cols, 128) <= sms / 2) return launch_tiles<MODE, 64, false, F32>(p, a, b, sms, s);
-    if (tm * ceil_div<int64_t>(p.cols, 256) <= sms / 2) return launch_tiles<MODE, 128, false, F32>(p, a, b, sms, s);
-    return launch_tiles<MODE, 256, true, F32>(p, a, b, sms, s);
+    const int64_t tm = ceil_div<int64_t>(p.rows, kBM), narrow = tm * ceil_div<int64_t>(p.cols, 64);
+    int splits = 1;
+    while (splits < 8 && narrow * splits <= sms && p.steps >= 8 * splits) splits *= 2;
+    if (splits > 1) return launch_tiles<MODE, 64, kSplit, F32>(p, a, b, sms, s, splits);
+    if (tm * ceil_div<int64_t>(p.cols, 128) <= sms / 2) return launch_tiles<MODE, 64, kSingle, F32>(p, a, b, sms, s);
+    if (tm * ceil_div<int64_t>(p.cols, 256) <= sms / 2) return launch_tiles<MODE, 128, kSingle, F32>(p, a, b, sms, s);
+    return launch_tiles<MODE, 256, kPair, F32>(p, a, b, sms, s);
 }
 
 // out (rows x cols) = epilogue(A B); a and b as they lie in memory
@@ -947,8 +1073,7 @@ ra_status ra_linear(const void *x, int64_t ld_x, const void *w, int64_t ld_w, in
             if (mats_overlap(wm, *all[i])) return RA_ERR_OVERLAP;
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = lay_out(mx, a, s);
-    if (e == cudaSuccess) e = lay_out(mw, b, s);
+    const cudaError_t e = launch_layouts(Layouts{layout_of(mx, a), layout_of(mw, b)}, s);
     if (e != cudaSuccess) return cuda_status(e);
     const Epilogue ep{y, bias, residual, save_q, save_e, ld_y, ld_res, ceil_div<int64_t>(n, kGroup), y_dtype == RA_F32, bias_dtype == RA_F32,
                       res_dtype == RA_F32, act, 0};
@@ -979,8 +1104,7 @@ ra_status ra_linear_dgrad(const void *dy, int64_t ld_dy, const void *w, int64_t 
             if (mats_overlap(wm, *all[i])) return RA_ERR_OVERLAP;
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = lay_out(md, a, s);
-    if (e == cudaSuccess) e = lay_out(mw, b, s);
+    const cudaError_t e = launch_layouts(Layouts{layout_of(md, a), layout_of(mw, b)}, s);
     if (e != cudaSuccess) return cuda_status(e);
     const Epilogue ep{dx, nullptr, residual, act ? const_cast<int8_t *>(z_q) : nullptr, const_cast<uint8_t *>(z_e), ld_dx, ld_res,
                       ceil_div<int64_t>(k, kGroup), dx_dtype == RA_F32, 0, res_dtype == RA_F32, act, 0};
@@ -1022,12 +1146,9 @@ ra_status ra_linear_wgrad(const void *x, int64_t ld_x, const int8_t *z_q, const 
         for (int i = 0; i < (from_kept ? 6 : 4); ++i)
             if (mats_overlap(wm, *all[i])) return RA_ERR_OVERLAP;
     }
-    if (from_kept && !a.empty()) {
-        const ra_status st = ra_checkpoint8_unpack(z_q, z_e, m, k, act, const_cast<void *>(a.data), a.ld, RA_BF16, stream);
-        if (st != RA_OK) return st;
-    }
-    cudaError_t e = from_kept ? cudaSuccess : lay_out(mx, a, s);
-    if (e == cudaSuccess) e = lay_out(md, b, s);
+    const PackParams kept8{nullptr, const_cast<void *>(a.data), a.ld, const_cast<int8_t *>(z_q), const_cast<uint8_t *>(z_e), m, k, ceil_div<int64_t>(k, kGroup), act};
+    const Layout lay_a = !from_kept ? layout_of(mx, a) : a.empty() ? Layout{} : layout_of(kept8);
+    cudaError_t e = launch_layouts(Layouts{lay_a, layout_of(md, b)}, s);
     if (e != cudaSuccess) return cuda_status(e);
     if (db && m > kColumnRows) {
         e = launch_column_sum(b, accumulate, db, s);
