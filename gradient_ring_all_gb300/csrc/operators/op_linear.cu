@@ -25,7 +25,9 @@ enum Mode { kForward = 0, kDgrad = 1, kWgrad = 2 };
 
 // How blocks share tiles: one tile a block, one for a pair of blocks that work
 // as one tensor core, or one for a cluster that splits k.
-enum Kind { kSingle = 0, kPair = 1, kSplit = 2 };
+// kSkinny is kSplit for up to kSkinnyRows rows.
+enum Kind { kSingle = 0, kPair = 1, kSplit = 2, kSkinny = 3 };
+constexpr int kSkinnyRows = 16;
 
 // ---------------------------------------------------------------------------
 // epilogue
@@ -38,59 +40,76 @@ struct Epilogue {
     uint8_t *e;
     int64_t ldo, ldr, groups;
     int out_f32, bias_f32, res_f32, act;
-    int vec;     // bias, the rows of out and res, and q start on 32-byte boundaries
+    int rows_aligned, bias_aligned, q_aligned;  // rows of out and res, bias, q: on 32-byte boundaries
 };
 
-// v += the 32 values at p[0..32) (those below count, where not all are there)
-__device__ __forceinline__ void add32(const void *base, int64_t at, int f32, bool full, int count, float (&v)[32]) {
-    if (f32) {
-        const float *p = static_cast<const float *>(base) + at;
-        if (full) {
+// v += the 32 values from p on
+template <bool F32>
+__device__ __forceinline__ void add32(const void *p, float (&v)[32]) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                uint32_t w[8];
-                load_sector(p + 8 * g, w);
+    for (int g = 0; g < (F32 ? 4 : 2); ++g) {
+        uint32_t w[8];
+        load_sector(static_cast<const char *>(p) + 32 * g, w);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[8 * g + k] += __uint_as_float(w[k]);
+        for (int k = 0; k < 8; ++k) {
+            if constexpr (F32) {
+                v[8 * g + k] += __uint_as_float(w[k]);
+            } else {
+                v[16 * g + 2 * k] += __uint_as_float(w[k] << 16);
+                v[16 * g + 2 * k + 1] += __uint_as_float(w[k] & 0xffff0000u);
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (j < count) v[j] += p[j];
-        }
-    } else {
-        const uint16_t *p = static_cast<const uint16_t *>(base) + at;
-        if (full) {
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                uint32_t w[8];
-                load_sector(p + 16 * g, w);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    v[16 * g + 2 * k] += __uint_as_float(w[k] << 16);
-                    v[16 * g + 2 * k + 1] += __uint_as_float(w[k] & 0xffff0000u);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (j < count) v[j] += bf16_bits_to_f32(p[j]);
         }
     }
 }
 
-// 32 neighbouring columns of one output row, from column n0 (a multiple of
-// 32, so one checkpoint group) on; `count` of them exist.  The sums of columns
-// that do not exist are not looked at: they are zero, or NaN where A's row
-// holds an infinity.
+// 32 values of 32 lanes, crosswise: lane l's v[k] becomes lane k's v[l]
+__device__ __forceinline__ void transpose32(float (&v)[32], int lane) {
+#pragma unroll
+    for (int s = 16; s > 0; s /= 2) {
+        const bool high = lane & s;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (j & s) continue;
+            const float got = __shfl_xor_sync(0xffffffffu, high ? v[j] : v[j + s], s);
+            if (high)
+                v[j] = got;
+            else
+                v[j + s] = got;
+        }
+    }
+}
+
+__device__ __forceinline__ float load_any(const void *p, int64_t i, int f32) {
+    return f32 ? static_cast<const float *>(p)[i] : bf16_bits_to_f32(static_cast<const uint16_t *>(p)[i]);
+}
+
+// A warp finishes 32 neighbouring columns of 32 output rows, from column n0 (a
+// multiple of 32, so one checkpoint group) and row row0 on, a row a lane;
+// `count` columns and `rows` rows of them exist.  The sums of columns that do
+// not exist are not looked at: they are zero, or NaN where A's row holds an
+// infinity.  Each lane reads and writes its row by whole sectors; rows that
+// start elsewhere, and the last columns, are taken crosswise, so that the lanes
+// of an access are neighbours (one lane a row cost 568 x 3688 x 2440 20 of its 44 us).
 // Returns the group's step byte (forward, with a checkpoint), which the caller
 // stores with its neighbours'.
 template <int MODE>
-__device__ __forceinline__ uint32_t finish32(const Epilogue &ep, int64_t row, int64_t n0, int count, float (&v)[32]) {
+__device__ __forceinline__ uint32_t finish32(const Epilogue &ep, int64_t row0, int rows, int64_t n0, int count, float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+    const int64_t row = row0 + lane;
     uint32_t step_byte = 0;
-    const bool full = count == 32 && ep.vec;
     if constexpr (MODE == kForward) {
-        if (ep.bias) add32(ep.bias, n0, ep.bias_f32, full, count, v);
+        if (ep.bias) {
+            if (count == 32 && ep.bias_aligned) {
+                if (ep.bias_f32)
+                    add32<true>(static_cast<const float *>(ep.bias) + n0, v);
+                else
+                    add32<false>(static_cast<const uint16_t *>(ep.bias) + n0, v);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (j < count) v[j] += load_any(ep.bias, n0 + j, ep.bias_f32);
+            }
+        }
         if (ep.q) {
             uint32_t top = 0;
 #pragma unroll
@@ -99,16 +118,17 @@ __device__ __forceinline__ uint32_t finish32(const Epilogue &ep, int64_t row, in
 #pragma unroll
             for (int j = 0; j < 32; j += 2) top = top_of(top, v[j], v[j + 1]);
             const Step step = step_of(top);
-            const int64_t u = row * ep.groups + n0 / kGroup;
             uint32_t w[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) w[k] = quantise4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3], step);
-            if (ep.vec) {
-                store_sector(ep.q + u * kGroup, w);
-            } else {
-                uint4 *q = reinterpret_cast<uint4 *>(ep.q + u * kGroup);
-                q[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            if (lane < rows) {
+                int8_t *q = ep.q + (row * ep.groups + n0 / kGroup) * kGroup;
+                if (ep.q_aligned) {
+                    store_sector(q, w);
+                } else {
+                    reinterpret_cast<uint4 *>(q)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                    reinterpret_cast<uint4 *>(q)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                }
             }
             step_byte = step.e;
         }
@@ -118,11 +138,11 @@ __device__ __forceinline__ uint32_t finish32(const Epilogue &ep, int64_t row, in
         });
     }
     if constexpr (MODE == kDgrad) {
-        if (ep.q) {
+        if (ep.q && lane < rows) {
             const int64_t u = row * ep.groups + n0 / kGroup;
             const float step = step_value(ep.e[u]);
             uint32_t w[8];
-            if (ep.vec) {
+            if (ep.q_aligned) {
                 load_sector(ep.q + u * kGroup, w);
             } else {
 #pragma unroll
@@ -134,38 +154,53 @@ __device__ __forceinline__ uint32_t finish32(const Epilogue &ep, int64_t row, in
             });
         }
     }
-    if (ep.res) add32(ep.res, row * ep.ldr + n0, ep.res_f32, full, count, v);
-    if (ep.out_f32) {
-        float *p = static_cast<float *>(ep.out) + row * ep.ldo + n0;
-        if (full) {
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                uint32_t w[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[8 * g + k]);
-                store_sector(p + 8 * g, w);
+    if (count == 32 && ep.rows_aligned) {
+        if (lane < rows) {
+            if (ep.res) {
+                if (ep.res_f32)
+                    add32<true>(static_cast<const float *>(ep.res) + row * ep.ldr + n0, v);
+                else
+                    add32<false>(static_cast<const uint16_t *>(ep.res) + row * ep.ldr + n0, v);
             }
-        } else {
+            char *p = static_cast<char *>(ep.out) + (row * ep.ldo + n0) * (ep.out_f32 ? 4 : 2);
+            uint32_t w[8];
+            if (ep.out_f32) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (j < count) p[j] = v[j];
+                for (int g = 0; g < 4; ++g) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[8 * g + k]);
+                    store_sector(p + 32 * g, w);
+                }
+            } else {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) w[k] = pack2(v[16 * g + 2 * k], v[16 * g + 2 * k + 1]);
+                    store_sector(p + 32 * g, w);
+                }
+            }
         }
-    } else {
-        uint16_t *p = static_cast<uint16_t *>(ep.out) + row * ep.ldo + n0;
-        if (full) {
+        __syncwarp();
+        return step_byte;
+    }
+    transpose32(v, lane);  // v[i]: row row0 + i, column n0 + lane
+    if (lane < count) {
+        if (ep.res) {
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                uint32_t w[8];
+            for (int i = 0; i < 32; ++i)
+                if (i < rows) v[i] += load_any(ep.res, (row0 + i) * ep.ldr + n0 + lane, ep.res_f32);
+        }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) w[k] = pack2(v[16 * g + 2 * k], v[16 * g + 2 * k + 1]);
-                store_sector(p + 16 * g, w);
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (j < count) p[j] = (uint16_t)f32_to_bf16_bits(v[j]);
+        for (int i = 0; i < 32; ++i) {
+            if (i >= rows) break;
+            const int64_t at = (row0 + i) * ep.ldo + n0 + lane;
+            if (ep.out_f32)
+                static_cast<float *>(ep.out)[at] = v[i];
+            else
+                static_cast<uint16_t *>(ep.out)[at] = (uint16_t)f32_to_bf16_bits(v[i]);
         }
     }
+    __syncwarp();
     return step_byte;
 }
 
@@ -349,18 +384,22 @@ constexpr int kGroupM = 8;  // row tiles that share the columns' tiles in L2
 // holds its own rows of A and half of B's columns, which the two share.
 template <int BN, int KIND>
 struct Shape {
-    static constexpr bool kIsPair = KIND == kPair, kIsSplit = KIND == kSplit;
+    static constexpr bool kIsPair = KIND == kPair, kIsSplit = KIND == kSplit || KIND == kSkinny;
+    // Rows of A that are loaded.  For a few rows, only those: the tensor core
+    // reads 128 all the same, whatever lies there, into sums that nothing uses.
+    static constexpr int kARows = KIND == kSkinny ? kSkinnyRows : kBM;
     static constexpr int kBlocks = kIsPair ? 2 : 1, kRows = kBM * kBlocks, kBCols = BN / kBlocks;
-    static constexpr int kABytes = kBM * kBK * 2, kBBytes = kBCols * kBK * 2;
+    static constexpr int kABytes = kARows * kBK * 2, kBBytes = kBCols * kBK * 2;
     static constexpr int kStageBytes = kABytes + kBBytes;
     // all of an SM's shared memory, or half of it where two blocks share an SM
-    static constexpr int kStages = kIsSplit ? 4 : kStageBytes > 24576 ? 7 : 8;
+    static constexpr int kStages = KIND == kSkinny ? 9 : kIsSplit ? 4 : kStageBytes > 24576 ? 7 : 8;
     static constexpr int kBlocksPerSm = kIsSplit ? 2 : 1;
     // epilogue warps: four take the tile's 128 rows, and every further four share its columns
     static constexpr int kWarps = BN >= 128 ? 16 : 8, kCols = BN / (kWarps / 4), kThreads = (kWarps + 2) * 32;
     static constexpr int kTmemCols = 2 * BN;  // two tiles' sums: one is finished while the next is made
     static constexpr int kColumnBytes = 2 * kBCols * 4;  // column sums of the two halves of dy's rows
-    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024 + 256 + kColumnBytes;
+    // (the last stage of a skinny tile is read past its end)
+    static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024 + 256 + kColumnBytes + (kBM - kARows) * kBK * 2;
     static_assert(kSmem <= kMaxDynamicSmem && kWarps == kBCols / 16 * 2, "shared memory, warps for the column sums");
 };
 
@@ -595,7 +634,8 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
         for (int tile = tile0; tile < tile_count && ok; tile += tile_step) {
             int tm, tn;
             tile_at(p, tile, &tm, &tn);
-            const int64_t row = (int64_t)tm * S::kRows + rank * kBM + warp % 4 * 32 + lane;
+            const int64_t row0 = (int64_t)tm * S::kRows + rank * kBM + warp % 4 * 32, row = row0 + lane;
+            const int rows = p.rows - row0 < 32 ? (int)(p.rows - row0) : 32;  // of the warp's 32 (none where not above 0)
             const int64_t c0 = (int64_t)tn * BN + warp / 4 * S::kCols;
             if (MODE == kWgrad && p.db && tm == 0 && part == 0)
                 column_sums<S>(p, (int64_t)tn * BN + rank * S::kBCols, reinterpret_cast<float *>(smem + S::kStages * S::kStageBytes + 256), warp, lane);
@@ -631,7 +671,8 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
 #pragma unroll
                 for (int g = 0; g < S::kCols / 32; ++g) {
                     const int64_t n0 = c0 + g * 32;
-                    if (row < p.rows && n0 < p.cols) step_bytes |= finish32<MODE>(p.ep, row, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), sum[g]) << (8 * g);
+                    if (rows > 0 && n0 < p.cols)
+                        step_bytes |= finish32<MODE>(p.ep, row0, rows, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), sum[g]) << (8 * g);
                 }
                 if (MODE == kForward && !S::kIsSplit && p.ep.q && row < p.rows && c0 < p.cols) store_steps<S::kCols>(p.ep, row, c0, step_bytes);
                 __syncwarp();
@@ -654,8 +695,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                         keep_sums(smem, warp / 4 * S::kCols + g * 32, warp % 4 * 32 + lane, v);
                         continue;
                     }
-                    if (row < p.rows) step_bytes |= finish32<MODE>(p.ep, row, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v) << (8 * g);
-                    __syncwarp();
+                    if (rows > 0) step_bytes |= finish32<MODE>(p.ep, row0, rows, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v) << (8 * g);
                 }
                 if (MODE == kForward && !S::kIsSplit && p.ep.q && row < p.rows && c0 < p.cols) store_steps<S::kCols>(p.ep, row, c0, step_bytes);
                 release<PAIR>(freed_bar + 8 * acc, lane);
@@ -669,15 +709,19 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
         // every block's sums lie in its shared memory: each block adds and
         // finishes its share of the rows, the splits in their order
         cluster_sync();
-        const int height = kBM / p.splits, at = threadIdx.x % height, g = threadIdx.x / height;
+        const int height = kBM / p.splits, per_group = height > 32 ? height / 32 : 1;  // warps a column group
+        const int g = warp / per_group, at0 = warp % per_group * 32;
         int tm, tn;
         tile_at(p, tile0, &tm, &tn);
-        const int in_tile = part * height + at;
-        const int64_t row = (int64_t)tm * kBM + in_tile, n0 = (int64_t)tn * BN + g * 32;
-        if (ok && g < BN / 32 && row < p.rows && n0 < p.cols) {
+        const int in_tile = part * height + at0;
+        const int64_t row0 = (int64_t)tm * kBM + in_tile, n0 = (int64_t)tn * BN + g * 32;
+        int rows = height < 32 ? height : 32;
+        if (p.rows - row0 < rows) rows = (int)(p.rows - row0);
+        if (ok && g < BN / 32 && rows > 0 && n0 < p.cols) {
             float v[32];
+            // (lanes past the block's rows read its neighbours' and drop them)
             for (int q = 0; q < p.splits; ++q) {
-                const uint32_t from = in_block(tiles + (g * 32 * kBM + in_tile) * 4, q);
+                const uint32_t from = in_block(tiles + (g * 32 * kBM + (in_tile + lane) % kBM) * 4, q);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
                     float x;
@@ -685,8 +729,8 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                     v[j] = q ? v[j] + x : x;
                 }
             }
-            const uint32_t step_byte = finish32<MODE>(p.ep, row, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
-            if (MODE == kForward && p.ep.q) store_steps<32>(p.ep, row, n0, step_byte);
+            const uint32_t step_byte = finish32<MODE>(p.ep, row0, rows, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
+            if (MODE == kForward && p.ep.q && lane < rows) store_steps<32>(p.ep, row0 + lane, n0, step_byte);
         }
         __syncwarp();
     }
@@ -947,7 +991,7 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     p.splits = splits;
     cudaError_t e = cudaSuccess;
     if (p.steps > 0) {
-        e = tensor_map(&p.a, a, MODE == kWgrad ? kBK : kBM);
+        e = tensor_map(&p.a, a, MODE == kWgrad ? kBK : S::kARows);
         if (e == cudaSuccess) e = tensor_map(&p.b, b, MODE == kDgrad ? S::kBCols : kBK);
         if (e != cudaSuccess) return e;
     }
@@ -982,6 +1026,8 @@ cudaError_t launch_width(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     const int64_t tm = ceil_div<int64_t>(p.rows, kBM), narrow = tm * ceil_div<int64_t>(p.cols, 64);
     int splits = 1;
     while (splits < 8 && narrow * splits <= sms && p.steps >= 8 * splits) splits *= 2;
+    if constexpr (MODE != kWgrad)
+        if (splits > 1 && p.rows <= kSkinnyRows) return launch_tiles<MODE, 64, kSkinny, F32>(p, a, b, sms, s, splits);
     if (splits > 1) return launch_tiles<MODE, 64, kSplit, F32>(p, a, b, sms, s, splits);
     if (tm * ceil_div<int64_t>(p.cols, 128) <= sms / 2) return launch_tiles<MODE, 64, kSingle, F32>(p, a, b, sms, s);
     if (tm * ceil_div<int64_t>(p.cols, 256) <= sms / 2) return launch_tiles<MODE, 128, kSingle, F32>(p, a, b, sms, s);
@@ -994,7 +1040,9 @@ cudaError_t launch_product(const Mat &a, const Mat &b, int64_t rows, int64_t col
                            cudaStream_t s, float *db = nullptr, int db_add = 0) {
     Product p = {};
     p.ep = ep;
-    p.ep.vec = out.aligned(32) && (bias.empty() || bias.aligned(32)) && (res.empty() || res.aligned(32)) && reinterpret_cast<uintptr_t>(ep.q) % 32 == 0;
+    p.ep.rows_aligned = out.aligned(32) && (res.empty() || res.aligned(32));
+    p.ep.bias_aligned = bias.aligned(32);
+    p.ep.q_aligned = reinterpret_cast<uintptr_t>(ep.q) % 32 == 0;
     p.rows = rows;
     p.cols = cols;
     p.steps = rows > 0 ? (int)ceil_div<int64_t>(k, kBK) : 0;
