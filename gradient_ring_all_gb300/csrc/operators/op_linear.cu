@@ -1018,16 +1018,26 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
 }
 
 // The tile: the widest that leaves half of the SMs or more one; the widest is
-// a pair's.  Where even the narrowest tiles leave SMs idle and k is long
-// enough, clusters of 2 to 8 blocks split it, two blocks an SM, so long as each
-// keeps 4 steps.
+// a pair's.  Where even the narrowest tiles leave half of the SMs idle and k is
+// long enough, clusters of 2 to 8 blocks split it: the exchange of the sums
+// costs about what 8 steps do.  With one row tile, where the weights' stream is
+// what counts, up to two blocks an SM.  Split / whole, us (GB300, graph replay):
+// 256 x 1024 x 1024 6.8 / 7.4, 512 x 2048 x 512 8.7 / 11.8, 128 x 4096 x 4096
+// 11.9 / 20.9, 16 x 2448 x 160 7.3 / 13.2; but 512 x 512 x 2048 7.0 / 5.3 with
+// only 4 steps each, and 300 x 3000 x 3000 20.2 / 18.3 with two blocks an SM.
 template <int MODE, bool F32>
 cudaError_t launch_width(Product &p, const Mat &a, const Mat &b, int sms, cudaStream_t s) {
     const int64_t tm = ceil_div<int64_t>(p.rows, kBM), narrow = tm * ceil_div<int64_t>(p.cols, 64);
+    const bool skinny = MODE != kWgrad && p.rows <= kSkinnyRows;
     int splits = 1;
-    while (splits < 8 && narrow * splits <= sms && p.steps >= 8 * splits) splits *= 2;
+    while (splits < 8) {
+        const bool one_each = narrow * splits * 2 <= sms && p.steps >= 16 * splits;
+        const bool two_each = tm == 1 && narrow * splits <= sms && p.steps >= (skinny ? 8 : 32) * splits;
+        if (!one_each && !two_each) break;
+        splits *= 2;
+    }
     if constexpr (MODE != kWgrad)
-        if (splits > 1 && p.rows <= kSkinnyRows) return launch_tiles<MODE, 64, kSkinny, F32>(p, a, b, sms, s, splits);
+        if (splits > 1 && skinny) return launch_tiles<MODE, 64, kSkinny, F32>(p, a, b, sms, s, splits);
     if (splits > 1) return launch_tiles<MODE, 64, kSplit, F32>(p, a, b, sms, s, splits);
     if (tm * ceil_div<int64_t>(p.cols, 128) <= sms / 2) return launch_tiles<MODE, 64, kSingle, F32>(p, a, b, sms, s);
     if (tm * ceil_div<int64_t>(p.cols, 256) <= sms / 2) return launch_tiles<MODE, 128, kSingle, F32>(p, a, b, sms, s);
