@@ -8,44 +8,40 @@ namespace {
 
 constexpr int kThreadsCkpt = 256;
 
-// Rows on 16-byte boundaries: a thread takes half a group, 16 values, with
-// 16-byte loads and stores; two neighbouring lanes settle the group's step.
+// Rows and q on 32-byte boundaries: a thread takes a group, by whole sectors.
 // Bound by memory: x once in (2 or 4 bytes a value), 33/32 byte out.
 template <class T>
 __global__ void __launch_bounds__(kThreadsCkpt) pack_kernel(const PackParams p) {
     pdl_enter();
-    const int64_t halves = 2 * p.groups, total = p.rows * halves;
-    const int64_t stride = (int64_t)gridDim.x * kThreadsCkpt;
-    // both lanes of a pair run or neither: `total` is even
+    const int64_t total = p.rows * p.groups, stride = (int64_t)gridDim.x * kThreadsCkpt;
     for (int64_t u = (int64_t)blockIdx.x * kThreadsCkpt + threadIdx.x; u < total; u += stride) {
         int64_t r, k;
-        row_of(u, halves, total, &r, &k);
-        const T *src = static_cast<const T *>(p.x) + r * p.ld + k * 16;
-        const int64_t left = p.cols - k * 16;
-        float x[16];
-        if (left >= 16) {
-            load_w<T, 16>(src, x);
+        row_of(u, p.groups, total, &r, &k);
+        const T *src = static_cast<const T *>(p.x) + r * p.ld + k * kGroup;
+        const int64_t left = p.cols - k * kGroup;
+        float x[kGroup];
+        if (left >= kGroup) {
+            load_group(src, x);
         } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = j < left ? to_f32<T>(src[j]) : 0.0f;
+            for (int j = 0; j < kGroup; ++j) x[j] = j < left ? to_f32<T>(src[j]) : 0.0f;
         }
         uint32_t top = 0;
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) top = top_of(top, x[j], x[j + 1]);
-        const uint32_t pair = 3u << (threadIdx.x & 30);
-        const Step step = step_of(max(top, __shfl_xor_sync(pair, top, 1)));
-        uint32_t w[4];
+        for (int j = 0; j < kGroup; j += 2) top = top_of(top, x[j], x[j + 1]);
+        const Step step = step_of(top);
+        uint32_t w[8];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) w[g] = quantise4(x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3], step);
-        reinterpret_cast<uint4 *>(p.q)[u] = make_uint4(w[0], w[1], w[2], w[3]);
-        if ((u & 1) == 0) p.e[u / 2] = (uint8_t)step.e;
+        for (int g = 0; g < 8; ++g) w[g] = quantise4(x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3], step);
+        store_sector(p.q + u * kGroup, w);
+        p.e[u] = (uint8_t)step.e;
     }
 }
 
 template <class T>
 __global__ void __launch_bounds__(kThreadsCkpt) unpack_kernel(const PackParams p) {
     pdl_enter();
-    unpack_halves<T>(p, (int64_t)blockIdx.x * kThreadsCkpt + threadIdx.x, (int64_t)gridDim.x * kThreadsCkpt);
+    unpack_groups<T>(p, (int64_t)blockIdx.x * kThreadsCkpt + threadIdx.x, (int64_t)gridDim.x * kThreadsCkpt);
 }
 
 // Byte j of the result is byte (lane mod 4) of lane j's word, of the four
@@ -103,21 +99,25 @@ __global__ void __launch_bounds__(kThreadsCkpt) unpack_scalar_kernel(const PackP
         const bool in = k * 4 + (lane & 3) < p.groups;
         const uint32_t e = in ? p.e[first + (lane & 3)] : 1;
         uint32_t w = in ? reinterpret_cast<const uint32_t *>(p.q + (first + (lane & 3)) * kGroup)[lane / 4] : 0;
-        w = transpose4(w, lane);  // the lane's value of each of the four groups
+        w = offset_bytes(transpose4(w, lane));  // the lane's value of each of the four groups
         T *dst = static_cast<T *>(p.out) + r * p.ld;
+        float v[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            float v = dequantise(w, g, step_value(__shfl_sync(0xffffffffu, e, g)));
-            with_act(p.act, [&](auto a) { v = act_value<decltype(a)::value>(v); });
+            v[g] = dequantise(w, g, step_value(__shfl_sync(0xffffffffu, e, g)));
+        }
+        with_act(p.act, [&](auto a) { act_all<decltype(a)::value>(v); });
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
             const int64_t c = (k * 4 + g) * kGroup + lane;
-            if (c < p.cols) dst[c] = from_f32<T>(v);
+            if (c < p.cols) dst[c] = from_f32<T>(v[g]);
         }
     }
 }
 
 template <class T>
 ra_status launch_ckpt(bool pack, bool wide, const PackParams &p, cudaStream_t s) {
-    const int64_t blocks = wide ? ceil_div<int64_t>(p.rows * p.groups * 2, kThreadsCkpt)
+    const int64_t blocks = wide ? ceil_div<int64_t>(p.rows * p.groups, kThreadsCkpt)
                                 : ceil_div<int64_t>(p.rows * ceil_div<int64_t>(p.groups, 4), kThreadsCkpt / 32);
     const int64_t grid = blocks < kMaxGrid ? blocks : kMaxGrid;
     return cuda_status(wide ? launch_pdl(pack ? pack_kernel<T> : unpack_kernel<T>, grid, kThreadsCkpt, 0, s, p)
@@ -137,7 +137,8 @@ ra_status run_ckpt(bool pack, const void *x, int64_t ld, int dtype, int64_t rows
     if (mats_overlap(a, mq) || mats_overlap(a, me) || mats_overlap(mq, me)) return RA_ERR_OVERLAP;
     const PackParams p{x, const_cast<void *>(x), ld, q, e, rows, cols, groups, act};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return dtype == RA_F32 ? launch_ckpt<float>(pack, a.aligned(16), p, s) : launch_ckpt<uint16_t>(pack, a.aligned(16), p, s);
+    const bool wide = a.aligned(32) && reinterpret_cast<uintptr_t>(q) % 32 == 0;
+    return dtype == RA_F32 ? launch_ckpt<float>(pack, wide, p, s) : launch_ckpt<uint16_t>(pack, wide, p, s);
 }
 
 }  // namespace

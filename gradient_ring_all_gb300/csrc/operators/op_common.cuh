@@ -210,48 +210,91 @@ __device__ __forceinline__ float fast_exp2(float x) {
 }
 __device__ __forceinline__ float logistic(float z) { return fast_rcp(1.0f + fast_exp2(z * -1.4426950408889634f)); }
 
-// The normal distribution function, and through *bell exp(-z^2 / 2).  The tail
-// 1 - cdf(|z|) is half of Abramowitz and Stegun's 7.1.26 for erfc(|z| / sqrt 2):
-// a polynomial in 1 / (1 + c |z|) times the exponential, within 0.75e-7, in
-// 12 instructions without a branch.  (erff takes two paths that most warps
-// both walk: 8192 x 8192 restored through gelu took 73 us with it.)
-__device__ __forceinline__ float gauss_cdf(float z, float *bell) {
-    const float a = fabsf(z);
-    const float e = fast_exp2(z * z * -0.72134752044448170f);
-    const float t = fast_rcp(fmaf(a, 0.3275911f * 0.70710678118654752f, 1.0f));
-    float s = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
-    s = fmaf(t, s, 0.5f * 1.421413741f);
-    s = fmaf(t, s, 0.5f * -0.284496736f);
-    s = fmaf(t, s, 0.5f * 0.254829592f);
-    const float tail = s * t * e;
+// Two binary32 values in one register pair, and arithmetic on both at once
+// (each rounded to nearest, as the scalar instructions round).
+struct Two {
+    uint64_t v;
+    __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ explicit Two(float a) : Two(a, a) {}
+    __device__ __forceinline__ void get(float *a, float *b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v)); }
+};
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+    return a;
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+    return a;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a.v) : "l"(b.v), "l"(c.v));
+    return a;
+}
+
+// The normal distribution function of two values, and through *bell
+// exp(-z^2 / 2).  The tail 1 - cdf(|z|) is half of Abramowitz and Stegun's
+// 7.1.26 for erfc(|z| / sqrt 2): a polynomial in 1 / (1 + c |z|) times the
+// exponential, within 0.75e-7, without a branch.  In pairs it takes 10
+// instructions a value.  (erff takes two paths that most warps both walk: 8192 x
+// 8192 restored through gelu took 73 us with it.)
+__device__ __forceinline__ void gauss_cdf(float z0, float z1, float *cdf0, float *cdf1, Two *bell) {
+    const Two z(z0, z1), x = z * z * Two(-0.72134752044448170f);
+    float e0, e1;
+    x.get(&e0, &e1);
+    const Two e(fast_exp2(e0), fast_exp2(e1));
+    constexpr float c = 0.3275911f * 0.70710678118654752f;
+    const Two t(fast_rcp(fmaf(fabsf(z0), c, 1.0f)), fast_rcp(fmaf(fabsf(z1), c, 1.0f)));
+    Two s = fma2(t, Two(0.5f * 1.061405429f), Two(0.5f * -1.453152027f));
+    s = fma2(t, s, Two(0.5f * 1.421413741f));
+    s = fma2(t, s, Two(0.5f * -0.284496736f));
+    s = fma2(t, s, Two(0.5f * 0.254829592f));
+    float tail0, tail1;
+    (s * t * e).get(&tail0, &tail1);
+    *cdf0 = z0 > 0.0f ? 1.0f - tail0 : tail0;
+    *cdf1 = z1 > 0.0f ? 1.0f - tail1 : tail1;
     *bell = e;
-    return z > 0.0f ? 1.0f - tail : tail;
 }
 
 template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-    if constexpr (ACT == RA_ACT_RELU) return z < 0.0f ? 0.0f : z;  // a NaN stays one
-    if constexpr (ACT == RA_ACT_GELU) {
-        float bell;
-        return z * gauss_cdf(z, &bell);
+__device__ __forceinline__ void act_values(float &z0, float &z1) {
+    if constexpr (ACT == RA_ACT_RELU) {  // a NaN stays one
+        z0 = z0 < 0.0f ? 0.0f : z0;
+        z1 = z1 < 0.0f ? 0.0f : z1;
+    } else if constexpr (ACT == RA_ACT_GELU) {
+        float c0, c1;
+        Two bell(0.0f);
+        gauss_cdf(z0, z1, &c0, &c1, &bell);
+        z0 *= c0;
+        z1 *= c1;
+    } else if constexpr (ACT == RA_ACT_SILU) {
+        z0 *= logistic(z0);
+        z1 *= logistic(z1);
     }
-    if constexpr (ACT == RA_ACT_SILU) return z * logistic(z);
-    return z;
 }
 
+// v *= act'(z)
 template <int ACT>
-__device__ __forceinline__ float act_slope(float z) {
-    if constexpr (ACT == RA_ACT_RELU) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
-    if constexpr (ACT == RA_ACT_GELU) {
-        float bell;
-        const float cdf = gauss_cdf(z, &bell);
-        return fmaf(z * 0.3989422804014327f, bell, cdf);
+__device__ __forceinline__ void times_slopes(float &v0, float &v1, float z0, float z1) {
+    if constexpr (ACT == RA_ACT_RELU) {
+        v0 *= z0 > 0.0f ? 1.0f : (z0 <= 0.0f ? 0.0f : z0);
+        v1 *= z1 > 0.0f ? 1.0f : (z1 <= 0.0f ? 0.0f : z1);
+    } else if constexpr (ACT == RA_ACT_GELU) {
+        float c0, c1;
+        Two bell(0.0f);
+        gauss_cdf(z0, z1, &c0, &c1, &bell);
+        (Two(v0, v1) * fma2(Two(z0, z1) * Two(0.3989422804014327f), bell, Two(c0, c1))).get(&v0, &v1);
+    } else if constexpr (ACT == RA_ACT_SILU) {
+        const float p0 = logistic(z0), p1 = logistic(z1);
+        v0 *= p0 * fmaf(z0, 1.0f - p0, 1.0f);
+        v1 *= p1 * fmaf(z1, 1.0f - p1, 1.0f);
     }
-    if constexpr (ACT == RA_ACT_SILU) {
-        const float p = logistic(z);
-        return p * fmaf(z, 1.0f - p, 1.0f);
-    }
-    return 1.0f;
+}
+
+// every value of an array of pairs
+template <int ACT, int N>
+__device__ __forceinline__ void act_all(float (&v)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; j += 2) act_values<ACT>(v[j], v[j + 1]);
 }
 
 // f(Const<ACT>) for a runtime activation
@@ -320,13 +363,23 @@ __device__ __forceinline__ uint32_t quantise4(float a, float b, float c, float d
     const uint32_t cd = __byte_perm(steps_bits(c, s.inverse), steps_bits(d, s.inverse), 0x0040);
     return s.e == kStepNan ? 0u : __byte_perm(ab, cd, 0x5410);
 }
-__device__ __forceinline__ float dequantise(uint32_t word, int k, float step) {
-    return (float)(int)(int8_t)(word >> (8 * k)) * step;
+// A word of four: each byte, offset by 128, as the low bits of 2^23, less
+// 2^23 + 128.  (An integer conversion shares the slow unit with the activations'
+// exponentials and reciprocals.)
+__device__ __forceinline__ uint32_t offset_bytes(uint32_t word) { return word ^ 0x80808080u; }
+__device__ __forceinline__ float offset_float(uint32_t offset_word, int k) {
+    return __uint_as_float(__byte_perm(offset_word, 0x4b000000u, 0x7650 + k));
 }
+__device__ __forceinline__ void dequantise4(uint32_t word, float step, float *v) {
+    const uint32_t w = offset_bytes(word);
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) ((Two(offset_float(w, k), offset_float(w, k + 1)) + Two(-8388736.0f)) * Two(step)).get(v + k, v + k + 1);
+}
+__device__ __forceinline__ float dequantise(uint32_t offset_word, int k, float step) { return (offset_float(offset_word, k) - 8388736.0f) * step; }
 
 struct PackParams {
     const void *x;  // pack: the activation
-    void *out;      // unpack: the restored activation, its rows on 16-byte boundaries
+    void *out;      // unpack: the restored activation
     int64_t ld;     // elements between the rows of x or out
     int8_t *q;
     uint8_t *e;
@@ -348,31 +401,64 @@ __device__ __forceinline__ void row_of(int64_t u, int64_t per_row, int64_t total
     }
 }
 
-// Threads `first`, `first` + `stride`, .. restore half groups (16 values) to
-// rows on 16-byte boundaries.
+// 32 neighbouring values of either type, by whole sectors (p on a 32-byte boundary)
 template <class T>
-__device__ __forceinline__ void unpack_halves(const PackParams &p, int64_t first, int64_t stride) {
-    const int64_t halves = 2 * p.groups, total = p.rows * halves;
+__device__ __forceinline__ void load_group(const T *p, float (&x)[kGroup]) {
+    constexpr int kEach = 32 / sizeof(T);
+#pragma unroll
+    for (int g = 0; g < kGroup / kEach; ++g) {
+        uint32_t w[8];
+        load_sector(p + g * kEach, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if constexpr (sizeof(T) == 4) {
+                x[g * 8 + k] = __uint_as_float(w[k]);
+            } else {
+                x[g * 16 + 2 * k] = __uint_as_float(w[k] << 16);
+                x[g * 16 + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+            }
+        }
+    }
+}
+template <class T>
+__device__ __forceinline__ void store_group(T *p, const float (&x)[kGroup]) {
+    constexpr int kEach = 32 / sizeof(T);
+#pragma unroll
+    for (int g = 0; g < kGroup / kEach; ++g) {
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if constexpr (sizeof(T) == 4)
+                w[k] = __float_as_uint(x[g * 8 + k]);
+            else
+                w[k] = pack2(x[g * 16 + 2 * k], x[g * 16 + 2 * k + 1]);
+        }
+        store_sector(p + g * kEach, w);
+    }
+}
+
+// Threads `first`, `first` + `stride`, .. restore a group each, to rows on
+// 32-byte boundaries.
+template <class T>
+__device__ __forceinline__ void unpack_groups(const PackParams &p, int64_t first, int64_t stride) {
+    const int64_t total = p.rows * p.groups;
     for (int64_t u = first; u < total; u += stride) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p.q) + u);
-        const float step = step_value(__ldg(p.e + u / 2));
+        const uint4 q0 = __ldg(reinterpret_cast<const uint4 *>(p.q + u * kGroup)), q1 = __ldg(reinterpret_cast<const uint4 *>(p.q + u * kGroup) + 1);
+        const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+        const float step = step_value(__ldg(p.e + u));
         int64_t r, k;
-        row_of(u, halves, total, &r, &k);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-        float v[16];
+        row_of(u, p.groups, total, &r, &k);
+        float v[kGroup];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = dequantise(w[j / 4], j % 4, step);
-        with_act(p.act, [&](auto a) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = act_value<decltype(a)::value>(v[j]);
-        });
-        T *dst = static_cast<T *>(p.out) + r * p.ld + k * 16;
-        const int64_t left = p.cols - k * 16;
-        if (left >= 16) {
-            store_w<T, 16>(dst, v);
+        for (int j = 0; j < 8; ++j) dequantise4(w[j], step, v + 4 * j);
+        with_act(p.act, [&](auto a) { act_all<decltype(a)::value>(v); });
+        T *dst = static_cast<T *>(p.out) + r * p.ld + k * kGroup;
+        const int64_t left = p.cols - k * kGroup;
+        if (left >= kGroup) {
+            store_group(dst, v);
         } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
+            for (int j = 0; j < kGroup; ++j)
                 if (j < left) dst[j] = from_f32<T>(v[j]);
         }
     }

@@ -132,10 +132,7 @@ __device__ __forceinline__ uint32_t finish32(const Epilogue &ep, int64_t row0, i
             }
             step_byte = step.e;
         }
-        with_act(ep.act, [&](auto a) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = act_value<decltype(a)::value>(v[j]);
-        });
+        with_act(ep.act, [&](auto a) { act_all<decltype(a)::value>(v); });
     }
     if constexpr (MODE == kDgrad) {
         if (ep.q && lane < rows) {
@@ -150,7 +147,12 @@ __device__ __forceinline__ uint32_t finish32(const Epilogue &ep, int64_t row0, i
             }
             with_act(ep.act, [&](auto a) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] *= act_slope<decltype(a)::value>(dequantise(w[j / 4], j % 4, step));
+                for (int k = 0; k < 8; ++k) {
+                    float z[4];
+                    dequantise4(w[k], step, z);
+                    times_slopes<decltype(a)::value>(v[4 * k], v[4 * k + 1], z[0], z[1]);
+                    times_slopes<decltype(a)::value>(v[4 * k + 2], v[4 * k + 3], z[2], z[3]);
+                }
             });
         }
     }
@@ -748,7 +750,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
 // ---------------------------------------------------------------------------
 // operands that TMA cannot read where they lie
 
-// An operand to bring into the workspace, as bf16 rows on 16-byte boundaries:
+// An operand to bring into the workspace, as bf16 rows on 32-byte boundaries:
 // a bf16 matrix of any stride, or an 8-bit checkpoint (through its activation).
 struct Layout {
     const uint16_t *x;  // null: the checkpoint
@@ -808,7 +810,7 @@ __global__ void __launch_bounds__(kLayoutThreads) layout_kernel(const Layouts p)
     if (l.x)
         lay_out(l, block);
     else
-        unpack_halves<uint16_t>(l.kept, block * kLayoutThreads + threadIdx.x, l.blocks * kLayoutThreads);
+        unpack_groups<uint16_t>(l.kept, block * kLayoutThreads + threadIdx.x, l.blocks * kLayoutThreads);
 }
 
 // Column sums of a bf16 matrix (the bias gradient) in a launch of their own,
@@ -895,15 +897,21 @@ cudaError_t tensor_map(CUtensorMap *map, const Mat &a, int box_rows) {
 
 bool tma_readable(const Mat &a) { return a.aligned(16) && (a.rows <= 1 || a.pitch() < ((int64_t)1 << 40)); }
 
-int64_t laid_out_bytes(int64_t rows, int64_t cols) { return ceil_div<int64_t>(rows * ceil_div<int64_t>(cols, 8) * 16, 256) * 256; }
+// rows of whole sectors (TMA asks for 16 bytes, restoring a checkpoint for 32)
+int64_t laid_out_ld(int64_t cols) { return ceil_div<int64_t>(cols, 16) * 16; }
+int64_t laid_out_bytes(int64_t rows, int64_t cols) { return ceil_div<int64_t>(rows * laid_out_ld(cols) * 2, 256) * 256; }
 
-// The caller's workspace, handed out front to back.
+// The caller's workspace, handed out front to back from its first 32-byte
+// boundary on.
+constexpr int64_t kWorkspaceSlack = 32;
 struct Workspace {
     char *at, *end;
     bool ok;
-    Workspace(void *ws, size_t bytes)
-        : at(static_cast<char *>(ws)), end(at + bytes), ok(ws == nullptr || reinterpret_cast<uintptr_t>(ws) % 16 == 0) {
-        if (ws == nullptr) end = at;
+    Workspace(void *ws, size_t bytes) : at(nullptr), end(nullptr), ok(ws == nullptr || reinterpret_cast<uintptr_t>(ws) % 16 == 0) {
+        if (ws == nullptr) return;
+        const uintptr_t skip = -reinterpret_cast<uintptr_t>(ws) & 31;
+        at = static_cast<char *>(ws) + (skip < bytes ? skip : bytes);
+        end = static_cast<char *>(ws) + bytes;
     }
     void *take(int64_t bytes) {
         if (!ok || bytes > end - at) return nullptr;
@@ -917,7 +925,7 @@ struct Workspace {
 bool place(const Mat &a, Workspace *ws, Mat *out) {
     *out = a;
     if (a.empty() || tma_readable(a)) return true;
-    out->ld = ceil_div<int64_t>(a.cols, 8) * 8;
+    out->ld = laid_out_ld(a.cols);
     out->data = ws->take(laid_out_bytes(a.rows, a.cols));
     return out->data != nullptr;
 }
@@ -934,7 +942,7 @@ Layout layout_of(const Mat &a, const Mat &placed) {
 Layout layout_of(const PackParams &kept) {
     Layout l = {};
     l.kept = kept;
-    const int64_t blocks = ceil_div<int64_t>(kept.rows * kept.groups * 2, kLayoutThreads);
+    const int64_t blocks = ceil_div<int64_t>(kept.rows * kept.groups, kLayoutThreads);
     l.blocks = blocks < kMaxGrid / 2 ? blocks : kMaxGrid / 2;
     return l;
 }
@@ -1096,7 +1104,7 @@ size_t ra_linear_workspace_bytes(int64_t m, int64_t k, int64_t n) {
     // at most two of the three matrices are laid out in one call
     const int64_t mk = laid_out_bytes(m, k), kn = laid_out_bytes(k, n), mn = laid_out_bytes(m, n);
     const int64_t least = mk < kn ? (mk < mn ? mk : mn) : (kn < mn ? kn : mn);
-    return (size_t)(mk + kn + mn - least);
+    return (size_t)(mk + kn + mn - least + kWorkspaceSlack);
 }
 
 ra_status ra_linear(const void *x, int64_t ld_x, const void *w, int64_t ld_w, int64_t m, int64_t k, int64_t n,
@@ -1192,7 +1200,7 @@ ra_status ra_linear_wgrad(const void *x, int64_t ld_x, const int8_t *z_q, const 
     Mat a, b;
     if (from_kept) {
         // the checkpoint's values (after the activation) as bf16 rows
-        a = Mat{nullptr, m, k, ceil_div<int64_t>(k, 8) * 8, 2};
+        a = Mat{nullptr, m, k, laid_out_ld(k), 2};
         if (!a.empty() && (a.data = space.take(laid_out_bytes(m, k))) == nullptr) return RA_ERR_INVALID_ARG;
     } else if (!place(mx, &space, &a)) {
         return RA_ERR_INVALID_ARG;
