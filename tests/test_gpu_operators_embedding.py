@@ -144,6 +144,17 @@ def test_grad_with_a_wide_vocabulary():
     check(ra.ra_embedding_grad(grad, ids, vocab), want, 2 * (n + 2) * U * size)
 
 
+@pytest.mark.parametrize("tokens", [16_384, 16_385, 131_072, 131_073, 300_001])
+def test_grad_by_number_of_tokens(tokens):
+    """One block's sort and the tiled one: the sums are exact here (small whole numbers)."""
+    for vocab in (200, 40_000):
+        ids = _ids("random", tokens, vocab, tokens)
+        ids[tokens // 3: tokens // 2] = 7
+        grad = torch.randint(-3, 4, (tokens, 5), generator=_gen(tokens), device="cuda").float()
+        want, _, _ = _grad64(grad, ids, vocab, 1.0)
+        assert torch.equal(ra.ra_embedding_grad(grad, ids, vocab).double(), want)
+
+
 def test_grad_of_no_tokens():
     ids = torch.empty(0, dtype=torch.int64, device="cuda")
     g = torch.empty(0, 8, device="cuda")
