@@ -83,6 +83,19 @@ __device__ __forceinline__ float load_any(const void *p, int64_t i, int f32) {
     return f32 ? static_cast<const float *>(p)[i] : bf16_bits_to_f32(static_cast<const uint16_t *>(p)[i]);
 }
 
+// v[i] += p[i * ld], i < rows; eight loads at a time (sixteen were no faster)
+template <class T>
+__device__ __forceinline__ void add_column(const T *p, int64_t ld, int rows, float (&v)[32]) {
+#pragma unroll
+    for (int i0 = 0; i0 < 32; i0 += 8) {
+        T x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = i0 + i < rows ? p[(i0 + i) * ld] : T(0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i0 + i] += to_f32<T>(x[i]);
+    }
+}
+
 // A warp finishes 32 neighbouring columns of 32 output rows, from column n0 (a
 // multiple of 32, so one checkpoint group) and row row0 on, a row a lane;
 // `count` columns and `rows` rows of them exist.  The sums of columns that do
@@ -188,9 +201,11 @@ __device__ __forceinline__ uint32_t finish32(const Epilogue &ep, int64_t row0, i
     transpose32(v, lane);  // v[i]: row row0 + i, column n0 + lane
     if (lane < count) {
         if (ep.res) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (i < rows) v[i] += load_any(ep.res, (row0 + i) * ep.ldr + n0 + lane, ep.res_f32);
+            const int64_t at = row0 * ep.ldr + n0 + lane;
+            if (ep.res_f32)
+                add_column(static_cast<const float *>(ep.res) + at, ep.ldr, rows, v);
+            else
+                add_column(static_cast<const uint16_t *>(ep.res) + at, ep.ldr, rows, v);
         }
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
@@ -397,7 +412,7 @@ struct Shape {
     static constexpr int kStages = KIND == kSkinny ? 9 : kIsSplit ? 4 : kStageBytes > 24576 ? 7 : 8;
     static constexpr int kBlocksPerSm = kIsSplit ? 2 : 1;
     // epilogue warps: four take the tile's 128 rows, and every further four share its columns
-    static constexpr int kWarps = BN >= 128 ? 16 : 8, kCols = BN / (kWarps / 4), kThreads = (kWarps + 2) * 32;
+    static constexpr int kWarps = kBCols >= 128 ? 16 : 8, kCols = BN / (kWarps / 4), kThreads = (kWarps + 2) * 32;
     static constexpr int kTmemCols = 2 * BN;  // two tiles' sums: one is finished while the next is made
     static constexpr int kColumnBytes = 2 * kBCols * 4;  // column sums of the two halves of dy's rows
     // (the last stage of a skinny tile is read past its end)
@@ -1025,8 +1040,14 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-// The tile: the widest that leaves half of the SMs or more one; the widest is
-// a pair's.  Where even the narrowest tiles leave half of the SMs idle and k is
+// The tile: the widest that leaves half of the SMs or more one.  What bounds
+// the smaller products is the rate at which an SM takes tiles in, about 50 bytes
+// a clock, so pairs, which share B, do better than single blocks of one width:
+// 568 x 3688 x 2440 in 128 columns 22.2 / 25.9 us, in 256 29.4; 1024 x 4096 x
+// 4096 in 256 columns 24.4 us, in 128 34.0 / 42.2, in 64 75.  With a step or two
+// of k the results' writes are all, and single blocks of 128 columns have more
+// tiles finishing at once: 8192 x 64 x 4096 19.3 us, a pair's 256 columns 25.2.
+// Where even the narrowest tiles leave half of the SMs idle and k is
 // long enough, clusters of 2 to 8 blocks split it: the exchange of the sums
 // costs about what 8 steps do.  With one row tile, where the weights' stream is
 // what counts, up to two blocks an SM.  Split / whole, us (GB300, graph replay):
@@ -1048,7 +1069,10 @@ cudaError_t launch_width(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
         if (splits > 1 && skinny) return launch_tiles<MODE, 64, kSkinny, F32>(p, a, b, sms, s, splits);
     if (splits > 1) return launch_tiles<MODE, 64, kSplit, F32>(p, a, b, sms, s, splits);
     if (tm * ceil_div<int64_t>(p.cols, 128) <= sms / 2) return launch_tiles<MODE, 64, kSingle, F32>(p, a, b, sms, s);
-    if (tm * ceil_div<int64_t>(p.cols, 256) <= sms / 2) return launch_tiles<MODE, 128, kSingle, F32>(p, a, b, sms, s);
+    const bool few = tm * ceil_div<int64_t>(p.cols, 256) <= sms / 2;
+    const bool one_wave = ceil_div<int64_t>(p.rows, 2 * kBM) * ceil_div<int64_t>(p.cols, 128) <= sms / 2;  // of pairs
+    if (p.steps <= 4 || (few && (tm == 1 || !one_wave))) return launch_tiles<MODE, 128, kSingle, F32>(p, a, b, sms, s);
+    if (few) return launch_tiles<MODE, 128, kPair, F32>(p, a, b, sms, s);
     return launch_tiles<MODE, 256, kPair, F32>(p, a, b, sms, s);
 }
 
