@@ -427,6 +427,11 @@ struct Product {
     int64_t rows, cols;
     int tiles_m, tiles_n, steps;  // steps of kBK along k
     int splits;                   // blocks that share a tile's steps
+    // pairs: tiles from `whole` on, which would leave most SMs idle in a last
+    // wave of their own, are made in `tail_parts` parts along k, each into its
+    // own 256 x 256 of `partial` (column by column), and joined afterwards
+    int whole, tail_parts;
+    float *partial;
     // wgrad: the column sums of B (dy) are wanted too
     float *db;
     const uint16_t *dy;
@@ -450,6 +455,13 @@ __device__ __forceinline__ void keep_sums(unsigned char *smem, int col, int row,
     float *to = reinterpret_cast<float *>(smem) + col * kBM + row;
 #pragma unroll
     for (int j = 0; j < 32; ++j) to[j * kBM] = v[j];
+}
+
+// 32 sums of a row of a tile's part, column by column
+template <int ROWS>
+__device__ __forceinline__ void keep_part(float *to, const float (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) to[j * ROWS] = v[j];
 }
 
 // The bias gradient, by the epilogue warps of the blocks with the first row
@@ -505,6 +517,24 @@ __device__ __forceinline__ void column_sums(const Product &p, int64_t c0, float 
     asm volatile("bar.sync 1, %0;" ::"n"(S::kWarps * 32) : "memory");
 }
 
+// What a block makes in its n-th turn: a tile, and the part of it and the steps
+// along k.
+struct Work {
+    int tile, part, k_begin, k_end;
+};
+template <int KIND>
+__device__ __forceinline__ Work work_at(const Product &p, int unit) {
+    if (KIND == kSplit || KIND == kSkinny) {
+        const int part = blockIdx.x % p.splits;
+        return Work{unit, part, p.steps * part / p.splits, p.steps * (part + 1) / p.splits};
+    }
+    if (KIND == kPair && unit >= p.whole) {
+        const int u = unit - p.whole, part = u % p.tail_parts;
+        return Work{p.whole + u / p.tail_parts, part, p.steps * part / p.tail_parts, p.steps * (part + 1) / p.tail_parts};
+    }
+    return Work{unit, 0, 0, p.steps};
+}
+
 template <int MODE, int BN, int KIND, bool F32>
 __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kBlocksPerSm) product_kernel(const __grid_constant__ Product p) {
     using S = Shape<BN, KIND>;
@@ -520,12 +550,9 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kStages * S::kStageBytes + 16 * S::kStages + 40);
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int rank = PAIR ? blockIdx.x & 1 : 0;
-    // the first tile and the distance to the next; the steps along k
+    // the first unit of work and the distance to the next
     const int share = S::kIsSplit ? p.splits : S::kBlocks;
-    const int tile0 = blockIdx.x / share, tile_step = gridDim.x / share;
-    const int part = S::kIsSplit ? blockIdx.x % p.splits : 0;
-    const int k_begin = S::kIsSplit ? p.steps * part / p.splits : 0, k_end = S::kIsSplit ? p.steps * (part + 1) / p.splits : p.steps;
-    const int steps = k_end - k_begin;
+    const int unit0 = blockIdx.x / share, unit_step = gridDim.x / share;
 
     if (warp == S::kWarps) {
         if (lane == 0) {
@@ -553,17 +580,18 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
     const uint32_t tmem = *tmem_slot;
     pdl_enter();
 
-    const int tile_count = p.tiles_m * p.tiles_n;
+    const int tile_count = p.tiles_m * p.tiles_n, unit_count = S::kIsPair ? p.whole + (tile_count - p.whole) * p.tail_parts : tile_count;
     bool ok = true;
     if (warp == S::kWarps) {  // TMA
         int s = 0;
         uint32_t phase = 0;
         int64_t issued = 0;
-        for (int tile = tile0; tile < tile_count && ok; tile += tile_step) {
+        for (int unit = unit0; unit < unit_count && ok; unit += unit_step) {
+            const Work work = work_at<KIND>(p, unit);
             int tm, tn;
-            tile_at(p, tile, &tm, &tn);
+            tile_at(p, work.tile, &tm, &tn);
             const int row = tm * S::kRows + rank * kBM, col = tn * BN + rank * S::kBCols;
-            for (int k = k_begin; k < k_end; ++k) {
+            for (int k = work.k_begin; k < work.k_end; ++k) {
                 ok = __all_sync(0xffffffffu, wait(empty + 8 * s, phase ^ 1));
                 if (!ok) break;
                 const uint32_t a = tiles + s * S::kStageBytes, b = a + S::kABytes;
@@ -602,7 +630,9 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
             const uint64_t a0 = operand(tiles, kAmn ? 8192 : 16, 1024), b0 = operand(tiles + S::kABytes, kBmn ? 8192 : 16, 1024);
             int s = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
-            for (int tile = tile0; tile < tile_count && ok; tile += tile_step) {
+            for (int unit = unit0; unit < unit_count && ok; unit += unit_step) {
+                const Work work = work_at<KIND>(p, unit);
+                const int steps = work.k_end - work.k_begin;
                 for (int k = 0; k < steps || k == 0; ++k) {
                     if (F32 ? k % kChunk == 0 : k == 0) {  // a new sum
                         ok = __all_sync(0xffffffffu, wait(freed + 8 * acc, acc_phase ^ 1));
@@ -648,14 +678,20 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
         int acc = 0;
         uint32_t acc_phase = 0;
         const uint32_t mine = tmem + (warp / 4) * S::kCols + ((uint32_t)(warp % 4 * 32) << 16);
-        for (int tile = tile0; tile < tile_count && ok; tile += tile_step) {
+        for (int unit = unit0; unit < unit_count && ok; unit += unit_step) {
+            const Work work = work_at<KIND>(p, unit);
+            const int steps = work.k_end - work.k_begin;
             int tm, tn;
-            tile_at(p, tile, &tm, &tn);
+            tile_at(p, work.tile, &tm, &tn);
             const int64_t row0 = (int64_t)tm * S::kRows + rank * kBM + warp % 4 * 32, row = row0 + lane;
             const int rows = p.rows - row0 < 32 ? (int)(p.rows - row0) : 32;  // of the warp's 32 (none where not above 0)
             const int64_t c0 = (int64_t)tn * BN + warp / 4 * S::kCols;
-            if (MODE == kWgrad && p.db && tm == 0 && part == 0)
+            if (MODE == kWgrad && p.db && tm == 0 && work.part == 0)
                 column_sums<S>(p, (int64_t)tn * BN + rank * S::kBCols, reinterpret_cast<float *>(smem + S::kStages * S::kStageBytes + 256), warp, lane);
+            // where a part's sums go, for its first column and this lane's row
+            const bool tail = S::kIsPair && unit >= p.whole;
+            float *to = !tail ? nullptr
+                              : p.partial + ((int64_t)(unit - p.whole) * BN + warp / 4 * S::kCols) * S::kRows + rank * kBM + warp % 4 * 32 + lane;
             if constexpr (F32) {
                 float sum[S::kCols / 32][32];
 #pragma unroll
@@ -684,6 +720,11 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                     for (int g = 0; g < S::kCols / 32; ++g) keep_sums(smem, warp / 4 * S::kCols + g * 32, warp % 4 * 32 + lane, sum[g]);
                     continue;
                 }
+                if (tail) {
+#pragma unroll
+                    for (int g = 0; g < S::kCols / 32; ++g) keep_part<S::kRows>(to + g * 32 * S::kRows, sum[g]);
+                    continue;
+                }
                 uint32_t step_bytes = 0;
 #pragma unroll
                 for (int g = 0; g < S::kCols / 32; ++g) {
@@ -691,7 +732,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                     if (rows > 0 && n0 < p.cols)
                         step_bytes |= finish32<MODE>(p.ep, row0, rows, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), sum[g]) << (8 * g);
                 }
-                if (MODE == kForward && !S::kIsSplit && p.ep.q && row < p.rows && c0 < p.cols) store_steps<S::kCols>(p.ep, row, c0, step_bytes);
+                if (MODE == kForward && !S::kIsSplit && !tail && p.ep.q && row < p.rows && c0 < p.cols) store_steps<S::kCols>(p.ep, row, c0, step_bytes);
                 __syncwarp();
             } else {
                 ok = __all_sync(0xffffffffu, wait(done + 8 * acc, acc_phase));
@@ -712,9 +753,13 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                         keep_sums(smem, warp / 4 * S::kCols + g * 32, warp % 4 * 32 + lane, v);
                         continue;
                     }
+                    if (tail) {
+                        keep_part<S::kRows>(to + g * 32 * S::kRows, v);
+                        continue;
+                    }
                     if (rows > 0) step_bytes |= finish32<MODE>(p.ep, row0, rows, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v) << (8 * g);
                 }
-                if (MODE == kForward && !S::kIsSplit && p.ep.q && row < p.rows && c0 < p.cols) store_steps<S::kCols>(p.ep, row, c0, step_bytes);
+                if (MODE == kForward && !S::kIsSplit && !tail && p.ep.q && row < p.rows && c0 < p.cols) store_steps<S::kCols>(p.ep, row, c0, step_bytes);
                 release<PAIR>(freed_bar + 8 * acc, lane);
                 flip(acc, acc_phase);
             }
@@ -729,8 +774,8 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
         const int height = kBM / p.splits, per_group = height > 32 ? height / 32 : 1;  // warps a column group
         const int g = warp / per_group, at0 = warp % per_group * 32;
         int tm, tn;
-        tile_at(p, tile0, &tm, &tn);
-        const int in_tile = part * height + at0;
+        tile_at(p, unit0, &tm, &tn);
+        const int in_tile = blockIdx.x % p.splits * height + at0;
         const int64_t row0 = (int64_t)tm * kBM + in_tile, n0 = (int64_t)tn * BN + g * 32;
         int rows = height < 32 ? height : 32;
         if (p.rows - row0 < rows) rows = (int)(p.rows - row0);
@@ -760,6 +805,31 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         tmem_free<PAIR, S::kTmemCols>(tmem);
     }
+}
+
+// The tiles made in parts: the sums of the parts in their order, then the
+// epilogue.  A block a 32-column stripe of a tile, a warp 32 of its rows.
+constexpr int kTailBN = 256, kTailRows = 2 * kBM, kTailThreads = kTailRows;
+template <int MODE>
+__global__ void __launch_bounds__(kTailThreads) join_tail_kernel(const __grid_constant__ Product p) {
+    pdl_enter();
+    const int t = blockIdx.x / (kTailBN / 32), g = blockIdx.x % (kTailBN / 32);
+    int tm, tn;
+    tile_at(p, p.whole + t, &tm, &tn);
+    const int64_t row0 = (int64_t)tm * kTailRows + threadIdx.x / 32 * 32, n0 = (int64_t)tn * kTailBN + g * 32;
+    if (row0 >= p.rows || n0 >= p.cols) return;
+    const float *from = p.partial + ((int64_t)t * p.tail_parts * kTailBN + g * 32) * kTailRows + threadIdx.x;
+    float v[32];
+    for (int q = 0; q < p.tail_parts; ++q, from += kTailBN * kTailRows) {
+        float x[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = __ldg(from + j * kTailRows);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = q ? v[j] + x[j] : x[j];
+    }
+    const int rows = p.rows - row0 < 32 ? (int)(p.rows - row0) : 32, lane = threadIdx.x & 31;
+    const uint32_t step_byte = finish32<MODE>(p.ep, row0, rows, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
+    if (MODE == kForward && p.ep.q && lane < rows) store_steps<32>(p.ep, row0 + lane, n0, step_byte);
 }
 
 // ---------------------------------------------------------------------------
@@ -1006,6 +1076,25 @@ cudaError_t launch_column_sum(const Mat &dy, int accumulate, float *db, cudaStre
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
+// The last wave of the pairs' 256 x 256 tiles: how many there are, and in how
+// many parts each is made.  In parts where these find SMs that would idle, and
+// the steps saved are worth the sums' way through memory and a launch (about 8
+// us): 8192 x 8192 x 2048, 256 tiles on 76 pairs, 161 us instead of 172.
+struct Tail {
+    int tiles, parts;
+};
+Tail tail_of(int64_t rows, int64_t cols, int64_t steps, int sms) {
+    const int64_t tiles = ceil_div<int64_t>(rows, kTailRows) * ceil_div<int64_t>(cols, kTailBN), pairs = sms / 2;
+    if (pairs == 0 || tiles < pairs || tiles % pairs == 0) return Tail{0, 1};
+    const int64_t last = tiles % pairs, parts = pairs / last < 4 ? pairs / last : 4;
+    if (parts < 2 || steps - steps / parts < 48) return Tail{0, 1};
+    return Tail{(int)last, (int)parts};
+}
+int64_t tail_bytes(int64_t rows, int64_t cols, int64_t k, int sms) {
+    const Tail t = tail_of(rows, cols, ceil_div<int64_t>(k, kBK), sms);
+    return (int64_t)t.tiles * t.parts * kTailRows * kTailBN * 4;
+}
+
 template <int MODE, int BN, int KIND, bool F32>
 cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaStream_t s, int splits = 1) {
     using S = Shape<BN, KIND>;
@@ -1022,6 +1111,9 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     if (e != cudaSuccess) return e;
     const int cluster = S::kIsSplit ? splits : S::kBlocks;
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, most = S::kIsSplit ? tiles : sms / S::kBlocks;
+    const Tail tail = KIND == kPair && BN == kTailBN && p.partial ? tail_of(p.rows, p.cols, p.steps, sms) : Tail{0, 1};
+    p.whole = (int)(tiles - tail.tiles);
+    p.tail_parts = tail.parts;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * cluster));
     cfg.blockDim = dim3(S::kThreads);
@@ -1037,7 +1129,9 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     cfg.attrs = attr;
     cfg.numAttrs = KIND == kSingle ? 1 : 2;
     e = cudaLaunchKernelEx(&cfg, product_kernel<MODE, BN, KIND, F32>, p);
-    return e == cudaSuccess ? cudaGetLastError() : e;
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess || tail.tiles == 0) return e;
+    return launch_pdl(join_tail_kernel<MODE>, tail.tiles * (kTailBN / 32), kTailThreads, 0, s, p);
 }
 
 // The tile: the widest that leaves half of the SMs or more one.  What bounds
@@ -1079,7 +1173,7 @@ cudaError_t launch_width(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
 // out (rows x cols) = epilogue(A B); a and b as they lie in memory
 template <int MODE>
 cudaError_t launch_product(const Mat &a, const Mat &b, int64_t rows, int64_t cols, int64_t k, Epilogue ep, const Mat &out, const Mat &bias, const Mat &res,
-                           cudaStream_t s, float *db = nullptr, int db_add = 0) {
+                           Workspace *space, cudaStream_t s, float *db = nullptr, int db_add = 0) {
     Product p = {};
     p.ep = ep;
     p.ep.rows_aligned = out.aligned(32) && (res.empty() || res.aligned(32));
@@ -1097,8 +1191,9 @@ cudaError_t launch_product(const Mat &a, const Mat &b, int64_t rows, int64_t col
     cudaError_t e = device_error_word(&p.err);
     if (e == cudaSuccess) e = sm_count(&sms);
     if (e != cudaSuccess) return e;
-    const int64_t tm = ceil_div<int64_t>(rows, kBM);
+    const int64_t tm = ceil_div<int64_t>(rows, kBM), part_bytes = tail_bytes(rows, cols, k, sms);
     if (tm * ceil_div<int64_t>(cols, 64) >= kMaxExtent) return cudaErrorInvalidValue;
+    if (part_bytes > 0) p.partial = static_cast<float *>(space->take(part_bytes));  // without room: tiles whole
     return ep.out_f32 ? launch_width<MODE, true>(p, a, b, sms, s) : launch_width<MODE, false>(p, a, b, sms, s);
 }
 
@@ -1131,6 +1226,14 @@ size_t ra_linear_workspace_bytes(int64_t m, int64_t k, int64_t n) {
     return (size_t)(mk + kn + mn - least + kWorkspaceSlack);
 }
 
+size_t ra_linear_split_bytes(int64_t rows, int64_t cols, int64_t k) {
+    if (rows < 0 || cols < 0 || k < 0 || rows >= kMaxExtent || cols >= kMaxExtent || k >= kMaxExtent) return 0;
+    int sms = 0;
+    if (sm_count(&sms) != cudaSuccess) return 0;
+    const int64_t bytes = tail_bytes(rows, cols, k, sms);
+    return bytes > 0 ? (size_t)(bytes + kWorkspaceSlack) : 0;
+}
+
 ra_status ra_linear(const void *x, int64_t ld_x, const void *w, int64_t ld_w, int64_t m, int64_t k, int64_t n,
                     const void *bias, int bias_dtype, int act, const void *residual, int64_t ld_res, int res_dtype,
                     int8_t *save_q, uint8_t *save_e, void *y, int64_t ld_y, int y_dtype, void *ws, size_t ws_bytes,
@@ -1156,7 +1259,7 @@ ra_status ra_linear(const void *x, int64_t ld_x, const void *w, int64_t ld_w, in
     Workspace space(ws, ws_bytes);
     Mat a, b;
     if (!place(mx, &space, &a) || !place(mw, &space, &b)) return RA_ERR_INVALID_ARG;
-    if (a.data != x || b.data != w) {
+    if (ws) {
         const Mat wm{ws, 1, (int64_t)ws_bytes, (int64_t)ws_bytes, 1};
         const Mat *all[] = {&mx, &mw, &my, &mb, &mr, &kept.q, &kept.e};
         for (int i = 0; i < (save_q ? 7 : 5); ++i)
@@ -1167,7 +1270,7 @@ ra_status ra_linear(const void *x, int64_t ld_x, const void *w, int64_t ld_w, in
     if (e != cudaSuccess) return cuda_status(e);
     const Epilogue ep{y, bias, residual, save_q, save_e, ld_y, ld_res, ceil_div<int64_t>(n, kGroup), y_dtype == RA_F32, bias_dtype == RA_F32,
                       res_dtype == RA_F32, act, 0};
-    return cuda_status(launch_product<kForward>(a, b, m, n, k, ep, my, mb, mr, s));
+    return cuda_status(launch_product<kForward>(a, b, m, n, k, ep, my, mb, mr, &space, s));
 }
 
 ra_status ra_linear_dgrad(const void *dy, int64_t ld_dy, const void *w, int64_t ld_w, int64_t m, int64_t k, int64_t n,
@@ -1187,7 +1290,7 @@ ra_status ra_linear_dgrad(const void *dy, int64_t ld_dy, const void *w, int64_t 
     Workspace space(ws, ws_bytes);
     Mat a, b;
     if (!place(md, &space, &a) || !place(mw, &space, &b)) return RA_ERR_INVALID_ARG;
-    if (a.data != dy || b.data != w) {
+    if (ws) {
         const Mat wm{ws, 1, (int64_t)ws_bytes, (int64_t)ws_bytes, 1};
         const Mat *all[] = {&md, &mw, &mx, &mr, &kept.q, &kept.e};
         for (int i = 0; i < (act != RA_ACT_NONE ? 6 : 4); ++i)
@@ -1198,7 +1301,7 @@ ra_status ra_linear_dgrad(const void *dy, int64_t ld_dy, const void *w, int64_t 
     if (e != cudaSuccess) return cuda_status(e);
     const Epilogue ep{dx, nullptr, residual, act ? const_cast<int8_t *>(z_q) : nullptr, const_cast<uint8_t *>(z_e), ld_dx, ld_res,
                       ceil_div<int64_t>(k, kGroup), dx_dtype == RA_F32, 0, res_dtype == RA_F32, act, 0};
-    return cuda_status(launch_product<kDgrad>(a, b, m, k, n, ep, mx, Mat{nullptr, 0, 0, 0, 1}, mr, s));
+    return cuda_status(launch_product<kDgrad>(a, b, m, k, n, ep, mx, Mat{nullptr, 0, 0, 0, 1}, mr, &space, s));
 }
 
 ra_status ra_linear_wgrad(const void *x, int64_t ld_x, const int8_t *z_q, const uint8_t *z_e, int act, const void *dy,
@@ -1230,7 +1333,7 @@ ra_status ra_linear_wgrad(const void *x, int64_t ld_x, const int8_t *z_q, const 
         return RA_ERR_INVALID_ARG;
     }
     if (!place(md, &space, &b)) return RA_ERR_INVALID_ARG;
-    if (a.data != x || b.data != dy) {
+    if (ws) {
         const Mat wm{ws, 1, (int64_t)ws_bytes, (int64_t)ws_bytes, 1};
         const Mat *all[] = {&mx, &md, &mw, &mb, &kept.q, &kept.e};
         for (int i = 0; i < (from_kept ? 6 : 4); ++i)
@@ -1247,7 +1350,7 @@ ra_status ra_linear_wgrad(const void *x, int64_t ld_x, const int8_t *z_q, const 
     }
     const Epilogue ep{dw, nullptr, accumulate ? dw : nullptr, nullptr, nullptr, ld_dw, ld_dw, 0, dw_dtype == RA_F32, 0, dw_dtype == RA_F32, 0, 0};
     const Mat none{nullptr, 0, 0, 0, 1};
-    return cuda_status(launch_product<kWgrad>(a, b, k, n, m, ep, mw, none, accumulate ? mw : none, s, db, accumulate));
+    return cuda_status(launch_product<kWgrad>(a, b, k, n, m, ep, mw, none, accumulate ? mw : none, &space, s, db, accumulate));
 }
 
 }  // extern "C"

@@ -21,6 +21,8 @@ import gradient_ring_all_gb300 as _ra
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 GROUP = 32  # values of a row that share a checkpoint's step
 
+_LARGE = 1 << 34  # for products below this ra_linear_split_bytes is not asked: a split would not repay the allocation
+
 _F32, _BF16 = torch.float32, torch.bfloat16
 _CODE = {_F32: 0, _BF16: 1}
 _ID_BYTES = {torch.int32: 4, torch.int64: 8}
@@ -44,13 +46,14 @@ def _load():
     lib.ra_embedding_grad_workspace_bytes.argtypes = [i64, i64, i64]
     lib.ra_embedding_grad.argtypes = [vp, i64, i32, vp, i32, i64, f32, i32, vp, i64, i32, i64, i64, vp, sz, vp]
     lib.ra_linear_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.ra_linear_split_bytes.argtypes = [i64, i64, i64]
     lib.ra_linear.argtypes = [vp, i64, vp, i64, i64, i64, i64, vp, i32, i32, vp, i64, i32, vp, vp, vp, i64, i32, vp, sz, vp]
     lib.ra_linear_dgrad.argtypes = [vp, i64, vp, i64, i64, i64, i64, vp, vp, i32, vp, i64, i32, vp, i64, i32, vp, sz, vp]
     lib.ra_linear_wgrad.argtypes = [vp, i64, vp, vp, i32, vp, i64, i64, i64, i64, i32, vp, i64, i32, vp, vp, sz, vp]
     for name in ("ra_checkpoint8_pack", "ra_checkpoint8_unpack", "ra_embedding_lookup", "ra_embedding_grad", "ra_linear",
                  "ra_linear_dgrad", "ra_linear_wgrad"):
         getattr(lib, name).restype = i32
-    for name in ("ra_embedding_grad_workspace_bytes", "ra_linear_workspace_bytes"):
+    for name in ("ra_embedding_grad_workspace_bytes", "ra_linear_workspace_bytes", "ra_linear_split_bytes"):
         getattr(lib, name).restype = sz
     _declared = lib
     return lib
@@ -147,6 +150,19 @@ def _workspace(workspace, need, like, stream):
     if not workspace.is_cuda or workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the call's device")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _room(workspace, in_place, rows, cols, k, mkn, like, stream, lib):
+    """The linear layer's workspace: (tensor to hold, pointer, bytes), none where it helps nothing."""
+    if workspace is None:
+        need = 0 if in_place else lib.ra_linear_workspace_bytes(*mkn)
+        if rows * cols * k >= _LARGE:
+            need += lib.ra_linear_split_bytes(rows, cols, k)
+        if need == 0:
+            return None, None, 0
+    else:
+        need = 0
+    return _workspace(workspace, need, like, stream)
 
 
 def _check(status, what):
@@ -315,9 +331,7 @@ def ra_linear(x, w, bias=None, act="none", residual=None, save=None, dtype=None,
         pq, pe = _kept(save, "save", m, n, dev)
     out, py, ldy, ycode = _output(out, m, n, dtype or (_BF16 if out is None else None), x, dev, stream)
     lib = _load()
-    ws, nws, hold = None, 0, None
-    if workspace is not None or not (_in_place(px, ldx, m) and _in_place(pw, ldw, k)):
-        hold, ws, nws = _workspace(workspace, lib.ra_linear_workspace_bytes(m, k, n), x, stream)
+    hold, ws, nws = _room(workspace, _in_place(px, ldx, m) and _in_place(pw, ldw, k), m, n, k, (m, k, n), x, stream, lib)
     _check(lib.ra_linear(px, ldx, pw, ldw, m, k, n, pb, bcode, _act(act), pr, ldr, rcode, pq, pe, py, ldy, ycode, ws, nws,
                          _stream_of(stream, dev)), "ra_linear")
     return out
@@ -341,9 +355,7 @@ def ra_linear_dgrad(dy, w, saved=None, act="none", residual=None, dtype=None, ou
         pr, ldr, rcode = _matrix(residual, "residual", dev, None, (m, k))
     out, px, ldx, xcode = _output(out, m, k, dtype or (_BF16 if out is None else None), dy, dev, stream)
     lib = _load()
-    ws, nws, hold = None, 0, None
-    if workspace is not None or not (_in_place(pd, ldd, m) and _in_place(pw, ldw, k)):
-        hold, ws, nws = _workspace(workspace, lib.ra_linear_workspace_bytes(m, k, n), dy, stream)
+    hold, ws, nws = _room(workspace, _in_place(pd, ldd, m) and _in_place(pw, ldw, k), m, k, n, (m, k, n), dy, stream, lib)
     _check(lib.ra_linear_dgrad(pd, ldd, pw, ldw, m, k, n, pq, pe, code, pr, ldr, rcode, px, ldx, xcode, ws, nws,
                                _stream_of(stream, dev)), "ra_linear_dgrad")
     return out
@@ -380,9 +392,7 @@ def ra_linear_wgrad(x, dy, act="none", dtype=None, out=None, bias_grad=False, ac
             raise ValueError("bias_grad must be True or a contiguous float32 CUDA vector of length %d" % n)
         pb = db.data_ptr()
     lib = _load()
-    ws, nws, hold = None, 0, None
-    if workspace is not None or px is None or not (_in_place(px, ldx, m) and _in_place(pd, ldd, m)):
-        hold, ws, nws = _workspace(workspace, lib.ra_linear_workspace_bytes(m, k, n), dy, stream)
+    hold, ws, nws = _room(workspace, px is not None and _in_place(px, ldx, m) and _in_place(pd, ldd, m), k, n, m, (m, k, n), dy, stream, lib)
     _check(lib.ra_linear_wgrad(px, ldx, pq, pe, code, pd, ldd, m, k, n, int(accumulate), pw, ldw, wcode, pb, ws, nws,
                                _stream_of(stream, dev)), "ra_linear_wgrad")
     return out if pb is None else (out, db)

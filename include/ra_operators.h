@@ -107,12 +107,20 @@ ra_status ra_embedding_grad(const void *grad, int64_t ld_grad, int grad_dtype, c
  *   save_q, save_e  NULL, or the 8-bit checkpoint (m x n) that receives
  *             z = x w + bias, for ra_linear_dgrad and ra_linear_wgrad
  *   y         m x n of y_dtype, rounded once
- *   ws        device workspace of ra_linear_workspace_bytes(m, k, n), 16-byte
- *             aligned; may be NULL where x and w start on 16-byte boundaries
- *             and their rows are multiples of 16 bytes apart (TMA reads them
- *             in place; others are first laid out in the workspace)
+ *   ws        device workspace, 16-byte aligned, for two things:
+ *             - ra_linear_workspace_bytes(m, k, n) where x or w does not start on
+ *               a 16-byte boundary or its rows are not multiples of 16 bytes
+ *               apart: TMA reads others in place, these are laid out first;
+ *             - ra_linear_split_bytes(m, n, k) more, by choice: where it is not
+ *               0, the last tiles would leave most SMs idle, and with this room
+ *               they are made in parts along k (faster; the sums are then
+ *               grouped differently, the same way in every such call).
+ *             NULL where neither is wanted.
  */
 size_t ra_linear_workspace_bytes(int64_t m, int64_t k, int64_t n);
+/* for an output of rows x cols summed over k: (m, n, k) for ra_linear, (m, k, n)
+ * for ra_linear_dgrad, (k, n, m) for ra_linear_wgrad */
+size_t ra_linear_split_bytes(int64_t rows, int64_t cols, int64_t k);
 ra_status ra_linear(const void *x, int64_t ld_x, const void *w, int64_t ld_w, int64_t m, int64_t k, int64_t n,
                     const void *bias, int bias_dtype, int act, const void *residual, int64_t ld_res, int res_dtype,
                     int8_t *save_q, uint8_t *save_e, void *y, int64_t ld_y, int y_dtype, void *ws, size_t ws_bytes,

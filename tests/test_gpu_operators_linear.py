@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import gradient_ring_all_gb300 as ra
+from gradient_ring_all_gb300 import operators
 from operator_reference import Framed, act64, check, pack64, rounding, slope64, sum_bound, values64
 
 pytestmark = pytest.mark.gpu
@@ -204,6 +205,68 @@ def test_wgrad_accumulates_over_micro_batches(out_type, lead, gap):
     check(dw.t, want, 1.01 * bound + 6 * rounding(out_type) * bound)
     check(db, b64, sum_bound(3 * m) * 3 * m * 4)
     dw.intact("wgrad accumulate")
+
+
+@pytest.mark.parametrize("out_type", [BF16, F32])
+def test_last_tiles_made_in_parts(out_type):
+    """Sizes whose last wave of tiles is split along k, ragged ones, in all three products; and the same without the room."""
+    lib = operators._load()
+    m, k, n = 2500, 4100, 2200
+    x, w = _normal(1, m, 4104)[:, :k], _normal(2, k, n, s=k ** -0.5)
+    bias, residual = _normal(3, n, dtype=F32), _normal(4, m, n)
+    assert lib.ra_linear_split_bytes(m, n, k) > 0
+    kept, out = ra.Checkpoint8(m, n), Framed(m, n, out_type, 0, 16)
+    ra.ra_linear(x, w, bias=bias, act="gelu", residual=residual, save=kept, out=out.t)
+    z, y, size = _forward64(x, w, bias, "gelu", residual)
+    bound = _forward_bound(k, z, y, size, out_type, residual)
+    check(out.t, y, bound)
+    out.intact("split")
+    groups = -(-n // 32)
+    off = sum_bound(k + 1) * size
+    top = torch.nn.functional.pad(z.abs() + off, (0, groups * 32 - n)).view(m, groups, 32).amax(2).repeat_interleave(32, 1)[:, :n]
+    check(ra.ra_checkpoint8_unpack(kept, dtype=F32), z, top / 127.5 * (1 + 2.0 ** -20) + off)
+    again = ra.ra_linear(x, w, bias=bias, act="gelu", residual=residual, dtype=out_type)
+    assert torch.equal(again, out.t)
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    check(ra.ra_linear(x, w, bias=bias, act="gelu", residual=residual, dtype=out_type, workspace=small), y, bound)
+    # x of the forward product as dy of the others: rows of dx, and of dw, over 4100
+    assert lib.ra_linear_split_bytes(m, n, k) > 0 and lib.ra_linear_split_bytes(n, m, k) > 0
+    wt = _normal(5, n, k, s=k ** -0.5)
+    z8 = ra.ra_checkpoint8_pack(_normal(6, m, n, s=2.0))
+    got = ra.ra_linear_dgrad(x, wt, saved=z8, act="silu", dtype=out_type)
+    zz = values64(z8.q, z8.e, n)
+    g, gsize = x.double() @ wt.double().t(), x.double().abs() @ wt.double().t().abs()
+    want = g * slope64(zz, "silu")
+    check(got, want, 1.13 * sum_bound(k) * gsize + 2.0 ** -20 * g.abs() * (1 + zz.abs()) + rounding(out_type) * want.abs())
+    a, dy = _normal(7, k, n), _normal(8, k, m + 4)[:, :m]
+    dw, db = ra.ra_linear_wgrad(a, dy, dtype=out_type, bias_grad=True)
+    want, size = a.double().t() @ dy.double(), a.double().t().abs() @ dy.double().abs()
+    check(dw, want, sum_bound(k) * size + rounding(out_type) * want.abs())
+    check(db, dy.double().sum(0), sum_bound(k) * dy.double().abs().sum(0))
+
+
+def test_past_32_bit_offsets():
+    """An output of more than 2^31 values, beside inputs whose last rows start beyond 2^31 bytes."""
+    m, k, n = 70_000, 64, 32_000
+    x, w = _normal(1, m, k), _normal(2, k, n)
+    y = ra.ra_linear(x, w)
+    kept = ra.ra_checkpoint8_pack(y)
+    for rows in ([0, 1, 255, 256], [m // 2, m // 2 + 1], [67_107, 67_108, 67_109], [m - 257, m - 2, m - 1]):
+        z = x[rows].double() @ w.double()
+        size = x[rows].double().abs() @ w.double().abs()
+        check(y[rows], z, sum_bound(k) * size + rounding(BF16) * z.abs())
+        q, e = pack64(y[rows])
+        assert torch.equal(kept.q[rows], q) and torch.equal(kept.e[rows], e)
+    back = ra.ra_checkpoint8_unpack(kept)
+    assert torch.equal(back[-3:].double(), values64(kept.q[-3:], kept.e[-3:], n))
+    dw = ra.ra_linear_wgrad(x, y, dtype=F32)
+    cols = [0, 1, n // 2, n - 1]
+    want, size = x.double().t() @ y[:, cols].double(), x.double().t().abs() @ y[:, cols].double().abs()
+    check(dw[:, cols], want, sum_bound(m) * size + rounding(F32) * want.abs())
+    dx = ra.ra_linear_dgrad(y, w)
+    rows = [0, 67_108, m - 1]
+    want, size = y[rows].double() @ w.double().t(), y[rows].double().abs() @ w.double().t().abs()
+    check(dx[rows], want, sum_bound(n) * size + rounding(BF16) * want.abs())
 
 
 def test_empty_sums_and_nothing_to_do():
