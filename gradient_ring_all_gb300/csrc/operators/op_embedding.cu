@@ -8,10 +8,10 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // lookup: out[t] = scale * table[id_t], zeros for an id outside the table.
-// A warp a token; each lane takes W neighbouring columns at a time, 4 of them
-// in flight.
+// A warp a token; each lane takes W neighbouring columns at a time, 8 such in
+// flight.  Bound by the rows' way in and out.
 
-constexpr int kLookupThreads = 256;
+constexpr int kLookupThreads = 256, kLookupFlight = 8;
 
 struct LookupParams {
     const void *table;
@@ -36,28 +36,21 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const LookupPara
         const int64_t id = load_id<I>(p.ids, t, p.vocab);
         const T *src = static_cast<const T *>(p.table) + (id < 0 ? 0 : id) * p.ldt;
         T *dst = static_cast<T *>(p.out) + t * p.ldo;
-        constexpr int kFlight = 4;
-        for (int64_t c0 = lane * W; c0 < p.d; c0 += 32 * W * kFlight) {
-            float x[kFlight][W];
+        for (int64_t c0 = lane * W; c0 < p.d; c0 += 32 * W * kLookupFlight) {
+            Raw<T, W> x[kLookupFlight];
 #pragma unroll
-            for (int k = 0; k < kFlight; ++k) {
+            for (int k = 0; k < kLookupFlight; ++k) {
                 const int64_t c = c0 + k * 32 * W;
-                if (c < p.d && id >= 0) {
-                    load_w<T, W>(src + c, x[k]);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < W; ++j) x[k][j] = 0.0f;
-                }
+                if (c < p.d && id >= 0) x[k].load(src + c);
             }
 #pragma unroll
-            for (int k = 0; k < kFlight; ++k) {
+            for (int k = 0; k < kLookupFlight; ++k) {
                 const int64_t c = c0 + k * 32 * W;
-                if (c >= p.d) continue;
-                if (id >= 0) {
+                if (c >= p.d) break;
+                float y[W];
 #pragma unroll
-                    for (int j = 0; j < W; ++j) x[k][j] = __fmul_rn(x[k][j], p.scale);
-                }
-                store_w<T, W>(dst + c, x[k]);
+                for (int j = 0; j < W; ++j) y[j] = id >= 0 ? __fmul_rn(x[k][j], p.scale) : 0.0f;
+                store_w<T, W>(dst + c, y);
             }
         }
     }
