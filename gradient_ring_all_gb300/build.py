@@ -5,8 +5,8 @@
 Compiles each csrc/*.cu and csrc/operators/*.cu into _build/*.o in parallel with nvcc and links
 lib/libgradient_ring_all.so against the shared CUDA runtime.  A stamp of the
 sources and flags skips the work when nothing changed.  --checked builds the
-bounds-checked library instead (RA_CHECKED=1: every kernel verifies each
-global range it touches and reports a violation through the error word),
+bounds-checked library instead (RA_CHECKED=1: every kernel of the ring verifies
+each global range it touches and reports a violation through the error word),
 into _build_checked/ and lib/libgradient_ring_all_checked.so; the tests use
 it, the product does not.
 """

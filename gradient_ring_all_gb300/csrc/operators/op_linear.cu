@@ -9,8 +9,15 @@
 //   wgrad    A = x^T, B = dy: both MN-major
 // The tensor cores take either order from shared memory, so nothing is
 // transposed: TMA lays 128-byte swizzled tiles of 64 k by 128 rows and by BN
-// columns, one thread issues tcgen05.mma on them, the sums stay in TMEM, and
+// columns, one warp issues tcgen05.mma on them, the sums stay in TMEM, and
 // the epilogue warps read them from there.
+//
+// A step of 64 k of a pair's 256 x 256 tile is 512 clocks of the tensor core and
+// 64 KB of loads; 7 such steps are in flight.  Large products run into the
+// power limit: 8192 x 2048 x 8192 144-150 us (1.83-1.9 PFLOP/s), 8192 x 8192 x
+// 2048 156-162 us, 8192^3 600 us on normal values and 495 us on zeros (2.2
+// PFLOP/s at 2070 MHz).  Small ones are bound by the rate at which an SM takes
+// tiles in and by a launch's start: one 64-column step alone takes 3 us.
 #include <cuda.h>
 
 #include <cooperative_groups.h>

@@ -30,6 +30,10 @@
  *   - results do not change from call to call: every sum is added in an order
  *     that the sizes and the token ids alone decide.
  *   - NaN and infinities go through by the formulas.
+ *   - the products' kernels wait for their own copies and tensor-core work with
+ *     the library's limit; ra_check_device_errors reports a wait that gave up.
+ *   - the first call of each kind looks up a driver entry point and loads its
+ *     kernels: make it before any stream capture.
  */
 #ifndef RA_OPERATORS_H
 #define RA_OPERATORS_H

@@ -347,7 +347,7 @@ ra_status ra_check_device_errors(void);
 
 /*
  * ra_selftest_bounds_check -- the bounds-checked build (libgradient_ring_all_
- * checked.so, built for the tests) verifies inside every kernel that each
+ * checked.so, built for the tests) verifies inside every ring kernel that each
  * global range it reads or writes lies in the caller's buffers, skips the
  * access otherwise, and records RA_ERR_BOUNDS for ra_check_device_errors().
  * This call exercises that check: it runs the fused all-reduce over the p
