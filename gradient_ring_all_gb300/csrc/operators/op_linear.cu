@@ -398,10 +398,10 @@ constexpr int kBM = 128, kBK = 64;
 // The tensor core adds to its binary32 sums by truncation: a sum over k comes
 // out about 1e-9 k short (measured: 2.3e-7 at k = 256, 4.4e-6 at 4096, 3.8e-5
 // at 32768, all toward zero).  That is far below a bf16 result's rounding, but
-// not below a binary32 one's: there the tensor core sums kChunk steps (512 of
-// k) at a time, and the epilogue warps add the chunks in registers with rounding
+// not below a binary32 one's: there the tensor core sums 512 of k
+// at a time, and the epilogue warps add the chunks in registers with rounding
 // to nearest, while the next chunk is made.
-constexpr int kChunk = 8;
+constexpr int kChunk64 = 8;
 constexpr int kGroupM = 8;  // row tiles that share the columns' tiles in L2
 
 // A tile is BN columns wide and 128 rows high per block; in a pair each block
@@ -414,9 +414,14 @@ struct Shape {
     static constexpr int kARows = KIND == kSkinny ? kSkinnyRows : kBM;
     static constexpr int kBlocks = kIsPair ? 2 : 1, kRows = kBM * kBlocks, kBCols = BN / kBlocks;
     static constexpr int kABytes = kARows * kBK * 2, kBBytes = kBCols * kBK * 2;
-    static constexpr int kStageBytes = kABytes + kBBytes;
+    // Steps of 64 k a stage holds, side by side.  A round of the loading and of the
+    // issuing warp (wait, elect, instructions, commit) takes some 300 clocks
+    // whatever it moves, so the smaller tiles take two steps a round.
+    static constexpr int kSub = KIND == kPair && BN == 256 ? 1 : 2;
+    static_assert(kSub <= 2, "the last stage has one step or all");
+    static constexpr int kSubBytes = kABytes + kBBytes, kStageBytes = kSub * kSubBytes;
     // all of an SM's shared memory, or half of it where two blocks share an SM
-    static constexpr int kStages = KIND == kSkinny ? 9 : kIsSplit ? 4 : kStageBytes > 24576 ? 7 : 8;
+    static constexpr int kStages = (KIND == kSkinny ? 9 : kIsSplit ? 4 : kSubBytes > 24576 ? 7 : 8) / kSub;
     static constexpr int kBlocksPerSm = kIsSplit ? 2 : 1;
     // epilogue warps: four take the tile's 128 rows, and every further four share its columns
     static constexpr int kWarps = kBCols >= 128 ? 16 : 8, kCols = BN / (kWarps / 4), kThreads = (kWarps + 2) * 32;
@@ -424,6 +429,7 @@ struct Shape {
     static constexpr int kColumnBytes = 2 * kBCols * 4;  // column sums of the two halves of dy's rows
     // (the last stage of a skinny tile is read past its end)
     static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024 + 256 + kColumnBytes + (kBM - kARows) * kBK * 2;
+    static_assert(!kIsSplit || kStages * kStageBytes >= kBM * BN * 4, "room for a split tile's sums");
     static_assert(kSmem <= kMaxDynamicSmem && kWarps == kBCols / 16 * 2, "shared memory, warps for the column sums");
 };
 
@@ -432,7 +438,8 @@ struct Product {
     Epilogue ep;
     unsigned int *err;
     int64_t rows, cols;
-    int tiles_m, tiles_n, steps;  // steps of kBK along k
+    int tiles_m, tiles_n;
+    int k64, steps;               // 64s of k, and steps: stages along k
     int splits;                   // blocks that share a tile's steps
     // pairs: tiles from `whole` on, which would leave most SMs idle in a last
     // wave of their own, are made in `tail_parts` parts along k, each into its
@@ -547,6 +554,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
     using S = Shape<BN, KIND>;
     constexpr bool PAIR = S::kIsPair;
     constexpr bool kAmn = MODE == kWgrad, kBmn = MODE != kDgrad;
+    constexpr int kChunk = kChunk64 / S::kSub, kStepK = kBK * S::kSub;
     extern __shared__ unsigned char raw[];
     unsigned char *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     const uint32_t tiles = smem_addr(smem);
@@ -604,18 +612,25 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                 const uint32_t a = tiles + s * S::kStageBytes, b = a + S::kABytes;
                 const uint32_t bar = PAIR ? in_leader(full + 8 * s) : full + 8 * s;
                 if (elected()) {
-                    if (rank == 0) mbar_expect(full + 8 * s, S::kStageBytes * S::kBlocks);
-                    if constexpr (kAmn) {
+                    const int subs = S::kSub == 1 || (k + 1) * S::kSub <= p.k64 ? S::kSub : 1;  // of the last stage
+                    if (rank == 0) mbar_expect(full + 8 * s, subs * S::kSubBytes * S::kBlocks);
 #pragma unroll
-                        for (int j = 0; j < kBM / 64; ++j) tma_load<PAIR>(a + j * 8192, &p.a, row + j * 64, k * kBK, bar);
-                    } else {
-                        tma_load<PAIR>(a, &p.a, k * kBK, row, bar);
-                    }
-                    if constexpr (kBmn) {
+                    for (int u = 0; u < S::kSub; ++u) {
+                        if (u >= subs) break;
+                        const int at = k * kStepK + u * kBK;
+                        const uint32_t au = a + u * S::kSubBytes, bu = b + u * S::kSubBytes;
+                        if constexpr (kAmn) {
 #pragma unroll
-                        for (int j = 0; j < S::kBCols / 64; ++j) tma_load<PAIR>(b + j * 8192, &p.b, col + j * 64, k * kBK, bar);
-                    } else {
-                        tma_load<PAIR>(b, &p.b, k * kBK, col, bar);
+                            for (int j = 0; j < kBM / 64; ++j) tma_load<PAIR>(au + j * 8192, &p.a, row + j * 64, at, bar);
+                        } else {
+                            tma_load<PAIR>(au, &p.a, at, row, bar);
+                        }
+                        if constexpr (kBmn) {
+#pragma unroll
+                            for (int j = 0; j < S::kBCols / 64; ++j) tma_load<PAIR>(bu + j * 8192, &p.b, col + j * 64, at, bar);
+                        } else {
+                            tma_load<PAIR>(bu, &p.b, at, col, bar);
+                        }
                     }
                 }
                 __syncwarp();
@@ -632,8 +647,9 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
     } else if (warp == S::kWarps + 1) {  // tcgen05.mma
         if (rank == 0) {
             constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (kAmn ? 1u << 15 : 0) | (kBmn ? 1u << 16 : 0) | (BN / 8) << 17 | (S::kRows / 16) << 24;
-            // 16 of k further on in a stage, and a stage further on, in the descriptors' 16-byte units
-            constexpr uint32_t a_next = (kAmn ? 2048 : 32) >> 4, b_next = (kBmn ? 2048 : 32) >> 4, stage_next = S::kStageBytes >> 4;
+            // 16 of k further on in a stage, a stage and a 64 of k further on, in the descriptors' 16-byte units
+            constexpr uint32_t a_next = (kAmn ? 2048 : 32) >> 4, b_next = (kBmn ? 2048 : 32) >> 4, stage_next = S::kStageBytes >> 4,
+                               sub_next = S::kSubBytes >> 4;
             const uint64_t a0 = operand(tiles, kAmn ? 8192 : 16, 1024), b0 = operand(tiles + S::kABytes, kBmn ? 8192 : 16, 1024);
             int s = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
@@ -652,10 +668,16 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                         if (!ok) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                         if (elected()) {
+                            const int subs = S::kSub == 1 || (work.k_begin + k + 1) * S::kSub <= p.k64 ? S::kSub : 1;
 #pragma unroll
-                            for (int j = 0; j < kBK / 16; ++j)
-                                mma_bf16<PAIR>(tmem + acc * BN, a0 + s * stage_next + j * a_next, b0 + s * stage_next + j * b_next, idesc,
-                                               (F32 ? k % kChunk : k) > 0 || j > 0);
+                            for (int u = 0; u < S::kSub; ++u) {
+                                if (u >= subs) break;
+#pragma unroll
+                                for (int j = 0; j < kBK / 16; ++j) {
+                                    const uint64_t at = s * stage_next + u * sub_next;
+                                    mma_bf16<PAIR>(tmem + acc * BN, a0 + at + j * a_next, b0 + at + j * b_next, idesc, (F32 ? k % kChunk : k) > 0 || u > 0 || j > 0);
+                                }
+                            }
                             mma_commit<PAIR>(empty + 8 * s);
                             if (last) mma_commit<PAIR>(done + 8 * acc);
                         }
@@ -1108,6 +1130,7 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     p.tiles_m = p.rows > 0 ? (int)ceil_div<int64_t>(p.rows, S::kRows) : 1;  // no rows: column sums alone
     p.tiles_n = (int)ceil_div<int64_t>(p.cols, BN);
     p.splits = splits;
+    p.steps = (int)ceil_div<int64_t>(p.k64, S::kSub);
     cudaError_t e = cudaSuccess;
     if (p.steps > 0) {
         e = tensor_map(&p.a, a, MODE == kWgrad ? kBK : S::kARows);
@@ -1118,7 +1141,7 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     if (e != cudaSuccess) return e;
     const int cluster = S::kIsSplit ? splits : S::kBlocks;
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, most = S::kIsSplit ? tiles : sms / S::kBlocks;
-    const Tail tail = KIND == kPair && BN == kTailBN && p.partial ? tail_of(p.rows, p.cols, p.steps, sms) : Tail{0, 1};
+    const Tail tail = KIND == kPair && BN == kTailBN && p.partial ? tail_of(p.rows, p.cols, p.k64, sms) : Tail{0, 1};
     p.whole = (int)(tiles - tail.tiles);
     p.tail_parts = tail.parts;
     cudaLaunchConfig_t cfg = {};
@@ -1161,8 +1184,8 @@ cudaError_t launch_width(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     const bool skinny = MODE != kWgrad && p.rows <= kSkinnyRows;
     int splits = 1;
     while (splits < 8) {
-        const bool one_each = narrow * splits * 2 <= sms && p.steps >= 16 * splits;
-        const bool two_each = tm == 1 && narrow * splits <= sms && p.steps >= (skinny ? 8 : 32) * splits;
+        const bool one_each = narrow * splits * 2 <= sms && p.k64 >= 16 * splits;
+        const bool two_each = tm == 1 && narrow * splits <= sms && p.k64 >= (skinny ? 8 : 32) * splits;
         if (!one_each && !two_each) break;
         splits *= 2;
     }
@@ -1172,7 +1195,7 @@ cudaError_t launch_width(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     if (tm * ceil_div<int64_t>(p.cols, 128) <= sms / 2) return launch_tiles<MODE, 64, kSingle, F32>(p, a, b, sms, s);
     const bool few = tm * ceil_div<int64_t>(p.cols, 256) <= sms / 2;
     const bool one_wave = ceil_div<int64_t>(p.rows, 2 * kBM) * ceil_div<int64_t>(p.cols, 128) <= sms / 2;  // of pairs
-    if (p.steps <= 4 || (few && (tm == 1 || !one_wave))) return launch_tiles<MODE, 128, kSingle, F32>(p, a, b, sms, s);
+    if (p.k64 <= 4 || (few && (tm == 1 || !one_wave))) return launch_tiles<MODE, 128, kSingle, F32>(p, a, b, sms, s);
     if (few) return launch_tiles<MODE, 128, kPair, F32>(p, a, b, sms, s);
     return launch_tiles<MODE, 256, kPair, F32>(p, a, b, sms, s);
 }
@@ -1188,7 +1211,7 @@ cudaError_t launch_product(const Mat &a, const Mat &b, int64_t rows, int64_t col
     p.ep.q_aligned = reinterpret_cast<uintptr_t>(ep.q) % 32 == 0;
     p.rows = rows;
     p.cols = cols;
-    p.steps = rows > 0 ? (int)ceil_div<int64_t>(k, kBK) : 0;
+    p.k64 = rows > 0 ? (int)ceil_div<int64_t>(k, kBK) : 0;
     p.db = db;
     p.dy = static_cast<const uint16_t *>(b.data);
     p.ld_dy = b.ld;
