@@ -264,6 +264,12 @@ __device__ __forceinline__ bool phase_over(uint32_t bar, uint32_t parity) {
                  : "=r"(over) : "r"(bar), "r"(parity) : "memory");
     return over;
 }
+__device__ __forceinline__ bool phase_seen(uint32_t bar, uint32_t parity) {
+    uint32_t over;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(over) : "r"(bar), "r"(parity) : "memory");
+    return over;
+}
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
     if (phase_over(bar, parity)) return true;
     const uint64_t t0 = global_ns();
@@ -651,32 +657,34 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
             constexpr uint32_t a_next = (kAmn ? 2048 : 32) >> 4, b_next = (kBmn ? 2048 : 32) >> 4, stage_next = S::kStageBytes >> 4,
                                sub_next = S::kSubBytes >> 4;
             const uint64_t a0 = operand(tiles, kAmn ? 8192 : 16, 1024), b0 = operand(tiles + S::kABytes, kBmn ? 8192 : 16, 1024);
+            const bool lead = elected();
             int s = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
+            bool landed = false;  // whether stage s is known to have
             for (int unit = unit0; unit < unit_count && ok; unit += unit_step) {
                 const Work work = work_at<KIND>(p, unit);
                 const int steps = work.k_end - work.k_begin;
                 for (int k = 0; k < steps || k == 0; ++k) {
-                    if (F32 ? k % kChunk == 0 : k == 0) {  // a new sum
+                    const int in_sum = F32 ? k % kChunk : k;
+                    if (in_sum == 0) {  // a new sum
                         ok = __all_sync(0xffffffffu, wait(freed + 8 * acc, acc_phase ^ 1));
                         if (!ok) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     }
-                    const bool last = k + 1 >= steps || (F32 && k % kChunk == kChunk - 1);
+                    const bool last = k + 1 >= steps || (F32 && in_sum == kChunk - 1);
                     if (steps > 0) {
-                        ok = __all_sync(0xffffffffu, wait(full + 8 * s, phase));
-                        if (!ok) break;
-                        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                        if (elected()) {
-                            const int subs = S::kSub == 1 || (work.k_begin + k + 1) * S::kSub <= p.k64 ? S::kSub : 1;
+                        if (!landed) {
+                            ok = __all_sync(0xffffffffu, wait(full + 8 * s, phase));
+                            if (!ok) break;
+                        }
+                        if (lead) {
+                            const uint64_t a = a0 + s * stage_next, b = b0 + s * stage_next;
+                            const uint32_t sum = tmem + acc * BN;
 #pragma unroll
-                            for (int u = 0; u < S::kSub; ++u) {
-                                if (u >= subs) break;
+                            for (int j = 0; j < kBK / 16; ++j) mma_bf16<PAIR>(sum, a + j * a_next, b + j * b_next, idesc, in_sum > 0 || j > 0);
+                            if (S::kSub > 1 && (work.k_begin + k + 1) * S::kSub <= p.k64) {  // not the last half of a stage
 #pragma unroll
-                                for (int j = 0; j < kBK / 16; ++j) {
-                                    const uint64_t at = s * stage_next + u * sub_next;
-                                    mma_bf16<PAIR>(tmem + acc * BN, a0 + at + j * a_next, b0 + at + j * b_next, idesc, (F32 ? k % kChunk : k) > 0 || u > 0 || j > 0);
-                                }
+                                for (int j = 0; j < kBK / 16; ++j) mma_bf16<PAIR>(sum, a + sub_next + j * a_next, b + sub_next + j * b_next, idesc, 1);
                             }
                             mma_commit<PAIR>(empty + 8 * s);
                             if (last) mma_commit<PAIR>(done + 8 * acc);
@@ -685,15 +693,17 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                             s = 0;
                             phase ^= 1;
                         }
-                    } else if (elected()) {
+                        // the next stage is looked at while these products run
+                        landed = __all_sync(0xffffffffu, phase_seen(full + 8 * s, phase));
+                    } else if (lead) {
                         mma_commit<PAIR>(done + 8 * acc);
                     }
-                    __syncwarp();
                     if (last) flip(acc, acc_phase);
                 }
             }
+            __syncwarp();
             // TMEM must outlive the products, also where a wait gave up
-            if (elected()) {
+            if (lead) {
                 if constexpr (PAIR)
                     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(drained) : "memory");
                 else
