@@ -31,9 +31,9 @@ namespace {
 enum Mode { kForward = 0, kDgrad = 1, kWgrad = 2 };
 
 // How blocks share tiles: one tile a block, one for a pair of blocks that work
-// as one tensor core, or one for a cluster that splits k.
-// kSkinny is kSplit for up to kSkinnyRows rows.
-enum Kind { kSingle = 0, kPair = 1, kSplit = 2, kSkinny = 3 };
+// as one tensor core, or one for a cluster that splits k, of single blocks or of
+// pairs.  kSkinny is kSplit for up to kSkinnyRows rows.
+enum Kind { kSingle = 0, kPair = 1, kSplit = 2, kSkinny = 3, kPairSplit = 4 };
 constexpr int kSkinnyRows = 16;
 
 // ---------------------------------------------------------------------------
@@ -46,8 +46,10 @@ struct Epilogue {
     int8_t *q;   // forward: the checkpoint of z, written; dgrad: read
     uint8_t *e;
     int64_t ldo, ldr, groups;
-    int out_f32, bias_f32, res_f32, act;
-    int rows_aligned, bias_aligned, q_aligned;  // rows of out and res, bias, q: on 32-byte boundaries
+    int bias_f32, res_f32, act;
+    // 32: rows of out and res on 32-byte boundaries; 16: bf16 rows of out alone, on 16-byte ones; 0: others
+    int rows_aligned;
+    int bias_aligned, q_aligned;  // on 32-byte boundaries
 };
 
 // v += the 32 values from p on
@@ -86,6 +88,41 @@ __device__ __forceinline__ void transpose32(float (&v)[32], int lane) {
     }
 }
 
+// The 32 values of a lane's row lie in N pieces of 16 bytes; N neighbouring
+// lanes trade theirs: lane l's piece i becomes piece l % N of the i-th of their
+// rows.  Doing it again takes it back.
+template <int N>
+__device__ __forceinline__ void trade(uint32_t (&w)[4 * N], int lane) {
+#pragma unroll
+    for (int s = 1; s < N; s *= 2) {
+        const bool high = lane & s;
+#pragma unroll
+        for (int j = 0; j < 4 * N; ++j) {
+            if (j / 4 & s) continue;
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w[j] : w[j + 4 * s], s);
+            if (high)
+                w[j] = got;
+            else
+                w[j + 4 * s] = got;
+        }
+    }
+}
+
+// 32 columns of bf16 rows on 16-byte boundaries, a row a lane: `rows` rows and
+// `pieces` pieces of 16 bytes of each are there.  An access takes 8 rows whole:
+// a lane's sectors would be shared with its row's next columns.
+__device__ __forceinline__ void store_pieces(uint16_t *p, int64_t ld, int rows, int pieces, const float (&v)[32], int lane) {
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = pack2(v[2 * j], v[2 * j + 1]);
+    trade<4>(w, lane);
+    const int r0 = lane / 4 * 4, c = lane % 4;
+    p += r0 * ld + 8 * c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (r0 + i < rows && c < pieces) *reinterpret_cast<uint4 *>(p + i * ld) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
 __device__ __forceinline__ float load_any(const void *p, int64_t i, int f32) {
     return f32 ? static_cast<const float *>(p)[i] : bf16_bits_to_f32(static_cast<const uint16_t *>(p)[i]);
 }
@@ -107,12 +144,14 @@ __device__ __forceinline__ void add_column(const T *p, int64_t ld, int rows, flo
 // multiple of 32, so one checkpoint group) and row row0 on, a row a lane;
 // `count` columns and `rows` rows of them exist.  The sums of columns that do
 // not exist are not looked at: they are zero, or NaN where A's row holds an
-// infinity.  Each lane reads and writes its row by whole sectors; rows that
+// infinity.  Each lane reads and writes its row by whole sectors.  Rows that
 // start elsewhere, and the last columns, are taken crosswise, so that the lanes
-// of an access are neighbours (one lane a row cost 568 x 3688 x 2440 20 of its 44 us).
+// of an access are neighbours (one lane a row cost 568 x 3688 x 2440 20 of its
+// 44 us); where they start on 16-byte boundaries and the result is bf16, four
+// lanes trade pieces of their rows, which is less work (that product: 22.7 -> 20.9 us).
 // Returns the group's step byte (forward, with a checkpoint), which the caller
 // stores with its neighbours'.
-template <int MODE>
+template <int MODE, bool F32>
 __device__ __forceinline__ uint32_t finish32(const Epilogue &ep, int64_t row0, int rows, int64_t n0, int count, float (&v)[32]) {
     const int lane = threadIdx.x & 31;
     const int64_t row = row0 + lane;
@@ -176,7 +215,7 @@ __device__ __forceinline__ uint32_t finish32(const Epilogue &ep, int64_t row0, i
             });
         }
     }
-    if (count == 32 && ep.rows_aligned) {
+    if (count == 32 && ep.rows_aligned == 32) {
         if (lane < rows) {
             if (ep.res) {
                 if (ep.res_f32)
@@ -184,26 +223,24 @@ __device__ __forceinline__ uint32_t finish32(const Epilogue &ep, int64_t row0, i
                 else
                     add32<false>(static_cast<const uint16_t *>(ep.res) + row * ep.ldr + n0, v);
             }
-            char *p = static_cast<char *>(ep.out) + (row * ep.ldo + n0) * (ep.out_f32 ? 4 : 2);
-            uint32_t w[8];
-            if (ep.out_f32) {
+            char *p = static_cast<char *>(ep.out) + (row * ep.ldo + n0) * (F32 ? 4 : 2);
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
+            for (int g = 0; g < (F32 ? 4 : 2); ++g) {
+                uint32_t w[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[8 * g + k]);
-                    store_sector(p + 32 * g, w);
-                }
-            } else {
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) w[k] = pack2(v[16 * g + 2 * k], v[16 * g + 2 * k + 1]);
-                    store_sector(p + 32 * g, w);
-                }
+                for (int k = 0; k < 8; ++k) w[k] = F32 ? __float_as_uint(v[8 * g + k]) : pack2(v[16 * g + 2 * k], v[16 * g + 2 * k + 1]);
+                store_sector(p + 32 * g, w);
             }
         }
         __syncwarp();
         return step_byte;
+    }
+    if constexpr (!F32) {
+        if (count % 8 == 0 && ep.rows_aligned == 16) {
+            store_pieces(static_cast<uint16_t *>(ep.out) + row0 * ep.ldo + n0, ep.ldo, rows, count / 8, v, lane);
+            __syncwarp();
+            return step_byte;
+        }
     }
     transpose32(v, lane);  // v[i]: row row0 + i, column n0 + lane
     if (lane < count) {
@@ -218,7 +255,7 @@ __device__ __forceinline__ uint32_t finish32(const Epilogue &ep, int64_t row0, i
         for (int i = 0; i < 32; ++i) {
             if (i >= rows) break;
             const int64_t at = (row0 + i) * ep.ldo + n0 + lane;
-            if (ep.out_f32)
+            if constexpr (F32)
                 static_cast<float *>(ep.out)[at] = v[i];
             else
                 static_cast<uint16_t *>(ep.out)[at] = (uint16_t)f32_to_bf16_bits(v[i]);
@@ -286,14 +323,19 @@ __device__ __forceinline__ bool elected() {
     asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
     return one;
 }
-// the same shared-memory place in another block of the cluster, and in a
-// pair's first
+// the same shared-memory place in another block of the cluster, and in the
+// first of this block's pair
 __device__ __forceinline__ uint32_t in_block(uint32_t addr, int rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ uint32_t in_leader(uint32_t addr) { return in_block(addr, 0); }
+__device__ __forceinline__ int cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return (int)r;
+}
+__device__ __forceinline__ uint32_t in_leader(uint32_t addr) { return in_block(addr, cluster_rank() & ~1); }
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -303,7 +345,7 @@ __device__ __forceinline__ void cluster_sync() {
 }
 // PAIR: two blocks of a cluster on neighbouring SMs work as one tensor core
 // (cta_group::2).  The loads of both count on the first one's barrier, and a
-// commit reaches the same barrier in both.
+// commit reaches the same barrier in both (`blocks`: a bit for each in the cluster).
 template <bool PAIR>
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
     if constexpr (PAIR)
@@ -314,9 +356,9 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
                      ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 template <bool PAIR>
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
+__device__ __forceinline__ void mma_commit(uint32_t bar, [[maybe_unused]] uint16_t blocks = 0) {
     if constexpr (PAIR)
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar), "h"((uint16_t)3)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar), "h"(blocks)
                      : "memory");
     else
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -414,7 +456,7 @@ constexpr int kGroupM = 8;  // row tiles that share the columns' tiles in L2
 // holds its own rows of A and half of B's columns, which the two share.
 template <int BN, int KIND>
 struct Shape {
-    static constexpr bool kIsPair = KIND == kPair, kIsSplit = KIND == kSplit || KIND == kSkinny;
+    static constexpr bool kIsPair = KIND == kPair || KIND == kPairSplit, kIsSplit = KIND == kSplit || KIND == kSkinny || KIND == kPairSplit;
     // Rows of A that are loaded.  For a few rows, only those: the tensor core
     // reads 128 all the same, whatever lies there, into sums that nothing uses.
     static constexpr int kARows = KIND == kSkinny ? kSkinnyRows : kBM;
@@ -423,12 +465,12 @@ struct Shape {
     // Steps of 64 k a stage holds, side by side.  A round of the loading and of the
     // issuing warp (wait, elect, instructions, commit) takes some 300 clocks
     // whatever it moves, so the smaller tiles take two steps a round.
-    static constexpr int kSub = KIND == kPair && BN == 256 ? 1 : 2;
+    static constexpr int kSub = kIsPair && BN == 256 ? 1 : 2;
     static_assert(kSub <= 2, "the last stage has one step or all");
     static constexpr int kSubBytes = kABytes + kBBytes, kStageBytes = kSub * kSubBytes;
     // all of an SM's shared memory, or half of it where two blocks share an SM
-    static constexpr int kStages = (KIND == kSkinny ? 9 : kIsSplit ? 4 : kSubBytes > 24576 ? 7 : 8) / kSub;
-    static constexpr int kBlocksPerSm = kIsSplit ? 2 : 1;
+    static constexpr int kStages = (KIND == kSkinny ? 9 : KIND == kSplit ? 4 : kSubBytes > 24576 ? 7 : 8) / kSub;
+    static constexpr int kBlocksPerSm = kIsSplit && !kIsPair ? 2 : 1;
     // epilogue warps: four take the tile's 128 rows, and every further four share its columns
     static constexpr int kWarps = kBCols >= 128 ? 16 : 8, kCols = BN / (kWarps / 4), kThreads = (kWarps + 2) * 32;
     static constexpr int kTmemCols = 2 * BN;  // two tiles' sums: one is finished while the next is made
@@ -475,6 +517,19 @@ __device__ __forceinline__ void keep_sums(unsigned char *smem, int col, int row,
     float *to = reinterpret_cast<float *>(smem) + col * kBM + row;
 #pragma unroll
     for (int j = 0; j < 32; ++j) to[j * kBM] = v[j];
+}
+
+// The sums of a tile of a few rows lie row by row.  The rows' distance is an odd
+// number of 16 bytes, so the lanes' stores meet in no bank.
+template <int BN>
+__device__ __forceinline__ uint32_t sums_at(int row, int col) {
+    return (uint32_t)(row * (BN + 4) + col) * 4;
+}
+template <int BN>
+__device__ __forceinline__ void keep_rows(unsigned char *smem, int col, int row, const float (&v)[32]) {
+    float4 *to = reinterpret_cast<float4 *>(smem + sums_at<BN>(row, col));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) to[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
 }
 
 // 32 sums of a row of a tile's part, column by column
@@ -544,8 +599,8 @@ struct Work {
 };
 template <int KIND>
 __device__ __forceinline__ Work work_at(const Product &p, int unit) {
-    if (KIND == kSplit || KIND == kSkinny) {
-        const int part = blockIdx.x % p.splits;
+    if (KIND == kSplit || KIND == kSkinny || KIND == kPairSplit) {
+        const int part = KIND == kPairSplit ? blockIdx.x / 2 % p.splits : blockIdx.x % p.splits;
         return Work{unit, part, p.steps * part / p.splits, p.steps * (part + 1) / p.splits};
     }
     if (KIND == kPair && unit >= p.whole) {
@@ -572,7 +627,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int rank = PAIR ? blockIdx.x & 1 : 0;
     // the first unit of work and the distance to the next
-    const int share = S::kIsSplit ? p.splits : S::kBlocks;
+    const int share = (S::kIsSplit ? p.splits : 1) * S::kBlocks;
     const int unit0 = blockIdx.x / share, unit_step = gridDim.x / share;
 
     if (warp == S::kWarps) {
@@ -601,7 +656,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
     const uint32_t tmem = *tmem_slot;
     pdl_enter();
 
-    const int tile_count = p.tiles_m * p.tiles_n, unit_count = S::kIsPair ? p.whole + (tile_count - p.whole) * p.tail_parts : tile_count;
+    const int tile_count = p.tiles_m * p.tiles_n, unit_count = KIND == kPair ? p.whole + (tile_count - p.whole) * p.tail_parts : tile_count;
     bool ok = true;
     if (warp == S::kWarps) {  // TMA
         int s = 0;
@@ -658,6 +713,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                                sub_next = S::kSubBytes >> 4;
             const uint64_t a0 = operand(tiles, kAmn ? 8192 : 16, 1024), b0 = operand(tiles + S::kABytes, kBmn ? 8192 : 16, 1024);
             const bool lead = elected();
+            const uint16_t both = PAIR ? 3 << cluster_rank() : 0;  // the pair's blocks (this is its first)
             int s = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool landed = false;  // whether stage s is known to have
@@ -686,8 +742,8 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
 #pragma unroll
                                 for (int j = 0; j < kBK / 16; ++j) mma_bf16<PAIR>(sum, a + sub_next + j * a_next, b + sub_next + j * b_next, idesc, 1);
                             }
-                            mma_commit<PAIR>(empty + 8 * s);
-                            if (last) mma_commit<PAIR>(done + 8 * acc);
+                            mma_commit<PAIR>(empty + 8 * s, both);
+                            if (last) mma_commit<PAIR>(done + 8 * acc, both);
                         }
                         if (++s == S::kStages) {
                             s = 0;
@@ -696,7 +752,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                         // the next stage is looked at while these products run
                         landed = __all_sync(0xffffffffu, phase_seen(full + 8 * s, phase));
                     } else if (lead) {
-                        mma_commit<PAIR>(done + 8 * acc);
+                        mma_commit<PAIR>(done + 8 * acc, both);
                     }
                     if (last) flip(acc, acc_phase);
                 }
@@ -728,7 +784,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
             if (MODE == kWgrad && p.db && tm == 0 && work.part == 0)
                 column_sums<S>(p, (int64_t)tn * BN + rank * S::kBCols, reinterpret_cast<float *>(smem + S::kStages * S::kStageBytes + 256), warp, lane);
             // where a part's sums go, for its first column and this lane's row
-            const bool tail = S::kIsPair && unit >= p.whole;
+            const bool tail = KIND == kPair && unit >= p.whole;
             float *to = !tail ? nullptr
                               : p.partial + ((int64_t)(unit - p.whole) * BN + warp / 4 * S::kCols) * S::kRows + rank * kBM + warp % 4 * 32 + lane;
             if constexpr (F32) {
@@ -756,7 +812,12 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                 if (!ok) break;
                 if constexpr (S::kIsSplit) {
 #pragma unroll
-                    for (int g = 0; g < S::kCols / 32; ++g) keep_sums(smem, warp / 4 * S::kCols + g * 32, warp % 4 * 32 + lane, sum[g]);
+                    for (int g = 0; g < S::kCols / 32; ++g) {
+                        if constexpr (KIND != kSkinny)
+                            keep_sums(smem, warp / 4 * S::kCols + g * 32, warp % 4 * 32 + lane, sum[g]);
+                        else if (warp % 4 == 0 && lane < kSkinnyRows)
+                            keep_rows<BN>(smem, warp / 4 * S::kCols + g * 32, lane, sum[g]);
+                    }
                     continue;
                 }
                 if (tail) {
@@ -769,7 +830,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                 for (int g = 0; g < S::kCols / 32; ++g) {
                     const int64_t n0 = c0 + g * 32;
                     if (rows > 0 && n0 < p.cols)
-                        step_bytes |= finish32<MODE>(p.ep, row0, rows, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), sum[g]) << (8 * g);
+                        step_bytes |= finish32<MODE, F32>(p.ep, row0, rows, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), sum[g]) << (8 * g);
                 }
                 if (MODE == kForward && !S::kIsSplit && !tail && p.ep.q && row < p.rows && c0 < p.cols) store_steps<S::kCols>(p.ep, row, c0, step_bytes);
                 __syncwarp();
@@ -789,14 +850,17 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                         for (int j = 0; j < 32; ++j) v[j] = 0.0f;
                     }
                     if constexpr (S::kIsSplit) {
-                        keep_sums(smem, warp / 4 * S::kCols + g * 32, warp % 4 * 32 + lane, v);
+                        if constexpr (KIND != kSkinny)
+                            keep_sums(smem, warp / 4 * S::kCols + g * 32, warp % 4 * 32 + lane, v);
+                        else if (warp % 4 == 0 && lane < kSkinnyRows)
+                            keep_rows<BN>(smem, warp / 4 * S::kCols + g * 32, lane, v);
                         continue;
                     }
                     if (tail) {
                         keep_part<S::kRows>(to + g * 32 * S::kRows, v);
                         continue;
                     }
-                    if (rows > 0) step_bytes |= finish32<MODE>(p.ep, row0, rows, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v) << (8 * g);
+                    if (rows > 0) step_bytes |= finish32<MODE, F32>(p.ep, row0, rows, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v) << (8 * g);
                 }
                 if (MODE == kForward && !S::kIsSplit && !tail && p.ep.q && row < p.rows && c0 < p.cols) store_steps<S::kCols>(p.ep, row, c0, step_bytes);
                 release<PAIR>(freed_bar + 8 * acc, lane);
@@ -806,7 +870,56 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
     }
     if (!ok) atomicOr(p.err, 1u);
     __syncwarp();
-    if constexpr (S::kIsSplit) {
+    if constexpr (KIND == kSkinny) {
+        // Every block's sums lie in its shared memory; the blocks share the work
+        // of adding and finishing them, 32 columns of 32 / splits rows at a time.
+        // Eight lanes read 128 bytes of a row of one split, and a lane's eight
+        // reads are all on their way at once; then the splits are added across
+        // the lanes, in a fixed order, and each lane gets its row.  With the first
+        // block alone reading, a row a lane and four bytes at a time as below,
+        // 16 x 2048 x 2048 took 8.2 us instead of 6.3.  (The 128 rows of a
+        // whole tile are better read that way: this one's exchanges between
+        // lanes then cost more than the reads, 7.3 against 6.5 us at 256 x 1024 x 1024.)
+        cluster_sync();
+        const int part = blockIdx.x % p.splits, per_task = 32 / p.splits, tasks = BN / 32 * (S::kARows / per_task);
+        int tm, tn;
+        tile_at(p, unit0, &tm, &tn);
+        const int sub = lane / 8, q0 = p.splits == 2 ? sub / 2 : sub, r0 = p.splits == 2 ? sub % 2 * 8 : 0;
+        for (int t = part + warp * p.splits; t < tasks && warp < S::kWarps && ok; t += S::kWarps * p.splits) {
+            const int g = t % (BN / 32), in_tile = t / (BN / 32) * per_task;
+            const int64_t row0 = (int64_t)tm * kBM + in_tile, n0 = (int64_t)tn * BN + g * 32;
+            if (row0 >= p.rows || n0 >= p.cols) continue;
+            const int rows = p.rows - row0 < per_task ? (int)(p.rows - row0) : per_task;
+            const uint32_t from = tiles + sums_at<BN>(in_tile + r0, g * 32 + lane % 8 * 4);
+            const uint32_t one = in_block(from, q0), two = p.splits == 8 ? in_block(from, (q0 + 4)) : one;
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {  // with eight splits four rows of each of two, else eight rows of one
+                const uint32_t at = p.splits == 8 ? (i < 4 ? one : two) + sums_at<BN>(i % 4, 0) : one + sums_at<BN>(i, 0);
+                asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3]) : "r"(at) : "memory");
+            }
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]);
+            if (p.splits == 8) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] += v[j + 16];
+            }
+            if (p.splits > 2) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], 8);
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j] + __shfl_xor_sync(0xffffffffu, v[j], 16));
+            trade<8>(w, lane);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]);
+            const uint32_t step_byte = finish32<MODE, F32>(p.ep, row0, rows, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
+            if (MODE == kForward && p.ep.q && lane < rows) store_steps<32>(p.ep, row0 + lane, n0, step_byte);
+        }
+        __syncwarp();
+    } else if constexpr (S::kIsSplit) {
         // every block's sums lie in its shared memory: each block adds and
         // finishes its share of the rows, the splits in their order
         cluster_sync();
@@ -814,15 +927,15 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
         const int g = warp / per_group, at0 = warp % per_group * 32;
         int tm, tn;
         tile_at(p, unit0, &tm, &tn);
-        const int in_tile = blockIdx.x % p.splits * height + at0;
-        const int64_t row0 = (int64_t)tm * kBM + in_tile, n0 = (int64_t)tn * BN + g * 32;
+        const int in_tile = blockIdx.x / S::kBlocks % p.splits * height + at0;
+        const int64_t row0 = (int64_t)tm * S::kRows + rank * kBM + in_tile, n0 = (int64_t)tn * BN + g * 32;
         int rows = height < 32 ? height : 32;
         if (p.rows - row0 < rows) rows = (int)(p.rows - row0);
         if (ok && g < BN / 32 && rows > 0 && n0 < p.cols) {
             float v[32];
             // (lanes past the block's rows read its neighbours' and drop them)
             for (int q = 0; q < p.splits; ++q) {
-                const uint32_t from = in_block(tiles + (g * 32 * kBM + (in_tile + lane) % kBM) * 4, q);
+                const uint32_t from = in_block(tiles + (g * 32 * kBM + (in_tile + lane) % kBM) * 4, q * S::kBlocks + rank);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
                     float x;
@@ -830,7 +943,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                     v[j] = q ? v[j] + x : x;
                 }
             }
-            const uint32_t step_byte = finish32<MODE>(p.ep, row0, rows, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
+            const uint32_t step_byte = finish32<MODE, F32>(p.ep, row0, rows, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
             if (MODE == kForward && p.ep.q && lane < rows) store_steps<32>(p.ep, row0 + lane, n0, step_byte);
         }
         __syncwarp();
@@ -849,7 +962,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
 // The tiles made in parts: the sums of the parts in their order, then the
 // epilogue.  A block a 32-column stripe of a tile, a warp 32 of its rows.
 constexpr int kTailBN = 256, kTailRows = 2 * kBM, kTailThreads = kTailRows;
-template <int MODE>
+template <int MODE, bool F32>
 __global__ void __launch_bounds__(kTailThreads) join_tail_kernel(const __grid_constant__ Product p) {
     pdl_enter();
     const int t = blockIdx.x / (kTailBN / 32), g = blockIdx.x % (kTailBN / 32);
@@ -867,7 +980,7 @@ __global__ void __launch_bounds__(kTailThreads) join_tail_kernel(const __grid_co
         for (int j = 0; j < 32; ++j) v[j] = q ? v[j] + x[j] : x[j];
     }
     const int rows = p.rows - row0 < 32 ? (int)(p.rows - row0) : 32, lane = threadIdx.x & 31;
-    const uint32_t step_byte = finish32<MODE>(p.ep, row0, rows, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
+    const uint32_t step_byte = finish32<MODE, F32>(p.ep, row0, rows, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
     if (MODE == kForward && p.ep.q && lane < rows) store_steps<32>(p.ep, row0 + lane, n0, step_byte);
 }
 
@@ -1149,7 +1262,7 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     }
     e = opt_in_smem<product_kernel<MODE, BN, KIND, F32>>((int)S::kSmem);
     if (e != cudaSuccess) return e;
-    const int cluster = S::kIsSplit ? splits : S::kBlocks;
+    const int cluster = splits * S::kBlocks;
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, most = S::kIsSplit ? tiles : sms / S::kBlocks;
     const Tail tail = KIND == kPair && BN == kTailBN && p.partial ? tail_of(p.rows, p.cols, p.k64, sms) : Tail{0, 1};
     p.whole = (int)(tiles - tail.tiles);
@@ -1171,7 +1284,7 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     e = cudaLaunchKernelEx(&cfg, product_kernel<MODE, BN, KIND, F32>, p);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess || tail.tiles == 0) return e;
-    return launch_pdl(join_tail_kernel<MODE>, tail.tiles * (kTailBN / 32), kTailThreads, 0, s, p);
+    return launch_pdl(join_tail_kernel<MODE, F32>, tail.tiles * (kTailBN / 32), kTailThreads, 0, s, p);
 }
 
 // The tile: the widest that leaves half of the SMs or more one.  What bounds
@@ -1188,10 +1301,45 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
 // 256 x 1024 x 1024 6.8 / 7.4, 512 x 2048 x 512 8.7 / 11.8, 128 x 4096 x 4096
 // 11.9 / 20.9, 16 x 2448 x 160 7.3 / 13.2; but 512 x 512 x 2048 7.0 / 5.3 with
 // only 4 steps each, and 300 x 3000 x 3000 20.2 / 18.3 with two blocks an SM.
+// With 48 steps or more, and 64 or more for four splits, pairs split better than
+// single blocks, as long as all of their clusters run at once (a GB300 holds 36
+// of two pairs, 15 of four).  Pairs' split / otherwise: 1024 x 4096 x 1024 12.2 / 15.3,
+// 256 x 8192 x 2048 15.2 / 20.5, 256 x 8192 x 1536 13.0 / 18.5, 512 x 8192 x 512
+// 12.3 / 14.7; but 1024 x 2048 x 1024 9.6 / 9.4 with 32 steps, and 512 x 3712 x 2560
+// 20.8 / 13.3 with 40 clusters.
+// how many clusters of `blocks` blocks of a kernel the device holds at once (0: not known)
+template <int MODE, int BN, int KIND, bool F32>
+int64_t clusters_at_once(int blocks) {
+    using S = Shape<BN, KIND>;
+    static std::atomic<int> known[64][9] = {};
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
+    n = known[dev][blocks].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    if (opt_in_smem<product_kernel<MODE, BN, KIND, F32>>((int)S::kSmem) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)blocks;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, product_kernel<MODE, BN, KIND, F32>, &cfg) != cudaSuccess) n = 0;
+    known[dev][blocks].store(n, std::memory_order_relaxed);
+    return n;
+}
 template <int MODE, bool F32>
 cudaError_t launch_width(Product &p, const Mat &a, const Mat &b, int sms, cudaStream_t s) {
     const int64_t tm = ceil_div<int64_t>(p.rows, kBM), narrow = tm * ceil_div<int64_t>(p.cols, 64);
     const bool skinny = MODE != kWgrad && p.rows <= kSkinnyRows;
+    const int64_t pairs = ceil_div<int64_t>(p.rows, 2 * kBM) * ceil_div<int64_t>(p.cols, 128);
+    if (tm > 1 && pairs * 4 <= sms)
+        for (int n = 4; n >= 2; n /= 2)
+            if (p.k64 >= (n == 4 ? 64 : 48) && pairs <= clusters_at_once<MODE, 128, kPairSplit, F32>(2 * n))
+                return launch_tiles<MODE, 128, kPairSplit, F32>(p, a, b, sms, s, n);
     int splits = 1;
     while (splits < 8) {
         const bool one_each = narrow * splits * 2 <= sms && p.k64 >= 16 * splits;
@@ -1216,7 +1364,10 @@ cudaError_t launch_product(const Mat &a, const Mat &b, int64_t rows, int64_t col
                            Workspace *space, cudaStream_t s, float *db = nullptr, int db_add = 0) {
     Product p = {};
     p.ep = ep;
-    p.ep.rows_aligned = out.aligned(32) && (res.empty() || res.aligned(32));
+    if (out.aligned(32) && (res.empty() || res.aligned(32)))
+        p.ep.rows_aligned = 32;
+    else if (out.esz == 2 && res.empty() && out.aligned(16))
+        p.ep.rows_aligned = 16;
     p.ep.bias_aligned = bias.aligned(32);
     p.ep.q_aligned = reinterpret_cast<uintptr_t>(ep.q) % 32 == 0;
     p.rows = rows;
@@ -1234,7 +1385,7 @@ cudaError_t launch_product(const Mat &a, const Mat &b, int64_t rows, int64_t col
     const int64_t tm = ceil_div<int64_t>(rows, kBM), part_bytes = tail_bytes(rows, cols, k, sms);
     if (tm * ceil_div<int64_t>(cols, 64) >= kMaxExtent) return cudaErrorInvalidValue;
     if (part_bytes > 0) p.partial = static_cast<float *>(space->take(part_bytes));  // without room: tiles whole
-    return ep.out_f32 ? launch_width<MODE, true>(p, a, b, sms, s) : launch_width<MODE, false>(p, a, b, sms, s);
+    return out.esz == 4 ? launch_width<MODE, true>(p, a, b, sms, s) : launch_width<MODE, false>(p, a, b, sms, s);
 }
 
 // the checkpoint's two arrays as matrices
@@ -1308,7 +1459,7 @@ ra_status ra_linear(const void *x, int64_t ld_x, const void *w, int64_t ld_w, in
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = launch_layouts(Layouts{layout_of(mx, a), layout_of(mw, b)}, s);
     if (e != cudaSuccess) return cuda_status(e);
-    const Epilogue ep{y, bias, residual, save_q, save_e, ld_y, ld_res, ceil_div<int64_t>(n, kGroup), y_dtype == RA_F32, bias_dtype == RA_F32,
+    const Epilogue ep{y, bias, residual, save_q, save_e, ld_y, ld_res, ceil_div<int64_t>(n, kGroup), bias_dtype == RA_F32,
                       res_dtype == RA_F32, act, 0};
     return cuda_status(launch_product<kForward>(a, b, m, n, k, ep, my, mb, mr, &space, s));
 }
@@ -1340,7 +1491,7 @@ ra_status ra_linear_dgrad(const void *dy, int64_t ld_dy, const void *w, int64_t 
     const cudaError_t e = launch_layouts(Layouts{layout_of(md, a), layout_of(mw, b)}, s);
     if (e != cudaSuccess) return cuda_status(e);
     const Epilogue ep{dx, nullptr, residual, act ? const_cast<int8_t *>(z_q) : nullptr, const_cast<uint8_t *>(z_e), ld_dx, ld_res,
-                      ceil_div<int64_t>(k, kGroup), dx_dtype == RA_F32, 0, res_dtype == RA_F32, act, 0};
+                      ceil_div<int64_t>(k, kGroup), 0, res_dtype == RA_F32, act, 0};
     return cuda_status(launch_product<kDgrad>(a, b, m, k, n, ep, mx, Mat{nullptr, 0, 0, 0, 1}, mr, &space, s));
 }
 
@@ -1388,7 +1539,7 @@ ra_status ra_linear_wgrad(const void *x, int64_t ld_x, const int8_t *z_q, const 
         if (e != cudaSuccess || mw.empty()) return cuda_status(e);
         db = nullptr;
     }
-    const Epilogue ep{dw, nullptr, accumulate ? dw : nullptr, nullptr, nullptr, ld_dw, ld_dw, 0, dw_dtype == RA_F32, 0, dw_dtype == RA_F32, 0, 0};
+    const Epilogue ep{dw, nullptr, accumulate ? dw : nullptr, nullptr, nullptr, ld_dw, ld_dw, 0, 0, dw_dtype == RA_F32, 0, 0};
     const Mat none{nullptr, 0, 0, 0, 1};
     return cuda_status(launch_product<kWgrad>(a, b, k, n, m, ep, mw, none, accumulate ? mw : none, &space, s, db, accumulate));
 }

@@ -245,6 +245,69 @@ def test_last_tiles_made_in_parts(out_type):
     check(db, dy.double().sum(0), sum_bound(k) * dy.double().abs().sum(0))
 
 
+@pytest.mark.parametrize("out_type", [BF16, F32])
+@pytest.mark.parametrize("m,k,n", [(300, 4104, 328), (129, 4096, 1000), (257, 3210, 2081), (700, 5000, 96)])
+def test_pairs_that_split_k(m, k, n, out_type):
+    """Long sums into few tiles, two and four ways, in all three products: with every part of the epilogue."""
+    x, w = _normal(1, m, k), _normal(2, k, n, s=k ** -0.5)
+    bias, residual = _normal(3, n, dtype=F32), _normal(4, m, n)
+    kept, out = ra.Checkpoint8(m, n), Framed(m, n, out_type, 0, 8)
+    ra.ra_linear(x, w, bias=bias, act="gelu", residual=residual, save=kept, out=out.t)
+    z, y, size = _forward64(x, w, bias, "gelu", residual)
+    check(out.t, y, _forward_bound(k, z, y, size, out_type, residual))
+    out.intact("pairs split")
+    groups = -(-n // 32)
+    off = sum_bound(k + 1) * size
+    top = torch.nn.functional.pad(z.abs() + off, (0, groups * 32 - n)).view(m, groups, 32).amax(2).repeat_interleave(32, 1)[:, :n]
+    check(ra.ra_checkpoint8_unpack(kept, dtype=F32), z, top / 127.5 * (1 + 2.0 ** -20) + off)
+    assert torch.equal(ra.ra_linear(x, w, bias=bias, act="gelu", residual=residual, dtype=out_type), out.t)
+    wt = _normal(5, n, k, s=k ** -0.5)
+    z8 = ra.ra_checkpoint8_pack(_normal(6, m, n, s=2.0))
+    got = ra.ra_linear_dgrad(x, wt, saved=z8, act="silu", dtype=out_type)
+    zz = values64(z8.q, z8.e, n)
+    g, gsize = x.double() @ wt.double().t(), x.double().abs() @ wt.double().t().abs()
+    want = g * slope64(zz, "silu")
+    check(got, want, 1.13 * sum_bound(k) * gsize + 2.0 ** -20 * g.abs() * (1 + zz.abs()) + rounding(out_type) * want.abs())
+    a, dy = _normal(7, k, m), _normal(8, k, n)
+    dw, db = ra.ra_linear_wgrad(a, dy, dtype=out_type, bias_grad=True)
+    want, size = a.double().t() @ dy.double(), a.double().t().abs() @ dy.double().abs()
+    check(dw, want, sum_bound(k) * size + rounding(out_type) * want.abs())
+    check(db, dy.double().sum(0), sum_bound(k) * dy.double().abs().sum(0))
+
+
+@pytest.mark.parametrize("m", [1, 2, 3, 4, 5, 8, 9, 15, 16])
+@pytest.mark.parametrize("k", [512, 1100, 4096])
+def test_few_rows_split_k(m, k):
+    """Every share of up to 16 rows among two, four and eight splits, whole and ragged columns."""
+    for n in (64, 200, 2081):
+        x, w = _normal(m, m, k), _normal(n, k, n, s=k ** -0.5)
+        bias, residual = _normal(3, n), _normal(4, m, n, dtype=F32)
+        kept = ra.Checkpoint8(m, n)
+        for out_type in (BF16, F32):
+            out = Framed(m, n, out_type)
+            ra.ra_linear(x, w, bias=bias, act="silu", residual=residual, save=kept, out=out.t)
+            z, y, size = _forward64(x, w, bias, "silu", residual)
+            check(out.t, y, _forward_bound(k, z, y, size, out_type, residual))
+            out.intact("few rows")
+            groups = -(-n // 32)
+            off = sum_bound(k + 1) * size
+            top = torch.nn.functional.pad(z.abs() + off, (0, groups * 32 - n)).view(m, groups, 32).amax(2).repeat_interleave(32, 1)[:, :n]
+            check(ra.ra_checkpoint8_unpack(kept, dtype=F32), z, top / 127.5 * (1 + 2.0 ** -20) + off)
+
+
+@pytest.mark.parametrize("lead,gap", [(0, 0), (8, 0), (0, 8), (16, 8), (24, 24), (4, 4)])
+@pytest.mark.parametrize("n", [8, 40, 56, 328, 1000])
+def test_rows_on_16_byte_boundaries(lead, gap, n):
+    """Results whose rows start on 16-byte but not on 32-byte boundaries, with columns up to any multiple of 8."""
+    for m, k in ((37, 72), (300, 200), (16, 1024)):
+        x, w, bias = _normal(1, m, k), _normal(2, k, n, s=k ** -0.5), _normal(3, n, dtype=F32)
+        out = Framed(m, n, BF16, lead, gap)
+        ra.ra_linear(x, w, bias=bias, act="relu", out=out.t)
+        z, y, size = _forward64(x, w, bias, "relu", None)
+        check(out.t, y, _forward_bound(k, z, y, size, BF16, None))
+        out.intact("16-byte rows")
+
+
 def test_past_32_bit_offsets():
     """An output of more than 2^31 values, beside inputs whose last rows start beyond 2^31 bytes."""
     m, k, n = 70_000, 64, 32_000
