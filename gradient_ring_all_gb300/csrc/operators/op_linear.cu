@@ -15,9 +15,11 @@
 // A step of 64 k of a pair's 256 x 256 tile is 512 clocks of the tensor core and
 // 64 KB of loads; 7 such steps are in flight.  Large products run into the
 // power limit: 8192 x 2048 x 8192 144-150 us (1.83-1.9 PFLOP/s), 8192 x 8192 x
-// 2048 156-162 us, 8192^3 600 us on normal values and 495 us on zeros (2.2
+// 2048 145-162 us, 8192^3 635 us on normal values and 473 us on zeros (2.3
 // PFLOP/s at 2070 MHz).  Small ones are bound by the rate at which an SM takes
-// tiles in and by a launch's start: one 64-column step alone takes 3 us.
+// tiles in and by a launch's start: one 64-column step alone takes 3 us, of
+// which the first loads take 0.9 and the epilogue 0.7.  A single token's forward
+// product has a kernel of its own.
 #include <cuda.h>
 
 #include <cooperative_groups.h>
@@ -985,6 +987,94 @@ __global__ void __launch_bounds__(kTailThreads) join_tail_kernel(const __grid_co
 }
 
 // ---------------------------------------------------------------------------
+// a single row
+
+// The forward product of one row, a single token's: the weights are read once
+// and all else is latency, so the multiplications are the ordinary ones and
+// nothing of the tensor core is set up.  A block takes 64 columns and its share
+// of k, in rounds of kTokenRound; eight lanes read 128 bytes of a weight row, a
+// thread kTokenFlight rows at once.  The threads', the warps' and the cluster's sums
+// are added in fixed orders.
+constexpr int kTokenCols = 64, kTokenThreads = 256, kTokenFlight = 16, kTokenRound = kTokenThreads / 8 * kTokenFlight;
+struct Token {
+    const uint16_t *x, *w;
+    int64_t ld_w, cols, k, k_each;  // k_each: k of a block, whole rounds
+    Epilogue ep;
+};
+
+// `count` neighbouring bf16 values (none where it is not above 0), zeros after
+// them; eight in one access
+__device__ __forceinline__ uint4 load8(const uint16_t *p, int64_t count) {
+    if (count >= 8) return __ldg(reinterpret_cast<const uint4 *>(p));
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = (2 * i < count ? p[2 * i] : 0u) | (2 * i + 1 < count ? (uint32_t)p[2 * i + 1] : 0u) << 16;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(kTokenThreads, 2) token_kernel(const __grid_constant__ Token p) {
+    namespace cg = cooperative_groups;
+    __shared__ float part[kTokenThreads / 32][kTokenCols], sum[kTokenCols];
+    pdl_enter();
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int splits = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int64_t col0 = (int64_t)(blockIdx.x / splits) * kTokenCols, col = col0 + threadIdx.x % 8 * 8;
+    const int64_t end = p.k < (rank + 1) * p.k_each ? p.k : (rank + 1) * p.k_each;
+    float acc[8] = {};
+    for (int64_t k = rank * p.k_each + threadIdx.x / 8 * kTokenFlight; k < end; k += kTokenRound) {
+        uint4 w[kTokenFlight], x[kTokenFlight / 8];
+#pragma unroll
+        for (int u = 0; u < kTokenFlight; ++u) w[u] = load8(p.w + (k + u) * p.ld_w + col, k + u < end ? p.cols - col : 0);
+#pragma unroll
+        for (int u = 0; u < kTokenFlight / 8; ++u) x[u] = load8(p.x + k + 8 * u, end - k - 8 * u);
+#pragma unroll
+        for (int u = 0; u < kTokenFlight; ++u) {
+            float wf[8], xf[8];
+            unpack8(w[u], wf);
+            unpack8(x[u / 8], xf);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = fmaf(xf[u % 8], wf[j], acc[j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 8);
+        acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], 16);
+        if (lane < 8) part[warp][lane * 8 + j] = acc[j];
+    }
+    __syncthreads();
+    if (threadIdx.x < kTokenCols) {
+        float t = part[0][threadIdx.x];
+#pragma unroll
+        for (int w = 1; w < kTokenThreads / 32; ++w) t += part[w][threadIdx.x];
+        sum[threadIdx.x] = t;
+    }
+    cluster.sync();
+    // two warps of the cluster finish 32 columns each
+    const int g = splits > 1 ? rank : warp;
+    const int64_t n0 = col0 + g * 32;
+    if ((splits == 1 || warp == 0) && g < kTokenCols / 32 && n0 < p.cols) {
+        float t = 0.0f, v[32];
+        for (int q = 0; q < splits; ++q) t += *cluster.map_shared_rank(&sum[g * 32 + lane], q);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __shfl_sync(0xffffffffu, t, j);
+        const uint32_t step_byte = finish32<kForward, F32>(p.ep, 0, 1, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
+        if (p.ep.q && lane == 0) store_steps<32>(p.ep, 0, n0, step_byte);
+    }
+    cluster.sync();  // no block's memory goes while another may read it
+}
+
+// ---------------------------------------------------------------------------
 // operands that TMA cannot read where they lie
 
 // An operand to bring into the workspace, as bf16 rows on 32-byte boundaries:
@@ -1358,6 +1448,38 @@ cudaError_t launch_width(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     return launch_tiles<MODE, 256, kPair, F32>(p, a, b, sms, s);
 }
 
+// A single token's product: k among as many blocks as run at once, with a round
+// or more each.  With less than a round in all, or with more than four a block (which
+// waits for each round's reads before it asks for the next), the tensor cores' few rows do
+// better.  This kernel / those, us (weights in L2; from memory where two are given):
+// 2048 x 8192 6.4 / 9.5 (9.4 / 10.5), 8192 x 2048 6.5 / 9.2 (9.4 / 10.6), 2048 x
+// 2048 4.3 / 6.2, 512 x 512 3.7 / 5.2, 2048 x 32000 27 / 35; but 8192 x 8192, eight rounds,
+// 25.7 / 24.5, and 100 x 64 3.9 / 2.9.  Two rows at once were no better than there (11.4 / 9.5).
+int token_splits(int64_t cols, int64_t k, int sms) {
+    const int64_t tiles = ceil_div<int64_t>(cols, kTokenCols);
+    int splits = 1;
+    while (splits < 8 && tiles * splits * 2 <= 2 * (int64_t)sms && k >= 2 * splits * kTokenRound) splits *= 2;
+    return splits;
+}
+template <bool F32>
+cudaError_t launch_token(const Token &p, int splits, cudaStream_t s) {
+    const int64_t tiles = ceil_div<int64_t>(p.cols, kTokenCols);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * splits));
+    cfg.blockDim = dim3(kTokenThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = RA_PDL;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)splits;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, token_kernel<F32>, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
 // out (rows x cols) = epilogue(A B); a and b as they lie in memory
 template <int MODE>
 cudaError_t launch_product(const Mat &a, const Mat &b, int64_t rows, int64_t cols, int64_t k, Epilogue ep, const Mat &out, const Mat &bias, const Mat &res,
@@ -1384,6 +1506,13 @@ cudaError_t launch_product(const Mat &a, const Mat &b, int64_t rows, int64_t col
     if (e != cudaSuccess) return e;
     const int64_t tm = ceil_div<int64_t>(rows, kBM), part_bytes = tail_bytes(rows, cols, k, sms);
     if (tm * ceil_div<int64_t>(cols, 64) >= kMaxExtent) return cudaErrorInvalidValue;
+    if constexpr (MODE == kForward) {
+        Token t{static_cast<const uint16_t *>(a.data), static_cast<const uint16_t *>(b.data), b.ld, cols, k, 0, p.ep};
+        const int splits = token_splits(cols, k, sms);
+        t.k_each = ceil_div<int64_t>(ceil_div<int64_t>(k, splits), kTokenRound) * kTokenRound;
+        if (rows == 1 && k >= kTokenRound && t.k_each <= 4 * kTokenRound)
+            return out.esz == 4 ? launch_token<true>(t, splits, s) : launch_token<false>(t, splits, s);
+    }
     if (part_bytes > 0) p.partial = static_cast<float *>(space->take(part_bytes));  // without room: tiles whole
     return out.esz == 4 ? launch_width<MODE, true>(p, a, b, sms, s) : launch_width<MODE, false>(p, a, b, sms, s);
 }

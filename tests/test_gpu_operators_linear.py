@@ -295,6 +295,41 @@ def test_few_rows_split_k(m, k):
             check(ra.ra_checkpoint8_unpack(kept, dtype=F32), z, top / 127.5 * (1 + 2.0 ** -20) + off)
 
 
+@pytest.mark.parametrize("out_type", [BF16, F32])
+@pytest.mark.parametrize("k", [511, 512, 513, 2047, 2048, 4100, 16384, 16390])
+def test_a_single_token(k, out_type):
+    """The form for one row: rounds of k whole, cut short and more than it takes, and weights of every alignment."""
+    for n, lead, gap in ((1, 0, 0), (8, 0, 8), (67, 0, 0), (640, 8, 24), (1001, 1, 0)):
+        x, w = _framed(_normal(1, 1, k), lead, 0), _framed(_normal(n, k, n, s=k ** -0.5), lead, gap)
+        bias, residual = _normal(3, n, dtype=F32), _normal(4, 1, n)
+        kept, out = ra.Checkpoint8(1, n), Framed(1, n, out_type, lead, gap)
+        ra.ra_linear(x.t, w.t, bias=bias, act="gelu", residual=residual, save=kept, out=out.t)
+        z, y, size = _forward64(x.t, w.t, bias, "gelu", residual)
+        check(out.t, y, _forward_bound(k, z, y, size, out_type, residual))
+        out.intact("token")
+        groups = -(-n // 32)
+        off = sum_bound(k + 1) * size
+        top = torch.nn.functional.pad(z.abs() + off, (0, groups * 32 - n)).view(1, groups, 32).amax(2).repeat_interleave(32, 1)[:, :n]
+        check(ra.ra_checkpoint8_unpack(kept, dtype=F32), z, top / 127.5 * (1 + 2.0 ** -20) + off)
+        again = Framed(1, n, out_type, lead, gap)
+        ra.ra_linear(x.t, w.t, bias=bias, act="gelu", residual=residual, out=again.t)
+        assert torch.equal(again.t, out.t)
+
+
+def test_a_single_token_with_values_that_are_not_finite():
+    """An infinite or NaN weight reaches its own column alone, a value of x all of them."""
+    k, n = 2048, 200
+    x, w = _normal(1, 1, k), _normal(2, k, n)
+    clean = ra.ra_linear(x, w, dtype=F32)
+    w[700, 33], w[2047, 199], w[0, 0] = float("inf"), float("nan"), float("-inf")
+    got = ra.ra_linear(x, w, dtype=F32)
+    hit = torch.zeros(n, dtype=torch.bool, device="cuda")
+    hit[[0, 33, 199]] = True
+    assert torch.equal(got[0, ~hit], clean[0, ~hit]) and not bool(got[0, hit].isfinite().any())
+    x[0, 5] = float("nan")
+    assert bool(ra.ra_linear(x, w, dtype=F32).isnan().all())
+
+
 @pytest.mark.parametrize("lead,gap", [(0, 0), (8, 0), (0, 8), (16, 8), (24, 24), (4, 4)])
 @pytest.mark.parametrize("n", [8, 40, 56, 328, 1000])
 def test_rows_on_16_byte_boundaries(lead, gap, n):
