@@ -490,7 +490,7 @@ struct Product {
     int64_t rows, cols;
     int tiles_m, tiles_n;
     int k64, steps;               // 64s of k, and steps: stages along k
-    int splits;                   // blocks that share a tile's steps
+    int splits;                   // blocks, or pairs, that share a tile's steps
     // pairs: tiles from `whole` on, which would leave most SMs idle in a last
     // wave of their own, are made in `tail_parts` parts along k, each into its
     // own 256 x 256 of `partial` (column by column), and joined afterwards
@@ -1380,7 +1380,7 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
 // The tile: the widest that leaves half of the SMs or more one.  What bounds
 // the smaller products is the rate at which an SM takes tiles in, about 50 bytes
 // a clock, so pairs, which share B, do better than single blocks of one width:
-// 568 x 3688 x 2440 in 128 columns 22.2 / 25.9 us, in 256 29.4; 1024 x 4096 x
+// 512 x 3712 x 2560 in a pair's 128 columns 13.3 us, in its 256 21.7; 1024 x 4096 x
 // 4096 in 256 columns 24.4 us, in 128 34.0 / 42.2, in 64 75.  With a step or two
 // of k the results' writes are all, and single blocks of 128 columns have more
 // tiles finishing at once: 8192 x 64 x 4096 19.3 us, a pair's 256 columns 25.2.
