@@ -1377,26 +1377,6 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     return launch_pdl(join_tail_kernel<MODE, F32>, tail.tiles * (kTailBN / 32), kTailThreads, 0, s, p);
 }
 
-// The tile: the widest that leaves half of the SMs or more one.  What bounds
-// the smaller products is the rate at which an SM takes tiles in, about 50 bytes
-// a clock, so pairs, which share B, do better than single blocks of one width:
-// 512 x 3712 x 2560 in a pair's 128 columns 13.3 us, in its 256 21.7; 1024 x 4096 x
-// 4096 in 256 columns 24.4 us, in 128 34.0 / 42.2, in 64 75.  With a step or two
-// of k the results' writes are all, and single blocks of 128 columns have more
-// tiles finishing at once: 8192 x 64 x 4096 19.3 us, a pair's 256 columns 25.2.
-// Where even the narrowest tiles leave half of the SMs idle and k is
-// long enough, clusters of 2 to 8 blocks split it: the exchange of the sums
-// costs about what 8 steps do.  With one row tile, where the weights' stream is
-// what counts, up to two blocks an SM.  Split / whole, us (GB300, graph replay):
-// 256 x 1024 x 1024 6.8 / 7.4, 512 x 2048 x 512 8.7 / 11.8, 128 x 4096 x 4096
-// 11.9 / 20.9, 16 x 2448 x 160 7.3 / 13.2; but 512 x 512 x 2048 7.0 / 5.3 with
-// only 4 steps each, and 300 x 3000 x 3000 20.2 / 18.3 with two blocks an SM.
-// With 48 steps or more, and 64 or more for four splits, pairs split better than
-// single blocks, as long as all of their clusters run at once (a GB300 holds 36
-// of two pairs, 15 of four).  Pairs' split / otherwise: 1024 x 4096 x 1024 12.2 / 15.3,
-// 256 x 8192 x 2048 15.2 / 20.5, 256 x 8192 x 1536 13.0 / 18.5, 512 x 8192 x 512
-// 12.3 / 14.7; but 1024 x 2048 x 1024 9.6 / 9.4 with 32 steps, and 512 x 3712 x 2560
-// 20.8 / 13.3 with 40 clusters.
 // how many clusters of `blocks` blocks of a kernel the device holds at once (0: not known)
 template <int MODE, int BN, int KIND, bool F32>
 int64_t clusters_at_once(int blocks) {
@@ -1421,6 +1401,27 @@ int64_t clusters_at_once(int blocks) {
     known[dev][blocks].store(n, std::memory_order_relaxed);
     return n;
 }
+
+// The tile: the widest that leaves half of the SMs or more one.  What bounds
+// the smaller products is the rate at which an SM takes tiles in, about 50 bytes
+// a clock, so pairs, which share B, do better than single blocks of one width:
+// 512 x 3712 x 2560 in a pair's 128 columns 13.3 us, in its 256 21.7; 1024 x 4096 x
+// 4096 in 256 columns 24.4 us, in 128 34.0 / 42.2, in 64 75.  With a step or two
+// of k the results' writes are all, and single blocks of 128 columns have more
+// tiles finishing at once: 8192 x 64 x 4096 19.3 us, a pair's 256 columns 25.2.
+// Where even the narrowest tiles leave half of the SMs idle and k is
+// long enough, clusters of 2 to 8 blocks split it: the exchange of the sums
+// costs about what 8 steps do.  With one row tile, where the weights' stream is
+// what counts, up to two blocks an SM.  Split / whole, us (GB300, graph replay):
+// 256 x 1024 x 1024 6.8 / 7.4, 512 x 2048 x 512 8.7 / 11.8, 128 x 4096 x 4096
+// 11.9 / 20.9, 16 x 2448 x 160 7.3 / 13.2; but 512 x 512 x 2048 7.0 / 5.3 with
+// only 4 steps each, and 300 x 3000 x 3000 20.2 / 18.3 with two blocks an SM.
+// With 48 steps or more, and 64 or more for four splits, pairs split better than
+// single blocks, as long as all of their clusters run at once (a GB300 holds 36
+// of two pairs, 15 of four).  Pairs' split / otherwise: 1024 x 4096 x 1024 12.2 / 15.3,
+// 256 x 8192 x 2048 15.2 / 20.5, 256 x 8192 x 1536 13.0 / 18.5, 512 x 8192 x 512
+// 12.3 / 14.7; but 1024 x 2048 x 1024 9.6 / 9.4 with 32 steps, and 512 x 3712 x 2560
+// 20.8 / 13.3 with 40 clusters.
 template <int MODE, bool F32>
 cudaError_t launch_width(Product &p, const Mat &a, const Mat &b, int sms, cudaStream_t s) {
     const int64_t tm = ceil_div<int64_t>(p.rows, kBM), narrow = tm * ceil_div<int64_t>(p.cols, 64);
