@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThreadsCkpt) pack_scalar_kernel(const PackPar
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
             const int64_t c = (k * 4 + g) * kGroup + lane;
-            x[g] = c < p.cols ? to_f32<T>(__ldg(src + c)) : 0.0f;
+            x[g] = c < p.cols ? to_f32<T>(src[c]) : 0.0f;
         }
         uint32_t w = 0, e = 0;
 #pragma unroll

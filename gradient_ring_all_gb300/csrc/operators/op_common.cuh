@@ -120,7 +120,10 @@ template <>
 __device__ __forceinline__ uint16_t from_f32<uint16_t>(float v) { return (uint16_t)f32_to_bf16_bits(v); }
 
 // W consecutive elements as they lie in memory, so that many can be in flight
-// in few registers; aligned to the access width (at most 16 bytes an access)
+// in few registers; aligned to the access width (at most 16 bytes an access).
+// Ordinary loads, here and everywhere: the read-only path is for memory that
+// nobody writes while the kernel lives, and a kernel launched early lives while
+// its predecessor writes.
 template <class T, int W>
 struct Raw {
     static constexpr int kBytes = W * sizeof(T), kWords = kBytes < 4 ? 1 : kBytes / 4;
@@ -129,20 +132,20 @@ struct Raw {
         if constexpr (kBytes >= 16) {
 #pragma unroll
             for (int g = 0; g < kBytes / 16; ++g) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + g);
+                const uint4 v = reinterpret_cast<const uint4 *>(p)[g];
                 w[4 * g] = v.x;
                 w[4 * g + 1] = v.y;
                 w[4 * g + 2] = v.z;
                 w[4 * g + 3] = v.w;
             }
         } else if constexpr (kBytes == 8) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
             w[0] = v.x;
             w[1] = v.y;
         } else if constexpr (kBytes == 4) {
-            w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
         } else {
-            w[0] = __ldg(reinterpret_cast<const uint16_t *>(p));
+            w[0] = *reinterpret_cast<const uint16_t *>(p);
         }
     }
     __device__ __forceinline__ void zero() {
@@ -443,9 +446,10 @@ template <class T>
 __device__ __forceinline__ void unpack_groups(const PackParams &p, int64_t first, int64_t stride) {
     const int64_t total = p.rows * p.groups;
     for (int64_t u = first; u < total; u += stride) {
-        const uint4 q0 = __ldg(reinterpret_cast<const uint4 *>(p.q + u * kGroup)), q1 = __ldg(reinterpret_cast<const uint4 *>(p.q + u * kGroup) + 1);
+        const uint4 *q = reinterpret_cast<const uint4 *>(p.q + u * kGroup);
+        const uint4 q0 = q[0], q1 = q[1];
         const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-        const float step = step_value(__ldg(p.e + u));
+        const float step = step_value(p.e[u]);
         int64_t r, k;
         row_of(u, p.groups, total, &r, &k);
         float v[kGroup];
