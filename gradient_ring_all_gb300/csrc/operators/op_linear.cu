@@ -1629,7 +1629,8 @@ ra_status ra_linear_wgrad(const void *x, int64_t ld_x, const int8_t *z_q, const 
                           int64_t ld_dy, int64_t m, int64_t k, int64_t n, int accumulate, void *dw, int64_t ld_dw,
                           int dw_dtype, float *db, void *ws, size_t ws_bytes, void *stream) {
     const int wsz = esize(dw_dtype);
-    const bool from_kept = x == nullptr && (z_q != nullptr || z_e != nullptr);
+    // (an empty checkpoint's arrays may have no address)
+    const bool from_kept = x == nullptr && (z_q != nullptr || z_e != nullptr || (act != RA_ACT_NONE && (m == 0 || k == 0)));
     if (wsz == 0 || !act_ok(act) || (!from_kept && act != RA_ACT_NONE)) return RA_ERR_INVALID_ARG;
     if (x != nullptr && (z_q != nullptr || z_e != nullptr)) return RA_ERR_INVALID_ARG;
     const Mat mx{x, from_kept ? 0 : m, k, from_kept ? k : ld_x, 2}, md{dy, m, n, ld_dy, 2}, mw{dw, k, n, ld_dw, wsz};

@@ -148,8 +148,9 @@ ra_status ra_linear_dgrad(const void *dy, int64_t ld_dy, const void *w, int64_t 
  * ra_linear_wgrad -- dw = a^T dy and db = the column sums of dy.
  *   x         m x k, bf16: a = x; or NULL and
  *   z_q, z_e  the 8-bit checkpoint of z (m x k): a = act(z), recomputed here
- *             (act is RA_ACT_NONE with x).  With RA_ACT_NONE a is exact; else
- *             act(z) is rounded to bf16 for the tensor cores
+ *             (act is RA_ACT_NONE with x); an empty checkpoint's pointers may
+ *             be NULL too.  With RA_ACT_NONE a is exact; else act(z) is
+ *             rounded to bf16 for the tensor cores
  *   dy        m x n, bf16
  *   dw        k x n of dw_dtype; accumulate != 0 adds to it (micro-batches)
  *   db        n binary32 values, or NULL; accumulate holds for it too

@@ -1,0 +1,58 @@
+"""Edges of the operators: empty checkpoints, sums with no rows, a bias
+gradient alone."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import gradient_ring_all_gb300 as ra
+from operator_reference import check, sum_bound
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+ACTS = ["none", "relu", "gelu", "silu"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from gradient_ring_all_gb300 import build
+    build.build()
+    ra.load()
+
+
+def _normal(seed, *shape, dtype=BF16, s=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * s).to(dtype)
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("out_type", [BF16, F32])
+def test_weight_gradient_of_no_tokens(act, out_type):
+    """No rows: zero sums, and accumulated ones stay."""
+    k, n = 24, 40
+    kept, dy = ra.Checkpoint8(0, k), torch.empty(0, n, dtype=BF16, device="cuda")
+    dw, db = ra.ra_linear_wgrad(kept, dy, act=act, dtype=out_type, bias_grad=True)
+    assert dw.shape == (k, n) and not bool(dw.any()) and db.shape == (n,) and not bool(db.any())
+    held, hb = torch.full((k, n), 2.0, dtype=out_type, device="cuda"), torch.full((n,), 3.0, device="cuda")
+    ra.ra_linear_wgrad(kept, dy, act=act, out=held, bias_grad=hb, accumulate=True)
+    assert bool((held == 2).all()) and bool((hb == 3).all())
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("m", [1, 100, 512, 513, 3000])
+@pytest.mark.parametrize("n", [40, 67])
+def test_bias_gradient_alone(act, m, n):
+    """An input without columns leaves the column sums of dy, on both sides of the number of rows at which they get a launch
+    of their own; accumulated they add."""
+    dy = _normal(m, m, n)
+    want, bound = dy.double().sum(0), sum_bound(m) * dy.double().abs().sum(0)
+    kept = ra.Checkpoint8(m, 0)
+    dw, db = ra.ra_linear_wgrad(kept, dy, act=act, bias_grad=True)
+    assert dw.shape == (0, n)
+    check(db, want, bound)
+    ra.ra_linear_wgrad(kept, dy, act=act, out=dw, bias_grad=db, accumulate=True)
+    check(db, 2 * want, 2 * bound + 2.0 ** -23 * want.abs())
+    if act == "none":
+        _, again = ra.ra_linear_wgrad(torch.empty(m, 0, dtype=BF16, device="cuda"), dy, bias_grad=True)
+        check(again, want, bound)
