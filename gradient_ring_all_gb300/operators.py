@@ -8,7 +8,8 @@ each call says, whose rows are contiguous (any row stride, so slices of a
 larger tensor work); the outputs are allocated here unless ``out`` is given.
 Work goes to the current torch stream unless ``stream`` is given; what is
 allocated here is allocated for that stream, and a tensor that another stream
-made or still uses needs the usual event or ``record_stream``.
+made or still uses needs the usual event or ``record_stream``.  The tensors
+have to be on the current device: the library launches there.
 """
 from __future__ import annotations
 
@@ -28,6 +29,7 @@ _CODE = {_F32: 0, _BF16: 1}
 _ID_BYTES = {torch.int32: 4, torch.int64: 8}
 _CUDA = torch.device("cuda")  # the current device
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
 _declared = None
@@ -62,6 +64,13 @@ def _load():
 # ---------------------------------------------------------------------------
 # marshalling (it runs on every call, and a small call takes the GPU less time
 # than the host: one look at each attribute)
+
+
+def _device(dev):
+    """The number of the call's device (-1: the host, which the tensors' own checks refuse)."""
+    if dev >= 0 and dev != _current_device():
+        raise ValueError("the call's tensors are on cuda:%d, the current device is cuda:%d" % (dev, _current_device()))
+    return dev
 
 
 def _matrix(t, what, dev, dtype, shape):
@@ -240,7 +249,7 @@ def ra_checkpoint8_pack(x, out=None, stream=None) -> Checkpoint8:
     """The 8-bit form of the matrix x (float32 or bfloat16): at most half a
     step, 1/127.5 of a group's largest magnitude, off."""
     rows, cols = s = _shape(x, "x")
-    dev = x.get_device()
+    dev = _device(x.get_device())
     p, ld, code = _matrix(x, "x", dev, None, s)
     if out is None:
         if stream is None:
@@ -260,7 +269,7 @@ def ra_checkpoint8_unpack(kept, act="none", dtype=None, out=None, stream=None):
     (bfloat16 unless given, exact without an activation)."""
     if not isinstance(kept, Checkpoint8):
         raise TypeError("kept must be a Checkpoint8")
-    dev, rows, cols = kept._dev, kept.rows, kept.cols
+    dev, rows, cols = _device(kept._dev), kept.rows, kept.cols
     out, p, ld, code = _output(out, rows, cols, dtype or (_BF16 if out is None else None), kept, dev, stream)
     _check(_load().ra_checkpoint8_unpack(kept._pq, kept._pe, rows, cols, _act(act), p, ld, code, _stream_of(stream, dev)),
            "ra_checkpoint8_unpack")
@@ -275,7 +284,7 @@ def ra_embedding_lookup(table, ids, scale: float = 1.0, out=None, stream=None):
     """scale * table[ids]: one row per id (ids of any shape, flattened), zeros
     for an id outside the table (padding)."""
     vocab, d = s = _shape(table, "table")
-    dev = table.get_device()
+    dev = _device(table.get_device())
     pt, ldt, code = _matrix(table, "table", dev, None, s)
     pi, size, count = _ids(ids, dev)
     out, po, ldo, _ = _output(out, count, d, table.dtype, table, dev, stream)
@@ -291,7 +300,7 @@ def ra_embedding_grad(grad, ids, vocab: int, scale: float = 1.0, dtype=None, out
     `out` may be a view of a worker's flat gradient; accumulate adds to it.
     dtype: the new output's type (grad's unless given)."""
     rows, d = s = _shape(grad, "grad")
-    dev = grad.get_device()
+    dev = _device(grad.get_device())
     pg, ldg, gcode = _matrix(grad, "grad", dev, None, s)
     pi, size, count = _ids(ids, dev)
     if rows != count:
@@ -315,7 +324,7 @@ def ra_linear(x, w, bias=None, act="none", residual=None, save=None, dtype=None,
     Checkpoint8 of shape (m, n), receives x @ w + bias in 8 bits.  `out` may be
     the residual itself."""
     m, k = s = _shape(x, "x")
-    dev = x.get_device()
+    dev = _device(x.get_device())
     px, ldx, _ = _matrix(x, "x", dev, _BF16, s)
     n = w.shape[-1]
     pw, ldw, _ = _matrix(w, "w", dev, _BF16, (k, n))
@@ -341,7 +350,7 @@ def ra_linear_dgrad(dy, w, saved=None, act="none", residual=None, dtype=None, ou
     """(dy @ w.T) * act'(z) + residual, dy [m, n] and w [k, n] bfloat16; z is
     the checkpoint `saved` of shape (m, k) (not needed with act "none")."""
     m, n = s = _shape(dy, "dy")
-    dev = dy.get_device()
+    dev = _device(dy.get_device())
     pd, ldd, _ = _matrix(dy, "dy", dev, _BF16, s)
     k = w.shape[0]
     pw, ldw, _ = _matrix(w, "w", dev, _BF16, (k, n))
@@ -368,7 +377,7 @@ def ra_linear_wgrad(x, dy, act="none", dtype=None, out=None, bias_grad=False, ac
     flat gradient; bias_grad True or a float32 vector of length n that receives
     db; accumulate adds to both."""
     m, n = s = _shape(dy, "dy")
-    dev = dy.get_device()
+    dev = _device(dy.get_device())
     pd, ldd, _ = _matrix(dy, "dy", dev, _BF16, s)
     k = x.shape[1]
     code = _act(act)

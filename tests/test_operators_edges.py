@@ -27,3 +27,41 @@ def test_weight_gradient_of_an_empty_checkpoint(lib, act):
     assert wgrad(16, 0, 32) == OK and wgrad(0, 24, 0) == OK and wgrad(0, 0, 0) == OK
     # a checkpoint that has values is asked for
     assert wgrad(16, 24, 32) == INVALID and wgrad(16, 24, 32, q=D) == INVALID and wgrad(16, 24, 32, e=E) == INVALID
+
+
+class _Elsewhere:
+    """The look of a matrix on device 1."""
+
+    def __init__(self, dtype, *shape):
+        import torch
+        self.shape, self.dtype = torch.Size(shape), dtype
+
+    def get_device(self):
+        return 1
+
+    def stride(self):
+        return self.shape[1], 1
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return self.shape.numel()
+
+    def data_ptr(self):
+        raise AssertionError("looked at an address on another device")
+
+
+def test_tensors_on_another_device_than_the_current_one_are_refused(monkeypatch):
+    """The library launches on the current device, whatever device the addresses belong to."""
+    torch = pytest.importorskip("torch")
+    from gradient_ring_all_gb300 import operators as op
+    monkeypatch.setattr(op, "_current_device", lambda: 0, raising=False)
+    x, w, ids = _Elsewhere(torch.bfloat16, 4, 8), _Elsewhere(torch.bfloat16, 8, 8), _Elsewhere(torch.int64, 4)
+    kept = object.__new__(op.Checkpoint8)
+    kept.rows, kept.cols, kept._dev, kept._pq, kept._pe = 4, 8, 1, 0, 0
+    for call in (lambda: op.ra_checkpoint8_pack(x), lambda: op.ra_checkpoint8_unpack(kept, out=x), lambda: op.ra_embedding_lookup(x, ids, out=x),
+                 lambda: op.ra_embedding_grad(x, ids, 4, out=x), lambda: op.ra_linear(x, w, out=x), lambda: op.ra_linear_dgrad(x, w, out=x),
+                 lambda: op.ra_linear_wgrad(x, x, out=w)):
+        with pytest.raises(ValueError, match="cuda:1"):
+            call()
