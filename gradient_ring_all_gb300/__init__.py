@@ -29,7 +29,7 @@ __all__ = [
     "ra_all_gather", "ra_allreduce_avg_bf16_wire", "ra_allreduce_avg_single_reducer", "Reducer", "ra_check_device_errors", "ra_selftest_wait_timeout", "ra_selftest_bounds_check", "ra_chunk_range", "ra_status_str",
     "ra_last_cuda_error", "RA_OK", "RA_ERR_TIMEOUT", "RA_ERR_BOUNDS", "CHECKED",
     "Checkpoint8", "ra_checkpoint8_pack", "ra_checkpoint8_unpack", "ra_embedding_lookup", "ra_embedding_grad",
-    "ra_linear", "ra_linear_dgrad", "ra_linear_wgrad",
+    "ra_linear", "ra_linear_dgrad", "ra_linear_wgrad", "ra_selftest_linear_stall",
 ]
 
 RA_F32 = 0
@@ -413,7 +413,7 @@ def ra_last_cuda_error() -> int:
 # calls and the build need no torch
 
 _OPERATORS = ("Checkpoint8", "ra_checkpoint8_pack", "ra_checkpoint8_unpack", "ra_embedding_lookup", "ra_embedding_grad",
-              "ra_linear", "ra_linear_dgrad", "ra_linear_wgrad")
+              "ra_linear", "ra_linear_dgrad", "ra_linear_wgrad", "ra_selftest_linear_stall")
 
 
 def __getattr__(name):

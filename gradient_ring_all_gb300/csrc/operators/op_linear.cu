@@ -295,8 +295,8 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Wait for a phase, for the library's limit at most; the clock is read only
-// where the phase is not over yet.
+// Wait for a phase, for `limit` ns at most, from `t0` on where that is given; the
+// clock is read only where the phase is not over yet.
 __device__ __forceinline__ bool phase_over(uint32_t bar, uint32_t parity) {
     uint32_t over;
     asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
@@ -309,11 +309,11 @@ __device__ __forceinline__ bool phase_seen(uint32_t bar, uint32_t parity) {
                  : "=r"(over) : "r"(bar), "r"(parity) : "memory");
     return over;
 }
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, uint64_t limit, uint64_t t0 = 0) {
     if (phase_over(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
+    if (t0 == 0) t0 = global_ns();
     while (!phase_over(bar, parity))
-        if (global_ns() - t0 > kWaitLimitNs) return false;
+        if (global_ns() - t0 > limit) return false;
     return true;
 }
 // One lane of a converged warp.  The TMA and MMA warps stay whole and choose a
@@ -487,6 +487,8 @@ struct Product {
     CUtensorMap a, b;
     Epilogue ep;
     unsigned int *err;
+    uint64_t wait_ns;  // the limit of each wait
+    int stalled;       // self-test: the block that makes no copies (-1: none)
     int64_t rows, cols;
     int tiles_m, tiles_n;
     int k64, steps;               // 64s of k, and steps: stages along k
@@ -670,7 +672,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
             tile_at(p, work.tile, &tm, &tn);
             const int row = tm * S::kRows + rank * kBM, col = tn * BN + rank * S::kBCols;
             for (int k = work.k_begin; k < work.k_end; ++k) {
-                ok = __all_sync(0xffffffffu, wait(empty + 8 * s, phase ^ 1));
+                ok = __all_sync(0xffffffffu, wait(empty + 8 * s, phase ^ 1, p.wait_ns));
                 if (!ok) break;
                 const uint32_t a = tiles + s * S::kStageBytes, b = a + S::kABytes;
                 const uint32_t bar = PAIR ? in_leader(full + 8 * s) : full + 8 * s;
@@ -679,7 +681,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                     if (rank == 0) mbar_expect(full + 8 * s, subs * S::kSubBytes * S::kBlocks);
 #pragma unroll
                     for (int u = 0; u < S::kSub; ++u) {
-                        if (u >= subs) break;
+                        if (u >= subs || blockIdx.x == p.stalled) break;
                         const int at = k * kStepK + u * kBK;
                         const uint32_t au = a + u * S::kSubBytes, bu = b + u * S::kSubBytes;
                         if constexpr (kAmn) {
@@ -706,7 +708,16 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
         }
         // shared memory must outlive the copies and the products that read it
         for (int64_t i = issued > S::kStages ? issued - S::kStages : 0; i < issued && ok; ++i)
-            ok = __all_sync(0xffffffffu, wait(empty + 8 * (uint32_t)(i % S::kStages), (uint32_t)(i / S::kStages) & 1));
+            ok = __all_sync(0xffffffffu, wait(empty + 8 * (uint32_t)(i % S::kStages), (uint32_t)(i / S::kStages) & 1, p.wait_ns));
+        // Also where a wait gave up: then nobody may read the stages any more,
+        // but copies can still be on their way.  A pair's all count on its
+        // first block's barriers, which the second, waiting at the end, may have
+        // asked for a round of stages more.
+        if (!ok && rank == 0) {
+            const uint64_t t0 = global_ns();
+            for (int64_t i = issued > S::kStages ? issued - S::kStages : 0; i < issued + (PAIR ? S::kStages : 0); ++i)
+                wait(full + 8 * (uint32_t)(i % S::kStages), (uint32_t)(i / S::kStages) & 1, p.wait_ns, t0);
+        }
     } else if (warp == S::kWarps + 1) {  // tcgen05.mma
         if (rank == 0) {
             constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (kAmn ? 1u << 15 : 0) | (kBmn ? 1u << 16 : 0) | (BN / 8) << 17 | (S::kRows / 16) << 24;
@@ -725,14 +736,14 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                 for (int k = 0; k < steps || k == 0; ++k) {
                     const int in_sum = F32 ? k % kChunk : k;
                     if (in_sum == 0) {  // a new sum
-                        ok = __all_sync(0xffffffffu, wait(freed + 8 * acc, acc_phase ^ 1));
+                        ok = __all_sync(0xffffffffu, wait(freed + 8 * acc, acc_phase ^ 1, p.wait_ns));
                         if (!ok) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     }
                     const bool last = k + 1 >= steps || (F32 && in_sum == kChunk - 1);
                     if (steps > 0) {
                         if (!landed) {
-                            ok = __all_sync(0xffffffffu, wait(full + 8 * s, phase));
+                            ok = __all_sync(0xffffffffu, wait(full + 8 * s, phase, p.wait_ns));
                             if (!ok) break;
                         }
                         if (lead) {
@@ -768,7 +779,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                     mma_commit<false>(drained);
             }
             __syncwarp();
-            ok &= wait(drained, 0);
+            ok &= wait(drained, 0, p.wait_ns);
         }
     } else {
         const uint32_t freed_bar = PAIR ? in_leader(freed) : freed;
@@ -796,7 +807,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
 #pragma unroll
                     for (int j = 0; j < 32; ++j) sum[g][j] = 0.0f;
                 for (int k = 0; k < steps || k == 0; k += kChunk) {
-                    ok = __all_sync(0xffffffffu, wait(done + 8 * acc, acc_phase));
+                    ok = __all_sync(0xffffffffu, wait(done + 8 * acc, acc_phase, p.wait_ns));
                     if (!ok) break;
                     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     if (steps > 0) {
@@ -837,7 +848,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                 if (MODE == kForward && !S::kIsSplit && !tail && p.ep.q && row < p.rows && c0 < p.cols) store_steps<S::kCols>(p.ep, row, c0, step_bytes);
                 __syncwarp();
             } else {
-                ok = __all_sync(0xffffffffu, wait(done + 8 * acc, acc_phase));
+                ok = __all_sync(0xffffffffu, wait(done + 8 * acc, acc_phase, p.wait_ns));
                 if (!ok) break;
                 asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                 uint32_t step_bytes = 0;
@@ -1195,6 +1206,13 @@ __global__ void __launch_bounds__(kColumnThreads) column_sum_kernel(const uint16
 // ---------------------------------------------------------------------------
 // host
 
+// ra_selftest_linear_stall: what this thread's next product is to do
+struct Stall {
+    int block;
+    uint64_t limit_ns;  // 0: nothing is asked for
+};
+thread_local Stall next_stall = {-1, 0};
+
 typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
@@ -1355,6 +1373,9 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     const int cluster = splits * S::kBlocks;
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, most = S::kIsSplit ? tiles : sms / S::kBlocks;
     const Tail tail = KIND == kPair && BN == kTailBN && p.partial ? tail_of(p.rows, p.cols, p.k64, sms) : Tail{0, 1};
+    p.wait_ns = next_stall.limit_ns ? next_stall.limit_ns : kWaitLimitNs;
+    p.stalled = next_stall.limit_ns ? next_stall.block : -1;
+    next_stall = {-1, 0};
     p.whole = (int)(tiles - tail.tiles);
     p.tail_parts = tail.parts;
     cudaLaunchConfig_t cfg = {};
@@ -1673,6 +1694,12 @@ ra_status ra_linear_wgrad(const void *x, int64_t ld_x, const int8_t *z_q, const 
     const Epilogue ep{dw, nullptr, accumulate ? dw : nullptr, nullptr, nullptr, ld_dw, ld_dw, 0, 0, dw_dtype == RA_F32, 0, 0};
     const Mat none{nullptr, 0, 0, 0, 1};
     return cuda_status(launch_product<kWgrad>(a, b, k, n, m, ep, mw, none, accumulate ? mw : none, &space, s, db, accumulate));
+}
+
+ra_status ra_selftest_linear_stall(int block, int timeout_us) {
+    if (block < 0 || timeout_us < 1 || timeout_us > 10000000) return RA_ERR_INVALID_ARG;
+    next_stall = {block, (uint64_t)timeout_us * 1000};
+    return RA_OK;
 }
 
 }  // extern "C"

@@ -52,8 +52,9 @@ def _load():
     lib.ra_linear.argtypes = [vp, i64, vp, i64, i64, i64, i64, vp, i32, i32, vp, i64, i32, vp, vp, vp, i64, i32, vp, sz, vp]
     lib.ra_linear_dgrad.argtypes = [vp, i64, vp, i64, i64, i64, i64, vp, vp, i32, vp, i64, i32, vp, i64, i32, vp, sz, vp]
     lib.ra_linear_wgrad.argtypes = [vp, i64, vp, vp, i32, vp, i64, i64, i64, i64, i32, vp, i64, i32, vp, vp, sz, vp]
+    lib.ra_selftest_linear_stall.argtypes = [i32, i32]
     for name in ("ra_checkpoint8_pack", "ra_checkpoint8_unpack", "ra_embedding_lookup", "ra_embedding_grad", "ra_linear",
-                 "ra_linear_dgrad", "ra_linear_wgrad"):
+                 "ra_linear_dgrad", "ra_linear_wgrad", "ra_selftest_linear_stall"):
         getattr(lib, name).restype = i32
     for name in ("ra_embedding_grad_workspace_bytes", "ra_linear_workspace_bytes", "ra_linear_split_bytes"):
         getattr(lib, name).restype = sz
@@ -405,3 +406,9 @@ def ra_linear_wgrad(x, dy, act="none", dtype=None, out=None, bias_grad=False, ac
     _check(lib.ra_linear_wgrad(px, ldx, pq, pe, code, pd, ldd, m, k, n, int(accumulate), pw, ldw, wcode, pb, ws, nws,
                                _stream_of(stream, dev)), "ra_linear_wgrad")
     return out if pb is None else (out, db)
+
+
+def ra_selftest_linear_stall(block: int, timeout_us: int) -> None:
+    """Let this thread's next product run out of time: block `block` of its grid makes no copies, and its waits are limited to
+    timeout_us (a timeout test)."""
+    _check(_load().ra_selftest_linear_stall(int(block), int(timeout_us)), "ra_selftest_linear_stall")

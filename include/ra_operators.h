@@ -160,6 +160,17 @@ ra_status ra_linear_wgrad(const void *x, int64_t ld_x, const int8_t *z_q, const 
                           int64_t ld_dy, int64_t m, int64_t k, int64_t n, int accumulate, void *dw, int64_t ld_dw,
                           int dw_dtype, float *db, void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * ra_selftest_linear_stall -- exercises the products' time limit on purpose: in
+ * the product that this host thread queues next through ra_linear (other than
+ * a single token's), ra_linear_dgrad or ra_linear_wgrad, block `block` of the
+ * grid makes no copies, and every wait is limited to timeout_us (1 .. 10^7).
+ * The waits that run out are recorded (ra_check_device_errors: RA_ERR_TIMEOUT)
+ * and the blocks return; nothing hangs, and no memory is touched that the call
+ * would not touch.  What a block that gave up would have stored stays as it was.
+ */
+ra_status ra_selftest_linear_stall(int block, int timeout_us);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,77 @@
+"""The products' waits are bounded: with a block that makes no copies every wait
+on them runs out, the call reports it, returns, and leaves what that block would
+have stored as it was.  No fault, no hang: the copies are simply not made."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import gradient_ring_all_gb300 as ra
+from operator_reference import check, rounding, sum_bound
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+LIMIT_US = 20_000
+HELD = -1e30  # what outputs hold before the call; far outside every result
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from gradient_ring_all_gb300 import build
+    build.build()
+    ra.load()
+
+
+def _normal(seed, *shape, dtype=BF16, s=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * s).to(dtype)
+
+
+def _timed_out():
+    torch.cuda.synchronize()
+    return ra.ra_check_device_errors() == ra.RA_ERR_TIMEOUT
+
+
+def _held_or_right(got, want, bound, most):
+    """Each value is the former one or the product's; between one and `most` of them are the former ones."""
+    held = got == torch.full((), HELD, dtype=got.dtype, device="cuda")
+    check(got[~held], want[~held], bound[~held])
+    assert 0 < int(held.sum()) <= most, (int(held.sum()), most)
+
+
+# (m, k, n): single blocks of 64 and 128 columns; pairs of 128 and 256; no block or pair has more than two tiles
+WHOLE = [(300, 200, 130), (2000, 130, 1500), (1000, 640, 2000), (4096, 512, 1100)]
+
+
+@pytest.mark.parametrize("out_type", [BF16, F32])
+@pytest.mark.parametrize("m,k,n", WHOLE)
+@pytest.mark.parametrize("block", [0, 1, 4])
+def test_a_block_that_gives_up(block, m, k, n, out_type):
+    x, w = _normal(1, m, k), _normal(2, k, n, s=k ** -0.5)
+    want, size = x.double() @ w.double(), x.double().abs() @ w.double().abs()
+    bound = sum_bound(k) * size + rounding(out_type) * want.abs()
+    out = torch.full((m, n), HELD, dtype=out_type, device="cuda")
+    assert ra.ra_check_device_errors() == ra.RA_OK
+    ra.ra_selftest_linear_stall(block, LIMIT_US)
+    ra.ra_linear(x, w, out=out)
+    assert _timed_out()
+    _held_or_right(out, want, bound, 2 * 256 * 256)
+    # the next call is an ordinary one
+    check(ra.ra_linear(x, w, dtype=out_type), want, bound)
+    assert ra.ra_check_device_errors() == ra.RA_OK
+    for product in (lambda o: ra.ra_linear_dgrad(x, wt, out=o), lambda o: ra.ra_linear_wgrad(xt, w, out=o)):
+        xt, wt = x.t().contiguous(), w.t().contiguous()
+        out.fill_(HELD)
+        ra.ra_selftest_linear_stall(block, LIMIT_US)
+        product(out)
+        assert _timed_out()
+        _held_or_right(out, want, bound, 2 * 256 * 256)
+        product(out)
+        check(out, want, bound)
+
+
+def test_limits_out_of_range():
+    for block, limit in ((-1, 10), (0, 0), (0, -5), (0, 10_000_001)):
+        with pytest.raises(ra.RaError):
+            ra.ra_selftest_linear_stall(block, limit)
