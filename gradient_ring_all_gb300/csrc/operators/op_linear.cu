@@ -544,13 +544,13 @@ __device__ __forceinline__ void keep_part(float *to, const float (&v)[32]) {
 }
 
 // The bias gradient, by the epilogue warps of the blocks with the first row
-// tile, while the tensor core makes that tile: the column sums of the block's
+// tile, while the tensor core makes its first tiles: the column sums of the block's
 // kBCols columns of dy.  A warp takes 16 columns (a sector a row) and half of
 // the rows, a lane every 32nd of these; then lanes and halves are added in a
 // fixed order.  For up to kColumnRows rows: a warp's loads are few enough in
 // flight to take longer than the tile's products past that.  Measured as what
 // the sums add to a 2048 x 2048 bf16 weight gradient, here / in a launch of their
-// own: 256 rows 1.7 / 3.5 us, 512 rows 3.8 / 5.0, 1024 rows 8.2 / 5.9, 4096 rows 32 / 6.8.
+// own: 256 rows 2.6 / 3.5 us, 512 rows 3.3 / 5.0, 1024 rows 8.2 / 5.9, 4096 rows 32 / 6.8.
 constexpr int64_t kColumnRows = 512;
 template <class S>
 __device__ __forceinline__ void column_sums(const Product &p, int64_t c0, float *half_sums, int warp, int lane) {
@@ -786,6 +786,18 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
         int acc = 0;
         uint32_t acc_phase = 0;
         const uint32_t mine = tmem + (warp / 4) * S::kCols + ((uint32_t)(warp % 4 * 32) << 16);
+        if (MODE == kWgrad && p.db) {
+            // All of the block's column sums before its first wait: they have
+            // barriers for all epilogue warps, and each of these decides by
+            // itself that a wait has run out.
+            for (int unit = unit0; unit < unit_count; unit += unit_step) {
+                const Work work = work_at<KIND>(p, unit);
+                int tm, tn;
+                tile_at(p, work.tile, &tm, &tn);
+                if (tm == 0 && work.part == 0)
+                    column_sums<S>(p, (int64_t)tn * BN + rank * S::kBCols, reinterpret_cast<float *>(smem + S::kStages * S::kStageBytes + 256), warp, lane);
+            }
+        }
         for (int unit = unit0; unit < unit_count && ok; unit += unit_step) {
             const Work work = work_at<KIND>(p, unit);
             const int steps = work.k_end - work.k_begin;
@@ -794,8 +806,6 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
             const int64_t row0 = (int64_t)tm * S::kRows + rank * kBM + warp % 4 * 32, row = row0 + lane;
             const int rows = p.rows - row0 < 32 ? (int)(p.rows - row0) : 32;  // of the warp's 32 (none where not above 0)
             const int64_t c0 = (int64_t)tn * BN + warp / 4 * S::kCols;
-            if (MODE == kWgrad && p.db && tm == 0 && work.part == 0)
-                column_sums<S>(p, (int64_t)tn * BN + rank * S::kBCols, reinterpret_cast<float *>(smem + S::kStages * S::kStageBytes + 256), warp, lane);
             // where a part's sums go, for its first column and this lane's row
             const bool tail = KIND == kPair && unit >= p.whole;
             float *to = !tail ? nullptr

@@ -167,7 +167,8 @@ ra_status ra_linear_wgrad(const void *x, int64_t ld_x, const int8_t *z_q, const 
  * grid makes no copies, and every wait is limited to timeout_us (1 .. 10^7).
  * The waits that run out are recorded (ra_check_device_errors: RA_ERR_TIMEOUT)
  * and the blocks return; nothing hangs, and no memory is touched that the call
- * would not touch.  What a block that gave up would have stored stays as it was.
+ * would not touch.  What a block that gave up would have stored stays as it
+ * was, but for db, which waits for nothing.
  */
 ra_status ra_selftest_linear_stall(int block, int timeout_us);
 

@@ -75,3 +75,24 @@ def test_limits_out_of_range():
     for block, limit in ((-1, 10), (0, 0), (0, -5), (0, 10_000_001)):
         with pytest.raises(ra.RaError):
             ra.ra_selftest_linear_stall(block, limit)
+
+
+@pytest.mark.parametrize("out_type", [BF16, F32])
+@pytest.mark.parametrize("m,k,n", [(256, 300, 130), (512, 2000, 2000), (256, 8192, 4000), (100, 4100, 8192)])
+@pytest.mark.parametrize("block", [0, 1, 76])
+def test_a_block_that_gives_up_beside_column_sums(block, m, k, n, out_type):
+    """The bias gradient's sums wait for no copies: they are whole, also where a block has several of the first row's tiles and
+    gives up at the first (the epilogue warps' common barriers must all be behind them by then)."""
+    x, dy = _normal(1, m, k), _normal(2, m, n)
+    out, db = torch.full((k, n), HELD, dtype=out_type, device="cuda"), torch.full((n,), HELD, device="cuda")
+    ra.ra_selftest_linear_stall(block, LIMIT_US)
+    ra.ra_linear_wgrad(x, dy, out=out, bias_grad=db)
+    timed_out = _timed_out()
+    want, size = x.double().t() @ dy.double(), x.double().t().abs() @ dy.double().abs()
+    bound = sum_bound(m) * size + rounding(out_type) * want.abs()
+    check(db, dy.double().sum(0), sum_bound(m) * dy.double().abs().sum(0))
+    if timed_out:
+        _held_or_right(out, want, bound, 8 * 256 * 256)
+    else:  # the grid has no such block
+        check(out, want, bound)
+    assert timed_out or block == 76
