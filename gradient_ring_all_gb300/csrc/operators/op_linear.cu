@@ -998,7 +998,7 @@ __global__ void __launch_bounds__(kTailThreads) join_tail_kernel(const __grid_co
     for (int q = 0; q < p.tail_parts; ++q, from += kTailBN * kTailRows) {
         float x[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = from[j * kTailRows];
+        for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(load_4(from + j * kTailRows));
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = q ? v[j] + x[j] : x[j];
     }
@@ -1026,7 +1026,7 @@ struct Token {
 // `count` neighbouring bf16 values (none where it is not above 0), zeros after
 // them; eight in one access
 __device__ __forceinline__ uint4 load8(const uint16_t *p, int64_t count) {
-    if (count >= 8) return *reinterpret_cast<const uint4 *>(p);
+    if (count >= 8) return load_16(p);
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = (2 * i < count ? p[2 * i] : 0u) | (2 * i + 1 < count ? (uint32_t)p[2 * i + 1] : 0u) << 16;
@@ -1128,7 +1128,7 @@ __device__ __forceinline__ void lay_out(const Layout &l, int64_t block) {
         const uintptr_t at = reinterpret_cast<uintptr_t>(src), word = at & ~(uintptr_t)15;
         uint32_t w[8];
         if (c + 8 <= l.cols && word >= lo && word + 32 <= hi) {
-            const uint4 x = reinterpret_cast<const uint4 *>(word)[0], y = reinterpret_cast<const uint4 *>(word)[1];
+            const uint4 x = load_16(reinterpret_cast<const void *>(word)), y = load_16(reinterpret_cast<const void *>(word + 16));
             w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
             if (at & 8)
 #pragma unroll
