@@ -536,6 +536,16 @@ __device__ __forceinline__ void keep_rows(unsigned char *smem, int col, int row,
     for (int j = 0; j < 8; ++j) to[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
 }
 
+// Whether a wait in one of a cluster's `blocks` blocks has run out: lane l's look
+// at block l (nothing for others), after the cluster has met.  What such a block
+// left is no sum, so none of them stores anything.  The look is taken beside the
+// first reads of the sums, and used after them.
+__device__ __forceinline__ uint32_t one_gave_up(const uint32_t *gave_up, int blocks, int lane) {
+    uint32_t f = 0;
+    if (lane < blocks) asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(f) : "r"(in_block(smem_addr(gave_up), lane)) : "memory");
+    return f;
+}
+
 // 32 sums of a row of a tile's part, column by column
 template <int ROWS>
 __device__ __forceinline__ void keep_part(float *to, const float (&v)[32]) {
@@ -628,6 +638,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
     // tile's sums are; freed: they have been read; drained: all products are
     const uint32_t full = bars, empty = full + 8 * S::kStages, done = empty + 8 * S::kStages, freed = done + 16, drained = freed + 16;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::kStages * S::kStageBytes + 16 * S::kStages + 40);
+    uint32_t *gave_up = tmem_slot + 1;  // whether a wait of the block did
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const int rank = PAIR ? blockIdx.x & 1 : 0;
     // the first unit of work and the distance to the next
@@ -645,6 +656,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                 mbar_init(freed + 8 * s, S::kWarps * S::kBlocks);
             }
             mbar_init(drained, 1);
+            *gave_up = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         __syncwarp();
@@ -891,7 +903,10 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
             }
         }
     }
-    if (!ok) atomicOr(p.err, 1u);
+    if (!ok) {
+        atomicOr(p.err, 1u);
+        *reinterpret_cast<volatile uint32_t *>(gave_up) = 1;
+    }
     __syncwarp();
     if constexpr (KIND == kSkinny) {
         // Every block's sums lie in its shared memory; the blocks share the work
@@ -904,11 +919,12 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
         // whole tile are better read that way: this one's exchanges between
         // lanes then cost more than the reads, 7.3 against 6.5 us at 256 x 1024 x 1024.)
         cluster_sync();
+        const uint32_t failed = one_gave_up(gave_up, p.splits, lane);
         const int part = blockIdx.x % p.splits, per_task = 32 / p.splits, tasks = BN / 32 * (S::kARows / per_task);
         int tm, tn;
         tile_at(p, unit0, &tm, &tn);
         const int sub = lane / 8, q0 = p.splits == 2 ? sub / 2 : sub, r0 = p.splits == 2 ? sub % 2 * 8 : 0;
-        for (int t = part + warp * p.splits; t < tasks && warp < S::kWarps && ok; t += S::kWarps * p.splits) {
+        for (int t = part + warp * p.splits; t < tasks && warp < S::kWarps; t += S::kWarps * p.splits) {
             const int g = t % (BN / 32), in_tile = t / (BN / 32) * per_task;
             const int64_t row0 = (int64_t)tm * kBM + in_tile, n0 = (int64_t)tn * BN + g * 32;
             if (row0 >= p.rows || n0 >= p.cols) continue;
@@ -922,6 +938,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                 asm volatile("ld.shared::cluster.v4.b32 {%0, %1, %2, %3}, [%4];"
                              : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3]) : "r"(at) : "memory");
             }
+            if (__any_sync(0xffffffffu, failed)) break;
             float v[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(w[j]);
@@ -946,6 +963,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
         // every block's sums lie in its shared memory: each block adds and
         // finishes its share of the rows, the splits in their order
         cluster_sync();
+        const uint32_t failed = one_gave_up(gave_up, p.splits * S::kBlocks, lane);
         const int height = kBM / p.splits, per_group = height > 32 ? height / 32 : 1;  // warps a column group
         const int g = warp / per_group, at0 = warp % per_group * 32;
         int tm, tn;
@@ -954,7 +972,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
         const int64_t row0 = (int64_t)tm * S::kRows + rank * kBM + in_tile, n0 = (int64_t)tn * BN + g * 32;
         int rows = height < 32 ? height : 32;
         if (p.rows - row0 < rows) rows = (int)(p.rows - row0);
-        if (ok && g < BN / 32 && rows > 0 && n0 < p.cols) {
+        if (g < BN / 32 && rows > 0 && n0 < p.cols) {
             float v[32];
             // (lanes past the block's rows read its neighbours' and drop them)
             for (int q = 0; q < p.splits; ++q) {
@@ -966,8 +984,10 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                     v[j] = q ? v[j] + x : x;
                 }
             }
-            const uint32_t step_byte = finish32<MODE, F32>(p.ep, row0, rows, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
-            if (MODE == kForward && p.ep.q && lane < rows) store_steps<32>(p.ep, row0 + lane, n0, step_byte);
+            if (!__any_sync(0xffffffffu, failed)) {
+                const uint32_t step_byte = finish32<MODE, F32>(p.ep, row0, rows, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
+                if (MODE == kForward && p.ep.q && lane < rows) store_steps<32>(p.ep, row0 + lane, n0, step_byte);
+            }
         }
         __syncwarp();
     }

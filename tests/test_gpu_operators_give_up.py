@@ -96,3 +96,44 @@ def test_a_block_that_gives_up_beside_column_sums(block, m, k, n, out_type):
     else:  # the grid has no such block
         check(out, want, bound)
     assert timed_out or block == 76
+
+
+# (m, k, n): clusters that split k, of single blocks (with few rows, and with a tile's), and of two and four pairs
+SPLIT = [(16, 2048, 2048), (3, 4096, 200), (1, 1100, 4000), (120, 4096, 4096), (256, 1024, 1024), (257, 3210, 2081), (300, 4104, 328)]
+
+
+@pytest.mark.parametrize("out_type", [BF16, F32])
+@pytest.mark.parametrize("m,k,n", SPLIT)
+@pytest.mark.parametrize("block", [0, 1, 2, 3, 7])
+def test_a_block_of_a_cluster_that_gives_up(block, m, k, n, out_type):
+    """No block of the cluster stores a sum in which that block's share is missing."""
+    w, bias = _normal(2, k, n, s=k ** -0.5), _normal(3, n, dtype=F32)
+    for rows in sorted({m, max(m, 2)}):  # a single row has a kernel without copies
+        x = _normal(1, rows, k)
+        z, size = x.double() @ w.double(), x.double().abs() @ w.double().abs()
+        want, bound = z + bias.double(), sum_bound(k + 1) * (size + bias.double().abs())
+        bound = bound + rounding(out_type) * want.abs()
+        out = torch.full((rows, n), HELD, dtype=out_type, device="cuda")
+        kept = ra.Checkpoint8(rows, n)
+        kept.q.fill_(77)
+        kept.e.fill_(3)
+        ra.ra_selftest_linear_stall(block, LIMIT_US)
+        if rows > 1:
+            ra.ra_linear(x, w, bias=bias, save=kept, out=out)
+            assert _timed_out()
+            _held_or_right(out, want, bound, 256 * 128)
+            held = (out == torch.full((), HELD, dtype=out_type, device="cuda")).any(0).int()
+            held = torch.nn.functional.pad(held, (0, -n % 32)).view(-1, 32).any(1)
+            tops = kept.e == 3  # no group of these sums has such a step
+            assert torch.equal(tops.any(0), held)
+            assert bool((kept.q.view(rows, -1, 32)[tops] == 77).all())
+        for product in (lambda o: ra.ra_linear_dgrad(x, wt, out=o), lambda o: ra.ra_linear_wgrad(xt, w, out=o)):
+            xt, wt = x.t().contiguous(), w.t().contiguous()
+            out.fill_(HELD)
+            ra.ra_selftest_linear_stall(block, LIMIT_US)
+            product(out)
+            timed_out = _timed_out()
+            if timed_out:
+                _held_or_right(out, z, sum_bound(k) * size + rounding(out_type) * z.abs(), 256 * 128)
+            product(out)
+            check(out, z, sum_bound(k) * size + rounding(out_type) * z.abs())
