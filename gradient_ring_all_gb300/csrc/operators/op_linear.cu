@@ -546,6 +546,10 @@ __device__ __forceinline__ uint32_t one_gave_up(const uint32_t *gave_up, int blo
     return f;
 }
 
+// What stands in the first of each 32 sums of a part that was not made because a
+// wait ran out: a NaN that no arithmetic gives (the hardware's has all other bits set).
+constexpr uint32_t kUnmade = 0x7fc0dead;
+
 // 32 sums of a row of a tile's part, column by column
 template <int ROWS>
 __device__ __forceinline__ void keep_part(float *to, const float (&v)[32]) {
@@ -798,6 +802,10 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
         int acc = 0;
         uint32_t acc_phase = 0;
         const uint32_t mine = tmem + (warp / 4) * S::kCols + ((uint32_t)(warp % 4 * 32) << 16);
+        // where a part's sums go, for the warp's first column and this lane's row
+        [[maybe_unused]] auto part_at = [&](int unit) {
+            return p.partial + ((int64_t)(unit - p.whole) * BN + warp / 4 * S::kCols) * S::kRows + rank * kBM + warp % 4 * 32 + lane;
+        };
         if (MODE == kWgrad && p.db) {
             // All of the block's column sums before its first wait: they have
             // barriers for all epilogue warps, and each of these decides by
@@ -810,7 +818,8 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                     column_sums<S>(p, (int64_t)tn * BN + rank * S::kBCols, reinterpret_cast<float *>(smem + S::kStages * S::kStageBytes + 256), warp, lane);
             }
         }
-        for (int unit = unit0; unit < unit_count && ok; unit += unit_step) {
+        int unit = unit0;
+        for (; unit < unit_count && ok; unit += unit_step) {
             const Work work = work_at<KIND>(p, unit);
             const int steps = work.k_end - work.k_begin;
             int tm, tn;
@@ -818,10 +827,8 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
             const int64_t row0 = (int64_t)tm * S::kRows + rank * kBM + warp % 4 * 32, row = row0 + lane;
             const int rows = p.rows - row0 < 32 ? (int)(p.rows - row0) : 32;  // of the warp's 32 (none where not above 0)
             const int64_t c0 = (int64_t)tn * BN + warp / 4 * S::kCols;
-            // where a part's sums go, for its first column and this lane's row
             const bool tail = KIND == kPair && unit >= p.whole;
-            float *to = !tail ? nullptr
-                              : p.partial + ((int64_t)(unit - p.whole) * BN + warp / 4 * S::kCols) * S::kRows + rank * kBM + warp % 4 * 32 + lane;
+            float *to = tail ? part_at(unit) : nullptr;
             if constexpr (F32) {
                 float sum[S::kCols / 32][32];
 #pragma unroll
@@ -902,6 +909,10 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                 flip(acc, acc_phase);
             }
         }
+        if constexpr (KIND == kPair)  // the parts that a wait which ran out leaves unmade
+            for (; unit < unit_count; unit += unit_step)
+                if (unit >= p.whole)
+                    for (int g = 0; g < S::kCols / 32; ++g) part_at(unit)[g * 32 * S::kRows] = __uint_as_float(kUnmade);
     }
     if (!ok) {
         atomicOr(p.err, 1u);
@@ -1003,7 +1014,8 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
 }
 
 // The tiles made in parts: the sums of the parts in their order, then the
-// epilogue.  A block a 32-column stripe of a tile, a warp 32 of its rows.
+// epilogue; nothing where a part was not made.  A block a 32-column stripe of a
+// tile, a warp 32 of its rows.
 constexpr int kTailBN = 256, kTailRows = 2 * kBM, kTailThreads = kTailRows;
 template <int MODE, bool F32>
 __global__ void __launch_bounds__(kTailThreads) join_tail_kernel(const __grid_constant__ Product p) {
@@ -1015,13 +1027,16 @@ __global__ void __launch_bounds__(kTailThreads) join_tail_kernel(const __grid_co
     if (row0 >= p.rows || n0 >= p.cols) return;
     const float *from = p.partial + ((int64_t)t * p.tail_parts * kTailBN + g * 32) * kTailRows + threadIdx.x;
     float v[32];
+    bool made = true;
     for (int q = 0; q < p.tail_parts; ++q, from += kTailBN * kTailRows) {
         float x[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(load_4(from + j * kTailRows));
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = q ? v[j] + x[j] : x[j];
+        made = made && __float_as_uint(x[0]) != kUnmade;
     }
+    if (!__all_sync(0xffffffffu, made)) return;
     const int rows = p.rows - row0 < 32 ? (int)(p.rows - row0) : 32, lane = threadIdx.x & 31;
     const uint32_t step_byte = finish32<MODE, F32>(p.ep, row0, rows, n0, (int)(p.cols - n0 < 32 ? p.cols - n0 : 32), v);
     if (MODE == kForward && p.ep.q && lane < rows) store_steps<32>(p.ep, row0 + lane, n0, step_byte);

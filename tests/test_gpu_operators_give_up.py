@@ -137,3 +137,32 @@ def test_a_block_of_a_cluster_that_gives_up(block, m, k, n, out_type):
                 _held_or_right(out, z, sum_bound(k) * size + rounding(out_type) * z.abs(), 256 * 128)
             product(out)
             check(out, z, sum_bound(k) * size + rounding(out_type) * z.abs())
+
+
+@pytest.mark.parametrize("out_type", [BF16, F32])
+@pytest.mark.parametrize("block", [0, 1, 30, 60, 151])
+def test_a_part_of_a_tile_that_is_not_made(block, out_type):
+    """Tiles whose sums are made in parts along k and joined afterwards: without one of the parts none of the tile is stored."""
+    from gradient_ring_all_gb300 import operators
+    m, k, n = 2500, 4100, 2200
+    x, w = _normal(1, m, 4104)[:, :k], _normal(2, k, n, s=k ** -0.5)
+    lib = operators._load()
+    need = lib.ra_linear_split_bytes(m, n, k)
+    assert need > 0
+    want, size = x.double() @ w.double(), x.double().abs() @ w.double().abs()
+    bound = sum_bound(k) * size + rounding(out_type) * want.abs()
+    out = torch.full((m, n), HELD, dtype=out_type, device="cuda")
+    workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
+    for product in (lambda: ra.ra_linear(x, w, out=out, workspace=workspace), lambda: ra.ra_linear_dgrad(x, wt, out=out, workspace=workspace),
+                    lambda: ra.ra_linear_wgrad(xt, w, out=out, workspace=workspace)):
+        xt, wt = torch.empty(k, 2504, dtype=BF16, device="cuda")[:, :m].copy_(x.t()), torch.empty(n, 4104, dtype=BF16, device="cuda")[:, :k].copy_(w.t())
+        product()  # right sums of every part lie in the workspace
+        check(out, want, bound)
+        out.fill_(HELD)
+        ra.ra_selftest_linear_stall(block, LIMIT_US)
+        product()
+        assert _timed_out()
+        # the pair's first tile, and the tile of its part
+        _held_or_right(out, want, bound, 2 * 256 * 256)
+        product()
+        check(out, want, bound)
