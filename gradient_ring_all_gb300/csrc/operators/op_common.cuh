@@ -61,7 +61,8 @@ inline bool mats_overlap(const Mat &a, const Mat &b) {
     return true;
 }
 
-inline bool same_mat(const Mat &a, const Mat &b) { return a.data == b.data && a.pitch() == b.pitch() && a.esz == b.esz; }
+// the same matrix by address, type and stride (which a single row does not have)
+inline bool same_mat(const Mat &a, const Mat &b) { return a.data == b.data && a.esz == b.esz && (a.pitch() == b.pitch() || a.rows <= 1); }
 
 inline ra_status cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return RA_OK;

@@ -56,3 +56,23 @@ def test_bias_gradient_alone(act, m, n):
     if act == "none":
         _, again = ra.ra_linear_wgrad(torch.empty(m, 0, dtype=BF16, device="cuda"), dy, bias_grad=True)
         check(again, want, bound)
+
+
+@pytest.mark.parametrize("out_type", [BF16, F32])
+@pytest.mark.parametrize("k", [64, 600])
+def test_one_row_in_place_whatever_its_stride(k, out_type):
+    """A single row has no stride: the residual may be the output under another one."""
+    n = 96
+    x, w, r = _normal(1, 1, k), _normal(2, k, n, s=k ** -0.5), _normal(3, 1, n, dtype=out_type)
+    want = ra.ra_linear(x, w, residual=r, dtype=out_type)
+    for lda, ldb in ((n, n + 32), (n + 7, n), (1, n)):
+        both = torch.cat([r.flatten(), torch.zeros(64, dtype=out_type, device="cuda")])
+        ra.ra_linear(x, w, residual=both.as_strided((1, n), (lda, 1)), out=both.as_strided((1, n), (ldb, 1)))
+        assert torch.equal(both[:n], want[0]) and not bool(both[n:].any())
+        both[:n] = r[0]
+        ra.ra_linear_dgrad(x, w.t().contiguous(), residual=both.as_strided((1, n), (lda, 1)), out=both.as_strided((1, n), (ldb, 1)))
+        check(both[None, :n], x.double() @ w.double() + r.double(), sum_bound(k) * (x.double().abs() @ w.double().abs()) + 2.0 ** -7 * (
+            (x.double() @ w.double()).abs() + r.double().abs()))
+    with pytest.raises(ra.RaError, match="OVERLAP"):  # a part of the row in place is not
+        both = torch.zeros(2 * n, dtype=out_type, device="cuda")
+        ra.ra_linear(x, w, residual=both[8:8 + n].view(1, n), out=both[:n].view(1, n))
