@@ -412,6 +412,7 @@ struct GradParams {
     int piece;  // tokens a piece
     float scale;
     int accumulate;
+    int list;  // whether the runs that cross pieces are to be listed
 };
 
 // the first index with key[index] >= v, by a warp (33-way search)
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_pieces_kernel(const GradPar
     if (threadIdx.x < count) pos[threadIdx.x] = p.pos[i0 + threadIdx.x];
     __syncthreads();
     const int64_t c = ((int64_t)blockIdx.y * kGradThreads * N + threadIdx.x) * W;  // and every kGradThreads * W on
-    if (blockIdx.y == 0 && threadIdx.x >= kGradThreads - 32) {
+    if (p.list && blockIdx.y == 0 && threadIdx.x >= kGradThreads - 32) {
         const uint32_t v = key[count];
         if (v < p.vocab && key[count + 1] == v && !(key[1] == v && key[0] == v)) {
             // a run begins here that later pieces go on with: how many of them, to its end
@@ -693,12 +694,25 @@ cudaError_t launch_2d(K kern, int64_t gx, int64_t gy, int threads, cudaStream_t 
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
+// Columns that a launch takes: the second grid extent, 32 * kJoinCols or more of
+// them a block, stays below 2^16.
+constexpr int64_t kLaunchCols = (int64_t)1 << 22;
 template <class TI, class TO, int W>
-cudaError_t launch_sums(const GradParams &p, cudaStream_t s) {
-    cudaError_t e = launch_2d(grad_pieces_kernel<TI, TO, W>, p.pieces, ceil_div<int64_t>(p.d * (int64_t)sizeof(TI), kGradThreads * kRowBytes), kGradThreads, s, p);
-    if (e != cudaSuccess || p.pieces < 2) return e;
-    return launch_2d(grad_join_kernel<TO, (W < kJoinCols ? W : kJoinCols)>, p.pieces - 1 < kJoinBlocks ? p.pieces - 1 : kJoinBlocks,
-                     ceil_div<int64_t>(p.d, 32 * kJoinCols), kJoinWarps * 32, s, p);
+cudaError_t launch_sums(const GradParams &whole, cudaStream_t s) {
+    for (int64_t c0 = 0; c0 < whole.d; c0 += kLaunchCols) {
+        GradParams p = whole;
+        p.grad = static_cast<const TI *>(whole.grad) + c0;
+        p.out = static_cast<TO *>(whole.out) + c0;
+        p.part = whole.part + c0;
+        p.d = whole.d - c0 < kLaunchCols ? whole.d - c0 : kLaunchCols;
+        p.list = c0 == 0;  // the runs are the same for all columns
+        cudaError_t e = launch_2d(grad_pieces_kernel<TI, TO, W>, p.pieces, ceil_div<int64_t>(p.d * (int64_t)sizeof(TI), kGradThreads * kRowBytes), kGradThreads, s, p);
+        if (e == cudaSuccess && p.pieces > 1)
+            e = launch_2d(grad_join_kernel<TO, (W < kJoinCols ? W : kJoinCols)>, p.pieces - 1 < kJoinBlocks ? p.pieces - 1 : kJoinBlocks,
+                          ceil_div<int64_t>(p.d, 32 * kJoinCols), kJoinWarps * 32, s, p);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 template <class TI, class TO>
@@ -758,7 +772,6 @@ ra_status ra_embedding_grad(const void *grad, int64_t ld_grad, int grad_dtype, c
     }
     if (mats_overlap(g, o) || mats_overlap(i, o)) return RA_ERR_OVERLAP;
     if (tokens == 0 && accumulate) return RA_OK;
-    if (plan.pieces > kMaxGrid || ceil_div<int64_t>(d, 32) > 65535) return RA_ERR_UNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     char *base = static_cast<char *>(ws);
     const ZeroShare zero{static_cast<char *>(out), vocab > 1 ? o.pitch() : o.row_bytes(), o.row_bytes(), 0, accumulate ? 0 : vocab};
@@ -771,7 +784,7 @@ ra_status ra_embedding_grad(const void *grad, int64_t ld_grad, int grad_dtype, c
                        reinterpret_cast<const uint32_t *>(base + plan.key[sorted]),
                        reinterpret_cast<const uint32_t *>(base + plan.pos[sorted]),
                        reinterpret_cast<float *>(base + plan.part), reinterpret_cast<Join *>(base + plan.joins),
-                       ld_grad, ld_out, plan.ldp, tokens, vocab, d, plan.pieces, plan.piece, scale, accumulate};
+                       ld_grad, ld_out, plan.ldp, tokens, vocab, d, plan.pieces, plan.piece, scale, accumulate, 1};
     const int width = common_width(g, o, d, 16 / gsz);
     if (gsz == 4) return cuda_status(osz == 4 ? launch_grad<float, float>(p, width, s) : launch_grad<float, uint16_t>(p, width, s));
     return cuda_status(osz == 4 ? launch_grad<uint16_t, float>(p, width, s) : launch_grad<uint16_t, uint16_t>(p, width, s));

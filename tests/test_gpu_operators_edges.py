@@ -76,3 +76,19 @@ def test_one_row_in_place_whatever_its_stride(k, out_type):
     with pytest.raises(ra.RaError, match="OVERLAP"):  # a part of the row in place is not
         both = torch.zeros(2 * n, dtype=out_type, device="cuda")
         ra.ra_linear(x, w, residual=both[8:8 + n].view(1, n), out=both[:n].view(1, n))
+
+
+@pytest.mark.parametrize("d", [2_097_120, 2_097_121, (1 << 22) + 5, (1 << 23) + 1024])
+@pytest.mark.parametrize("out_type", [BF16, F32])
+def test_table_gradient_of_very_wide_rows(d, out_type):
+    """Any width below 2^31: the columns go out in as many launches as they need, the runs that cross pieces are listed once.
+    The sums are exact (small whole numbers)."""
+    tokens, vocab = 27, 3
+    ids = torch.tensor([0, 2, -1, 2], device="cuda").repeat(7)[:tokens]
+    grad = torch.randint(-3, 4, (tokens, d), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda", dtype=torch.int8).to(BF16)
+    want = torch.zeros(vocab, d, device="cuda").index_add_(0, ids[ids >= 0], grad[ids >= 0].float())
+    got = ra.ra_embedding_grad(grad, ids, vocab, dtype=out_type)
+    assert torch.equal(got.float(), want)
+    ra.ra_embedding_grad(grad, ids, vocab, out=got, accumulate=True)
+    assert torch.equal(got.float(), 2 * want)
+    assert torch.equal(ra.ra_embedding_lookup(got, ids[:1]).float(), 2 * want[:1])
