@@ -445,13 +445,18 @@ __device__ __forceinline__ void release(uint32_t bar, int lane) {
 // the product
 
 constexpr int kBM = 128, kBK = 64;
-// The tensor core adds to its binary32 sums by truncation: a sum over k comes
-// out about 1e-9 k short (measured: 2.3e-7 at k = 256, 4.4e-6 at 4096, 3.8e-5
-// at 32768, all toward zero).  That is far below a bf16 result's rounding, but
-// not below a binary32 one's: there the tensor core sums 512 of k
-// at a time, and the epilogue warps add the chunks in registers with rounding
-// to nearest, while the next chunk is made.
+// The tensor core adds to its binary32 sums by truncation: of a product that is
+// small beside the sum, bits are lost below the sum's last place.  A sum over k
+// comes out short of itself by about 1e-9 k where signs are mixed (2.3e-7 at k = 256,
+// 4.4e-6 at 4096, 3.8e-5 at 32768), and by 5e-9 to 2e-8 k where all products have one
+// sign (7.5e-5 at 16384, 1.6e-3 to 6e-3 at 262144).  Up to kLongSum of k that is at most a
+// fifth of half a bf16 step.  A binary32 result, and a longer sum, is made in chunks: the
+// tensor core sums 512 of k at a time, and the epilogue warps add the chunks in
+// registers with rounding to nearest, while the next chunk is made (8192 x 16384 x
+// 2048 into bf16: 301 us, 289 without; 2048 x 32000 x 2048 160 either way).
 constexpr int kChunk64 = 8;
+constexpr int64_t kLongSum = 16384;
+enum Sums { kBf16 = 0, kF32 = 1, kBf16Long = 2 };  // the result's type, and whether bf16 ones are made in chunks
 constexpr int kGroupM = 8;  // row tiles that share the columns' tiles in L2
 
 // A tile is BN columns wide and 128 rows high per block; in a pair each block
@@ -628,10 +633,10 @@ __device__ __forceinline__ Work work_at(const Product &p, int unit) {
     return Work{unit, 0, 0, p.steps};
 }
 
-template <int MODE, int BN, int KIND, bool F32>
+template <int MODE, int BN, int KIND, int SUMS>
 __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kBlocksPerSm) product_kernel(const __grid_constant__ Product p) {
     using S = Shape<BN, KIND>;
-    constexpr bool PAIR = S::kIsPair;
+    constexpr bool PAIR = S::kIsPair, CHUNKED = SUMS != kBf16, F32 = SUMS == kF32;
     constexpr bool kAmn = MODE == kWgrad, kBmn = MODE != kDgrad;
     constexpr int kChunk = kChunk64 / S::kSub, kStepK = kBK * S::kSub;
     extern __shared__ unsigned char raw[];
@@ -750,13 +755,13 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
                 const Work work = work_at<KIND>(p, unit);
                 const int steps = work.k_end - work.k_begin;
                 for (int k = 0; k < steps || k == 0; ++k) {
-                    const int in_sum = F32 ? k % kChunk : k;
+                    const int in_sum = CHUNKED ? k % kChunk : k;
                     if (in_sum == 0) {  // a new sum
                         ok = __all_sync(0xffffffffu, wait(freed + 8 * acc, acc_phase ^ 1, p.wait_ns));
                         if (!ok) break;
                         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
                     }
-                    const bool last = k + 1 >= steps || (F32 && in_sum == kChunk - 1);
+                    const bool last = k + 1 >= steps || (CHUNKED && in_sum == kChunk - 1);
                     if (steps > 0) {
                         if (!landed) {
                             ok = __all_sync(0xffffffffu, wait(full + 8 * s, phase, p.wait_ns));
@@ -829,7 +834,7 @@ __global__ void __launch_bounds__(Shape<BN, KIND>::kThreads, Shape<BN, KIND>::kB
             const int64_t c0 = (int64_t)tn * BN + warp / 4 * S::kCols;
             const bool tail = KIND == kPair && unit >= p.whole;
             float *to = tail ? part_at(unit) : nullptr;
-            if constexpr (F32) {
+            if constexpr (CHUNKED) {
                 float sum[S::kCols / 32][32];
 #pragma unroll
                 for (int g = 0; g < S::kCols / 32; ++g)
@@ -1400,7 +1405,7 @@ int64_t tail_bytes(int64_t rows, int64_t cols, int64_t k, int sms) {
     return (int64_t)t.tiles * t.parts * kTailRows * kTailBN * 4;
 }
 
-template <int MODE, int BN, int KIND, bool F32>
+template <int MODE, int BN, int KIND, int SUMS>
 cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaStream_t s, int splits = 1) {
     using S = Shape<BN, KIND>;
     p.tiles_m = p.rows > 0 ? (int)ceil_div<int64_t>(p.rows, S::kRows) : 1;  // no rows: column sums alone
@@ -1413,7 +1418,7 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
         if (e == cudaSuccess) e = tensor_map(&p.b, b, MODE == kDgrad ? S::kBCols : kBK);
         if (e != cudaSuccess) return e;
     }
-    e = opt_in_smem<product_kernel<MODE, BN, KIND, F32>>((int)S::kSmem);
+    e = opt_in_smem<product_kernel<MODE, BN, KIND, SUMS>>((int)S::kSmem);
     if (e != cudaSuccess) return e;
     const int cluster = splits * S::kBlocks;
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, most = S::kIsSplit ? tiles : sms / S::kBlocks;
@@ -1437,14 +1442,14 @@ cudaError_t launch_tiles(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = KIND == kSingle ? 1 : 2;
-    e = cudaLaunchKernelEx(&cfg, product_kernel<MODE, BN, KIND, F32>, p);
+    e = cudaLaunchKernelEx(&cfg, product_kernel<MODE, BN, KIND, SUMS>, p);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess || tail.tiles == 0) return e;
-    return launch_pdl(join_tail_kernel<MODE, F32>, tail.tiles * (kTailBN / 32), kTailThreads, 0, s, p);
+    return launch_pdl(join_tail_kernel<MODE, SUMS == kF32>, tail.tiles * (kTailBN / 32), kTailThreads, 0, s, p);
 }
 
 // how many clusters of `blocks` blocks of a kernel the device holds at once (0: not known)
-template <int MODE, int BN, int KIND, bool F32>
+template <int MODE, int BN, int KIND, int SUMS>
 int64_t clusters_at_once(int blocks) {
     using S = Shape<BN, KIND>;
     static std::atomic<int> known[64][9] = {};
@@ -1452,7 +1457,7 @@ int64_t clusters_at_once(int blocks) {
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return 0;
     n = known[dev][blocks].load(std::memory_order_relaxed);
     if (n > 0) return n;
-    if (opt_in_smem<product_kernel<MODE, BN, KIND, F32>>((int)S::kSmem) != cudaSuccess) return 0;
+    if (opt_in_smem<product_kernel<MODE, BN, KIND, SUMS>>((int)S::kSmem) != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(S::kThreads);
@@ -1463,7 +1468,7 @@ int64_t clusters_at_once(int blocks) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, product_kernel<MODE, BN, KIND, F32>, &cfg) != cudaSuccess) n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, product_kernel<MODE, BN, KIND, SUMS>, &cfg) != cudaSuccess) n = 0;
     known[dev][blocks].store(n, std::memory_order_relaxed);
     return n;
 }
@@ -1488,15 +1493,15 @@ int64_t clusters_at_once(int blocks) {
 // 256 x 8192 x 2048 15.2 / 20.5, 256 x 8192 x 1536 13.0 / 18.5, 512 x 8192 x 512
 // 12.3 / 14.7; but 1024 x 2048 x 1024 9.6 / 9.4 with 32 steps, and 512 x 3712 x 2560
 // 20.8 / 13.3 with 40 clusters.
-template <int MODE, bool F32>
+template <int MODE, int SUMS>
 cudaError_t launch_width(Product &p, const Mat &a, const Mat &b, int sms, cudaStream_t s) {
     const int64_t tm = ceil_div<int64_t>(p.rows, kBM), narrow = tm * ceil_div<int64_t>(p.cols, 64);
     const bool skinny = MODE != kWgrad && p.rows <= kSkinnyRows;
     const int64_t pairs = ceil_div<int64_t>(p.rows, 2 * kBM) * ceil_div<int64_t>(p.cols, 128);
     if (tm > 1 && pairs * 4 <= sms)
         for (int n = 4; n >= 2; n /= 2)
-            if (p.k64 >= (n == 4 ? 64 : 48) && pairs <= clusters_at_once<MODE, 128, kPairSplit, F32>(2 * n))
-                return launch_tiles<MODE, 128, kPairSplit, F32>(p, a, b, sms, s, n);
+            if (p.k64 >= (n == 4 ? 64 : 48) && pairs <= clusters_at_once<MODE, 128, kPairSplit, SUMS>(2 * n))
+                return launch_tiles<MODE, 128, kPairSplit, SUMS>(p, a, b, sms, s, n);
     int splits = 1;
     while (splits < 8) {
         const bool one_each = narrow * splits * 2 <= sms && p.k64 >= 16 * splits;
@@ -1505,14 +1510,14 @@ cudaError_t launch_width(Product &p, const Mat &a, const Mat &b, int sms, cudaSt
         splits *= 2;
     }
     if constexpr (MODE != kWgrad)
-        if (splits > 1 && skinny) return launch_tiles<MODE, 64, kSkinny, F32>(p, a, b, sms, s, splits);
-    if (splits > 1) return launch_tiles<MODE, 64, kSplit, F32>(p, a, b, sms, s, splits);
-    if (tm * ceil_div<int64_t>(p.cols, 128) <= sms / 2) return launch_tiles<MODE, 64, kSingle, F32>(p, a, b, sms, s);
+        if (splits > 1 && skinny) return launch_tiles<MODE, 64, kSkinny, SUMS>(p, a, b, sms, s, splits);
+    if (splits > 1) return launch_tiles<MODE, 64, kSplit, SUMS>(p, a, b, sms, s, splits);
+    if (tm * ceil_div<int64_t>(p.cols, 128) <= sms / 2) return launch_tiles<MODE, 64, kSingle, SUMS>(p, a, b, sms, s);
     const bool few = tm * ceil_div<int64_t>(p.cols, 256) <= sms / 2;
     const bool one_wave = ceil_div<int64_t>(p.rows, 2 * kBM) * ceil_div<int64_t>(p.cols, 128) <= sms / 2;  // of pairs
-    if (p.k64 <= 4 || (few && (tm == 1 || !one_wave))) return launch_tiles<MODE, 128, kSingle, F32>(p, a, b, sms, s);
-    if (few) return launch_tiles<MODE, 128, kPair, F32>(p, a, b, sms, s);
-    return launch_tiles<MODE, 256, kPair, F32>(p, a, b, sms, s);
+    if (p.k64 <= 4 || (few && (tm == 1 || !one_wave))) return launch_tiles<MODE, 128, kSingle, SUMS>(p, a, b, sms, s);
+    if (few) return launch_tiles<MODE, 128, kPair, SUMS>(p, a, b, sms, s);
+    return launch_tiles<MODE, 256, kPair, SUMS>(p, a, b, sms, s);
 }
 
 // A single token's product: k among as many blocks as run at once, with a round
@@ -1581,7 +1586,8 @@ cudaError_t launch_product(const Mat &a, const Mat &b, int64_t rows, int64_t col
             return out.esz == 4 ? launch_token<true>(t, splits, s) : launch_token<false>(t, splits, s);
     }
     if (part_bytes > 0) p.partial = static_cast<float *>(space->take(part_bytes));  // without room: tiles whole
-    return out.esz == 4 ? launch_width<MODE, true>(p, a, b, sms, s) : launch_width<MODE, false>(p, a, b, sms, s);
+    if (out.esz == 4) return launch_width<MODE, kF32>(p, a, b, sms, s);
+    return k > kLongSum ? launch_width<MODE, kBf16Long>(p, a, b, sms, s) : launch_width<MODE, kBf16>(p, a, b, sms, s);
 }
 
 // the checkpoint's two arrays as matrices

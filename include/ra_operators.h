@@ -30,6 +30,11 @@
  *   - results do not change from call to call: every sum is added in an order
  *     that the sizes and the token ids alone decide.
  *   - NaN and infinities go through by the formulas.
+ *   - products are summed in binary32 by the tensor cores, which round toward
+ *     zero: a bf16 result over up to 16384 of k may be short by a fifth of half a
+ *     bf16 step where all products have one sign, and by far less where they
+ *     have not.  Longer sums, and binary32 results, are made in chunks of 512
+ *     that are added with rounding to nearest.
  *   - the products' kernels wait for their own copies and tensor-core work with
  *     the library's limit; ra_check_device_errors reports a wait that gave up.
  *   - the first call of each kind looks up a driver entry point and loads its
