@@ -247,8 +247,9 @@ def _kept(c, what, rows, cols, dev):
 
 
 def ra_checkpoint8_pack(x, out=None, stream=None) -> Checkpoint8:
-    """The 8-bit form of the matrix x (float32 or bfloat16): at most half a
-    step, 1/127.5 of a group's largest magnitude, off."""
+    """The 8-bit form of the matrix x (float32 or bfloat16): values are off by
+    at most half a step, 1/127.5 of a group's largest magnitude (three times
+    that in a group that reaches 255 * 2**120; see the C header)."""
     rows, cols = s = _shape(x, "x")
     dev = _device(x.get_device())
     p, ld, code = _matrix(x, "x", dev, None, s)
@@ -374,9 +375,10 @@ def ra_linear_dgrad(dy, w, saved=None, act="none", residual=None, dtype=None, ou
 def ra_linear_wgrad(x, dy, act="none", dtype=None, out=None, bias_grad=False, accumulate: bool = False, workspace=None, stream=None):
     """a.T @ dy, and with `bias_grad` also the column sums of dy: (dw, db).
     x is the layer's input [m, k] in bfloat16 (a = x) or the Checkpoint8 of z
-    (a = act(z)); dy [m, n] bfloat16.  `out` (dw) may be a view of a worker's
-    flat gradient; bias_grad True or a float32 vector of length n that receives
-    db; accumulate adds to both."""
+    (a = act(z), rounded to bfloat16 also where dw is float32); dy [m, n]
+    bfloat16.  `out` (dw) may be a view of a worker's flat gradient; bias_grad
+    True or a float32 vector of length n that receives db; accumulate adds to
+    both."""
     m, n = s = _shape(dy, "dy")
     dev = _device(dy.get_device())
     pd, ldd, _ = _matrix(dy, "dy", dev, _BF16, s)

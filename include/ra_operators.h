@@ -28,7 +28,8 @@
  *   - a size of zero is allowed: nothing to write is RA_OK without a launch, an
  *     empty sum is zero.
  *   - results do not change from call to call: every sum is added in an order
- *     that the sizes and the token ids alone decide.
+ *     that the sizes, the token ids, whether ws has the room that
+ *     ra_linear_split_bytes asks for, and the device's number of SMs alone decide.
  *   - NaN and infinities go through by the formulas.
  *   - products are summed in binary32 by the tensor cores, which round toward
  *     zero: a bf16 result over up to 16384 of k may be short by a fifth of half a
@@ -37,8 +38,15 @@
  *     that are added with rounding to nearest.
  *   - the products' kernels wait for their own copies and tensor-core work with
  *     the library's limit; ra_check_device_errors reports a wait that gave up.
- *   - the first call of each kind looks up a driver entry point and loads its
- *     kernels: make it before any stream capture.
+ *     What the blocks concerned would have stored keeps its former value.
+ *   - gelu, silu and their slopes are within 2^-20 of |z| (of 1 + |z| for a
+ *     slope); far out on gelu's negative side, where the values are that small
+ *     themselves, they do not keep their relative accuracy (0.2 % at z = -5).
+ *   - a call may be the first to look up a driver entry point, and loads the
+ *     kernels it is the first to launch; which these are depends on sizes, types,
+ *     row alignment, activation, and whether a checkpoint, a bias gradient and
+ *     the room for parts are there.  Before capturing a call, make the same call
+ *     once outside any stream capture.
  */
 #ifndef RA_OPERATORS_H
 #define RA_OPERATORS_H
@@ -64,10 +72,13 @@ typedef enum { RA_ACT_NONE = 0, RA_ACT_RELU = 1, RA_ACT_GELU = 2, RA_ACT_SILU = 
  *   e  rows * groups bytes; the step is 2^(e - 127)
  * with groups = ceil(cols / 32).  e is 6 below the (biased) exponent of the
  * group's largest magnitude, one more where that would round to 128 steps, and
- * between 1 and 248 (a group whose largest magnitude is 255 * 2^120 or more is
- * taken times 127/128, so that no restored value is infinite): the error is at most half a step, 1/127.5 of that magnitude.  A
- * power-of-two step makes every restored value exact in bf16 (and in
- * binary32), so the tensor cores read a checkpoint without a second rounding.
+ * between 1 and 248.  A value is off by at most half a step: 1/127.5 of that
+ * magnitude, or 2^-127 where the magnitude is below 2^-120.  Only a group whose
+ * largest magnitude is 255 * 2^120 or more, of which a restored value could be
+ * infinite, is taken times 127/128: there a value is off by at most 1.5 steps,
+ * 1/85 of the magnitude.  A power-of-two step makes every restored value exact
+ * in bf16 (and in binary32), so the tensor cores read a checkpoint without a
+ * second rounding.
  * A group with an infinity or a NaN is marked (e = 255, q = 0) and reads back as
  * NaN throughout, so that such a value is not lost.
  */
@@ -155,7 +166,9 @@ ra_status ra_linear_dgrad(const void *dy, int64_t ld_dy, const void *w, int64_t 
  *   z_q, z_e  the 8-bit checkpoint of z (m x k): a = act(z), recomputed here
  *             (act is RA_ACT_NONE with x); an empty checkpoint's pointers may
  *             be NULL too.  With RA_ACT_NONE a is exact; else act(z) is
- *             rounded to bf16 for the tensor cores
+ *             rounded to bf16 for the tensor cores, whatever type dw has: the
+ *             forward layer's own product read its input rounded so, and a
+ *             second product over what the rounding drops would double the work
  *   dy        m x n, bf16
  *   dw        k x n of dw_dtype; accumulate != 0 adds to it (micro-batches)
  *   db        n binary32 values, or NULL; accumulate holds for it too

@@ -92,3 +92,27 @@ def test_table_gradient_of_very_wide_rows(d, out_type):
     ra.ra_embedding_grad(grad, ids, vocab, out=got, accumulate=True)
     assert torch.equal(got.float(), 2 * want)
     assert torch.equal(ra.ra_embedding_lookup(got, ids[:1]).float(), 2 * want[:1])
+
+
+@pytest.mark.parametrize("top_steps", [100.0, 127.25, 127.5, 127.75, 127.99999])
+@pytest.mark.parametrize("power", [-126, -120, 0, 100, 120, 121])
+def test_checkpoint_error_by_magnitude(top_steps, power):
+    """Off by at most half a step, also where the step is held at 2^-126; at the very top of binary32, where a group is taken
+    times 127/128, by 1.5 steps (the scaling's 128 / 128 and the rounding's half)."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = (torch.rand(64, 32, generator=g, device="cuda", dtype=torch.float64) * 2 - 1) * top_steps
+    x[:, 3] = top_steps
+    x[::2, 7] = -top_steps + 0.25
+    x = (x * 2.0 ** power).float()
+    assert bool(torch.isfinite(x).all())
+    kept = ra.ra_checkpoint8_pack(x)
+    back = ra.ra_checkpoint8_unpack(kept, dtype=F32).double()
+    assert bool(torch.isfinite(back).all())
+    step = torch.exp2(kept.e.double() - 127).repeat_interleave(32, 1)
+    scaled = x.abs().amax(1, keepdim=True).double() >= 255 * 2.0 ** 120
+    limit = torch.where(scaled, 1.5, 0.5) * step
+    off = (back - x.double()).abs()
+    assert bool((off <= limit).all())
+    assert bool(scaled.any()) == (power == 121 and top_steps >= 127.5)
+    top = x.abs().amax(1, keepdim=True).double()
+    assert bool((off <= torch.where(scaled, top / 85, torch.clamp(top / 127.5, min=2.0 ** -127))).all())

@@ -65,3 +65,14 @@ def test_tensors_on_another_device_than_the_current_one_are_refused(monkeypatch)
                  lambda: op.ra_linear_wgrad(x, x, out=w)):
         with pytest.raises(ValueError, match="cuda:1"):
             call()
+
+
+def test_column_slices_side_by_side(lib):
+    """x and y as column slices of one array: side by side they are fine (the call then asks for the workspace that rows 57
+    values apart need), a column into each other they overlap; so do slices of arrays with another stride."""
+    def linear(at, ld=57):
+        return lib.ra_linear(A, 57, B, 32, 16, 24, 32, None, F32, 0, None, 0, F32, None, None, A + 2 * at, ld, BF16, None, 0, None)
+
+    assert linear(24) == INVALID and linear(25) == INVALID
+    assert linear(23) == OVERLAP and linear(26) == OVERLAP  # into x's columns; into those of x's next row
+    assert linear(24, 58) == OVERLAP
