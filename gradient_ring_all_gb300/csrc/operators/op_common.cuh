@@ -46,14 +46,14 @@ inline bool mat_ok(const Mat &a) {
 }
 
 // Whether two matrices share a byte.  Views with one pitch (column slices of
-// one array) interleave without sharing any; every other pair is judged by
-// the byte ranges that it spans.
+// one array) interleave without sharing any, and a single row can lie between
+// another's; every other pair is judged by the byte ranges that it spans.
 inline bool mats_overlap(const Mat &a, const Mat &b) {
     if (a.empty() || b.empty()) return false;
     const uintptr_t pa = reinterpret_cast<uintptr_t>(a.data), pb = reinterpret_cast<uintptr_t>(b.data);
     if (pa + (uintptr_t)a.span() <= pb || pb + (uintptr_t)b.span() <= pa) return false;
-    if (a.pitch() == b.pitch() && a.rows > 1 && b.rows > 1) {
-        const int64_t pitch = a.pitch();
+    const int64_t pitch = a.rows > 1 ? a.pitch() : b.pitch();
+    if ((a.rows > 1 || b.rows > 1) && (a.rows <= 1 || b.rows <= 1 || a.pitch() == b.pitch())) {
         const int64_t d = pb >= pa ? (int64_t)((pb - pa) % (uintptr_t)pitch)
                                    : (pitch - (int64_t)((pa - pb) % (uintptr_t)pitch)) % pitch;
         if (d >= a.row_bytes() && d + b.row_bytes() <= pitch) return false;

@@ -76,3 +76,18 @@ def test_column_slices_side_by_side(lib):
     assert linear(24) == INVALID and linear(25) == INVALID
     assert linear(23) == OVERLAP and linear(26) == OVERLAP  # into x's columns; into those of x's next row
     assert linear(24, 58) == OVERLAP
+
+
+def test_a_single_row_between_another_matrix_rows(lib):
+    """A vector, or one row, in the gap between the rows of an output shares no byte with it (the call then asks for the
+    workspace that rows 57 values apart need); one that reaches into the next row does."""
+    def linear(bias, n=32, ldy=100):
+        return lib.ra_linear(A, 57, B, n, 16, 24, n, bias, BF16, 0, None, 0, F32, None, None, C, ldy, BF16, None, 0, None)
+
+    assert linear(C + 2 * 32) == INVALID and linear(C + 2 * 68) == INVALID and linear(C + 2 * 332) == INVALID
+    assert linear(C + 2 * 31) == OVERLAP and linear(C + 2 * 69) == OVERLAP and linear(C) == OVERLAP and linear(C + 2 * 100) == OVERLAP
+    # in front of the first row and behind the last one it is elsewhere
+    assert linear(C - 2 * 32) == INVALID and linear(C + 2 * (15 * 100 + 32)) == INVALID
+    assert linear(C - 2 * 31) == OVERLAP and linear(C + 2 * (15 * 100 + 31)) == OVERLAP
+    # a row as long as the distance of the other's rows or longer fits no gap
+    assert linear(C + 2 * 64, n=64, ldy=100) == OVERLAP
