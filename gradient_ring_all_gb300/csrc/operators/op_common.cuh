@@ -37,12 +37,12 @@ struct Mat {
 constexpr int64_t kMaxExtent = (int64_t)1 << 31;  // rows and columns stay below 2^31
 constexpr int64_t kMaxSpan = (int64_t)1 << 46;    // so that no byte offset can wrap
 
-inline bool mat_ok(const Mat &a) {
+inline bool size_ok(const Mat &a) {
     if (a.rows < 0 || a.cols < 0 || a.rows >= kMaxExtent || a.cols >= kMaxExtent) return false;
-    if (a.empty()) return true;
-    if (a.rows > 1 && a.ld < a.cols) return false;
-    if (a.data == nullptr || reinterpret_cast<uintptr_t>(a.data) % a.esz != 0) return false;
-    return a.rows <= 1 || a.ld <= kMaxSpan / a.rows / a.esz;
+    return a.rows <= 1 || a.cols == 0 || (a.ld >= a.cols && a.ld <= kMaxSpan / a.rows / a.esz);
+}
+inline bool mat_ok(const Mat &a) {
+    return size_ok(a) && (a.empty() || (a.data != nullptr && reinterpret_cast<uintptr_t>(a.data) % a.esz == 0));
 }
 
 // Whether two matrices share a byte.  Views with one pitch (column slices of

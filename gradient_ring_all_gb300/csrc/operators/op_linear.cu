@@ -1294,7 +1294,10 @@ bool tma_readable(const Mat &a) { return a.aligned(16) && (a.rows <= 1 || a.pitc
 
 // rows of whole sectors (TMA asks for 16 bytes, restoring a checkpoint for 32)
 int64_t laid_out_ld(int64_t cols) { return ceil_div<int64_t>(cols, 16) * 16; }
-int64_t laid_out_bytes(int64_t rows, int64_t cols) { return ceil_div<int64_t>(rows * laid_out_ld(cols) * 2, 256) * 256; }
+int64_t laid_out_bytes(int64_t rows, int64_t cols) {
+    if (rows > 0 && laid_out_ld(cols) > 2 * kMaxSpan / rows) return 4 * kMaxSpan;  // of a matrix that no call takes
+    return ceil_div<int64_t>(rows * laid_out_ld(cols) * 2, 256) * 256;
+}
 
 // The caller's workspace, handed out front to back from its first 32-byte
 // boundary on.
@@ -1598,7 +1601,7 @@ struct Kept {
 Kept kept_mats(const int8_t *q, const uint8_t *e, int64_t rows, int64_t cols) {
     const int64_t groups = ceil_div<int64_t>(cols, kGroup);
     Kept k{{q, rows, groups * kGroup, groups * kGroup, 1}, {e, rows, groups, groups, 1}, true};
-    k.ok = q != nullptr && e != nullptr && reinterpret_cast<uintptr_t>(q) % 16 == 0;
+    k.ok = q != nullptr && e != nullptr && reinterpret_cast<uintptr_t>(q) % 16 == 0 && (k.q.empty() || k.q.pitch() <= kMaxSpan / rows);
     return k;
 }
 
@@ -1613,6 +1616,8 @@ extern "C" {
 
 size_t ra_linear_workspace_bytes(int64_t m, int64_t k, int64_t n) {
     if (m < 0 || k < 0 || n < 0 || m >= kMaxExtent || k >= kMaxExtent || n >= kMaxExtent) return 0;
+    for (const Mat &a : {Mat{nullptr, m, k, k, 2}, Mat{nullptr, k, n, n, 2}, Mat{nullptr, m, n, n, 2}})
+        if (!size_ok(a)) return 0;
     // at most two of the three matrices are laid out in one call
     const int64_t mk = laid_out_bytes(m, k), kn = laid_out_bytes(k, n), mn = laid_out_bytes(m, n);
     const int64_t least = mk < kn ? (mk < mn ? mk : mn) : (kn < mn ? kn : mn);

@@ -91,3 +91,14 @@ def test_a_single_row_between_another_matrix_rows(lib):
     assert linear(C - 2 * 31) == OVERLAP and linear(C + 2 * (15 * 100 + 31)) == OVERLAP
     # a row as long as the distance of the other's rows or longer fits no gap
     assert linear(C + 2 * 64, n=64, ldy=100) == OVERLAP
+
+
+def test_workspace_of_sizes_that_no_call_takes(lib):
+    """Matrices past 2^46 bytes are refused by the calls; the questions about their workspaces answer 0."""
+    big = (1 << 31) - 1
+    for m, k, n in ((big, big, 1), (1, big, big), (big, 1, big), (big, big, big), (1 << 23, 1 << 23, 8)):
+        assert lib.ra_linear_workspace_bytes(m, k, n) == 0
+    assert lib.ra_linear(A, big, B, 1, big, big, 1, None, F32, 0, None, 0, F32, None, None, C, 1, BF16, W, 1 << 24, None) == INVALID
+    # the largest that is taken: two matrices laid out, rows of whole 32 bytes
+    assert lib.ra_linear_workspace_bytes(1 << 22, 1 << 22, 7) == (1 << 45) + (1 << 22) * 32 + 32
+    assert lib.ra_linear_workspace_bytes(5, 7, 9) == 2 * 256 + 32
