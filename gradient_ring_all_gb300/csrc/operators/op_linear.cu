@@ -14,12 +14,13 @@
 //
 // A step of 64 k of a pair's 256 x 256 tile is 512 clocks of the tensor core and
 // 64 KB of loads; 7 such steps are in flight.  Large products run into the
-// power limit: 8192 x 2048 x 8192 144-150 us (1.83-1.9 PFLOP/s), 8192 x 8192 x
-// 2048 145-162 us, 8192^3 635 us on normal values and 473 us on zeros (2.3
-// PFLOP/s at 2070 MHz).  Small ones are bound by the rate at which an SM takes
-// tiles in and by a launch's start: one 64-column step alone takes 3 us, of
-// which the first loads take 0.9 and the epilogue 0.7.  A single token's forward
-// product has a kernel of its own.
+// power limit, the more the warmer the GPU is: on normal values, without a
+// residual, 8192 x 2048 x 8192 takes 148-165 us, 8192 x 8192 x 2048 149-169 us,
+// 8192^3 550-630 us; on zeros 127, 131 and 469 us (2.34 PFLOP/s at 2070 MHz).
+// Small ones are bound by the rate at which an SM takes tiles in and by a
+// launch's start: one 64-column step alone takes 3 us, of which the first loads
+// take 0.9 and the epilogue 0.7.  A single token's forward product has a kernel
+// of its own.
 #include <cuda.h>
 
 #include <cooperative_groups.h>
@@ -1392,7 +1393,8 @@ cudaError_t launch_column_sum(const Mat &dy, int accumulate, float *db, cudaStre
 // The last wave of the pairs' 256 x 256 tiles: how many there are, and in how
 // many parts each is made.  In parts where these find SMs that would idle, and
 // the steps saved are worth the sums' way through memory and a launch (about 8
-// us): 8192 x 8192 x 2048, 256 tiles on 76 pairs, 161 us instead of 172.
+// us): 8192 x 8192 x 2048, 256 tiles on 76 pairs, 131 us instead of 142 on zeros and 167
+// instead of 181 on normal values.
 struct Tail {
     int tiles, parts;
 };
