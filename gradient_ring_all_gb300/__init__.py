@@ -1,6 +1,7 @@
 """Python binding of the GB300 ring all-reduce library (C ABI in
 ``include/ring_allreduce.h``; the training-step operators of
-``include/ra_operators.h`` are bound in ``operators.py`` and offered here).
+``include/ra_operators.h`` are bound in ``operators.py`` and
+``block_operators.py`` and offered here).
 
 The functions carry the C names and only marshal arguments: every step of
 the all-reduce runs in the library's CUDA kernels.  PyTorch supplies device
@@ -30,6 +31,7 @@ __all__ = [
     "ra_last_cuda_error", "RA_OK", "RA_ERR_TIMEOUT", "RA_ERR_BOUNDS", "CHECKED",
     "Checkpoint8", "ra_checkpoint8_pack", "ra_checkpoint8_unpack", "ra_embedding_lookup", "ra_embedding_grad",
     "ra_linear", "ra_linear_dgrad", "ra_linear_wgrad", "ra_selftest_linear_stall",
+    "ra_dropout", "Norm", "NormBlockGrads", "ra_norm_block", "ra_norm_block_grad", "LogProbs", "ra_logprobs", "ra_logprobs_grad",
 ]
 
 RA_F32 = 0
@@ -409,17 +411,23 @@ def ra_last_cuda_error() -> int:
 
 
 # ---------------------------------------------------------------------------
-# the training-step operators (operators.py), imported on first use: the ring's
-# calls and the build need no torch
+# the training-step operators, imported on first use: the ring's calls and the
+# build need no torch
 
-_OPERATORS = ("Checkpoint8", "ra_checkpoint8_pack", "ra_checkpoint8_unpack", "ra_embedding_lookup", "ra_embedding_grad",
-              "ra_linear", "ra_linear_dgrad", "ra_linear_wgrad", "ra_selftest_linear_stall")
+_OPERATORS = {
+    "operators": ("Checkpoint8", "ra_checkpoint8_pack", "ra_checkpoint8_unpack", "ra_embedding_lookup", "ra_embedding_grad",
+                  "ra_linear", "ra_linear_dgrad", "ra_linear_wgrad", "ra_selftest_linear_stall"),
+    "block_operators": ("ra_dropout", "Norm", "NormBlockGrads", "ra_norm_block", "ra_norm_block_grad", "LogProbs", "ra_logprobs",
+                        "ra_logprobs_grad"),
+}
 
 
 def __getattr__(name):
-    if name in _OPERATORS:
-        from . import operators
-        for nm in _OPERATORS:
-            globals()[nm] = getattr(operators, nm)
-        return globals()[name]
+    for module, names in _OPERATORS.items():
+        if name in names:
+            import importlib
+            found = importlib.import_module("." + module, __name__)
+            for nm in names:
+                globals()[nm] = getattr(found, nm)
+            return globals()[name]
     raise AttributeError("module %r has no attribute %r" % (__name__, name))

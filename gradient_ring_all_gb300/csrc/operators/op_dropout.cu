@@ -1,0 +1,218 @@
+// op_dropout.cu -- values dropped by a counter-based generator, with the
+// residual they are added to: ra_dropout.
+//
+// y = residual + (u >= t ? x * scale : 0), u 16 bits of Philox4x32-10 (Salmon,
+// Moraes, Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011)
+// for the counter (column / 8, site, row) under the seed.  One evaluation makes
+// the bits of 8 neighbouring values, so the mask costs 5 integer operations a
+// value and no memory.  16 bits a value keep the drop probability to a
+// 65536th; the scale is that of the rounded probability, so the mean is exact.
+#include "op_common.cuh"
+
+namespace ra {
+namespace op {
+namespace {
+
+constexpr int kDropThreads = 256;
+constexpr int kDropFlight = 4;  // groups of 8 a thread has in flight
+
+// u / d for any 32-bit u by a multiplication: with s = ceil(log2 d) and
+// m = floor(2^32 (2^s - d) / d) + 1, u / d = (umulhi(u, m) + u) >> s without
+// the sum's overflow (Granlund and Montgomery, "Division by invariant integers
+// using multiplication", 1994).
+struct Divisor {
+    uint32_t d, m;
+    int s1, s2;
+    explicit Divisor(uint32_t by) : d(by) {
+        int s = 0;
+        while (((uint64_t)1 << s) < by) ++s;
+        m = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << s) - by)) / by + 1);
+        s1 = s < 1 ? s : 1;
+        s2 = s < 1 ? 0 : s - 1;
+    }
+    __device__ __forceinline__ uint32_t of(uint32_t u) const {
+        const uint32_t h = __umulhi(u, m);
+        return (h + ((u - h) >> s1)) >> s2;
+    }
+};
+
+struct DropParams {
+    const void *x, *residual;
+    void *y;
+    const uint64_t *seed_at;
+    int64_t ldx, ldr, ldy, rows, cols, first_row;
+    int64_t units, per_row;  // pieces of work, and how many a row has
+    Divisor by;              // per_row
+    uint64_t seed;
+    uint32_t site, t;  // a value is kept where its 16 bits are >= t
+    float scale;
+};
+
+__device__ __forceinline__ uint4 philox(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0, uint32_t k1) {
+#pragma unroll
+    for (int round = 0; round < 10; ++round) {
+        const uint64_t a = (uint64_t)0xD2511F53u * c0, b = (uint64_t)0xCD9E8D57u * c2;
+        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c1 = (uint32_t)b;
+        c3 = (uint32_t)a;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return make_uint4(c0, c1, c2, c3);
+}
+
+// the bits of group g of row r
+__device__ __forceinline__ uint4 bits_of(const DropParams &p, uint64_t seed, int64_t r, uint32_t g) {
+    const uint64_t row = (uint64_t)(p.first_row + r);
+    return philox(g, p.site, (uint32_t)row, (uint32_t)(row >> 32), (uint32_t)seed, (uint32_t)(seed >> 32));
+}
+
+// whether value j of a group is kept
+__device__ __forceinline__ bool kept_of(const uint4 &w, int j, uint32_t t) {
+    const uint32_t word = j < 4 ? (j < 2 ? w.x : w.y) : (j < 6 ? w.z : w.w);
+    return (j & 1 ? word >> 16 : word & 0xffffu) >= t;
+}
+
+__device__ __forceinline__ uint64_t seed_of(const DropParams &p) { return p.seed + (p.seed_at ? *p.seed_at : 0); }
+
+// A unit's row and its place in the row.
+__device__ __forceinline__ void place_of(const DropParams &p, int64_t u, int64_t *r, int64_t *k) {
+    if (p.units <= 0xffffffffll) {
+        *r = p.by.of((uint32_t)u);
+        *k = (uint32_t)u - (uint32_t)*r * (uint32_t)p.per_row;
+    } else {
+        *r = u / p.per_row;
+        *k = u - *r * p.per_row;
+    }
+}
+
+// TR: the residual's type, void for none
+template <class TR>
+struct Residual {
+    using T = TR;
+    static constexpr bool on = true;
+};
+template <>
+struct Residual<void> {
+    using T = float;
+    static constexpr bool on = false;
+};
+
+// Rows on 16-byte boundaries, whole groups: a thread takes groups, kDropFlight
+// in flight, by 16-byte accesses.
+template <class TX, class TR, class TY>
+__global__ void __launch_bounds__(kDropThreads) dropout_kernel(const DropParams p) {
+    pdl_enter();
+    using R = Residual<TR>;
+    const uint64_t seed = seed_of(p);
+    constexpr int64_t kPer = kDropThreads * kDropFlight;
+    for (int64_t u0 = (int64_t)blockIdx.x * kPer + threadIdx.x; u0 < p.units; u0 += (int64_t)gridDim.x * kPer) {
+        Raw<TX, 8> x[kDropFlight];
+        Raw<typename R::T, 8> res[kDropFlight];
+        int64_t r[kDropFlight], k[kDropFlight];
+#pragma unroll
+        for (int j = 0; j < kDropFlight; ++j) {
+            const int64_t u = u0 + j * kDropThreads;
+            if (u < p.units) {
+                place_of(p, u, &r[j], &k[j]);
+                x[j].load(static_cast<const TX *>(p.x) + r[j] * p.ldx + k[j] * 8);
+                if constexpr (R::on) res[j].load(static_cast<const typename R::T *>(p.residual) + r[j] * p.ldr + k[j] * 8);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kDropFlight; ++j) {
+            if (u0 + j * kDropThreads >= p.units) break;
+            const uint4 w = bits_of(p, seed, r[j], (uint32_t)k[j]);
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                y[i] = kept_of(w, i, p.t) ? x[j][i] * p.scale : 0.0f;
+                if constexpr (R::on) y[i] += res[j][i];
+            }
+            store_w<TY, 8>(static_cast<TY *>(p.y) + r[j] * p.ldy + k[j] * 8, y);
+        }
+    }
+}
+
+// Any stride, width and alignment: a warp takes 256 neighbouring columns of a
+// row.  A lane makes the bits of one group, and the lanes read and write the
+// groups' values side by side.
+template <class TX, class TR, class TY>
+__global__ void __launch_bounds__(kDropThreads) dropout_scalar_kernel(const DropParams p) {
+    pdl_enter();
+    using R = Residual<TR>;
+    const uint64_t seed = seed_of(p);
+    const int lane = threadIdx.x & 31;
+    const int64_t step = (int64_t)gridDim.x * (kDropThreads / 32);
+    for (int64_t u = (int64_t)blockIdx.x * (kDropThreads / 32) + threadIdx.x / 32; u < p.units; u += step) {
+        int64_t r, k;
+        place_of(p, u, &r, &k);
+        const int64_t c0 = k * 256 + lane;
+        Raw<TX, 1> x[8];
+        Raw<typename R::T, 1> res[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t c = c0 + 32 * j;
+            if (c >= p.cols) break;
+            x[j].load(static_cast<const TX *>(p.x) + r * p.ldx + c);
+            if constexpr (R::on) res[j].load(static_cast<const typename R::T *>(p.residual) + r * p.ldr + c);
+        }
+        const uint4 w = bits_of(p, seed, r, (uint32_t)(k * 32 + lane));
+        uint32_t mine = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mine |= kept_of(w, j, p.t) ? 1u << j : 0u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t group = __shfl_sync(0xffffffffu, mine, 4 * j + lane / 8);
+            const int64_t c = c0 + 32 * j;
+            if (c < p.cols) {
+                float y = (group >> (lane % 8)) & 1 ? x[j][0] * p.scale : 0.0f;
+                if constexpr (R::on) y += res[j][0];
+                static_cast<TY *>(p.y)[r * p.ldy + c] = from_f32<TY>(y);
+            }
+        }
+    }
+}
+
+template <class TX, class TR, class TY>
+cudaError_t launch_drop(const DropParams &p, bool wide, cudaStream_t s) {
+    const int64_t blocks = ceil_div<int64_t>(p.units, wide ? kDropThreads * kDropFlight : kDropThreads / 32);
+    const int64_t grid = blocks < kMaxGrid ? blocks : kMaxGrid;
+    return launch_pdl(wide ? dropout_kernel<TX, TR, TY> : dropout_scalar_kernel<TX, TR, TY>, grid, kDropThreads, 0, s, p);
+}
+
+template <class TX, class TY>
+cudaError_t launch_drop(const DropParams &p, int res_dtype, bool wide, cudaStream_t s) {
+    if (p.residual == nullptr) return launch_drop<TX, void, TY>(p, wide, s);
+    return res_dtype == RA_F32 ? launch_drop<TX, float, TY>(p, wide, s) : launch_drop<TX, uint16_t, TY>(p, wide, s);
+}
+
+}  // namespace
+}  // namespace op
+}  // namespace ra
+
+extern "C" ra_status ra_dropout(const void *x, int64_t ld_x, int x_dtype, int64_t rows, int64_t cols, double p, uint64_t seed,
+                                const uint64_t *seed_at, uint32_t site, int64_t first_row, const void *residual, int64_t ld_res,
+                                int res_dtype, void *y, int64_t ld_y, int y_dtype, void *stream) {
+    using namespace ra;
+    using namespace ra::op;
+    if (esize(x_dtype) == 0 || esize(y_dtype) == 0 || (residual != nullptr && esize(res_dtype) == 0)) return RA_ERR_INVALID_ARG;
+    if (!(p >= 0.0 && p <= 1.0) || first_row < 0 || reinterpret_cast<uintptr_t>(seed_at) % 8 != 0) return RA_ERR_INVALID_ARG;
+    const Mat a{x, rows, cols, ld_x, esize(x_dtype)}, b{y, rows, cols, ld_y, esize(y_dtype)};
+    const Mat c{residual, residual ? rows : 0, cols, ld_res, residual ? esize(res_dtype) : 4};
+    if (!mat_ok(a) || !mat_ok(b) || !mat_ok(c) || first_row > INT64_MAX - rows) return RA_ERR_INVALID_ARG;
+    if (a.empty()) return RA_OK;
+    const Mat at{seed_at, seed_at ? 1 : 0, 1, 1, 8};
+    if ((mats_overlap(a, b) && !same_mat(a, b)) || (mats_overlap(c, b) && !same_mat(c, b)) || mats_overlap(at, b)) return RA_ERR_OVERLAP;
+    const bool wide = cols % 8 == 0 && a.aligned(16) && b.aligned(16) && (residual == nullptr || c.aligned(16));
+    const int64_t per_row = wide ? cols / 8 : ceil_div<int64_t>(cols, 256);
+    const uint32_t t = (uint32_t)nearbyint(65536.0 * p);
+    const DropParams q{x, residual, y, seed_at, ld_x, ld_res, ld_y, rows, cols, first_row, rows * per_row, per_row, Divisor((uint32_t)per_row),
+                       seed, site, t, t < 65536 ? (float)(65536.0 / (65536 - (int)t)) : 0.0f};
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (x_dtype == RA_F32)
+        return cuda_status(y_dtype == RA_F32 ? launch_drop<float, float>(q, res_dtype, wide, s) : launch_drop<float, uint16_t>(q, res_dtype, wide, s));
+    return cuda_status(y_dtype == RA_F32 ? launch_drop<uint16_t, float>(q, res_dtype, wide, s)
+                                         : launch_drop<uint16_t, uint16_t>(q, res_dtype, wide, s));
+}

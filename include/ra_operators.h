@@ -10,6 +10,11 @@
  *   ra_linear_wgrad        act(z)^T dy and the column sums of dy
  *   ra_checkpoint8_pack    an activation kept in 8 bits
  *   ra_checkpoint8_unpack  and restored
+ *   ra_dropout             values dropped by a counter-based generator, + residual
+ *   ra_norm_block          the join behind a block and the norm before the next
+ *   ra_norm_block_grad     its gradients
+ *   ra_logprobs            log probabilities of given tokens, entropy, alternatives
+ *   ra_logprobs_grad       the logits' gradient
  *
  * The layers are those of the Transformer whose gradients the library's
  * workloads average ("How GPipe works", section 1: embedding V x d, weights
@@ -189,6 +194,185 @@ ra_status ra_linear_wgrad(const void *x, int64_t ld_x, const int8_t *z_q, const 
  * was, but for db, which waits for nothing.
  */
 ra_status ra_selftest_linear_stall(int block, int timeout_us);
+
+/*
+ * ra_dropout -- y = residual + (kept ? x * 1/(1-p) : 0), a value kept or dropped
+ * by 16 bits that its place and the seed alone decide: the mask is never stored.
+ * The gradient with respect to x is the same call on dy without a residual; a
+ * recomputation in the backward pass, and a micro-batch of a larger batch
+ * (first_row), meet the same mask again.
+ *   x         rows x cols of x_dtype
+ *   p         in [0, 1]: a value is dropped with probability t / 65536, t =
+ *             65536 p rounded to a whole number (ties to even), and the others are
+ *             scaled by 65536 / (65536 - t), so that the mean is kept exactly.
+ *             Nothing is kept at t = 65536.  What is dropped counts as 0, whatever
+ *             it holds.
+ *   seed      the generator's key; with seed_at (8-byte aligned device memory, or
+ *             NULL) the 64-bit number found there when the kernel runs is added to
+ *             it, so that a captured call takes another mask at each replay
+ *   site      tells the calls of one step apart
+ *   first_row, >= 0: row r of x is row first_row + r of the mask
+ *   residual  rows x cols of res_dtype, or NULL
+ *   y         rows x cols of y_dtype, rounded once; may be x or the residual itself
+ *             (same address, ld and type)
+ * The bits: Philox4x32-10 (Salmon, Moraes, Dror and Shaw 2011) under the key (low,
+ * high word of the seed) makes four words of the counter (column / 8, site, low,
+ * high word of the row); column 8 g + j takes the low half of word j / 2 where j
+ * is even, the high half where it is odd; a value is kept where they are t or more.
+ */
+ra_status ra_dropout(const void *x, int64_t ld_x, int x_dtype, int64_t rows, int64_t cols, double p, uint64_t seed,
+                     const uint64_t *seed_at, uint32_t site, int64_t first_row, const void *residual, int64_t ld_res,
+                     int res_dtype, void *y, int64_t ld_y, int y_dtype, void *stream);
+
+/* A norm over a row v of d values: (v - m) * rstd * gain + bias,
+ *   m = mean of v (RA_NORM_LAYER) or 0 (RA_NORM_RMS), rstd = (mean of (v - m)^2 + eps)^-1/2.
+ * Moments are binary32, the second one of the differences from the first. */
+typedef enum { RA_NORM_NONE = 0, RA_NORM_LAYER = 1, RA_NORM_RMS = 2 } ra_norm_kind;
+#define RA_NORM_MAX_D 32768
+
+typedef struct {
+    const void *gain; /* d values of dtype, or NULL: ones */
+    const void *bias; /* d values of dtype, or NULL: zeros */
+    int dtype;        /* of both */
+    int kind;         /* ra_norm_kind; RA_NORM_NONE: no norm, the rest is not looked at */
+    float eps;        /* >= 0 */
+    int reserved;     /* 0 */
+} ra_norm;
+
+typedef enum { RA_GATE_NONE = 0, RA_GATE_VECTOR = 1, RA_GATE_MATRIX = 2 } ra_gate_kind;
+
+/*
+ * ra_norm_block -- what lies between two blocks of a layer, in one pass over its
+ * rows:
+ *   x' = alpha x + beta gate * post(f),   h = pre(x')
+ * x is the residual stream, f the output of the block behind, h the input of the
+ * block ahead.  x' is rounded to its type and pre() is that of the rounded row, so
+ * that h is what a call of its own would make of x' and the backward pass, which
+ * reads x', differentiates what was computed.
+ *   f      NULL: x' is x, x_out is not written, and only pre() is computed
+ *   post   RA_NORM_NONE: f itself;  pre  RA_NORM_NONE: no h (only with f)
+ *   gate   d values of gate_dtype, or rows x d of f_dtype; RA_GATE_NONE: ones
+ *   x_out  rows x d of x_dtype; may be x itself (same address and ld)
+ *   h      rows x d of f_dtype, which is the type of f too
+ *   kept   4 values a row, contiguous and 16-byte aligned, or NULL: m and rstd of
+ *          post and of pre (zeros where there is no such norm), for the backward pass
+ * x_dtype and f_dtype: both RA_F32, both RA_BF16, or RA_F32 and RA_BF16.
+ * d is at most RA_NORM_MAX_D (RA_ERR_UNSUPPORTED).
+ */
+typedef struct {
+    int64_t rows, d;
+    const void *x;
+    int64_t ld_x;
+    const void *f;
+    int64_t ld_f;
+    const void *gate;
+    int64_t ld_gate; /* of a matrix */
+    void *x_out;
+    int64_t ld_x_out;
+    void *h;
+    int64_t ld_h;
+    float *kept;
+    ra_norm post, pre;
+    int x_dtype, f_dtype, gate_kind, gate_dtype; /* gate_dtype: of a vector */
+    float alpha, beta;
+} ra_norm_block_args;
+
+ra_status ra_norm_block(const ra_norm_block_args *args, void *stream);
+
+/*
+ * ra_norm_block_grad -- the gradients of ra_norm_block, from dh (of h) and dx_new
+ * (of x', what the later part of the stream sends back).  With v = (x' - m) rstd of
+ * pre and w = (f - m) rstd of post:
+ *   D  = dx_new + the gradient of pre() with respect to x'
+ *   dx = alpha D  (D where there is no f),   dgate = beta D post(f)
+ *   df = the gradient of post() for  u = beta gate D
+ *   dpre_gain = sum of dh v,  dpre_bias = sum of dh,  dpost_gain = sum of u w,
+ *   dpost_bias = sum of u, sums over the rows
+ *   dh     rows x d of f_dtype; NULL exactly where pre is RA_NORM_NONE
+ *   dx_new rows x d of x_dtype, or NULL: zeros (not where dh is NULL too)
+ *   x      x' as ra_norm_block left it (or took it, without an f); not read without pre
+ *   f, gate, kept, post, pre, alpha, beta  as there
+ *   dx     rows x d of x_dtype, may be dx_new itself;  df  rows x d of f_dtype
+ *   dgate  d binary32 values (a vector's: summed over the rows), or rows x d of
+ *          f_dtype (a matrix's)
+ *   dpost_gain, ...  d binary32 values each, 4-byte aligned
+ *   accumulate != 0 adds to the vectors of d values (micro-batches); dx, df and a
+ *          matrix's dgate are always overwritten
+ * Any output may be NULL; then it is not made.  With rows 0 the vectors become 0
+ * (or stay, with accumulate), whatever parts there are.  ws: device workspace of
+ * at least ra_norm_block_grad_workspace_bytes(rows, d), 16-byte aligned, where a
+ * vector of sums is wanted; else it may be NULL.
+ */
+typedef struct {
+    int64_t rows, d;
+    const void *dh;
+    int64_t ld_dh;
+    const void *dx_new;
+    int64_t ld_dx_new;
+    const void *x;
+    int64_t ld_x;
+    const void *f;
+    int64_t ld_f;
+    const void *gate;
+    int64_t ld_gate;
+    const float *kept;
+    void *dx;
+    int64_t ld_dx;
+    void *df;
+    int64_t ld_df;
+    void *dgate;
+    int64_t ld_dgate;
+    float *dpost_gain, *dpost_bias, *dpre_gain, *dpre_bias;
+    void *ws;
+    size_t ws_bytes;
+    ra_norm post, pre;
+    int x_dtype, f_dtype, gate_kind, gate_dtype; /* gate_dtype: of a vector */
+    float alpha, beta;
+    int accumulate, reserved;
+} ra_norm_block_grad_args;
+
+size_t ra_norm_block_grad_workspace_bytes(int64_t rows, int64_t d);
+ra_status ra_norm_block_grad(const ra_norm_block_grad_args *args, void *stream);
+
+/*
+ * ra_logprobs -- for each row of logits, z = scale * logits[r, :]:
+ *   lse[r]     = log of the sum of exp z
+ *   logp[r]    = z[ids[r]] - lse[r]; 0 for an id outside [0, vocab) (padding)
+ *   entropy[r] = - sum of p log p, p = exp(z - lse)
+ *   top_ids, top_logp  the `top` most likely tokens, by falling logit and, among
+ *              equals, by rising index, with their log probabilities
+ * A logit of minus infinity is a token that cannot be: it adds nothing, its log
+ * probability is minus infinity, and it is no alternative.  Where fewer than `top`
+ * tokens can be, the rest of the row is -1 and minus infinity.  A row in which no
+ * token can be has lse minus infinity, entropy 0 and logp minus infinity (0 for
+ * padding).  A row with a NaN or plus infinity gives NaN in place of every number
+ * but a padding's logp (NaN ranks before plus infinity among the alternatives).
+ *   logits   rows x vocab of dtype;  ids  rows integers of id_bytes (4 or 8)
+ *   scale    the inverse of a temperature: > 0, and 1.443 scale is finite
+ *   logp, lse, entropy  rows binary32 values each; logp (then ids too) and entropy
+ *            may be NULL
+ *   top      0 .. RA_LOGPROBS_MAX_TOP;  top_ids, top_logp  rows x top, contiguous
+ */
+#define RA_LOGPROBS_MAX_TOP 32
+ra_status ra_logprobs(const void *logits, int64_t ld, int dtype, int64_t rows, int64_t vocab, const void *ids, int id_bytes,
+                      float scale, float *logp, float *lse, float *entropy, int top, int64_t *top_ids, float *top_logp,
+                      void *stream);
+
+/*
+ * ra_logprobs_grad -- the gradient with respect to the logits, from those of logp
+ * (g) and of the entropy (e), p = exp(z - lse):
+ *   out[r, j] = scale * (g[r] ([j = ids[r]] - p_j) - e[r] p_j (z_j - lse[r] + entropy[r]))
+ * Padding's g counts for nothing, whatever it holds.  A token that cannot be has
+ * p = 0 and adds no entropy; a row in which none can be has gradient 0.
+ *   lse, entropy  as ra_logprobs left them; entropy only with grad_entropy
+ *   grad_logp, grad_entropy  rows binary32 values, or NULL: zeros; without
+ *            grad_logp ids are not looked at
+ *   out      rows x vocab of out_dtype, rounded once; may be the logits themselves
+ *            (same address, ld and type)
+ */
+ra_status ra_logprobs_grad(const void *logits, int64_t ld, int dtype, int64_t rows, int64_t vocab, const void *ids,
+                           int id_bytes, float scale, const float *lse, const float *entropy, const float *grad_logp,
+                           const float *grad_entropy, void *out, int64_t ld_out, int out_dtype, void *stream);
 
 #ifdef __cplusplus
 }
