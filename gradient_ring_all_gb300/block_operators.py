@@ -316,7 +316,8 @@ def ra_logprobs(logits, ids=None, scale: float = 1.0, entropy: bool = False, top
     the sum of exponentials, and if asked the entropy and the `top` most likely
     tokens (int64, -1 where no possible token is left) with their log
     probabilities, the lowest index first among equals.  A logit of minus
-    infinity is a token that cannot be.  All results are float32."""
+    infinity is a token that cannot be; a row with a NaN or plus infinity gives
+    NaN.  All results but the tokens are float32."""
     rows, vocab = s = _shape(logits, "logits")
     dev = _device(logits.get_device())
     pz, ldz, code = _matrix(logits, "logits", dev, None, s)

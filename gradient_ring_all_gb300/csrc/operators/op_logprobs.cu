@@ -12,14 +12,26 @@ constexpr float kInf = INFINITY;
 
 // ---------------------------------------------------------------------------
 // forward
+//
+// One pass over the logits: every thread keeps the largest logit it has met and
+// the sums of 2^y and y 2^y relative to it, and these shares are joined at the
+// row's end.  WARPS warps take a row (8 rows a block with one warp), in tiles of
+// kSlots 16-byte vectors a thread.  A tile is read asynchronously into the
+// thread's own places in shared memory and from there into registers, after
+// which the next tile, of this row or the next, is on its way while this one is
+// worked on: no thread waits for another's loads.  Rows of any alignment: the
+// few logits before the first and after the last whole vector are one more value
+// of the first threads.
+
+constexpr int kSlots = 8;
 
 struct LogParams {
     const void *logits, *ids;
     float *logp, *lse, *entropy, *top_logp;
     int64_t *top_ids;
-    int64_t ld, rows, vocab;
+    int64_t ld, rows;
+    int vocab, top, id_bytes;
     float scale, scale2;  // scale2: scale / ln 2
-    int top, id_bytes;
 };
 
 // A share of a row: m the largest logit, s the sum of 2^y, w that of y 2^y, with
@@ -49,119 +61,479 @@ __device__ __forceinline__ Share join(Share a, Share b, float scale2) {
     rebase(b, m, scale2);
     return Share{m, a.s + b.s, a.w + b.w};
 }
-__device__ __forceinline__ void add(Share &a, float z, float scale2) {
-    if (z > a.m) rebase(a, z, scale2);
-    const float y = at_least((z - base_of(a.m)) * scale2), e = fast_exp2(y);
-    a.s += e;
-    a.w = fmaf(e, y, a.w);
+template <int LANES>
+__device__ __forceinline__ Share join_lanes(Share a, float scale2) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o /= 2)
+        a = join(a, Share{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.w, o)}, scale2);
+    return a;
+}
+
+// A 16-byte vector of logits as it lies in memory.
+template <class T>
+struct Vec {
+    static constexpr int kEach = 16 / sizeof(T);
+    uint32_t w[4];
+    __device__ __forceinline__ void none() {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+    }
+    // what was made of the words before is made again, not held in registers
+    __device__ __forceinline__ void anew() {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) asm volatile("" : "+r"(w[k]));
+    }
+    __device__ __forceinline__ float operator[](int j) const {
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(w[j]);
+        else
+            return j & 1 ? __uint_as_float(w[j / 2] & 0xffff0000u) : __uint_as_float(w[j / 2] << 16);
+    }
+};
+// the larger of two words of logits (NaN aside)
+template <class T>
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (sizeof(T) == 4)
+        r = __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    else
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <class T>
+__device__ __forceinline__ float largest(uint32_t w) {
+    if constexpr (sizeof(T) == 4)
+        return __uint_as_float(w);
+    else
+        return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
 // A logit and its index as a number that orders as the alternatives do: by
-// value (a NaN first), among equals by falling index.  0 comes after every
-// token that can be.
-__device__ __forceinline__ uint64_t rank_of(float z, uint32_t i) {
-    if (z == -kInf) return 0;
+// value, among equals by falling index.  0 comes after every token that can be.
+__device__ __forceinline__ uint32_t key_of(float z) {
     const uint32_t b = __float_as_uint(z + 0.0f);  // one zero
-    const uint32_t key = z != z ? 0xff800001u : (b & 0x80000000u ? ~b : b | 0x80000000u);
-    return (uint64_t)key << 32 | (uint32_t)~i;
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key); }
+__device__ __forceinline__ uint64_t rank_of(float z, uint32_t i) { return z == -kInf ? 0 : (uint64_t)key_of(z) << 32 | ~i; }
+__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+    return (uint64_t)hi << 32 | lo;
 }
 
-template <class T, int WARPS>
-__global__ void __launch_bounds__(WARPS == 1 ? 256 : WARPS * 32) logprobs_kernel(const LogParams p) {
-    constexpr int kThreads = WARPS * 32, kGroups = WARPS == 1 ? 8 : 1;
-    __shared__ Share shares[WARPS];
-    __shared__ uint64_t best[WARPS];
-    pdl_enter();
-    const int t = threadIdx.x % kThreads, id = threadIdx.x / kThreads;
-    for (int64_t r = (int64_t)blockIdx.x * kGroups + id; r < p.rows; r += (int64_t)gridDim.x * kGroups) {
-        const T *row = static_cast<const T *>(p.logits) + r * p.ld;
-        Share a{-kInf, 0.0f, 0.0f};
-        for (int64_t c = t; c < p.vocab; c += kThreads) add(a, to_f32<T>(row[c]), p.scale2);
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2)
-            a = join(a, Share{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.w, o)}, p.scale2);
-        if constexpr (WARPS > 1) {
-            __syncthreads();
-            if (t % 32 == 0) shares[t / 32] = a;
-            __syncthreads();
-            a = shares[0];
-            for (int w = 1; w < WARPS; ++w) a = join(a, shares[w], p.scale2);
+constexpr int kMostTop = RA_LOGPROBS_MAX_TOP;
+
+// What a row's group has in shared memory beside the landing places.  list: the
+// best so far, then candidates; far_*: what the other blocks of a cluster send
+// to the first.
+template <int WARPS, bool TOP, bool CLUSTER>
+struct RowRoom {
+    static constexpr int kList = !TOP ? 1 : WARPS == 1 ? 256 : 1024;
+    uint64_t list[TOP ? kMostTop + kList : 1];
+    uint64_t far_list[TOP && CLUSTER ? kMostBlocks * kMostTop : 1];
+    uint64_t round[WARPS];
+    Share shares[2][WARPS];
+    Share far_share[CLUSTER ? kMostBlocks : 1];
+    uint32_t keys[WARPS];
+    int count;
+};
+
+// The `top` highest of list[0 .. n), in order, by one warp: lane j has the j-th.
+__device__ __forceinline__ uint64_t select(const uint64_t *list, int n, int top, int lane) {
+    uint64_t last = ~0ull, mine = 0;
+    for (int k = 0; k < top; ++k) {
+        uint64_t best = 0;
+        for (int i = lane; i < n; i += 32) {
+            const uint64_t v = list[i];
+            if (v < last && v > best) best = v;
         }
-        const bool none = a.m == -kInf && a.s == 0.0f;
-        const float base = base_of(a.m), log_s = logf(a.s);
-        if (t == 0) {
-            const float lse = none ? -kInf : fmaf(base, p.scale, log_s);
-            p.lse[r] = lse;
-            if (p.entropy != nullptr) {
-                const float h = none ? 0.0f : log_s - a.w / a.s * kLn2;
-                p.entropy[r] = h < 0.0f ? 0.0f : h;  // by the roundings of a certain token's row
-            }
-            if (p.logp != nullptr) {
-                const int64_t id = p.id_bytes == 8 ? static_cast<const int64_t *>(p.ids)[r] : static_cast<const int32_t *>(p.ids)[r];
-                float y = 0.0f;
-                if (id >= 0 && id < p.vocab) y = none ? -kInf : (to_f32<T>(row[id]) - base) * p.scale - log_s;
-                p.logp[r] = y;
-            }
-        }
-        uint64_t last = ~0ull;
-        for (int k = 0; k < p.top; ++k) {
-            uint64_t mine = 0;
-            for (int64_t c = t; c < p.vocab; c += kThreads) {
-                const uint64_t rank = rank_of(to_f32<T>(row[c]), (uint32_t)c);
-                if (rank < last && rank > mine) mine = rank;
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o /= 2) {
-                const uint64_t other = __shfl_xor_sync(0xffffffffu, mine, o);
-                mine = other > mine ? other : mine;
-            }
-            if constexpr (WARPS > 1) {
-                __syncthreads();
-                if (t % 32 == 0) best[t / 32] = mine;
-                __syncthreads();
-                for (int w = 0; w < WARPS; ++w) mine = best[w] > mine ? best[w] : mine;
-            }
-            if (t == 0) {
-                const uint32_t i = ~(uint32_t)mine;
-                p.top_ids[r * p.top + k] = mine ? (int64_t)i : -1;
-                p.top_logp[r * p.top + k] = mine ? (to_f32<T>(row[i]) - base) * p.scale - log_s : -kInf;
-            }
-            last = mine;
-        }
+        last = warp_max(best);
+        if (lane == k) mine = last;
     }
+    return mine;
+}
+
+template <int WARPS>
+constexpr int log_threads() {
+    return WARPS == 1 ? 256 : WARPS * 32;
+}
+template <int WARPS>
+constexpr int log_blocks() {  // resident on an SM
+    return WARPS == 1 ? 4 : WARPS == 4 ? 8 : 2;
+}
+template <int WARPS, bool TOP, bool CLUSTER>
+constexpr int log_smem() {
+    return log_threads<WARPS>() * kSlots * 16 + log_threads<WARPS>() / (WARPS * 32) * (int)sizeof(RowRoom<WARPS, TOP, CLUSTER>);
+}
+
+template <class T, int WARPS, bool TOP, bool CLUSTER>
+__global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) logprobs_kernel(const LogParams p) {
+    using Room = RowRoom<WARPS, TOP, CLUSTER>;
+    constexpr int kThreads = WARPS * 32, kGroups = log_threads<WARPS>() / kThreads, kEach = Vec<T>::kEach, kTile = kThreads * kSlots;  // vectors
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int t = threadIdx.x % kThreads, lane = threadIdx.x & 31, warp = t / 32, id = threadIdx.x / kThreads;
+    Room &room = reinterpret_cast<Room *>(smem + log_threads<WARPS>() * kSlots * 16)[id];
+    uint4 *land = reinterpret_cast<uint4 *>(smem) + threadIdx.x;  // slot i at land[i * log_threads]
+    if (t == 0) room.count = 0;
+    group_meet<WARPS>(id);
+    pdl_enter();
+    const int parts = CLUSTER ? (int)cluster_blocks() : 1, part = CLUSTER ? (int)cluster_block() : 0;
+    if constexpr (CLUSTER) cluster_meet();
+    const int64_t first = CLUSTER ? blockIdx.x / parts : (int64_t)blockIdx.x * kGroups + id, stride = CLUSTER ? gridDim.x / parts : (int64_t)gridDim.x * kGroups;
+
+    // where a row's whole vectors begin and how many there are
+    auto shape = [&](int64_t r, const T *&row, int &head, int &vecs, int &steps) {
+        row = static_cast<const T *>(p.logits) + r * p.ld;
+        head = min((int)(-(reinterpret_cast<intptr_t>(row) / (int)sizeof(T)) & (kEach - 1)), p.vocab);
+        vecs = (p.vocab - head) / kEach;
+        steps = max(1, ceil_div(vecs, kTile * parts));
+    };
+    // the loads of one tile
+    auto fetch = [&](const T *row, int head, int vecs, int step) {
+        const int v0 = (step * parts + part) * kTile + t;
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i)
+            if (v0 + i * kThreads < vecs)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(land + i * log_threads<WARPS>())), "l"(row + head + (int64_t)(v0 + i * kThreads) * kEach)
+                             : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    const T *row;
+    int head, vecs, steps, turn = 0;
+    if (first < p.rows) {
+        shape(first, row, head, vecs, steps);
+        fetch(row, head, vecs, 0);
+    }
+    for (int64_t r = first; r < p.rows; r += stride) {
+        Share a{-kInf, 0.0f, 0.0f};
+        // the logits outside the whole vectors: one a thread of the first 16
+        float odd = -kInf;
+        int odd_at = 0;
+        if (part == 0 && t < 16) {
+            const int tail = head + vecs * kEach;
+            odd_at = t < 8 ? t : tail + t - 8;
+            if (t < 8 ? t < head : odd_at < p.vocab) odd = to_f32<T>(row[odd_at]);
+        }
+        float given = 0.0f;  // the given token's logit
+        bool inside = false;
+        if (part == 0 && t == 0 && p.logp != nullptr) {
+            const int64_t i = p.id_bytes == 8 ? static_cast<const int64_t *>(p.ids)[r] : static_cast<const int32_t *>(p.ids)[r];
+            inside = i >= 0 && i < p.vocab;
+            if (inside) given = to_f32<T>(row[i]);
+        }
+        const T *now = row;
+        const int now_head = head, now_vecs = vecs, now_steps = steps;
+        for (int step = 0; step < now_steps; ++step) {
+            const int v0 = (step * parts + part) * kTile + t;
+            Vec<T> x[kSlots];
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i) {
+                if (v0 + i * kThreads < now_vecs) {
+                    const uint4 q = land[i * log_threads<WARPS>()];
+                    x[i].w[0] = q.x;
+                    x[i].w[1] = q.y;
+                    x[i].w[2] = q.z;
+                    x[i].w[3] = q.w;
+                } else {
+                    x[i].none();
+                }
+            }
+            uint32_t high = x[0].w[0];
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) high = larger<T>(high, x[i].w[k]);
+            const float most = fmaxf(largest<T>(high), odd);
+            // the next tile (what this one's places held has been used)
+            if (step + 1 < now_steps) {
+                fetch(now, now_head, now_vecs, step + 1);
+            } else if (r + stride < p.rows) {
+                shape(r + stride, row, head, vecs, steps);
+                fetch(row, head, vecs, 0);
+            }
+
+            rebase(a, fmaxf(a.m, most), p.scale2);
+            {
+                const float base = base_of(a.m);
+                const Two off(-base), by(p.scale2);
+                Two s(a.s, 0.0f), w(a.w, 0.0f);
+                auto add = [&](float z0, float z1) {
+                    float y0, y1;
+                    ((Two(z0, z1) + off) * by).get(&y0, &y1);
+                    y0 = at_least(y0);
+                    y1 = at_least(y1);
+                    const Two e(fast_exp2(y0), fast_exp2(y1));
+                    s = s + e;
+                    w = fma2(e, Two(y0, y1), w);
+                };
+#pragma unroll
+                for (int i = 0; i < kSlots; ++i) {
+                    if (v0 - t + i * kThreads >= now_vecs) break;  // the same for the whole group
+#pragma unroll
+                    for (int j = 0; j < kEach; j += 2) add(x[i][j], x[i][j + 1]);
+                }
+                if (step == 0) add(odd, -kInf);
+                float s0, s1, w0, w1;
+                s.get(&s0, &s1);
+                w.get(&w0, &w1);
+                a.s = s0 + s1;
+                a.w = w0 + w1;
+            }
+
+            if constexpr (TOP) {
+                const uint32_t index0 = (uint32_t)now_head + (uint32_t)v0 * kEach;
+                // A bound: each warp finds the ceil(top / WARPS)-th of its lanes'
+                // largest logits; the least of these over the warps has `top`
+                // logits at or above it.  Those that reach it are the candidates.
+                uint32_t key = key_of(most), low = 0;
+                for (int k = 0; k < p.top; k += WARPS) {
+                    low = __reduce_max_sync(0xffffffffu, key);
+                    const uint32_t who = __ballot_sync(0xffffffffu, key == low);
+                    if (lane == __ffs(who) - 1) key = 0;
+                }
+                if (lane == 0) room.keys[warp] = low;
+                group_meet<WARPS>(id);
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w) low = min(low, room.keys[w]);
+                if (step > 0) low = max(low, (uint32_t)(room.list[p.top - 1] >> 32));  // of the best so far
+                const float least = fmaxf(low ? value_of(low) : -kInf, -3.402823466e38f);
+                auto push = [&](float z, uint32_t i) {
+                    if (z >= least && *(volatile int *)&room.count <= Room::kList) {
+                        const int at = atomicAdd(&room.count, 1);
+                        if (at < Room::kList) room.list[kMostTop + at] = rank_of(z, i);
+                    }
+                };
+                if (most >= least) {
+#pragma unroll
+                    for (int i = 0; i < kSlots; ++i) {
+                        x[i].anew();
+                        uint32_t h = x[i].w[0];
+#pragma unroll
+                        for (int k = 1; k < 4; ++k) h = larger<T>(h, x[i].w[k]);
+                        if (largest<T>(h) >= least) {
+#pragma unroll
+                            for (int j = 0; j < kEach; ++j) push(x[i][j], index0 + (uint32_t)(i * kThreads * kEach + j));
+                        }
+                    }
+                    push(odd, odd_at);
+                }
+                group_meet<WARPS>(id);
+                // (the first warp sets the count back below; a warp that reads it later
+                // finds no more than the list holds, unless all of them go on to meet)
+                int n = room.count;
+                if (n > Room::kList) {
+                    // too many reach the bound (equal logits): the best one by one
+                    uint64_t last = ~0ull;
+                    for (int k = 0; k < p.top; ++k) {
+                        uint64_t best = 0;
+                        auto look = [&](float z, uint32_t i) {
+                            const uint64_t v = rank_of(z, i);
+                            if (v < last && v > best) best = v;
+                        };
+#pragma unroll
+                        for (int i = 0; i < kSlots; ++i) x[i].anew();
+#pragma unroll
+                        for (int i = 0; i < kSlots; ++i)
+#pragma unroll
+                            for (int j = 0; j < kEach; ++j) look(x[i][j], index0 + (uint32_t)(i * kThreads * kEach + j));
+                        look(odd, odd_at);
+                        best = warp_max(best);
+                        if constexpr (WARPS > 1) {
+                            if (lane == 0) room.round[warp] = best;
+                            group_meet<WARPS>(id);
+#pragma unroll
+                            for (int w = 0; w < WARPS; ++w) best = room.round[w] > best ? room.round[w] : best;
+                            group_meet<WARPS>(id);
+                        }
+                        last = best;
+                        if (t == 0) room.list[kMostTop + k] = best;
+                    }
+                    n = p.top;
+                }
+                if (warp == 0) {
+                    __syncwarp();
+                    if (step == 0 && lane < kMostTop) room.list[lane] = 0;
+                    __syncwarp();
+                    const uint64_t mine = select(room.list, kMostTop + n, p.top, lane);
+                    __syncwarp();
+                    if (lane < kMostTop) room.list[lane] = mine;
+                    if (lane == 0) room.count = 0;
+                    __syncwarp();
+                }
+            }
+            odd = -kInf;  // it was in the first tile
+        }
+
+        a = join_lanes<32>(a, p.scale2);
+        if constexpr (WARPS > 1) {
+            if (lane == 0) room.shares[turn][warp] = a;
+            group_meet<WARPS>(id);
+            if (warp == 0) {
+                a = lane < WARPS ? room.shares[turn][lane] : Share{-kInf, 0.0f, 0.0f};
+                a = join_lanes<32>(a, p.scale2);
+            }
+            turn ^= 1;
+        }
+        if constexpr (CLUSTER) {
+            if (warp == 0) {
+                if (lane == 0) {
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(place_in(&room.far_share[part].m, 0)), "f"(a.m) : "memory");
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(place_in(&room.far_share[part].s, 0)), "f"(a.s) : "memory");
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(place_in(&room.far_share[part].w, 0)), "f"(a.w) : "memory");
+                }
+                if constexpr (TOP)
+                    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(place_in(&room.far_list[part * kMostTop + lane], 0)), "l"(room.list[lane]) : "memory");
+            }
+            cluster_meet();
+            if (part == 0 && warp == 0) {
+                a = lane < parts ? room.far_share[lane] : Share{-kInf, 0.0f, 0.0f};
+                a = join_lanes<32>(a, p.scale2);
+                if constexpr (TOP) {
+                    const uint64_t mine = select(room.far_list, parts * kMostTop, p.top, lane);
+                    room.list[lane] = mine;
+                    __syncwarp();
+                }
+            }
+        }
+        if (part == 0 && warp == 0) {
+            const bool none = a.m == -kInf && a.s == 0.0f, odd_row = a.s != a.s;
+            const float base = base_of(a.m), log_s = logf(a.s);
+            if (lane == 0) {
+                p.lse[r] = none ? -kInf : fmaf(base, p.scale, log_s);
+                if (p.entropy != nullptr) {
+                    const float h = none ? 0.0f : log_s - a.w / a.s * kLn2;
+                    p.entropy[r] = h < 0.0f ? 0.0f : h;  // by the roundings of a certain token's row
+                }
+                if (p.logp != nullptr) p.logp[r] = !inside ? 0.0f : none ? -kInf : (given - base) * p.scale - log_s;
+            }
+            if constexpr (TOP) {
+                if (lane < p.top) {
+                    const uint64_t v = odd_row ? 0 : room.list[lane];
+                    p.top_ids[r * p.top + lane] = v ? (int64_t)(uint32_t)~(uint32_t)v : -1;
+                    p.top_logp[r * p.top + lane] = odd_row ? a.s : v ? (value_of((uint32_t)(v >> 32)) - base) * p.scale - log_s : -kInf;
+                }
+            }
+        }
+        if constexpr (CLUSTER) cluster_meet();  // the first block has read what the others sent
+    }
+}
+
+template <class T, int WARPS, bool TOP, bool CLUSTER>
+cudaError_t launch_logprobs(const LogParams &p, int cluster, cudaStream_t s) {
+    constexpr int kBytes = log_smem<WARPS, TOP, CLUSTER>();
+    const cudaError_t e = opt_in_smem<logprobs_kernel<T, WARPS, TOP, CLUSTER>>(kBytes);
+    if (e != cudaSuccess) return e;
+    const int64_t groups = WARPS == 1 ? log_threads<1>() / 32 : 1, blocks = ceil_div<int64_t>(p.rows, groups), most = 152 * log_blocks<WARPS>() / cluster;
+    return launch_clusters(logprobs_kernel<T, WARPS, TOP, CLUSTER>, (blocks < most ? blocks : most) * cluster, cluster, log_threads<WARPS>(), kBytes, s, p);
+}
+
+template <class T, bool TOP>
+cudaError_t launch_logprobs(const LogParams &p, cudaStream_t s) {
+    const int vecs = ceil_div(p.vocab, Vec<T>::kEach);
+    if (vecs <= 32 * kSlots) return launch_logprobs<T, 1, TOP, false>(p, 1, s);
+    if (vecs <= 128 * kSlots) return launch_logprobs<T, 4, TOP, false>(p, 1, s);
+    // few long rows: clusters share a row, while all blocks run at once
+    const int64_t tiles = ceil_div(vecs, 512 * kSlots);
+    int cluster = 1;
+    while (cluster < kMostBlocks && cluster < tiles && p.rows * cluster * 2 <= 152 * log_blocks<16>()) cluster *= 2;
+    return cluster == 1 ? launch_logprobs<T, 16, TOP, false>(p, 1, s) : launch_logprobs<T, 16, TOP, true>(p, cluster, s);
 }
 
 // ---------------------------------------------------------------------------
 // backward
+//
+// d = q (c0 + c1 y) for y = log2 p, q = 2^y, and scale g more at the given token:
+// c0 = -scale (g + e H), c1 = -scale e ln 2.  A warp takes a stretch of a row,
+// kFlight vectors of 8 logits a lane, so that rows of any length share one
+// kernel and its few numbers a row are read beside the logits.
+
+constexpr int kGradThreads = 256, kFlight = 4, kStretch = 32 * kFlight;  // vectors
 
 struct LogGradParams {
     const void *logits, *ids;
     const float *lse, *entropy, *g, *ge;
     void *out;
-    int64_t ld, ld_out, rows, vocab;
-    float scale;
-    int id_bytes;
+    int64_t ld, ld_out, rows, stretches;  // of a row
+    int vocab, id_bytes;
+    float scale, scale2;
 };
 
-template <class T, class TO>
-__global__ void __launch_bounds__(256) logprobs_grad_kernel(const LogGradParams p) {
+template <class T, class TO, bool ENTROPY>
+__global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const LogGradParams p) {
     pdl_enter();
-    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
+    const int lane = threadIdx.x & 31;
+    const int64_t total = p.rows * p.stretches;
+    for (int64_t u = (int64_t)blockIdx.x * (kGradThreads / 32) + threadIdx.x / 32; u < total; u += (int64_t)gridDim.x * (kGradThreads / 32)) {
+        int64_t r, k;
+        row_of(u, p.stretches, total, &r, &k);
         const T *row = static_cast<const T *>(p.logits) + r * p.ld;
         TO *out = static_cast<TO *>(p.out) + r * p.ld_out;
+        // whole vectors of 8 begin where the narrower type's do; rows whose two
+        // sides disagree there are done value by value
+        constexpr int kMask = sizeof(T) == 4 && sizeof(TO) == 4 ? 3 : 7;
+        const intptr_t narrow = sizeof(T) <= sizeof(TO) ? reinterpret_cast<intptr_t>(row) / (int)sizeof(T) : reinterpret_cast<intptr_t>(out) / (int)sizeof(TO);
+        int head = min((int)(-narrow & kMask), p.vocab), vecs = (p.vocab - head) / 8;
+        if (((reinterpret_cast<uintptr_t>(row + head) | reinterpret_cast<uintptr_t>(out + head)) & 15) != 0) vecs = 0;
+        Raw<T, 8> x[kFlight];
+        const int v0 = (int)k * kStretch + lane;
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i)
+            if (v0 + 32 * i < vecs) x[i].load(row + head + (int64_t)(v0 + 32 * i) * 8);
         const int64_t id = p.g == nullptr ? -1 : p.id_bytes == 8 ? static_cast<const int64_t *>(p.ids)[r] : static_cast<const int32_t *>(p.ids)[r];
-        const bool given = id >= 0 && id < p.vocab;
-        const float lse = p.lse[r], g = given ? p.g[r] : 0.0f, ge = p.ge != nullptr ? p.ge[r] : 0.0f, h = p.ge != nullptr ? p.entropy[r] : 0.0f;
-        for (int64_t c = threadIdx.x; c < p.vocab; c += 256) {
-            const float z = to_f32<T>(row[c]);
-            const float logp = fmaf(z, p.scale, -lse);
-            const float q = fast_exp2(logp * kLog2e);
-            float d = given ? -g * q : 0.0f;
-            if (given && c == id) d += g;
-            if (p.ge != nullptr && z != -kInf) d = fmaf(-ge * q, logp + h, d);
-            out[c] = from_f32<TO>(lse == -kInf ? 0.0f : d * p.scale);
+        const float lse = p.lse[r], g = id >= 0 && id < p.vocab ? p.g[r] : 0.0f;
+        const float ge = ENTROPY ? p.ge[r] : 0.0f, h = ENTROPY ? p.entropy[r] : 0.0f;
+        const bool none = lse == -kInf;  // no token can be: zeros
+        const int at = none || id < 0 || id >= p.vocab ? -1 : (int)id;
+        const float off = none ? 0.0f : -lse * kLog2e, hot = p.scale * g;
+        const float c0 = none ? 0.0f : ENTROPY ? -p.scale * fmaf(ge, h, g) : -hot, c1 = none ? 0.0f : -p.scale * kLn2 * ge;
+        auto slope = [&](float z) {
+            float y = fmaf(z, p.scale2, off);
+            if constexpr (ENTROPY) {
+                y = at_least(y);
+                return fast_exp2(y) * fmaf(c1, y, c0);
+            } else {
+                return fast_exp2(y) * c0;
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kFlight; ++i) {
+            if (v0 + 32 * i >= vecs) break;
+            const int c = head + (v0 + 32 * i) * 8;
+            float d[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) d[j] = slope(x[i][j]);
+            if ((unsigned)(at - c) < 8u) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (at - c == j) d[j] += hot;
+            }
+            store_w<TO, 8>(out + c, d);
+        }
+        if (vecs > 0 && k == 0) {  // the values outside the whole vectors
+            const int tail = head + vecs * 8, c = lane < 8 ? lane : tail + lane - 8;
+            if (lane < 8 ? lane < head : lane < 16 && c < p.vocab) {
+                float d = slope(to_f32<T>(row[c]));
+                if (c == at) d += hot;
+                out[c] = from_f32<TO>(d);
+            }
+        } else if (vecs == 0) {
+            const int64_t end = min((int64_t)p.vocab, (k + 1) * kStretch * 8);
+            for (int64_t c = k * kStretch * 8 + lane; c < end; c += 32) {
+                float d = slope(to_f32<T>(row[c]));
+                if (c == at) d += hot;
+                out[c] = from_f32<TO>(d);
+            }
         }
     }
+}
+
+template <class T, class TO>
+cudaError_t launch_logprobs_grad(const LogGradParams &p, cudaStream_t s) {
+    const int64_t blocks = ceil_div<int64_t>(p.rows * p.stretches, kGradThreads / 32), grid = blocks < kMaxGrid ? blocks : kMaxGrid;
+    return launch_pdl(p.ge ? logprobs_grad_kernel<T, TO, true> : logprobs_grad_kernel<T, TO, false>, grid, kGradThreads, 0, s, p);
 }
 
 bool ids_ok(const void *ids, int id_bytes, int64_t rows) {
@@ -197,13 +569,10 @@ ra_status ra_logprobs(const void *logits, int64_t ld, int dtype, int64_t rows, i
         for (int q = 0; q < o; ++q)
             if (mats_overlap(out[o], out[q])) return RA_ERR_OVERLAP;
     }
-    const LogParams p{logits, ids, logp, lse, entropy, top_logp, top_ids, ld, rows, vocab, scale, scale * kLog2e, top, id_bytes};
+    const LogParams p{logits, ids, logp, lse, entropy, top_logp, top_ids, ld, rows, (int)vocab, top, id_bytes, scale, scale * kLog2e};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool narrow = vocab <= 1024;
-    const int64_t blocks = narrow ? ceil_div<int64_t>(rows, 8) : rows, grid = blocks < kMaxGrid ? blocks : kMaxGrid;
-    if (dtype == RA_F32)
-        return cuda_status(narrow ? launch_pdl(logprobs_kernel<float, 1>, grid, 256, 0, s, p) : launch_pdl(logprobs_kernel<float, 16>, grid, 512, 0, s, p));
-    return cuda_status(narrow ? launch_pdl(logprobs_kernel<uint16_t, 1>, grid, 256, 0, s, p) : launch_pdl(logprobs_kernel<uint16_t, 16>, grid, 512, 0, s, p));
+    if (dtype == RA_F32) return cuda_status(top > 0 ? launch_logprobs<float, true>(p, s) : launch_logprobs<float, false>(p, s));
+    return cuda_status(top > 0 ? launch_logprobs<uint16_t, true>(p, s) : launch_logprobs<uint16_t, false>(p, s));
 }
 
 ra_status ra_logprobs_grad(const void *logits, int64_t ld, int dtype, int64_t rows, int64_t vocab, const void *ids,
@@ -225,13 +594,11 @@ ra_status ra_logprobs_grad(const void *logits, int64_t ld, int dtype, int64_t ro
     for (const Mat &m : in)
         if (mats_overlap(b, m)) return RA_ERR_OVERLAP;
     if (mats_overlap(a, b) && !same_mat(a, b)) return RA_ERR_OVERLAP;
-    const LogGradParams p{logits, ids, lse, entropy, grad_logp, grad_entropy, out, ld, ld_out, rows, vocab, scale, id_bytes};
+    const LogGradParams p{logits, ids, lse, entropy, grad_logp, grad_entropy, out, ld, ld_out, rows, ceil_div<int64_t>(vocab, kStretch * 8), (int)vocab, id_bytes, scale,
+                          scale * kLog2e};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dtype == RA_F32)
-        return cuda_status(out_dtype == RA_F32 ? launch_pdl(logprobs_grad_kernel<float, float>, rows, 256, 0, s, p)
-                                               : launch_pdl(logprobs_grad_kernel<float, uint16_t>, rows, 256, 0, s, p));
-    return cuda_status(out_dtype == RA_F32 ? launch_pdl(logprobs_grad_kernel<uint16_t, float>, rows, 256, 0, s, p)
-                                           : launch_pdl(logprobs_grad_kernel<uint16_t, uint16_t>, rows, 256, 0, s, p));
+    if (dtype == RA_F32) return cuda_status(out_dtype == RA_F32 ? launch_logprobs_grad<float, float>(p, s) : launch_logprobs_grad<float, uint16_t>(p, s));
+    return cuda_status(out_dtype == RA_F32 ? launch_logprobs_grad<uint16_t, float>(p, s) : launch_logprobs_grad<uint16_t, uint16_t>(p, s));
 }
 
 }  // extern "C"

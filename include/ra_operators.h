@@ -346,7 +346,7 @@ ra_status ra_norm_block_grad(const ra_norm_block_grad_args *args, void *stream);
  * tokens can be, the rest of the row is -1 and minus infinity.  A row in which no
  * token can be has lse minus infinity, entropy 0 and logp minus infinity (0 for
  * padding).  A row with a NaN or plus infinity gives NaN in place of every number
- * but a padding's logp (NaN ranks before plus infinity among the alternatives).
+ * but a padding's logp, and -1 as its alternatives.
  *   logits   rows x vocab of dtype;  ids  rows integers of id_bytes (4 or 8)
  *   scale    the inverse of a temperature: > 0, and 1.443 scale is finite
  *   logp, lse, entropy  rows binary32 values each; logp (then ids too) and entropy

@@ -160,14 +160,16 @@ def distribution64(logits, scale):
 
 
 def alternatives64(logits, count):
-    """The `count` likeliest tokens of each row by value and index, on the host: -1 where none is left."""
+    """The `count` likeliest tokens of each row by value and index, on the host: -1 where none is left, and throughout a row with
+    a NaN or plus infinity."""
     rows, vocab = logits.shape
     z = logits.float().cpu().numpy()
     out = np.full((rows, count), -1, dtype=np.int64)
     for r in range(rows):
         row = z[r] + np.float32(0)
-        key = np.where(np.isnan(row), np.float32(np.inf), row)
-        order = np.lexsort((np.arange(vocab), -key.astype(np.float64), ~np.isnan(row)))
+        if np.isnan(row).any() or (row == np.inf).any():
+            continue
+        order = np.lexsort((np.arange(vocab), -row.astype(np.float64)))
         order = order[~(row[order] == -np.inf)][:count]
         out[r, :len(order)] = order
     return torch.from_numpy(out)

@@ -147,7 +147,7 @@ def test_non_finite_rows(vocab):
         r = ra.ra_logprobs(z, torch.tensor([0, 1, 2, 3, -1], device="cuda"), entropy=True, top=3)
         for t in (r.lse, r.logp, r.entropy, r.top_logp):
             assert bool(torch.isnan(t[1:4]).all()) and bool(torch.isfinite(t[0]).all()) and bool(torch.isfinite(t[4]).all())
-        assert torch.equal(r.top_ids.cpu(), alternatives64(z, 3)) and r.top_ids[3].tolist() == [0, 1, 2] and int(r.top_ids[1, 0]) == vocab // 2
+        assert torch.equal(r.top_ids.cpu(), alternatives64(z, 3)) and bool((r.top_ids[1:4] == -1).all())
 
 
 def test_nothing_to_do():
