@@ -31,8 +31,22 @@ struct LogParams {
     int64_t *top_ids;
     int64_t ld, rows;
     int vocab, top, id_bytes;
-    float scale, scale2;  // scale2: scale / ln 2
+    float scale, scale2, reach;  // scale2: scale / ln 2; reach: 200 / scale2, beyond which 2^y is 0
 };
+
+// A logit and its index as a number that orders as the alternatives do: by
+// value, among equals by falling index.  0 comes after every token that can be.
+__device__ __forceinline__ uint32_t key_of(float z) {
+    const uint32_t b = __float_as_uint(z + 0.0f);  // one zero
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key); }
+__device__ __forceinline__ uint64_t rank_of(float z, uint32_t i) { return z == -kInf ? 0 : (uint64_t)key_of(z) << 32 | ~i; }
+__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+    return (uint64_t)hi << 32 | lo;
+}
 
 // A share of a row: m the largest logit, s the sum of 2^y, w that of y 2^y, with
 // y = (z - m) scale2 held to at least kLeast, where 2^y is 0 (the exponential
@@ -55,17 +69,14 @@ __device__ __forceinline__ void rebase(Share &a, float m, float scale2) {
     a.s = f * a.s;
     a.m = m;
 }
-__device__ __forceinline__ Share join(Share a, Share b, float scale2) {
-    const float m = fmaxf(a.m, b.m);
-    rebase(a, m, scale2);
-    rebase(b, m, scale2);
-    return Share{m, a.s + b.s, a.w + b.w};
-}
-template <int LANES>
+// the warp's shares as one, in every lane
 __device__ __forceinline__ Share join_lanes(Share a, float scale2) {
+    rebase(a, value_of(__reduce_max_sync(0xffffffffu, key_of(a.m))), scale2);
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o /= 2)
-        a = join(a, Share{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.w, o)}, scale2);
+    for (int o = 16; o > 0; o /= 2) {
+        a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+        a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
+    }
     return a;
 }
 
@@ -83,6 +94,19 @@ struct Vec {
 #pragma unroll
         for (int k = 0; k < 4; ++k) asm volatile("" : "+r"(w[k]));
     }
+    // the first value goes, the others move up
+    __device__ __forceinline__ void next() {
+        if constexpr (sizeof(T) == 4) {
+            w[0] = w[1];
+            w[1] = w[2];
+            w[2] = w[3];
+        } else {
+            w[0] = __funnelshift_r(w[0], w[1], 16);
+            w[1] = __funnelshift_r(w[1], w[2], 16);
+            w[2] = __funnelshift_r(w[2], w[3], 16);
+            w[3] >>= 16;
+        }
+    }
     __device__ __forceinline__ float operator[](int j) const {
         if constexpr (sizeof(T) == 4)
             return __uint_as_float(w[j]);
@@ -90,6 +114,16 @@ struct Vec {
             return j & 1 ? __uint_as_float(w[j / 2] & 0xffff0000u) : __uint_as_float(w[j / 2] << 16);
     }
 };
+// the largest bf16 not above x, twice in a word
+__device__ __forceinline__ uint32_t floor_bf16x2(float x) {
+    const uint32_t b = __float_as_uint(x), h = (b & 0x80000000u ? b + 0xffffu : b) >> 16;
+    return __byte_perm(h, h, 0x1010);
+}
+__device__ __forceinline__ uint32_t larger_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 // the larger of two words of logits (NaN aside)
 template <class T>
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
@@ -108,20 +142,6 @@ __device__ __forceinline__ float largest(uint32_t w) {
         return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// A logit and its index as a number that orders as the alternatives do: by
-// value, among equals by falling index.  0 comes after every token that can be.
-__device__ __forceinline__ uint32_t key_of(float z) {
-    const uint32_t b = __float_as_uint(z + 0.0f);  // one zero
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float value_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key); }
-__device__ __forceinline__ uint64_t rank_of(float z, uint32_t i) { return z == -kInf ? 0 : (uint64_t)key_of(z) << 32 | ~i; }
-__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
-    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
-    const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
-    return (uint64_t)hi << 32 | lo;
-}
-
 constexpr int kMostTop = RA_LOGPROBS_MAX_TOP;
 
 // What a row's group has in shared memory beside the landing places.  list: the
@@ -135,12 +155,24 @@ struct RowRoom {
     uint64_t round[WARPS];
     Share shares[2][WARPS];
     Share far_share[CLUSTER ? kMostBlocks : 1];
-    uint32_t keys[WARPS];
+    uint32_t keys[32];
     int count;
 };
 
 // The `top` highest of list[0 .. n), in order, by one warp: lane j has the j-th.
+// Up to 32 are ranked by counting those above, more are picked one by one.
 __device__ __forceinline__ uint64_t select(const uint64_t *list, int n, int top, int lane) {
+    if (n <= 32) {
+        const uint64_t v = lane < n ? list[lane] : 0;
+        int above = 0;
+        for (int i = 0; i < n; ++i) above += __shfl_sync(0xffffffffu, v, i) > v;
+        uint64_t mine = 0;
+        for (int i = 0; i < n; ++i) {
+            const uint64_t o = __shfl_sync(0xffffffffu, v, i);
+            if (__shfl_sync(0xffffffffu, above, i) == lane && lane < top && o != 0) mine = o;
+        }
+        return mine;
+    }
     uint64_t last = ~0ull, mine = 0;
     for (int k = 0; k < top; ++k) {
         uint64_t best = 0;
@@ -180,11 +212,11 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
     pdl_enter();
     const int parts = CLUSTER ? (int)cluster_blocks() : 1, part = CLUSTER ? (int)cluster_block() : 0;
     if constexpr (CLUSTER) cluster_meet();
-    const int64_t first = CLUSTER ? blockIdx.x / parts : (int64_t)blockIdx.x * kGroups + id, stride = CLUSTER ? gridDim.x / parts : (int64_t)gridDim.x * kGroups;
+    const int first = CLUSTER ? blockIdx.x / parts : blockIdx.x * kGroups + id, stride = CLUSTER ? gridDim.x / parts : gridDim.x * kGroups, last_row = (int)p.rows;
 
     // where a row's whole vectors begin and how many there are
-    auto shape = [&](int64_t r, const T *&row, int &head, int &vecs, int &steps) {
-        row = static_cast<const T *>(p.logits) + r * p.ld;
+    auto shape = [&](int r, const T *&row, int &head, int &vecs, int &steps) {
+        row = static_cast<const T *>(p.logits) + (int64_t)r * p.ld;
         head = min((int)(-(reinterpret_cast<intptr_t>(row) / (int)sizeof(T)) & (kEach - 1)), p.vocab);
         vecs = (p.vocab - head) / kEach;
         steps = max(1, ceil_div(vecs, kTile * parts));
@@ -202,11 +234,11 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
 
     const T *row;
     int head, vecs, steps, turn = 0;
-    if (first < p.rows) {
+    if (first < last_row) {
         shape(first, row, head, vecs, steps);
         fetch(row, head, vecs, 0);
     }
-    for (int64_t r = first; r < p.rows; r += stride) {
+    for (int r = first; r < last_row; r += stride) {
         Share a{-kInf, 0.0f, 0.0f};
         // the logits outside the whole vectors: one a thread of the first 16
         float odd = -kInf;
@@ -227,10 +259,13 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
         const int now_head = head, now_vecs = vecs, now_steps = steps;
         for (int step = 0; step < now_steps; ++step) {
             const int v0 = (step * parts + part) * kTile + t;
+            const int g0 = v0 - t, slots = min(kSlots, ceil_div(now_vecs - g0, kThreads));  // the same for the whole group
             Vec<T> x[kSlots];
+            uint32_t high = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
             asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
             for (int i = 0; i < kSlots; ++i) {
+                if (i >= slots) break;
                 if (v0 + i * kThreads < now_vecs) {
                     const uint4 q = land[i * log_threads<WARPS>()];
                     x[i].w[0] = q.x;
@@ -240,17 +275,14 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
                 } else {
                     x[i].none();
                 }
-            }
-            uint32_t high = x[0].w[0];
-#pragma unroll
-            for (int i = 0; i < kSlots; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) high = larger<T>(high, x[i].w[k]);
+            }
             const float most = fmaxf(largest<T>(high), odd);
             // the next tile (what this one's places held has been used)
             if (step + 1 < now_steps) {
                 fetch(now, now_head, now_vecs, step + 1);
-            } else if (r + stride < p.rows) {
+            } else if (r + stride < last_row) {
                 shape(r + stride, row, head, vecs, steps);
                 fetch(row, head, vecs, 0);
             }
@@ -260,22 +292,42 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
                 const float base = base_of(a.m);
                 const Two off(-base), by(p.scale2);
                 Two s(a.s, 0.0f), w(a.w, 0.0f);
-                auto add = [&](float z0, float z1) {
+                auto add = [&](float z0, float z1, bool held) {
+                    Two y = (Two(z0, z1) + off) * by;
                     float y0, y1;
-                    ((Two(z0, z1) + off) * by).get(&y0, &y1);
-                    y0 = at_least(y0);
-                    y1 = at_least(y1);
+                    y.get(&y0, &y1);
+                    if (!held) {
+                        y0 = at_least(y0);
+                        y1 = at_least(y1);
+                        y = Two(y0, y1);
+                    }
                     const Two e(fast_exp2(y0), fast_exp2(y1));
                     s = s + e;
-                    w = fma2(e, Two(y0, y1), w);
+                    w = fma2(e, y, w);
                 };
+                // bf16 logits are held in pairs, before they are taken apart, to a
+                // least value whose exponential is 0; beside the lowest finite
+                // ones there is no such value
+                const uint32_t low = floor_bf16x2(base - p.reach);
+                if (sizeof(T) == 4 || (low != 0xff80ff80u && (base - __uint_as_float(low & 0xffff0000u)) * p.scale2 >= -kLeast)) {
 #pragma unroll
-                for (int i = 0; i < kSlots; ++i) {
-                    if (v0 - t + i * kThreads >= now_vecs) break;  // the same for the whole group
+                    for (int i = 0; i < kSlots; ++i) {
+                        if (i >= slots) break;
+                        Vec<T> v = x[i];
+                        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-                    for (int j = 0; j < kEach; j += 2) add(x[i][j], x[i][j + 1]);
+                            for (int k = 0; k < 4; ++k) v.w[k] = larger_nan(v.w[k], low);
+                        }
+#pragma unroll
+                        for (int j = 0; j < kEach; j += 2) add(v[j], v[j + 1], sizeof(T) == 2);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = now_head + v0 * kEach; c < now_head + now_vecs * kEach && c < now_head + (g0 + kTile) * kEach; c += kThreads * kEach)
+#pragma unroll 1
+                        for (int j = 0; j < kEach; j += 2) add(to_f32<T>(now[c + j]), to_f32<T>(now[c + j + 1]), false);
                 }
-                if (step == 0) add(odd, -kInf);
+                if (step == 0) add(odd, -kInf, false);
                 float s0, s1, w0, w1;
                 s.get(&s0, &s1);
                 w.get(&w0, &w1);
@@ -284,20 +336,23 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
             }
 
             if constexpr (TOP) {
-                const uint32_t index0 = (uint32_t)now_head + (uint32_t)v0 * kEach;
-                // A bound: each warp finds the ceil(top / WARPS)-th of its lanes'
-                // largest logits; the least of these over the warps has `top`
-                // logits at or above it.  Those that reach it are the candidates.
+                // A bound that `top` logits reach: each warp gives the
+                // ceil(top / WARPS) highest of its lanes' largest logits, and of
+                // these, 32 at most, it is the `top`-th.  The logits that reach it
+                // are the candidates, few more than `top` as a rule.
                 uint32_t key = key_of(most), low = 0;
-                for (int k = 0; k < p.top; k += WARPS) {
+                int given_keys = 0;
+                for (int k = 0; k < p.top; k += WARPS, ++given_keys) {
                     low = __reduce_max_sync(0xffffffffu, key);
-                    const uint32_t who = __ballot_sync(0xffffffffu, key == low);
-                    if (lane == __ffs(who) - 1) key = 0;
+                    if (lane == __ffs(__ballot_sync(0xffffffffu, key == low)) - 1) key = 0;
+                    if (lane == 0) room.keys[given_keys * WARPS + warp] = low;
                 }
-                if (lane == 0) room.keys[warp] = low;
                 group_meet<WARPS>(id);
-#pragma unroll
-                for (int w = 0; w < WARPS; ++w) low = min(low, room.keys[w]);
+                key = lane < given_keys * WARPS ? room.keys[lane] : 0;
+                for (int k = 0; k < p.top; ++k) {
+                    low = __reduce_max_sync(0xffffffffu, key);
+                    if (lane == __ffs(__ballot_sync(0xffffffffu, key == low)) - 1) key = 0;
+                }
                 if (step > 0) low = max(low, (uint32_t)(room.list[p.top - 1] >> 32));  // of the best so far
                 const float least = fmaxf(low ? value_of(low) : -kInf, -3.402823466e38f);
                 auto push = [&](float z, uint32_t i) {
@@ -306,16 +361,29 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
                         if (at < Room::kList) room.list[kMostTop + at] = rank_of(z, i);
                     }
                 };
+                const uint32_t index0 = (uint32_t)now_head + (uint32_t)v0 * kEach;
                 if (most >= least) {
+                    uint32_t hits = 0;
 #pragma unroll
                     for (int i = 0; i < kSlots; ++i) {
+                        if (i >= slots) break;
                         x[i].anew();
                         uint32_t h = x[i].w[0];
 #pragma unroll
                         for (int k = 1; k < 4; ++k) h = larger<T>(h, x[i].w[k]);
-                        if (largest<T>(h) >= least) {
+                        hits |= largest<T>(h) >= least ? 1u << i : 0u;
+                    }
+#pragma unroll 1
+                    for (; hits != 0; hits &= hits - 1) {
+                        const int i = __ffs(hits) - 1;
+                        Vec<T> v = x[0];
 #pragma unroll
-                            for (int j = 0; j < kEach; ++j) push(x[i][j], index0 + (uint32_t)(i * kThreads * kEach + j));
+                        for (int q = 1; q < kSlots; ++q)
+                            if (q == i) v = x[q];
+#pragma unroll 1
+                        for (int j = 0; j < kEach; ++j) {
+                            push(v[0], index0 + (uint32_t)(i * kThreads * kEach + j));
+                            v.next();
                         }
                     }
                     push(odd, odd_at);
@@ -327,6 +395,7 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
                 if (n > Room::kList) {
                     // too many reach the bound (equal logits): the best one by one
                     uint64_t last = ~0ull;
+#pragma unroll 1
                     for (int k = 0; k < p.top; ++k) {
                         uint64_t best = 0;
                         auto look = [&](float z, uint32_t i) {
@@ -334,11 +403,16 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
                             if (v < last && v > best) best = v;
                         };
 #pragma unroll
-                        for (int i = 0; i < kSlots; ++i) x[i].anew();
-#pragma unroll
-                        for (int i = 0; i < kSlots; ++i)
-#pragma unroll
-                            for (int j = 0; j < kEach; ++j) look(x[i][j], index0 + (uint32_t)(i * kThreads * kEach + j));
+                        for (int i = 0; i < kSlots; ++i) {
+                            if (i >= slots) break;
+                            Vec<T> v = x[i];
+                            v.anew();
+#pragma unroll 1
+                            for (int j = 0; j < kEach; ++j) {
+                                look(v[0], index0 + (uint32_t)(i * kThreads * kEach + j));
+                                v.next();
+                            }
+                        }
                         look(odd, odd_at);
                         best = warp_max(best);
                         if constexpr (WARPS > 1) {
@@ -355,9 +429,7 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
                 }
                 if (warp == 0) {
                     __syncwarp();
-                    if (step == 0 && lane < kMostTop) room.list[lane] = 0;
-                    __syncwarp();
-                    const uint64_t mine = select(room.list, kMostTop + n, p.top, lane);
+                    const uint64_t mine = step == 0 ? select(room.list + kMostTop, n, p.top, lane) : select(room.list, kMostTop + n, p.top, lane);
                     __syncwarp();
                     if (lane < kMostTop) room.list[lane] = mine;
                     if (lane == 0) room.count = 0;
@@ -367,13 +439,13 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
             odd = -kInf;  // it was in the first tile
         }
 
-        a = join_lanes<32>(a, p.scale2);
+        a = join_lanes(a, p.scale2);
         if constexpr (WARPS > 1) {
             if (lane == 0) room.shares[turn][warp] = a;
             group_meet<WARPS>(id);
             if (warp == 0) {
                 a = lane < WARPS ? room.shares[turn][lane] : Share{-kInf, 0.0f, 0.0f};
-                a = join_lanes<32>(a, p.scale2);
+                a = join_lanes(a, p.scale2);
             }
             turn ^= 1;
         }
@@ -390,7 +462,7 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
             cluster_meet();
             if (part == 0 && warp == 0) {
                 a = lane < parts ? room.far_share[lane] : Share{-kInf, 0.0f, 0.0f};
-                a = join_lanes<32>(a, p.scale2);
+                a = join_lanes(a, p.scale2);
                 if constexpr (TOP) {
                     const uint64_t mine = select(room.far_list, parts * kMostTop, p.top, lane);
                     room.list[lane] = mine;
@@ -412,8 +484,8 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
             if constexpr (TOP) {
                 if (lane < p.top) {
                     const uint64_t v = odd_row ? 0 : room.list[lane];
-                    p.top_ids[r * p.top + lane] = v ? (int64_t)(uint32_t)~(uint32_t)v : -1;
-                    p.top_logp[r * p.top + lane] = odd_row ? a.s : v ? (value_of((uint32_t)(v >> 32)) - base) * p.scale - log_s : -kInf;
+                    p.top_ids[(int64_t)r * p.top + lane] = v ? (int64_t)(uint32_t)~(uint32_t)v : -1;
+                    p.top_logp[(int64_t)r * p.top + lane] = odd_row ? a.s : v ? (value_of((uint32_t)(v >> 32)) - base) * p.scale - log_s : -kInf;
                 }
             }
         }
@@ -558,6 +630,7 @@ ra_status ra_logprobs(const void *logits, int64_t ld, int dtype, int64_t rows, i
     if (esz == 0 || !scale_ok(scale) || top < 0 || top > RA_LOGPROBS_MAX_TOP) return RA_ERR_INVALID_ARG;
     const Mat a{logits, rows, vocab, ld, esz};
     if (!mat_ok(a)) return RA_ERR_INVALID_ARG;
+    if (vocab > RA_LOGPROBS_MAX_VOCAB) return RA_ERR_UNSUPPORTED;
     if (rows == 0) return RA_OK;
     if (lse == nullptr || !floats_ok(lse) || !floats_ok(logp) || !floats_ok(entropy) || (logp != nullptr && !ids_ok(ids, id_bytes, rows))) return RA_ERR_INVALID_ARG;
     if (top > 0 && (top_ids == nullptr || top_logp == nullptr || !floats_ok(top_logp) || reinterpret_cast<uintptr_t>(top_ids) % 8 != 0)) return RA_ERR_INVALID_ARG;
@@ -569,7 +642,7 @@ ra_status ra_logprobs(const void *logits, int64_t ld, int dtype, int64_t rows, i
         for (int q = 0; q < o; ++q)
             if (mats_overlap(out[o], out[q])) return RA_ERR_OVERLAP;
     }
-    const LogParams p{logits, ids, logp, lse, entropy, top_logp, top_ids, ld, rows, (int)vocab, top, id_bytes, scale, scale * kLog2e};
+    const LogParams p{logits, ids, logp, lse, entropy, top_logp, top_ids, ld, rows, (int)vocab, top, id_bytes, scale, scale * kLog2e, 200.0f / (scale * kLog2e)};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == RA_F32) return cuda_status(top > 0 ? launch_logprobs<float, true>(p, s) : launch_logprobs<float, false>(p, s));
     return cuda_status(top > 0 ? launch_logprobs<uint16_t, true>(p, s) : launch_logprobs<uint16_t, false>(p, s));
@@ -584,6 +657,7 @@ ra_status ra_logprobs_grad(const void *logits, int64_t ld, int dtype, int64_t ro
     if (esz == 0 || eso == 0 || !scale_ok(scale)) return RA_ERR_INVALID_ARG;
     const Mat a{logits, rows, vocab, ld, esz}, b{out, rows, vocab, ld_out, eso};
     if (!mat_ok(a) || !mat_ok(b)) return RA_ERR_INVALID_ARG;
+    if (vocab > RA_LOGPROBS_MAX_VOCAB) return RA_ERR_UNSUPPORTED;
     if (a.empty()) return RA_OK;
     if (lse == nullptr || !floats_ok(lse) || !floats_ok(entropy) || !floats_ok(grad_logp) || !floats_ok(grad_entropy) ||
         (grad_logp != nullptr && !ids_ok(ids, id_bytes, rows)))

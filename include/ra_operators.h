@@ -354,6 +354,7 @@ ra_status ra_norm_block_grad(const ra_norm_block_grad_args *args, void *stream);
  *   top      0 .. RA_LOGPROBS_MAX_TOP;  top_ids, top_logp  rows x top, contiguous
  */
 #define RA_LOGPROBS_MAX_TOP 32
+#define RA_LOGPROBS_MAX_VOCAB (1 << 30) /* RA_ERR_UNSUPPORTED beyond, for the gradient too */
 ra_status ra_logprobs(const void *logits, int64_t ld, int dtype, int64_t rows, int64_t vocab, const void *ids, int id_bytes,
                       float scale, float *logp, float *lse, float *entropy, int top, int64_t *top_ids, float *top_logp,
                       void *stream);
