@@ -31,7 +31,7 @@ struct LogParams {
     int64_t *top_ids;
     int64_t ld, rows;
     int vocab, top, id_bytes;
-    float scale, scale2, reach;  // scale2: scale / ln 2; reach: 200 / scale2, beyond which 2^y is 0
+    float scale, scale2;  // scale2: scale / ln 2
 };
 
 // A logit and its index as a number that orders as the alternatives do: by
@@ -48,10 +48,12 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
     return (uint64_t)hi << 32 | lo;
 }
 
-// A share of a row: m the largest logit, s the sum of 2^y, w that of y 2^y, with
+// A share of a row: m one of its logits, s the sum of 2^y, w that of y 2^y, with
 // y = (z - m) scale2 held to at least kLeast, where 2^y is 0 (the exponential
 // flushes what is below 2^-126): so a token that cannot be, or is that far off,
-// adds 0 and no 0 * infinity.  A NaN stays one.
+// adds 0 and no 0 * infinity.  A NaN stays one.  m need not be the largest: the
+// sums are in floating point, and where they grow beyond 1e37 they are made again
+// from the largest.  An empty share has m minus infinity and s = w = 0.
 struct Share {
     float m, s, w;
 };
@@ -61,7 +63,11 @@ __device__ __forceinline__ float at_least(float y) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(y), "f"(kLeast));
     return r;
 }
-// what is taken out before the exponential: 0 where the largest is minus infinity
+__device__ __forceinline__ float max3(float a, float b, float c) {  // NaN aside
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ float base_of(float m) { return m == -kInf ? 0.0f : m; }
 __device__ __forceinline__ void rebase(Share &a, float m, float scale2) {
     const float y = at_least((a.m - base_of(m)) * scale2), f = fast_exp2(y);
@@ -89,10 +95,15 @@ struct Vec {
 #pragma unroll
         for (int k = 0; k < 4; ++k) w[k] = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
     }
-    // what was made of the words before is made again, not held in registers
-    __device__ __forceinline__ void anew() {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) asm volatile("" : "+r"(w[k]));
+    __device__ __forceinline__ void take(uint32_t shared) {
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(shared) : "memory");
+    }
+    __device__ __forceinline__ void load(const T *p) {
+        const uint4 q = load_16(p);
+        w[0] = q.x;
+        w[1] = q.y;
+        w[2] = q.z;
+        w[3] = q.w;
     }
     // the first value goes, the others move up
     __device__ __forceinline__ void next() {
@@ -114,76 +125,57 @@ struct Vec {
             return j & 1 ? __uint_as_float(w[j / 2] & 0xffff0000u) : __uint_as_float(w[j / 2] << 16);
     }
 };
-// the largest bf16 not above x, twice in a word
-__device__ __forceinline__ uint32_t floor_bf16x2(float x) {
-    const uint32_t b = __float_as_uint(x), h = (b & 0x80000000u ? b + 0xffffu : b) >> 16;
-    return __byte_perm(h, h, 0x1010);
-}
-__device__ __forceinline__ uint32_t larger_nan(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-// the larger of two words of logits (NaN aside)
 template <class T>
-__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
-    uint32_t r;
-    if constexpr (sizeof(T) == 4)
-        r = __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
-    else
-        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-template <class T>
-__device__ __forceinline__ float largest(uint32_t w) {
-    if constexpr (sizeof(T) == 4)
-        return __uint_as_float(w);
-    else
-        return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+__device__ __forceinline__ float largest(const Vec<T> &v) {
+    float m = fmaxf(v[0], v[1]);
+#pragma unroll
+    for (int j = 2; j < Vec<T>::kEach; j += 2) m = max3(m, v[j], v[j + 1]);
+    return m;
 }
 
 constexpr int kMostTop = RA_LOGPROBS_MAX_TOP;
 
 // What a row's group has in shared memory beside the landing places.  list: the
-// best so far, then candidates; far_*: what the other blocks of a cluster send
-// to the first.
+// best so far, then candidates, of this tile and the last one; far_*: what the
+// other blocks of a cluster send to the first.
 template <int WARPS, bool TOP, bool CLUSTER>
 struct RowRoom {
-    static constexpr int kList = !TOP ? 1 : WARPS == 1 ? 256 : 1024;
-    uint64_t list[TOP ? kMostTop + kList : 1];
+    static constexpr int kList = !TOP ? 1 : WARPS == 1 ? 224 : 992;
+    uint64_t list[2][TOP ? kMostTop + kList : 1];
     uint64_t far_list[TOP && CLUSTER ? kMostBlocks * kMostTop : 1];
     uint64_t round[WARPS];
     Share shares[2][WARPS];
     Share far_share[CLUSTER ? kMostBlocks : 1];
     uint32_t keys[32];
-    int count;
+    int count[2];
 };
 
-// The `top` highest of list[0 .. n), in order, by one warp: lane j has the j-th.
-// Up to 32 are ranked by counting those above, more are picked one by one.
-__device__ __forceinline__ uint64_t select(const uint64_t *list, int n, int top, int lane) {
-    if (n <= 32) {
-        const uint64_t v = lane < n ? list[lane] : 0;
-        int above = 0;
-        for (int i = 0; i < n; ++i) above += __shfl_sync(0xffffffffu, v, i) > v;
-        uint64_t mine = 0;
-        for (int i = 0; i < n; ++i) {
-            const uint64_t o = __shfl_sync(0xffffffffu, v, i);
-            if (__shfl_sync(0xffffffffu, above, i) == lane && lane < top && o != 0) mine = o;
-        }
-        return mine;
-    }
-    uint64_t last = ~0ull, mine = 0;
+// The `top` highest of list[0 .. n), by one warp: lane j gets the j-th.
+__device__ __noinline__ uint64_t pick(const uint64_t *list, int n, int top, int lane) {
+    uint64_t last = ~0ull, mine = 0, best = 0;
+    bool look = true;
     for (int k = 0; k < top; ++k) {
-        uint64_t best = 0;
-        for (int i = lane; i < n; i += 32) {
-            const uint64_t v = list[i];
-            if (v < last && v > best) best = v;
+        if (look) {
+            best = 0;
+            for (int i = lane; i < n; i += 32) {
+                const uint64_t v = list[i];
+                if (v < last && v > best) best = v;
+            }
         }
+        __syncwarp();
         last = warp_max(best);
+        look = best == last;
         if (lane == k) mine = last;
     }
     return mine;
+}
+
+// how many of list[0 .. n) are above v
+__device__ __forceinline__ int above(const uint64_t *list, int n, uint64_t v) {
+    int k = 0;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) k += list[i] > v;
+    return k;
 }
 
 template <int WARPS>
@@ -192,11 +184,25 @@ constexpr int log_threads() {
 }
 template <int WARPS>
 constexpr int log_blocks() {  // resident on an SM
-    return WARPS == 1 ? 4 : WARPS == 4 ? 8 : 2;
+    return WARPS == 1 ? 3 : WARPS == 4 ? 8 : 2;
 }
 template <int WARPS, bool TOP, bool CLUSTER>
 constexpr int log_smem() {
     return log_threads<WARPS>() * kSlots * 16 + log_threads<WARPS>() / (WARPS * 32) * (int)sizeof(RowRoom<WARPS, TOP, CLUSTER>);
+}
+
+// f(Const<0>()), f(Const<1>()), ..: a tile's places as constants
+template <class F>
+__device__ __forceinline__ void each_slot(F &&f) {
+    static_assert(kSlots == 8, "each_slot");
+    f(Const<0>());
+    f(Const<1>());
+    f(Const<2>());
+    f(Const<3>());
+    f(Const<4>());
+    f(Const<5>());
+    f(Const<6>());
+    f(Const<7>());
 }
 
 template <class T, int WARPS, bool TOP, bool CLUSTER>
@@ -206,8 +212,9 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
     extern __shared__ __align__(16) unsigned char smem[];
     const int t = threadIdx.x % kThreads, lane = threadIdx.x & 31, warp = t / 32, id = threadIdx.x / kThreads;
     Room &room = reinterpret_cast<Room *>(smem + log_threads<WARPS>() * kSlots * 16)[id];
-    uint4 *land = reinterpret_cast<uint4 *>(smem) + threadIdx.x;  // slot i at land[i * log_threads]
-    if (t == 0) room.count = 0;
+    const uint32_t land = smem_addr(smem) + threadIdx.x * 16;  // the thread's places, kPitch apart
+    constexpr int kPitch = log_threads<WARPS>() * 16;
+    if (t < 2) room.count[t] = 0;
     group_meet<WARPS>(id);
     pdl_enter();
     const int parts = CLUSTER ? (int)cluster_blocks() : 1, part = CLUSTER ? (int)cluster_block() : 0;
@@ -221,22 +228,22 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
         vecs = (p.vocab - head) / kEach;
         steps = max(1, ceil_div(vecs, kTile * parts));
     };
-    // the loads of one tile
-    auto fetch = [&](const T *row, int head, int vecs, int step) {
-        const int v0 = (step * parts + part) * kTile + t;
-#pragma unroll
-        for (int i = 0; i < kSlots; ++i)
-            if (v0 + i * kThreads < vecs)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(land + i * log_threads<WARPS>())), "l"(row + head + (int64_t)(v0 + i * kThreads) * kEach)
-                             : "memory");
-        asm volatile("cp.async.commit_group;" ::: "memory");
+    // one load of a tile, into place i: `left` vectors are left of the row from `from` on
+    auto fetch = [&](auto place, const T *from, int left) {
+        constexpr int i = decltype(place)::value;
+        if (left > i * kThreads)
+            asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(land), "l"(from), "n"(i * kPitch), "n"(i * kThreads * 16) : "memory");
+        else
+            asm volatile("st.shared.v4.b32 [%0 + %2], {%1, %1, %1, %1};" ::"r"(land), "r"(sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u), "n"(i * kPitch) : "memory");
     };
 
     const T *row;
-    int head, vecs, steps, turn = 0;
+    int head, vecs, steps, turn = 0, side = 0;
     if (first < last_row) {
         shape(first, row, head, vecs, steps);
-        fetch(row, head, vecs, 0);
+        const int v0 = part * kTile + t;
+        each_slot([&](auto place) { fetch(place, row + head + (int64_t)v0 * kEach, vecs - v0); });
+        asm volatile("cp.async.commit_group;" ::: "memory");
     }
     for (int r = first; r < last_row; r += stride) {
         Share a{-kInf, 0.0f, 0.0f};
@@ -257,141 +264,151 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
         }
         const T *now = row;
         const int now_head = head, now_vecs = vecs, now_steps = steps;
+        int have = 0;  // of the best
         for (int step = 0; step < now_steps; ++step) {
             const int v0 = (step * parts + part) * kTile + t;
             const int g0 = v0 - t, slots = min(kSlots, ceil_div(now_vecs - g0, kThreads));  // the same for the whole group
-            Vec<T> x[kSlots];
-            uint32_t high = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+            const bool last_step = step + 1 == now_steps;
+            // where the next tile's loads are: this row's, the next row's, or none
+            const T *ahead = now + now_head + (int64_t)(v0 + kTile * parts) * kEach;
+            int ahead_left = now_vecs - (v0 + kTile * parts);
+            if (last_step) {
+                ahead_left = 0;
+                if (r + stride < last_row) {
+                    shape(r + stride, row, head, vecs, steps);
+                    ahead = row + head + (int64_t)(part * kTile + t) * kEach;
+                    ahead_left = vecs - (part * kTile + t);
+                }
+            }
+            float s[2] = {0.0f, 0.0f}, w[2] = {0.0f, 0.0f}, most = odd, off = 0.0f;
             asm volatile("cp.async.wait_group 0;" ::: "memory");
-#pragma unroll
-            for (int i = 0; i < kSlots; ++i) {
-                if (i >= slots) break;
-                if (v0 + i * kThreads < now_vecs) {
-                    const uint4 q = land[i * log_threads<WARPS>()];
-                    x[i].w[0] = q.x;
-                    x[i].w[1] = q.y;
-                    x[i].w[2] = q.z;
-                    x[i].w[3] = q.w;
-                } else {
-                    x[i].none();
+            Vec<T> x[2];  // a place is read while the one before is worked on
+            x[0].take(land);
+            each_slot([&](auto place) {
+                constexpr int i = decltype(place)::value;
+                if constexpr (i + 1 < kSlots) x[(i + 1) & 1].take(land + (i + 1) * kPitch);
+                fetch(place, ahead, ahead_left);  // what this place held has been read
+                if (i >= slots) return;
+                const Vec<T> &v = x[i & 1];
+                if (i == 0) {
+                    if (a.m == -kInf) a.m = fmaxf(odd, largest(v));
+                    off = base_of(a.m) * p.scale2;
                 }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) high = larger<T>(high, x[i].w[k]);
+                for (int j = 0; j < kEach; j += 2) most = max3(most, v[j], v[j + 1]);
+#pragma unroll
+                for (int j = 0; j < kEach; ++j) {
+                    const float y = at_least(fmaf(v[j], p.scale2, -off)), e = fast_exp2(y);
+                    s[j & 1] += e;
+                    w[j & 1] = fmaf(e, y, w[j & 1]);
+                }
+                // in this order, or the compiler reads all places first and runs out of registers
+                asm volatile("" : "+f"(s[0]), "+f"(s[1]), "+f"(w[0]), "+f"(w[1]), "+f"(most));
+            });
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (step == 0) {
+                if (slots <= 0) {
+                    a.m = odd;
+                    off = base_of(odd) * p.scale2;
+                }
+                const float y = at_least(fmaf(odd, p.scale2, -off)), e = fast_exp2(y);
+                s[0] += e;
+                w[0] = fmaf(e, y, w[0]);
             }
-            const float most = fmaxf(largest<T>(high), odd);
-            // the next tile (what this one's places held has been used)
-            if (step + 1 < now_steps) {
-                fetch(now, now_head, now_vecs, step + 1);
-            } else if (r + stride < last_row) {
-                shape(r + stride, row, head, vecs, steps);
-                fetch(row, head, vecs, 0);
-            }
-
-            rebase(a, fmaxf(a.m, most), p.scale2);
             {
-                const float base = base_of(a.m);
-                const Two off(-base), by(p.scale2);
-                Two s(a.s, 0.0f), w(a.w, 0.0f);
-                auto add = [&](float z0, float z1, bool held) {
-                    Two y = (Two(z0, z1) + off) * by;
-                    float y0, y1;
-                    y.get(&y0, &y1);
-                    if (!held) {
-                        y0 = at_least(y0);
-                        y1 = at_least(y1);
-                        y = Two(y0, y1);
-                    }
-                    const Two e(fast_exp2(y0), fast_exp2(y1));
-                    s = s + e;
-                    w = fma2(e, y, w);
-                };
-                // bf16 logits are held in pairs, before they are taken apart, to a
-                // least value whose exponential is 0; beside the lowest finite
-                // ones there is no such value
-                const uint32_t low = floor_bf16x2(base - p.reach);
-                if (sizeof(T) == 4 || (low != 0xff80ff80u && (base - __uint_as_float(low & 0xffff0000u)) * p.scale2 >= -kLeast)) {
-#pragma unroll
-                    for (int i = 0; i < kSlots; ++i) {
-                        if (i >= slots) break;
-                        Vec<T> v = x[i];
-                        if constexpr (sizeof(T) == 2) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) v.w[k] = larger_nan(v.w[k], low);
-                        }
-#pragma unroll
-                        for (int j = 0; j < kEach; j += 2) add(v[j], v[j + 1], sizeof(T) == 2);
-                    }
-                } else {
+                // y came with what the rounding of `off` leaves, `by`
+                const float by = fmaf(base_of(a.m), p.scale2, -off), sum = s[0] + s[1], f = fmaf(by, -kLn2, 1.0f);
+                const float s_new = fmaf(sum, f, a.s), w_new = fmaf(fmaf(-by, sum, w[0] + w[1]), f, a.w);
+                if (fabsf(off) < 1e30f && s_new < 1e37f) {
+                    a.s = s_new;
+                    a.w = w_new;
+                    if (a.m == -kInf && most > -kInf) a.m = 0.0f;  // what was taken out
+                } else {  // from the largest, one by one (also: logits near the type's ends, NaN)
+                    rebase(a, fmaxf(a.m, most), p.scale2);
+                    const float base = base_of(a.m);
+                    auto add = [&](float z) {
+                        const float y = at_least((z - base) * p.scale2), e = fast_exp2(y);
+                        a.s += e;
+                        a.w = fmaf(e, y, a.w);
+                    };
+                    const int end = now_head + min(now_vecs, g0 + kTile) * kEach;
 #pragma unroll 1
-                    for (int c = now_head + v0 * kEach; c < now_head + now_vecs * kEach && c < now_head + (g0 + kTile) * kEach; c += kThreads * kEach)
+                    for (int c = now_head + v0 * kEach; c < end; c += kThreads * kEach)
 #pragma unroll 1
-                        for (int j = 0; j < kEach; j += 2) add(to_f32<T>(now[c + j]), to_f32<T>(now[c + j + 1]), false);
+                        for (int j = 0; j < kEach; ++j) add(to_f32<T>(now[c + j]));
+                    if (step == 0) add(odd);
                 }
-                if (step == 0) add(odd, -kInf, false);
-                float s0, s1, w0, w1;
-                s.get(&s0, &s1);
-                w.get(&w0, &w1);
-                a.s = s0 + s1;
-                a.w = w0 + w1;
+            }
+            if (last_step) {
+                a = join_lanes(a, p.scale2);
+                if (WARPS > 1 && lane == 0) room.shares[turn][warp] = a;
             }
 
             if constexpr (TOP) {
-                // A bound that `top` logits reach: each warp gives the
-                // ceil(top / WARPS) highest of its lanes' largest logits, and of
-                // these, 32 at most, it is the `top`-th.  The logits that reach it
-                // are the candidates, few more than `top` as a rule.
-                uint32_t key = key_of(most), low = 0;
-                int given_keys = 0;
-                for (int k = 0; k < p.top; k += WARPS, ++given_keys) {
-                    low = __reduce_max_sync(0xffffffffu, key);
-                    if (lane == __ffs(__ballot_sync(0xffffffffu, key == low)) - 1) key = 0;
-                    if (lane == 0) room.keys[given_keys * WARPS + warp] = low;
-                }
+                // A bound that `top` logits reach: of the largest logits of 32 groups of
+                // threads the top-th.  The logits that reach it are the candidates,
+                // few more than top (9 for 8, 31 for 20, where they lie at random).
+                constexpr int kEachWarp = 32 / WARPS;  // groups
+                uint32_t key = key_of(most);
+#pragma unroll
+                for (int o = 16 / kEachWarp; o > 0; o /= 2) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
+                if (lane % (32 / kEachWarp) == 0) room.keys[warp * kEachWarp + lane / (32 / kEachWarp)] = key;
                 group_meet<WARPS>(id);
-                key = lane < given_keys * WARPS ? room.keys[lane] : 0;
-                for (int k = 0; k < p.top; ++k) {
-                    low = __reduce_max_sync(0xffffffffu, key);
-                    if (lane == __ffs(__ballot_sync(0xffffffffu, key == low)) - 1) key = 0;
+                key = room.keys[lane];
+                uint32_t low = key;
+                if (p.top == 32) {
+                    low = __reduce_min_sync(0xffffffffu, key);
+                } else {
+                    for (int k = 0; k < p.top; ++k) {
+                        low = __reduce_max_sync(0xffffffffu, key);
+                        if (lane == __ffs(__ballot_sync(0xffffffffu, key == low)) - 1) key = 0;
+                    }
                 }
-                if (step > 0) low = max(low, (uint32_t)(room.list[p.top - 1] >> 32));  // of the best so far
-                const float least = fmaxf(low ? value_of(low) : -kInf, -3.402823466e38f);
+                key = low;
+                uint64_t *const list = room.list[side];
+                if (have == p.top) key = max(key, (uint32_t)(list[p.top - 1] >> 32));  // of the best so far
+                const float least = fmaxf(value_of(key), -3.402823466e38f);
+                int *const count = &room.count[side];
                 auto push = [&](float z, uint32_t i) {
-                    if (z >= least && *(volatile int *)&room.count <= Room::kList) {
-                        const int at = atomicAdd(&room.count, 1);
-                        if (at < Room::kList) room.list[kMostTop + at] = rank_of(z, i);
+                    if (z >= least && *(volatile int *)count <= Room::kList) {
+                        const int at = atomicAdd(count, 1);
+                        if (at < Room::kList) list[have + at] = rank_of(z, i);
                     }
                 };
                 const uint32_t index0 = (uint32_t)now_head + (uint32_t)v0 * kEach;
                 if (most >= least) {
-                    uint32_t hits = 0;
-#pragma unroll
-                    for (int i = 0; i < kSlots; ++i) {
-                        if (i >= slots) break;
-                        x[i].anew();
-                        uint32_t h = x[i].w[0];
-#pragma unroll
-                        for (int k = 1; k < 4; ++k) h = larger<T>(h, x[i].w[k]);
-                        hits |= largest<T>(h) >= least ? 1u << i : 0u;
-                    }
+                    // read again, by the few threads that have some (from L2), four at a time
+                    const T *from = now + now_head + (int64_t)v0 * kEach;
+                    const int left = now_vecs - v0;
 #pragma unroll 1
-                    for (; hits != 0; hits &= hits - 1) {
-                        const int i = __ffs(hits) - 1;
-                        Vec<T> v = x[0];
+                    for (int i0 = 0; i0 < kSlots && left > i0 * kThreads; i0 += 4) {
+                        Vec<T> q[4];
+                        uint32_t hits = 0;
 #pragma unroll
-                        for (int q = 1; q < kSlots; ++q)
-                            if (q == i) v = x[q];
+                        for (int i = 0; i < 4; ++i) {
+                            q[i].none();
+                            if (left > (i0 + i) * kThreads) q[i].load(from + (i0 + i) * kThreads * kEach);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) hits |= largest(q[i]) >= least ? 1u << i : 0u;
 #pragma unroll 1
-                        for (int j = 0; j < kEach; ++j) {
-                            push(v[0], index0 + (uint32_t)(i * kThreads * kEach + j));
-                            v.next();
+                        for (; hits != 0; hits &= hits - 1) {
+                            const int i = __ffs(hits) - 1;
+                            Vec<T> v = q[0];
+#pragma unroll
+                            for (int k = 1; k < 4; ++k)
+                                if (k == i) v = q[k];
+#pragma unroll 1
+                            for (int j = 0; j < kEach; ++j) {
+                                push(v[0], index0 + (uint32_t)((i0 + i) * kThreads * kEach + j));
+                                v.next();
+                            }
                         }
                     }
                     push(odd, odd_at);
                 }
                 group_meet<WARPS>(id);
-                // (the first warp sets the count back below; a warp that reads it later
-                // finds no more than the list holds, unless all of them go on to meet)
-                int n = room.count;
+                int n = *(volatile int *)count;
                 if (n > Room::kList) {
                     // too many reach the bound (equal logits): the best one by one
                     uint64_t last = ~0ull;
@@ -402,17 +419,9 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
                             const uint64_t v = rank_of(z, i);
                             if (v < last && v > best) best = v;
                         };
-#pragma unroll
-                        for (int i = 0; i < kSlots; ++i) {
-                            if (i >= slots) break;
-                            Vec<T> v = x[i];
-                            v.anew();
-#pragma unroll 1
-                            for (int j = 0; j < kEach; ++j) {
-                                look(v[0], index0 + (uint32_t)(i * kThreads * kEach + j));
-                                v.next();
-                            }
-                        }
+                        const int end = now_head + min(now_vecs, g0 + kTile) * kEach;
+                        for (int c = now_head + v0 * kEach; c < end; c += kThreads * kEach)
+                            for (int j = 0; j < kEach; ++j) look(to_f32<T>(now[c + j]), c + j);
                         look(odd, odd_at);
                         best = warp_max(best);
                         if constexpr (WARPS > 1) {
@@ -420,32 +429,53 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
                             group_meet<WARPS>(id);
 #pragma unroll
                             for (int w = 0; w < WARPS; ++w) best = room.round[w] > best ? room.round[w] : best;
-                            group_meet<WARPS>(id);
                         }
                         last = best;
-                        if (t == 0) room.list[kMostTop + k] = best;
+                        if (t == 0) list[have + k] = best;
+                        group_meet<WARPS>(id);
                     }
                     n = p.top;
                 }
-                if (warp == 0) {
-                    __syncwarp();
-                    const uint64_t mine = step == 0 ? select(room.list + kMostTop, n, p.top, lane) : select(room.list, kMostTop + n, p.top, lane);
-                    __syncwarp();
-                    if (lane < kMostTop) room.list[lane] = mine;
-                    if (lane == 0) room.count = 0;
-                    __syncwarp();
+                n += have;
+                // The best of them, in order.  (The other list and count are free: all
+                // threads have met twice since they were looked at.)
+                if (t == 0) room.count[side ^ 1] = 0;
+                have = min(n, p.top);
+                side ^= 1;
+                const bool few = n <= 64;
+                if (warp == 0 || (few && warp * 32 < n)) {
+                    const bool out = !CLUSTER && last_step;
+                    if (WARPS > 1 && out) a = join_lanes(lane < WARPS ? room.shares[turn][lane] : Share{-kInf, 0.0f, 0.0f}, p.scale2);
+                    const bool odd_row = a.s != a.s;
+                    const float base = base_of(a.m), log_s = logf(a.s);
+                    auto emit = [&](int k, uint64_t v) {
+                        if (out) {
+                            p.top_ids[(int64_t)r * p.top + k] = odd_row || v == 0 ? -1 : (int64_t)(uint32_t)~(uint32_t)v;
+                            p.top_logp[(int64_t)r * p.top + k] = odd_row ? a.s : v == 0 ? -kInf : (value_of((uint32_t)(v >> 32)) - base) * p.scale - log_s;
+                        } else {
+                            room.list[side][k] = v;
+                        }
+                    };
+                    if (few) {  // each finds its place by counting those above it
+                        for (int i = t; i < n; i += kThreads) {
+                            const uint64_t v = list[i];
+                            const int k = above(list, n, v);
+                            if (k < p.top) emit(k, v);
+                        }
+                        if (t >= have && t < p.top) emit(t, 0);
+                    } else {  // one by one, by one warp
+                        const uint64_t mine = pick(list, n, p.top, lane);
+                        if (lane < p.top) emit(lane, mine);
+                    }
                 }
             }
             odd = -kInf;  // it was in the first tile
         }
 
-        a = join_lanes(a, p.scale2);
         if constexpr (WARPS > 1) {
-            if (lane == 0) room.shares[turn][warp] = a;
-            group_meet<WARPS>(id);
-            if (warp == 0) {
-                a = lane < WARPS ? room.shares[turn][lane] : Share{-kInf, 0.0f, 0.0f};
-                a = join_lanes(a, p.scale2);
+            if (!TOP || CLUSTER) {
+                group_meet<WARPS>(id);
+                if (warp == 0) a = join_lanes(lane < WARPS ? room.shares[turn][lane] : Share{-kInf, 0.0f, 0.0f}, p.scale2);
             }
             turn ^= 1;
         }
@@ -456,38 +486,45 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
                     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(place_in(&room.far_share[part].s, 0)), "f"(a.s) : "memory");
                     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(place_in(&room.far_share[part].w, 0)), "f"(a.w) : "memory");
                 }
-                if constexpr (TOP)
-                    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(place_in(&room.far_list[part * kMostTop + lane], 0)), "l"(room.list[lane]) : "memory");
+                if constexpr (TOP) {
+                    const uint64_t v = lane < have ? room.list[side][lane] : 0;
+                    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(place_in(&room.far_list[part * kMostTop + lane], 0)), "l"(v) : "memory");
+                }
             }
             cluster_meet();
-            if (part == 0 && warp == 0) {
-                a = lane < parts ? room.far_share[lane] : Share{-kInf, 0.0f, 0.0f};
-                a = join_lanes(a, p.scale2);
+            if (part == 0 && (TOP || warp == 0)) {
+                a = join_lanes(lane < parts ? room.far_share[lane] : Share{-kInf, 0.0f, 0.0f}, p.scale2);
                 if constexpr (TOP) {
-                    const uint64_t mine = select(room.far_list, parts * kMostTop, p.top, lane);
-                    room.list[lane] = mine;
-                    __syncwarp();
+                    const bool odd_row = a.s != a.s;
+                    const float base = base_of(a.m), log_s = logf(a.s);
+                    int there = 0;
+                    for (int i = t; i < parts * kMostTop; i += kThreads) {
+                        const uint64_t v = room.far_list[i];
+                        const int k = v ? above(room.far_list, parts * kMostTop, v) : kMostTop;
+                        if (k < p.top) {
+                            p.top_ids[(int64_t)r * p.top + k] = odd_row ? -1 : (int64_t)(uint32_t)~(uint32_t)v;
+                            p.top_logp[(int64_t)r * p.top + k] = odd_row ? a.s : (value_of((uint32_t)(v >> 32)) - base) * p.scale - log_s;
+                        }
+                    }
+                    if (warp == 0) {
+                        there = above(room.far_list, parts * kMostTop, 0);
+                        if (lane >= there && lane < p.top) {
+                            p.top_ids[(int64_t)r * p.top + lane] = -1;
+                            p.top_logp[(int64_t)r * p.top + lane] = odd_row ? a.s : -kInf;
+                        }
+                    }
                 }
             }
         }
-        if (part == 0 && warp == 0) {
-            const bool none = a.m == -kInf && a.s == 0.0f, odd_row = a.s != a.s;
+        if (part == 0 && t == 0) {
+            const bool none = a.m == -kInf && a.s == 0.0f;
             const float base = base_of(a.m), log_s = logf(a.s);
-            if (lane == 0) {
-                p.lse[r] = none ? -kInf : fmaf(base, p.scale, log_s);
-                if (p.entropy != nullptr) {
-                    const float h = none ? 0.0f : log_s - a.w / a.s * kLn2;
-                    p.entropy[r] = h < 0.0f ? 0.0f : h;  // by the roundings of a certain token's row
-                }
-                if (p.logp != nullptr) p.logp[r] = !inside ? 0.0f : none ? -kInf : (given - base) * p.scale - log_s;
+            p.lse[r] = none ? -kInf : fmaf(base, p.scale, log_s);
+            if (p.entropy != nullptr) {
+                const float h = none ? 0.0f : log_s - a.w / a.s * kLn2;
+                p.entropy[r] = h < 0.0f ? 0.0f : h;  // by the roundings of a certain token's row
             }
-            if constexpr (TOP) {
-                if (lane < p.top) {
-                    const uint64_t v = odd_row ? 0 : room.list[lane];
-                    p.top_ids[(int64_t)r * p.top + lane] = v ? (int64_t)(uint32_t)~(uint32_t)v : -1;
-                    p.top_logp[(int64_t)r * p.top + lane] = odd_row ? a.s : v ? (value_of((uint32_t)(v >> 32)) - base) * p.scale - log_s : -kInf;
-                }
-            }
+            if (p.logp != nullptr) p.logp[r] = !inside ? 0.0f : none ? -kInf : (given - base) * p.scale - log_s;
         }
         if constexpr (CLUSTER) cluster_meet();  // the first block has read what the others sent
     }
@@ -557,7 +594,7 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const LogGr
         const int64_t id = p.g == nullptr ? -1 : p.id_bytes == 8 ? static_cast<const int64_t *>(p.ids)[r] : static_cast<const int32_t *>(p.ids)[r];
         const float lse = p.lse[r], g = id >= 0 && id < p.vocab ? p.g[r] : 0.0f;
         const float ge = ENTROPY ? p.ge[r] : 0.0f, h = ENTROPY ? p.entropy[r] : 0.0f;
-        const bool none = lse == -kInf;  // no token can be: zeros
+        const bool none = lse < -1e30f;  // no token can be: zeros
         const int at = none || id < 0 || id >= p.vocab ? -1 : (int)id;
         const float off = none ? 0.0f : -lse * kLog2e, hot = p.scale * g;
         const float c0 = none ? 0.0f : ENTROPY ? -p.scale * fmaf(ge, h, g) : -hot, c1 = none ? 0.0f : -p.scale * kLn2 * ge;
@@ -642,7 +679,7 @@ ra_status ra_logprobs(const void *logits, int64_t ld, int dtype, int64_t rows, i
         for (int q = 0; q < o; ++q)
             if (mats_overlap(out[o], out[q])) return RA_ERR_OVERLAP;
     }
-    const LogParams p{logits, ids, logp, lse, entropy, top_logp, top_ids, ld, rows, (int)vocab, top, id_bytes, scale, scale * kLog2e, 200.0f / (scale * kLog2e)};
+    const LogParams p{logits, ids, logp, lse, entropy, top_logp, top_ids, ld, rows, (int)vocab, top, id_bytes, scale, scale * kLog2e};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == RA_F32) return cuda_status(top > 0 ? launch_logprobs<float, true>(p, s) : launch_logprobs<float, false>(p, s));
     return cuda_status(top > 0 ? launch_logprobs<uint16_t, true>(p, s) : launch_logprobs<uint16_t, false>(p, s));

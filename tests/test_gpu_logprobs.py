@@ -231,6 +231,10 @@ def test_gradient_of_masked_rows(vocab):
         for entropy in (False, True):
             got = _check_grad(z, ids, 1.0, entropy)
             assert not bool(got[1].any()) and not bool(got[0, 5:].any()) and not bool(got[2, :-1].any())
+    z[0] = torch.finfo(dtype).min  # masked throughout by the type's lowest value: no gradient either
+    r = ra.ra_logprobs(z, ids, entropy=True)
+    e = torch.ones(6, device="cuda")
+    assert not bool(ra.ra_logprobs_grad(z, ids, r.lse, e, entropy=r.entropy, grad_entropy=e)[0].any())
     z[5, 1] = NAN
     r = ra.ra_logprobs(z, ids)
     got = ra.ra_logprobs_grad(z, torch.zeros_like(ids), r.lse, torch.ones(6, device="cuda"))
