@@ -13,17 +13,16 @@ constexpr float kInf = INFINITY;
 // ---------------------------------------------------------------------------
 // forward
 //
-// One pass over the logits: every thread keeps the largest logit it has met and
-// the sums of 2^y and y 2^y relative to it, and these shares are joined at the
-// row's end.  WARPS warps take a row (8 rows a block with one warp), in tiles of
-// kSlots 16-byte vectors a thread.  A tile is read asynchronously into the
-// thread's own places in shared memory and from there into registers, after
-// which the next tile, of this row or the next, is on its way while this one is
-// worked on: no thread waits for another's loads.  Rows of any alignment: the
-// few logits before the first and after the last whole vector are one more value
-// of the first threads.
+// One pass over the logits: every thread keeps the sums of 2^y and y 2^y relative
+// to one of its logits, and these shares are joined at the row's end.  WARPS warps
+// take a row, in tiles of kSlots 16-byte vectors a thread.  A tile is read
+// asynchronously into the thread's own places in shared memory; as a place is read
+// from there, the same place of the next tile, of this row or the next, is on its
+// way: no thread waits for another's loads.  Rows of any alignment: the few logits
+// before the first and after the last whole vector are one more value of the first
+// threads.
 
-constexpr int kSlots = 8;
+constexpr int kSlots = 16, kBatch = 4, kLogThreads = 256;
 
 struct LogParams {
     const void *logits, *ids;
@@ -31,7 +30,7 @@ struct LogParams {
     int64_t *top_ids;
     int64_t ld, rows;
     int vocab, top, id_bytes;
-    float scale, scale2;  // scale2: scale / ln 2
+    float scale, scale2, reach;  // scale2: scale / ln 2; reach: 200 / scale2, beyond which 2^y is 0
 };
 
 // A logit and its index as a number that orders as the alternatives do: by
@@ -125,6 +124,16 @@ struct Vec {
             return j & 1 ? __uint_as_float(w[j / 2] & 0xffff0000u) : __uint_as_float(w[j / 2] << 16);
     }
 };
+// the largest bf16 not above x, twice in a word
+__device__ __forceinline__ uint32_t floor_bf16x2(float x) {
+    const uint32_t b = __float_as_uint(x), h = (b & 0x80000000u ? b + 0xffffu : b) >> 16;
+    return __byte_perm(h, h, 0x1010);
+}
+__device__ __forceinline__ uint32_t larger_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 template <class T>
 __device__ __forceinline__ float largest(const Vec<T> &v) {
     float m = fmaxf(v[0], v[1]);
@@ -140,8 +149,8 @@ constexpr int kMostTop = RA_LOGPROBS_MAX_TOP;
 // other blocks of a cluster send to the first.
 template <int WARPS, bool TOP, bool CLUSTER>
 struct RowRoom {
-    static constexpr int kList = !TOP ? 1 : WARPS == 1 ? 224 : 992;
-    uint64_t list[2][TOP ? kMostTop + kList : 1];
+    static constexpr int kList = !TOP ? 1 : WARPS == 8 ? 480 : 224;  // what log_blocks leave room for
+    uint64_t list[WARPS == 8 ? 2 : 1][TOP ? kMostTop + kList : 1];  // rows of fewer warps are one tile
     uint64_t far_list[TOP && CLUSTER ? kMostBlocks * kMostTop : 1];
     uint64_t round[WARPS];
     Share shares[2][WARPS];
@@ -178,42 +187,36 @@ __device__ __forceinline__ int above(const uint64_t *list, int n, uint64_t v) {
     return k;
 }
 
-template <int WARPS>
-constexpr int log_threads() {
-    return WARPS == 1 ? 256 : WARPS * 32;
-}
-template <int WARPS>
+template <int WARPS, bool TOP>
 constexpr int log_blocks() {  // resident on an SM
-    return WARPS == 1 ? 3 : WARPS == 4 ? 8 : 2;
+    return WARPS < 8 && TOP ? 2 : 3;
 }
 template <int WARPS, bool TOP, bool CLUSTER>
 constexpr int log_smem() {
-    return log_threads<WARPS>() * kSlots * 16 + log_threads<WARPS>() / (WARPS * 32) * (int)sizeof(RowRoom<WARPS, TOP, CLUSTER>);
+    return kLogThreads * kSlots * 16 + kLogThreads / (WARPS * 32) * (int)sizeof(RowRoom<WARPS, TOP, CLUSTER>);
 }
 
-// f(Const<0>()), f(Const<1>()), ..: a tile's places as constants
-template <class F>
-__device__ __forceinline__ void each_slot(F &&f) {
-    static_assert(kSlots == 8, "each_slot");
-    f(Const<0>());
-    f(Const<1>());
-    f(Const<2>());
-    f(Const<3>());
-    f(Const<4>());
-    f(Const<5>());
-    f(Const<6>());
-    f(Const<7>());
+// a * b + c and a + b on pairs, the result in registers of its own
+__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 template <class T, int WARPS, bool TOP, bool CLUSTER>
-__global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) logprobs_kernel(const LogParams p) {
+__global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprobs_kernel(const LogParams p) {
     using Room = RowRoom<WARPS, TOP, CLUSTER>;
-    constexpr int kThreads = WARPS * 32, kGroups = log_threads<WARPS>() / kThreads, kEach = Vec<T>::kEach, kTile = kThreads * kSlots;  // vectors
+    constexpr int kThreads = WARPS * 32, kGroups = kLogThreads / kThreads, kEach = Vec<T>::kEach, kTile = kThreads * kSlots;  // vectors
     extern __shared__ __align__(16) unsigned char smem[];
     const int t = threadIdx.x % kThreads, lane = threadIdx.x & 31, warp = t / 32, id = threadIdx.x / kThreads;
-    Room &room = reinterpret_cast<Room *>(smem + log_threads<WARPS>() * kSlots * 16)[id];
+    Room &room = reinterpret_cast<Room *>(smem + kLogThreads * kSlots * 16)[id];
     const uint32_t land = smem_addr(smem) + threadIdx.x * 16;  // the thread's places, kPitch apart
-    constexpr int kPitch = log_threads<WARPS>() * 16;
+    constexpr int kPitch = kLogThreads * 16;
     if (t < 2) room.count[t] = 0;
     group_meet<WARPS>(id);
     pdl_enter();
@@ -228,13 +231,18 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
         vecs = (p.vocab - head) / kEach;
         steps = max(1, ceil_div(vecs, kTile * parts));
     };
-    // one load of a tile, into place i: `left` vectors are left of the row from `from` on
-    auto fetch = [&](auto place, const T *from, int left) {
-        constexpr int i = decltype(place)::value;
-        if (left > i * kThreads)
-            asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(land), "l"(from), "n"(i * kPitch), "n"(i * kThreads * 16) : "memory");
-        else
-            asm volatile("st.shared.v4.b32 [%0 + %2], {%1, %1, %1, %1};" ::"r"(land), "r"(sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u), "n"(i * kPitch) : "memory");
+    // the loads of a tile into places i0 .. i0 + 3; `left` vectors are left of the row from `from` on
+    auto fetch = [&](int i0, const T *from, int left) {
+        const uint32_t to = land + i0 * kPitch;
+        from += i0 * kThreads * kEach;
+        left -= i0 * kThreads;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (left > i * kThreads)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * kPitch), "l"(from + i * kThreads * kEach) : "memory");
+            else
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to + i * kPitch), "r"(sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u) : "memory");
+        }
     };
 
     const T *row;
@@ -242,7 +250,7 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
     if (first < last_row) {
         shape(first, row, head, vecs, steps);
         const int v0 = part * kTile + t;
-        each_slot([&](auto place) { fetch(place, row + head + (int64_t)v0 * kEach, vecs - v0); });
+        for (int i0 = 0; i0 < kSlots && i0 * kThreads < vecs - v0 + t; i0 += kBatch) fetch(i0, row + head + (int64_t)v0 * kEach, vecs - v0);
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
     for (int r = first; r < last_row; r += stride) {
@@ -280,37 +288,66 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
                     ahead_left = vecs - (part * kTile + t);
                 }
             }
-            float s[2] = {0.0f, 0.0f}, w[2] = {0.0f, 0.0f}, most = odd, off = 0.0f;
+            // y = z scale2 - off.  bf16 logits are held in pairs, before they are taken
+            // apart, to a least value whose exponential is 0 (low); beside the lowest
+            // finite ones there is none.  Where that is so, or the thread's first
+            // logits cannot be, the sums are made the other way below (not plain).
+            uint64_t s2 = Two(0.0f).v, w2 = Two(0.0f).v, off2 = Two(0.0f).v;
+            const uint64_t scale2 = Two(p.scale2).v;
+            float most = odd, off = 0.0f;
+            uint32_t low = 0;
+            bool plain = true;
+            auto start = [&](float m) {
+                if (a.m == -kInf) a.m = m;
+                const float base = base_of(a.m);
+                off = base * p.scale2;
+                off2 = Two(-off).v;
+                plain = a.m > -kInf && fabsf(off) < 1e30f;
+                if constexpr (sizeof(T) == 2) {
+                    low = floor_bf16x2(base - p.reach);
+                    plain = plain && low != 0xff80ff80u && (base - __uint_as_float(low & 0xffff0000u)) * p.scale2 >= -kLeast;
+                }
+            };
+            const int ahead_slots = min(kSlots, ceil_div(ahead_left + t, kThreads)), both = max(slots, ahead_slots);
             asm volatile("cp.async.wait_group 0;" ::: "memory");
-            Vec<T> x[2];  // a place is read while the one before is worked on
-            x[0].take(land);
-            each_slot([&](auto place) {
-                constexpr int i = decltype(place)::value;
-                if constexpr (i + 1 < kSlots) x[(i + 1) & 1].take(land + (i + 1) * kPitch);
-                fetch(place, ahead, ahead_left);  // what this place held has been read
-                if (i >= slots) return;
-                const Vec<T> &v = x[i & 1];
-                if (i == 0) {
-                    if (a.m == -kInf) a.m = fmaxf(odd, largest(v));
-                    off = base_of(a.m) * p.scale2;
-                }
+            if (slots <= 0) start(odd);
+#pragma unroll 1
+            for (int i0 = 0; i0 < both; i0 += kBatch) {
+                Vec<T> x[kBatch];
+                if (i0 < slots) {
 #pragma unroll
-                for (int j = 0; j < kEach; j += 2) most = max3(most, v[j], v[j + 1]);
-#pragma unroll
-                for (int j = 0; j < kEach; ++j) {
-                    const float y = at_least(fmaf(v[j], p.scale2, -off)), e = fast_exp2(y);
-                    s[j & 1] += e;
-                    w[j & 1] = fmaf(e, y, w[j & 1]);
+                    for (int i = 0; i < kBatch; ++i) x[i].take(land + (i0 + i) * kPitch);
                 }
-                // in this order, or the compiler reads all places first and runs out of registers
-                asm volatile("" : "+f"(s[0]), "+f"(s[1]), "+f"(w[0]), "+f"(w[1]), "+f"(most));
-            });
+                if (i0 < ahead_slots) fetch(i0, ahead, ahead_left);  // what these places held has been read
+                if (i0 == 0 && slots > 0) start(fmaxf(odd, largest(x[0])));
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    if (i0 + i >= slots) break;
+#pragma unroll
+                    for (int j = 0; j < kEach; j += 2) {
+                        if constexpr (sizeof(T) == 2) x[i].w[j / 2] = larger_nan(x[i].w[j / 2], low);
+                        const float z0 = x[i][j], z1 = x[i][j + 1];
+                        most = max3(most, z0, z1);
+                        Two y(0.0f);
+                        y.v = pair_fma(Two(z0, z1).v, scale2, off2);
+                        float y0, y1;
+                        y.get(&y0, &y1);
+                        if constexpr (sizeof(T) == 4) {
+                            y0 = at_least(y0);
+                            y1 = at_least(y1);
+                            y = Two(y0, y1);
+                        }
+                        const uint64_t e = Two(fast_exp2(y0), fast_exp2(y1)).v;
+                        s2 = pair_add(s2, e);
+                        w2 = pair_fma(e, y.v, w2);
+                    }
+                }
+            }
             asm volatile("cp.async.commit_group;" ::: "memory");
+            float s[2], w[2];
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(s[0]), "=f"(s[1]) : "l"(s2));
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(w[0]), "=f"(w[1]) : "l"(w2));
             if (step == 0) {
-                if (slots <= 0) {
-                    a.m = odd;
-                    off = base_of(odd) * p.scale2;
-                }
                 const float y = at_least(fmaf(odd, p.scale2, -off)), e = fast_exp2(y);
                 s[0] += e;
                 w[0] = fmaf(e, y, w[0]);
@@ -319,24 +356,27 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
                 // y came with what the rounding of `off` leaves, `by`
                 const float by = fmaf(base_of(a.m), p.scale2, -off), sum = s[0] + s[1], f = fmaf(by, -kLn2, 1.0f);
                 const float s_new = fmaf(sum, f, a.s), w_new = fmaf(fmaf(-by, sum, w[0] + w[1]), f, a.w);
-                if (fabsf(off) < 1e30f && s_new < 1e37f) {
+                if (plain && s_new < 1e37f) {
                     a.s = s_new;
                     a.w = w_new;
-                    if (a.m == -kInf && most > -kInf) a.m = 0.0f;  // what was taken out
                 } else {  // from the largest, one by one (also: logits near the type's ends, NaN)
+                    const int end = now_head + min(now_vecs, g0 + kTile) * kEach;
+                    auto all = [&](auto &&f) {
+#pragma unroll 1
+                        for (int c = now_head + v0 * kEach; c < end; c += kThreads * kEach)
+#pragma unroll 1
+                            for (int j = 0; j < kEach; ++j) f(to_f32<T>(now[c + j]));
+                        f(odd);
+                    };
+                    most = -kInf;
+                    all([&](float z) { most = fmaxf(most, z); });
                     rebase(a, fmaxf(a.m, most), p.scale2);
                     const float base = base_of(a.m);
-                    auto add = [&](float z) {
+                    all([&](float z) {
                         const float y = at_least((z - base) * p.scale2), e = fast_exp2(y);
                         a.s += e;
                         a.w = fmaf(e, y, a.w);
-                    };
-                    const int end = now_head + min(now_vecs, g0 + kTile) * kEach;
-#pragma unroll 1
-                    for (int c = now_head + v0 * kEach; c < end; c += kThreads * kEach)
-#pragma unroll 1
-                        for (int j = 0; j < kEach; ++j) add(to_f32<T>(now[c + j]));
-                    if (step == 0) add(odd);
+                    });
                 }
             }
             if (last_step) {
@@ -365,7 +405,7 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
                     }
                 }
                 key = low;
-                uint64_t *const list = room.list[side];
+                uint64_t *const list = room.list[WARPS == 8 ? side : 0];
                 if (have == p.top) key = max(key, (uint32_t)(list[p.top - 1] >> 32));  // of the best so far
                 const float least = fmaxf(value_of(key), -3.402823466e38f);
                 int *const count = &room.count[side];
@@ -453,7 +493,7 @@ __global__ void __launch_bounds__(log_threads<WARPS>(), log_blocks<WARPS>()) log
                             p.top_ids[(int64_t)r * p.top + k] = odd_row || v == 0 ? -1 : (int64_t)(uint32_t)~(uint32_t)v;
                             p.top_logp[(int64_t)r * p.top + k] = odd_row ? a.s : v == 0 ? -kInf : (value_of((uint32_t)(v >> 32)) - base) * p.scale - log_s;
                         } else {
-                            room.list[side][k] = v;
+                            room.list[WARPS == 8 ? side : 0][k] = v;  // (never with fewer warps)
                         }
                     };
                     if (few) {  // each finds its place by counting those above it
@@ -535,20 +575,20 @@ cudaError_t launch_logprobs(const LogParams &p, int cluster, cudaStream_t s) {
     constexpr int kBytes = log_smem<WARPS, TOP, CLUSTER>();
     const cudaError_t e = opt_in_smem<logprobs_kernel<T, WARPS, TOP, CLUSTER>>(kBytes);
     if (e != cudaSuccess) return e;
-    const int64_t groups = WARPS == 1 ? log_threads<1>() / 32 : 1, blocks = ceil_div<int64_t>(p.rows, groups), most = 152 * log_blocks<WARPS>() / cluster;
-    return launch_clusters(logprobs_kernel<T, WARPS, TOP, CLUSTER>, (blocks < most ? blocks : most) * cluster, cluster, log_threads<WARPS>(), kBytes, s, p);
+    const int64_t blocks = ceil_div<int64_t>(p.rows, kLogThreads / (WARPS * 32)), most = 152 * log_blocks<WARPS, TOP>() / cluster;
+    return launch_clusters(logprobs_kernel<T, WARPS, TOP, CLUSTER>, (blocks < most ? blocks : most) * cluster, cluster, kLogThreads, kBytes, s, p);
 }
 
 template <class T, bool TOP>
 cudaError_t launch_logprobs(const LogParams &p, cudaStream_t s) {
     const int vecs = ceil_div(p.vocab, Vec<T>::kEach);
     if (vecs <= 32 * kSlots) return launch_logprobs<T, 1, TOP, false>(p, 1, s);
-    if (vecs <= 128 * kSlots) return launch_logprobs<T, 4, TOP, false>(p, 1, s);
+    if (vecs <= 64 * kSlots) return launch_logprobs<T, 2, TOP, false>(p, 1, s);
     // few long rows: clusters share a row, while all blocks run at once
-    const int64_t tiles = ceil_div(vecs, 512 * kSlots);
+    const int64_t tiles = ceil_div(vecs, kLogThreads * kSlots);
     int cluster = 1;
-    while (cluster < kMostBlocks && cluster < tiles && p.rows * cluster * 2 <= 152 * log_blocks<16>()) cluster *= 2;
-    return cluster == 1 ? launch_logprobs<T, 16, TOP, false>(p, 1, s) : launch_logprobs<T, 16, TOP, true>(p, cluster, s);
+    while (cluster < kMostBlocks && cluster < tiles && p.rows * cluster * 2 <= 152 * 2) cluster *= 2;
+    return cluster == 1 ? launch_logprobs<T, 8, TOP, false>(p, 1, s) : launch_logprobs<T, 8, TOP, true>(p, cluster, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -679,7 +719,7 @@ ra_status ra_logprobs(const void *logits, int64_t ld, int dtype, int64_t rows, i
         for (int q = 0; q < o; ++q)
             if (mats_overlap(out[o], out[q])) return RA_ERR_OVERLAP;
     }
-    const LogParams p{logits, ids, logp, lse, entropy, top_logp, top_ids, ld, rows, (int)vocab, top, id_bytes, scale, scale * kLog2e};
+    const LogParams p{logits, ids, logp, lse, entropy, top_logp, top_ids, ld, rows, (int)vocab, top, id_bytes, scale, scale * kLog2e, 200.0f / (scale * kLog2e)};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == RA_F32) return cuda_status(top > 0 ? launch_logprobs<float, true>(p, s) : launch_logprobs<float, false>(p, s));
     return cuda_status(top > 0 ? launch_logprobs<uint16_t, true>(p, s) : launch_logprobs<uint16_t, false>(p, s));
