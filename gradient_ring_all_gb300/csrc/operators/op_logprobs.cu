@@ -29,7 +29,7 @@ struct LogParams {
     float *logp, *lse, *entropy, *top_logp;
     int64_t *top_ids;
     int64_t ld, rows;
-    int vocab, top, id_bytes;
+    int vocab, top, groups, id_bytes;  // groups: the next power of 2 to top
     float scale, scale2, reach;  // scale2: scale / ln 2; reach: 200 / scale2, beyond which 2^y is 0
 };
 
@@ -104,18 +104,10 @@ struct Vec {
         w[2] = q.z;
         w[3] = q.w;
     }
-    // the first value goes, the others move up
-    __device__ __forceinline__ void next() {
-        if constexpr (sizeof(T) == 4) {
-            w[0] = w[1];
-            w[1] = w[2];
-            w[2] = w[3];
-        } else {
-            w[0] = __funnelshift_r(w[0], w[1], 16);
-            w[1] = __funnelshift_r(w[1], w[2], 16);
-            w[2] = __funnelshift_r(w[2], w[3], 16);
-            w[3] >>= 16;
-        }
+    __device__ __forceinline__ float at(int j) const {  // j not a constant
+        const int k = sizeof(T) == 4 ? j : j / 2;
+        const uint32_t v = k < 2 ? (k == 0 ? w[0] : w[1]) : (k == 2 ? w[2] : w[3]);
+        return __uint_as_float(sizeof(T) == 4 ? v : j & 1 ? v & 0xffff0000u : v << 16);
     }
     __device__ __forceinline__ float operator[](int j) const {
         if constexpr (sizeof(T) == 4)
@@ -156,6 +148,7 @@ struct RowRoom {
     Share shares[2][WARPS];
     Share far_share[CLUSTER ? kMostBlocks : 1];
     uint32_t keys[32];
+    int64_t token[2];  // this row's id and the next one's, as they lie in memory
     int count[2];
 };
 
@@ -224,12 +217,19 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
     if constexpr (CLUSTER) cluster_meet();
     const int first = CLUSTER ? blockIdx.x / parts : blockIdx.x * kGroups + id, stride = CLUSTER ? gridDim.x / parts : gridDim.x * kGroups, last_row = (int)p.rows;
 
-    // where a row's whole vectors begin and how many there are
-    auto shape = [&](int r, const T *&row, int &head, int &vecs, int &steps) {
-        row = static_cast<const T *>(p.logits) + (int64_t)r * p.ld;
-        head = min((int)(-(reinterpret_cast<intptr_t>(row) / (int)sizeof(T)) & (kEach - 1)), p.vocab);
-        vecs = (p.vocab - head) / kEach;
-        steps = max(1, ceil_div(vecs, kTile * parts));
+    struct Row {  // where a row's whole vectors begin, how many logits are before them, how many vectors there are
+        const T *begin;
+        int head, vecs;
+        // the index of the logit outside the whole vectors that thread t has, or -1
+        __device__ __forceinline__ int odd_place(int t, int vocab) const {
+            const int i = t < 8 ? t : head + vecs * kEach + t - 8;
+            return t < 16 && i < (t < 8 ? head : vocab) ? i : -1;
+        }
+    };
+    auto row_at = [&](int r) {
+        const T *from = static_cast<const T *>(p.logits) + (int64_t)r * p.ld;
+        const int head = min((int)(-(reinterpret_cast<intptr_t>(from) / (int)sizeof(T)) & (kEach - 1)), p.vocab);
+        return Row{from + head, head, (p.vocab - head) / kEach};
     };
     // the loads of a tile into places i0 .. i0 + 3; `left` vectors are left of the row from `from` on
     auto fetch = [&](int i0, const T *from, int left) {
@@ -245,47 +245,55 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
         }
     };
 
-    const T *row;
-    int head, vecs, steps, turn = 0, side = 0;
+    int turn = 0, side = 0;
+    const bool finishes = part == 0 && t == 0 && p.logp != nullptr;  // looks after the given token
+    auto fetch_token = [&](int r) {
+        if (!finishes) return;
+        const uint32_t to = smem_addr(&room.token[turn]);
+        if (p.id_bytes == 8)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(static_cast<const int64_t *>(p.ids) + r) : "memory");
+        else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(static_cast<const int32_t *>(p.ids) + r) : "memory");
+    };
+
     if (first < last_row) {
-        shape(first, row, head, vecs, steps);
+        const Row row = row_at(first);
         const int v0 = part * kTile + t;
-        for (int i0 = 0; i0 < kSlots && i0 * kThreads < vecs - v0 + t; i0 += kBatch) fetch(i0, row + head + (int64_t)v0 * kEach, vecs - v0);
+        for (int i0 = 0; i0 < kSlots && i0 * kThreads < row.vecs - v0 + t; i0 += kBatch) fetch(i0, row.begin + (int64_t)v0 * kEach, row.vecs - v0);
+        fetch_token(first);
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
     for (int r = first; r < last_row; r += stride) {
+        const Row row = row_at(r);
+        const int steps = max(1, ceil_div(row.vecs, kTile * parts));
         Share a{-kInf, 0.0f, 0.0f};
-        // the logits outside the whole vectors: one a thread of the first 16
-        float odd = -kInf;
-        int odd_at = 0;
-        if (part == 0 && t < 16) {
-            const int tail = head + vecs * kEach;
-            odd_at = t < 8 ? t : tail + t - 8;
-            if (t < 8 ? t < head : odd_at < p.vocab) odd = to_f32<T>(row[odd_at]);
-        }
-        float given = 0.0f;  // the given token's logit
+        // one of the logits outside the whole vectors, for the first 16 threads
+        Raw<T, 1> odd_raw, given;
+        const int odd_at = row.odd_place(t, p.vocab);
+        const bool has_odd = part == 0 && odd_at >= 0;
+        if (has_odd) odd_raw.load(row.begin - row.head + odd_at);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         bool inside = false;
-        if (part == 0 && t == 0 && p.logp != nullptr) {
-            const int64_t i = p.id_bytes == 8 ? static_cast<const int64_t *>(p.ids)[r] : static_cast<const int32_t *>(p.ids)[r];
+        if (finishes) {
+            const int64_t i = p.id_bytes == 8 ? *(volatile int64_t *)&room.token[turn] : *(volatile int32_t *)&room.token[turn];
             inside = i >= 0 && i < p.vocab;
-            if (inside) given = to_f32<T>(row[i]);
+            if (inside) given.load(row.begin - row.head + i);
         }
-        const T *now = row;
-        const int now_head = head, now_vecs = vecs, now_steps = steps;
+        turn ^= 1;
         int have = 0;  // of the best
-        for (int step = 0; step < now_steps; ++step) {
+        for (int step = 0; step < steps; ++step) {
             const int v0 = (step * parts + part) * kTile + t;
-            const int g0 = v0 - t, slots = min(kSlots, ceil_div(now_vecs - g0, kThreads));  // the same for the whole group
-            const bool last_step = step + 1 == now_steps;
+            const int g0 = v0 - t, slots = min(kSlots, ceil_div(row.vecs - g0, kThreads));  // the same for the whole group
+            const bool last_step = step + 1 == steps;
             // where the next tile's loads are: this row's, the next row's, or none
-            const T *ahead = now + now_head + (int64_t)(v0 + kTile * parts) * kEach;
-            int ahead_left = now_vecs - (v0 + kTile * parts);
+            const T *ahead = row.begin + (int64_t)(v0 + kTile * parts) * kEach;
+            int ahead_left = row.vecs - (v0 + kTile * parts);
             if (last_step) {
                 ahead_left = 0;
                 if (r + stride < last_row) {
-                    shape(r + stride, row, head, vecs, steps);
-                    ahead = row + head + (int64_t)(part * kTile + t) * kEach;
-                    ahead_left = vecs - (part * kTile + t);
+                    const Row next = row_at(r + stride);
+                    ahead = next.begin + (int64_t)(part * kTile + t) * kEach;
+                    ahead_left = next.vecs - (part * kTile + t);
                 }
             }
             // y = z scale2 - off.  bf16 logits are held in pairs, before they are taken
@@ -294,7 +302,8 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
             // logits cannot be, the sums are made the other way below (not plain).
             uint64_t s2 = Two(0.0f).v, w2 = Two(0.0f).v, off2 = Two(0.0f).v;
             const uint64_t scale2 = Two(p.scale2).v;
-            float most = odd, off = 0.0f;
+            float most = -kInf, second = -kInf, off = 0.0f;  // largest of the batches, and of the others
+            int most_at = 0;
             uint32_t low = 0;
             bool plain = true;
             auto start = [&](float m) {
@@ -309,8 +318,7 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
                 }
             };
             const int ahead_slots = min(kSlots, ceil_div(ahead_left + t, kThreads)), both = max(slots, ahead_slots);
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            if (slots <= 0) start(odd);
+            if (step > 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll 1
             for (int i0 = 0; i0 < both; i0 += kBatch) {
                 Vec<T> x[kBatch];
@@ -319,7 +327,8 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
                     for (int i = 0; i < kBatch; ++i) x[i].take(land + (i0 + i) * kPitch);
                 }
                 if (i0 < ahead_slots) fetch(i0, ahead, ahead_left);  // what these places held has been read
-                if (i0 == 0 && slots > 0) start(fmaxf(odd, largest(x[0])));
+                if (i0 == 0 && slots > 0) start(largest(x[0]));
+                float here = -kInf;
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
                     if (i0 + i >= slots) break;
@@ -327,7 +336,7 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
                     for (int j = 0; j < kEach; j += 2) {
                         if constexpr (sizeof(T) == 2) x[i].w[j / 2] = larger_nan(x[i].w[j / 2], low);
                         const float z0 = x[i][j], z1 = x[i][j + 1];
-                        most = max3(most, z0, z1);
+                        if constexpr (TOP) here = max3(here, z0, z1);
                         Two y(0.0f);
                         y.v = pair_fma(Two(z0, z1).v, scale2, off2);
                         float y0, y1;
@@ -342,8 +351,16 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
                         w2 = pair_fma(e, y.v, w2);
                     }
                 }
+                if constexpr (TOP) {
+                    second = fmaxf(second, fminf(most, here));
+                    most_at = here > most ? i0 : most_at;
+                    most = fmaxf(most, here);
+                }
             }
+            if (last_step && r + stride < last_row) fetch_token(r + stride);
             asm volatile("cp.async.commit_group;" ::: "memory");
+            const float odd = has_odd && step == 0 ? odd_raw[0] : -kInf;
+            if (slots <= 0) start(odd);
             float s[2], w[2];
             asm("mov.b64 {%0, %1}, %2;" : "=f"(s[0]), "=f"(s[1]) : "l"(s2));
             asm("mov.b64 {%0, %1}, %2;" : "=f"(w[0]), "=f"(w[1]) : "l"(w2));
@@ -360,23 +377,25 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
                     a.s = s_new;
                     a.w = w_new;
                 } else {  // from the largest, one by one (also: logits near the type's ends, NaN)
-                    const int end = now_head + min(now_vecs, g0 + kTile) * kEach;
+                    const int end = min(row.vecs, g0 + kTile) * kEach;
                     auto all = [&](auto &&f) {
 #pragma unroll 1
-                        for (int c = now_head + v0 * kEach; c < end; c += kThreads * kEach)
+                        for (int c = v0 * kEach; c < end; c += kThreads * kEach)
 #pragma unroll 1
-                            for (int j = 0; j < kEach; ++j) f(to_f32<T>(now[c + j]));
-                        f(odd);
+                            for (int j = 0; j < kEach; ++j) f(to_f32<T>(row.begin[c + j]));
                     };
                     most = -kInf;
                     all([&](float z) { most = fmaxf(most, z); });
-                    rebase(a, fmaxf(a.m, most), p.scale2);
+                    second = most;
+                    rebase(a, max3(a.m, most, odd), p.scale2);
                     const float base = base_of(a.m);
-                    all([&](float z) {
+                    auto add = [&](float z) {
                         const float y = at_least((z - base) * p.scale2), e = fast_exp2(y);
                         a.s += e;
                         a.w = fmaf(e, y, a.w);
-                    });
+                    };
+                    all(add);
+                    add(odd);
                 }
             }
             if (last_step) {
@@ -386,66 +405,72 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
 
             if constexpr (TOP) {
                 // A bound that `top` logits reach: of the largest logits of 32 groups of
-                // threads the top-th.  The logits that reach it are the candidates,
-                // few more than top (9 for 8, 31 for 20, where they lie at random).
+                // threads the top-th, or for up to 8 the least of as many groups as the
+                // next power of 2.  The logits that reach it are the candidates (22 for
+                // 8, 31 for 20, where they lie at random).
                 constexpr int kEachWarp = 32 / WARPS;  // groups
-                uint32_t key = key_of(most);
+                uint32_t key = key_of(fmaxf(most, odd));
 #pragma unroll
                 for (int o = 16 / kEachWarp; o > 0; o /= 2) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
                 if (lane % (32 / kEachWarp) == 0) room.keys[warp * kEachWarp + lane / (32 / kEachWarp)] = key;
                 group_meet<WARPS>(id);
                 key = room.keys[lane];
-                uint32_t low = key;
-                if (p.top == 32) {
-                    low = __reduce_min_sync(0xffffffffu, key);
+                if (p.top <= 8) {
+                    for (int o = p.groups; o < 32; o *= 2) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
+                    key = __reduce_min_sync(0xffffffffu, key);
                 } else {
-                    for (int k = 0; k < p.top; ++k) {
-                        low = __reduce_max_sync(0xffffffffu, key);
-                        if (lane == __ffs(__ballot_sync(0xffffffffu, key == low)) - 1) key = 0;
+                    int before = 0;
+#pragma unroll 8
+                    for (int i = 0; i < 32; ++i) {
+                        const uint32_t o = room.keys[i];
+                        before += o > key || (o == key && i < lane);
                     }
+                    key = __shfl_sync(0xffffffffu, key, __ffs(__ballot_sync(0xffffffffu, before == p.top - 1)) - 1);
                 }
-                key = low;
                 uint64_t *const list = room.list[WARPS == 8 ? side : 0];
                 if (have == p.top) key = max(key, (uint32_t)(list[p.top - 1] >> 32));  // of the best so far
                 const float least = fmaxf(value_of(key), -3.402823466e38f);
                 int *const count = &room.count[side];
                 auto push = [&](float z, uint32_t i) {
-                    if (z >= least && *(volatile int *)count <= Room::kList) {
+                    if (*(volatile int *)count <= Room::kList) {
                         const int at = atomicAdd(count, 1);
                         if (at < Room::kList) list[have + at] = rank_of(z, i);
                     }
                 };
-                const uint32_t index0 = (uint32_t)now_head + (uint32_t)v0 * kEach;
+                if (odd >= least) push(odd, odd_at);
                 if (most >= least) {
-                    // read again, by the few threads that have some (from L2), four at a time
-                    const T *from = now + now_head + (int64_t)v0 * kEach;
-                    const int left = now_vecs - v0;
-#pragma unroll 1
-                    for (int i0 = 0; i0 < kSlots && left > i0 * kThreads; i0 += 4) {
-                        Vec<T> q[4];
+                    // The batch that has the largest is read again (from L2, by few
+                    // threads), the others where they have some too.
+                    auto again = [&](int i0) {
+                        const int v = v0 + i0 * kThreads, left = row.vecs - v;
+                        const T *from = row.begin + (int64_t)v * kEach;
+                        Vec<T> q[kBatch];
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i)
+                            if (left > i * kThreads) q[i].load(from + i * kThreads * kEach);
                         uint32_t hits = 0;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            q[i].none();
-                            if (left > (i0 + i) * kThreads) q[i].load(from + (i0 + i) * kThreads * kEach);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) hits |= largest(q[i]) >= least ? 1u << i : 0u;
+                        for (int i = 0; i < kBatch; ++i) hits |= left > i * kThreads && largest(q[i]) >= least ? 1u << i : 0u;
 #pragma unroll 1
                         for (; hits != 0; hits &= hits - 1) {
                             const int i = __ffs(hits) - 1;
-                            Vec<T> v = q[0];
+                            Vec<T> x = q[0];
 #pragma unroll
-                            for (int k = 1; k < 4; ++k)
-                                if (k == i) v = q[k];
+                            for (int k = 1; k < kBatch; ++k)
+                                if (k == i) x = q[k];
+                            uint32_t which = 0;
+#pragma unroll
+                            for (int j = 0; j < kEach; ++j) which |= x[j] >= least ? 1u << j : 0u;
 #pragma unroll 1
-                            for (int j = 0; j < kEach; ++j) {
-                                push(v[0], index0 + (uint32_t)((i0 + i) * kThreads * kEach + j));
-                                v.next();
+                            for (; which != 0; which &= which - 1) {
+                                const int j = __ffs(which) - 1;
+                                push(x.at(j), (uint32_t)row.head + (uint32_t)(v + i * kThreads) * kEach + j);
                             }
                         }
-                    }
-                    push(odd, odd_at);
+                    };
+                    const bool more = second >= least;
+#pragma unroll 1
+                    for (int i0 = more ? 0 : most_at; i0 < slots; i0 += more ? kBatch : kSlots) again(i0);
                 }
                 group_meet<WARPS>(id);
                 int n = *(volatile int *)count;
@@ -459,9 +484,9 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
                             const uint64_t v = rank_of(z, i);
                             if (v < last && v > best) best = v;
                         };
-                        const int end = now_head + min(now_vecs, g0 + kTile) * kEach;
-                        for (int c = now_head + v0 * kEach; c < end; c += kThreads * kEach)
-                            for (int j = 0; j < kEach; ++j) look(to_f32<T>(now[c + j]), c + j);
+                        const int end = min(row.vecs, g0 + kTile) * kEach;
+                        for (int c = v0 * kEach; c < end; c += kThreads * kEach)
+                            for (int j = 0; j < kEach; ++j) look(to_f32<T>(row.begin[c + j]), row.head + c + j);
                         look(odd, odd_at);
                         best = warp_max(best);
                         if constexpr (WARPS > 1) {
@@ -509,7 +534,6 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
                     }
                 }
             }
-            odd = -kInf;  // it was in the first tile
         }
 
         if constexpr (WARPS > 1) {
@@ -517,7 +541,6 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
                 group_meet<WARPS>(id);
                 if (warp == 0) a = join_lanes(lane < WARPS ? room.shares[turn][lane] : Share{-kInf, 0.0f, 0.0f}, p.scale2);
             }
-            turn ^= 1;
         }
         if constexpr (CLUSTER) {
             if (warp == 0) {
@@ -564,7 +587,7 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
                 const float h = none ? 0.0f : log_s - a.w / a.s * kLn2;
                 p.entropy[r] = h < 0.0f ? 0.0f : h;  // by the roundings of a certain token's row
             }
-            if (p.logp != nullptr) p.logp[r] = !inside ? 0.0f : none ? -kInf : (given - base) * p.scale - log_s;
+            if (p.logp != nullptr) p.logp[r] = !inside ? 0.0f : none ? -kInf : (given[0] - base) * p.scale - log_s;
         }
         if constexpr (CLUSTER) cluster_meet();  // the first block has read what the others sent
     }
@@ -719,7 +742,9 @@ ra_status ra_logprobs(const void *logits, int64_t ld, int dtype, int64_t rows, i
         for (int q = 0; q < o; ++q)
             if (mats_overlap(out[o], out[q])) return RA_ERR_OVERLAP;
     }
-    const LogParams p{logits, ids, logp, lse, entropy, top_logp, top_ids, ld, rows, (int)vocab, top, id_bytes, scale, scale * kLog2e, 200.0f / (scale * kLog2e)};
+    int groups = 1;
+    while (groups < top) groups *= 2;
+    const LogParams p{logits, ids, logp, lse, entropy, top_logp, top_ids, ld, rows, (int)vocab, top, groups, id_bytes, scale, scale * kLog2e, 200.0f / (scale * kLog2e)};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == RA_F32) return cuda_status(top > 0 ? launch_logprobs<float, true>(p, s) : launch_logprobs<float, false>(p, s));
     return cuda_status(top > 0 ? launch_logprobs<uint16_t, true>(p, s) : launch_logprobs<uint16_t, false>(p, s));
