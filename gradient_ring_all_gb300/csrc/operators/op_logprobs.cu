@@ -22,7 +22,7 @@ constexpr float kInf = INFINITY;
 // before the first and after the last whole vector are one more value of the first
 // threads.
 
-constexpr int kSlots = 16, kBatch = 4, kLogThreads = 256;
+constexpr int kSlots = 16, kLogThreads = 256;
 
 struct LogParams {
     const void *logits, *ids;
@@ -141,19 +141,19 @@ constexpr int kMostTop = RA_LOGPROBS_MAX_TOP;
 // other blocks of a cluster send to the first.
 template <int WARPS, bool TOP, bool CLUSTER>
 struct RowRoom {
-    static constexpr int kList = !TOP ? 1 : WARPS == 8 ? 480 : 224;  // what log_blocks leave room for
+    static constexpr int kList = !TOP ? 1 : WARPS == 8 ? 224 : 288;  // what log_blocks leave room for
     uint64_t list[WARPS == 8 ? 2 : 1][TOP ? kMostTop + kList : 1];  // rows of fewer warps are one tile
     uint64_t far_list[TOP && CLUSTER ? kMostBlocks * kMostTop : 1];
     uint64_t round[WARPS];
     Share shares[2][WARPS];
     Share far_share[CLUSTER ? kMostBlocks : 1];
-    uint32_t keys[32];
+    uint32_t keys[64];
     int64_t token[2];  // this row's id and the next one's, as they lie in memory
     int count[2];
 };
 
 // The `top` highest of list[0 .. n), by one warp: lane j gets the j-th.
-__device__ __noinline__ uint64_t pick(const uint64_t *list, int n, int top, int lane) {
+__device__ __forceinline__ uint64_t pick(const uint64_t *list, int n, int top, int lane) {
     uint64_t last = ~0ull, mine = 0, best = 0;
     bool look = true;
     for (int k = 0; k < top; ++k) {
@@ -180,13 +180,69 @@ __device__ __forceinline__ int above(const uint64_t *list, int n, uint64_t v) {
     return k;
 }
 
+// one more candidate, as long as the list has room
+__device__ __forceinline__ void push(float z, uint32_t i, uint64_t *list, int room, int *count) {
+    if (*(volatile int *)count <= room) {
+        const int at = atomicAdd(count, 1);
+        if (at < room) list[at] = rank_of(z, i);
+    }
+}
+__device__ __forceinline__ float height_at(uint32_t shared) {
+    float h;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(h) : "r"(shared) : "memory");
+    return h;
+}
+// The logits from `least` on of a thread's vectors, BATCH a batch and THREADS apart,
+// of the `left` that are left of the row from `from` on (index: the first one's).
+// The batches that have some (heights: each one's largest, in shared memory) are
+// read again from L2.
+template <class T, int THREADS, int BATCH>
+__device__ __forceinline__ void collect(const T *from, int left, uint32_t index, int slots, uint32_t heights, float least, uint64_t *list, int room, int *count) {
+    constexpr int kEach = Vec<T>::kEach;
+    uint32_t which = 0;  // batches
+#pragma unroll
+    for (int i = 0; i < kSlots / BATCH; ++i) which |= i * BATCH < slots && height_at(heights + i * 4) >= least ? 1u << i : 0u;
+#pragma unroll 1
+    for (; which != 0; which &= which - 1) {
+        const int first = (__ffs(which) - 1) * (BATCH * THREADS);
+        Vec<T> q[BATCH];
+        uint32_t hits = 0;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+            if (left > first + i * THREADS) q[i].load(from + (first + i * THREADS) * kEach);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) hits |= left > first + i * THREADS && largest(q[i]) >= least ? 1u << i : 0u;
+#pragma unroll 1
+        for (; hits != 0; hits &= hits - 1) {
+            const int i = __ffs(hits) - 1;
+            Vec<T> x = q[0];
+#pragma unroll
+            for (int k = 1; k < BATCH; ++k)
+                if (k == i) x = q[k];
+            uint32_t these = 0;
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) these |= x[j] >= least ? 1u << j : 0u;
+#pragma unroll 1
+            for (; these != 0; these &= these - 1) {
+                const int j = __ffs(these) - 1;
+                push(x.at(j), index + (uint32_t)((first + i * THREADS) * kEach + j), list, room, count);
+            }
+        }
+    }
+}
+
+// places worked on at a time; rows of few vectors are not to fill four
+template <int WARPS>
+constexpr int batch_of() {
+    return WARPS == 1 ? 2 : 4;
+}
 template <int WARPS, bool TOP>
 constexpr int log_blocks() {  // resident on an SM
     return WARPS < 8 && TOP ? 2 : 3;
 }
 template <int WARPS, bool TOP, bool CLUSTER>
 constexpr int log_smem() {
-    return kLogThreads * kSlots * 16 + kLogThreads / (WARPS * 32) * (int)sizeof(RowRoom<WARPS, TOP, CLUSTER>);
+    return kLogThreads * kSlots * 16 + (TOP ? kLogThreads * kSlots / batch_of<WARPS>() * 4 : 0) + kLogThreads / (WARPS * 32) * (int)sizeof(RowRoom<WARPS, TOP, CLUSTER>);
 }
 
 // a * b + c and a + b on pairs, the result in registers of its own
@@ -205,9 +261,11 @@ template <class T, int WARPS, bool TOP, bool CLUSTER>
 __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprobs_kernel(const LogParams p) {
     using Room = RowRoom<WARPS, TOP, CLUSTER>;
     constexpr int kThreads = WARPS * 32, kGroups = kLogThreads / kThreads, kEach = Vec<T>::kEach, kTile = kThreads * kSlots;  // vectors
+    constexpr int kBatch = batch_of<WARPS>(), kHeights = TOP ? kLogThreads * kSlots / kBatch * 4 : 0;
     extern __shared__ __align__(16) unsigned char smem[];
     const int t = threadIdx.x % kThreads, lane = threadIdx.x & 31, warp = t / 32, id = threadIdx.x / kThreads;
-    Room &room = reinterpret_cast<Room *>(smem + kLogThreads * kSlots * 16)[id];
+    Room &room = reinterpret_cast<Room *>(smem + kLogThreads * kSlots * 16 + kHeights)[id];
+    const uint32_t heights = smem_addr(smem) + kLogThreads * kSlots * 16 + threadIdx.x * (kSlots / kBatch * 4);  // the largest logit of each batch
     const uint32_t land = smem_addr(smem) + threadIdx.x * 16;  // the thread's places, kPitch apart
     constexpr int kPitch = kLogThreads * 16;
     if (t < 2) room.count[t] = 0;
@@ -231,17 +289,24 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
         const int head = min((int)(-(reinterpret_cast<intptr_t>(from) / (int)sizeof(T)) & (kEach - 1)), p.vocab);
         return Row{from + head, head, (p.vocab - head) / kEach};
     };
-    // the loads of a tile into places i0 .. i0 + 3; `left` vectors are left of the row from `from` on
+    // the loads of a tile into places i0 .. i0 + 3; `left` vectors are left of the
+    // row from `from` on, this thread's first
     auto fetch = [&](int i0, const T *from, int left) {
         const uint32_t to = land + i0 * kPitch;
         from += i0 * kThreads * kEach;
         left -= i0 * kThreads;
+        if (left + t >= kBatch * kThreads) {  // all of the group's
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (left > i * kThreads)
+            for (int i = 0; i < kBatch; ++i)
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * kPitch), "l"(from + i * kThreads * kEach) : "memory");
-            else
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to + i * kPitch), "r"(sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u) : "memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (left > i * kThreads)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * kPitch), "l"(from + i * kThreads * kEach) : "memory");
+                else
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to + i * kPitch), "r"(sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u) : "memory");
+            }
         }
     };
 
@@ -302,8 +367,7 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
             // logits cannot be, the sums are made the other way below (not plain).
             uint64_t s2 = Two(0.0f).v, w2 = Two(0.0f).v, off2 = Two(0.0f).v;
             const uint64_t scale2 = Two(p.scale2).v;
-            float most = -kInf, second = -kInf, off = 0.0f;  // largest of the batches, and of the others
-            int most_at = 0;
+            float most = -kInf, off = 0.0f;  // the largest
             uint32_t low = 0;
             bool plain = true;
             auto start = [&](float m) {
@@ -322,16 +386,15 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
 #pragma unroll 1
             for (int i0 = 0; i0 < both; i0 += kBatch) {
                 Vec<T> x[kBatch];
-                if (i0 < slots) {
+                // places that no vector went to hold minus infinity
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i) x[i].take(land + (i0 + i) * kPitch);
-                }
+                for (int i = 0; i < kBatch; ++i) x[i].take(land + (i0 + i) * kPitch);
                 if (i0 < ahead_slots) fetch(i0, ahead, ahead_left);  // what these places held has been read
-                if (i0 == 0 && slots > 0) start(largest(x[0]));
+                if (i0 >= slots) continue;
+                if (i0 == 0) start(largest(x[0]));
                 float here = -kInf;
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    if (i0 + i >= slots) break;
 #pragma unroll
                     for (int j = 0; j < kEach; j += 2) {
                         if constexpr (sizeof(T) == 2) x[i].w[j / 2] = larger_nan(x[i].w[j / 2], low);
@@ -352,8 +415,7 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
                     }
                 }
                 if constexpr (TOP) {
-                    second = fmaxf(second, fminf(most, here));
-                    most_at = here > most ? i0 : most_at;
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(heights + i0 / kBatch * 4), "f"(here) : "memory");
                     most = fmaxf(most, here);
                 }
             }
@@ -386,7 +448,8 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
                     };
                     most = -kInf;
                     all([&](float z) { most = fmaxf(most, z); });
-                    second = most;
+                    if constexpr (TOP)
+                        for (int i = 0; i < kSlots / kBatch; ++i) asm volatile("st.shared.f32 [%0], %1;" ::"r"(heights + i * 4), "f"(most) : "memory");
                     rebase(a, max3(a.m, most, odd), p.scale2);
                     const float base = base_of(a.m);
                     auto add = [&](float z) {
@@ -404,21 +467,31 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
             }
 
             if constexpr (TOP) {
-                // A bound that `top` logits reach: of the largest logits of 32 groups of
-                // threads the top-th, or for up to 8 the least of as many groups as the
-                // next power of 2.  The logits that reach it are the candidates (22 for
-                // 8, 31 for 20, where they lie at random).
+                // A bound that `top` logits reach: of the largest logits of groups of
+                // threads the top-th.  The logits that reach it are the candidates.  Up
+                // to 8: as many groups as the next power of 2, the least of them; up to
+                // 20: 32 groups, each place found by counting; else 64 groups, one by
+                // one.  (22 candidates for 8, 31 for 20, 44 for 32, where logits lie at
+                // random; more groups cost more than fewer candidates save.)
                 constexpr int kEachWarp = 32 / WARPS;  // groups
-                uint32_t key = key_of(fmaxf(most, odd));
-#pragma unroll
-                for (int o = 16 / kEachWarp; o > 0; o /= 2) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
-                if (lane % (32 / kEachWarp) == 0) room.keys[warp * kEachWarp + lane / (32 / kEachWarp)] = key;
+                const int fine = p.top > 20 ? 2 : 1;   // times as many
+                uint32_t key = key_of(fmaxf(most, odd)), other = 0;
+                if (WARPS == 1 && fine == 2) {  // a lane's batches are two groups
+                    float h[2] = {odd, -kInf};
+                    for (int i = 0; i * kBatch < slots; ++i) h[i & 1] = fmaxf(h[i & 1], height_at(heights + i * 4));
+                    key = key_of(h[0]);
+                    other = key_of(h[1]);
+                    room.keys[32 + lane] = other;
+                }
+                const int lanes = WARPS == 1 ? 1 : 32 / (kEachWarp * fine);  // of a group
+                for (int o = lanes / 2; o > 0; o /= 2) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
+                if (lane % lanes == 0) room.keys[(warp * 32 + lane) / lanes] = key;
                 group_meet<WARPS>(id);
                 key = room.keys[lane];
                 if (p.top <= 8) {
                     for (int o = p.groups; o < 32; o *= 2) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
                     key = __reduce_min_sync(0xffffffffu, key);
-                } else {
+                } else if (fine == 1) {
                     int before = 0;
 #pragma unroll 8
                     for (int i = 0; i < 32; ++i) {
@@ -426,52 +499,24 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
                         before += o > key || (o == key && i < lane);
                     }
                     key = __shfl_sync(0xffffffffu, key, __ffs(__ballot_sync(0xffffffffu, before == p.top - 1)) - 1);
+                } else {
+                    other = room.keys[32 + lane];
+                    uint32_t low = 0;
+#pragma unroll 1
+                    for (int k = 0; k < p.top; ++k) {
+                        low = __reduce_max_sync(0xffffffffu, max(key, other));
+                        if (lane == __ffs(__ballot_sync(0xffffffffu, max(key, other) == low)) - 1) (key == low ? key : other) = 0;
+                    }
+                    key = low;
                 }
                 uint64_t *const list = room.list[WARPS == 8 ? side : 0];
                 if (have == p.top) key = max(key, (uint32_t)(list[p.top - 1] >> 32));  // of the best so far
                 const float least = fmaxf(value_of(key), -3.402823466e38f);
                 int *const count = &room.count[side];
-                auto push = [&](float z, uint32_t i) {
-                    if (*(volatile int *)count <= Room::kList) {
-                        const int at = atomicAdd(count, 1);
-                        if (at < Room::kList) list[have + at] = rank_of(z, i);
-                    }
-                };
-                if (odd >= least) push(odd, odd_at);
-                if (most >= least) {
-                    // The batch that has the largest is read again (from L2, by few
-                    // threads), the others where they have some too.
-                    auto again = [&](int i0) {
-                        const int v = v0 + i0 * kThreads, left = row.vecs - v;
-                        const T *from = row.begin + (int64_t)v * kEach;
-                        Vec<T> q[kBatch];
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i)
-                            if (left > i * kThreads) q[i].load(from + i * kThreads * kEach);
-                        uint32_t hits = 0;
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i) hits |= left > i * kThreads && largest(q[i]) >= least ? 1u << i : 0u;
-#pragma unroll 1
-                        for (; hits != 0; hits &= hits - 1) {
-                            const int i = __ffs(hits) - 1;
-                            Vec<T> x = q[0];
-#pragma unroll
-                            for (int k = 1; k < kBatch; ++k)
-                                if (k == i) x = q[k];
-                            uint32_t which = 0;
-#pragma unroll
-                            for (int j = 0; j < kEach; ++j) which |= x[j] >= least ? 1u << j : 0u;
-#pragma unroll 1
-                            for (; which != 0; which &= which - 1) {
-                                const int j = __ffs(which) - 1;
-                                push(x.at(j), (uint32_t)row.head + (uint32_t)(v + i * kThreads) * kEach + j);
-                            }
-                        }
-                    };
-                    const bool more = second >= least;
-#pragma unroll 1
-                    for (int i0 = more ? 0 : most_at; i0 < slots; i0 += more ? kBatch : kSlots) again(i0);
-                }
+                if (odd >= least) push(odd, odd_at, list + have, Room::kList, count);
+                if (most >= least)
+                    collect<T, kThreads, kBatch>(row.begin + (int64_t)v0 * kEach, row.vecs - v0, (uint32_t)row.head + (uint32_t)v0 * kEach, slots, heights, least,
+                                                 list + have, Room::kList, count);
                 group_meet<WARPS>(id);
                 int n = *(volatile int *)count;
                 if (n > Room::kList) {
@@ -551,7 +596,7 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
                 }
                 if constexpr (TOP) {
                     const uint64_t v = lane < have ? room.list[side][lane] : 0;
-                    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(place_in(&room.far_list[part * kMostTop + lane], 0)), "l"(v) : "memory");
+                    if (lane < p.top) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(place_in(&room.far_list[part * p.top + lane], 0)), "l"(v) : "memory");
                 }
             }
             cluster_meet();
@@ -561,16 +606,16 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
                     const bool odd_row = a.s != a.s;
                     const float base = base_of(a.m), log_s = logf(a.s);
                     int there = 0;
-                    for (int i = t; i < parts * kMostTop; i += kThreads) {
+                    for (int i = t; i < parts * p.top; i += kThreads) {
                         const uint64_t v = room.far_list[i];
-                        const int k = v ? above(room.far_list, parts * kMostTop, v) : kMostTop;
+                        const int k = v ? above(room.far_list, parts * p.top, v) : kMostTop;
                         if (k < p.top) {
                             p.top_ids[(int64_t)r * p.top + k] = odd_row ? -1 : (int64_t)(uint32_t)~(uint32_t)v;
                             p.top_logp[(int64_t)r * p.top + k] = odd_row ? a.s : (value_of((uint32_t)(v >> 32)) - base) * p.scale - log_s;
                         }
                     }
                     if (warp == 0) {
-                        there = above(room.far_list, parts * kMostTop, 0);
+                        there = above(room.far_list, parts * p.top, 0);
                         if (lane >= there && lane < p.top) {
                             p.top_ids[(int64_t)r * p.top + lane] = -1;
                             p.top_logp[(int64_t)r * p.top + lane] = odd_row ? a.s : -kInf;
