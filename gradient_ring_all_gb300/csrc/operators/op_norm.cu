@@ -20,7 +20,7 @@ struct NormParams {
 template <class TX, class TF, int W, int N, int WARPS, bool JOIN, bool CLUSTER>
 __global__ void __launch_bounds__(WARPS * 32 < kNormThreads ? kNormThreads : WARPS * 32) norm_kernel(const NormParams p) {
     constexpr int kGroups = WARPS * 32 < kNormThreads ? kNormThreads / (WARPS * 32) : 1;  // rows at a time
-    using Sums = RowSums<1, WARPS, CLUSTER>;
+    using Sums = RowSums<2, WARPS, CLUSTER>;
     __shared__ Sums sums[kGroups];
     pdl_enter();
     if constexpr (CLUSTER) cluster_meet();  // every block is there before another writes to it
@@ -29,28 +29,42 @@ __global__ void __launch_bounds__(WARPS * 32 < kNormThreads ? kNormThreads : WAR
     int turn = 0;
     const int64_t blocks = CLUSTER ? gridDim.x / cluster_blocks() : gridDim.x, block = CLUSTER ? blockIdx.x / cluster_blocks() : blockIdx.x;
 
-    // m and rstd of a row
+    // m and rstd of a row.  The sums of the values and of their squares are made at
+    // once; where the mean is so large that their difference loses more than 4
+    // bits, the squares of the differences from it are summed after it.
     auto moments = [&](const float (&v)[N][W], const Side &side, float *m, float *rstd) {
-        float s[1] = {0.0f};
-        *m = 0.0f;
-        if (side.kind == RA_NORM_LAYER) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-#pragma unroll
-                for (int j = 0; j < W; ++j) s[0] += v[i][j];  // columns past the row's end hold 0
-            row_sum(s, sums[id], id, turn);
-            *m = s[0] * p.per_d;
-        }
-        s[0] = 0.0f;
+        float s[2] = {0.0f, 0.0f}, var;
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int j = 0; j < W; ++j) {
-                const float c = v[i][j] - *m;
-                if (col[i] < p.d) s[0] = fmaf(c, c, s[0]);
+            for (int j = 0; j < W; ++j) {  // columns past the row's end hold 0
+                s[0] += v[i][j];
+                s[1] = fmaf(v[i][j], v[i][j], s[1]);
             }
         row_sum(s, sums[id], id, turn);
-        *rstd = rsqrtf(fmaf(s[0], p.per_d, side.eps));
+        *m = 0.0f;
+        var = s[1] * p.per_d;
+        if (side.kind == RA_NORM_LAYER) {
+            *m = s[0] * p.per_d;
+            const float left = fmaf(-*m, *m, var);
+            if (!(left * 16.0f >= var) && var > 0.0f) {  // the same for the whole row
+                s[0] = s[1] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (col[i] < p.d) {
+#pragma unroll
+                        for (int j = 0; j < W; ++j) {
+                            const float c = v[i][j] - *m;
+                            s[0] = fmaf(c, c, s[0]);
+                        }
+                    }
+                row_sum(s, sums[id], id, turn);
+                var = s[0] * p.per_d;
+            } else {
+                var = left;
+            }
+        }
+        *rstd = rsqrtf(var + side.eps);
     };
     auto apply = [&](float (&v)[W], const Side &side, float m, float rstd, int64_t c) {
         float g[W], b[W];
