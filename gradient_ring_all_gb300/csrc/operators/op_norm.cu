@@ -10,54 +10,75 @@ struct NormParams {
     const void *x, *f, *gate;
     void *x_out, *h;
     float *kept;
-    int64_t ld_x, ld_f, ld_gate, ld_x_out, ld_h, rows, d;
+    int64_t ld_x, ld_f, ld_gate, ld_x_out, ld_h, rows;
+    int d, gate_kind;
     Side post, pre;
-    int gate_kind;
-    bool gate_f32, gate_wide;
+    bool gate_f32;
     float alpha, beta, per_d;  // per_d: 1 / d
 };
 
-template <class TX, class TF, int W, int N, int WARPS, bool JOIN, bool CLUSTER>
-__global__ void __launch_bounds__(WARPS * 32 < kNormThreads ? kNormThreads : WARPS * 32) norm_kernel(const NormParams p) {
-    constexpr int kGroups = WARPS * 32 < kNormThreads ? kNormThreads / (WARPS * 32) : 1;  // rows at a time
-    using Sums = RowSums<2, WARPS, CLUSTER>;
-    __shared__ Sums sums[kGroups];
+constexpr int kNormStages = 3, kNormBlocks = 3;  // rows under way a group, blocks an SM
+
+// 16-byte places a thread needs for a row
+template <class TX, class TF, bool JOIN>
+int norm_places(bool gate_matrix) {
+    return places<TX>() + (JOIN ? places<TF>() * (gate_matrix ? 2 : 1) : 0);
+}
+
+template <class TX, class TF, bool WIDE, int WARPS, bool JOIN, bool CLUSTER>
+__global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 ? 1 : kNormBlocks) norm_kernel(const NormParams p) {
+    constexpr int kThreads = WARPS == 16 ? 512 : kNormThreads, kGroups = kThreads / (WARPS * 32);  // kGroups: rows at a time
+    constexpr int kPitch = kThreads * 16, kAhead = kNormStages - 1;
+    __shared__ RowSums<2, WARPS, CLUSTER> sums[kGroups];
+    extern __shared__ __align__(16) unsigned char ring[];
     pdl_enter();
     if constexpr (CLUSTER) cluster_meet();  // every block is there before another writes to it
     const int id = threadIdx.x / (WARPS * 32);
-    const Columns<W, N, WARPS, CLUSTER> col;
+    const Columns<WIDE, WARPS, CLUSTER> col;
+    const int count = col.count(p.d);
     int turn = 0;
-    const int64_t blocks = CLUSTER ? gridDim.x / cluster_blocks() : gridDim.x, block = CLUSTER ? blockIdx.x / cluster_blocks() : blockIdx.x;
+    const bool by_matrix = JOIN && p.gate_kind == RA_GATE_MATRIX;
+
+    // post as (v - m) rstd a + b with the gate and beta in a and b, unless the gate
+    // has a value of its own for each v
+    float a_post[JOIN ? kOwn : 1], b_post[JOIN ? kOwn : 1], a_pre[kOwn], b_pre[kOwn];
+    if constexpr (JOIN) {
+        float g[kOwn];
+        load_param(p.post.gain, p.post.f32, col, count, 1.0f, a_post);
+        load_param(p.post.bias, p.post.f32, col, count, 0.0f, b_post);
+        load_param(p.gate_kind == RA_GATE_VECTOR ? p.gate : nullptr, p.gate_f32, col, count, 1.0f, g);
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j) {
+            a_post[j] *= p.beta * g[j];
+            b_post[j] *= p.beta * g[j];
+        }
+    }
+    load_param(p.pre.gain, p.pre.f32, col, count, 1.0f, a_pre);
+    load_param(p.pre.bias, p.pre.f32, col, count, 0.0f, b_pre);
 
     // m and rstd of a row.  The sums of the values and of their squares are made at
     // once; where the mean is so large that their difference loses more than 4
     // bits, the squares of the differences from it are summed after it.
-    auto moments = [&](const float (&v)[N][W], const Side &side, float *m, float *rstd) {
-        float s[2] = {0.0f, 0.0f}, var;
+    auto moments = [&](const float (&v)[kOwn], const Side &side, float *m, float *rstd) {
+        float s[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-#pragma unroll
-            for (int j = 0; j < W; ++j) {  // columns past the row's end hold 0
-                s[0] += v[i][j];
-                s[1] = fmaf(v[i][j], v[i][j], s[1]);
-            }
+        for (int j = 0; j < kOwn; ++j) {  // columns past the row's end hold 0
+            s[0] += v[j];
+            s[1] = fmaf(v[j], v[j], s[1]);
+        }
         row_sum(s, sums[id], id, turn);
         *m = 0.0f;
-        var = s[1] * p.per_d;
+        float var = s[1] * p.per_d;
         if (side.kind == RA_NORM_LAYER) {
             *m = s[0] * p.per_d;
             const float left = fmaf(-*m, *m, var);
             if (!(left * 16.0f >= var) && var > 0.0f) {  // the same for the whole row
                 s[0] = s[1] = 0.0f;
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (col[i] < p.d) {
-#pragma unroll
-                        for (int j = 0; j < W; ++j) {
-                            const float c = v[i][j] - *m;
-                            s[0] = fmaf(c, c, s[0]);
-                        }
-                    }
+                for (int j = 0; j < kOwn; ++j) {
+                    const float c = v[j] - *m;
+                    if (j < count) s[0] = fmaf(c, c, s[0]);
+                }
                 row_sum(s, sums[id], id, turn);
                 var = s[0] * p.per_d;
             } else {
@@ -66,70 +87,76 @@ __global__ void __launch_bounds__(WARPS * 32 < kNormThreads ? kNormThreads : WAR
         }
         *rstd = rsqrtf(var + side.eps);
     };
-    auto apply = [&](float (&v)[W], const Side &side, float m, float rstd, int64_t c) {
-        float g[W], b[W];
-        load_param<W>(side.gain, side.f32, side.gain_wide, c, 1.0f, g);
-        load_param<W>(side.bias, side.f32, side.bias_wide, c, 0.0f, b);
-#pragma unroll
-        for (int j = 0; j < W; ++j) v[j] = fmaf((v[j] - m) * rstd, g[j], b[j]);
-    };
 
-    for (int64_t r = block * kGroups + id; r < p.rows; r += blocks * kGroups) {
-        Raw<TX, W> rx[N];
-        Raw<TF, W> rf[JOIN ? N : 1], rg[JOIN ? N : 1];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (col[i] < p.d) {
-                rx[i].load(static_cast<const TX *>(p.x) + r * p.ld_x + col[i]);
-                if constexpr (JOIN) {
-                    rf[i].load(static_cast<const TF *>(p.f) + r * p.ld_f + col[i]);
-                    if (p.gate_kind == RA_GATE_MATRIX) rg[i].load(static_cast<const TF *>(p.gate) + r * p.ld_gate + col[i]);
-                }
-            } else {
-                rx[i].zero();
-                if constexpr (JOIN) rf[i].zero();
+    const int blocks = CLUSTER ? gridDim.x / cluster_blocks() : gridDim.x, block = CLUSTER ? blockIdx.x / cluster_blocks() : blockIdx.x;
+    const int64_t first = (int64_t)block * kGroups + id, step = (int64_t)blocks * kGroups;
+    const int stage_bytes = (places<TX>() + (JOIN ? places<TF>() * (by_matrix ? 2 : 1) : 0)) * kPitch;
+    const uint32_t mine = smem_addr(ring) + threadIdx.x * 16;
+    auto fetch = [&](int64_t r, int stage) {
+        if (r < p.rows && count > 0) {
+            uint32_t to = mine + stage * stage_bytes;
+            to = copy_own(to, kPitch, static_cast<const TX *>(p.x) + r * p.ld_x + col.first);
+            if constexpr (JOIN) {
+                to = copy_own(to, kPitch, static_cast<const TF *>(p.f) + r * p.ld_f + col.first);
+                if (by_matrix) copy_own(to, kPitch, static_cast<const TF *>(p.gate) + r * p.ld_gate + col.first);
             }
         }
-        float v[N][W], m_f = 0.0f, rstd_f = 0.0f, m_x = 0.0f, rstd_x = 0.0f;
+        copies_done();
+    };
+    int stage = 0;
+    if constexpr (WIDE) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) fetch(first + k * step, k);
+    }
+    for (int64_t r = first; r < p.rows; r += step) {
+        Own<TX, WIDE> x;
+        Own<TF, WIDE> f, g;
+        if constexpr (WIDE) {
+            fetch(r + kAhead * step, stage == 0 ? kAhead : stage - 1);
+            await_copies<kAhead>();
+            x.zero();
+            if constexpr (JOIN) f.zero();
+            if (count > 0) {
+                const uint32_t at = mine + stage * stage_bytes;
+                x.take(at, kPitch);
+                if constexpr (JOIN) {
+                    f.take(at + places<TX>() * kPitch, kPitch);
+                    if (by_matrix) g.take(at + (places<TX>() + places<TF>()) * kPitch, kPitch);
+                }
+            }
+            stage = stage == kAhead ? 0 : stage + 1;
+        } else {
+            x.load(static_cast<const TX *>(p.x) + r * p.ld_x, col, count);
+            if constexpr (JOIN) {
+                f.load(static_cast<const TF *>(p.f) + r * p.ld_f, col, count);
+                if (by_matrix) g.load(static_cast<const TF *>(p.gate) + r * p.ld_gate, col, count);
+            }
+        }
+        float v[kOwn], m_f = 0.0f, rstd_f = 0.0f, m_x = 0.0f, rstd_x = 0.0f;
         if constexpr (JOIN) {
 #pragma unroll
-            for (int i = 0; i < N; ++i)
+            for (int j = 0; j < kOwn; ++j) v[j] = f[j];
+            const bool normed = p.post.kind != RA_NORM_NONE;
+            if (normed) moments(v, p.post, &m_f, &rstd_f);
+            const float scale = normed ? rstd_f : 1.0f;
 #pragma unroll
-                for (int j = 0; j < W; ++j) v[i][j] = rf[i][j];
-            if (p.post.kind != RA_NORM_NONE) moments(v, p.post, &m_f, &rstd_f);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                if (col[i] >= p.d) continue;
-                if (p.post.kind != RA_NORM_NONE) apply(v[i], p.post, m_f, rstd_f, col[i]);
-                if (p.gate_kind == RA_GATE_MATRIX) {
-#pragma unroll
-                    for (int j = 0; j < W; ++j) v[i][j] *= rg[i][j];
-                } else if (p.gate_kind == RA_GATE_VECTOR) {
-                    float g[W];
-                    load_param<W>(p.gate, p.gate_f32, p.gate_wide, col[i], 1.0f, g);
-#pragma unroll
-                    for (int j = 0; j < W; ++j) v[i][j] *= g[j];
-                }
-#pragma unroll
-                for (int j = 0; j < W; ++j) v[i][j] = fmaf(p.alpha, rx[i][j], p.beta * v[i][j]);
-                store_w<TX, W>(static_cast<TX *>(p.x_out) + r * p.ld_x_out + col[i], v[i]);
-#pragma unroll
-                for (int j = 0; j < W; ++j) v[i][j] = to_f32<TX>(from_f32<TX>(v[i][j]));  // the norm is that of the row as stored
+            for (int j = 0; j < kOwn; ++j) {
+                v[j] = fmaf(v[j] - m_f, scale * a_post[j], b_post[j]);
+                if (by_matrix) v[j] *= g[j];
+                v[j] = fmaf(p.alpha, x[j], v[j]);
             }
+            store_own<TX, WIDE>(static_cast<TX *>(p.x_out) + r * p.ld_x_out, col, count, v);
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) v[j] = j < count ? to_f32<TX>(from_f32<TX>(v[j])) : 0.0f;  // the norm is that of the row as stored
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-#pragma unroll
-                for (int j = 0; j < W; ++j) v[i][j] = rx[i][j];
+            for (int j = 0; j < kOwn; ++j) v[j] = x[j];
         }
         if (p.pre.kind != RA_NORM_NONE) {
             moments(v, p.pre, &m_x, &rstd_x);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                if (col[i] >= p.d) continue;
-                apply(v[i], p.pre, m_x, rstd_x, col[i]);
-                store_w<TF, W>(static_cast<TF *>(p.h) + r * p.ld_h + col[i], v[i]);
-            }
+            for (int j = 0; j < kOwn; ++j) v[j] = fmaf(v[j] - m_x, rstd_x * a_pre[j], b_pre[j]);
+            store_own<TF, WIDE>(static_cast<TF *>(p.h) + r * p.ld_h, col, count, v);
         }
         if (p.kept != nullptr && col.first == 0) reinterpret_cast<float4 *>(p.kept)[r] = make_float4(m_f, rstd_f, m_x, rstd_x);
     }
@@ -137,29 +164,18 @@ __global__ void __launch_bounds__(WARPS * 32 < kNormThreads ? kNormThreads : WAR
 
 template <class TX, class TF, bool JOIN>
 cudaError_t launch_norm(const NormParams &p, bool wide, cudaStream_t s) {
-    auto go = [&](auto kernel, int warps, int cluster) {
-        const Shape sh{warps, cluster};
-        const int64_t most = 152 * 16;
-        const int64_t blocks = ceil_div<int64_t>(p.rows, sh.groups());
-        return launch_clusters(kernel, (blocks < most ? blocks : most) * cluster, cluster, sh.threads(), 0, s, p);
-    };
-    const int64_t d = p.d;
-    if (wide) {
-        if (d <= 256) return go(norm_kernel<TX, TF, 8, 1, 1, JOIN, false>, 1, 1);
-        if (d <= 512) return go(norm_kernel<TX, TF, 8, 2, 1, JOIN, false>, 1, 1);
-        if (d <= 1024) return go(norm_kernel<TX, TF, 8, 2, 2, JOIN, false>, 2, 1);
-        if (d <= 2048) return go(norm_kernel<TX, TF, 8, 2, 4, JOIN, false>, 4, 1);
-        if (d <= 4096) return go(norm_kernel<TX, TF, 8, 2, 8, JOIN, false>, 8, 1);
-        if (d <= 8192) return go(norm_kernel<TX, TF, 8, 2, 16, JOIN, false>, 16, 1);
-        return go(norm_kernel<TX, TF, 8, 2, 16, JOIN, true>, 16, d <= 16384 ? 2 : 4);
-    }
-    if (d <= 256) return go(norm_kernel<TX, TF, 1, 8, 1, JOIN, false>, 1, 1);
-    if (d <= 512) return go(norm_kernel<TX, TF, 1, 16, 1, JOIN, false>, 1, 1);
-    if (d <= 1024) return go(norm_kernel<TX, TF, 1, 16, 2, JOIN, false>, 2, 1);
-    if (d <= 2048) return go(norm_kernel<TX, TF, 1, 16, 4, JOIN, false>, 4, 1);
-    if (d <= 4096) return go(norm_kernel<TX, TF, 1, 16, 8, JOIN, false>, 8, 1);
-    if (d <= 8192) return go(norm_kernel<TX, TF, 1, 16, 16, JOIN, false>, 16, 1);
-    return go(norm_kernel<TX, TF, 1, 16, 16, JOIN, true>, 16, d <= 16384 ? 2 : 4);
+    const Shape sh(p.d);
+    return with_shape(sh, [&](auto warps, auto cluster) {
+        constexpr int kWarps = decltype(warps)::value;
+        constexpr bool kCluster = decltype(cluster)::value != 0;
+        const int64_t grid = sh.shares(p.rows, kNormBlocks) * sh.cluster;
+        if (!wide) return launch_clusters(norm_kernel<TX, TF, false, kWarps, JOIN, kCluster>, grid, sh.cluster, sh.threads(), 0, s, p);
+        constexpr int kMost = kNormStages * (places<TX>() + (JOIN ? 2 * places<TF>() : 0)) * 16 * (kWarps == 16 ? 512 : kNormThreads);
+        const cudaError_t e = opt_in_smem<norm_kernel<TX, TF, true, kWarps, JOIN, kCluster>>(kMost);
+        if (e != cudaSuccess) return e;
+        const int bytes = kNormStages * norm_places<TX, TF, JOIN>(p.gate_kind == RA_GATE_MATRIX) * 16 * sh.threads();
+        return launch_clusters(norm_kernel<TX, TF, true, kWarps, JOIN, kCluster>, grid, sh.cluster, sh.threads(), bytes, s, p);
+    });
 }
 
 template <bool JOIN>
@@ -201,8 +217,8 @@ extern "C" ra_status ra_norm_block(const ra_norm_block_args *args, void *stream)
             if (mats_overlap(out[o], out[q])) return RA_ERR_OVERLAP;
     }
     const Mat rows[] = {x, f, x_out, h, gate == RA_GATE_MATRIX ? gm : Mat{nullptr, 0, 0, 0, 4}};
-    const NormParams p{a.x,  a.f,  a.gate, a.x_out, a.h,     a.kept, a.ld_x, a.ld_f,                  a.ld_gate,       a.ld_x_out, a.ld_h, a.rows,
-                       a.d,  post, ahead,  gate,    gate == RA_GATE_VECTOR && a.gate_dtype == RA_F32, wide_at(a.gate), a.alpha,    a.beta, 1.0f / (float)a.d};
+    const NormParams p{a.x, a.f, a.gate, a.x_out, a.h, a.kept, a.ld_x, a.ld_f, a.ld_gate, a.ld_x_out, a.ld_h, a.rows, (int)a.d, gate, post, ahead,
+                       gate == RA_GATE_VECTOR && a.gate_dtype == RA_F32, a.alpha, a.beta, 1.0f / (float)a.d};
     const bool wide = all_wide(rows, a.d);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return cuda_status(join ? launch_norm<true>(p, a.x_dtype, a.f_dtype, wide, s) : launch_norm<false>(p, a.x_dtype, a.f_dtype, wide, s));

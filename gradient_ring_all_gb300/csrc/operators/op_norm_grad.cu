@@ -8,173 +8,230 @@ namespace {
 
 enum { kPreGain, kPreBias, kPostGain, kPostBias, kGate, kVectors };
 
+// A thread's values of a vector of parameters, read anew for each row (from L1): in
+// registers they would leave no room for the sums.
+template <bool WIDE, class C>
+__device__ __forceinline__ void load_vector(const void *v, bool f32, const C &col, int count, float none, float (&out)[kOwn]) {
+    if (v != nullptr && count > 0 && WIDE && reinterpret_cast<uintptr_t>(v) % 16 == 0) {
+        if (f32)
+            load_w<float, kOwn>(static_cast<const float *>(v) + col.first, out);
+        else
+            load_w<uint16_t, kOwn>(static_cast<const uint16_t *>(v) + col.first, out);
+    } else {
+        load_param(v, f32, col, count, none, out);
+    }
+}
+template <bool WIDE, int WARPS, bool CLUSTER>
+__device__ __forceinline__ void load_gain(const Side &side, const Columns<WIDE, WARPS, CLUSTER> &col, int count, float (&out)[kOwn]) {
+    load_vector<WIDE>(side.gain, side.f32, col, count, 1.0f, out);
+}
+
 struct NormGradParams {
     const void *dh, *dx_new, *x, *f, *gate;
     const float *kept;
     void *dx, *df, *dgate;  // dgate: a matrix's
-    float *parts;           // blocks x (kVectors or 2) x d, or null
-    int64_t ld_dh, ld_dx_new, ld_x, ld_f, ld_gate, ld_dx, ld_df, ld_dgate, rows, d;
+    float *parts;           // shares x (kVectors or 2) x d, or null
+    int64_t ld_dh, ld_dx_new, ld_x, ld_f, ld_gate, ld_dx, ld_df, ld_dgate, rows;
+    int d, gate_kind;
     Side post, pre;
-    int gate_kind;
-    bool gate_f32, gate_wide;
+    bool gate_f32;
     float alpha, beta, per_d;
 };
 
-template <class TX, class TF, int W, int N, int WARPS, bool JOIN, bool CLUSTER>
-__global__ void __launch_bounds__(WARPS * 32 < kNormThreads ? kNormThreads : WARPS * 32) norm_grad_kernel(const NormGradParams p) {
-    constexpr int kGroups = WARPS * 32 < kNormThreads ? kNormThreads / (WARPS * 32) : 1, kSums = JOIN ? kVectors : 2;
-    using Sums = RowSums<2, WARPS, CLUSTER>;
-    using Cols = Columns<W, N, WARPS, CLUSTER>;
-    __shared__ Sums sums[kGroups];
-    __shared__ float joined[kGroups > 1 ? Cols::kMost : 1];
+// rows under way a group
+template <class TX, class TF>
+constexpr int grad_stages() {
+    return sizeof(TF) == 4 ? 2 : 3;
+}
+// 16-byte places a thread needs for a row: dh, x, dx_new, f, the gate, kept
+template <class TX, class TF, bool JOIN>
+__host__ __device__ constexpr int grad_places(bool gate_matrix) {
+    return 1 + places<TF>() * ((JOIN ? 2 : 1) + (gate_matrix ? 1 : 0)) + 2 * places<TX>();
+}
+
+template <class TX, class TF, bool WIDE, int WARPS, bool JOIN, bool CLUSTER>
+__global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 ? 1 : 2) norm_grad_kernel(const NormGradParams p) {
+    constexpr int kThreads = WARPS == 16 ? 512 : kNormThreads, kGroups = kThreads / (WARPS * 32), kSums = JOIN ? kVectors : 2;
+    constexpr int kPitch = kThreads * 16, kAhead = grad_stages<TX, TF>() - 1;
+    __shared__ RowSums<2, WARPS, CLUSTER> sums[kGroups];
+    __shared__ float joined[kGroups > 1 ? WARPS * 32 * kOwn : 1];
+    extern __shared__ __align__(16) unsigned char ring[];
     pdl_enter();
     if constexpr (CLUSTER) cluster_meet();
     const int id = threadIdx.x / (WARPS * 32);
-    const Cols col;
+    const Columns<WIDE, WARPS, CLUSTER> col;
+    const int count = col.count(p.d);
     int turn = 0;
-    const int64_t blocks = CLUSTER ? gridDim.x / cluster_blocks() : gridDim.x, block = CLUSTER ? blockIdx.x / cluster_blocks() : blockIdx.x;
-    float acc[kSums][N][W];
+    const bool by_matrix = JOIN && p.gate_kind == RA_GATE_MATRIX, has_pre = p.dh != nullptr, has_new = p.dx_new != nullptr;
+    const bool normed = p.post.kind != RA_NORM_NONE;
+
+    float acc[kSums][kOwn];
 #pragma unroll
     for (int a = 0; a < kSums; ++a)
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-#pragma unroll
-            for (int j = 0; j < W; ++j) acc[a][i][j] = 0.0f;
+        for (int j = 0; j < kOwn; ++j) acc[a][j] = 0.0f;
 
-    for (int64_t r = block * kGroups + id; r < p.rows; r += blocks * kGroups) {
-        Raw<TX, W> rx[N], rd[N];
-        Raw<TF, W> rh[N], rf[JOIN ? N : 1], rg[JOIN ? N : 1];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            rx[i].zero();
-            rd[i].zero();
-            rh[i].zero();
-            if constexpr (JOIN) rf[i].zero();
-            if constexpr (JOIN) rg[i].zero();
-            if (col[i] < p.d) {
-                if (p.dh != nullptr) {
-                    rh[i].load(static_cast<const TF *>(p.dh) + r * p.ld_dh + col[i]);
-                    rx[i].load(static_cast<const TX *>(p.x) + r * p.ld_x + col[i]);
-                }
-                if (p.dx_new != nullptr) rd[i].load(static_cast<const TX *>(p.dx_new) + r * p.ld_dx_new + col[i]);
-                if constexpr (JOIN) {
-                    rf[i].load(static_cast<const TF *>(p.f) + r * p.ld_f + col[i]);
-                    if (p.gate_kind == RA_GATE_MATRIX) rg[i].load(static_cast<const TF *>(p.gate) + r * p.ld_gate + col[i]);
-                }
+    const int blocks = CLUSTER ? gridDim.x / cluster_blocks() : gridDim.x, block = CLUSTER ? blockIdx.x / cluster_blocks() : blockIdx.x;
+    const int64_t first = (int64_t)block * kGroups + id, step = (int64_t)blocks * kGroups;
+    const int stage_bytes = grad_places<TX, TF, JOIN>(by_matrix) * kPitch;
+    const uint32_t mine = smem_addr(ring) + threadIdx.x * 16;
+    auto fetch = [&](int64_t r, int stage) {
+        if (r < p.rows && count > 0) {
+            uint32_t to = mine + stage * stage_bytes;
+            if (p.kept != nullptr) copy_own(to, kPitch, reinterpret_cast<const uint16_t *>(p.kept + r * 4));
+            to += kPitch;
+            if (has_pre) {
+                copy_own(to, kPitch, static_cast<const TF *>(p.dh) + r * p.ld_dh + col.first);
+                copy_own(to + places<TF>() * kPitch, kPitch, static_cast<const TX *>(p.x) + r * p.ld_x + col.first);
+            }
+            to += (places<TF>() + places<TX>()) * kPitch;
+            if (has_new) copy_own(to, kPitch, static_cast<const TX *>(p.dx_new) + r * p.ld_dx_new + col.first);
+            to += places<TX>() * kPitch;
+            if constexpr (JOIN) {
+                to = copy_own(to, kPitch, static_cast<const TF *>(p.f) + r * p.ld_f + col.first);
+                if (by_matrix) copy_own(to, kPitch, static_cast<const TF *>(p.gate) + r * p.ld_gate + col.first);
             }
         }
-        const float4 kept = p.kept != nullptr ? reinterpret_cast<const float4 *>(p.kept)[r] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float full[N][W];
+        copies_done();
+    };
+    int stage = 0;
+    if constexpr (WIDE) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-#pragma unroll
-            for (int j = 0; j < W; ++j) full[i][j] = rd[i][j];
-        if (p.dh != nullptr) {
-            float s[2] = {0.0f, 0.0f}, v[N][W];
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                if (col[i] >= p.d) continue;
-                load_param<W>(p.pre.gain, p.pre.f32, p.pre.gain_wide, col[i], 1.0f, v[i]);
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    const float unit = (rx[i][j] - kept.z) * kept.w;
-                    v[i][j] *= rh[i][j];
-                    s[0] = fmaf(v[i][j], unit, s[0]);
-                    s[1] += v[i][j];
-                    acc[kPreGain][i][j] = fmaf(rh[i][j], unit, acc[kPreGain][i][j]);
-                    acc[kPreBias][i][j] += rh[i][j];
+        for (int k = 0; k < kAhead; ++k) fetch(first + k * step, k);
+    }
+    for (int64_t r = first; r < p.rows; r += step) {
+        Own<TX, WIDE> x, d;
+        Own<TF, WIDE> h, f, g;
+        float4 kept = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        uint32_t at = mine + stage * stage_bytes + kPitch;
+        if constexpr (WIDE) {
+            fetch(r + kAhead * step, stage == 0 ? kAhead : stage - 1);
+            await_copies<kAhead>();
+            h.zero();
+            x.zero();
+            if (count > 0) {
+                if (p.kept != nullptr)
+                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(kept.x), "=f"(kept.y), "=f"(kept.z), "=f"(kept.w) : "r"(at - kPitch) : "memory");
+                if (has_pre) {
+                    h.take(at, kPitch);
+                    x.take(at + places<TF>() * kPitch, kPitch);
                 }
+            }
+            at += (places<TF>() + places<TX>()) * kPitch;
+            stage = stage == kAhead ? 0 : stage + 1;
+        } else {
+            if (p.kept != nullptr) kept = reinterpret_cast<const float4 *>(p.kept)[r];
+            h.zero();
+            x.zero();
+            if (has_pre) {
+                h.load(static_cast<const TF *>(p.dh) + r * p.ld_dh, col, count);
+                x.load(static_cast<const TX *>(p.x) + r * p.ld_x, col, count);
+            }
+            d.zero();
+            if (has_new) d.load(static_cast<const TX *>(p.dx_new) + r * p.ld_dx_new, col, count);
+            if constexpr (JOIN) {
+                f.load(static_cast<const TF *>(p.f) + r * p.ld_f, col, count);
+                if (by_matrix) g.load(static_cast<const TF *>(p.gate) + r * p.ld_gate, col, count);
+            }
+        }
+        float full[kOwn], by_unit = 0.0f, plain = 0.0f;
+        if (has_pre) {
+            float s[2] = {0.0f, 0.0f}, gain[kOwn];
+            load_gain(p.pre, col, count, gain);
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) {  // columns past the row's end: h and x are 0, and so is what they add
+                const float unit = (x[j] - kept.z) * kept.w;
+                full[j] = h[j] * gain[j];
+                s[0] = fmaf(full[j], unit, s[0]);
+                s[1] += full[j];
+                acc[kPreGain][j] = fmaf(h[j], unit, acc[kPreGain][j]);
+                acc[kPreBias][j] += h[j];
             }
             row_sum(s, sums[id], id, turn);
-            const float by_unit = s[0] * p.per_d, plain = p.pre.kind == RA_NORM_LAYER ? s[1] * p.per_d : 0.0f;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                if (col[i] >= p.d) continue;
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    const float unit = (rx[i][j] - kept.z) * kept.w;
-                    full[i][j] = fmaf(kept.w, v[i][j] - plain - unit * by_unit, full[i][j]);
+            by_unit = s[0] * p.per_d;
+            plain = p.pre.kind == RA_NORM_LAYER ? s[1] * p.per_d : 0.0f;
+        }
+        if constexpr (WIDE) {
+            d.zero();
+            if (count > 0) {
+                if (has_new) d.take(at, kPitch);
+                if constexpr (JOIN) {
+                    f.take(at + places<TX>() * kPitch, kPitch);
+                    if (by_matrix) g.take(at + (places<TX>() + places<TF>()) * kPitch, kPitch);
                 }
+            } else if constexpr (JOIN) {
+                f.zero();
             }
         }
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j)
+            full[j] = has_pre ? fmaf(kept.w, full[j] - plain - (x[j] - kept.z) * kept.w * by_unit, d[j]) : d[j];
         if (p.dx != nullptr) {
+            float y[kOwn];
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                if (col[i] >= p.d) continue;
-                float y[W];
-#pragma unroll
-                for (int j = 0; j < W; ++j) y[j] = JOIN ? p.alpha * full[i][j] : full[i][j];
-                store_w<TX, W>(static_cast<TX *>(p.dx) + r * p.ld_dx + col[i], y);
-            }
+            for (int j = 0; j < kOwn; ++j) y[j] = JOIN ? p.alpha * full[j] : full[j];
+            store_own<TX, WIDE>(static_cast<TX *>(p.dx) + r * p.ld_dx, col, count, y);
         }
         if constexpr (JOIN) {
-            float s[2] = {0.0f, 0.0f};
-            const bool normed = p.post.kind != RA_NORM_NONE;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                if (col[i] >= p.d) continue;
-                float gain[W], bias[W], gate[W];
-                load_param<W>(normed ? p.post.gain : nullptr, p.post.f32, p.post.gain_wide, col[i], 1.0f, gain);
-                load_param<W>(normed ? p.post.bias : nullptr, p.post.f32, p.post.bias_wide, col[i], 0.0f, bias);
-                load_param<W>(p.gate_kind == RA_GATE_VECTOR ? p.gate : nullptr, p.gate_f32, p.gate_wide, col[i], 1.0f, gate);
-                float dg[W];
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    const float unit = normed ? (rf[i][j] - kept.x) * kept.y : rf[i][j];
-                    const float u = p.beta * full[i][j];
-                    dg[j] = u * fmaf(unit, gain[j], bias[j]);
-                    acc[kGate][i][j] += dg[j];
-                    const float v = u * (p.gate_kind == RA_GATE_MATRIX ? rg[i][j] : gate[j]);
-                    acc[kPostGain][i][j] = fmaf(v, unit, acc[kPostGain][i][j]);
-                    acc[kPostBias][i][j] += v;
-                    full[i][j] = v * gain[j];
-                    s[0] = fmaf(full[i][j], unit, s[0]);
-                    s[1] += full[i][j];
-                }
-                if (p.dgate != nullptr) store_w<TF, W>(static_cast<TF *>(p.dgate) + r * p.ld_dgate + col[i], dg);
-            }
+            float s[2] = {0.0f, 0.0f}, gain[kOwn], bias[kOwn], gate[kOwn], dg[kOwn];
             if (normed) {
+                load_gain(p.post, col, count, gain);
+            } else {
+                kept.x = 0.0f;
+                kept.y = 1.0f;
+#pragma unroll
+                for (int j = 0; j < kOwn; ++j) gain[j] = 1.0f;
+            }
+            load_vector<WIDE>(normed ? p.post.bias : nullptr, p.post.f32, col, count, 0.0f, bias);
+            load_vector<WIDE>(p.gate_kind == RA_GATE_VECTOR ? p.gate : nullptr, p.gate_f32, col, count, 1.0f, gate);
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) {
+                if (!WIDE && j >= count) full[j] = 0.0f;
+                const float unit = (f[j] - kept.x) * kept.y, u = p.beta * full[j];
+                dg[j] = u * fmaf(unit, gain[j], bias[j]);
+                acc[kGate][j] += dg[j];
+                const float v = u * (by_matrix ? g[j] : gate[j]);
+                acc[kPostGain][j] = fmaf(v, unit, acc[kPostGain][j]);
+                acc[kPostBias][j] += v;
+                full[j] = v * gain[j];
+                s[0] = fmaf(full[j], unit, s[0]);
+                s[1] += full[j];
+            }
+            if (p.dgate != nullptr) store_own<TF, WIDE>(static_cast<TF *>(p.dgate) + r * p.ld_dgate, col, count, dg);
+            if (normed) {
+                if (WIDE && count == 0) s[0] = s[1] = 0.0f;
                 row_sum(s, sums[id], id, turn);
-                const float by_unit = s[0] * p.per_d, plain = p.post.kind == RA_NORM_LAYER ? s[1] * p.per_d : 0.0f;
+                by_unit = s[0] * p.per_d;
+                plain = p.post.kind == RA_NORM_LAYER ? s[1] * p.per_d : 0.0f;
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-#pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        const float unit = (rf[i][j] - kept.x) * kept.y;
-                        full[i][j] = kept.y * (full[i][j] - plain - unit * by_unit);
-                    }
+                for (int j = 0; j < kOwn; ++j) full[j] = kept.y * (full[j] - plain - (f[j] - kept.x) * kept.y * by_unit);
             }
-            if (p.df != nullptr) {
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (col[i] < p.d) store_w<TF, W>(static_cast<TF *>(p.df) + r * p.ld_df + col[i], full[i]);
-            }
+            if (p.df != nullptr) store_own<TF, WIDE>(static_cast<TF *>(p.df) + r * p.ld_df, col, count, full);
         }
     }
 
     if (p.parts == nullptr) return;
+    float *const part = p.parts + (int64_t)block * kSums * p.d;
 #pragma unroll
     for (int a = 0; a < kSums; ++a) {
         if constexpr (kGroups > 1) {  // the groups' sums in their order
-            for (int g = 0; g < kGroups; ++g) {
+            for (int k = 0; k < kGroups; ++k) {
                 __syncthreads();
-                if (id != g) continue;
+                if (id != k) continue;
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-#pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        float &at = joined[col[i] + j];
-                        at = g == 0 ? acc[a][i][j] : at + acc[a][i][j];
-                    }
+                for (int j = 0; j < kOwn; ++j) {
+                    float &to = joined[col[j]];
+                    to = k == 0 ? acc[a][j] : to + acc[a][j];
+                }
             }
             __syncthreads();
-            for (int64_t c = threadIdx.x; c < p.d; c += kNormThreads) p.parts[(block * kSums + a) * p.d + c] = joined[c];
+            for (int c = threadIdx.x; c < p.d; c += kThreads) part[(int64_t)a * p.d + c] = joined[c];
+        } else if constexpr (WIDE) {
+            if (count > 0) store_w<float, kOwn>(part + (int64_t)a * p.d + col.first, acc[a]);
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-#pragma unroll
-                for (int j = 0; j < W; ++j)
-                    if (col[i] < p.d) p.parts[(block * kSums + a) * p.d + col[i] + j] = acc[a][i][j];
+            for (int j = 0; j < kOwn; ++j)
+                if (j < count) part[(int64_t)a * p.d + col[j]] = acc[a][j];
         }
     }
 }
@@ -211,37 +268,23 @@ __global__ void __launch_bounds__(256) parts_kernel(const PartsParams p) {
 // ---------------------------------------------------------------------------
 // host
 
-// 8 values a thread, as their sums over the rows are held beside them
-Shape grad_shape(int64_t d) {
-    if (d <= 256) return {1, 1};
-    if (d <= 512) return {2, 1};
-    if (d <= 1024) return {4, 1};
-    if (d <= 2048) return {8, 1};
-    if (d <= 4096) return {16, 1};
-    return {16, d <= 8192 ? 2 : d <= 16384 ? 4 : 8};
-}
 // blocks (or clusters) that share the rows, each with a part of the sums
-int64_t grad_parts(int64_t rows, int64_t d) {
-    const Shape sh = grad_shape(d);
-    const int64_t most = 152 * (sh.warps == 16 ? 1 : 2) / sh.cluster, blocks = ceil_div<int64_t>(rows, sh.groups());
-    return blocks < most ? blocks : most;
-}
+int64_t grad_parts(int64_t rows, int64_t d) { return Shape(d).shares(rows, 2); }
 
 template <class TX, class TF, bool JOIN>
 cudaError_t launch_grad(const NormGradParams &p, bool wide, cudaStream_t s) {
-    const Shape sh = grad_shape(p.d);
-    auto go = [&](auto kernel, auto scalar) {
-        return launch_clusters(wide ? kernel : scalar, grad_parts(p.rows, p.d) * sh.cluster, sh.cluster, sh.threads(), 0, s, p);
-    };
-    switch (sh.warps) {
-        case 1: return go(norm_grad_kernel<TX, TF, 8, 1, 1, JOIN, false>, norm_grad_kernel<TX, TF, 1, 8, 1, JOIN, false>);
-        case 2: return go(norm_grad_kernel<TX, TF, 8, 1, 2, JOIN, false>, norm_grad_kernel<TX, TF, 1, 8, 2, JOIN, false>);
-        case 4: return go(norm_grad_kernel<TX, TF, 8, 1, 4, JOIN, false>, norm_grad_kernel<TX, TF, 1, 8, 4, JOIN, false>);
-        case 8: return go(norm_grad_kernel<TX, TF, 8, 1, 8, JOIN, false>, norm_grad_kernel<TX, TF, 1, 8, 8, JOIN, false>);
-        default: break;
-    }
-    if (sh.cluster == 1) return go(norm_grad_kernel<TX, TF, 8, 1, 16, JOIN, false>, norm_grad_kernel<TX, TF, 1, 8, 16, JOIN, false>);
-    return go(norm_grad_kernel<TX, TF, 8, 1, 16, JOIN, true>, norm_grad_kernel<TX, TF, 1, 8, 16, JOIN, true>);
+    const Shape sh(p.d);
+    return with_shape(sh, [&](auto warps, auto cluster) {
+        constexpr int kWarps = decltype(warps)::value;
+        constexpr bool kCluster = decltype(cluster)::value != 0;
+        const int64_t grid = grad_parts(p.rows, p.d) * sh.cluster;
+        if (!wide) return launch_clusters(norm_grad_kernel<TX, TF, false, kWarps, JOIN, kCluster>, grid, sh.cluster, sh.threads(), 0, s, p);
+        const int place = grad_stages<TX, TF>() * 16 * sh.threads();
+        const cudaError_t e = opt_in_smem<norm_grad_kernel<TX, TF, true, kWarps, JOIN, kCluster>>(place * grad_places<TX, TF, JOIN>(JOIN));
+        if (e != cudaSuccess) return e;
+        return launch_clusters(norm_grad_kernel<TX, TF, true, kWarps, JOIN, kCluster>, grid, sh.cluster, sh.threads(),
+                               place * grad_places<TX, TF, JOIN>(p.gate_kind == RA_GATE_MATRIX), s, p);
+    });
 }
 
 template <bool JOIN>
@@ -310,8 +353,8 @@ ra_status ra_norm_block_grad(const ra_norm_block_grad_args *args, void *stream) 
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (!none) {
         const NormGradParams p{a.dh, a.dx_new, a.x, a.f, a.gate, pre || post ? a.kept : nullptr, a.dx, a.df, by_matrix ? a.dgate : nullptr,
-                               sums ? static_cast<float *>(a.ws) : nullptr, a.ld_dh, a.ld_dx_new, a.ld_x, a.ld_f, a.ld_gate, a.ld_dx, a.ld_df, a.ld_dgate, a.rows, a.d,
-                               behind, ahead, gate, by_vector && a.gate_dtype == RA_F32, wide_at(a.gate), a.alpha, a.beta, 1.0f / (float)a.d};
+                               sums ? static_cast<float *>(a.ws) : nullptr, a.ld_dh, a.ld_dx_new, a.ld_x, a.ld_f, a.ld_gate, a.ld_dx, a.ld_df, a.ld_dgate, a.rows, (int)a.d,
+                               gate, behind, ahead, by_vector && a.gate_dtype == RA_F32, a.alpha, a.beta, 1.0f / (float)a.d};
         const bool wide = all_wide(rows, a.d);
         const cudaError_t e = join ? launch_grad<true>(p, a.x_dtype, a.f_dtype, wide, s) : launch_grad<false>(p, a.x_dtype, a.f_dtype, wide, s);
         if (e != cudaSuccess) return cuda_status(e);
