@@ -245,18 +245,6 @@ constexpr int log_smem() {
     return kLogThreads * kSlots * 16 + (TOP ? kLogThreads * kSlots / batch_of<WARPS>() * 4 : 0) + kLogThreads / (WARPS * 32) * (int)sizeof(RowRoom<WARPS, TOP, CLUSTER>);
 }
 
-// a * b + c and a + b on pairs, the result in registers of its own
-__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 template <class T, int WARPS, bool TOP, bool CLUSTER>
 __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprobs_kernel(const LogParams p) {
     using Room = RowRoom<WARPS, TOP, CLUSTER>;

@@ -17,55 +17,91 @@ struct NormParams {
     float alpha, beta, per_d;  // per_d: 1 / d
 };
 
-constexpr int kNormStages = 3, kNormBlocks = 3;  // rows under way a group, blocks an SM
+constexpr int kOwn = 16;  // columns a thread has, in every row
 
+// rows under way a group: as many as shared memory has room for in the widest blocks
+template <class TX, class TF, bool JOIN>
+constexpr int norm_stages() {
+    return JOIN && sizeof(TF) == 4 ? 2 : 3;
+}
 // 16-byte places a thread needs for a row
 template <class TX, class TF, bool JOIN>
-int norm_places(bool gate_matrix) {
-    return places<TX>() + (JOIN ? places<TF>() * (gate_matrix ? 2 : 1) : 0);
+__host__ __device__ constexpr int norm_places(bool gate_matrix) {
+    return places<TX, kOwn>() + (JOIN ? places<TF, kOwn>() * (gate_matrix ? 2 : 1) : 0);
 }
 
 template <class TX, class TF, bool WIDE, int WARPS, bool JOIN, bool CLUSTER>
-__global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 ? 1 : kNormBlocks) norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 ? 1 : 2) norm_kernel(const NormParams p) {
     constexpr int kThreads = WARPS == 16 ? 512 : kNormThreads, kGroups = kThreads / (WARPS * 32);  // kGroups: rows at a time
-    constexpr int kPitch = kThreads * 16, kAhead = kNormStages - 1;
+    constexpr int kPitch = kThreads * 16, kAhead = norm_stages<TX, TF, JOIN>() - 1, kPairs = kOwn / 2;
+    using C = Columns<kOwn, WIDE, WARPS, CLUSTER>;
     __shared__ RowSums<2, WARPS, CLUSTER> sums[kGroups];
     extern __shared__ __align__(16) unsigned char ring[];
     pdl_enter();
     if constexpr (CLUSTER) cluster_meet();  // every block is there before another writes to it
     const int id = threadIdx.x / (WARPS * 32);
-    const Columns<WIDE, WARPS, CLUSTER> col;
+    const C col;
     const int count = col.count(p.d);
     int turn = 0;
     const bool by_matrix = JOIN && p.gate_kind == RA_GATE_MATRIX;
 
+    const int blocks = CLUSTER ? gridDim.x / cluster_blocks() : gridDim.x, block = CLUSTER ? blockIdx.x / cluster_blocks() : blockIdx.x;
+    const int64_t first = (int64_t)block * kGroups + id, step = (int64_t)blocks * kGroups;
+    const int stage_bytes = norm_places<TX, TF, JOIN>(by_matrix) * kPitch;
+    const uint32_t mine = smem_addr(ring) + threadIdx.x * 16;
+    auto fetch = [&](int64_t r, int stage) {
+        if (r < p.rows) {
+            const uint32_t to = mine + stage * stage_bytes;
+            if constexpr (JOIN) {
+                copy_own(to, kPitch, static_cast<const TF *>(p.f) + r * p.ld_f, col, count);
+                if (by_matrix) copy_own(to + places<TF, kOwn>() * kPitch, kPitch, static_cast<const TF *>(p.gate) + r * p.ld_gate, col, count);
+            }
+            copy_own(to + stage_bytes - places<TX, kOwn>() * kPitch, kPitch, static_cast<const TX *>(p.x) + r * p.ld_x, col, count);
+        }
+        copies_done();
+    };
+    int stage = 0;
+    if constexpr (WIDE) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) fetch(first + k * step, k);
+    }
+
     // post as (v - m) rstd a + b with the gate and beta in a and b, unless the gate
     // has a value of its own for each v
-    float a_post[JOIN ? kOwn : 1], b_post[JOIN ? kOwn : 1], a_pre[kOwn], b_pre[kOwn];
-    if constexpr (JOIN) {
-        float g[kOwn];
-        load_param(p.post.gain, p.post.f32, col, count, 1.0f, a_post);
-        load_param(p.post.bias, p.post.f32, col, count, 0.0f, b_post);
-        load_param(p.gate_kind == RA_GATE_VECTOR ? p.gate : nullptr, p.gate_f32, col, count, 1.0f, g);
+    Pair a_post[JOIN ? kPairs : 1], b_post[JOIN ? kPairs : 1], a_pre[kPairs], b_pre[kPairs];
+    {
+        float a[kOwn], b[kOwn];
+        if constexpr (JOIN) {
+            float g[kOwn];
+            load_param(p.post.gain, p.post.f32, col, count, 1.0f, a);
+            load_param(p.post.bias, p.post.f32, col, count, 0.0f, b);
+            load_param(p.gate_kind == RA_GATE_VECTOR ? p.gate : nullptr, p.gate_f32, col, count, 1.0f, g);
 #pragma unroll
-        for (int j = 0; j < kOwn; ++j) {
-            a_post[j] *= p.beta * g[j];
-            b_post[j] *= p.beta * g[j];
+            for (int j = 0; j < kPairs; ++j) {
+                a_post[j] = pair(a[2 * j] * (p.beta * g[2 * j]), a[2 * j + 1] * (p.beta * g[2 * j + 1]));
+                b_post[j] = pair(b[2 * j] * (p.beta * g[2 * j]), b[2 * j + 1] * (p.beta * g[2 * j + 1]));
+            }
+        }
+        load_param(p.pre.gain, p.pre.f32, col, count, 1.0f, a);
+        load_param(p.pre.bias, p.pre.f32, col, count, 0.0f, b);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            a_pre[j] = pair(a[2 * j], a[2 * j + 1]);
+            b_pre[j] = pair(b[2 * j], b[2 * j + 1]);
         }
     }
-    load_param(p.pre.gain, p.pre.f32, col, count, 1.0f, a_pre);
-    load_param(p.pre.bias, p.pre.f32, col, count, 0.0f, b_pre);
 
     // m and rstd of a row.  The sums of the values and of their squares are made at
     // once; where the mean is so large that their difference loses more than 4
     // bits, the squares of the differences from it are summed after it.
-    auto moments = [&](const float (&v)[kOwn], const Side &side, float *m, float *rstd) {
-        float s[2] = {0.0f, 0.0f};
+    auto moments = [&](const Pair (&v)[kPairs], const Side &side, float *m, float *rstd) {
+        Pair sum = both(0.0f), squares = both(0.0f);
 #pragma unroll
-        for (int j = 0; j < kOwn; ++j) {  // columns past the row's end hold 0
-            s[0] += v[j];
-            s[1] = fmaf(v[j], v[j], s[1]);
+        for (int j = 0; j < kPairs; ++j) {  // columns past the row's end hold 0
+            sum = pair_add(sum, v[j]);
+            squares = pair_fma(v[j], v[j], squares);
         }
+        float s[2] = {pair_sum(sum), pair_sum(squares)};
         row_sum(s, sums[id], id, turn);
         *m = 0.0f;
         float var = s[1] * p.per_d;
@@ -76,7 +112,9 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
                 s[0] = s[1] = 0.0f;
 #pragma unroll
                 for (int j = 0; j < kOwn; ++j) {
-                    const float c = v[j] - *m;
+                    float a, b;
+                    apart(v[j / 2], a, b);
+                    const float c = (j & 1 ? b : a) - *m;
                     if (j < count) s[0] = fmaf(c, c, s[0]);
                 }
                 row_sum(s, sums[id], id, turn);
@@ -88,42 +126,14 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
         *rstd = rsqrtf(var + side.eps);
     };
 
-    const int blocks = CLUSTER ? gridDim.x / cluster_blocks() : gridDim.x, block = CLUSTER ? blockIdx.x / cluster_blocks() : blockIdx.x;
-    const int64_t first = (int64_t)block * kGroups + id, step = (int64_t)blocks * kGroups;
-    const int stage_bytes = (places<TX>() + (JOIN ? places<TF>() * (by_matrix ? 2 : 1) : 0)) * kPitch;
-    const uint32_t mine = smem_addr(ring) + threadIdx.x * 16;
-    auto fetch = [&](int64_t r, int stage) {
-        if (r < p.rows && count > 0) {
-            uint32_t to = mine + stage * stage_bytes;
-            to = copy_own(to, kPitch, static_cast<const TX *>(p.x) + r * p.ld_x + col.first);
-            if constexpr (JOIN) {
-                to = copy_own(to, kPitch, static_cast<const TF *>(p.f) + r * p.ld_f + col.first);
-                if (by_matrix) copy_own(to, kPitch, static_cast<const TF *>(p.gate) + r * p.ld_gate + col.first);
-            }
-        }
-        copies_done();
-    };
-    int stage = 0;
-    if constexpr (WIDE) {
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) fetch(first + k * step, k);
-    }
     for (int64_t r = first; r < p.rows; r += step) {
-        Own<TX, WIDE> x;
-        Own<TF, WIDE> f, g;
+        Own<TX, C> x;
+        Own<TF, C> f, g;
+        const uint32_t at = mine + stage * stage_bytes;
         if constexpr (WIDE) {
             fetch(r + kAhead * step, stage == 0 ? kAhead : stage - 1);
             await_copies<kAhead>();
-            x.zero();
-            if constexpr (JOIN) f.zero();
-            if (count > 0) {
-                const uint32_t at = mine + stage * stage_bytes;
-                x.take(at, kPitch);
-                if constexpr (JOIN) {
-                    f.take(at + places<TX>() * kPitch, kPitch);
-                    if (by_matrix) g.take(at + (places<TX>() + places<TF>()) * kPitch, kPitch);
-                }
-            }
+            if constexpr (JOIN) f.take(at, kPitch, count);
             stage = stage == kAhead ? 0 : stage + 1;
         } else {
             x.load(static_cast<const TX *>(p.x) + r * p.ld_x, col, count);
@@ -132,31 +142,43 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
                 if (by_matrix) g.load(static_cast<const TF *>(p.gate) + r * p.ld_gate, col, count);
             }
         }
-        float v[kOwn], m_f = 0.0f, rstd_f = 0.0f, m_x = 0.0f, rstd_x = 0.0f;
+        Pair v[kPairs];
+        float m_f = 0.0f, rstd_f = 0.0f, m_x = 0.0f, rstd_x = 0.0f;
         if constexpr (JOIN) {
 #pragma unroll
-            for (int j = 0; j < kOwn; ++j) v[j] = f[j];
+            for (int j = 0; j < kPairs; ++j) v[j] = f.two(j);
             const bool normed = p.post.kind != RA_NORM_NONE;
             if (normed) moments(v, p.post, &m_f, &rstd_f);
-            const float scale = normed ? rstd_f : 1.0f;
-#pragma unroll
-            for (int j = 0; j < kOwn; ++j) {
-                v[j] = fmaf(v[j] - m_f, scale * a_post[j], b_post[j]);
-                if (by_matrix) v[j] *= g[j];
-                v[j] = fmaf(p.alpha, x[j], v[j]);
+            if constexpr (WIDE) {
+                if (by_matrix) g.take(at + places<TF, kOwn>() * kPitch, kPitch, count);
+                x.take(at + stage_bytes - places<TX, kOwn>() * kPitch, kPitch, count);
             }
-            store_own<TX, WIDE>(static_cast<TX *>(p.x_out) + r * p.ld_x_out, col, count, v);
+            const Pair scale = both(normed ? rstd_f : 1.0f), off = both(-m_f), alpha = both(p.alpha);
 #pragma unroll
-            for (int j = 0; j < kOwn; ++j) v[j] = j < count ? to_f32<TX>(from_f32<TX>(v[j])) : 0.0f;  // the norm is that of the row as stored
+            for (int j = 0; j < kPairs; ++j) {
+                v[j] = pair_fma(pair_add(v[j], off), pair_mul(scale, a_post[j]), b_post[j]);
+                if (by_matrix) v[j] = pair_mul(v[j], g.two(j));
+                v[j] = pair_fma(alpha, x.two(j), v[j]);
+            }
+            x.set(v);
+            x.store(static_cast<TX *>(p.x_out) + r * p.ld_x_out, col, count);
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {  // the norm is that of the row as stored
+                v[j] = x.two(j);
+                if (!WIDE || kOwn > 8) v[j] = pair(2 * j < count ? x[2 * j] : 0.0f, 2 * j + 1 < count ? x[2 * j + 1] : 0.0f);
+            }
         } else {
+            if constexpr (WIDE) x.take(at, kPitch, count);
 #pragma unroll
-            for (int j = 0; j < kOwn; ++j) v[j] = x[j];
+            for (int j = 0; j < kPairs; ++j) v[j] = x.two(j);
         }
         if (p.pre.kind != RA_NORM_NONE) {
             moments(v, p.pre, &m_x, &rstd_x);
+            const Pair scale = both(rstd_x), off = both(-m_x);
 #pragma unroll
-            for (int j = 0; j < kOwn; ++j) v[j] = fmaf(v[j] - m_x, rstd_x * a_pre[j], b_pre[j]);
-            store_own<TF, WIDE>(static_cast<TF *>(p.h) + r * p.ld_h, col, count, v);
+            for (int j = 0; j < kPairs; ++j) v[j] = pair_fma(pair_add(v[j], off), pair_mul(scale, a_pre[j]), b_pre[j]);
+            f.set(v);
+            f.store(static_cast<TF *>(p.h) + r * p.ld_h, col, count);
         }
         if (p.kept != nullptr && col.first == 0) reinterpret_cast<float4 *>(p.kept)[r] = make_float4(m_f, rstd_f, m_x, rstd_x);
     }
@@ -164,17 +186,17 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
 
 template <class TX, class TF, bool JOIN>
 cudaError_t launch_norm(const NormParams &p, bool wide, cudaStream_t s) {
-    const Shape sh(p.d);
+    const Shape sh(p.d, kOwn);
     return with_shape(sh, [&](auto warps, auto cluster) {
         constexpr int kWarps = decltype(warps)::value;
         constexpr bool kCluster = decltype(cluster)::value != 0;
-        const int64_t grid = sh.shares(p.rows, kNormBlocks) * sh.cluster;
+        const int64_t grid = sh.shares(p.rows) * sh.cluster;
         if (!wide) return launch_clusters(norm_kernel<TX, TF, false, kWarps, JOIN, kCluster>, grid, sh.cluster, sh.threads(), 0, s, p);
-        constexpr int kMost = kNormStages * (places<TX>() + (JOIN ? 2 * places<TF>() : 0)) * 16 * (kWarps == 16 ? 512 : kNormThreads);
-        const cudaError_t e = opt_in_smem<norm_kernel<TX, TF, true, kWarps, JOIN, kCluster>>(kMost);
+        const int place = norm_stages<TX, TF, JOIN>() * 16 * sh.threads();
+        const cudaError_t e = opt_in_smem<norm_kernel<TX, TF, true, kWarps, JOIN, kCluster>>(place * norm_places<TX, TF, JOIN>(JOIN));
         if (e != cudaSuccess) return e;
-        const int bytes = kNormStages * norm_places<TX, TF, JOIN>(p.gate_kind == RA_GATE_MATRIX) * 16 * sh.threads();
-        return launch_clusters(norm_kernel<TX, TF, true, kWarps, JOIN, kCluster>, grid, sh.cluster, sh.threads(), bytes, s, p);
+        return launch_clusters(norm_kernel<TX, TF, true, kWarps, JOIN, kCluster>, grid, sh.cluster, sh.threads(),
+                               place * norm_places<TX, TF, JOIN>(p.gate_kind == RA_GATE_MATRIX), s, p);
     });
 }
 

@@ -16,91 +16,112 @@ struct Side {
     bool f32;
 };
 
-constexpr int kOwn = 8;  // columns a thread has, in every row
-
-// The columns of a thread: 8 neighbours (WIDE: rows on 16-byte boundaries, d a
-// multiple of 8), or 8 that are the row's threads apart.
-template <bool WIDE, int WARPS, bool CLUSTER>
+// The columns of a thread, OWN of them: 8 neighbours at a time (WIDE: rows on
+// 16-byte boundaries, d a multiple of 8), or single ones that are the row's threads
+// apart.
+template <int OWN, bool WIDE, int WARPS, bool CLUSTER>
 struct Columns {
-    static constexpr int kThreads = WARPS * 32;
+    static constexpr int kThreads = WARPS * 32, kOwn = OWN, kEach = WIDE ? 8 : 1, kParts = OWN / kEach;
     int first;
     __device__ __forceinline__ Columns()
-        : first((CLUSTER ? (int)cluster_block() * kThreads * kOwn : 0) + (int)threadIdx.x % kThreads * (WIDE ? kOwn : 1)) {}
-    __device__ __forceinline__ int operator[](int j) const { return first + j * (WIDE ? 1 : kThreads); }
+        : first((CLUSTER ? (int)cluster_block() * kThreads * OWN : 0) + (int)threadIdx.x % kThreads * kEach) {}
+    __device__ __forceinline__ int operator[](int j) const { return first + j / kEach * (kEach * kThreads) + j % kEach; }
     // how many of them are within a row of d
-    __device__ __forceinline__ int count(int d) const {
-        return WIDE ? (first < d ? kOwn : 0) : max(0, min(kOwn, ceil_div(d - first, kThreads)));
-    }
+    __device__ __forceinline__ int count(int d) const { return max(0, min(kParts, ceil_div(d - first, kEach * kThreads))) * kEach; }
 };
 
 // a thread's values of a vector of parameters, `none` where there is no vector
 template <class C>
-__device__ __forceinline__ void load_param(const void *v, bool f32, const C &col, int count, float none, float (&out)[kOwn]) {
+__device__ __forceinline__ void load_param(const void *v, bool f32, const C &col, int count, float none, float (&out)[C::kOwn]) {
 #pragma unroll
-    for (int j = 0; j < kOwn; ++j) {
+    for (int j = 0; j < C::kOwn; ++j) {
         out[j] = none;
         if (v != nullptr && j < count) out[j] = f32 ? static_cast<const float *>(v)[col[j]] : to_f32<uint16_t>(static_cast<const uint16_t *>(v)[col[j]]);
     }
 }
 
 // A thread's values of one row of a matrix as they lie in memory.
-template <class T, bool WIDE>
+template <class T, class C>
 struct Own {
-    Raw<T, WIDE ? kOwn : 1> v[WIDE ? 1 : kOwn];
-    __device__ __forceinline__ float operator[](int j) const {
-        if constexpr (WIDE)
-            return v[0][j];
-        else
-            return v[j][0];
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int j = 0; j < (WIDE ? 1 : kOwn); ++j) v[j].zero();
-    }
-    template <class C>
+    Raw<T, C::kEach> v[C::kParts];
+    __device__ __forceinline__ float operator[](int j) const { return v[j / C::kEach][j % C::kEach]; }
+    __device__ __forceinline__ Pair two(int j) const { return pair((*this)[2 * j], (*this)[2 * j + 1]); }
+    // values past the row's end are 0
     __device__ __forceinline__ void load(const T *row, const C &col, int count) {
-        zero();
-        if constexpr (WIDE) {
-            if (count > 0) v[0].load(row + col.first);
-        } else {
 #pragma unroll
-            for (int j = 0; j < kOwn; ++j)
-                if (j < count) v[j].load(row + col[j]);
+        for (int i = 0; i < C::kParts; ++i) {
+            v[i].zero();
+            if (i * C::kEach < count) v[i].load(row + col[i * C::kEach]);
         }
     }
-    // from the thread's own place in shared memory
-    __device__ __forceinline__ void take(uint32_t shared, int pitch) {
-        static_assert(WIDE, "take");
+    // from the thread's own places in shared memory
+    __device__ __forceinline__ void take(uint32_t shared, int pitch, int count) {
+        static_assert(C::kEach == 8, "take");
 #pragma unroll
-        for (int k = 0; k < (int)sizeof(T) / 2; ++k)
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v[0].w[4 * k]), "=r"(v[0].w[4 * k + 1]), "=r"(v[0].w[4 * k + 2]), "=r"(v[0].w[4 * k + 3]) : "r"(shared + k * pitch) : "memory");
+        for (int i = 0; i < C::kParts; ++i) {
+            v[i].zero();
+            if (i * 8 < count) {
+#pragma unroll
+                for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v[i].w[4 * k]), "=r"(v[i].w[4 * k + 1]), "=r"(v[i].w[4 * k + 2]), "=r"(v[i].w[4 * k + 3])
+                                 : "r"(shared + (i * ((int)sizeof(T) / 2) + k) * pitch) : "memory");
+            }
+        }
+    }
+    // the values rounded to T
+    __device__ __forceinline__ void set(const Pair (&p)[C::kOwn / 2]) {
+#pragma unroll
+        for (int j = 0; j < C::kOwn; j += 2) {
+            float a, b;
+            apart(p[j / 2], a, b);
+            if constexpr (sizeof(T) == 4) {
+                v[j / C::kEach].w[j % C::kEach] = __float_as_uint(a);
+                v[(j + 1) / C::kEach].w[(j + 1) % C::kEach] = __float_as_uint(b);
+            } else if constexpr (C::kEach == 8) {
+                v[j / 8].w[j % 8 / 2] = pack2(a, b);
+            } else {
+                const uint32_t w = pack2(a, b);
+                v[j].w[0] = w & 0xffffu;
+                v[j + 1].w[0] = w >> 16;
+            }
+        }
+    }
+    __device__ __forceinline__ void store(T *row, const C &col, int count) const {
+#pragma unroll
+        for (int i = 0; i < C::kParts; ++i) {
+            if (i * C::kEach >= count) continue;
+            T *to = row + col[i * C::kEach];
+            if constexpr (C::kEach == 8) {
+#pragma unroll
+                for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+                    reinterpret_cast<uint4 *>(to)[k] = make_uint4(v[i].w[4 * k], v[i].w[4 * k + 1], v[i].w[4 * k + 2], v[i].w[4 * k + 3]);
+            } else if constexpr (sizeof(T) == 4) {
+                *to = __uint_as_float(v[i].w[0]);
+            } else {
+                *to = (T)v[i].w[0];
+            }
+        }
     }
 };
-template <class T, bool WIDE, class C>
-__device__ __forceinline__ void store_own(T *row, const C &col, int count, const float (&v)[kOwn]) {
-    if constexpr (WIDE) {
-        if (count > 0) store_w<T, kOwn>(row + col.first, v);
-    } else {
-#pragma unroll
-        for (int j = 0; j < kOwn; ++j)
-            if (j < count) row[col[j]] = from_f32<T>(v[j]);
-    }
-}
 
 // Rows read ahead (WIDE): every thread copies its own values of the next rows
 // asynchronously to places of its own in shared memory, 16 bytes each, kThreads
 // places apart, and reads them from there: nobody waits for another's copies.
-template <class T>
-constexpr int places() {  // of 8 values
-    return sizeof(T) / 2;
+template <class T, int OWN>
+__host__ __device__ constexpr int places() {  // of a thread's values of a row
+    return OWN / 8 * (int)sizeof(T) / 2;
 }
-template <class T>
-__device__ __forceinline__ uint32_t copy_own(uint32_t to, int pitch, const T *from) {
+// one vector of 8 values after another; returns the place behind them
+template <class T, class C>
+__device__ __forceinline__ void copy_own(uint32_t to, int pitch, const T *row, const C &col, int count) {
 #pragma unroll
-    for (int k = 0; k < places<T>(); ++k)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + k * pitch), "l"(from + k * (16 / (int)sizeof(T))) : "memory");
-    return to + places<T>() * pitch;
+    for (int i = 0; i < C::kParts; ++i)
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+            if (i * 8 < count)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (i * ((int)sizeof(T) / 2) + k) * pitch), "l"(row + col[i * 8] + k * (16 / (int)sizeof(T)))
+                             : "memory");
 }
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT>
@@ -135,17 +156,20 @@ bool all_wide(const Mat (&m)[K], int64_t d) {
     return true;
 }
 
-// How a row of d is shared: 8 columns a thread, up to 512 threads a block (blocks of
-// 256 where a row takes fewer, several rows at a time), beyond that the blocks of a
-// cluster.
+// How a row of d is shared: `own` columns a thread, up to 512 threads a block (blocks
+// of 256 where a row takes fewer, several rows at a time), beyond that the blocks of
+// a cluster.
 struct Shape {
     int warps, cluster;
-    explicit Shape(int64_t d) : warps(d <= 256 ? 1 : d <= 512 ? 2 : d <= 1024 ? 4 : d <= 2048 ? 8 : 16), cluster(d <= 4096 ? 1 : d <= 8192 ? 2 : d <= 16384 ? 4 : 8) {}
+    Shape(int64_t d, int own) : warps(1), cluster(1) {
+        while (warps < 16 && warps * 32 * own < d) warps *= 2;
+        while (cluster < kMostBlocks && (int64_t)cluster * 512 * own < d) cluster *= 2;
+    }
     int64_t groups() const { return warps * 32 < kNormThreads ? kNormThreads / (warps * 32) : 1; }
     int threads() const { return warps * 32 < kNormThreads ? kNormThreads : warps * 32; }
-    // blocks, or clusters, that share the rows; at most `each` blocks an SM
-    int64_t shares(int64_t rows, int each) const {
-        const int64_t most = 152 * (warps == 16 && each > 1 ? each / 2 : each) / cluster, blocks = ceil_div<int64_t>(rows, groups());
+    // blocks, or clusters, that share the rows: two blocks of 256 an SM, or one of 512
+    int64_t shares(int64_t rows) const {
+        const int64_t most = 152 * (warps == 16 ? 1 : 2) / cluster, blocks = ceil_div<int64_t>(rows, groups());
         return blocks < most ? blocks : most;
     }
 };

@@ -6,13 +6,18 @@ namespace ra {
 namespace op {
 namespace {
 
-enum { kPreGain, kPreBias, kPostGain, kPostBias, kGate, kVectors };
+constexpr int kOwn = 8;  // columns a thread has, in every row: their sums stay in its registers
 
-// A thread's values of a vector of parameters, read anew for each row (from L1): in
-// registers they would leave no room for the sums.
-template <bool WIDE, class C>
+// What is summed over the rows, with v and w the normed x' and f and D the whole
+// gradient of x': dh v, dh, and D w, D (with a matrix's gate: D gate w, D gate).  The
+// gradients of post's gain and bias, and of a vector's gate, follow from the last
+// two, as the gate and beta are the same for all rows of a column.
+enum { kDhUnit, kDh, kDUnit, kD, kSumsMost };
+
+// A thread's values of a vector of parameters.
+template <class C>
 __device__ __forceinline__ void load_vector(const void *v, bool f32, const C &col, int count, float none, float (&out)[kOwn]) {
-    if (v != nullptr && count > 0 && WIDE && reinterpret_cast<uintptr_t>(v) % 16 == 0) {
+    if (v != nullptr && count > 0 && C::kEach == 8 && reinterpret_cast<uintptr_t>(v) % 16 == 0) {
         if (f32)
             load_w<float, kOwn>(static_cast<const float *>(v) + col.first, out);
         else
@@ -21,16 +26,12 @@ __device__ __forceinline__ void load_vector(const void *v, bool f32, const C &co
         load_param(v, f32, col, count, none, out);
     }
 }
-template <bool WIDE, int WARPS, bool CLUSTER>
-__device__ __forceinline__ void load_gain(const Side &side, const Columns<WIDE, WARPS, CLUSTER> &col, int count, float (&out)[kOwn]) {
-    load_vector<WIDE>(side.gain, side.f32, col, count, 1.0f, out);
-}
 
 struct NormGradParams {
     const void *dh, *dx_new, *x, *f, *gate;
     const float *kept;
     void *dx, *df, *dgate;  // dgate: a matrix's
-    float *parts;           // shares x (kVectors or 2) x d, or null
+    float *parts;           // shares x (kSumsMost or 2) x d, or null
     int64_t ld_dh, ld_dx_new, ld_x, ld_f, ld_gate, ld_dx, ld_df, ld_dgate, rows;
     int d, gate_kind;
     Side post, pre;
@@ -43,53 +44,48 @@ template <class TX, class TF>
 constexpr int grad_stages() {
     return sizeof(TF) == 4 ? 2 : 3;
 }
-// 16-byte places a thread needs for a row: dh, x, dx_new, f, the gate, kept
+// 16-byte places a thread needs for a row: kept, dh, x, dx_new, f, the gate
 template <class TX, class TF, bool JOIN>
 __host__ __device__ constexpr int grad_places(bool gate_matrix) {
-    return 1 + places<TF>() * ((JOIN ? 2 : 1) + (gate_matrix ? 1 : 0)) + 2 * places<TX>();
+    return 1 + places<TF, kOwn>() * ((JOIN ? 2 : 1) + (gate_matrix ? 1 : 0)) + 2 * places<TX, kOwn>();
 }
 
 template <class TX, class TF, bool WIDE, int WARPS, bool JOIN, bool CLUSTER>
 __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 ? 1 : 2) norm_grad_kernel(const NormGradParams p) {
-    constexpr int kThreads = WARPS == 16 ? 512 : kNormThreads, kGroups = kThreads / (WARPS * 32), kSums = JOIN ? kVectors : 2;
-    constexpr int kPitch = kThreads * 16, kAhead = grad_stages<TX, TF>() - 1;
+    constexpr int kThreads = WARPS == 16 ? 512 : kNormThreads, kGroups = kThreads / (WARPS * 32), kSums = JOIN ? kSumsMost : 2;
+    constexpr int kPitch = kThreads * 16, kAhead = grad_stages<TX, TF>() - 1, kPairs = kOwn / 2;
+    using C = Columns<kOwn, WIDE, WARPS, CLUSTER>;
     __shared__ RowSums<2, WARPS, CLUSTER> sums[kGroups];
     __shared__ float joined[kGroups > 1 ? WARPS * 32 * kOwn : 1];
     extern __shared__ __align__(16) unsigned char ring[];
     pdl_enter();
     if constexpr (CLUSTER) cluster_meet();
     const int id = threadIdx.x / (WARPS * 32);
-    const Columns<WIDE, WARPS, CLUSTER> col;
+    const C col;
     const int count = col.count(p.d);
     int turn = 0;
     const bool by_matrix = JOIN && p.gate_kind == RA_GATE_MATRIX, has_pre = p.dh != nullptr, has_new = p.dx_new != nullptr;
-    const bool normed = p.post.kind != RA_NORM_NONE;
-
-    float acc[kSums][kOwn];
-#pragma unroll
-    for (int a = 0; a < kSums; ++a)
-#pragma unroll
-        for (int j = 0; j < kOwn; ++j) acc[a][j] = 0.0f;
+    const bool normed = JOIN && p.post.kind != RA_NORM_NONE;
 
     const int blocks = CLUSTER ? gridDim.x / cluster_blocks() : gridDim.x, block = CLUSTER ? blockIdx.x / cluster_blocks() : blockIdx.x;
     const int64_t first = (int64_t)block * kGroups + id, step = (int64_t)blocks * kGroups;
+    // a stage: kept, dh, x, dx_new, f, the gate
+    constexpr int kAtDh = kPitch, kAtX = kAtDh + places<TF, kOwn>() * kPitch, kAtNew = kAtX + places<TX, kOwn>() * kPitch,
+                  kAtF = kAtNew + places<TX, kOwn>() * kPitch, kAtGate = kAtF + places<TF, kOwn>() * kPitch;
     const int stage_bytes = grad_places<TX, TF, JOIN>(by_matrix) * kPitch;
     const uint32_t mine = smem_addr(ring) + threadIdx.x * 16;
     auto fetch = [&](int64_t r, int stage) {
-        if (r < p.rows && count > 0) {
-            uint32_t to = mine + stage * stage_bytes;
-            if (p.kept != nullptr) copy_own(to, kPitch, reinterpret_cast<const uint16_t *>(p.kept + r * 4));
-            to += kPitch;
+        if (r < p.rows) {
+            const uint32_t to = mine + stage * stage_bytes;
+            if (p.kept != nullptr) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p.kept + r * 4) : "memory");
             if (has_pre) {
-                copy_own(to, kPitch, static_cast<const TF *>(p.dh) + r * p.ld_dh + col.first);
-                copy_own(to + places<TF>() * kPitch, kPitch, static_cast<const TX *>(p.x) + r * p.ld_x + col.first);
+                copy_own(to + kAtDh, kPitch, static_cast<const TF *>(p.dh) + r * p.ld_dh, col, count);
+                copy_own(to + kAtX, kPitch, static_cast<const TX *>(p.x) + r * p.ld_x, col, count);
             }
-            to += (places<TF>() + places<TX>()) * kPitch;
-            if (has_new) copy_own(to, kPitch, static_cast<const TX *>(p.dx_new) + r * p.ld_dx_new + col.first);
-            to += places<TX>() * kPitch;
+            if (has_new) copy_own(to + kAtNew, kPitch, static_cast<const TX *>(p.dx_new) + r * p.ld_dx_new, col, count);
             if constexpr (JOIN) {
-                to = copy_own(to, kPitch, static_cast<const TF *>(p.f) + r * p.ld_f + col.first);
-                if (by_matrix) copy_own(to, kPitch, static_cast<const TF *>(p.gate) + r * p.ld_gate + col.first);
+                copy_own(to + kAtF, kPitch, static_cast<const TF *>(p.f) + r * p.ld_f, col, count);
+                if (by_matrix) copy_own(to + kAtGate, kPitch, static_cast<const TF *>(p.gate) + r * p.ld_gate, col, count);
             }
         }
         copies_done();
@@ -99,114 +95,139 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) fetch(first + k * step, k);
     }
+
+    // pre's gain; and beta times the gate times post's gain (without a matrix's gate)
+    Pair gain[kPairs], back[JOIN ? kPairs : 1], acc[kSums][kPairs];
+    {
+        float a[kOwn], b[kOwn];
+        load_vector(p.pre.gain, p.pre.f32, col, count, 1.0f, a);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) gain[j] = pair(a[2 * j], a[2 * j + 1]);
+        if constexpr (JOIN) {
+            load_vector(p.post.gain, p.post.f32, col, count, 1.0f, a);
+            load_vector(p.gate_kind == RA_GATE_VECTOR ? p.gate : nullptr, p.gate_f32, col, count, 1.0f, b);
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) back[j] = pair(p.beta * b[2 * j] * a[2 * j], p.beta * b[2 * j + 1] * a[2 * j + 1]);
+        }
+    }
+#pragma unroll
+    for (int a = 0; a < kSums; ++a)
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) acc[a][j] = both(0.0f);
+
     for (int64_t r = first; r < p.rows; r += step) {
-        Own<TX, WIDE> x, d;
-        Own<TF, WIDE> h, f, g;
+        Own<TX, C> x;
+        Own<TF, C> h;
         float4 kept = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        uint32_t at = mine + stage * stage_bytes + kPitch;
+        const uint32_t at = mine + stage * stage_bytes;
         if constexpr (WIDE) {
             fetch(r + kAhead * step, stage == 0 ? kAhead : stage - 1);
             await_copies<kAhead>();
-            h.zero();
-            x.zero();
-            if (count > 0) {
-                if (p.kept != nullptr)
-                    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(kept.x), "=f"(kept.y), "=f"(kept.z), "=f"(kept.w) : "r"(at - kPitch) : "memory");
-                if (has_pre) {
-                    h.take(at, kPitch);
-                    x.take(at + places<TF>() * kPitch, kPitch);
-                }
-            }
-            at += (places<TF>() + places<TX>()) * kPitch;
+            if (p.kept != nullptr) asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(kept.x), "=f"(kept.y), "=f"(kept.z), "=f"(kept.w) : "r"(at) : "memory");
             stage = stage == kAhead ? 0 : stage + 1;
-        } else {
-            if (p.kept != nullptr) kept = reinterpret_cast<const float4 *>(p.kept)[r];
-            h.zero();
-            x.zero();
+        } else if (p.kept != nullptr) {
+            kept = reinterpret_cast<const float4 *>(p.kept)[r];
+        }
+        // the rest of a row's values, where they are needed
+        auto read = [&](auto &to, const auto *from, int64_t ld, int place) {
+            if constexpr (WIDE)
+                to.take(at + place, kPitch, count);
+            else
+                to.load(from + r * ld, col, count);
+        };
+        // columns past the row's end hold 0, and add 0 to the sums
+
+        Pair full[kPairs];
+        {
+            Pair unit[kPairs], by_unit = both(0.0f), plain = both(0.0f);
             if (has_pre) {
-                h.load(static_cast<const TF *>(p.dh) + r * p.ld_dh, col, count);
-                x.load(static_cast<const TX *>(p.x) + r * p.ld_x, col, count);
-            }
-            d.zero();
-            if (has_new) d.load(static_cast<const TX *>(p.dx_new) + r * p.ld_dx_new, col, count);
-            if constexpr (JOIN) {
-                f.load(static_cast<const TF *>(p.f) + r * p.ld_f, col, count);
-                if (by_matrix) g.load(static_cast<const TF *>(p.gate) + r * p.ld_gate, col, count);
-            }
-        }
-        float full[kOwn], by_unit = 0.0f, plain = 0.0f;
-        if (has_pre) {
-            float s[2] = {0.0f, 0.0f}, gain[kOwn];
-            load_gain(p.pre, col, count, gain);
+                read(h, static_cast<const TF *>(p.dh), p.ld_dh, kAtDh);
+                read(x, static_cast<const TX *>(p.x), p.ld_x, kAtX);
+                const Pair off = both(-kept.z), scale = both(kept.w);
+                Pair s0 = both(0.0f), s1 = both(0.0f);
 #pragma unroll
-            for (int j = 0; j < kOwn; ++j) {  // columns past the row's end: h and x are 0, and so is what they add
-                const float unit = (x[j] - kept.z) * kept.w;
-                full[j] = h[j] * gain[j];
-                s[0] = fmaf(full[j], unit, s[0]);
-                s[1] += full[j];
-                acc[kPreGain][j] = fmaf(h[j], unit, acc[kPreGain][j]);
-                acc[kPreBias][j] += h[j];
-            }
-            row_sum(s, sums[id], id, turn);
-            by_unit = s[0] * p.per_d;
-            plain = p.pre.kind == RA_NORM_LAYER ? s[1] * p.per_d : 0.0f;
-        }
-        if constexpr (WIDE) {
-            d.zero();
-            if (count > 0) {
-                if (has_new) d.take(at, kPitch);
-                if constexpr (JOIN) {
-                    f.take(at + places<TX>() * kPitch, kPitch);
-                    if (by_matrix) g.take(at + (places<TX>() + places<TF>()) * kPitch, kPitch);
+                for (int j = 0; j < kPairs; ++j) {
+                    const Pair dh = h.two(j);
+                    unit[j] = pair_mul(pair_add(x.two(j), off), scale);
+                    full[j] = pair_mul(dh, gain[j]);
+                    s0 = pair_fma(full[j], unit[j], s0);
+                    s1 = pair_add(s1, full[j]);
+                    acc[kDhUnit][j] = pair_fma(dh, unit[j], acc[kDhUnit][j]);
+                    acc[kDh][j] = pair_add(acc[kDh][j], dh);
                 }
-            } else if constexpr (JOIN) {
-                f.zero();
+                float s[2] = {pair_sum(s0), pair_sum(s1)};
+                row_sum(s, sums[id], id, turn);
+                by_unit = both(-s[0] * p.per_d);
+                plain = both(p.pre.kind == RA_NORM_LAYER ? -s[1] * p.per_d : 0.0f);
             }
+            Own<TX, C> d;
+            if (has_new) {
+                read(d, static_cast<const TX *>(p.dx_new), p.ld_dx_new, kAtNew);
+            } else {
+#pragma unroll
+                for (int i = 0; i < C::kParts; ++i) d.v[i].zero();
+            }
+            const Pair scale = both(kept.w);
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) full[j] = has_pre ? pair_fma(pair_fma(unit[j], by_unit, pair_add(full[j], plain)), scale, d.two(j)) : d.two(j);
         }
-#pragma unroll
-        for (int j = 0; j < kOwn; ++j)
-            full[j] = has_pre ? fmaf(kept.w, full[j] - plain - (x[j] - kept.z) * kept.w * by_unit, d[j]) : d[j];
         if (p.dx != nullptr) {
-            float y[kOwn];
+            const Pair alpha = both(JOIN ? p.alpha : 1.0f);
+            Pair y[kPairs];
 #pragma unroll
-            for (int j = 0; j < kOwn; ++j) y[j] = JOIN ? p.alpha * full[j] : full[j];
-            store_own<TX, WIDE>(static_cast<TX *>(p.dx) + r * p.ld_dx, col, count, y);
+            for (int j = 0; j < kPairs; ++j) y[j] = pair_mul(full[j], alpha);
+            x.set(y);
+            x.store(static_cast<TX *>(p.dx) + r * p.ld_dx, col, count);
         }
         if constexpr (JOIN) {
-            float s[2] = {0.0f, 0.0f}, gain[kOwn], bias[kOwn], gate[kOwn], dg[kOwn];
-            if (normed) {
-                load_gain(p.post, col, count, gain);
-            } else {
-                kept.x = 0.0f;
-                kept.y = 1.0f;
+            Own<TF, C> f;
+            read(f, static_cast<const TF *>(p.f), p.ld_f, kAtF);
+            Pair unit[kPairs], s0 = both(0.0f), s1 = both(0.0f);
+            const Pair off = both(normed ? -kept.x : 0.0f), scale = both(normed ? kept.y : 1.0f);
 #pragma unroll
-                for (int j = 0; j < kOwn; ++j) gain[j] = 1.0f;
-            }
-            load_vector<WIDE>(normed ? p.post.bias : nullptr, p.post.f32, col, count, 0.0f, bias);
-            load_vector<WIDE>(p.gate_kind == RA_GATE_VECTOR ? p.gate : nullptr, p.gate_f32, col, count, 1.0f, gate);
+            for (int j = 0; j < kPairs; ++j) unit[j] = pair_mul(pair_add(f.two(j), off), scale);
+            if (by_matrix) {
+                float a[kOwn], b[kOwn];
+                load_vector(p.post.gain, p.post.f32, col, count, 1.0f, a);
+                load_vector(p.post.bias, p.post.f32, col, count, 0.0f, b);
+                Own<TF, C> g;
+                read(g, static_cast<const TF *>(p.gate), p.ld_gate, kAtGate);
+                const Pair beta = both(p.beta);
+                Pair dg[kPairs];
 #pragma unroll
-            for (int j = 0; j < kOwn; ++j) {
-                if (!WIDE && j >= count) full[j] = 0.0f;
-                const float unit = (f[j] - kept.x) * kept.y, u = p.beta * full[j];
-                dg[j] = u * fmaf(unit, gain[j], bias[j]);
-                acc[kGate][j] += dg[j];
-                const float v = u * (by_matrix ? g[j] : gate[j]);
-                acc[kPostGain][j] = fmaf(v, unit, acc[kPostGain][j]);
-                acc[kPostBias][j] += v;
-                full[j] = v * gain[j];
-                s[0] = fmaf(full[j], unit, s[0]);
-                s[1] += full[j];
+                for (int j = 0; j < kPairs; ++j) {
+                    dg[j] = pair_mul(pair_mul(beta, full[j]), pair_fma(unit[j], pair(a[2 * j], a[2 * j + 1]), pair(b[2 * j], b[2 * j + 1])));
+                    full[j] = pair_mul(full[j], g.two(j));
+                }
+                if (p.dgate != nullptr) {
+                    g.set(dg);
+                    g.store(static_cast<TF *>(p.dgate) + r * p.ld_dgate, col, count);
+                }
             }
-            if (p.dgate != nullptr) store_own<TF, WIDE>(static_cast<TF *>(p.dgate) + r * p.ld_dgate, col, count, dg);
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+                if (count < kOwn) {
+                    float a, b;
+                    apart(full[j], a, b);
+                    full[j] = pair(2 * j < count ? a : 0.0f, 2 * j + 1 < count ? b : 0.0f);
+                }
+                acc[kDUnit][j] = pair_fma(full[j], unit[j], acc[kDUnit][j]);
+                acc[kD][j] = pair_add(acc[kD][j], full[j]);
+                full[j] = pair_mul(full[j], back[j]);
+                s0 = pair_fma(full[j], unit[j], s0);
+                s1 = pair_add(s1, full[j]);
+            }
             if (normed) {
-                if (WIDE && count == 0) s[0] = s[1] = 0.0f;
+                float s[2] = {pair_sum(s0), pair_sum(s1)};
                 row_sum(s, sums[id], id, turn);
-                by_unit = s[0] * p.per_d;
-                plain = p.post.kind == RA_NORM_LAYER ? s[1] * p.per_d : 0.0f;
+                const Pair by_unit = both(-s[0] * p.per_d), plain = both(p.post.kind == RA_NORM_LAYER ? -s[1] * p.per_d : 0.0f);
 #pragma unroll
-                for (int j = 0; j < kOwn; ++j) full[j] = kept.y * (full[j] - plain - (f[j] - kept.x) * kept.y * by_unit);
+                for (int j = 0; j < kPairs; ++j) full[j] = pair_mul(pair_fma(unit[j], by_unit, pair_add(full[j], plain)), scale);
             }
-            if (p.df != nullptr) store_own<TF, WIDE>(static_cast<TF *>(p.df) + r * p.ld_df, col, count, full);
+            if (p.df != nullptr) {
+                f.set(full);
+                f.store(static_cast<TF *>(p.df) + r * p.ld_df, col, count);
+            }
         }
     }
 
@@ -214,6 +235,9 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
     float *const part = p.parts + (int64_t)block * kSums * p.d;
 #pragma unroll
     for (int a = 0; a < kSums; ++a) {
+        float v[kOwn];
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) apart(acc[a][j], v[2 * j], v[2 * j + 1]);
         if constexpr (kGroups > 1) {  // the groups' sums in their order
             for (int k = 0; k < kGroups; ++k) {
                 __syncthreads();
@@ -221,59 +245,86 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
 #pragma unroll
                 for (int j = 0; j < kOwn; ++j) {
                     float &to = joined[col[j]];
-                    to = k == 0 ? acc[a][j] : to + acc[a][j];
+                    to = k == 0 ? v[j] : to + v[j];
                 }
             }
             __syncthreads();
             for (int c = threadIdx.x; c < p.d; c += kThreads) part[(int64_t)a * p.d + c] = joined[c];
         } else if constexpr (WIDE) {
-            if (count > 0) store_w<float, kOwn>(part + (int64_t)a * p.d + col.first, acc[a]);
+            if (count > 0) store_w<float, kOwn>(part + (int64_t)a * p.d + col.first, v);
         } else {
 #pragma unroll
             for (int j = 0; j < kOwn; ++j)
-                if (j < count) part[(int64_t)a * p.d + col[j]] = acc[a][j];
+                if (j < count) part[(int64_t)a * p.d + col[j]] = v[j];
         }
     }
 }
 
-// The blocks' sums, added in their order: a block takes 32 columns of one
-// vector, warp w the parts w, w + 8, ...
+// The blocks' sums, added in their order, and the gradients they give: a block takes
+// 32 columns, four warps each of the sums, warp w of these the parts w, w + 4, ... with
+// 8 of them in flight.
 struct PartsParams {
     const float *parts;
-    float *out[kVectors];
+    float *dpre_gain, *dpre_bias, *dpost_gain, *dpost_bias, *dgate;
+    const void *post_gain, *post_bias, *gate;
     int64_t count, d;  // parts
-    int vectors, accumulate;
+    int sums, accumulate;
+    bool post_f32, gate_f32;
+    float beta;
 };
-__global__ void __launch_bounds__(256) parts_kernel(const PartsParams p) {
-    __shared__ float sum[8][32];
+constexpr int kPartWarps = 4;
+__global__ void __launch_bounds__(kSumsMost *kPartWarps * 32) parts_kernel(const PartsParams p) {
+    __shared__ float sum[kSumsMost][kPartWarps][32];
     pdl_enter();
-    const int64_t strips = ceil_div<int64_t>(p.d, 32);
-    const int a = (int)(blockIdx.x / strips), lane = threadIdx.x & 31, w = threadIdx.x / 32;
-    const int64_t c = blockIdx.x % strips * 32 + lane;
-    float *out = p.out[0];
-#pragma unroll
-    for (int k = 1; k < kVectors; ++k)
-        if (a == k) out = p.out[k];
-    if (out == nullptr) return;
+    const int lane = threadIdx.x & 31, a = threadIdx.x / (32 * kPartWarps), w = threadIdx.x / 32 % kPartWarps;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.0f;
-    if (c < p.d)
-        for (int64_t b = w; b < p.count; b += 8) s += p.parts[(b * p.vectors + a) * p.d + c];
-    sum[w][lane] = s;
+    if (c < p.d && a < p.sums) {
+        const float *at = p.parts + a * p.d + c;
+        const int64_t pitch = p.sums * p.d;
+        int64_t b = w;
+        for (; b + 7 * kPartWarps < p.count; b += 8 * kPartWarps) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = at[(b + k * kPartWarps) * pitch];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += v[k];
+        }
+        for (; b < p.count; b += kPartWarps) s += at[b * pitch];
+    }
+    sum[a][w][lane] = s;
     __syncthreads();
-    if (w != 0 || c >= p.d) return;
-    for (int k = 1; k < 8; ++k) s += sum[k][lane];
-    out[c] = p.accumulate ? out[c] + s : s;
+    if (threadIdx.x >= 32 || c >= p.d) return;
+    float t[kSumsMost];
+#pragma unroll
+    for (int k = 0; k < kSumsMost; ++k) {
+        t[k] = sum[k][0][lane];
+#pragma unroll
+        for (int i = 1; i < kPartWarps; ++i) t[k] += sum[k][i][lane];
+    }
+    auto value = [&](const void *v, bool f32, float none) {
+        return v == nullptr ? none : f32 ? static_cast<const float *>(v)[c] : to_f32<uint16_t>(static_cast<const uint16_t *>(v)[c]);
+    };
+    auto put = [&](float *to, float v) {
+        if (to != nullptr) to[c] = p.accumulate ? to[c] + v : v;
+    };
+    const float by = p.beta * value(p.gate, p.gate_f32, 1.0f);
+    put(p.dpre_gain, t[kDhUnit]);
+    put(p.dpre_bias, t[kDh]);
+    put(p.dpost_gain, by * t[kDUnit]);
+    put(p.dpost_bias, by * t[kD]);
+    if (p.dgate != nullptr) put(p.dgate, p.beta * fmaf(value(p.post_gain, p.post_f32, 1.0f), t[kDUnit], value(p.post_bias, p.post_f32, 0.0f) * t[kD]));
 }
 
 // ---------------------------------------------------------------------------
 // host
 
 // blocks (or clusters) that share the rows, each with a part of the sums
-int64_t grad_parts(int64_t rows, int64_t d) { return Shape(d).shares(rows, 2); }
+int64_t grad_parts(int64_t rows, int64_t d) { return Shape(d, kOwn).shares(rows); }
 
 template <class TX, class TF, bool JOIN>
 cudaError_t launch_grad(const NormGradParams &p, bool wide, cudaStream_t s) {
-    const Shape sh(p.d);
+    const Shape sh(p.d, kOwn);
     return with_shape(sh, [&](auto warps, auto cluster) {
         constexpr int kWarps = decltype(warps)::value;
         constexpr bool kCluster = decltype(cluster)::value != 0;
@@ -302,7 +353,7 @@ extern "C" {
 size_t ra_norm_block_grad_workspace_bytes(int64_t rows, int64_t d) {
     using namespace ra::op;
     if (!sizes_ok(rows, d) || rows == 0 || d == 0 || d > RA_NORM_MAX_D) return 0;
-    return (size_t)(grad_parts(rows, d) * kVectors * d * 4);
+    return (size_t)(grad_parts(rows, d) * kSumsMost * d * 4);
 }
 
 ra_status ra_norm_block_grad(const ra_norm_block_grad_args *args, void *stream) {
@@ -328,15 +379,13 @@ ra_status ra_norm_block_grad(const ra_norm_block_grad_args *args, void *stream) 
     const Mat kept{a.kept, pre || post ? a.rows : 0, 4, 4, 4};
     const Mat dx{a.dx, a.dx ? a.rows : 0, a.d, a.ld_dx, ex}, df{a.df, a.df ? a.rows : 0, a.d, a.ld_df, ef};
     const Mat dgate{a.dgate, a.dgate ? (by_matrix ? a.rows : 1) : 0, a.d, a.ld_dgate, by_matrix ? ef : 4};
-    float *const vectors[kVectors] = {a.dpre_gain, a.dpre_bias, a.dpost_gain, a.dpost_bias, by_vector ? static_cast<float *>(a.dgate) : nullptr};
     const Mat all[] = {dh, dx_new, x, f, gm, kept, dx, df, dgate, vector_of(a.dpre_gain, a.d, 4), vector_of(a.dpre_bias, a.d, 4), vector_of(a.dpost_gain, a.d, 4),
                        vector_of(a.dpost_bias, a.d, 4)};
     for (const Mat &m : all)
         if (!mat_ok(m)) return RA_ERR_INVALID_ARG;
     if (!wide_at(a.kept)) return RA_ERR_INVALID_ARG;
     if (a.d > RA_NORM_MAX_D) return RA_ERR_UNSUPPORTED;
-    bool sums = false;
-    for (const float *v : vectors) sums = sums || v != nullptr;
+    const bool sums = a.dpre_gain || a.dpre_bias || a.dpost_gain || a.dpost_bias || (by_vector && a.dgate);
     const size_t need = sums ? ra_norm_block_grad_workspace_bytes(a.rows, a.d) : 0;
     if (need > 0 && (a.ws == nullptr || !wide_at(a.ws) || a.ws_bytes < need)) return RA_ERR_INVALID_ARG;
     const Side behind = join ? side_of(a.post) : Side{}, ahead = side_of(a.pre);
@@ -360,9 +409,10 @@ ra_status ra_norm_block_grad(const ra_norm_block_grad_args *args, void *stream) 
         if (e != cudaSuccess) return cuda_status(e);
     }
     if (!sums) return RA_OK;
-    PartsParams q{static_cast<const float *>(a.ws), {}, none ? 0 : grad_parts(a.rows, a.d), a.d, join ? kVectors : 2, a.accumulate};
-    for (int k = 0; k < kVectors; ++k) q.out[k] = vectors[k];
-    return cuda_status(launch_pdl(parts_kernel, ceil_div<int64_t>(a.d, 32) * q.vectors, 256, 0, s, q));
+    const PartsParams q{static_cast<const float *>(a.ws), a.dpre_gain, a.dpre_bias, a.dpost_gain, a.dpost_bias, by_vector ? static_cast<float *>(a.dgate) : nullptr,
+                        behind.gain, behind.bias, by_vector ? a.gate : nullptr, none ? 0 : grad_parts(a.rows, a.d), a.d, join ? kSumsMost : 2, a.accumulate, behind.f32,
+                        by_vector && a.gate_dtype == RA_F32, a.beta};
+    return cuda_status(launch_pdl(parts_kernel, ceil_div<int64_t>(a.d, 32), kSumsMost * kPartWarps * 32, 0, s, q));
 }
 
 }  // extern "C"

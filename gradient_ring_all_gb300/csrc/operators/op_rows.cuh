@@ -52,16 +52,19 @@ struct RowSums {
 
 template <int K, int WARPS, bool CLUSTER>
 __device__ __forceinline__ void row_sum(float (&v)[K], RowSums<K, WARPS, CLUSTER> &at, int id, int &turn) {
+    static_assert(K == 2, "two sums");
+    // the half warps trade one sum for the other, and each half adds up its own
+    const int lane = threadIdx.x & 31;
+    const float give = lane < 16 ? v[1] : v[0];
+    float own = (lane < 16 ? v[0] : v[1]) + __shfl_xor_sync(0xffffffffu, give, 16);
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int o = 16; o > 0; o /= 2) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    for (int o = 8; o > 0; o /= 2) own += __shfl_xor_sync(0xffffffffu, own, o);
+    if constexpr (WARPS == 1) {
+        v[0] = __shfl_sync(0xffffffffu, own, 0);
+        v[1] = __shfl_sync(0xffffffffu, own, 16);
+    }
     if constexpr (WARPS > 1) {
-        const int t = threadIdx.x % (WARPS * 32);
-        if (t % 32 == 0) {
-#pragma unroll
-            for (int k = 0; k < K; ++k) at.warp[turn][k][t / 32] = v[k];
-        }
+        if (lane % 16 == 0) at.warp[turn][lane / 16][threadIdx.x % (WARPS * 32) / 32] = own;
         group_meet<WARPS>(id);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -85,6 +88,37 @@ __device__ __forceinline__ void row_sum(float (&v)[K], RowSums<K, WARPS, CLUSTER
         }
     }
     turn ^= 1;
+}
+
+// Two binary32 values as one operand, and arithmetic on both at once with the
+// result in registers of its own.
+using Pair = uint64_t;
+__device__ __forceinline__ Pair pair(float a, float b) {
+    Pair v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+    return v;
+}
+__device__ __forceinline__ Pair both(float a) { return pair(a, a); }
+__device__ __forceinline__ void apart(Pair v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ Pair pair_fma(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair pair_mul(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float pair_sum(Pair v) {
+    float a, b;
+    apart(v, a, b);
+    return a + b;
 }
 
 // launch_pdl, in clusters of `cluster` blocks
