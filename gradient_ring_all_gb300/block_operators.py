@@ -60,6 +60,15 @@ def _vector(t, what, dev, n, dtype=None):
     return t.data_ptr(), code
 
 
+def _like(t, what, dev, dtype, s):
+    """(pointer, row stride) of a matrix of this type and shape: one look at what is right as a rule, _matrix says what is wrong."""
+    if t.dtype is dtype and t.shape == s and t.get_device() == dev >= 0:
+        ld, one = t.stride()
+        if one == 1 and ld >= s[1]:
+            return t.data_ptr(), ld
+    return _matrix(t, what, dev, dtype, s)[:2]
+
+
 # ---------------------------------------------------------------------------
 # dropout
 
@@ -125,14 +134,16 @@ def _norm(n, what, dev, d):
     """The fields of a ra_norm."""
     if n is None:
         return _NO_NORM
-    if not isinstance(n, Norm):
+    if n.__class__ is not Norm and not isinstance(n, Norm):
         raise TypeError("%s must be a Norm" % what)
-    pg, pb, code = 0, 0, 0
-    if n.gain is not None:
-        pg, code = _vector(n.gain, what + ".gain", dev, d)
-    if n.bias is not None:
-        pb, code = _vector(n.bias, what + ".bias", dev, d, None if n.gain is None else n.gain.dtype)
-    return pg, pb, code, n._kind, n.eps, 0
+    gain, bias = n.gain, n.bias
+    if gain is None:
+        if bias is None:
+            return 0, 0, 0, n._kind, n.eps, 0
+        pb, code = _vector(bias, what + ".bias", dev, d)
+        return 0, pb, code, n._kind, n.eps, 0
+    pg, code = _vector(gain, what + ".gain", dev, d)
+    return pg, 0 if bias is None else _vector(bias, what + ".bias", dev, d, gain.dtype)[0], code, n._kind, n.eps, 0
 
 
 def _gate(gate, dev, rows, d, f):
@@ -144,6 +155,11 @@ def _gate(gate, dev, rows, d, f):
         return p, d, 1, code
     p, ld, code = _matrix(gate, "gate", dev, f.dtype, (rows, d))
     return p, ld, 2, code
+
+
+def _new(like, dtype, stream):
+    """A new matrix beside `like`, of its shape."""
+    return _empty(like.shape, dtype, like.device, stream)
 
 
 def _block_type(f, x):
@@ -169,16 +185,17 @@ def ra_norm_block(x, f=None, post=None, gate=None, alpha: float = 1.0, beta: flo
     rows, d = s = _shape(x, "x")
     dev = _device(x.get_device())
     px, ldx, xcode = _matrix(x, "x", dev, None, s)
-    pf, ldf, po, ldo, pg, ldg, gkind, gcode = 0, 0, 0, 0, 0, 0, 0, 0
+    pf = ldf = po = ldo = pg = ldg = gkind = gcode = 0
     if f is not None:
         block = _block_type(f.dtype, x.dtype)
         if dtype is not None and dtype != block:
             raise TypeError("dtype must be that of f, %s, got %s" % (block, dtype))
-        pf, ldf, _ = _matrix(f, "f", dev, None, s)
-        pg, ldg, gkind, gcode = _gate(gate, dev, rows, d, f)
-        out, po, ldo, ocode = _output(out, rows, d, x.dtype, x, dev, stream)
-        if ocode != xcode:
-            raise TypeError("out must be %s, got %s" % (x.dtype, out.dtype))
+        pf, ldf = _like(f, "f", dev, block, s)
+        if gate is not None:
+            pg, ldg, gkind, gcode = _gate(gate, dev, rows, d, f)
+        if out is None:
+            out = _new(x, x.dtype, stream)
+        po, ldo = _like(out, "out", dev, x.dtype, s)
     else:
         if post is not None or gate is not None or out is not None:
             raise ValueError("post, gate and out need f")
@@ -186,17 +203,19 @@ def ra_norm_block(x, f=None, post=None, gate=None, alpha: float = 1.0, beta: flo
             raise ValueError("give f, pre, or both")
         block = _block_type(dtype or (_BF16 if h is None else h.dtype), x.dtype)
         out = x
-    ph, ldh = 0, 0
+    ph = ldh = 0
     behind, ahead = _norm(post, "post", dev, d), _norm(pre, "pre", dev, d)
     if pre is not None:
-        h, ph, ldh, hcode = _output(h, rows, d, block, x, dev, stream, "h")
-        if hcode != _CODE[block]:
-            raise TypeError("h must be %s, got %s" % (block, h.dtype))
+        if h is None:
+            h = _new(x, block, stream)
+        ph, ldh = _like(h, "h", dev, block, s)
     elif h is not None:
         raise ValueError("h needs pre")
-    kept = _empty((rows, 4), _F32, x.device, stream) if keep else None
-    args = _BLOCK.pack(rows, d, px, ldx, pf, ldf, pg, ldg, po, ldo, ph, ldh, kept.data_ptr() if keep else 0, *behind, *ahead, xcode, _CODE[block], gkind,
-                       gcode, alpha, beta)
+    pk, kept = 0, None
+    if keep:
+        kept = _empty((rows, 4), _F32, x.device, stream)
+        pk = kept.data_ptr()
+    args = _BLOCK.pack(rows, d, px, ldx, pf, ldf, pg, ldg, po, ldo, ph, ldh, pk, *behind, *ahead, xcode, _CODE[block], gkind, gcode, alpha, beta)
     _check(_load().ra_norm_block(args, _stream_of(stream, dev)), "ra_norm_block")
     return out, h, kept
 
@@ -225,73 +244,102 @@ def ra_norm_block_grad(dh, x, kept, f=None, post=None, gate=None, alpha: float =
     flat gradient or fewer gradients; its dx may be the dx given.  accumulate adds
     to its vectors (micro-batches)."""
     rows, d = s = _shape(x, "x")
+    stream_type = x.dtype
     dev = _device(x.get_device())
     px, ldx, xcode = _matrix(x, "x", dev, None, s)
-    ph, ldh, pd, ldd, pf, ldf, pg, ldg, gkind, gcode = 0, 0, 0, 0, 0, 0, 0, 0, 0, 0
+    ph = ldh = pd = ldd = pf = ldf = pg = ldg = gkind = gcode = pk = 0
     block = None
     if f is not None:
-        block = _block_type(f.dtype, x.dtype)
-        pf, ldf, _ = _matrix(f, "f", dev, None, s)
-        pg, ldg, gkind, gcode = _gate(gate, dev, rows, d, f)
+        block = _block_type(f.dtype, stream_type)
+        pf, ldf = _like(f, "f", dev, block, s)
+        if gate is not None:
+            pg, ldg, gkind, gcode = _gate(gate, dev, rows, d, f)
     elif post is not None or gate is not None:
         raise ValueError("post and gate need f")
     if (dh is None) != (pre is None):
         raise ValueError("dh and pre go together")
     if dh is not None:
-        block = _block_type(dh.dtype, x.dtype) if block is None else block
-        ph, ldh, _ = _matrix(dh, "dh", dev, block, s)
+        if block is None:
+            block = _block_type(dh.dtype, stream_type)
+        ph, ldh = _like(dh, "dh", dev, block, s)
     elif dx is None:
         raise ValueError("give dh, dx, or both")
     if dx is not None:
-        pd, ldd, _ = _matrix(dx, "dx", dev, x.dtype, s)
-    pk = 0
+        pd, ldd = _like(dx, "dx", dev, stream_type, s)
     if pre is not None or post is not None:
-        if kept is None or kept.dtype != _F32 or kept.shape != (rows, 4) or kept.get_device() != dev or not kept.is_contiguous():
+        if kept is None or kept.dtype is not _F32 or kept.shape != (rows, 4) or kept.get_device() != dev or not kept.is_contiguous():
             raise ValueError("kept must be the float32 [%d, 4] tensor that ra_norm_block returned" % rows)
         pk = kept.data_ptr()
     behind, ahead = _norm(post, "post", dev, d), _norm(pre, "pre", dev, d)
+    lib = _load()
+    need = lib.ra_norm_block_grad_workspace_bytes(rows, d)
+    po = ldo = pdf = lddf = pdg = lddg = pgg = pgb = prg = prb = pw = 0
+    hold = None
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
         out = NormBlockGrads()
-        out.dx = _empty((rows, d), x.dtype, x.device, stream)
-        names = [n for n, there in (("pre_gain", ahead[0]), ("pre_bias", ahead[1]), ("post_gain", behind[0]), ("post_bias", behind[1]), ("gate", gkind == 1))
-                 if there]
+        out.dx = t = _new(x, stream_type, stream)
+        po, ldo = t.data_ptr(), d
         if f is not None:
-            out.df = _empty((rows, d), block, x.device, stream)
+            out.df = t = _new(x, block, stream)
+            pdf, lddf = t.data_ptr(), d
             if gkind == 2:
-                out.gate = _empty((rows, d), block, x.device, stream)
-        if names:
-            for n, t in zip(names, _empty((len(names), d), _F32, x.device, stream).unbind(0)):
-                setattr(out, n, t)
+                out.gate = t = _new(x, block, stream)
+                pdg, lddg = t.data_ptr(), d
+        # the vectors' gradients lie side by side, the workspace (unless given) before them
+        count = (ahead[0] != 0) + (ahead[1] != 0) + (behind[0] != 0) + (behind[1] != 0) + (gkind == 1)
+        if count:
+            if workspace is None:
+                first, pitch = need // 4, -(-d // 4) * 4
+                flat = _empty((first + count * pitch,), _F32, x.device, stream)
+                pw = flat.data_ptr()
+            else:
+                hold, pw, need = _workspace(workspace, need, x, stream)
+                first, pitch = 0, -(-d // 4) * 4
+                flat = _empty((count * pitch,), _F32, x.device, stream)
+            at = flat.data_ptr() + 4 * first
+            if ahead[0]:
+                out.pre_gain, prg = flat[first:first + d], at
+                first, at = first + pitch, at + 4 * pitch
+            if ahead[1]:
+                out.pre_bias, prb = flat[first:first + d], at
+                first, at = first + pitch, at + 4 * pitch
+            if behind[0]:
+                out.post_gain, pgg = flat[first:first + d], at
+                first, at = first + pitch, at + 4 * pitch
+            if behind[1]:
+                out.post_bias, pgb = flat[first:first + d], at
+                first, at = first + pitch, at + 4 * pitch
+            if gkind == 1:
+                out.gate, pdg, lddg = flat[first:first + d], at, d
     elif not isinstance(out, NormBlockGrads):
         raise TypeError("out must be a NormBlockGrads")
-    po, ldo, pdf, lddf, pdg, lddg = 0, 0, 0, 0, 0, 0
-    if out.dx is not None:
-        po, ldo, _ = _matrix(out.dx, "out.dx", dev, x.dtype, s)
-    if out.df is not None:
-        if f is None:
-            raise ValueError("out.df needs f")
-        pdf, lddf, _ = _matrix(out.df, "out.df", dev, block, s)
-    if out.gate is not None:
-        if gkind == 0:
-            raise ValueError("out.gate needs a gate")
-        if gkind == 2:
-            pdg, lddg, _ = _matrix(out.gate, "out.gate", dev, block, s)
-        else:
-            pdg, lddg = _vector(out.gate, "out.gate", dev, d, _F32)[0], d
-    vectors = []
-    for name, norm in (("post_gain", post), ("post_bias", post), ("pre_gain", pre), ("pre_bias", pre)):
-        t = getattr(out, name)
-        if t is not None and norm is None:
-            raise ValueError("out.%s needs that norm" % name)
-        vectors.append(0 if t is None else _vector(t, "out." + name, dev, d, _F32)[0])
-    lib = _load()
-    hold, pw, nw = None, 0, 0
-    if any(vectors) or (gkind == 1 and pdg):
-        hold, pw, nw = _workspace(workspace, lib.ra_norm_block_grad_workspace_bytes(rows, d), x, stream)
-    args = _BLOCK_GRAD.pack(rows, d, ph, ldh, pd, ldd, px, ldx, pf, ldf, pg, ldg, pk, po, ldo, pdf, lddf, pdg, lddg, *vectors, pw, nw, *behind, *ahead,
-                            xcode, xcode if block is None else _CODE[block], gkind, gcode, alpha, beta, int(accumulate), 0)
+    else:
+        if out.dx is not None:
+            po, ldo = _like(out.dx, "out.dx", dev, stream_type, s)
+        if out.df is not None:
+            if f is None:
+                raise ValueError("out.df needs f")
+            pdf, lddf = _like(out.df, "out.df", dev, block, s)
+        if out.gate is not None:
+            if gkind == 0:
+                raise ValueError("out.gate needs a gate")
+            if gkind == 2:
+                pdg, lddg = _like(out.gate, "out.gate", dev, block, s)
+            else:
+                pdg, lddg = _vector(out.gate, "out.gate", dev, d, _F32)[0], d
+        if (out.post_gain is not None or out.post_bias is not None) and post is None:
+            raise ValueError("out.post_gain and out.post_bias need post")
+        if (out.pre_gain is not None or out.pre_bias is not None) and pre is None:
+            raise ValueError("out.pre_gain and out.pre_bias need pre")
+        pgg, pgb, prg, prb = (0 if t is None else _vector(t, what, dev, d, _F32)[0]
+                              for t, what in ((out.post_gain, "out.post_gain"), (out.post_bias, "out.post_bias"), (out.pre_gain, "out.pre_gain"),
+                                              (out.pre_bias, "out.pre_bias")))
+        if pgg or pgb or prg or prb or (gkind == 1 and pdg):
+            hold, pw, need = _workspace(workspace, need, x, stream)
+    args = _BLOCK_GRAD.pack(rows, d, ph, ldh, pd, ldd, px, ldx, pf, ldf, pg, ldg, pk, po, ldo, pdf, lddf, pdg, lddg, pgg, pgb, prg, prb, pw, need, *behind,
+                            *ahead, xcode, xcode if block is None else _CODE[block], gkind, gcode, alpha, beta, int(accumulate), 0)
     _check(lib.ra_norm_block_grad(args, _stream_of(stream, dev)), "ra_norm_block_grad")
     return out
 

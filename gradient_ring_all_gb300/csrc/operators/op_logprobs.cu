@@ -351,8 +351,9 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
             }
             // y = z scale2 - off.  bf16 logits are held in pairs, before they are taken
             // apart, to a least value whose exponential is 0 (low); beside the lowest
-            // finite ones there is none.  Where that is so, or the thread's first
-            // logits cannot be, the sums are made the other way below (not plain).
+            // finite ones there is none.  Where that is so the sums are made the other
+            // way below (not plain).  Batches of tokens that cannot be add nothing
+            // before the first logit to start from.
             uint64_t s2 = Two(0.0f).v, w2 = Two(0.0f).v, off2 = Two(0.0f).v;
             const uint64_t scale2 = Two(p.scale2).v;
             float most = -kInf, off = 0.0f;  // the largest
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
                 const float base = base_of(a.m);
                 off = base * p.scale2;
                 off2 = Two(-off).v;
-                plain = a.m > -kInf && fabsf(off) < 1e30f;
+                plain = fabsf(off) < 1e30f;
                 if constexpr (sizeof(T) == 2) {
                     low = floor_bf16x2(base - p.reach);
                     plain = plain && low != 0xff80ff80u && (base - __uint_as_float(low & 0xffff0000u)) * p.scale2 >= -kLeast;
@@ -379,7 +380,12 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
                 for (int i = 0; i < kBatch; ++i) x[i].take(land + (i0 + i) * kPitch);
                 if (i0 < ahead_slots) fetch(i0, ahead, ahead_left);  // what these places held has been read
                 if (i0 >= slots) continue;
-                if (i0 == 0) start(largest(x[0]));
+                if (i0 == 0 || a.m == -kInf) {
+                    float m = largest(x[0]);
+#pragma unroll
+                    for (int i = 1; i < kBatch; ++i) m = fmaxf(m, largest(x[i]));
+                    start(m);
+                }
                 float here = -kInf;
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
@@ -403,6 +409,8 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
                     }
                 }
                 if constexpr (TOP) {
+                    // nothing but the least value: no token that can be, or one that far off
+                    if (sizeof(T) == 2 && here <= __uint_as_float(low & 0xffff0000u) && a.m == -kInf) here = -kInf;
                     asm volatile("st.shared.f32 [%0], %1;" ::"r"(heights + i0 / kBatch * 4), "f"(here) : "memory");
                     most = fmaxf(most, here);
                 }
@@ -410,7 +418,7 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
             if (last_step && r + stride < last_row) fetch_token(r + stride);
             asm volatile("cp.async.commit_group;" ::: "memory");
             const float odd = has_odd && step == 0 ? odd_raw[0] : -kInf;
-            if (slots <= 0) start(odd);
+            if (a.m == -kInf) start(odd);
             float s[2], w[2];
             asm("mov.b64 {%0, %1}, %2;" : "=f"(s[0]), "=f"(s[1]) : "l"(s2));
             asm("mov.b64 {%0, %1}, %2;" : "=f"(w[0]), "=f"(w[1]) : "l"(w2));
@@ -466,7 +474,11 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
                 uint32_t key = key_of(fmaxf(most, odd)), other = 0;
                 if (WARPS == 1 && fine == 2) {  // a lane's batches are two groups
                     float h[2] = {odd, -kInf};
-                    for (int i = 0; i * kBatch < slots; ++i) h[i & 1] = fmaxf(h[i & 1], height_at(heights + i * 4));
+                    const float lowest = sizeof(T) == 2 && plain ? __uint_as_float(low & 0xffff0000u) : -kInf;
+                    for (int i = 0; i * kBatch < slots; ++i) {
+                        const float v = height_at(heights + i * 4);
+                        h[i & 1] = fmaxf(h[i & 1], v > lowest ? v : -kInf);  // (the least value stands for any below it)
+                    }
                     key = key_of(h[0]);
                     other = key_of(h[1]);
                     room.keys[32 + lane] = other;
