@@ -44,43 +44,55 @@ struct DropParams {
     int64_t units, per_row;  // pieces of work, and how many a row has
     Divisor by;              // per_row
     uint64_t seed;
-    uint32_t site, t;  // a value is kept where its 16 bits are >= t
+    uint32_t keys[20];  // each round's two, from the seed (without seed_at)
+    uint32_t site, t;   // a value is kept where its 16 bits are >= t / 65536
     float scale;
+    bool none, dense;  // nothing is kept; each matrix is one run of rows without gaps
 };
 
-__device__ __forceinline__ uint4 philox(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0, uint32_t k1) {
+// What a round adds to the key: the golden ratio's and sqrt(3)'s fractions.
+constexpr uint32_t kWeyl0 = 0x9E3779B9u, kWeyl1 = 0xBB67AE85u;
+
+// AT: the key is made from the seed in device memory; else it is in the constants.
+template <bool AT>
+__device__ __forceinline__ uint4 philox(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, const DropParams &p, uint64_t seed) {
+    uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
 #pragma unroll
     for (int round = 0; round < 10; ++round) {
         const uint64_t a = (uint64_t)0xD2511F53u * c0, b = (uint64_t)0xCD9E8D57u * c2;
-        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
-        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c0 = (uint32_t)(b >> 32) ^ c1 ^ (AT ? k0 : p.keys[2 * round]);
+        c2 = (uint32_t)(a >> 32) ^ c3 ^ (AT ? k1 : p.keys[2 * round + 1]);
         c1 = (uint32_t)b;
         c3 = (uint32_t)a;
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
+        k0 += kWeyl0;
+        k1 += kWeyl1;
     }
     return make_uint4(c0, c1, c2, c3);
 }
 
 // the bits of group g of row r
+template <bool AT>
 __device__ __forceinline__ uint4 bits_of(const DropParams &p, uint64_t seed, int64_t r, uint32_t g) {
     const uint64_t row = (uint64_t)(p.first_row + r);
-    return philox(g, p.site, (uint32_t)row, (uint32_t)(row >> 32), (uint32_t)seed, (uint32_t)(seed >> 32));
+    return philox<AT>(g, p.site, (uint32_t)row, (uint32_t)(row >> 32), p, seed);
 }
 
-// whether value j of a group is kept
+// whether value j of a group is kept: its half of the word, in the high bits, against t
 __device__ __forceinline__ bool kept_of(const uint4 &w, int j, uint32_t t) {
     const uint32_t word = j < 4 ? (j < 2 ? w.x : w.y) : (j < 6 ? w.z : w.w);
-    return (j & 1 ? word >> 16 : word & 0xffffu) >= t;
+    return (j & 1 ? word : word << 16) >= t;
 }
 
-__device__ __forceinline__ uint64_t seed_of(const DropParams &p) { return p.seed + (p.seed_at ? *p.seed_at : 0); }
+template <bool AT>
+__device__ __forceinline__ uint64_t seed_of(const DropParams &p) {
+    return AT ? p.seed + *p.seed_at : p.seed;
+}
 
 // A unit's row and its place in the row.
 __device__ __forceinline__ void place_of(const DropParams &p, int64_t u, int64_t *r, int64_t *k) {
     if (p.units <= 0xffffffffll) {
         *r = p.by.of((uint32_t)u);
-        *k = (uint32_t)u - (uint32_t)*r * (uint32_t)p.per_row;
+        *k = (uint32_t)u - (uint32_t)*r * p.by.d;
     } else {
         *r = u / p.per_row;
         *k = u - *r * p.per_row;
@@ -101,36 +113,44 @@ struct Residual<void> {
 
 // Rows on 16-byte boundaries, whole groups: a thread takes groups, kDropFlight
 // in flight, by 16-byte accesses.
-template <class TX, class TR, class TY>
-__global__ void __launch_bounds__(kDropThreads) dropout_kernel(const DropParams p) {
+template <class TX, class TR, class TY, bool AT>
+__global__ void __launch_bounds__(kDropThreads, 4) dropout_kernel(const DropParams p) {
     pdl_enter();
     using R = Residual<TR>;
-    const uint64_t seed = seed_of(p);
+    const uint64_t seed = seed_of<AT>(p);
     constexpr int64_t kPer = kDropThreads * kDropFlight;
+    auto at = [&](auto *base, int64_t ld, int64_t u) {
+        if (p.dense) return base + u * 8;
+        int64_t r, k;
+        place_of(p, u, &r, &k);
+        return base + r * ld + k * 8;
+    };
     for (int64_t u0 = (int64_t)blockIdx.x * kPer + threadIdx.x; u0 < p.units; u0 += (int64_t)gridDim.x * kPer) {
         Raw<TX, 8> x[kDropFlight];
         Raw<typename R::T, 8> res[kDropFlight];
-        int64_t r[kDropFlight], k[kDropFlight];
 #pragma unroll
         for (int j = 0; j < kDropFlight; ++j) {
             const int64_t u = u0 + j * kDropThreads;
             if (u < p.units) {
-                place_of(p, u, &r[j], &k[j]);
-                x[j].load(static_cast<const TX *>(p.x) + r[j] * p.ldx + k[j] * 8);
-                if constexpr (R::on) res[j].load(static_cast<const typename R::T *>(p.residual) + r[j] * p.ldr + k[j] * 8);
+                x[j].load(at(static_cast<const TX *>(p.x), p.ldx, u));
+                if constexpr (R::on) res[j].load(at(static_cast<const typename R::T *>(p.residual), p.ldr, u));
             }
         }
 #pragma unroll
         for (int j = 0; j < kDropFlight; ++j) {
-            if (u0 + j * kDropThreads >= p.units) break;
-            const uint4 w = bits_of(p, seed, r[j], (uint32_t)k[j]);
+            const int64_t u = u0 + j * kDropThreads;
+            if (u >= p.units) break;
+            int64_t r, k;
+            place_of(p, u, &r, &k);
+            const uint4 w = bits_of<AT>(p, seed, r, (uint32_t)k);
+            if (p.none) x[j].zero();
             float y[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 y[i] = kept_of(w, i, p.t) ? x[j][i] * p.scale : 0.0f;
                 if constexpr (R::on) y[i] += res[j][i];
             }
-            store_w<TY, 8>(static_cast<TY *>(p.y) + r[j] * p.ldy + k[j] * 8, y);
+            store_w<TY, 8>(at(static_cast<TY *>(p.y), p.ldy, u), y);
         }
     }
 }
@@ -138,11 +158,11 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const DropParams 
 // Any stride, width and alignment: a warp takes 256 neighbouring columns of a
 // row.  A lane makes the bits of one group, and the lanes read and write the
 // groups' values side by side.
-template <class TX, class TR, class TY>
+template <class TX, class TR, class TY, bool AT>
 __global__ void __launch_bounds__(kDropThreads) dropout_scalar_kernel(const DropParams p) {
     pdl_enter();
     using R = Residual<TR>;
-    const uint64_t seed = seed_of(p);
+    const uint64_t seed = seed_of<AT>(p);
     const int lane = threadIdx.x & 31;
     const int64_t step = (int64_t)gridDim.x * (kDropThreads / 32);
     for (int64_t u = (int64_t)blockIdx.x * (kDropThreads / 32) + threadIdx.x / 32; u < p.units; u += step) {
@@ -158,10 +178,10 @@ __global__ void __launch_bounds__(kDropThreads) dropout_scalar_kernel(const Drop
             x[j].load(static_cast<const TX *>(p.x) + r * p.ldx + c);
             if constexpr (R::on) res[j].load(static_cast<const typename R::T *>(p.residual) + r * p.ldr + c);
         }
-        const uint4 w = bits_of(p, seed, r, (uint32_t)(k * 32 + lane));
+        const uint4 w = bits_of<AT>(p, seed, r, (uint32_t)(k * 32 + lane));
         uint32_t mine = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) mine |= kept_of(w, j, p.t) ? 1u << j : 0u;
+        for (int j = 0; j < 8; ++j) mine |= kept_of(w, j, p.t) && !p.none ? 1u << j : 0u;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const uint32_t group = __shfl_sync(0xffffffffu, mine, 4 * j + lane / 8);
@@ -175,11 +195,15 @@ __global__ void __launch_bounds__(kDropThreads) dropout_scalar_kernel(const Drop
     }
 }
 
-template <class TX, class TR, class TY>
+template <class TX, class TR, class TY, bool AT>
 cudaError_t launch_drop(const DropParams &p, bool wide, cudaStream_t s) {
     const int64_t blocks = ceil_div<int64_t>(p.units, wide ? kDropThreads * kDropFlight : kDropThreads / 32);
     const int64_t grid = blocks < kMaxGrid ? blocks : kMaxGrid;
-    return launch_pdl(wide ? dropout_kernel<TX, TR, TY> : dropout_scalar_kernel<TX, TR, TY>, grid, kDropThreads, 0, s, p);
+    return launch_pdl(wide ? dropout_kernel<TX, TR, TY, AT> : dropout_scalar_kernel<TX, TR, TY, AT>, grid, kDropThreads, 0, s, p);
+}
+template <class TX, class TR, class TY>
+cudaError_t launch_drop(const DropParams &p, bool wide, cudaStream_t s) {
+    return p.seed_at != nullptr ? launch_drop<TX, TR, TY, true>(p, wide, s) : launch_drop<TX, TR, TY, false>(p, wide, s);
 }
 
 template <class TX, class TY>
@@ -208,8 +232,13 @@ extern "C" ra_status ra_dropout(const void *x, int64_t ld_x, int x_dtype, int64_
     const bool wide = cols % 8 == 0 && a.aligned(16) && b.aligned(16) && (residual == nullptr || c.aligned(16));
     const int64_t per_row = wide ? cols / 8 : ceil_div<int64_t>(cols, 256);
     const uint32_t t = (uint32_t)nearbyint(65536.0 * p);
-    const DropParams q{x, residual, y, seed_at, ld_x, ld_res, ld_y, rows, cols, first_row, rows * per_row, per_row, Divisor((uint32_t)per_row),
-                       seed, site, t, t < 65536 ? (float)(65536.0 / (65536 - (int)t)) : 0.0f};
+    const bool dense = rows == 1 || (ld_x == cols && ld_y == cols && (residual == nullptr || ld_res == cols));
+    DropParams q{x, residual, y, seed_at, ld_x, ld_res, ld_y, rows, cols, first_row, rows * per_row, per_row, Divisor((uint32_t)per_row), seed, {}, site, t << 16,
+                 t < 65536 ? (float)(65536.0 / (65536 - (int)t)) : 0.0f, t == 65536, dense};
+    for (uint32_t k = 0; k < 10; ++k) {
+        q.keys[2 * k] = (uint32_t)seed + k * kWeyl0;
+        q.keys[2 * k + 1] = (uint32_t)(seed >> 32) + k * kWeyl1;
+    }
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (x_dtype == RA_F32)
         return cuda_status(y_dtype == RA_F32 ? launch_drop<float, float>(q, res_dtype, wide, s) : launch_drop<float, uint16_t>(q, res_dtype, wide, s));
