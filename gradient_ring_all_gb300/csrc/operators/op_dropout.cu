@@ -14,7 +14,6 @@ namespace op {
 namespace {
 
 constexpr int kDropThreads = 256;
-constexpr int kDropFlight = 4;  // groups of 8 a thread has in flight
 
 // u / d for any 32-bit u by a multiplication: with s = ceil(log2 d) and
 // m = floor(2^32 (2^s - d) / d) + 1, u / d = (umulhi(u, m) + u) >> s without
@@ -111,46 +110,113 @@ struct Residual<void> {
     static constexpr bool on = false;
 };
 
-// Rows on 16-byte boundaries, whole groups: a thread takes groups, kDropFlight
-// in flight, by 16-byte accesses.
-template <class TX, class TR, class TY, bool AT>
-__global__ void __launch_bounds__(kDropThreads, 4) dropout_kernel(const DropParams p) {
+// SPAN neighbours of a row, 8 or 16, as they lie in memory; rows on 16-byte
+// boundaries, or on 32-byte ones where that is the access (whole sectors).
+template <class T, int SPAN>
+struct Span {
+    uint32_t w[SPAN * sizeof(T) / 4];
+    template <bool SECTOR>
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (SECTOR) {
+#pragma unroll
+            for (int i = 0; i < (int)(SPAN * sizeof(T)) / 32; ++i) {
+                uint32_t s[8];
+                load_sector(reinterpret_cast<const char *>(p) + 32 * i, s);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) w[8 * i + k] = s[k];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < (int)(SPAN * sizeof(T)) / 16; ++i) {
+                const uint4 v = load_16(reinterpret_cast<const char *>(p) + 16 * i);
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
+            }
+        }
+    }
+    __device__ __forceinline__ float operator[](int j) const {
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(w[j]);
+        else
+            return __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+    }
+    __device__ __forceinline__ void set(int j, float a, float b) {
+        if constexpr (sizeof(T) == 4) {
+            w[j] = __float_as_uint(a);
+            w[j + 1] = __float_as_uint(b);
+        } else {
+            w[j / 2] = pack2(a, b);
+        }
+    }
+    template <bool SECTOR>
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (SECTOR) {
+#pragma unroll
+            for (int i = 0; i < (int)(SPAN * sizeof(T)) / 32; ++i) {
+                uint32_t s[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) s[k] = w[8 * i + k];
+                store_sector(reinterpret_cast<char *>(p) + 32 * i, s);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < (int)(SPAN * sizeof(T)) / 16; ++i)
+                reinterpret_cast<uint4 *>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+    }
+};
+
+// Whole groups of 8 (SPAN 8, rows on 16-byte boundaries) or pairs of groups (SPAN
+// 16, rows on 32-byte boundaries): a thread takes kFlight spans at a time.
+template <class TX, class TR, class TY, bool AT, int SPAN>
+__global__ void __launch_bounds__(kDropThreads) dropout_kernel(const DropParams p) {
     pdl_enter();
     using R = Residual<TR>;
+    constexpr int kFlight = SPAN == 16 ? (R::on ? 1 : 2) : (R::on ? 2 : 4);
+    constexpr bool kSector = SPAN == 16;
     const uint64_t seed = seed_of<AT>(p);
-    constexpr int64_t kPer = kDropThreads * kDropFlight;
+    constexpr int64_t kPer = kDropThreads * kFlight;
     auto at = [&](auto *base, int64_t ld, int64_t u) {
-        if (p.dense) return base + u * 8;
+        if (p.dense) return base + u * SPAN;
         int64_t r, k;
         place_of(p, u, &r, &k);
-        return base + r * ld + k * 8;
+        return base + r * ld + k * SPAN;
     };
     for (int64_t u0 = (int64_t)blockIdx.x * kPer + threadIdx.x; u0 < p.units; u0 += (int64_t)gridDim.x * kPer) {
-        Raw<TX, 8> x[kDropFlight];
-        Raw<typename R::T, 8> res[kDropFlight];
+        Span<TX, SPAN> x[kFlight];
+        Span<typename R::T, SPAN> res[kFlight];
 #pragma unroll
-        for (int j = 0; j < kDropFlight; ++j) {
+        for (int j = 0; j < kFlight; ++j) {
             const int64_t u = u0 + j * kDropThreads;
             if (u < p.units) {
-                x[j].load(at(static_cast<const TX *>(p.x), p.ldx, u));
-                if constexpr (R::on) res[j].load(at(static_cast<const typename R::T *>(p.residual), p.ldr, u));
+                x[j].template load<kSector>(at(static_cast<const TX *>(p.x), p.ldx, u));
+                if constexpr (R::on) res[j].template load<kSector>(at(static_cast<const typename R::T *>(p.residual), p.ldr, u));
             }
         }
 #pragma unroll
-        for (int j = 0; j < kDropFlight; ++j) {
+        for (int j = 0; j < kFlight; ++j) {
             const int64_t u = u0 + j * kDropThreads;
             if (u >= p.units) break;
             int64_t r, k;
             place_of(p, u, &r, &k);
-            const uint4 w = bits_of<AT>(p, seed, r, (uint32_t)k);
-            if (p.none) x[j].zero();
-            float y[8];
+            Span<TY, SPAN> out;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                y[i] = kept_of(w, i, p.t) ? x[j][i] * p.scale : 0.0f;
-                if constexpr (R::on) y[i] += res[j][i];
+            for (int g = 0; g < SPAN / 8; ++g) {
+                const uint4 w = bits_of<AT>(p, seed, r, (uint32_t)k * (SPAN / 8) + g);
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const int c = 8 * g + i;
+                    float y0 = kept_of(w, i, p.t) && !p.none ? x[j][c] * p.scale : 0.0f, y1 = kept_of(w, i + 1, p.t) && !p.none ? x[j][c + 1] * p.scale : 0.0f;
+                    if constexpr (R::on) {
+                        y0 += res[j][c];
+                        y1 += res[j][c + 1];
+                    }
+                    out.set(c, y0, y1);
+                }
             }
-            store_w<TY, 8>(at(static_cast<TY *>(p.y), p.ldy, u), y);
+            out.template store<kSector>(at(static_cast<TY *>(p.y), p.ldy, u));
         }
     }
 }
@@ -195,21 +261,23 @@ __global__ void __launch_bounds__(kDropThreads) dropout_scalar_kernel(const Drop
     }
 }
 
+// values a thread takes at once: 16, 8, or (any stride, width and alignment) 0
 template <class TX, class TR, class TY, bool AT>
-cudaError_t launch_drop(const DropParams &p, bool wide, cudaStream_t s) {
-    const int64_t blocks = ceil_div<int64_t>(p.units, wide ? kDropThreads * kDropFlight : kDropThreads / 32);
-    const int64_t grid = blocks < kMaxGrid ? blocks : kMaxGrid;
-    return launch_pdl(wide ? dropout_kernel<TX, TR, TY, AT> : dropout_scalar_kernel<TX, TR, TY, AT>, grid, kDropThreads, 0, s, p);
+cudaError_t launch_drop(const DropParams &p, int span, cudaStream_t s) {
+    const int64_t each = span == 0 ? kDropThreads / 32 : kDropThreads * (32 / span) / (p.residual ? 2 : 1);
+    const int64_t blocks = ceil_div<int64_t>(p.units, each), grid = blocks < kMaxGrid ? blocks : kMaxGrid;
+    return launch_pdl(span == 16 ? dropout_kernel<TX, TR, TY, AT, 16> : span == 8 ? dropout_kernel<TX, TR, TY, AT, 8> : dropout_scalar_kernel<TX, TR, TY, AT>, grid,
+                      kDropThreads, 0, s, p);
 }
 template <class TX, class TR, class TY>
-cudaError_t launch_drop(const DropParams &p, bool wide, cudaStream_t s) {
-    return p.seed_at != nullptr ? launch_drop<TX, TR, TY, true>(p, wide, s) : launch_drop<TX, TR, TY, false>(p, wide, s);
+cudaError_t launch_drop(const DropParams &p, int span, cudaStream_t s) {
+    return p.seed_at != nullptr ? launch_drop<TX, TR, TY, true>(p, span, s) : launch_drop<TX, TR, TY, false>(p, span, s);
 }
 
 template <class TX, class TY>
-cudaError_t launch_drop(const DropParams &p, int res_dtype, bool wide, cudaStream_t s) {
-    if (p.residual == nullptr) return launch_drop<TX, void, TY>(p, wide, s);
-    return res_dtype == RA_F32 ? launch_drop<TX, float, TY>(p, wide, s) : launch_drop<TX, uint16_t, TY>(p, wide, s);
+cudaError_t launch_drop(const DropParams &p, int res_dtype, int span, cudaStream_t s) {
+    if (p.residual == nullptr) return launch_drop<TX, void, TY>(p, span, s);
+    return res_dtype == RA_F32 ? launch_drop<TX, float, TY>(p, span, s) : launch_drop<TX, uint16_t, TY>(p, span, s);
 }
 
 }  // namespace
@@ -229,8 +297,9 @@ extern "C" ra_status ra_dropout(const void *x, int64_t ld_x, int x_dtype, int64_
     if (a.empty()) return RA_OK;
     const Mat at{seed_at, seed_at ? 1 : 0, 1, 1, 8};
     if ((mats_overlap(a, b) && !same_mat(a, b)) || (mats_overlap(c, b) && !same_mat(c, b)) || mats_overlap(at, b)) return RA_ERR_OVERLAP;
-    const bool wide = cols % 8 == 0 && a.aligned(16) && b.aligned(16) && (residual == nullptr || c.aligned(16));
-    const int64_t per_row = wide ? cols / 8 : ceil_div<int64_t>(cols, 256);
+    auto aligned = [&](int bytes) { return cols % (bytes / 2) == 0 && a.aligned(bytes) && b.aligned(bytes) && (residual == nullptr || c.aligned(bytes)); };
+    const int span = aligned(32) ? 16 : aligned(16) ? 8 : 0;
+    const int64_t per_row = span ? cols / span : ceil_div<int64_t>(cols, 256);
     const uint32_t t = (uint32_t)nearbyint(65536.0 * p);
     const bool dense = rows == 1 || (ld_x == cols && ld_y == cols && (residual == nullptr || ld_res == cols));
     DropParams q{x, residual, y, seed_at, ld_x, ld_res, ld_y, rows, cols, first_row, rows * per_row, per_row, Divisor((uint32_t)per_row), seed, {}, site, t << 16,
@@ -241,7 +310,7 @@ extern "C" ra_status ra_dropout(const void *x, int64_t ld_x, int x_dtype, int64_
     }
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (x_dtype == RA_F32)
-        return cuda_status(y_dtype == RA_F32 ? launch_drop<float, float>(q, res_dtype, wide, s) : launch_drop<float, uint16_t>(q, res_dtype, wide, s));
-    return cuda_status(y_dtype == RA_F32 ? launch_drop<uint16_t, float>(q, res_dtype, wide, s)
-                                         : launch_drop<uint16_t, uint16_t>(q, res_dtype, wide, s));
+        return cuda_status(y_dtype == RA_F32 ? launch_drop<float, float>(q, res_dtype, span, s) : launch_drop<float, uint16_t>(q, res_dtype, span, s));
+    return cuda_status(y_dtype == RA_F32 ? launch_drop<uint16_t, float>(q, res_dtype, span, s)
+                                         : launch_drop<uint16_t, uint16_t>(q, res_dtype, span, s));
 }
