@@ -663,11 +663,12 @@ cudaError_t launch_logprobs(const LogParams &p, cudaStream_t s) {
 // backward
 //
 // d = q (c0 + c1 y) for y = log2 p, q = 2^y, and scale g more at the given token:
-// c0 = -scale (g + e H), c1 = -scale e ln 2.  A warp takes a stretch of a row,
-// kFlight vectors of 8 logits a lane, so that rows of any length share one
-// kernel and its few numbers a row are read beside the logits.
+// c0 = -scale (g + e H), c1 = -scale e ln 2.  LANES lanes take a stretch of a row,
+// kFlight vectors of 8 logits a lane: a warp, or for short rows a quarter of one, so
+// that four rows' few numbers and logits are under way at once (65521 x 257 bf16 with
+// the entropy's gradient: 36 us a warp a row, 14 so).
 
-constexpr int kGradThreads = 256, kFlight = 4, kStretch = 32 * kFlight;  // vectors
+constexpr int kGradThreads = 256, kFlight = 4;
 
 struct LogGradParams {
     const void *logits, *ids;
@@ -678,12 +679,13 @@ struct LogGradParams {
     float scale, scale2;
 };
 
-template <class T, class TO, bool ENTROPY>
+template <class T, class TO, bool ENTROPY, int LANES>
 __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const LogGradParams p) {
     pdl_enter();
-    const int lane = threadIdx.x & 31;
+    constexpr int kStretch = LANES * kFlight, kAtOnce = kGradThreads / LANES;  // vectors, stretches
+    const int lane = threadIdx.x % LANES;
     const int64_t total = p.rows * p.stretches;
-    for (int64_t u = (int64_t)blockIdx.x * (kGradThreads / 32) + threadIdx.x / 32; u < total; u += (int64_t)gridDim.x * (kGradThreads / 32)) {
+    for (int64_t u = (int64_t)blockIdx.x * kAtOnce + threadIdx.x / LANES; u < total; u += (int64_t)gridDim.x * kAtOnce) {
         int64_t r, k;
         row_of(u, p.stretches, total, &r, &k);
         const T *row = static_cast<const T *>(p.logits) + r * p.ld;
@@ -698,13 +700,13 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const LogGr
         const int v0 = (int)k * kStretch + lane;
 #pragma unroll
         for (int i = 0; i < kFlight; ++i)
-            if (v0 + 32 * i < vecs) x[i].load(row + head + (int64_t)(v0 + 32 * i) * 8);
+            if (v0 + LANES * i < vecs) x[i].load(row + head + (int64_t)(v0 + LANES * i) * 8);
         const int64_t id = p.g == nullptr ? -1 : p.id_bytes == 8 ? static_cast<const int64_t *>(p.ids)[r] : static_cast<const int32_t *>(p.ids)[r];
-        const float lse = p.lse[r], g = id >= 0 && id < p.vocab ? p.g[r] : 0.0f;
+        const float lse = p.lse[r], given = p.g == nullptr ? 0.0f : p.g[r];
         const float ge = ENTROPY ? p.ge[r] : 0.0f, h = ENTROPY ? p.entropy[r] : 0.0f;
-        const bool none = lse < -1e30f;  // no token can be: zeros
-        const int at = none || id < 0 || id >= p.vocab ? -1 : (int)id;
-        const float off = none ? 0.0f : -lse * kLog2e, hot = p.scale * g;
+        const bool none = lse < -1e30f, inside = id >= 0 && id < p.vocab;  // none: no token can be: zeros
+        const int at = none || !inside ? -1 : (int)id;
+        const float g = inside ? given : 0.0f, off = none ? 0.0f : -lse * kLog2e, hot = p.scale * g;
         const float c0 = none ? 0.0f : ENTROPY ? -p.scale * fmaf(ge, h, g) : -hot, c1 = none ? 0.0f : -p.scale * kLn2 * ge;
         auto slope = [&](float z) {
             float y = fmaf(z, p.scale2, off);
@@ -717,8 +719,8 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const LogGr
         };
 #pragma unroll
         for (int i = 0; i < kFlight; ++i) {
-            if (v0 + 32 * i >= vecs) break;
-            const int c = head + (v0 + 32 * i) * 8;
+            if (v0 + LANES * i >= vecs) break;
+            const int c = head + (v0 + LANES * i) * 8;
             float d[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) d[j] = slope(x[i][j]);
@@ -729,28 +731,33 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const LogGr
             }
             store_w<TO, 8>(out + c, d);
         }
-        if (vecs > 0 && k == 0) {  // the values outside the whole vectors
-            const int tail = head + vecs * 8, c = lane < 8 ? lane : tail + lane - 8;
-            if (lane < 8 ? lane < head : lane < 16 && c < p.vocab) {
-                float d = slope(to_f32<T>(row[c]));
-                if (c == at) d += hot;
-                out[c] = from_f32<TO>(d);
-            }
-        } else if (vecs == 0) {
-            const int64_t end = min((int64_t)p.vocab, (k + 1) * kStretch * 8);
-            for (int64_t c = k * kStretch * 8 + lane; c < end; c += 32) {
-                float d = slope(to_f32<T>(row[c]));
-                if (c == at) d += hot;
-                out[c] = from_f32<TO>(d);
+        auto one = [&](int64_t c) {
+            float d = slope(to_f32<T>(row[c]));
+            if (c == at) d += hot;
+            out[c] = from_f32<TO>(d);
+        };
+        if (vecs == 0) {
+            const int64_t end = k + 1 < p.stretches ? (k + 1) * kStretch * 8 : p.vocab;
+            for (int64_t c = k * kStretch * 8 + lane; c < end; c += LANES) one(c);
+        } else if (k == 0) {  // the values outside the whole vectors
+#pragma unroll
+            for (int i = lane; i < 16; i += LANES) {
+                const int c = i < 8 ? i : head + vecs * 8 + i - 8;
+                if (c < (i < 8 ? head : p.vocab)) one(c);
             }
         }
     }
 }
 
+template <class T, class TO, int LANES>
+cudaError_t launch_logprobs_grad(LogGradParams p, cudaStream_t s) {
+    p.stretches = p.vocab < 8 ? 1 : ceil_div<int64_t>(p.vocab / 8, LANES * kFlight);
+    const int64_t blocks = ceil_div<int64_t>(p.rows * p.stretches, kGradThreads / LANES), grid = blocks < kMaxGrid ? blocks : kMaxGrid;
+    return launch_pdl(p.ge ? logprobs_grad_kernel<T, TO, true, LANES> : logprobs_grad_kernel<T, TO, false, LANES>, grid, kGradThreads, 0, s, p);
+}
 template <class T, class TO>
 cudaError_t launch_logprobs_grad(const LogGradParams &p, cudaStream_t s) {
-    const int64_t blocks = ceil_div<int64_t>(p.rows * p.stretches, kGradThreads / 32), grid = blocks < kMaxGrid ? blocks : kMaxGrid;
-    return launch_pdl(p.ge ? logprobs_grad_kernel<T, TO, true> : logprobs_grad_kernel<T, TO, false>, grid, kGradThreads, 0, s, p);
+    return p.vocab <= 520 ? launch_logprobs_grad<T, TO, 8>(p, s) : launch_logprobs_grad<T, TO, 32>(p, s);
 }
 
 bool ids_ok(const void *ids, int id_bytes, int64_t rows) {
@@ -815,7 +822,7 @@ ra_status ra_logprobs_grad(const void *logits, int64_t ld, int dtype, int64_t ro
     for (const Mat &m : in)
         if (mats_overlap(b, m)) return RA_ERR_OVERLAP;
     if (mats_overlap(a, b) && !same_mat(a, b)) return RA_ERR_OVERLAP;
-    const LogGradParams p{logits, ids, lse, entropy, grad_logp, grad_entropy, out, ld, ld_out, rows, ceil_div<int64_t>(vocab, kStretch * 8), (int)vocab, id_bytes, scale,
+    const LogGradParams p{logits, ids, lse, entropy, grad_logp, grad_entropy, out, ld, ld_out, rows, 1, (int)vocab, id_bytes, scale,
                           scale * kLog2e};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == RA_F32) return cuda_status(out_dtype == RA_F32 ? launch_logprobs_grad<float, float>(p, s) : launch_logprobs_grad<float, uint16_t>(p, s));
