@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
     pdl_enter();
     const int parts = CLUSTER ? (int)cluster_blocks() : 1, part = CLUSTER ? (int)cluster_block() : 0;
     if constexpr (CLUSTER) cluster_meet();
-    const int first = CLUSTER ? blockIdx.x / parts : blockIdx.x * kGroups + id, stride = CLUSTER ? gridDim.x / parts : gridDim.x * kGroups, last_row = (int)p.rows;
+    // (below 2^31 rows: no sum of these wraps)
+    const uint32_t first = CLUSTER ? blockIdx.x / parts : blockIdx.x * kGroups + id, stride = CLUSTER ? gridDim.x / parts : gridDim.x * kGroups, last_row = (uint32_t)p.rows;
 
     struct Row {  // where a row's whole vectors begin, how many logits are before them, how many vectors there are
         const T *begin;
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
             return t < 16 && i < (t < 8 ? head : vocab) ? i : -1;
         }
     };
-    auto row_at = [&](int r) {
+    auto row_at = [&](uint32_t r) {
         const T *from = static_cast<const T *>(p.logits) + (int64_t)r * p.ld;
         const int head = min((int)(-(reinterpret_cast<intptr_t>(from) / (int)sizeof(T)) & (kEach - 1)), p.vocab);
         return Row{from + head, head, (p.vocab - head) / kEach};
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
 
     int turn = 0, side = 0;
     const bool finishes = part == 0 && t == 0 && p.logp != nullptr;  // looks after the given token
-    auto fetch_token = [&](int r) {
+    auto fetch_token = [&](uint32_t r) {
         if (!finishes) return;
         const uint32_t to = smem_addr(&room.token[turn]);
         if (p.id_bytes == 8)
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
         fetch_token(first);
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    for (int r = first; r < last_row; r += stride) {
+    for (uint32_t r = first; r < last_row; r += stride) {
         const Row row = row_at(r);
         const int steps = max(1, ceil_div(row.vecs, kTile * parts));
         Share a{-kInf, 0.0f, 0.0f};

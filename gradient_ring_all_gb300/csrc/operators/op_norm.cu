@@ -46,17 +46,18 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
     const bool by_matrix = JOIN && p.gate_kind == RA_GATE_MATRIX;
 
     const int blocks = CLUSTER ? gridDim.x / cluster_blocks() : gridDim.x, block = CLUSTER ? blockIdx.x / cluster_blocks() : blockIdx.x;
-    const int64_t first = (int64_t)block * kGroups + id, step = (int64_t)blocks * kGroups;
+    // (below 2^31 rows: no sum of these wraps)
+    const uint32_t first = block * kGroups + id, step = blocks * kGroups, last = (uint32_t)p.rows;
     const int stage_bytes = norm_places<TX, TF, JOIN>(by_matrix) * kPitch;
     const uint32_t mine = smem_addr(ring) + threadIdx.x * 16;
-    auto fetch = [&](int64_t r, int stage) {
-        if (r < p.rows) {
+    auto fetch = [&](uint32_t r, int stage) {
+        if (r < last) {
             const uint32_t to = mine + stage * stage_bytes;
             if constexpr (JOIN) {
-                copy_own(to, kPitch, static_cast<const TF *>(p.f) + r * p.ld_f, col, count);
-                if (by_matrix) copy_own(to + places<TF, kOwn>() * kPitch, kPitch, static_cast<const TF *>(p.gate) + r * p.ld_gate, col, count);
+                copy_own(to, kPitch, row_of_matrix<WIDE>(static_cast<const TF *>(p.f), p.ld_f, r), col, count);
+                if (by_matrix) copy_own(to + places<TF, kOwn>() * kPitch, kPitch, row_of_matrix<WIDE>(static_cast<const TF *>(p.gate), p.ld_gate, r), col, count);
             }
-            copy_own(to + stage_bytes - places<TX, kOwn>() * kPitch, kPitch, static_cast<const TX *>(p.x) + r * p.ld_x, col, count);
+            copy_own(to + stage_bytes - places<TX, kOwn>() * kPitch, kPitch, row_of_matrix<WIDE>(static_cast<const TX *>(p.x), p.ld_x, r), col, count);
         }
         copies_done();
     };
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
         *rstd = rsqrtf(var + side.eps);
     };
 
-    for (int64_t r = first; r < p.rows; r += step) {
+    for (uint32_t r = first; r < last; r += step) {
         Own<TX, C> x;
         Own<TF, C> f, g;
         const uint32_t at = mine + stage * stage_bytes;
@@ -136,10 +137,10 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
             if constexpr (JOIN) f.take(at, kPitch, count);
             stage = stage == kAhead ? 0 : stage + 1;
         } else {
-            x.load(static_cast<const TX *>(p.x) + r * p.ld_x, col, count);
+            x.load(row_of_matrix<WIDE>(static_cast<const TX *>(p.x), p.ld_x, r), col, count);
             if constexpr (JOIN) {
-                f.load(static_cast<const TF *>(p.f) + r * p.ld_f, col, count);
-                if (by_matrix) g.load(static_cast<const TF *>(p.gate) + r * p.ld_gate, col, count);
+                f.load(row_of_matrix<WIDE>(static_cast<const TF *>(p.f), p.ld_f, r), col, count);
+                if (by_matrix) g.load(row_of_matrix<WIDE>(static_cast<const TF *>(p.gate), p.ld_gate, r), col, count);
             }
         }
         Pair v[kPairs];
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
                 v[j] = pair_fma(alpha, x.two(j), v[j]);
             }
             x.set(v);
-            x.store(static_cast<TX *>(p.x_out) + r * p.ld_x_out, col, count);
+            x.store(row_of_matrix<WIDE>(static_cast<TX *>(p.x_out), p.ld_x_out, r), col, count);
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) {  // the norm is that of the row as stored
                 v[j] = x.two(j);
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) v[j] = pair_fma(pair_add(v[j], off), pair_mul(scale, a_pre[j]), b_pre[j]);
             f.set(v);
-            f.store(static_cast<TF *>(p.h) + r * p.ld_h, col, count);
+            f.store(row_of_matrix<WIDE>(static_cast<TF *>(p.h), p.ld_h, r), col, count);
         }
         if (p.kept != nullptr && col.first == 0) reinterpret_cast<float4 *>(p.kept)[r] = make_float4(m_f, rstd_f, m_x, rstd_x);
     }

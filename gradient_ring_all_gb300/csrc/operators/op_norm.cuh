@@ -40,6 +40,16 @@ __device__ __forceinline__ void load_param(const void *v, bool f32, const C &col
     }
 }
 
+// Row r of a matrix.  WIDE: rows and the bytes between them fit 31 bits each (the
+// host sees to it), so that the place is one multiplication; else 64-bit ones.
+template <bool WIDE, class T>
+__device__ __forceinline__ T *row_of_matrix(T *base, int64_t ld, int64_t r) {
+    if constexpr (WIDE)
+        return reinterpret_cast<T *>(reinterpret_cast<uintptr_t>(base) + (uint64_t)(uint32_t)r * ((uint32_t)ld * (uint32_t)sizeof(T)));
+    else
+        return base + r * ld;
+}
+
 // A thread's values of one row of a matrix as they lie in memory.
 template <class T, class C>
 struct Own {
@@ -147,12 +157,13 @@ inline Side side_of(const ra_norm &n) {
 inline bool types_ok(int x_dtype, int f_dtype) { return esize(x_dtype) != 0 && esize(f_dtype) != 0 && !(x_dtype == RA_BF16 && f_dtype == RA_F32); }
 inline bool sizes_ok(int64_t rows, int64_t d) { return rows >= 0 && d >= 0 && rows < kMaxExtent && d < kMaxExtent; }
 
-// whether every matrix given can be read by vectors of 8
+// whether every matrix given can be read by vectors of 8, its rows' places by 32-bit
+// numbers
 template <int K>
 bool all_wide(const Mat (&m)[K], int64_t d) {
     if (d % 8 != 0) return false;
     for (const Mat &a : m)
-        if (!a.empty() && !a.aligned(16)) return false;
+        if (!a.empty() && (!a.aligned(16) || (a.rows > 1 && a.pitch() >= kMaxExtent))) return false;
     return true;
 }
 

@@ -68,24 +68,25 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
     const bool normed = JOIN && p.post.kind != RA_NORM_NONE;
 
     const int blocks = CLUSTER ? gridDim.x / cluster_blocks() : gridDim.x, block = CLUSTER ? blockIdx.x / cluster_blocks() : blockIdx.x;
-    const int64_t first = (int64_t)block * kGroups + id, step = (int64_t)blocks * kGroups;
+    // (below 2^31 rows: no sum of these wraps)
+    const uint32_t first = block * kGroups + id, step = blocks * kGroups, last = (uint32_t)p.rows;
     // a stage: kept, dh, x, dx_new, f, the gate
     constexpr int kAtDh = kPitch, kAtX = kAtDh + places<TF, kOwn>() * kPitch, kAtNew = kAtX + places<TX, kOwn>() * kPitch,
                   kAtF = kAtNew + places<TX, kOwn>() * kPitch, kAtGate = kAtF + places<TF, kOwn>() * kPitch;
     const int stage_bytes = grad_places<TX, TF, JOIN>(by_matrix) * kPitch;
     const uint32_t mine = smem_addr(ring) + threadIdx.x * 16;
-    auto fetch = [&](int64_t r, int stage) {
-        if (r < p.rows) {
+    auto fetch = [&](uint32_t r, int stage) {
+        if (r < last) {
             const uint32_t to = mine + stage * stage_bytes;
-            if (p.kept != nullptr) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p.kept + r * 4) : "memory");
+            if (p.kept != nullptr) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p.kept + (int64_t)r * 4) : "memory");
             if (has_pre) {
-                copy_own(to + kAtDh, kPitch, static_cast<const TF *>(p.dh) + r * p.ld_dh, col, count);
-                copy_own(to + kAtX, kPitch, static_cast<const TX *>(p.x) + r * p.ld_x, col, count);
+                copy_own(to + kAtDh, kPitch, row_of_matrix<WIDE>(static_cast<const TF *>(p.dh), p.ld_dh, r), col, count);
+                copy_own(to + kAtX, kPitch, row_of_matrix<WIDE>(static_cast<const TX *>(p.x), p.ld_x, r), col, count);
             }
-            if (has_new) copy_own(to + kAtNew, kPitch, static_cast<const TX *>(p.dx_new) + r * p.ld_dx_new, col, count);
+            if (has_new) copy_own(to + kAtNew, kPitch, row_of_matrix<WIDE>(static_cast<const TX *>(p.dx_new), p.ld_dx_new, r), col, count);
             if constexpr (JOIN) {
-                copy_own(to + kAtF, kPitch, static_cast<const TF *>(p.f) + r * p.ld_f, col, count);
-                if (by_matrix) copy_own(to + kAtGate, kPitch, static_cast<const TF *>(p.gate) + r * p.ld_gate, col, count);
+                copy_own(to + kAtF, kPitch, row_of_matrix<WIDE>(static_cast<const TF *>(p.f), p.ld_f, r), col, count);
+                if (by_matrix) copy_own(to + kAtGate, kPitch, row_of_matrix<WIDE>(static_cast<const TF *>(p.gate), p.ld_gate, r), col, count);
             }
         }
         copies_done();
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) acc[a][j] = both(0.0f);
 
-    for (int64_t r = first; r < p.rows; r += step) {
+    for (uint32_t r = first; r < last; r += step) {
         Own<TX, C> x;
         Own<TF, C> h;
         float4 kept = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
             if constexpr (WIDE)
                 to.take(at + place, kPitch, count);
             else
-                to.load(from + r * ld, col, count);
+                to.load(row_of_matrix<WIDE>(from, ld, r), col, count);
         };
         // columns past the row's end hold 0, and add 0 to the sums
 
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) y[j] = pair_mul(full[j], alpha);
             x.set(y);
-            x.store(static_cast<TX *>(p.dx) + r * p.ld_dx, col, count);
+            x.store(row_of_matrix<WIDE>(static_cast<TX *>(p.dx), p.ld_dx, r), col, count);
         }
         if constexpr (JOIN) {
             Own<TF, C> f;
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
                 }
                 if (p.dgate != nullptr) {
                     g.set(dg);
-                    g.store(static_cast<TF *>(p.dgate) + r * p.ld_dgate, col, count);
+                    g.store(row_of_matrix<WIDE>(static_cast<TF *>(p.dgate), p.ld_dgate, r), col, count);
                 }
             }
 #pragma unroll
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
             }
             if (p.df != nullptr) {
                 f.set(full);
-                f.store(static_cast<TF *>(p.df) + r * p.ld_df, col, count);
+                f.store(row_of_matrix<WIDE>(static_cast<TF *>(p.df), p.ld_df, r), col, count);
             }
         }
     }
@@ -261,8 +262,8 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
 }
 
 // The blocks' sums, added in their order, and the gradients they give: a block takes
-// 32 columns, four warps each of the sums, warp w of these the parts w, w + 4, ... with
-// 8 of them in flight.
+// 32 columns, kPartWarps warps each of the sums, warp w of these every kPartWarps-th part
+// from w on, kPartFlight in flight.
 struct PartsParams {
     const float *parts;
     float *dpre_gain, *dpre_bias, *dpost_gain, *dpost_bias, *dgate;
@@ -272,7 +273,7 @@ struct PartsParams {
     bool post_f32, gate_f32;
     float beta;
 };
-constexpr int kPartWarps = 4;
+constexpr int kPartWarps = 8, kPartFlight = 16;
 __global__ void __launch_bounds__(kSumsMost *kPartWarps * 32) parts_kernel(const PartsParams p) {
     __shared__ float sum[kSumsMost][kPartWarps][32];
     pdl_enter();
@@ -282,15 +283,13 @@ __global__ void __launch_bounds__(kSumsMost *kPartWarps * 32) parts_kernel(const
     if (c < p.d && a < p.sums) {
         const float *at = p.parts + a * p.d + c;
         const int64_t pitch = p.sums * p.d;
-        int64_t b = w;
-        for (; b + 7 * kPartWarps < p.count; b += 8 * kPartWarps) {
-            float v[8];
+        for (int64_t b = w; b < p.count; b += kPartFlight * kPartWarps) {
+            float v[kPartFlight];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = at[(b + k * kPartWarps) * pitch];
+            for (int k = 0; k < kPartFlight; ++k) v[k] = b + k * kPartWarps < p.count ? at[(b + k * kPartWarps) * pitch] : 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) s += v[k];
+            for (int k = 0; k < kPartFlight; ++k) s += v[k];
         }
-        for (; b < p.count; b += kPartWarps) s += at[b * pitch];
     }
     sum[a][w][lane] = s;
     __syncthreads();
