@@ -24,47 +24,61 @@ template <class TX, class TF, bool JOIN>
 constexpr int norm_stages() {
     return JOIN && sizeof(TF) == 4 ? 2 : 3;
 }
-// 16-byte places a thread needs for a row
+// bytes a thread needs for a row
 template <class TX, class TF, bool JOIN>
-__host__ __device__ constexpr int norm_places(bool gate_matrix) {
-    return places<TX, kOwn>() + (JOIN ? places<TF, kOwn>() * (gate_matrix ? 2 : 1) : 0);
+__host__ __device__ constexpr int norm_bytes(bool gate_matrix) {
+    return kOwn * (int)(sizeof(TX) + (JOIN ? sizeof(TF) * (gate_matrix ? 2 : 1) : 0));
 }
 
 template <class TX, class TF, bool WIDE, int WARPS, bool JOIN, bool CLUSTER>
 __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 ? 1 : 2) norm_kernel(const NormParams p) {
     constexpr int kThreads = WARPS == 16 ? 512 : kNormThreads, kGroups = kThreads / (WARPS * 32);  // kGroups: rows at a time
-    constexpr int kPitch = kThreads * 16, kAhead = norm_stages<TX, TF, JOIN>() - 1, kPairs = kOwn / 2;
-    using C = Columns<kOwn, WIDE, WARPS, CLUSTER>;
-    __shared__ RowSums<2, WARPS, CLUSTER> sums[kGroups];
+    constexpr int kAhead = norm_stages<TX, TF, JOIN>() - 1, kPairs = kOwn / 2;
+    constexpr int kEach = each_of<TX, TF, WIDE>();
+    constexpr bool kRing = WIDE && !CLUSTER;
+    using C = Columns<kOwn, kEach, WARPS, CLUSTER>;
+    __shared__ RowSums<WARPS, CLUSTER> sums[kGroups];
     extern __shared__ __align__(16) unsigned char ring[];
     pdl_enter();
     if constexpr (CLUSTER) cluster_meet();  // every block is there before another writes to it
     const int id = threadIdx.x / (WARPS * 32);
-    const C col;
-    const int count = col.count(p.d);
+    const C col(p.d);
+    const int count = col.count();
     int turn = 0;
     const bool by_matrix = JOIN && p.gate_kind == RA_GATE_MATRIX;
 
     const int blocks = CLUSTER ? gridDim.x / cluster_blocks() : gridDim.x, block = CLUSTER ? blockIdx.x / cluster_blocks() : blockIdx.x;
     // (below 2^31 rows: no sum of these wraps)
     const uint32_t first = block * kGroups + id, step = blocks * kGroups, last = (uint32_t)p.rows;
-    const int stage_bytes = norm_places<TX, TF, JOIN>(by_matrix) * kPitch;
-    const uint32_t mine = smem_addr(ring) + threadIdx.x * 16;
+    // a stage: f, the gate, x; the threads' pieces of each side by side
+    constexpr int kRowF = kOwn * (int)sizeof(TF) * kThreads, kRowX = kOwn * (int)sizeof(TX) * kThreads;
+    const int stage_bytes = norm_bytes<TX, TF, JOIN>(by_matrix) * kThreads;
+    const uint32_t base = smem_addr(ring), mine_f = base + threadIdx.x * kEach * (int)sizeof(TF), mine_x = base + stage_bytes - kRowX + threadIdx.x * kEach * (int)sizeof(TX);
     auto fetch = [&](uint32_t r, int stage) {
         if (r < last) {
-            const uint32_t to = mine + stage * stage_bytes;
+            const int to = stage * stage_bytes;
             if constexpr (JOIN) {
-                copy_own(to, kPitch, row_of_matrix<WIDE>(static_cast<const TF *>(p.f), p.ld_f, r), col, count);
-                if (by_matrix) copy_own(to + places<TF, kOwn>() * kPitch, kPitch, row_of_matrix<WIDE>(static_cast<const TF *>(p.gate), p.ld_gate, r), col, count);
+                copy_own(mine_f + to, kThreads, row_of_matrix<WIDE>(static_cast<const TF *>(p.f), p.ld_f, r), col, count);
+                if (by_matrix) copy_own(mine_f + to + kRowF, kThreads, row_of_matrix<WIDE>(static_cast<const TF *>(p.gate), p.ld_gate, r), col, count);
             }
-            copy_own(to + stage_bytes - places<TX, kOwn>() * kPitch, kPitch, row_of_matrix<WIDE>(static_cast<const TX *>(p.x), p.ld_x, r), col, count);
+            copy_own(mine_x + to, kThreads, row_of_matrix<WIDE>(static_cast<const TX *>(p.x), p.ld_x, r), col, count);
         }
         copies_done();
     };
+    auto cache = [&](uint32_t r) {
+        if (WARPS == 1 || r >= last) return;
+        cache_own(row_of_matrix<WIDE>(static_cast<const TX *>(p.x), p.ld_x, r), col);
+        if constexpr (JOIN) {
+            cache_own(row_of_matrix<WIDE>(static_cast<const TF *>(p.f), p.ld_f, r), col);
+            if (by_matrix) cache_own(row_of_matrix<WIDE>(static_cast<const TF *>(p.gate), p.ld_gate, r), col);
+        }
+    };
     int stage = 0;
-    if constexpr (WIDE) {
+    if constexpr (kRing) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) fetch(first + k * step, k);
+    } else {
+        cache(first + step);
     }
 
     // post as (v - m) rstd a + b with the gate and beta in a and b, unless the gate
@@ -130,13 +144,14 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
     for (uint32_t r = first; r < last; r += step) {
         Own<TX, C> x;
         Own<TF, C> f, g;
-        const uint32_t at = mine + stage * stage_bytes;
-        if constexpr (WIDE) {
+        const int at = stage * stage_bytes;
+        if constexpr (kRing) {
             fetch(r + kAhead * step, stage == 0 ? kAhead : stage - 1);
             await_copies<kAhead>();
-            if constexpr (JOIN) f.take(at, kPitch, count);
+            if constexpr (JOIN) f.take(mine_f + at, kThreads, count);
             stage = stage == kAhead ? 0 : stage + 1;
         } else {
+            cache(r + 2 * step);
             x.load(row_of_matrix<WIDE>(static_cast<const TX *>(p.x), p.ld_x, r), col, count);
             if constexpr (JOIN) {
                 f.load(row_of_matrix<WIDE>(static_cast<const TF *>(p.f), p.ld_f, r), col, count);
@@ -150,9 +165,9 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
             for (int j = 0; j < kPairs; ++j) v[j] = f.two(j);
             const bool normed = p.post.kind != RA_NORM_NONE;
             if (normed) moments(v, p.post, &m_f, &rstd_f);
-            if constexpr (WIDE) {
-                if (by_matrix) g.take(at + places<TF, kOwn>() * kPitch, kPitch, count);
-                x.take(at + stage_bytes - places<TX, kOwn>() * kPitch, kPitch, count);
+            if constexpr (kRing) {
+                if (by_matrix) g.take(mine_f + at + kRowF, kThreads, count);
+                x.take(mine_x + at, kThreads, count);
             }
             const Pair scale = both(normed ? rstd_f : 1.0f), off = both(-m_f), alpha = both(p.alpha);
 #pragma unroll
@@ -169,7 +184,7 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
                 if (!WIDE || kOwn > 8) v[j] = pair(2 * j < count ? x[2 * j] : 0.0f, 2 * j + 1 < count ? x[2 * j + 1] : 0.0f);
             }
         } else {
-            if constexpr (WIDE) x.take(at, kPitch, count);
+            if constexpr (kRing) x.take(mine_x + at, kThreads, count);
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) v[j] = x.two(j);
         }
@@ -193,11 +208,11 @@ cudaError_t launch_norm(const NormParams &p, bool wide, cudaStream_t s) {
         constexpr bool kCluster = decltype(cluster)::value != 0;
         const int64_t grid = sh.shares(p.rows) * sh.cluster;
         if (!wide) return launch_clusters(norm_kernel<TX, TF, false, kWarps, JOIN, kCluster>, grid, sh.cluster, sh.threads(), 0, s, p);
-        const int place = norm_stages<TX, TF, JOIN>() * 16 * sh.threads();
-        const cudaError_t e = opt_in_smem<norm_kernel<TX, TF, true, kWarps, JOIN, kCluster>>(place * norm_places<TX, TF, JOIN>(JOIN));
+        const int rows = kCluster ? 0 : norm_stages<TX, TF, JOIN>() * sh.threads();
+        const cudaError_t e = opt_in_smem<norm_kernel<TX, TF, true, kWarps, JOIN, kCluster>>(rows * norm_bytes<TX, TF, JOIN>(JOIN));
         if (e != cudaSuccess) return e;
         return launch_clusters(norm_kernel<TX, TF, true, kWarps, JOIN, kCluster>, grid, sh.cluster, sh.threads(),
-                               place * norm_places<TX, TF, JOIN>(p.gate_kind == RA_GATE_MATRIX), s, p);
+                               rows * norm_bytes<TX, TF, JOIN>(p.gate_kind == RA_GATE_MATRIX), s, p);
     });
 }
 

@@ -8,6 +8,12 @@ namespace op {
 
 constexpr int kNormThreads = 256;  // of a block, unless a row takes more
 
+// neighbours a thread takes at a time: 16 bytes of the wider of two types
+template <class TX, class TF, bool WIDE>
+constexpr int each_of() {
+    return !WIDE ? 1 : sizeof(TX) == 4 || sizeof(TF) == 4 ? 4 : 8;
+}
+
 // A norm as the kernels take it.
 struct Side {
     const void *gain, *bias;
@@ -16,18 +22,26 @@ struct Side {
     bool f32;
 };
 
-// The columns of a thread, OWN of them: 8 neighbours at a time (WIDE: rows on
+// The columns of a thread, OWN of them: EACH neighbours at a time (WIDE: rows on
 // 16-byte boundaries, d a multiple of 8), or single ones that are the row's threads
-// apart.
-template <int OWN, bool WIDE, int WARPS, bool CLUSTER>
+// apart.  EACH is 16 bytes of the wider type, so that the lanes' accesses lie side by
+// side: with 8 of binary32 8192 rows of 2048 took 66 us forward and 138 backward,
+// with 4 they take 48 and 97.  The blocks of a cluster have equal shares.
+template <int OWN, int EACH, int WARPS, bool CLUSTER>
 struct Columns {
-    static constexpr int kThreads = WARPS * 32, kOwn = OWN, kEach = WIDE ? 8 : 1, kParts = OWN / kEach;
-    int first;
-    __device__ __forceinline__ Columns()
-        : first((CLUSTER ? (int)cluster_block() * kThreads * OWN : 0) + (int)threadIdx.x % kThreads * kEach) {}
+    static constexpr int kThreads = WARPS * 32, kOwn = OWN, kEach = EACH, kParts = OWN / kEach;
+    int begin, end, first;  // of the block, and the thread's first
+    __device__ __forceinline__ explicit Columns(int d) : begin(0), end(d) {
+        if constexpr (CLUSTER) {
+            const int share = ceil_div(d, 8 * (int)cluster_blocks()) * 8;
+            begin = (int)cluster_block() * share;
+            end = min(d, begin + share);
+        }
+        first = begin + (int)threadIdx.x % kThreads * kEach;
+    }
     __device__ __forceinline__ int operator[](int j) const { return first + j / kEach * (kEach * kThreads) + j % kEach; }
-    // how many of them are within a row of d
-    __device__ __forceinline__ int count(int d) const { return max(0, min(kParts, ceil_div(d - first, kEach * kThreads))) * kEach; }
+    // how many of them are within the block's share
+    __device__ __forceinline__ int count() const { return max(0, min(kParts, ceil_div(end - first, kEach * kThreads))) * kEach; }
 };
 
 // a thread's values of a vector of parameters, `none` where there is no vector
@@ -65,17 +79,17 @@ struct Own {
         }
     }
     // from the thread's own places in shared memory
-    __device__ __forceinline__ void take(uint32_t shared, int pitch, int count) {
-        static_assert(C::kEach == 8, "take");
+    __device__ __forceinline__ void take(uint32_t shared, int threads, int count) {
+        constexpr int kBytes = C::kEach * (int)sizeof(T);
 #pragma unroll
         for (int i = 0; i < C::kParts; ++i) {
             v[i].zero();
-            if (i * 8 < count) {
-#pragma unroll
-                for (int k = 0; k < (int)sizeof(T) / 2; ++k)
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(v[i].w[4 * k]), "=r"(v[i].w[4 * k + 1]), "=r"(v[i].w[4 * k + 2]), "=r"(v[i].w[4 * k + 3])
-                                 : "r"(shared + (i * ((int)sizeof(T) / 2) + k) * pitch) : "memory");
+            if (i * C::kEach < count) {
+                const uint32_t at = shared + i * threads * kBytes;
+                if constexpr (kBytes == 16)
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[i].w[0]), "=r"(v[i].w[1]), "=r"(v[i].w[2]), "=r"(v[i].w[3]) : "r"(at) : "memory");
+                else
+                    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[i].w[0]), "=r"(v[i].w[1]) : "r"(at) : "memory");
             }
         }
     }
@@ -88,8 +102,8 @@ struct Own {
             if constexpr (sizeof(T) == 4) {
                 v[j / C::kEach].w[j % C::kEach] = __float_as_uint(a);
                 v[(j + 1) / C::kEach].w[(j + 1) % C::kEach] = __float_as_uint(b);
-            } else if constexpr (C::kEach == 8) {
-                v[j / 8].w[j % 8 / 2] = pack2(a, b);
+            } else if constexpr (C::kEach > 1) {
+                v[j / C::kEach].w[j % C::kEach / 2] = pack2(a, b);
             } else {
                 const uint32_t w = pack2(a, b);
                 v[j].w[0] = w & 0xffffu;
@@ -102,10 +116,10 @@ struct Own {
         for (int i = 0; i < C::kParts; ++i) {
             if (i * C::kEach >= count) continue;
             T *to = row + col[i * C::kEach];
-            if constexpr (C::kEach == 8) {
-#pragma unroll
-                for (int k = 0; k < (int)sizeof(T) / 2; ++k)
-                    reinterpret_cast<uint4 *>(to)[k] = make_uint4(v[i].w[4 * k], v[i].w[4 * k + 1], v[i].w[4 * k + 2], v[i].w[4 * k + 3]);
+            if constexpr (C::kEach * sizeof(T) == 16) {
+                *reinterpret_cast<uint4 *>(to) = make_uint4(v[i].w[0], v[i].w[1], v[i].w[2], v[i].w[3]);
+            } else if constexpr (C::kEach > 1) {
+                *reinterpret_cast<uint2 *>(to) = make_uint2(v[i].w[0], v[i].w[1]);
             } else if constexpr (sizeof(T) == 4) {
                 *to = __uint_as_float(v[i].w[0]);
             } else {
@@ -116,22 +130,29 @@ struct Own {
 };
 
 // Rows read ahead (WIDE): every thread copies its own values of the next rows
-// asynchronously to places of its own in shared memory, 16 bytes each, kThreads
-// places apart, and reads them from there: nobody waits for another's copies.
-template <class T, int OWN>
-__host__ __device__ constexpr int places() {  // of a thread's values of a row
-    return OWN / 8 * (int)sizeof(T) / 2;
-}
-// one vector of 8 values after another; returns the place behind them
+// asynchronously to places of its own in shared memory, beside the other threads',
+// and reads them from there: nobody waits for another's copies.
 template <class T, class C>
-__device__ __forceinline__ void copy_own(uint32_t to, int pitch, const T *row, const C &col, int count) {
+__device__ __forceinline__ void copy_own(uint32_t to, int threads, const T *row, const C &col, int count) {
+    constexpr int kBytes = C::kEach * (int)sizeof(T);
 #pragma unroll
     for (int i = 0; i < C::kParts; ++i)
-#pragma unroll
-        for (int k = 0; k < (int)sizeof(T) / 2; ++k)
-            if (i * 8 < count)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + (i * ((int)sizeof(T) / 2) + k) * pitch), "l"(row + col[i * 8] + k * (16 / (int)sizeof(T)))
-                             : "memory");
+        if (i * C::kEach < count) {
+            if constexpr (kBytes == 16)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * threads * kBytes), "l"(row + col[i * C::kEach]) : "memory");
+            else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to + i * threads * kBytes), "l"(row + col[i * C::kEach]) : "memory");
+        }
+}
+// Other rows, and a cluster's: only into the L2 cache, a line of 128 bytes a thread
+// (8192 rows of 2047 bf16 backward: 136 us without, 95 with; rows of one warp, 18 and
+// 19 at 250 columns, go without).  A cluster's blocks meet once a sum, and a meeting
+// waits for the copies under way: with them 2048 rows of 8192 bf16 took 125 us
+// backward, and 87 without a join, with this 107 and 59.
+template <class T, class C>
+__device__ __forceinline__ void cache_own(const T *row, const C &col) {
+    const int at = col.begin + (int)threadIdx.x % C::kThreads * (128 / (int)sizeof(T));
+    if (at < col.end) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + at) : "memory");
 }
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int LEFT>
@@ -174,13 +195,16 @@ struct Shape {
     int warps, cluster;
     Shape(int64_t d, int own) : warps(1), cluster(1) {
         while (warps < 16 && warps * 32 * own < d) warps *= 2;
-        while (cluster < kMostBlocks && (int64_t)cluster * 512 * own < d) cluster *= 2;
+        cluster = (int)ceil_div<int64_t>(d, warps * 32 * own);
     }
     int64_t groups() const { return warps * 32 < kNormThreads ? kNormThreads / (warps * 32) : 1; }
     int threads() const { return warps * 32 < kNormThreads ? kNormThreads : warps * 32; }
-    // blocks, or clusters, that share the rows: two blocks of 256 an SM, or one of 512
+    // blocks, or clusters, that share the rows: as many as run at once, with two blocks
+    // of 256 an SM or one of 512 (what the occupancy query gives for clusters, which
+    // stay within a GPC's SMs)
     int64_t shares(int64_t rows) const {
-        const int64_t most = 152 * (warps == 16 ? 1 : 2) / cluster, blocks = ceil_div<int64_t>(rows, groups());
+        constexpr int kClusters[kMostBlocks] = {152, 76, 46, 36, 28, 23, 15, 15};
+        const int64_t most = warps == 16 ? kClusters[cluster - 1] : 304, blocks = ceil_div<int64_t>(rows, groups());
         return blocks < most ? blocks : most;
     }
 };

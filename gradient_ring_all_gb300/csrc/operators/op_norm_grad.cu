@@ -17,11 +17,17 @@ enum { kDhUnit, kDh, kDUnit, kD, kSumsMost };
 // A thread's values of a vector of parameters.
 template <class C>
 __device__ __forceinline__ void load_vector(const void *v, bool f32, const C &col, int count, float none, float (&out)[kOwn]) {
-    if (v != nullptr && count > 0 && C::kEach == 8 && reinterpret_cast<uintptr_t>(v) % 16 == 0) {
-        if (f32)
-            load_w<float, kOwn>(static_cast<const float *>(v) + col.first, out);
-        else
-            load_w<uint16_t, kOwn>(static_cast<const uint16_t *>(v) + col.first, out);
+    if (v != nullptr && count == kOwn && C::kEach > 1 && reinterpret_cast<uintptr_t>(v) % 16 == 0) {
+#pragma unroll
+        for (int i = 0; i < C::kParts; ++i) {
+            float w[C::kEach];
+            if (f32)
+                load_w<float, C::kEach>(static_cast<const float *>(v) + col[i * C::kEach], w);
+            else
+                load_w<uint16_t, C::kEach>(static_cast<const uint16_t *>(v) + col[i * C::kEach], w);
+#pragma unroll
+            for (int j = 0; j < C::kEach; ++j) out[i * C::kEach + j] = w[j];
+        }
     } else {
         load_param(v, f32, col, count, none, out);
     }
@@ -44,25 +50,27 @@ template <class TX, class TF>
 constexpr int grad_stages() {
     return sizeof(TF) == 4 ? 2 : 3;
 }
-// 16-byte places a thread needs for a row: kept, dh, x, dx_new, f, the gate
+// bytes a thread needs for a row: kept, dh, x, dx_new, f, the gate
 template <class TX, class TF, bool JOIN>
-__host__ __device__ constexpr int grad_places(bool gate_matrix) {
-    return 1 + places<TF, kOwn>() * ((JOIN ? 2 : 1) + (gate_matrix ? 1 : 0)) + 2 * places<TX, kOwn>();
+__host__ __device__ constexpr int grad_bytes(bool gate_matrix) {
+    return 16 + kOwn * (int)(sizeof(TF) * ((JOIN ? 2 : 1) + (gate_matrix ? 1 : 0)) + 2 * sizeof(TX));
 }
 
 template <class TX, class TF, bool WIDE, int WARPS, bool JOIN, bool CLUSTER>
 __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 ? 1 : 2) norm_grad_kernel(const NormGradParams p) {
     constexpr int kThreads = WARPS == 16 ? 512 : kNormThreads, kGroups = kThreads / (WARPS * 32), kSums = JOIN ? kSumsMost : 2;
-    constexpr int kPitch = kThreads * 16, kAhead = grad_stages<TX, TF>() - 1, kPairs = kOwn / 2;
-    using C = Columns<kOwn, WIDE, WARPS, CLUSTER>;
-    __shared__ RowSums<2, WARPS, CLUSTER> sums[kGroups];
+    constexpr int kAhead = grad_stages<TX, TF>() - 1, kPairs = kOwn / 2;
+    constexpr int kEach = each_of<TX, TF, WIDE>();
+    constexpr bool kRing = WIDE && !CLUSTER;
+    using C = Columns<kOwn, kEach, WARPS, CLUSTER>;
+    __shared__ RowSums<WARPS, CLUSTER> sums[kGroups];
     __shared__ float joined[kGroups > 1 ? WARPS * 32 * kOwn : 1];
     extern __shared__ __align__(16) unsigned char ring[];
     pdl_enter();
     if constexpr (CLUSTER) cluster_meet();
     const int id = threadIdx.x / (WARPS * 32);
-    const C col;
-    const int count = col.count(p.d);
+    const C col(p.d);
+    const int count = col.count();
     int turn = 0;
     const bool by_matrix = JOIN && p.gate_kind == RA_GATE_MATRIX, has_pre = p.dh != nullptr, has_new = p.dx_new != nullptr;
     const bool normed = JOIN && p.post.kind != RA_NORM_NONE;
@@ -70,31 +78,47 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
     const int blocks = CLUSTER ? gridDim.x / cluster_blocks() : gridDim.x, block = CLUSTER ? blockIdx.x / cluster_blocks() : blockIdx.x;
     // (below 2^31 rows: no sum of these wraps)
     const uint32_t first = block * kGroups + id, step = blocks * kGroups, last = (uint32_t)p.rows;
-    // a stage: kept, dh, x, dx_new, f, the gate
-    constexpr int kAtDh = kPitch, kAtX = kAtDh + places<TF, kOwn>() * kPitch, kAtNew = kAtX + places<TX, kOwn>() * kPitch,
-                  kAtF = kAtNew + places<TX, kOwn>() * kPitch, kAtGate = kAtF + places<TF, kOwn>() * kPitch;
-    const int stage_bytes = grad_places<TX, TF, JOIN>(by_matrix) * kPitch;
-    const uint32_t mine = smem_addr(ring) + threadIdx.x * 16;
+    // a stage: kept, dh, x, dx_new, f, the gate; the threads' pieces of each side by side
+    constexpr int kRowF = kOwn * (int)sizeof(TF) * kThreads, kRowX = kOwn * (int)sizeof(TX) * kThreads;
+    constexpr int kAtDh = 16 * kThreads, kAtX = kAtDh + kRowF, kAtNew = kAtX + kRowX, kAtF = kAtNew + kRowX, kAtGate = kAtF + kRowF;
+    const int stage_bytes = grad_bytes<TX, TF, JOIN>(by_matrix) * kThreads;
+    const uint32_t base = smem_addr(ring), mine = base + threadIdx.x * 16, mine_f = base + threadIdx.x * kEach * (int)sizeof(TF),
+                   mine_x = base + threadIdx.x * kEach * (int)sizeof(TX);
     auto fetch = [&](uint32_t r, int stage) {
         if (r < last) {
-            const uint32_t to = mine + stage * stage_bytes;
-            if (p.kept != nullptr) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p.kept + (int64_t)r * 4) : "memory");
+            const int to = stage * stage_bytes;
+            if (p.kept != nullptr) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(mine + to), "l"(p.kept + (int64_t)r * 4) : "memory");
             if (has_pre) {
-                copy_own(to + kAtDh, kPitch, row_of_matrix<WIDE>(static_cast<const TF *>(p.dh), p.ld_dh, r), col, count);
-                copy_own(to + kAtX, kPitch, row_of_matrix<WIDE>(static_cast<const TX *>(p.x), p.ld_x, r), col, count);
+                copy_own(mine_f + to + kAtDh, kThreads, row_of_matrix<WIDE>(static_cast<const TF *>(p.dh), p.ld_dh, r), col, count);
+                copy_own(mine_x + to + kAtX, kThreads, row_of_matrix<WIDE>(static_cast<const TX *>(p.x), p.ld_x, r), col, count);
             }
-            if (has_new) copy_own(to + kAtNew, kPitch, row_of_matrix<WIDE>(static_cast<const TX *>(p.dx_new), p.ld_dx_new, r), col, count);
+            if (has_new) copy_own(mine_x + to + kAtNew, kThreads, row_of_matrix<WIDE>(static_cast<const TX *>(p.dx_new), p.ld_dx_new, r), col, count);
             if constexpr (JOIN) {
-                copy_own(to + kAtF, kPitch, row_of_matrix<WIDE>(static_cast<const TF *>(p.f), p.ld_f, r), col, count);
-                if (by_matrix) copy_own(to + kAtGate, kPitch, row_of_matrix<WIDE>(static_cast<const TF *>(p.gate), p.ld_gate, r), col, count);
+                copy_own(mine_f + to + kAtF, kThreads, row_of_matrix<WIDE>(static_cast<const TF *>(p.f), p.ld_f, r), col, count);
+                if (by_matrix) copy_own(mine_f + to + kAtGate, kThreads, row_of_matrix<WIDE>(static_cast<const TF *>(p.gate), p.ld_gate, r), col, count);
             }
         }
         copies_done();
     };
+    auto cache = [&](uint32_t r) {
+        if (WARPS == 1 || r >= last) return;
+        if (has_pre) {
+            cache_own(row_of_matrix<WIDE>(static_cast<const TF *>(p.dh), p.ld_dh, r), col);
+            cache_own(row_of_matrix<WIDE>(static_cast<const TX *>(p.x), p.ld_x, r), col);
+        }
+        if (has_new) cache_own(row_of_matrix<WIDE>(static_cast<const TX *>(p.dx_new), p.ld_dx_new, r), col);
+        if constexpr (JOIN) {
+            cache_own(row_of_matrix<WIDE>(static_cast<const TF *>(p.f), p.ld_f, r), col);
+            if (by_matrix) cache_own(row_of_matrix<WIDE>(static_cast<const TF *>(p.gate), p.ld_gate, r), col);
+        }
+    };
     int stage = 0;
-    if constexpr (WIDE) {
+    if constexpr (kRing) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) fetch(first + k * step, k);
+    } else {
+        cache(first);
+        cache(first + step);
     }
 
     // pre's gain; and beta times the gate times post's gain (without a matrix's gate)
@@ -120,19 +144,20 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
         Own<TX, C> x;
         Own<TF, C> h;
         float4 kept = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const uint32_t at = mine + stage * stage_bytes;
-        if constexpr (WIDE) {
+        const int at = stage * stage_bytes;
+        if constexpr (kRing) {
             fetch(r + kAhead * step, stage == 0 ? kAhead : stage - 1);
             await_copies<kAhead>();
-            if (p.kept != nullptr) asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(kept.x), "=f"(kept.y), "=f"(kept.z), "=f"(kept.w) : "r"(at) : "memory");
+            if (p.kept != nullptr) asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(kept.x), "=f"(kept.y), "=f"(kept.z), "=f"(kept.w) : "r"(mine + at) : "memory");
             stage = stage == kAhead ? 0 : stage + 1;
-        } else if (p.kept != nullptr) {
-            kept = reinterpret_cast<const float4 *>(p.kept)[r];
+        } else {
+            cache(r + 2 * step);
+            if (p.kept != nullptr) kept = reinterpret_cast<const float4 *>(p.kept)[r];
         }
         // the rest of a row's values, where they are needed
         auto read = [&](auto &to, const auto *from, int64_t ld, int place) {
-            if constexpr (WIDE)
-                to.take(at + place, kPitch, count);
+            if constexpr (kRing)
+                to.take((place == kAtX || place == kAtNew ? mine_x : mine_f) + at + place, kThreads, count);
             else
                 to.load(row_of_matrix<WIDE>(from, ld, r), col, count);
         };
@@ -252,7 +277,13 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
             __syncthreads();
             for (int c = threadIdx.x; c < p.d; c += kThreads) part[(int64_t)a * p.d + c] = joined[c];
         } else if constexpr (WIDE) {
-            if (count > 0) store_w<float, kOwn>(part + (int64_t)a * p.d + col.first, v);
+#pragma unroll
+            for (int i = 0; i < C::kParts; ++i) {
+                float w[C::kEach];
+#pragma unroll
+                for (int j = 0; j < C::kEach; ++j) w[j] = v[i * C::kEach + j];
+                if (i * C::kEach < count) store_w<float, C::kEach>(part + (int64_t)a * p.d + col[i * C::kEach], w);
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < kOwn; ++j)
@@ -329,11 +360,11 @@ cudaError_t launch_grad(const NormGradParams &p, bool wide, cudaStream_t s) {
         constexpr bool kCluster = decltype(cluster)::value != 0;
         const int64_t grid = grad_parts(p.rows, p.d) * sh.cluster;
         if (!wide) return launch_clusters(norm_grad_kernel<TX, TF, false, kWarps, JOIN, kCluster>, grid, sh.cluster, sh.threads(), 0, s, p);
-        const int place = grad_stages<TX, TF>() * 16 * sh.threads();
-        const cudaError_t e = opt_in_smem<norm_grad_kernel<TX, TF, true, kWarps, JOIN, kCluster>>(place * grad_places<TX, TF, JOIN>(JOIN));
+        const int rows = kCluster ? 0 : grad_stages<TX, TF>() * sh.threads();
+        const cudaError_t e = opt_in_smem<norm_grad_kernel<TX, TF, true, kWarps, JOIN, kCluster>>(rows * grad_bytes<TX, TF, JOIN>(JOIN));
         if (e != cudaSuccess) return e;
         return launch_clusters(norm_grad_kernel<TX, TF, true, kWarps, JOIN, kCluster>, grid, sh.cluster, sh.threads(),
-                               place * grad_places<TX, TF, JOIN>(p.gate_kind == RA_GATE_MATRIX), s, p);
+                               rows * grad_bytes<TX, TF, JOIN>(p.gate_kind == RA_GATE_MATRIX), s, p);
     });
 }
 

@@ -39,20 +39,18 @@ __device__ __forceinline__ void group_meet(int id) {
         asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "n"(WARPS * 32) : "memory");
 }
 
-// Sums over a row that WARPS warps hold, or the blocks of a cluster with WARPS
-// warps each (CLUSTER).  Lanes are added by shuffles, warps and blocks in their
-// order, so a sum has one order and every thread the same result.  Two sets of
-// places take turns: whoever writes a set again has met the others after they
-// read it.
-template <int K, int WARPS, bool CLUSTER>
+// Two sums over a row that WARPS warps hold, or the blocks of a cluster with WARPS
+// warps each (CLUSTER).  Lanes are added by shuffles, then the warps' sums, which
+// every warp writes to every block, by each thread in one order: a sum has one value
+// in all of them.  Two sets of places take turns: whoever writes a set again has met
+// the others after they read it.
+template <int WARPS, bool CLUSTER>
 struct RowSums {
-    float warp[2][K][WARPS];
-    float block[CLUSTER ? 2 : 1][K][CLUSTER ? kMostBlocks : 1];
+    alignas(16) float warp[2][2][CLUSTER ? kMostBlocks : 1][WARPS];
 };
 
-template <int K, int WARPS, bool CLUSTER>
-__device__ __forceinline__ void row_sum(float (&v)[K], RowSums<K, WARPS, CLUSTER> &at, int id, int &turn) {
-    static_assert(K == 2, "two sums");
+template <int WARPS, bool CLUSTER>
+__device__ __forceinline__ void row_sum(float (&v)[2], RowSums<WARPS, CLUSTER> &at, int id, int &turn) {
     // the half warps trade one sum for the other, and each half adds up its own
     const int lane = threadIdx.x & 31;
     const float give = lane < 16 ? v[1] : v[0];
@@ -62,30 +60,40 @@ __device__ __forceinline__ void row_sum(float (&v)[K], RowSums<K, WARPS, CLUSTER
     if constexpr (WARPS == 1) {
         v[0] = __shfl_sync(0xffffffffu, own, 0);
         v[1] = __shfl_sync(0xffffffffu, own, 16);
+        return;
     }
-    if constexpr (WARPS > 1) {
-        if (lane % 16 == 0) at.warp[turn][lane / 16][threadIdx.x % (WARPS * 32) / 32] = own;
-        group_meet<WARPS>(id);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            v[k] = at.warp[turn][k][0];
-#pragma unroll
-            for (int w = 1; w < WARPS; ++w) v[k] += at.warp[turn][k][w];
-        }
-    }
+    const int w = threadIdx.x % (WARPS * 32) / 32;
+    uint32_t blocks = 1;
     if constexpr (CLUSTER) {
-        const uint32_t blocks = cluster_blocks();
-        if (threadIdx.x < blocks) {
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(place_in(&at.block[turn][k][cluster_block()], threadIdx.x)), "f"(v[k]) : "memory");
-        }
+        blocks = cluster_blocks();
+        if (lane % 16 < blocks)
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(place_in(&at.warp[turn][lane / 16][cluster_block()][w], lane % 16)), "f"(own) : "memory");
         cluster_meet();
+    } else {
+        if (lane % 16 == 0) at.warp[turn][lane / 16][0][w] = own;
+        group_meet<WARPS>(id);
+    }
+    constexpr int kEach = WARPS < 4 ? WARPS : 4;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            v[k] = at.block[turn][k][0];
-            for (uint32_t b = 1; b < blocks; ++b) v[k] += at.block[turn][k][b];
-        }
+    for (int k = 0; k < 2; ++k) {
+        float s[kEach] = {};
+#pragma unroll 1
+        for (uint32_t b = 0; b < blocks; ++b)
+#pragma unroll
+            for (int i = 0; i < WARPS; i += kEach) {
+                const float *from = &at.warp[turn][k][CLUSTER ? b : 0][i];
+                if constexpr (kEach == 4) {
+                    const float4 q = *reinterpret_cast<const float4 *>(from);
+                    s[0] += q.x;
+                    s[1] += q.y;
+                    s[2] += q.z;
+                    s[3] += q.w;
+                } else {
+                    s[0] += from[0];
+                    s[1] += from[1];
+                }
+            }
+        v[k] = kEach == 4 ? (s[0] + s[1]) + (s[kEach - 2] + s[kEach - 1]) : s[0] + s[1];
     }
     turn ^= 1;
 }
