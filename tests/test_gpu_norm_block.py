@@ -114,6 +114,16 @@ def test_layouts(d, lead, gap, stream, block):
         c.check_backward(x, kept)
 
 
+@pytest.mark.parametrize("stream,block", TYPES)
+@pytest.mark.parametrize("rows,d", [(300, 4999), (200, 12000), (130, 11999), (70, 24000), (50, 27999), (40, 32760)])
+def test_rows_shared_by_a_cluster(rows, d, stream, block):
+    """Two to eight blocks a row, with several rows each, and columns that do not fill the last block's share."""
+    for kind, gate in (("layer", "vector"), ("rms", "matrix")):
+        c = _Case(rows, d, stream, block, kind, gate)
+        x, _, kept = c.check_forward()
+        c.check_backward(x, kept)
+
+
 def test_parts_that_are_not_there():
     """No post norm, no gate, no gains, no pre norm, no gradient of one side."""
     rows, d = 50, 640
