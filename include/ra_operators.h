@@ -226,7 +226,8 @@ ra_status ra_dropout(const void *x, int64_t ld_x, int x_dtype, int64_t rows, int
 
 /* A norm over a row v of d values: (v - m) * rstd * gain + bias,
  *   m = mean of v (RA_NORM_LAYER) or 0 (RA_NORM_RMS), rstd = (mean of (v - m)^2 + eps)^-1/2.
- * Moments are binary32, the second one of the differences from the first. */
+ * Moments are binary32, the second one of the differences from the first (or of the
+ * values, less m^2, where that costs 4 bits at most). */
 typedef enum { RA_NORM_NONE = 0, RA_NORM_LAYER = 1, RA_NORM_RMS = 2 } ra_norm_kind;
 #define RA_NORM_MAX_D 32768
 
