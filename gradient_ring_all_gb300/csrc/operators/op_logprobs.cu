@@ -141,7 +141,7 @@ constexpr int kMostTop = RA_LOGPROBS_MAX_TOP;
 // other blocks of a cluster send to the first.
 template <int WARPS, bool TOP, bool CLUSTER>
 struct RowRoom {
-    static constexpr int kList = !TOP ? 1 : WARPS == 8 ? 224 : 288;  // what log_blocks leave room for
+    static constexpr int kList = !TOP ? 1 : WARPS == 8 ? 224 : 288;  // what three blocks an SM leave room for
     uint64_t list[WARPS == 8 ? 2 : 1][TOP ? kMostTop + kList : 1];  // rows of fewer warps are one tile
     uint64_t far_list[TOP && CLUSTER ? kMostBlocks * kMostTop : 1];
     uint64_t round[WARPS];
@@ -236,25 +236,28 @@ template <int WARPS>
 constexpr int batch_of() {
     return WARPS == 1 ? 2 : 4;
 }
-template <int WARPS, bool TOP>
-constexpr int log_blocks() {  // resident on an SM
-    return WARPS < 8 && TOP ? 2 : 3;
+constexpr int kLogBlocks = 3;  // resident on an SM, as far as registers go
+// shared memory: the rooms, the batches' largest logits, and a row's `slots` places,
+// which begin where a line does
+template <int WARPS, bool TOP, bool CLUSTER>
+constexpr int log_fixed() {
+    return kLogThreads / (WARPS * 32) * (int)sizeof(RowRoom<WARPS, TOP, CLUSTER>) + (TOP ? kLogThreads * kSlots / batch_of<WARPS>() * 4 : 0);
 }
 template <int WARPS, bool TOP, bool CLUSTER>
-constexpr int log_smem() {
-    return kLogThreads * kSlots * 16 + (TOP ? kLogThreads * kSlots / batch_of<WARPS>() * 4 : 0) + kLogThreads / (WARPS * 32) * (int)sizeof(RowRoom<WARPS, TOP, CLUSTER>);
+constexpr int log_smem(int slots) {
+    return ceil_div(log_fixed<WARPS, TOP, CLUSTER>(), 128) * 128 + kLogThreads * slots * 16;
 }
 
 template <class T, int WARPS, bool TOP, bool CLUSTER>
-__global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprobs_kernel(const LogParams p) {
+__global__ void __launch_bounds__(kLogThreads, kLogBlocks) logprobs_kernel(const LogParams p) {
     using Room = RowRoom<WARPS, TOP, CLUSTER>;
     constexpr int kThreads = WARPS * 32, kGroups = kLogThreads / kThreads, kEach = Vec<T>::kEach, kTile = kThreads * kSlots;  // vectors
-    constexpr int kBatch = batch_of<WARPS>(), kHeights = TOP ? kLogThreads * kSlots / kBatch * 4 : 0;
-    extern __shared__ __align__(16) unsigned char smem[];
+    constexpr int kBatch = batch_of<WARPS>();
+    extern __shared__ __align__(128) unsigned char smem[];
     const int t = threadIdx.x % kThreads, lane = threadIdx.x & 31, warp = t / 32, id = threadIdx.x / kThreads;
-    Room &room = reinterpret_cast<Room *>(smem + kLogThreads * kSlots * 16 + kHeights)[id];
-    const uint32_t heights = smem_addr(smem) + kLogThreads * kSlots * 16 + threadIdx.x * (kSlots / kBatch * 4);  // the largest logit of each batch
-    const uint32_t land = smem_addr(smem) + threadIdx.x * 16;  // the thread's places, kPitch apart
+    Room &room = reinterpret_cast<Room *>(smem)[id];
+    const uint32_t heights = smem_addr(smem) + kGroups * (int)sizeof(Room) + threadIdx.x * (kSlots / kBatch * 4);  // the largest logit of each batch
+    const uint32_t land = smem_addr(smem) + log_smem<WARPS, TOP, CLUSTER>(0) + threadIdx.x * 16;  // the thread's places, kPitch apart
     constexpr int kPitch = kLogThreads * 16;
     if (t < 2) room.count[t] = 0;
     group_meet<WARPS>(id);
@@ -641,11 +644,14 @@ __global__ void __launch_bounds__(kLogThreads, log_blocks<WARPS, TOP>()) logprob
 
 template <class T, int WARPS, bool TOP, bool CLUSTER>
 cudaError_t launch_logprobs(const LogParams &p, int cluster, cudaStream_t s) {
-    constexpr int kBytes = log_smem<WARPS, TOP, CLUSTER>();
-    const cudaError_t e = opt_in_smem<logprobs_kernel<T, WARPS, TOP, CLUSTER>>(kBytes);
+    // a row of one tile has only the places that it needs
+    const int batch = batch_of<WARPS>(), vecs = ceil_div(p.vocab, Vec<T>::kEach), used = ceil_div(ceil_div(vecs, WARPS * 32), batch) * batch;
+    const int bytes = log_smem<WARPS, TOP, CLUSTER>(used < kSlots ? used > batch ? used : batch : kSlots);
+    const cudaError_t e = opt_in_smem<logprobs_kernel<T, WARPS, TOP, CLUSTER>>(log_smem<WARPS, TOP, CLUSTER>(kSlots));
     if (e != cudaSuccess) return e;
-    const int64_t blocks = ceil_div<int64_t>(p.rows, kLogThreads / (WARPS * 32)), most = 152 * log_blocks<WARPS, TOP>() / cluster;
-    return launch_clusters(logprobs_kernel<T, WARPS, TOP, CLUSTER>, (blocks < most ? blocks : most) * cluster, cluster, kLogThreads, kBytes, s, p);
+    const int room = (228 << 10) / (bytes + 1024), resident = room < kLogBlocks ? room : kLogBlocks;
+    const int64_t blocks = ceil_div<int64_t>(p.rows, kLogThreads / (WARPS * 32)), most = 152 * resident / cluster;
+    return launch_clusters(logprobs_kernel<T, WARPS, TOP, CLUSTER>, (blocks < most ? blocks : most) * cluster, cluster, kLogThreads, bytes, s, p);
 }
 
 template <class T, bool TOP>
