@@ -21,6 +21,11 @@ constexpr float kInf = INFINITY;
 // way: no thread waits for another's loads.  Rows of any alignment: the few logits
 // before the first and after the last whole vector are one more value of the first
 // threads.
+//
+// Without alternatives memory bounds it: 8192 x 32000 bf16 82 us (6.4 TB/s), 5 us a row
+// and block, three blocks an SM.  8 alternatives make it 154: their bound, the second
+// look and the order are one after another in a row, in eight warps that meet, and
+// shared memory has room for three rows an SM.
 
 constexpr int kSlots = 16, kLogThreads = 256;
 
@@ -656,10 +661,16 @@ cudaError_t launch_logprobs(const LogParams &p, int cluster, cudaStream_t s) {
 
 template <class T, bool TOP>
 cudaError_t launch_logprobs(const LogParams &p, cudaStream_t s) {
+    // As few warps as hold the row in one tile: more rows are under way at once, and fewer
+    // warps meet (65536 x 1000 bf16: one warp 46 us, two 94, eight 351; 16384 x 4000 27,
+    // 34, 90; 8192 x 8000 two 27, eight 47; 8192 x 8300 four 38, eight 59; x 16000 46, 59;
+    // with 8 alternatives 81, 119).  A few rows lose up to 2 us by it.
     const int vecs = ceil_div(p.vocab, Vec<T>::kEach);
     if (vecs <= 32 * kSlots) return launch_logprobs<T, 1, TOP, false>(p, 1, s);
     if (vecs <= 64 * kSlots) return launch_logprobs<T, 2, TOP, false>(p, 1, s);
-    // few long rows: clusters share a row, while all blocks run at once
+    if (vecs <= 128 * kSlots) return launch_logprobs<T, 4, TOP, false>(p, 1, s);
+    // few long rows: clusters share a row, while all blocks run at once (16 x 131071
+    // binary32 6.5 us, 12.4 a block a row; with 8 alternatives 12 and 28)
     const int64_t tiles = ceil_div(vecs, kLogThreads * kSlots);
     int cluster = 1;
     while (cluster < kMostBlocks && cluster < tiles && p.rows * cluster * 2 <= 152 * 2) cluster *= 2;
@@ -672,8 +683,9 @@ cudaError_t launch_logprobs(const LogParams &p, cudaStream_t s) {
 // d = q (c0 + c1 y) for y = log2 p, q = 2^y, and scale g more at the given token:
 // c0 = -scale (g + e H), c1 = -scale e ln 2.  LANES lanes take a stretch of a row,
 // kFlight vectors of 8 logits a lane: a warp, or for short rows a quarter of one, so
-// that four rows' few numbers and logits are under way at once (65521 x 257 bf16 with
-// the entropy's gradient: 36 us a warp a row, 14 so).
+// that four rows' few numbers and logits are under way at once (65536 x 100 bf16 20 us
+// a warp a row, 8 so; x 257 25 and 14; x 512 29 and 24; from 600 on the same).
+// Memory bounds the long rows: 8192 x 32000 bf16 150 us, 7.0 TB/s.
 
 constexpr int kGradThreads = 256, kFlight = 4;
 

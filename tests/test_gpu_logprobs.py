@@ -150,6 +150,22 @@ def test_non_finite_rows(vocab):
         assert torch.equal(r.top_ids.cpu(), alternatives64(z, 3)) and bool((r.top_ids[1:4] == -1).all())
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,vocab", [(2000, 700), (1500, 6007), (1300, 12001), (900, 20011)])
+def test_several_rows_a_group(rows, vocab, dtype):
+    """One, two, four and eight warps a row, each group with several rows, rows of all alignments."""
+    z = _logits(rows, vocab, dtype, gap=1)
+    for scale, top in ((1.0, 0), (1.1, 8), (0.9, 20), (1.0, 32)):
+        _check(z.t, _ids(rows, vocab), scale, top)
+
+
+@pytest.mark.parametrize("vocab", [6007, 12001])
+def test_four_warps_a_row(vocab):
+    test_rows_with_equal_and_ordered_logits(vocab)
+    test_tokens_that_cannot_be(vocab)
+    test_non_finite_rows(vocab)
+
+
 def test_nothing_to_do():
     z = torch.zeros(4, 10, device="cuda")
     r = ra.ra_logprobs(z[:0], torch.zeros(0, dtype=torch.int64, device="cuda"), entropy=True, top=2)
