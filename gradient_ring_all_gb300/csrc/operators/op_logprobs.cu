@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kLogThreads, kLogBlocks) logprobs_kernel(const
             const uint64_t scale2 = Two(p.scale2).v;
             float most = -kInf, off = 0.0f;  // the largest
             uint32_t low = 0;
-            bool plain = true;
+            bool plain = true, one_by_one = false;
             auto start = [&](float m) {
                 if (a.m == -kInf) a.m = m;
                 const float base = base_of(a.m);
@@ -440,7 +440,8 @@ __global__ void __launch_bounds__(kLogThreads, kLogBlocks) logprobs_kernel(const
                 // y came with what the rounding of `off` leaves, `by`
                 const float by = fmaf(base_of(a.m), p.scale2, -off), sum = s[0] + s[1], f = fmaf(by, -kLn2, 1.0f);
                 const float s_new = fmaf(sum, f, a.s), w_new = fmaf(fmaf(-by, sum, w[0] + w[1]), f, a.w);
-                if (plain && s_new < 1e37f) {
+                one_by_one = !(plain && s_new < 1e37f);
+                if (!one_by_one) {
                     a.s = s_new;
                     a.w = w_new;
                 } else {  // from the largest, one by one (also: logits near the type's ends, NaN)
@@ -488,8 +489,9 @@ __global__ void __launch_bounds__(kLogThreads, kLogBlocks) logprobs_kernel(const
                         const float v = height_at(heights + i * 4);
                         h[i & 1] = fmaxf(h[i & 1], v > lowest ? v : -kInf);  // (the least value stands for any below it)
                     }
+                    // (after the sums made one by one every batch has the lane's largest: one group)
                     key = key_of(h[0]);
-                    other = key_of(h[1]);
+                    other = key_of(one_by_one ? -kInf : h[1]);
                     room.keys[32 + lane] = other;
                 }
                 const int lanes = WARPS == 1 ? 1 : 32 / (kEachWarp * fine);  // of a group
