@@ -360,8 +360,8 @@ __global__ void __launch_bounds__(kLogThreads, kLogBlocks) logprobs_kernel(const
             }
             // y = z scale2 - off.  bf16 logits are held in pairs, before they are taken
             // apart, to a least value whose exponential is 0 (low); beside the lowest
-            // finite ones there is none.  Where that is so the sums are made the other
-            // way below (not plain).  Batches of tokens that cannot be add nothing
+            // finite ones there is none.  Where that is so, or the rounding of off is too
+            // large, the sums are made the other way below (not plain).  Batches of tokens that cannot be add nothing
             // before the first logit to start from.
             uint64_t s2 = Two(0.0f).v, w2 = Two(0.0f).v, off2 = Two(0.0f).v;
             const uint64_t scale2 = Two(p.scale2).v;
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kLogThreads, kLogBlocks) logprobs_kernel(const
                 const float base = base_of(a.m);
                 off = base * p.scale2;
                 off2 = Two(-off).v;
-                plain = fabsf(off) < 1e30f;
+                plain = fabsf(off) < 4096.0f;  // what is left of the first-order factor below is then 4e-9
                 if constexpr (sizeof(T) == 2) {
                     low = floor_bf16x2(base - p.reach);
                     plain = plain && low != 0xff80ff80u && (base - __uint_as_float(low & 0xffff0000u)) * p.scale2 >= -kLeast;
