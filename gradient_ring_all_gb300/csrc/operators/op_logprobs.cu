@@ -14,8 +14,8 @@ constexpr float kInf = INFINITY;
 // forward
 //
 // One pass over the logits: every thread keeps the sums of 2^y and y 2^y relative
-// to one of its logits, and these shares are joined at the row's end.  WARPS warps
-// take a row, in tiles of kSlots 16-byte vectors a thread.  A tile is read
+// to one of its logits, and these shares are joined at the row's end (Growing, Share).
+// WARPS warps take a row, in tiles of kSlots 16-byte vectors a thread.  A tile is read
 // asynchronously into the thread's own places in shared memory; as a place is read
 // from there, the same place of the next tile, of this row or the next, is on its
 // way: no thread waits for another's loads.  Rows of any alignment: the few logits
@@ -35,7 +35,7 @@ struct LogParams {
     int64_t *top_ids;
     int64_t ld, rows;
     int vocab, top, groups, id_bytes;  // groups: the next power of 2 to top
-    float scale, scale2, reach;  // scale2: scale / ln 2; reach: 200 / scale2, beyond which 2^y is 0
+    float scale, scale2, reach, far;  // scale2: scale / ln 2; reach: 200 / scale2, beyond which 2^y is 0; far: kMostBits / scale2
 };
 
 // A logit and its index as a number that orders as the alternatives do: by
@@ -55,13 +55,14 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
 // A share of a row: m one of its logits, s the sum of 2^y, w that of y 2^y, with
 // y = (z - m) scale2 held to at least kLeast, where 2^y is 0 (the exponential
 // flushes what is below 2^-126): so a token that cannot be, or is that far off,
-// adds 0 and no 0 * infinity.  A NaN stays one.  m need not be the largest: the
-// sums are in floating point, and where they grow beyond 1e37 they are made again
-// from the largest.  An empty share has m minus infinity and s = w = 0.
+// adds 0 and no 0 * infinity.  A NaN stays one.  m need not be the largest, but no
+// logit is more than kMostBits above it: no sum can leave binary32, and a share whose
+// m is so far below another's that its factor is 0 is worth less than 2^-60 of the
+// other.  An empty share has m minus infinity and s = w = 0.
 struct Share {
     float m, s, w;
 };
-constexpr float kLeast = -160.0f;
+constexpr float kLeast = -160.0f, kMostBits = 16.0f;
 __device__ __forceinline__ float at_least(float y) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(y), "f"(kLeast));
@@ -138,6 +139,107 @@ __device__ __forceinline__ float largest(const Vec<T> &v) {
     for (int j = 2; j < Vec<T>::kEach; j += 2) m = max3(m, v[j], v[j + 1]);
     return m;
 }
+
+// the largest of a batch, NaN aside (NaN if there is nothing else)
+template <class T, int BATCH>
+__device__ __forceinline__ float largest_of(const Vec<T> (&x)[BATCH]) {
+    if constexpr (sizeof(T) == 2) {
+        uint32_t c[BATCH], m;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            c[i] = x[i].w[0];
+#pragma unroll
+            for (int k = 1; k < 4; ++k) asm("max.bf16x2 %0, %0, %1;" : "+r"(c[i]) : "r"(x[i].w[k]));
+        }
+        m = c[0];
+#pragma unroll
+        for (int i = 1; i < BATCH; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(c[i]));
+        return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    } else {
+        float m = largest(x[0]);
+#pragma unroll
+        for (int i = 1; i < BATCH; ++i) m = max3(max3(m, x[i][0], x[i][1]), x[i][2], x[i][3]);
+        return m;
+    }
+}
+
+// A thread's share of a row as it grows: the logit m that its sums are relative to, and
+// the tile's sums in pairs.  A batch with a logit above `above` first makes its largest
+// the m (so does the first batch: m begins as minus infinity), which scales what has
+// been summed.  So a finite mask costs little more than minus infinity: 8192 x 32000
+// bf16 with the first half at the type's lowest value take 92 us, at minus infinity 84,
+// unmasked 84.  (The warp's largest as the first m would take 84 and not 113 where 95 %
+// at random are at -10^4, and ordinary rows 1 to 2 % more; to look at a batch's sums
+// instead of its largest logit takes 87.)
+//
+// y = (z - m) scale2.  Where m allows it (near) two bf16 logits take one instruction
+// less, and their bounds one less (84 us; 91 without; binary32 gains nothing by it):
+// y = z scale2 - off, off the rounded m scale2, below 2^12, so that what the rounding
+// left (`by`, at most 2^-13) goes out of the sums by its first-order factor, within
+// 4e-9; and logits are held in pairs, before they are taken apart, to a least value
+// whose exponential is 0 (low), which there is unless m is next to the type's lowest.
+template <class T>
+struct Growing {
+    float m, above;
+    Pair s2, w2, minus;
+    uint32_t low;
+    bool near;
+    __device__ __forceinline__ explicit Growing(const LogParams &p) : s2(pair(0.0f, 0.0f)), w2(pair(0.0f, 0.0f)) { from(-kInf, p); }
+    __device__ __forceinline__ void from(float logit, const LogParams &p) {
+        m = logit;
+        above = m == -kInf ? m : fminf(m + p.far, 3.402823466e38f);  // plus infinity is above any
+        const float base = base_of(m), off = base * p.scale2;
+        near = false;
+        if constexpr (sizeof(T) == 2) {
+            low = floor_bf16x2(base - p.reach);
+            near = fabsf(off) < 4096.0f && low != 0xff80ff80u && (base - __uint_as_float(low & 0xffff0000u)) * p.scale2 >= -kLeast;
+        }
+        minus = both(near ? -off : -base);
+    }
+    __device__ __forceinline__ float by(const LogParams &p) const {
+        float off, same;
+        apart(minus, off, same);
+        return near ? fmaf(base_of(m), p.scale2, off) : 0.0f;
+    }
+    // former: the sums of the tiles before, or null
+    __device__ __forceinline__ void move(float logit, const LogParams &p, volatile float *former) {
+        const float y = at_least(fmaf(m - logit, p.scale2, -by(p))), f = fast_exp2(y);
+        w2 = pair_mul(both(f), pair_fma(both(y), s2, w2));
+        s2 = pair_mul(both(f), s2);
+        if (former != nullptr) {
+            former[1] = f * fmaf(y, former[0], former[1]);
+            former[0] = f * former[0];
+        }
+        from(logit, p);
+    }
+    template <bool NEAR, int BATCH>
+    __device__ __forceinline__ void add(Vec<T> (&x)[BATCH], Pair scale2) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+#pragma unroll
+            for (int j = 0; j < Vec<T>::kEach; j += 2) {
+                if constexpr (NEAR) x[i].w[j / 2] = larger_nan(x[i].w[j / 2], low);
+                const Pair z = pair(x[i][j], x[i][j + 1]);
+                Pair y = NEAR ? pair_fma(z, scale2, minus) : pair_mul(pair_add(z, minus), scale2);
+                float y0, y1;
+                apart(y, y0, y1);
+                if constexpr (!NEAR) {
+                    y0 = at_least(y0);
+                    y1 = at_least(y1);
+                    y = pair(y0, y1);
+                }
+                const Pair e = pair(fast_exp2(y0), fast_exp2(y1));
+                s2 = pair_add(s2, e);
+                w2 = pair_fma(e, y, w2);
+            }
+        }
+    }
+    // with the sums in whole
+    __device__ __forceinline__ Share share(const LogParams &p, float s, float w) const {
+        const float left = by(p), f = fmaf(left, -kLn2, 1.0f);
+        return Share{m, s * f, fmaf(-left, s, w) * f};
+    }
+};
 
 constexpr int kMostTop = RA_LOGPROBS_MAX_TOP;
 
@@ -308,6 +410,7 @@ __global__ void __launch_bounds__(kLogThreads, kLogBlocks) logprobs_kernel(const
     };
 
     int turn = 0, side = 0;
+    const Pair scale2 = both(p.scale2);
     const bool finishes = part == 0 && t == 0 && p.logp != nullptr;  // looks after the given token
     auto fetch_token = [&](uint32_t r) {
         if (!finishes) return;
@@ -328,7 +431,9 @@ __global__ void __launch_bounds__(kLogThreads, kLogBlocks) logprobs_kernel(const
     for (uint32_t r = first; r < last_row; r += stride) {
         const Row row = row_at(r);
         const int steps = max(1, ceil_div(row.vecs, kTile * parts));
-        Share a{-kInf, 0.0f, 0.0f};
+        Share a;
+        Growing<T> sums(p);
+        volatile float former[2];  // sums of the tiles before, not in registers (there they make 142 us 154, with 8 alternatives)
         // one of the logits outside the whole vectors, for the first 16 threads
         Raw<T, 1> odd_raw, given;
         const int odd_at = row.odd_place(t, p.vocab);
@@ -358,68 +463,28 @@ __global__ void __launch_bounds__(kLogThreads, kLogBlocks) logprobs_kernel(const
                     ahead_left = next.vecs - (part * kTile + t);
                 }
             }
-            // y = z scale2 - off.  bf16 logits are held in pairs, before they are taken
-            // apart, to a least value whose exponential is 0 (low); beside the lowest
-            // finite ones there is none.  Where that is so, or the rounding of off is too
-            // large, the sums are made the other way below (not plain).  Batches of tokens that cannot be add nothing
-            // before the first logit to start from.
-            uint64_t s2 = Two(0.0f).v, w2 = Two(0.0f).v, off2 = Two(0.0f).v;
-            const uint64_t scale2 = Two(p.scale2).v;
-            float most = -kInf, off = 0.0f;  // the largest
-            uint32_t low = 0;
-            bool plain = true, one_by_one = false;
-            auto start = [&](float m) {
-                if (a.m == -kInf) a.m = m;
-                const float base = base_of(a.m);
-                off = base * p.scale2;
-                off2 = Two(-off).v;
-                plain = fabsf(off) < 4096.0f;  // what is left of the first-order factor below is then 4e-9
-                if constexpr (sizeof(T) == 2) {
-                    low = floor_bf16x2(base - p.reach);
-                    plain = plain && low != 0xff80ff80u && (base - __uint_as_float(low & 0xffff0000u)) * p.scale2 >= -kLeast;
-                }
-            };
-            const int ahead_slots = min(kSlots, ceil_div(ahead_left + t, kThreads)), both = max(slots, ahead_slots);
+            float most = -kInf;  // the largest
+            const int ahead_slots = min(kSlots, ceil_div(ahead_left + t, kThreads)), most_slots = max(slots, ahead_slots);
             if (step > 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll 1
-            for (int i0 = 0; i0 < both; i0 += kBatch) {
+            for (int i0 = 0; i0 < most_slots; i0 += kBatch) {
                 Vec<T> x[kBatch];
                 // places that no vector went to hold minus infinity
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) x[i].take(land + (i0 + i) * kPitch);
                 if (i0 < ahead_slots) fetch(i0, ahead, ahead_left);  // what these places held has been read
                 if (i0 >= slots) continue;
-                if (i0 == 0 || a.m == -kInf) {
-                    float m = largest(x[0]);
-#pragma unroll
-                    for (int i = 1; i < kBatch; ++i) m = fmaxf(m, largest(x[i]));
-                    start(m);
-                }
-                float here = -kInf;
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-#pragma unroll
-                    for (int j = 0; j < kEach; j += 2) {
-                        if constexpr (sizeof(T) == 2) x[i].w[j / 2] = larger_nan(x[i].w[j / 2], low);
-                        const float z0 = x[i][j], z1 = x[i][j + 1];
-                        if constexpr (TOP) here = max3(here, z0, z1);
-                        Two y(0.0f);
-                        y.v = pair_fma(Two(z0, z1).v, scale2, off2);
-                        float y0, y1;
-                        y.get(&y0, &y1);
-                        if constexpr (sizeof(T) == 4) {
-                            y0 = at_least(y0);
-                            y1 = at_least(y1);
-                            y = Two(y0, y1);
-                        }
-                        const uint64_t e = Two(fast_exp2(y0), fast_exp2(y1)).v;
-                        s2 = pair_add(s2, e);
-                        w2 = pair_fma(e, y.v, w2);
-                    }
+                const float here = largest_of(x);
+                if (here > sums.above) sums.move(here, p, WARPS == 8 && step > 0 ? former : nullptr);
+                if constexpr (sizeof(T) == 2) {
+                    if (sums.near)
+                        sums.template add<true>(x, scale2);
+                    else
+                        sums.template add<false>(x, scale2);
+                } else {
+                    sums.template add<false>(x, scale2);
                 }
                 if constexpr (TOP) {
-                    // nothing but the least value: no token that can be, or one that far off
-                    if (sizeof(T) == 2 && here <= __uint_as_float(low & 0xffff0000u) && a.m == -kInf) here = -kInf;
                     asm volatile("st.shared.f32 [%0], %1;" ::"r"(heights + i0 / kBatch * 4), "f"(here) : "memory");
                     most = fmaxf(most, here);
                 }
@@ -427,47 +492,21 @@ __global__ void __launch_bounds__(kLogThreads, kLogBlocks) logprobs_kernel(const
             if (last_step && r + stride < last_row) fetch_token(r + stride);
             asm volatile("cp.async.commit_group;" ::: "memory");
             const float odd = has_odd && step == 0 ? odd_raw[0] : -kInf;
-            if (a.m == -kInf) start(odd);
-            float s[2], w[2];
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(s[0]), "=f"(s[1]) : "l"(s2));
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(w[0]), "=f"(w[1]) : "l"(w2));
-            if (step == 0) {
-                const float y = at_least(fmaf(odd, p.scale2, -off)), e = fast_exp2(y);
-                s[0] += e;
-                w[0] = fmaf(e, y, w[0]);
-            }
-            {
-                // y came with what the rounding of `off` leaves, `by`
-                const float by = fmaf(base_of(a.m), p.scale2, -off), sum = s[0] + s[1], f = fmaf(by, -kLn2, 1.0f);
-                const float s_new = fmaf(sum, f, a.s), w_new = fmaf(fmaf(-by, sum, w[0] + w[1]), f, a.w);
-                one_by_one = !(plain && s_new < 1e37f);
-                if (!one_by_one) {
-                    a.s = s_new;
-                    a.w = w_new;
-                } else {  // from the largest, one by one (also: logits near the type's ends, NaN)
-                    const int end = min(row.vecs, g0 + kTile) * kEach;
-                    auto all = [&](auto &&f) {
-#pragma unroll 1
-                        for (int c = v0 * kEach; c < end; c += kThreads * kEach)
-#pragma unroll 1
-                            for (int j = 0; j < kEach; ++j) f(to_f32<T>(row.begin[c + j]));
-                    };
-                    most = -kInf;
-                    all([&](float z) { most = fmaxf(most, z); });
-                    if constexpr (TOP)
-                        for (int i = 0; i < kSlots / kBatch; ++i) asm volatile("st.shared.f32 [%0], %1;" ::"r"(heights + i * 4), "f"(most) : "memory");
-                    rebase(a, max3(a.m, most, odd), p.scale2);
-                    const float base = base_of(a.m);
-                    auto add = [&](float z) {
-                        const float y = at_least((z - base) * p.scale2), e = fast_exp2(y);
-                        a.s += e;
-                        a.w = fmaf(e, y, a.w);
-                    };
-                    all(add);
-                    add(odd);
-                }
+            if (WARPS == 8 && !last_step) {  // a tile's sums are added up by themselves
+                former[0] = (step > 0 ? former[0] : 0.0f) + pair_sum(sums.s2);
+                former[1] = (step > 0 ? former[1] : 0.0f) + pair_sum(sums.w2);
+                sums.s2 = sums.w2 = both(0.0f);
             }
             if (last_step) {
+                const bool more = WARPS == 8 && step > 0;
+                a = sums.share(p, pair_sum(sums.s2) + (more ? former[0] : 0.0f), pair_sum(sums.w2) + (more ? former[1] : 0.0f));
+                if (has_odd) {
+                    const float z = odd_raw[0];
+                    if (z > a.m) rebase(a, z, p.scale2);
+                    const float y = at_least((z - base_of(a.m)) * p.scale2), e = fast_exp2(y);
+                    a.s += e;
+                    a.w = fmaf(e, y, a.w);
+                }
                 a = join_lanes(a, p.scale2);
                 if (WARPS > 1 && lane == 0) room.shares[turn][warp] = a;
             }
@@ -484,14 +523,9 @@ __global__ void __launch_bounds__(kLogThreads, kLogBlocks) logprobs_kernel(const
                 uint32_t key = key_of(fmaxf(most, odd)), other = 0;
                 if (WARPS == 1 && fine == 2) {  // a lane's batches are two groups
                     float h[2] = {odd, -kInf};
-                    const float lowest = sizeof(T) == 2 && plain ? __uint_as_float(low & 0xffff0000u) : -kInf;
-                    for (int i = 0; i * kBatch < slots; ++i) {
-                        const float v = height_at(heights + i * 4);
-                        h[i & 1] = fmaxf(h[i & 1], v > lowest ? v : -kInf);  // (the least value stands for any below it)
-                    }
-                    // (after the sums made one by one every batch has the lane's largest: one group)
+                    for (int i = 0; i * kBatch < slots; ++i) h[i & 1] = fmaxf(h[i & 1], height_at(heights + i * 4));
                     key = key_of(h[0]);
-                    other = key_of(one_by_one ? -kInf : h[1]);
+                    other = key_of(h[1]);
                     room.keys[32 + lane] = other;
                 }
                 const int lanes = WARPS == 1 ? 1 : 32 / (kEachWarp * fine);  // of a group
@@ -817,7 +851,7 @@ ra_status ra_logprobs(const void *logits, int64_t ld, int dtype, int64_t rows, i
     }
     int groups = 1;
     while (groups < top) groups *= 2;
-    const LogParams p{logits, ids, logp, lse, entropy, top_logp, top_ids, ld, rows, (int)vocab, top, groups, id_bytes, scale, scale * kLog2e, 200.0f / (scale * kLog2e)};
+    const LogParams p{logits, ids, logp, lse, entropy, top_logp, top_ids, ld, rows, (int)vocab, top, groups, id_bytes, scale, scale * kLog2e, 200.0f / (scale * kLog2e), kMostBits / (scale * kLog2e)};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == RA_F32) return cuda_status(top > 0 ? launch_logprobs<float, true>(p, s) : launch_logprobs<float, false>(p, s));
     return cuda_status(top > 0 ? launch_logprobs<uint16_t, true>(p, s) : launch_logprobs<uint16_t, false>(p, s));

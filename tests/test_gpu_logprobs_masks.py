@@ -1,5 +1,5 @@
-"""ra_logprobs on rows with finite masks and logits far from zero, against the plain
-form in 64 bits and with the bounds of test_gpu_logprobs.py."""
+"""ra_logprobs on rows with finite masks, wide spreads and logits far from zero,
+against the plain form in 64 bits and with the bounds of test_gpu_logprobs.py."""
 from __future__ import annotations
 
 import pytest
@@ -86,3 +86,45 @@ def test_logits_far_from_zero(vocab, dtype):
     z = _logits(4, vocab, dtype, seed=6).t
     for scale in (1e3, 1e5, 1e8, 1e30):
         _check(z, _ids(4, vocab), scale, 3)
+
+
+def _first_batch(vocab, dtype):
+    """As many logits as the threads of a row start from, and the few before them."""
+    each = 8 if dtype == BF16 else 4
+    vecs = -(-vocab // each)
+    warps = 1 if vecs <= 512 else 2 if vecs <= 1024 else 4 if vecs <= 2048 else 8
+    return warps * 32 * each * (2 if warps == 1 else 4) + each
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("vocab", [800, 1536, 6007, 12001, 20011, 70000, 131071])
+def test_spreads(vocab, dtype):
+    """A row's first logits, its last ones, or those of some lanes are far below the others, by gaps about which the sums
+    leave binary32: the exponential's least argument, its flushed results, the sums' range."""
+    gaps = (10.0, 20.0, 40.0, 60.0, 70.0, 81.0, 83.0, 84.0, 84.5, 85.0, 85.5, 87.0, 88.5, 90.0, 100.0, 110.0, 115.0, 120.0, 130.0, 150.0)
+    first = min(_first_batch(vocab, dtype), vocab // 2)
+    n = torch.arange(vocab, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    rows = []
+    for gap in gaps:
+        plain = torch.randn(vocab, generator=g, device="cuda")
+        rows.append(torch.where(n < first, -gap, plain))
+        for high in (4.0, 7.0):  # of one token among the first
+            rows.append(torch.where(n == first // 3, high, rows[-1] if high == 4.0 else rows[-2]))
+        rows.append(torch.where(n >= vocab - first, plain - gap, plain))
+        rows.append(torch.where(n // 8 % 32 < 20, plain - gap, plain))
+        rows.append(torch.where(n % (first + 77) == 5, plain, plain - gap))  # the high ones are few
+    z = torch.stack(rows).to(dtype)
+    ids = _ids(len(rows), vocab)
+    for scale, top in ((1.0, 0), (1.0, 8), (0.8, 32)):
+        _check(z, ids, scale, top)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("vocab", [1536, 12001, 40000])
+def test_logits_that_rise_along_the_row(vocab, dtype):
+    """Every batch is above the last one, from a little to so far that nothing is left of it."""
+    n = torch.arange(vocab, device="cuda").double() / vocab
+    z = torch.stack([n * rise for rise in (30.0, 300.0, 3e3, 3e4, 3e6, 1e12)] + [10.0 ** (n * 38), -(10.0 ** (38 - n * 38))]).to(dtype)
+    for scale, top in ((1.0, 0), (1.0, 8), (0.7, 32)):
+        _check(z, _ids(len(z), vocab), scale, top)
