@@ -68,6 +68,11 @@ __device__ __forceinline__ float at_least(float y) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(y), "f"(kLeast));
     return r;
 }
+__device__ __forceinline__ float at_most_0(float y) {
+    float r;
+    asm("min.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(y));
+    return r;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {  // NaN aside
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -717,11 +722,14 @@ cudaError_t launch_logprobs(const LogParams &p, cudaStream_t s) {
 // backward
 //
 // d = q (c0 + c1 y) for y = log2 p, q = 2^y, and scale g more at the given token:
-// c0 = -scale (g + e H), c1 = -scale e ln 2.  LANES lanes take a stretch of a row,
-// kFlight vectors of 8 logits a lane: a warp, or for short rows a quarter of one, so
-// that four rows' few numbers and logits are under way at once (65536 x 100 bf16 20 us
-// a warp a row, 8 so; x 257 25 and 14; x 512 29 and 24; from 600 on the same).
-// Memory bounds the long rows: 8192 x 32000 bf16 150 us, 7.0 TB/s.
+// c0 = -scale (g + e H), c1 = -scale e ln 2.  y = (z scale - lse) log2 e, the difference
+// by one rounding: what is left is lse's own, which is not to make a p above 1.
+//
+// LANES lanes take a stretch of a row, kFlight vectors of 8 logits a lane: a warp, or
+// for short rows a quarter of one, so that four rows' few numbers and logits are under
+// way at once (65536 x 100 bf16 20 us a warp a row, 7 so; x 257 25 and 13; x 512 29 and
+// 24; from 600 on the same).  Memory bounds the long rows: 8192 x 32000 bf16 150 us,
+// 7.0 TB/s (152 without arithmetic on pairs).
 
 constexpr int kGradThreads = 256, kFlight = 4;
 
@@ -731,7 +739,7 @@ struct LogGradParams {
     void *out;
     int64_t ld, ld_out, rows, stretches;  // of a row
     int vocab, id_bytes;
-    float scale, scale2;
+    float scale;
 };
 
 template <class T, class TO, bool ENTROPY, int LANES>
@@ -759,17 +767,24 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const LogGr
         const int64_t id = p.g == nullptr ? -1 : p.id_bytes == 8 ? static_cast<const int64_t *>(p.ids)[r] : static_cast<const int32_t *>(p.ids)[r];
         const float lse = p.lse[r], given = p.g == nullptr ? 0.0f : p.g[r];
         const float ge = ENTROPY ? p.ge[r] : 0.0f, h = ENTROPY ? p.entropy[r] : 0.0f;
-        const bool none = lse < -1e30f, inside = id >= 0 && id < p.vocab;  // none: no token can be: zeros
+        // none: no token can be, or lse is so low that its rounding leaves p no digit: zeros
+        const bool none = lse < -16777216.0f, inside = id >= 0 && id < p.vocab;
         const int at = none || !inside ? -1 : (int)id;
-        const float g = inside ? given : 0.0f, off = none ? 0.0f : -lse * kLog2e, hot = p.scale * g;
+        const float g = inside ? given : 0.0f, off = none ? 0.0f : -lse, hot = p.scale * g;
         const float c0 = none ? 0.0f : ENTROPY ? -p.scale * fmaf(ge, h, g) : -hot, c1 = none ? 0.0f : -p.scale * kLn2 * ge;
-        auto slope = [&](float z) {
-            float y = fmaf(z, p.scale2, off);
+        const Pair scale = both(p.scale), offs = both(off);
+        auto slopes = [&](float z0, float z1, float &d0, float &d1) {
+            float y0, y1;
+            apart(pair_fma(pair(z0, z1), scale, offs), y0, y1);
+            apart(pair_mul(pair(at_most_0(y0), at_most_0(y1)), both(kLog2e)), y0, y1);
             if constexpr (ENTROPY) {
-                y = at_least(y);
-                return fast_exp2(y) * fmaf(c1, y, c0);
+                y0 = at_least(y0);
+                y1 = at_least(y1);
+                d0 = fast_exp2(y0) * fmaf(c1, y0, c0);
+                d1 = fast_exp2(y1) * fmaf(c1, y1, c0);
             } else {
-                return fast_exp2(y) * c0;
+                d0 = fast_exp2(y0) * c0;
+                d1 = fast_exp2(y1) * c0;
             }
         };
 #pragma unroll
@@ -778,7 +793,7 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const LogGr
             const int c = head + (v0 + LANES * i) * 8;
             float d[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] = slope(x[i][j]);
+            for (int j = 0; j < 8; j += 2) slopes(x[i][j], x[i][j + 1], d[j], d[j + 1]);
             if ((unsigned)(at - c) < 8u) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -787,7 +802,8 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(const LogGr
             store_w<TO, 8>(out + c, d);
         }
         auto one = [&](int64_t c) {
-            float d = slope(to_f32<T>(row[c]));
+            float d, same;
+            slopes(to_f32<T>(row[c]), 0.0f, d, same);
             if (c == at) d += hot;
             out[c] = from_f32<TO>(d);
         };
@@ -877,8 +893,7 @@ ra_status ra_logprobs_grad(const void *logits, int64_t ld, int dtype, int64_t ro
     for (const Mat &m : in)
         if (mats_overlap(b, m)) return RA_ERR_OVERLAP;
     if (mats_overlap(a, b) && !same_mat(a, b)) return RA_ERR_OVERLAP;
-    const LogGradParams p{logits, ids, lse, entropy, grad_logp, grad_entropy, out, ld, ld_out, rows, 1, (int)vocab, id_bytes, scale,
-                          scale * kLog2e};
+    const LogGradParams p{logits, ids, lse, entropy, grad_logp, grad_entropy, out, ld, ld_out, rows, 1, (int)vocab, id_bytes, scale};
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (dtype == RA_F32) return cuda_status(out_dtype == RA_F32 ? launch_logprobs_grad<float, float>(p, s) : launch_logprobs_grad<float, uint16_t>(p, s));
     return cuda_status(out_dtype == RA_F32 ? launch_logprobs_grad<uint16_t, float>(p, s) : launch_logprobs_grad<uint16_t, uint16_t>(p, s));

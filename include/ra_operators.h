@@ -365,9 +365,10 @@ ra_status ra_logprobs(const void *logits, int64_t ld, int dtype, int64_t rows, i
  * (g) and of the entropy (e), p = exp(z - lse):
  *   out[r, j] = scale * (g[r] ([j = ids[r]] - p_j) - e[r] p_j (z_j - lse[r] + entropy[r]))
  * Padding's g counts for nothing, whatever it holds.  A token that cannot be has
- * p = 0 and adds no entropy; a row in which none can be, or all logits are those
- * of a mask near the type's lowest value (lse below -10^30), has gradient 0.  p is
- * off by up to 2^-24 |lse| of itself, as lse is.
+ * p = 0 and adds no entropy; a row in which none can be has gradient 0.  lse is a
+ * binary32 number: its rounding makes p off by a factor of up to exp(2^-24 |lse|),
+ * never above 1.  So a row with lse below -2^24, of which p would have no digit (a
+ * row masked throughout by a finite value such as -10^9), has gradient 0 too.
  *   lse, entropy  as ra_logprobs left them; entropy only with grad_entropy
  *   grad_logp, grad_entropy  rows binary32 values, or NULL: zeros; without
  *            grad_logp ids are not looked at
