@@ -115,7 +115,8 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
 
     // m and rstd of a row.  The sums of the values and of their squares are made at
     // once; where the mean is so large that their difference loses more than 4
-    // bits, the squares of the differences from it are summed after it.
+    // bits, or the squares leave binary32, the squares of the differences from it are
+    // summed after it.
     auto moments = [&](const Pair (&v)[kPairs], const Side &side, float *m, float *rstd) {
         Pair sum = both(0.0f), squares = both(0.0f);
 #pragma unroll
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
         if (side.kind == RA_NORM_LAYER) {
             *m = s[0] * p.per_d;
             const float left = fmaf(-*m, *m, var);
-            if (!(left * 16.0f >= var) && var > 0.0f) {  // the same for the whole row
+            if (!(left * 16.0f >= var && var < INFINITY) && var > 0.0f) {  // the same for the whole row
                 s[0] = s[1] = 0.0f;
 #pragma unroll
                 for (int j = 0; j < kOwn; ++j) {
