@@ -168,7 +168,18 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
             else
                 to.load(row_of_matrix<WIDE>(from, ld, r), col, count);
         };
-        // columns past the row's end hold 0, and add 0 to the sums
+        // Columns past the row's end hold 0, and add 0 to the sums; but where m rstd is no
+        // binary32 number (huge equal values) their units would be infinite: 0 then.
+        auto no_units = [&](Pair (&unit)[kPairs], float m, float rstd) {
+            if (fabsf(m) * rstd > 3.402823466e38f) {
+#pragma unroll
+                for (int j = 0; j < kPairs; ++j) {
+                    float a, b;
+                    apart(unit[j], a, b);
+                    unit[j] = pair(2 * j < count ? a : 0.0f, 2 * j + 1 < count ? b : 0.0f);
+                }
+            }
+        };
 
         Pair full[kPairs];
         {
@@ -179,9 +190,11 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
                 const Pair off = both(-kept.z), scale = both(kept.w);
                 Pair s0 = both(0.0f), s1 = both(0.0f);
 #pragma unroll
+                for (int j = 0; j < kPairs; ++j) unit[j] = pair_mul(pair_add(x.two(j), off), scale);
+                no_units(unit, kept.z, kept.w);
+#pragma unroll
                 for (int j = 0; j < kPairs; ++j) {
                     const Pair dh = h.two(j);
-                    unit[j] = pair_mul(pair_add(x.two(j), off), scale);
                     full[j] = pair_mul(dh, gain[j]);
                     s0 = pair_fma(full[j], unit[j], s0);
                     s1 = pair_add(s1, full[j]);
@@ -219,6 +232,7 @@ __global__ void __launch_bounds__(WARPS == 16 ? 512 : kNormThreads, WARPS == 16 
             const Pair off = both(normed ? -kept.x : 0.0f), scale = both(normed ? kept.y : 1.0f);
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) unit[j] = pair_mul(pair_add(f.two(j), off), scale);
+            no_units(unit, kept.x, kept.y);
             if (by_matrix) {
                 float a[kOwn], b[kOwn];
                 load_vector(p.post.gain, p.post.f32, col, count, 1.0f, a);

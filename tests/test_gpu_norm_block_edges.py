@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import gradient_ring_all_gb300 as ra
-from block_reference import CHAIN, _norm64, half_step, join64
+from block_reference import CHAIN, _norm64, grads64, half_step, join64
 from operator_reference import check
 
 pytestmark = pytest.mark.gpu
@@ -46,3 +46,29 @@ def test_a_mean_whose_square_leaves_binary32(d):
     new, _, kept = ra.ra_norm_block(zero, x, post=n)
     want, size = join64(zero, x, n, None, 1.0, 1.0)
     check(new, want, CHAIN * size + half_step(F32) * want.abs(), "x'")
+
+
+@pytest.mark.parametrize("d", [8, 16, 64])
+def test_even_rows_of_huge_values(d):
+    """m rstd is no binary32 number in a row of equal values of 2^120: what lies beside the row's end must not enter its sums."""
+    x = torch.full((3, d), 2.0 ** 120, device="cuda")
+    x[1] = torch.randn(d, device="cuda")
+    n = ra.Norm(torch.randn(d, device="cuda"), torch.randn(d, device="cuda"))
+    _, h, kept = ra.ra_norm_block(x, pre=n, dtype=F32)
+    assert kept[0, 2] == 2.0 ** 120 and torch.equal(h[0], n.bias)
+    dh = torch.randn(3, d, device="cuda")
+    got = ra.ra_norm_block_grad(dh, x, kept, pre=n)
+    want = grads64(dh, x, None, None, None, 1.0, 1.0, n, None)
+    # the huge rows' normed values are 0, so their part of the magnitudes is that of a row of zeros
+    small = x.clone()
+    small[0], small[2] = 0.0, 0.0
+    size = grads64(dh, small, None, None, None, 1.0, 1.0, n, None)
+    check(got.dx, want["dx"][0], CHAIN * size["dx"][1] + half_step(F32) * want["dx"][0].abs(), "dx")
+    check(got.pre_gain, want["pre_gain"][0], CHAIN * size["pre_gain"][1], "pre_gain")
+    zero = torch.zeros(3, d, device="cuda")
+    new, _, kept = ra.ra_norm_block(zero, x, post=n)
+    got = ra.ra_norm_block_grad(None, new, kept, f=x, post=n, dx=dh)
+    want = grads64(None, new, x, n, None, 1.0, 1.0, None, dh)
+    size = grads64(None, new, small, n, None, 1.0, 1.0, None, dh)
+    check(got.df, want["df"][0], CHAIN * size["df"][1] + half_step(F32) * want["df"][0].abs(), "df")
+    check(got.post_gain, want["post_gain"][0], CHAIN * size["post_gain"][1], "post_gain")
