@@ -357,6 +357,7 @@ __global__ void __launch_bounds__(kSumsMost *kPartWarps * 32) parts_kernel(const
         return v == nullptr ? none : f32 ? static_cast<const float *>(v)[c] : to_f32<uint16_t>(static_cast<const uint16_t *>(v)[c]);
     };
     auto put = [&](float *to, float v) {
+        if (p.count == 0) v = 0.0f;  // no rows: 0, whatever it was multiplied with
         if (to != nullptr) to[c] = p.accumulate ? to[c] + v : v;
     };
     const float by = p.beta * value(p.gate, p.gate_f32, 1.0f);

@@ -72,3 +72,19 @@ def test_even_rows_of_huge_values(d):
     size = grads64(None, new, small, n, None, 1.0, 1.0, None, dh)
     check(got.df, want["df"][0], CHAIN * size["df"][1] + half_step(F32) * want["df"][0].abs(), "df")
     check(got.post_gain, want["post_gain"][0], CHAIN * size["post_gain"][1], "post_gain")
+
+
+def test_no_rows_beside_parameters_that_are_not_finite():
+    """A sum over no rows is 0, whatever it would be multiplied with."""
+    d = 24
+    x = torch.zeros(0, d, device="cuda")
+    odd = torch.full((d,), float("inf"), device="cuda")
+    odd[3] = float("nan")
+    n = ra.Norm(odd, odd)
+    new, h, kept = ra.ra_norm_block(x, x, post=n, gate=odd, pre=n, dtype=F32)
+    g = ra.ra_norm_block_grad(h, new, kept, f=x, post=n, gate=odd, pre=n)
+    for t in (g.pre_gain, g.pre_bias, g.post_gain, g.post_bias, g.gate):
+        assert not bool(t.any()) and not bool(torch.isnan(t).any())
+    out = ra.NormBlockGrads(gate=torch.ones(d, device="cuda"), post_gain=torch.full((d,), 2.0, device="cuda"))
+    ra.ra_norm_block_grad(h, new, kept, f=x, post=n, gate=odd, pre=n, out=out, accumulate=True)
+    assert bool((out.gate == 1).all()) and bool((out.post_gain == 2).all())
