@@ -101,10 +101,6 @@ template <class T>
 struct Vec {
     static constexpr int kEach = 16 / sizeof(T);
     uint32_t w[4];
-    __device__ __forceinline__ void none() {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
-    }
     __device__ __forceinline__ void take(uint32_t shared) {
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(shared) : "memory");
     }
