@@ -17,6 +17,7 @@ from . import operators as _op
 from .operators import _BF16, _CODE, _F32, _check, _device, _empty, _ids, _matrix, _output, _shape, _stream_of, _workspace
 
 KINDS = {"layer": 1, "rms": 2}
+_KIND_NAMES = {code: kind for kind, code in KINDS.items()}
 MAX_TOP = 32  # alternatives of a row
 
 _NORM = "QQiifi"  # ra_norm
@@ -123,15 +124,23 @@ class Norm:
     mean ("layer") or 0 ("rms"), rstd = (mean (v - m)^2 + eps)^-1/2.  gain and
     bias: vectors of one type (float32 or bfloat16), or None."""
 
-    __slots__ = ("gain", "bias", "kind", "eps", "_kind")
+    __slots__ = ("gain", "bias", "eps", "_kind")
 
     def __init__(self, gain=None, bias=None, kind: str = "layer", eps: float = 1e-5):
+        if not 0.0 <= eps < float("inf"):
+            raise ValueError("eps must be finite and not negative, got %r" % (eps,))
+        self.gain, self.bias, self.eps, self.kind = gain, bias, eps, kind
+
+    @property
+    def kind(self):
+        return _KIND_NAMES[self._kind]
+
+    @kind.setter
+    def kind(self, kind):
         code = KINDS.get(kind)
         if code is None:
             raise ValueError("kind must be one of %s, got %r" % (", ".join(KINDS), kind))
-        if not 0.0 <= eps < float("inf"):
-            raise ValueError("eps must be finite and not negative, got %r" % (eps,))
-        self.gain, self.bias, self.kind, self.eps, self._kind = gain, bias, kind, eps, code
+        self._kind = code
 
 
 def _norm(n, what, dev, d):
