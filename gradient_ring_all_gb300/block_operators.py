@@ -129,7 +129,11 @@ class Norm:
     def __init__(self, gain=None, bias=None, kind: str = "layer", eps: float = 1e-5):
         if not 0.0 <= eps < float("inf"):
             raise ValueError("eps must be finite and not negative, got %r" % (eps,))
-        self.gain, self.bias, self.eps, self.kind = gain, bias, eps, kind
+        self.gain, self.bias, self.eps, self._kind = gain, bias, eps, KINDS.get(kind) or self._unknown(kind)
+
+    @staticmethod
+    def _unknown(kind):
+        raise ValueError("kind must be one of %s, got %r" % (", ".join(KINDS), kind))
 
     @property
     def kind(self):
@@ -137,10 +141,7 @@ class Norm:
 
     @kind.setter
     def kind(self, kind):
-        code = KINDS.get(kind)
-        if code is None:
-            raise ValueError("kind must be one of %s, got %r" % (", ".join(KINDS), kind))
-        self._kind = code
+        self._kind = KINDS.get(kind) or self._unknown(kind)
 
 
 def _norm(n, what, dev, d):
