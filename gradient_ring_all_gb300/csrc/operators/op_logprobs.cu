@@ -22,8 +22,8 @@ constexpr float kInf = INFINITY;
 // before the first and after the last whole vector are one more value of the first
 // threads.
 //
-// Without alternatives memory bounds it: 8192 x 32000 bf16 82 us (6.4 TB/s), 5 us a row
-// and block, three blocks an SM.  8 alternatives make it 154: their bound, the second
+// Without alternatives memory bounds it: 8192 x 32000 bf16 84 us (6.2 TB/s), 5 us a row
+// and block, three blocks an SM.  8 alternatives make it 142: their bound, the second
 // look and the order are one after another in a row, in eight warps that meet, and
 // shared memory has room for three rows an SM.
 

@@ -23,7 +23,7 @@ struct NormParams {
 // meanwhile (op_norm.cuh).  Memory bounds rows of 16-byte boundaries: 8192 x 2048 bf16
 // with a join take 27 us (5.0 TB/s), 2048 x 8192 binary32 to bf16 without one 18 (5.7);
 // what is left of the way to 20 and 15 is the sums over a row, one or two in turn, in
-// 16 warps an SM.  Rows of odd lengths take 44 us (2047): one value an access.
+// 16 warps an SM.  Rows of odd lengths take 39 us (2047): one value an access.
 constexpr int kOwn = 16;  // columns a thread has, in every row
 
 // rows under way a group: as many as shared memory has room for in the widest blocks

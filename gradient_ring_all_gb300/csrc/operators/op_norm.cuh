@@ -145,10 +145,10 @@ __device__ __forceinline__ void copy_own(uint32_t to, int threads, const T *row,
         }
 }
 // Other rows, and a cluster's: only into the L2 cache, a line of 128 bytes a thread
-// (8192 rows of 2047 bf16 backward: 136 us without, 95 with; rows of one warp, 18 and
-// 19 at 250 columns, go without).  A cluster's blocks meet once a sum, and a meeting
-// waits for the copies under way: with them 2048 rows of 8192 bf16 took 125 us
-// backward, and 87 without a join, with this 107 and 59.
+// (8192 rows of 2047 bf16 backward: 136 us without, 95 with, and 84 since; rows of one
+// warp, 18 and 19 at 250 columns, go without).  A cluster's blocks meet once a sum, and
+// a meeting waits for the copies under way: with them 2048 rows of 8192 bf16 took 125
+// us backward, and 87 without a join, with this 107 and 59.
 template <class T, class C>
 __device__ __forceinline__ void cache_own(const T *row, const C &col) {
     const int at = col.begin + (int)threadIdx.x % C::kThreads * (128 / (int)sizeof(T));

@@ -227,7 +227,8 @@ ra_status ra_dropout(const void *x, int64_t ld_x, int x_dtype, int64_t rows, int
 /* A norm over a row v of d values: (v - m) * rstd * gain + bias,
  *   m = mean of v (RA_NORM_LAYER) or 0 (RA_NORM_RMS), rstd = (mean of (v - m)^2 + eps)^-1/2.
  * Moments are binary32, the second one of the differences from the first (or of the
- * values, less m^2, where that costs 4 bits at most). */
+ * values, less m^2, where that costs 4 bits at most).  Where the sum of these squares
+ * is no binary32 number rstd is 0; where that of the values is none the row is NaN. */
 typedef enum { RA_NORM_NONE = 0, RA_NORM_LAYER = 1, RA_NORM_RMS = 2 } ra_norm_kind;
 #define RA_NORM_MAX_D 32768
 
@@ -258,7 +259,8 @@ typedef enum { RA_GATE_NONE = 0, RA_GATE_VECTOR = 1, RA_GATE_MATRIX = 2 } ra_gat
  *   kept   4 values a row, contiguous and 16-byte aligned, or NULL: m and rstd of
  *          post and of pre (zeros where there is no such norm), for the backward pass
  * x_dtype and f_dtype: both RA_F32, both RA_BF16, or RA_F32 and RA_BF16.
- * d is at most RA_NORM_MAX_D (RA_ERR_UNSUPPORTED).
+ * d is at most RA_NORM_MAX_D (RA_ERR_UNSUPPORTED).  Beside an infinite gate or gain a
+ * value may be NaN where the formula has an infinity.
  */
 typedef struct {
     int64_t rows, d;
@@ -347,7 +349,10 @@ ra_status ra_norm_block_grad(const ra_norm_block_grad_args *args, void *stream);
  * tokens can be, the rest of the row is -1 and minus infinity.  A row in which no
  * token can be has lse minus infinity, entropy 0 and logp minus infinity (0 for
  * padding).  A row with a NaN or plus infinity gives NaN in place of every number
- * but a padding's logp, and -1 as its alternatives.
+ * but a padding's logp, and -1 as its alternatives.  Finite logits may lie anywhere:
+ * sums are of exp of differences from logits of the row, so that rows far from zero,
+ * or masked by any finite value, keep their digits; lse itself is a binary32 number
+ * (minus infinity below the least one).  A difference that is none counts as infinite.
  *   logits   rows x vocab of dtype;  ids  rows integers of id_bytes (4 or 8)
  *   scale    the inverse of a temperature: > 0, and 1.443 scale is finite
  *   logp, lse, entropy  rows binary32 values each; logp (then ids too) and entropy
