@@ -352,7 +352,7 @@ ra_status ra_norm_block_grad(const ra_norm_block_grad_args *args, void *stream);
  * but a padding's logp, and -1 as its alternatives.  Finite logits may lie anywhere:
  * sums are of exp of differences from logits of the row, so that rows far from zero,
  * or masked by any finite value, keep their digits; lse itself is a binary32 number
- * (minus infinity below the least one).  A difference that is none counts as infinite.
+ * (an infinity beyond the range).  A difference that is none counts as infinite.
  *   logits   rows x vocab of dtype;  ids  rows integers of id_bytes (4 or 8)
  *   scale    the inverse of a temperature: > 0, and 1.443 scale is finite
  *   logp, lse, entropy  rows binary32 values each; logp (then ids too) and entropy
